@@ -8,6 +8,9 @@
  *   -> SwiGLU gate/up projection, bf16 intermediate, MXFP8 quantisation of h
  *   -> down projection
  *   -> weighted combine (+ an optional always-active shared expert).
+ * In front of it, the attention of the layer: per-head RMSNorm, rotary
+ * positions and the append to a paged MXFP4 key/value cache, attention over
+ * that cache, and causal attention over prompts.
  *
  * Passages that define the operation (page title, section):
  *  - "SGLang's Low-Latency Mode Boosts DeepSeek-V4.1-Flash Speed by 1.56x on
@@ -64,7 +67,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 3
+#define MOE_ABI_VERSION 4
 
 typedef enum {
   MOE_OK = 0,
@@ -372,6 +375,144 @@ moe_status_t moe_plan_diagnostics(void *plan, int64_t *out8);
 moe_status_t moe_forward_static_scratch(const moe_config_t *config, const moe_weights_t *weights, const void *x,
                                         const float *logits, int32_t T, void *y, int32_t *d_status,
                                         void *cuda_stream);
+
+/* ---------------------------------------------------------------- attention
+ * The attention in front of the MoE step, over a key/value cache in the
+ * library's own 4-bit format. Three calls:
+ *   moe_qkv_append     RMSNorm of each query and key head, rotary positions,
+ *                      MXFP4 quantisation of keys and values into the cache;
+ *   moe_attend_paged   attention of the newest rows of each sequence (one
+ *                      token, or the rows of a verify step) over the cache;
+ *   moe_attend_prompt  causal attention over packed prompts in 16 bits.
+ * None needs a plan. They run on the current device, allocate nothing and do
+ * not synchronise, so they can be captured in CUDA graphs; two calls may
+ * overlap on the GPU as long as neither writes what the other reads (the
+ * workspace of moe_attend_paged counts as written).
+ *
+ * Sizes that live in device memory (lengths, offsets, pages, slots,
+ * positions) are checked by the kernels. What is out of range is not accessed,
+ * and MOE_ERR_DEVICE_BOUNDS is stored in *d_status. Unlike the plan's calls,
+ * these never store MOE_OK: the caller sets the word to MOE_OK once, and a
+ * later check covers every call made until then. d_status NULL: such errors
+ * are not reported.
+ *
+ * Query heads share key/value heads in groups: head h reads kv head
+ * h / (num_heads / num_kv_heads). head_dim is 64 or 128. Row strides are in
+ * elements and multiples of 8; the heads of one row are contiguous, so the
+ * q, k and v parts of one fused projection can be passed in place. */
+
+/* 16-bit element types of queries, keys, values and outputs. */
+#define MOE_DTYPE_BF16 0u
+#define MOE_DTYPE_F16 1u
+
+/* A paged key/value cache in MXFP4 (OCP MX v1.0; the codes and scales of
+ * moe_quantize_mxfp4 along head_dim). Page p of kv head h holds page_size
+ * tokens:
+ *   codes  uint8 [num_pages][num_kv_heads][page_size][head_dim/2]
+ *   scales uint8 [num_pages][num_kv_heads][page_size][head_dim/32]
+ * 16-byte aligned device memory, owned by the caller. Tokens that were never
+ * appended may hold anything: no call reads past a sequence's length. */
+typedef struct moe_kv_cache {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int32_t num_pages;
+  int32_t page_size;    /* tokens per page: a multiple of 16, 16..1024 */
+  int32_t num_kv_heads; /* 1..1024 */
+  int32_t head_dim;     /* 64 or 128 */
+} moe_kv_cache_t;
+
+typedef struct moe_qkv_append_io {
+  const void *q, *k, *v;             /* [T][num_heads][D], [T][num_kv_heads][D] (twice), 16-bit */
+  int64_t q_stride, k_stride, v_stride;  /* elements from one token's row to the next */
+  int32_t num_tokens;                /* T >= 0 */
+  int32_t num_heads, num_kv_heads, head_dim;
+  uint32_t dtype;                    /* MOE_DTYPE_*: of q, k, v, the norm weights and the outputs */
+  int32_t rotary_dim;                /* R: the first R dimensions are rotated; 0, or a multiple of 16 up to D */
+  int32_t interleaved;               /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1) */
+  int32_t rope_positions;            /* rows of rope */
+  const float *rope;                 /* fp32 [rope_positions][R]: R/2 cosines, then R/2 sines (NULL with R = 0) */
+  const int32_t *positions;          /* [T] row of rope for each token (NULL with R = 0) */
+  const void *q_norm, *k_norm;       /* [D] RMSNorm weights, or NULL: that part is not normalised */
+  float norm_eps;                    /* finite, >= 0 */
+  const int64_t *slots;              /* [T] place of each token in the cache, page * page_size + offset; < 0: the
+                                      * token is not cached. NULL when no cache is given. */
+  void *q_out;                       /* [T][num_heads][D] */
+  void *k_out;                       /* optional [T][num_kv_heads][D]: the rotated keys before 4 bits */
+  void *k_cached, *v_cached;         /* optional [T][num_kv_heads][D]: the values that 4 bits keep, whether or not
+                                      * the token is cached: attention over them equals attention over the cache */
+} moe_qkv_append_io_t;
+
+/* Norm, rotation and append in one pass over one projection's output:
+ *   n = x * w / sqrt(mean(x^2) + eps) for each q and k head (x itself without w)
+ *   rotated pair (a, b) at angle t: (a cos t - b sin t, b cos t + a sin t)
+ *   q_out = the rotated q, rounded once to 16 bits; the keys likewise, and the
+ *   cache gets MXFP4 of those 16-bit keys and of v.
+ * The keys are computed in two-float arithmetic (about 2^-45 relative), so their
+ * 16-bit values, and with them the 4-bit codes, are those of the formula.
+ * q_out may be q itself (the same pointer with q_stride == num_heads * D);
+ * otherwise outputs must not overlap inputs. The slots of one call must be
+ * distinct: two tokens with the same slot leave a mixture of both there.
+ * cache may be NULL (norm and rotation only). positions out of range: the
+ * token is skipped. slots past the cache: the token is not cached. */
+moe_status_t moe_qkv_append(const moe_qkv_append_io_t *io, const moe_kv_cache_t *cache, int32_t *d_status,
+                            void *cuda_stream);
+
+typedef struct moe_attend_paged_io {
+  const void *q;              /* [num_rows][num_heads][D] */
+  int64_t q_stride;           /* elements from one row to the next */
+  void *out;                  /* [num_rows][num_heads][D] */
+  int64_t out_stride;
+  float *lse;                 /* optional fp32 [num_rows][num_heads]: log sum exp of the scaled scores */
+  const int32_t *page_table;  /* [num_seqs][max_pages]: the pages of each sequence in order */
+  const int32_t *lengths;     /* [num_seqs] tokens of each sequence in the cache, its query rows included */
+  const int32_t *cu_rows;     /* [num_seqs + 1] first query row of each sequence, then the end */
+  int32_t num_seqs;           /* 0..4096 */
+  int32_t num_rows;           /* rows of q and out */
+  int32_t max_pages;          /* columns of page_table */
+  int32_t max_rows;           /* query rows that a sequence usually has at most: picks the kernel variant; any
+                               * value >= 1 gives right results */
+  int32_t num_heads;          /* a multiple of the cache's num_kv_heads */
+  uint32_t dtype;             /* MOE_DTYPE_*: of q and out */
+  float scale;                /* of the scores, finite */
+} moe_attend_paged_io_t;
+
+/* Bytes of device workspace that moe_attend_paged needs for these sizes (the
+ * pointers are not looked at), the same for every content of the device
+ * arrays. It depends on the current device. */
+moe_status_t moe_attend_paged_workspace(const moe_attend_paged_io_t *io, const moe_kv_cache_t *cache,
+                                        int64_t *bytes_out);
+
+/* Attention over the paged MXFP4 cache. Row i of the n rows of a sequence of
+ * length L sees the keys 0 .. L - n + i (the rows are its last n tokens):
+ *   s_j = scale * (q . K_j),  out = sum_j softmax(s)_j V_j,  lse = log sum_j exp s_j
+ * with K, V the values the cache stands for. A row that sees no key (L < n)
+ * gets out = 0 and lse = -inf. Rows of q past cu_rows[num_seqs] are not
+ * touched. workspace: 16-byte aligned device memory of at least the size
+ * above; its content before the call does not matter, and calls that may
+ * overlap on the GPU need one each. */
+moe_status_t moe_attend_paged(const moe_attend_paged_io_t *io, const moe_kv_cache_t *cache, void *workspace,
+                              int64_t workspace_bytes, int32_t *d_status, void *cuda_stream);
+
+typedef struct moe_attend_prompt_io {
+  const void *q, *k, *v;      /* [num_rows][num_heads][D], [num_keys][num_kv_heads][D] (twice) */
+  int64_t q_stride, k_stride, v_stride;
+  void *out;                  /* [num_rows][num_heads][D] */
+  int64_t out_stride;
+  float *lse;                 /* optional fp32 [num_rows][num_heads] */
+  const int32_t *cu_rows;     /* [num_seqs + 1] first query row of each sequence, then the end */
+  const int32_t *cu_keys;     /* [num_seqs + 1] first key of each sequence, then the end */
+  int32_t num_seqs;           /* 0..4096 */
+  int32_t num_rows, num_keys; /* rows of q and out; rows of k and v */
+  int32_t num_heads, num_kv_heads, head_dim;
+  uint32_t dtype;
+  int32_t causal;             /* 1: row i of n sees keys 0 .. m - n + i of its sequence's m; 0: all of them */
+  float scale;
+} moe_attend_prompt_io_t;
+
+/* Attention over packed prompts, or over chunks of prompts with the keys that
+ * precede them (m > n). Formula and empty rows as for moe_attend_paged. The
+ * rows behind the last sequence are not touched. A NaN or infinity in a key or
+ * value of one sequence never reaches another sequence. */
+moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_status, void *cuda_stream);
 
 /* Teardown: frees the plan's device memory and events, after a device-wide
  * synchronise. NULL is a no-op. */

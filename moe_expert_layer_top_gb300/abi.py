@@ -12,7 +12,7 @@ import os
 
 from . import build as _build
 
-MOE_ABI_VERSION = 3
+MOE_ABI_VERSION = 4
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = 1
@@ -24,6 +24,9 @@ MOE_ERR_DEVICE_BOUNDS = 6
 
 MOE_WEIGHTS_MXFP8 = 0
 MOE_WEIGHTS_MXFP4 = 1
+
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
 
 MOE_FLAG_TIMING = 1 << 0
 MOE_FLAG_PATH_GEMV = 1 << 1
@@ -46,6 +49,10 @@ EXPORTED = (
     "moe_plan_status",
     "moe_plan_diagnostics",
     "moe_forward_static_scratch",
+    "moe_qkv_append",
+    "moe_attend_paged_workspace",
+    "moe_attend_paged",
+    "moe_attend_prompt",
     "moe_destroy",
 )
 
@@ -105,6 +112,70 @@ class MoeFusedIO(ctypes.Structure):
     ]
 
 
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + [
+        (n, ctypes.c_int32) for n in ("num_pages", "page_size", "num_kv_heads", "head_dim")]
+
+
+class MoeQkvAppendIO(ctypes.Structure):
+    _fields_ = [
+        ("q", _P), ("k", _P), ("v", _P),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("num_tokens", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_uint32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("rope_positions", ctypes.c_int32),
+        ("rope", _P),
+        ("positions", _P),
+        ("q_norm", _P), ("k_norm", _P),
+        ("norm_eps", ctypes.c_float),
+        ("slots", _P),
+        ("q_out", _P),
+        ("k_out", _P),
+        ("k_cached", _P), ("v_cached", _P),
+    ]
+
+
+class MoeAttendPagedIO(ctypes.Structure):
+    _fields_ = [
+        ("q", _P),
+        ("q_stride", ctypes.c_int64),
+        ("out", _P),
+        ("out_stride", ctypes.c_int64),
+        ("lse", _P),
+        ("page_table", _P),
+        ("lengths", _P),
+        ("cu_rows", _P),
+        ("num_seqs", ctypes.c_int32),
+        ("num_rows", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("dtype", ctypes.c_uint32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class MoeAttendPromptIO(ctypes.Structure):
+    _fields_ = [
+        ("q", _P), ("k", _P), ("v", _P),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("out", _P),
+        ("out_stride", ctypes.c_int64),
+        ("lse", _P),
+        ("cu_rows", _P),
+        ("cu_keys", _P),
+        ("num_seqs", ctypes.c_int32),
+        ("num_rows", ctypes.c_int32), ("num_keys", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_uint32),
+        ("causal", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 _lib = None
 
 
@@ -150,6 +221,16 @@ def load(path: str | None = None):
     lib.moe_forward_static_scratch.restype = ctypes.c_int
     lib.moe_forward_static_scratch.argtypes = [ctypes.POINTER(MoeConfig), ctypes.POINTER(MoeWeights), _P, _P,
                                                ctypes.c_int32, _P, _P, _P]
+    lib.moe_qkv_append.restype = ctypes.c_int
+    lib.moe_qkv_append.argtypes = [ctypes.POINTER(MoeQkvAppendIO), ctypes.POINTER(MoeKvCache), _P, _P]
+    lib.moe_attend_paged_workspace.restype = ctypes.c_int
+    lib.moe_attend_paged_workspace.argtypes = [ctypes.POINTER(MoeAttendPagedIO), ctypes.POINTER(MoeKvCache),
+                                               ctypes.POINTER(ctypes.c_int64)]
+    lib.moe_attend_paged.restype = ctypes.c_int
+    lib.moe_attend_paged.argtypes = [ctypes.POINTER(MoeAttendPagedIO), ctypes.POINTER(MoeKvCache), _P,
+                                     ctypes.c_int64, _P, _P]
+    lib.moe_attend_prompt.restype = ctypes.c_int
+    lib.moe_attend_prompt.argtypes = [ctypes.POINTER(MoeAttendPromptIO), _P, _P]
     lib.moe_destroy.restype = ctypes.c_int
     lib.moe_destroy.argtypes = [_P]
     if lib.moe_abi_version() != MOE_ABI_VERSION:
@@ -280,6 +361,36 @@ def moe_forward_static_scratch(config: MoeConfig, weights: MoeWeights, x, logits
     lib = load()
     return lib.moe_forward_static_scratch(ctypes.byref(config), ctypes.byref(weights), ptr(x), ptr(logits), T, ptr(y),
                                           ptr(d_status), stream_ptr(stream))
+
+
+def moe_qkv_append(io: MoeQkvAppendIO, cache: MoeKvCache | None, d_status=None, stream=None) -> int:
+    """Per-head RMSNorm, rotary positions and the MXFP4 append of keys and values."""
+    lib = load()
+    return lib.moe_qkv_append(ctypes.byref(io), ctypes.byref(cache) if cache is not None else None, ptr(d_status),
+                              stream_ptr(stream))
+
+
+def moe_attend_paged_workspace(io: MoeAttendPagedIO, cache: MoeKvCache) -> int:
+    """Bytes of workspace that moe_attend_paged needs; raises MoeError on a non-OK status."""
+    lib = load()
+    n = ctypes.c_int64()
+    check("moe_attend_paged_workspace",
+          lib.moe_attend_paged_workspace(ctypes.byref(io), ctypes.byref(cache), ctypes.byref(n)))
+    return n.value
+
+
+def moe_attend_paged(io: MoeAttendPagedIO, cache: MoeKvCache, workspace, workspace_bytes: int, d_status=None,
+                     stream=None) -> int:
+    """Attention of the newest rows of each sequence over the paged MXFP4 cache."""
+    lib = load()
+    return lib.moe_attend_paged(ctypes.byref(io), ctypes.byref(cache), ptr(workspace), workspace_bytes,
+                                ptr(d_status), stream_ptr(stream))
+
+
+def moe_attend_prompt(io: MoeAttendPromptIO, d_status=None, stream=None) -> int:
+    """Causal attention over packed prompts."""
+    lib = load()
+    return lib.moe_attend_prompt(ctypes.byref(io), ptr(d_status), stream_ptr(stream))
 
 
 def moe_destroy(plan: int | None) -> int:

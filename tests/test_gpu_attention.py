@@ -1,0 +1,516 @@
+"""The attention calls on the GPU against the 64-bit oracle.
+
+Bounds are derived in ``attention_cases.check_attention`` and beside each test. The 4-bit cache is compared bit for
+bit: the keys' codes are those of the exact formula.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import attention as oa
+from moe_expert_layer_top_gb300 import abi, attention
+from moe_expert_layer_top_gb300.layer import quantize_mxfp4
+
+import attention_cases as ac
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import moe_expert_layer_top_gb300.build as b
+    b.build()
+    abi.load()
+    assert torch.cuda.is_available()
+
+
+def status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ append
+
+APPEND = [
+    # T, heads, kv heads, D, R, interleaved, norms, page, dtype
+    (6, 32, 8, 128, 128, False, True, 64, "bf16"),
+    (1, 1, 1, 128, 64, True, True, 16, "bf16"),
+    (7, 5, 1, 64, 64, False, True, 32, "fp16"),
+    (33, 8, 8, 64, 32, True, True, 16, "bf16"),
+    (19, 12, 4, 128, 48, False, True, 48, "fp16"),    # half of R is not a power of two
+    (5, 6, 2, 128, 112, True, False, 16, "bf16"),     # no norm
+    (40, 3, 3, 64, 0, False, True, 16, "fp16"),       # no rotation
+    (700, 32, 8, 128, 128, False, True, 64, "bf16"),  # one block a token
+    (1500, 16, 2, 64, 16, False, True, 128, "fp16"),
+]
+
+
+def append_case(T, H, K, D, R, dtype, norm, page, seed=0):
+    rng = np.random.default_rng(seed)
+    qkv = ac.rows16(rng, (T, H + 2 * K, D), dtype, 1.7)
+    qn = oa.round16(1 + 0.25 * rng.standard_normal(D), dtype) if norm else None
+    kn = oa.round16(1 + 0.25 * rng.standard_normal(D), dtype) if norm else None
+    pos = rng.integers(0, 50000, T)
+    rope = attention.rope_table(50000, R, device="cpu") if R else None
+    pages = 2 * T // page + 2
+    slots = rng.permutation(pages * page)[:T]
+    return qkv, qn, kn, pos, rope, pages, slots
+
+
+@pytest.mark.parametrize("T,H,K,D,R,inter,norm,page,dtype", APPEND, ids=[f"T{c[0]}_D{c[3]}_R{c[4]}_{c[8]}" for c in APPEND])
+def test_append_matches_the_oracle(T, H, K, D, R, inter, norm, page, dtype):
+    qkv, qn, kn, pos, rope, pages, slots = append_case(T, H, K, D, R, dtype, norm, page)
+    eps = 1e-6
+    x = ac.dev(qkv, dtype)
+    slots[::5] = -1  # some tokens stay out of the cache
+    c = attention.KVCacheMXFP4.empty(pages, page, K, D)
+    for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+        t.fill_(0xA5)
+    st = status()
+    out = attention.qkv_append(x[:, :H], x[:, H:H + K], x[:, H + K:], positions=ac.dev(pos.astype(np.int32)) if R else None,
+                               rope=rope.cuda() if R else None, interleaved=inter,
+                               q_norm=ac.dev(qn, dtype) if norm else None, k_norm=ac.dev(kn, dtype) if norm else None,
+                               eps=eps, cache=c, slots=ac.dev(slots.astype(np.int64)), rotated_keys=True,
+                               cached_values=True, d_status=st)
+    assert st.item() == abi.MOE_OK
+    table = rope.double().numpy()[pos] if R else np.zeros((T, 0))
+    cos, sin = table[:, :R // 2], table[:, R // 2:]
+    eps32 = float(np.float32(eps))
+    q = oa.norm_rotate(qkv[:, :H], qn, eps32, cos, sin, inter)
+    # binary32: 8 + log2(D/8) additions of squares, half of that relative in the root, rsqrt (2 ulp), three products,
+    # two products and a sum of the rotation: 16 roundings of terms no larger than |a| + |b|
+    size = np.abs(q)
+    if R:
+        size = size + np.sqrt((q[..., :R] ** 2).max(-1, keepdims=True)) * np.sqrt(2)
+    bound = ac.HALF_STEP[dtype] * np.abs(q) + 16 * 2.0 ** -24 * size + ac.HALF_TINY[dtype]
+    assert (np.abs(ac.f64(out["q"]) - q) <= bound).all()
+    k = oa.round16(oa.norm_rotate(qkv[:, H:H + K], kn, eps32, cos, sin, inter), dtype)
+    np.testing.assert_array_equal(ac.f64(out["k"]), k)
+    want = {}
+    for name, vals in (("k", k), ("v", qkv[:, H + K:])):
+        codes, scales = oracle.mxfp4_quantize(vals.reshape(T * K, D))
+        kept = oracle.mxfp4_dequantize(codes, scales).reshape(T, K, D)
+        np.testing.assert_array_equal(ac.f64(out[name + "_cached"]), oa.round16(kept, dtype))
+        for part, rows, width in (("codes", codes, D // 2), ("scales", scales, D // 32)):
+            full = np.full((pages, K, page, width), 0xA5, dtype=np.uint8)
+            for t in range(T):
+                if slots[t] >= 0:
+                    full[slots[t] // page, :, slots[t] % page] = rows.reshape(T, K, width)[t]
+            want[f"{name}_{part}"] = full
+    for name, full in want.items():
+        np.testing.assert_array_equal(getattr(c, name).cpu().numpy(), full, err_msg=name)
+
+
+def test_append_codes_are_those_of_the_quantiser():
+    T, K, D = 64, 4, 128
+    x = torch.randn(T, 3 * K, D, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).bfloat16()
+    c = attention.KVCacheMXFP4.empty(4, 16, K, D)
+    out = attention.qkv_append(x[:, :K], x[:, K:2 * K], x[:, 2 * K:], cache=c, slots=torch.arange(T, device="cuda"),
+                               rotated_keys=True)
+    assert torch.equal(out["q"], x[:, :K]) and torch.equal(out["k"], x[:, K:2 * K])  # no norm, no rotation
+    for vals, codes, scales in ((x[:, K:2 * K], c.k_codes, c.k_scales), (x[:, 2 * K:], c.v_codes, c.v_scales)):
+        q, s = quantize_mxfp4(vals.contiguous())
+        assert torch.equal(codes.transpose(1, 2).reshape(T, K, D // 2), q)
+        assert torch.equal(scales.transpose(1, 2).reshape(T, K, D // 32), s)
+
+
+def test_append_special_values():
+    """Zeros, the smallest and largest magnitudes, infinities and NaN: the quantiser's codes, and nothing else moves."""
+    K, D = 1, 64
+    rows = torch.zeros(7, 1, D)
+    rows[1, 0, :4] = torch.tensor([2.0 ** -133, -2.0 ** -130, 2.0 ** -126, 0.0])
+    rows[2, 0, 0], rows[2, 0, 40] = 3.3e38, -3.3e38
+    rows[3, 0, 5] = float("inf")
+    rows[4, 0, 6] = float("nan")
+    rows[5] = -0.0
+    rows[6] = torch.linspace(-6, 6, D)
+    x = rows.bfloat16().cuda()
+    c = attention.KVCacheMXFP4.empty(1, 16, K, D)
+    attention.qkv_append(x, x, x, cache=c, slots=torch.arange(7, device="cuda"))
+    q, s = quantize_mxfp4(x)
+    for codes, scales in ((c.k_codes, c.k_scales), (c.v_codes, c.v_scales)):
+        assert torch.equal(codes[0, 0, :7], q[:, 0]) and torch.equal(scales[0, 0, :7], s[:, 0])
+
+
+def test_append_in_place_and_without_a_cache():
+    T, H, K, D = 9, 4, 2, 64
+    qkv, qn, kn, pos, rope, _, _ = append_case(T, H, K, D, 64, "bf16", True, 16, seed=4)
+    q, k, v = (ac.dev(p, "bf16") for p in (qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:]))
+    kw = dict(positions=ac.dev(pos.astype(np.int32)), rope=rope.cuda(), q_norm=ac.dev(qn, "bf16"))
+    want = attention.qkv_append(q, k, v, **kw)["q"]
+    got = attention.qkv_append(q, k, v, q_out=q, **kw)["q"]
+    assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
+    assert attention.qkv_append(q[:0], k[:0], v[:0])["q"].shape == (0, H, D)
+
+
+def test_append_reports_positions_and_slots_out_of_range():
+    T, K, D = 5, 2, 64
+    x = torch.randn(T, 3 * K, D, device="cuda").bfloat16()
+    rope = attention.rope_table(10, 64)
+    c = attention.KVCacheMXFP4.empty(2, 16, K, D)
+    for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+        t.zero_()
+    q_out = torch.full((T, K, D), 7.0, device="cuda").bfloat16()
+    st = status()
+    attention.qkv_append(x[:, :K], x[:, K:2 * K], x[:, 2 * K:], positions=ac.i32([0, 10, 9, -1, 3]), rope=rope, cache=c,
+                         slots=torch.tensor([3, 4, 32, 5, 31], device="cuda"), q_out=q_out, d_status=st)
+    assert st.item() == abi.MOE_ERR_DEVICE_BOUNDS
+    assert (q_out[[1, 3]] == 7).all() and not (q_out[[0, 2, 4]] == 7).all(-1).any()
+    live = (c.k_codes != 0).any(-1).any(1).flatten().nonzero().flatten().tolist()
+    assert live == [3, 31]
+
+
+# ------------------------------------------------------------------ prompts
+
+PROMPT = [
+    # (rows, keys) of each sequence, heads, kv heads, D, dtype, causal
+    ([(1, 1)], 1, 1, 128, "bf16", True),
+    ([(5, 5), (0, 0), (1, 1), (70, 70)], 4, 2, 64, "bf16", True),
+    ([(33, 33), (127, 127), (128, 128), (129, 129)], 2, 1, 128, "fp16", True),
+    ([(3, 200), (40, 41), (17, 300)], 8, 2, 128, "bf16", True),       # chunks behind a prefix
+    ([(20, 7), (4, 0), (9, 9)], 3, 3, 64, "fp16", True),              # rows without keys
+    ([(20, 7), (4, 0), (65, 140)], 5, 1, 128, "bf16", False),         # no mask
+    ([(257, 257)], 8, 1, 64, "bf16", True),
+    ([(300, 555)], 2, 2, 128, "fp16", True),
+    ([(0, 5), (2, 2)], 16, 1, 128, "bf16", True),
+]
+
+
+def run_prompt(seqs, H, K, D, dtype, causal, seed=0, sigma=1.0, scale=None, check=True):
+    rng = np.random.default_rng(seed)
+    n, m = sum(s[0] for s in seqs), sum(s[1] for s in seqs)
+    q, k, v = ac.rows16(rng, (n, H, D), dtype, 1.5 * sigma), ac.rows16(rng, (m, K, D), dtype, sigma), ac.rows16(rng, (m, K, D), dtype)
+    scale = D ** -0.5 if scale is None else scale
+    cr, ck = ac.offsets([s[0] for s in seqs]), ac.offsets([s[1] for s in seqs])
+    st = status()
+    out, lse = attention.attend_prompt(ac.dev(q, dtype), ac.dev(k, dtype), ac.dev(v, dtype), ac.i32(cr), ac.i32(ck),
+                                       causal=causal, scale=scale, return_lse=True, d_status=st)
+    assert st.item() == abi.MOE_OK
+    if check:
+        for b in range(len(seqs)):
+            r, s = slice(cr[b], cr[b + 1]), slice(ck[b], ck[b + 1])
+            ac.check_attention(out[r], lse[r], q[r], k[s], v[s], scale, dtype, dtype, causal)
+    return out, lse
+
+
+@pytest.mark.parametrize("case", PROMPT, ids=[f"{c[0][0][0]}x{c[0][0][1]}_D{c[3]}_{c[4]}_{'c' if c[5] else 'f'}" for c in PROMPT])
+def test_prompt_matches_the_oracle(case):
+    run_prompt(*case, seed=len(case[0]))
+
+
+@pytest.mark.parametrize("sigma,scale", [(30.0, None), (1.0, 0.0), (1.0, -0.2), (1e-4, None), (1.0, 3.0)])
+def test_prompt_scales(sigma, scale):
+    """Peaked rows, flat rows, a zero and a negative scale."""
+    run_prompt([(150, 150), (10, 60)], 2, 1, 128, "bf16", True, seed=9, sigma=sigma, scale=scale)
+
+
+def test_prompt_strides_and_rows_behind_the_last_sequence():
+    H, K, D, T = 4, 2, 128, 50
+    rng = np.random.default_rng(12)
+    qkv = ac.rows16(rng, (T, H + 2 * K, D), "bf16")
+    x = ac.dev(qkv, "bf16")
+    out = torch.full((T, H + 1, D), 5.0, device="cuda").bfloat16()
+    cu = ac.i32([0, 20, 41])
+    got, lse = attention.attend_prompt(x[:, :H], x[:, H:H + K], x[:, H + K:], cu, cu, out=out[:, :H], return_lse=True)
+    assert (out[41:] == 5).all() and (out[:, H] == 5).all()
+    for a, b in ((0, 20), (20, 41)):
+        ac.check_attention(got[a:b], lse[a:b], qkv[a:b, :H], qkv[a:b, H:H + K], qkv[a:b, H + K:], D ** -0.5, "bf16", "bf16")
+
+
+def test_prompt_nan_of_one_sequence_stays_there():
+    H, K, D = 2, 1, 64
+    x = torch.randn(150, H + 2 * K, D, device="cuda", generator=torch.Generator("cuda").manual_seed(5)).bfloat16()
+    cu = ac.i32([0, 60, 75, 150])
+    want = attention.attend_prompt(x[:, :H], x[:, H:H + K], x[:, H + K:], cu, cu)
+    y = x.clone()
+    y[60:75, H:] = float("nan")
+    y[62, H + K:] = float("inf")
+    got = attention.attend_prompt(y[:, :H], y[:, H:H + K], y[:, H + K:], cu, cu)
+    assert torch.equal(got[:60], want[:60]) and torch.equal(got[75:], want[75:])
+
+
+def test_prompt_nan_in_later_keys_stays_out_of_earlier_rows():
+    """Masked keys have no weight: not even a NaN among them reaches a row."""
+    H, K, D, n = 2, 1, 128, 40
+    x = torch.randn(n, H + 2 * K, D, device="cuda", generator=torch.Generator("cuda").manual_seed(6)).bfloat16()
+    cu = ac.i32([0, n])
+    want = attention.attend_prompt(x[:, :H], x[:, H:H + K], x[:, H + K:], cu, cu)
+    y = x.clone()
+    y[30:, H:H + K] = float("nan")  # keys
+    got = attention.attend_prompt(y[:, :H], y[:, H:H + K], y[:, H + K:], cu, cu)
+    assert torch.equal(got[:30], want[:30])
+
+
+def test_prompt_reports_bad_offsets():
+    x = torch.randn(40, 3, 64, device="cuda").bfloat16()
+    q, k, v = x[:, :1], x[:, 1:2], x[:, 2:]
+    good = attention.attend_prompt(q, k, v, ac.i32([0, 10, 40]), ac.i32([0, 10, 40]))
+    for rows, keys in (([0, 10, 41], [0, 10, 40]), ([0, 10, 40], [0, 10, 50]), ([0, 10, 5], [0, 10, 40]),
+                       ([0, 10, 40], [0, 10, -1]), ([0, 10, 2 ** 31 - 1], [0, 10, 40])):
+        st = status()
+        out = torch.zeros_like(good)
+        attention.attend_prompt(q, k, v, ac.i32(rows), ac.i32(keys), out=out, d_status=st)
+        assert st.item() == abi.MOE_ERR_DEVICE_BOUNDS
+        assert torch.equal(out[:10], good[:10])
+
+
+def test_prompt_offsets_past_32_bits():
+    """The last rows of a tensor of more than 2^31 elements."""
+    H, K, D, T = 32, 8, 128, 700_000
+    q = torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda")
+    kv = torch.empty(T, 2 * K, D, dtype=torch.bfloat16, device="cuda")
+    a, b = T - 130, T - 3
+    gen = torch.Generator("cuda").manual_seed(8)
+    q[a:b] = torch.randn(b - a, H, D, device="cuda", generator=gen)
+    kv[a:b] = torch.randn(b - a, 2 * K, D, device="cuda", generator=gen)
+    cu = ac.i32([a, b])
+    out = torch.zeros_like(q)
+    attention.attend_prompt(q, kv[:, :K], kv[:, K:], cu, cu, out=out)
+    one = ac.i32([0, b - a])
+    want = attention.attend_prompt(q[a:b].clone(), kv[a:b, :K].clone(), kv[a:b, K:].clone(), one, one)
+    assert torch.equal(out[a:b], want) and not out[b:].any() and not out[a - 200:a].any()
+
+
+# ------------------------------------------------------------------ paged cache
+
+PAGED = [
+    # (rows, length) of each sequence, heads, kv heads, D, page, dtype, max_rows
+    ([(1, 1)], 1, 1, 128, 16, "bf16", 1),
+    ([(1, 16), (1, 17), (1, 15), (1, 64), (1, 65)], 4, 1, 128, 16, "bf16", 1),
+    ([(6, 100)], 8, 2, 128, 64, "bf16", 6),
+    ([(6, 6), (6, 300), (6, 129)], 12, 3, 64, 32, "fp16", 6),
+    ([(4, 2), (3, 0), (0, 50), (2, 2), (0, 0)], 4, 2, 128, 16, "bf16", 4),   # rows without keys, sequences without rows
+    ([(1, 700), (2, 63), (8, 200), (3, 1000)], 8, 1, 64, 48, "bf16", 8),
+    ([(1, 900)] * 3, 5, 5, 128, 128, "fp16", 1),
+    ([(40, 500), (1, 31)], 8, 2, 128, 64, "bf16", 1),                         # more rows than announced
+    ([(3, 77)], 64, 1, 64, 16, "fp16", 3),                                    # 192 rows on one kv head
+    ([(2, 1500)], 32, 8, 128, 1024, "bf16", 1000),
+]
+
+
+def run_paged(seqs, H, K, D, page, dtype, max_rows, seed=0, sigma=1.0, vsigma=None):
+    rng = np.random.default_rng(seed)
+    lengths = [s[1] for s in seqs]
+    c = ac.Cache(rng, lengths, K, D, page, sigma=sigma)
+    cr = ac.offsets([s[0] for s in seqs])
+    q = ac.rows16(rng, (cr[-1] + 2, H, D), dtype, 1.5)
+    out = torch.full((cr[-1] + 2, H, D), 3.0, device="cuda").to(ac.TORCH[dtype])
+    st = status()
+    got, lse = attention.attend_paged(ac.dev(q, dtype), c.cache, c.table, ac.i32(lengths), ac.i32(cr), max_rows=max_rows,
+                                      out=out, return_lse=True, d_status=st)
+    assert st.item() == abi.MOE_OK
+    assert (out[cr[-1]:] == 3).all()
+    for b in range(len(seqs)):
+        r = slice(cr[b], cr[b + 1])
+        ac.check_attention(got[r], lse[r], q[r], c.k[b], c.v[b], D ** -0.5, dtype, "fp16")
+    return c, q, got, lse
+
+
+@pytest.mark.parametrize("case", PAGED, ids=[f"{c[0][0][0]}x{c[0][0][1]}_H{c[1]}_D{c[3]}_p{c[4]}_{c[5]}" for c in PAGED])
+def test_paged_matches_the_oracle(case):
+    run_paged(*case, seed=len(case[0]) + case[1])
+
+
+@pytest.mark.parametrize("sigma", [2.0 ** -9, 2.0 ** 6, 20.0])
+def test_paged_scales(sigma):
+    run_paged([(3, 130), (1, 40)], 4, 2, 128, 16, "bf16", 3, seed=20, sigma=sigma)
+
+
+def test_paged_long_sequence():
+    run_paged([(2, 20011)], 4, 1, 128, 64, "bf16", 2, seed=21)
+
+
+def test_paged_value_outliers():
+    """Values 2^12 times the rest in a few tokens, and tiny ones: scales far apart within a tile."""
+    rng = np.random.default_rng(22)
+    n, H, K, D = 300, 4, 1, 128
+    c = ac.Cache(rng, [n], K, D, 16)
+    s = c.cache.v_scales
+    table = c.table[0].long()
+    for j, shift in ((7, 12), (100, 9), (101, -12), (250, 12)):
+        s[table[j // 16], :, j % 16] += shift
+        c.v[0][j] *= 2.0 ** shift
+    q = ac.rows16(rng, (2, H, D), "bf16", 1.5)
+    out, lse = attention.attend_paged(ac.dev(q, "bf16"), c.cache, c.table, ac.i32([n]), ac.i32([0, 2]), return_lse=True)
+    ac.check_attention(out, lse, q, c.k[0], c.v[0], D ** -0.5, "bf16", "fp16")
+
+
+def test_paged_strides():
+    rng = np.random.default_rng(23)
+    H, K, D = 8, 2, 64
+    c = ac.Cache(rng, [90, 33], K, D, 32)
+    q = ac.rows16(rng, (5, H + 3, D), "fp16", 1.5)
+    out = torch.full((5, H + 2, D), 3.0, device="cuda").half()
+    x = ac.dev(q, "fp16")
+    got, lse = attention.attend_paged(x[:, 1:H + 1], c.cache, c.table, ac.i32([90, 33]), ac.i32([0, 2, 5]), out=out[:, :H],
+                                      return_lse=True, max_rows=3)
+    assert (out[:, H:] == 3).all()
+    for b, r in ((0, slice(0, 2)), (1, slice(2, 5))):
+        ac.check_attention(got[r], lse[r], q[r, 1:H + 1], c.k[b], c.v[b], D ** -0.5, "fp16", "fp16")
+
+
+def test_paged_repeats_bit_for_bit():
+    c, q, got, lse = run_paged([(6, 777), (2, 1200), (1, 30)], 8, 2, 128, 64, "bf16", 6, seed=24)
+    x = ac.dev(q, "bf16")
+    for _ in range(3):
+        again, z = attention.attend_paged(x[:9], c.cache, c.table, ac.i32([777, 1200, 30]), ac.i32([0, 6, 8, 9]), max_rows=6,
+                                          return_lse=True)
+        assert torch.equal(again, got[:9]) and torch.equal(z, lse[:9])
+
+
+def test_paged_reports_bad_pages_lengths_and_offsets():
+    rng = np.random.default_rng(25)
+    H, K, D = 4, 1, 128
+    lengths = [70, 40]
+    c = ac.Cache(rng, lengths, K, D, 16)
+    q = torch.randn(4, H, D, device="cuda").bfloat16()
+    cu = ac.i32([0, 2, 4])
+    good = attention.attend_paged(q, c.cache, c.table, ac.i32(lengths), cu)
+    bad_page, negative = c.table.clone(), c.table.clone()
+    bad_page[1, 2], negative[1, 0] = 10 ** 6, -1
+    for table, lens, rows in ((bad_page, lengths, [0, 2, 4]), (negative, lengths, [0, 2, 4]),
+                              (c.table, [70, 10 ** 8], [0, 2, 4]), (c.table, [70, -5], [0, 2, 4]),
+                              (c.table, lengths, [0, 2, 9]), (c.table, lengths, [0, 2, 1])):
+        st = status()
+        out = attention.attend_paged(q, c.cache, table, ac.i32(lens), ac.i32(rows), d_status=st)
+        assert st.item() == abi.MOE_ERR_DEVICE_BOUNDS
+        assert torch.equal(out[:2], good[:2])
+
+
+def test_paged_offsets_past_32_bits():
+    """Pages beyond 2^31 bytes of codes."""
+    H, K, D, page, pages = 4, 8, 128, 64, 90_000
+    c = attention.KVCacheMXFP4.empty(pages, page, K, D)
+    small = attention.KVCacheMXFP4.empty(2, page, K, D)
+    gen = torch.Generator("cuda").manual_seed(26)
+    for a, b in ((small.k_codes, c.k_codes), (small.v_codes, c.v_codes)):
+        a.copy_(torch.randint(0, 256, a.shape, device="cuda", generator=gen))
+        b[-2:] = a
+    for a, b in ((small.k_scales, c.k_scales), (small.v_scales, c.v_scales)):
+        a.copy_(torch.randint(122, 128, a.shape, device="cuda", generator=gen))
+        b[-2:] = a
+    q = torch.randn(1, 2 * K, D, device="cuda", generator=gen).bfloat16()
+    far = attention.attend_paged(q, c, ac.i32([[pages - 2, pages - 1]]), ac.i32([100]), ac.i32([0, 1]))
+    near = attention.attend_paged(q, small, ac.i32([[0, 1]]), ac.i32([100]), ac.i32([0, 1]))
+    assert torch.equal(far, near)
+    # and an append there
+    x = torch.randn(1, 3 * K, D, device="cuda", generator=gen).bfloat16()
+    attention.qkv_append(x[:, :K], x[:, K:2 * K], x[:, 2 * K:], cache=c,
+                         slots=torch.tensor([pages * page - 1], device="cuda"))
+    codes, scales = quantize_mxfp4(x[:, 2 * K:].contiguous())
+    assert torch.equal(c.v_codes[-1, :, -1], codes[0]) and torch.equal(c.v_scales[-1, :, -1], scales[0])
+
+
+# ------------------------------------------------------------------ streams, graphs, a run of all
+
+def test_other_streams_and_concurrent_calls():
+    """Two streams at once, each with its own workspace, against the same calls one by one."""
+    rng = np.random.default_rng(30)
+    cases = []
+    for lengths in ([3000, 100, 40], [50, 2500]):
+        c = ac.Cache(rng, lengths, 2, 128, 64)
+        q = torch.randn(len(lengths) * 2, 8, 128, device="cuda").bfloat16()
+        cases.append((q, c.cache, c.table, ac.i32(lengths), ac.i32([2 * i for i in range(len(lengths) + 1)])))
+    want = [attention.attend_paged(*x, max_rows=2) for x in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [attention.attend_paged(*x, max_rows=2, stream=s) for x, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
+def test_graph_replay_follows_lengths_and_two_graphs_do_not_share():
+    rng = np.random.default_rng(31)
+    H, K, D, page = 8, 2, 128, 16
+    c = ac.Cache(rng, [1000, 333], K, D, page)
+    q = torch.randn(4, H, D, device="cuda").bfloat16()
+    lens, cu = ac.i32([1000, 333]), ac.i32([0, 2, 4])
+    calls = [(q, 2), (q * 0.5, 2)]
+    for x, r in calls:
+        attention.attend_paged(x, c.cache, c.table, lens, cu, max_rows=r)  # warm up before the capture
+    graphs, outs = [], []
+    for x, r in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(attention.attend_paged(x, c.cache, c.table, lens, cu, max_rows=r))
+        graphs.append(g)
+    for a, b in ((1000, 333), (17, 300), (0, 1), (999, 2)):
+        lens.copy_(torch.tensor([a, b], dtype=torch.int32))
+        want = [attention.attend_paged(x, c.cache, c.table, lens, cu, max_rows=r) for x, r in calls]
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for s, g in zip((s1, s2), graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
+def test_prompt_in_a_graph():
+    x = torch.randn(300, 6, 128, device="cuda").bfloat16()
+    cu = ac.i32([0, 100, 300])
+    want = attention.attend_prompt(x[:, :4], x[:, 4:5], x[:, 5:], cu, cu)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = attention.attend_prompt(x[:, :4], x[:, 4:5], x[:, 5:], cu, cu)
+    out.zero_()
+    g.replay()
+    assert torch.equal(out, want)
+
+
+def test_layer_prompt_then_verify_steps():
+    """A layer as a server runs it: a prompt through append and prompt attention, then steps of six rows through
+    append, paged attention and the MoE step; the paged rows equal prompt attention over the cached values."""
+    from moe_expert_layer_top_gb300 import synthetic
+    from moe_expert_layer_top_gb300.layer import MoEStep
+    gen = torch.Generator("cuda").manual_seed(40)
+    H, K, D, page = 8, 2, 64, 16
+    hidden = H * D
+    lens = [45, 18]
+    pages = [list(range(0, 5)), list(range(5, 10))]
+    c = attention.KVCacheMXFP4.empty(10, page, K, D)
+    table = ac.i32(pages)
+    rope = attention.rope_table(200, D)
+    kn = torch.ones(D, device="cuda").bfloat16()
+    w = synthetic.make_weights(5, 8, hidden, 256)
+    step = MoEStep(hidden, 256, 8, 2, w, 12)
+    keys, values = [[], []], [[], []]
+
+    def rows(counts, starts):
+        n = sum(counts)
+        x = torch.randn(n, H + 2 * K, D, device="cuda", generator=gen).bfloat16()
+        pos = torch.cat([torch.arange(s, s + k) for s, k in zip(starts, counts)])
+        slot = torch.tensor([pages[b][p // page] * page + p % page for b in range(2) for p in
+                             range(starts[b], starts[b] + counts[b])], device="cuda")
+        st = status()
+        o = attention.qkv_append(x[:, :H], x[:, H:H + K], x[:, H + K:], positions=pos.int().cuda(), rope=rope,
+                                 q_norm=kn, k_norm=kn, cache=c, slots=slot, cached_values=True, d_status=st)
+        assert st.item() == abi.MOE_OK
+        at = ac.offsets(counts)
+        for b in range(2):
+            keys[b].append(o["k_cached"][at[b]:at[b + 1]])
+            values[b].append(o["v_cached"][at[b]:at[b + 1]])
+        return o, at
+
+    o, at = rows(lens, [0, 0])
+    y = attention.attend_prompt(o["q"], o["k_cached"], o["v_cached"], ac.i32(at), ac.i32(at))
+    assert torch.isfinite(y).all()
+    for _ in range(3):
+        o, at = rows([6, 6], lens)
+        lens = [n + 6 for n in lens]
+        y, lse = attention.attend_paged(o["q"], c, table, ac.i32(lens), ac.i32(at), max_rows=6, return_lse=True)
+        for b in range(2):
+            ac.check_attention(y[at[b]:at[b + 1]], lse[at[b]:at[b + 1]], ac.f64(o["q"][at[b]:at[b + 1]]),
+                               ac.f64(torch.cat(keys[b])), ac.f64(torch.cat(values[b])), D ** -0.5, "bf16", "fp16")
+        # the same rows by prompt attention over the cached values: both within their bounds of the same result
+        far = attention.attend_prompt(o["q"], torch.cat(keys[0] + keys[1]), torch.cat(values[0] + values[1]), ac.i32(at),
+                                      ac.i32(ac.offsets(lens)))
+        assert (far.float() - y.float()).abs().max() <= 4 * 2.0 ** -8 * max(1.0, y.float().abs().max().item())
+        x = y.reshape(12, hidden)
+        out = step.forward_fused(x, w_router=torch.randn(8, hidden, device="cuda", generator=gen).bfloat16(),
+                                 resid=x.view(12, 1, hidden).clone(), norm_weight=torch.ones(hidden, device="cuda").bfloat16())
+        assert torch.isfinite(out["y"]).all()
+    step.close()
