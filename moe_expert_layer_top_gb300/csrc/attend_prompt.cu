@@ -1,58 +1,562 @@
-// attend_prompt.cu — causal attention over packed prompts with grouped heads.
+// attend_prompt.cu — causal attention over packed prompts, on the 5th-generation tensor cores.
+//
+// Mathematics. For each row: s_j = scale q . k_j over the keys it sees,
+// o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m). One pass over the keys in
+// tiles of 128 keeps a reference m and the two sums. The reference only moves
+// when the running maximum has grown by more than 2^8 in the exponent: until
+// then the terms are at most 2^8, which neither binary32 sums nor 16-bit P can
+// overflow, so the accumulator is rarely rescaled. P is rounded to the
+// inputs' type for the second product (half a step, 2^-9 or 2^-12 in the root
+// mean square of a row: what the output's own rounding costs); sums are binary32.
+//
+// Bound. 4 D flops per (row, head, key) against 16-bit inputs read once: the
+// tensor pipe, for all but the shortest prompts.
+//
+// Layout. A row of the tile is a (token, head) pair: the G heads of a kv head's
+// group are packed, r = token * G + head, so one key tile serves all of them and
+// short prompts still fill the 128 rows of an MMA. A block takes two row tiles A
+// and B of 128. While the tensor cores work for one, the softmax of the other
+// runs on the CUDA cores:
+//   warps 0-3   softmax of tile A, one row (TMEM lane) a thread
+//   warps 4-7   softmax of tile B
+//   warp 8      TMA: K and V tiles of 128 keys into a ring of shared memory;
+//               at the end it zeroes the rows of the last V tile that lie past
+//               the sequence (they belong to the next one, and 0 * NaN is NaN)
+//   warp 9      MMA issuer (one lane): S = Q K^T (both operands from shared memory), then
+//               O += P V with P from TMEM, where the softmax wrote it over S
+// TMEM: S of A and B (128 columns each), O of A and B (D columns each).
+// The MMAs of one thread run in the order of issue. So when S of tile j + 1 is
+// complete, O holds every tile up to j, and the softmax may rescale it in place.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
-#include "attend_simple.cuh"
+#include "attention.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
 namespace {
 
-template <class T>
-struct PromptSource {
-  const uint16_t *k, *v;
-  int64_t k_stride, v_stride;
-  const int32_t *cu_keys;
-  int num_keys;
+constexpr int kRows = 128;     // rows of a tile (MMA M, TMEM lanes)
+constexpr int kKeys = 128;     // keys of a tile
+constexpr int kSoftmaxThreads = 256, kThreads = 384;  // three warpgroups; two warps of the last have no work
+// Registers: 168 a thread at launch (384 x 168 = 64,512). The softmax keeps a
+// row of 128 scores, so the last warpgroup hands most of its share to the other
+// two: 2 x 128 x 224 + 128 x 56 = 64,512.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 224, kRegsOther = 56;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "register split");
+constexpr int kWarpLoad = 8, kWarpMma = 9;
+constexpr uint32_t kTmemCols = 512, kColO = 256;
+constexpr int64_t kWaitNs = 1000000000;  // bound of every wait
+constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
 
-  __device__ int keys(int b, int n, int, int32_t *status, int *first) const {
-    const Span s = seq_span(cu_keys, b, num_keys, status);
-    *first = s.first;
-    return s.n;
-  }
-
-  template <int D>
-  __device__ bool load(bool value, int, int kv, int j, int i, float2 *out, int32_t *) const {
-    const uint32_t w = *reinterpret_cast<const uint32_t *>((value ? v + j * v_stride : k + j * k_stride) + kv * D + 2 * i);
-    *out = make_float2(T::lo(w), T::hi(w));
-    return true;
-  }
+struct PromptArgs {
+  const uint16_t *q;
+  int64_t q_stride;
+  uint16_t *out;
+  int64_t out_stride;
+  float *lse;
+  const int32_t *cu_rows, *cu_keys;
+  int num_seqs, num_rows, num_keys, num_heads, group, causal;
+  float scale2;    // |scale| log2 e, at least 2^-100: scores times this are exponents of two
+  uint32_t flip;   // 0x80008000 with a negative scale: the queries are negated
+  int32_t *status;
 };
+
+template <int D>
+struct Smem {
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of Q, K or V: D/64 parts of 128 rows x 128 bytes
+  uint8_t q[2][kTileBytes];
+  uint8_t kv[kStages][kTileBytes];
+  uint64_t q_full;           // 256 arrivals
+  uint64_t full[kStages];    // a K or V tile landed
+  uint64_t empty[kStages];   // the MMAs that read it are done
+  uint64_t tail;             // the last V tile is zeroed past the sequence's end
+  uint64_t s_full[2];        // S of a tile complete
+  uint64_t p_full[2];        // P written (4 warps)
+  uint64_t o_full[2];        // the last MMA into O of a tile is done
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int seq, local, tiles;
+  static constexpr size_t kBytes = 2 * kTileBytes + kStages * kTileBytes + 512 + 1024;
+};
+
+// ------------------------------------------------------------------ PTX wrappers
+
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// D (+)= A B^T for K = 16 values of 16 bits, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with A in TMEM (two values per 32-bit column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of V as the N-major B operand: 64 values of N (128 bytes) by 8
+// keys is one swizzled block of 1024 bytes; blocks of the next 8 keys follow
+// (stride offset), the next 64 values of N lie a part (128 keys) further
+// (leading offset).
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  return (sw128_desc(saddr) & ~(uint64_t(0x3FFFu) << 16)) | (uint64_t(kKeys * 128 >> 4) << 16);
+}
+
+// 32 consecutive columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Every load of this thread has its values. The registers pass through, so
+// that no use of them moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------------------------ the block's work
+
+struct Work {
+  int row0, rows;    // the sequence's first row, its rows times group
+  int key0, keys;    // its first key, its keys
+  int n;             // its query rows
+  int r0;            // the block's first (row, head) pair
+  int kv;            // kv head
+  int tiles[2];      // key tiles of row tiles A and B
+};
+
+// Keys that pair r sees.
+__device__ __forceinline__ int key_limit(const PromptArgs &a, const Work &w, int r) {
+  if (r >= w.rows) return 0;
+  return a.causal ? min(w.keys, max(0, w.keys - w.n + r / a.group + 1)) : w.keys;
+}
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (mbar_wait(bar, parity, kWaitNs)) return true;
+  if (status) report_error(status, MOE_ERR_TIMEOUT);
+  return false;
+}
+
+// ------------------------------------------------------------------ TMA (warp 8)
+
+template <int D>
+__device__ void load_warp(const CUtensorMap *kmap, const CUtensorMap *vmap, const PromptArgs &a, Smem<D> &sm,
+                          const Work &w, int n) {
+  using S = Smem<D>;
+  const int lane = threadIdx.x & 31;
+  int issued = 0;
+  if (lane == 0) {
+    for (int i = 0; i < 2 * n; ++i) {  // K 0, V 0, K 1, V 1, ...
+      const int s = i % S::kStages;
+      if (!wait(&sm.empty[s], ((i / S::kStages) & 1) ^ 1, a.status)) break;
+      mbar_arrive_expect_tx(&sm.full[s], S::kTileBytes);
+      const CUtensorMap *map = i & 1 ? vmap : kmap;
+#pragma unroll
+      for (int p = 0; p < D / 64; ++p)
+        tma_load(sm.kv[s] + p * (kKeys * 128), map, w.kv * D + 64 * p, w.key0 + (i >> 1) * kKeys, &sm.full[s]);
+      ++issued;
+    }
+  }
+  issued = __shfl_sync(0xFFFFFFFFu, issued, 0);
+  const int cut = w.keys - (n - 1) * kKeys;  // keys of the last tile
+  if (issued == 2 * n && cut < kKeys) {
+    const int i = 2 * n - 1, s = i % S::kStages;
+    if (wait(&sm.full[s], (i / S::kStages) & 1, a.status)) {
+      for (int p = 0; p < D / 64; ++p)
+        for (int c = cut * 8 + lane; c < kKeys * 8; c += 32)
+          *reinterpret_cast<uint4 *>(sm.kv[s] + p * (kKeys * 128) + c * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.tail);
+    }
+  }
+  // no copy may be in flight when the block exits
+  for (int j = 1; j <= S::kStages && j <= issued; ++j) {
+    const int i = issued - j;
+    mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, kWaitNs);
+  }
+}
+
+// ------------------------------------------------------------------ MMA issuer (one lane of warp 9)
+
+template <class T, int D>
+__device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, int n, uint32_t tmem) {
+  using S = Smem<D>;
+  constexpr uint32_t kType = T::kMmaType;
+  constexpr uint32_t kBase = (1u << 4) | (kType << 7) | (kType << 10) | (uint32_t(kRows >> 4) << 24);
+  constexpr uint32_t kDescS = kBase | (uint32_t(kKeys >> 3) << 17);
+  constexpr uint32_t kDescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);  // B is N-major
+  bool ok = wait(&sm.q_full, 0, a.status);
+  const auto landed = [&](int i) { return wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, a.status); };
+  const auto scores = [&](int x, int j) {  // S of row tile x, key tile j
+    const uint32_t q = smem_u32(sm.q[x]), k = smem_u32(sm.kv[(2 * j) % S::kStages]);
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p) {
+      const uint64_t qd = sw128_desc(q + p * (kRows * 128)), kd = sw128_desc(k + p * (kKeys * 128));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // 16 values are 32 bytes: 2 in the descriptor's address field
+        mma_ss(tmem + x * kKeys, qd + 2 * i, kd + 2 * i, kDescS, (p | i) != 0);
+    }
+    mma_commit(&sm.s_full[x]);
+  };
+  if (ok) ok = landed(0);
+  if (ok) {
+    tmem_fence_after();
+    for (int x = 0; x < 2; ++x)
+      if (w.tiles[x] > 0) scores(x, 0);
+    mma_commit(&sm.empty[0]);
+  }
+  for (int j = 0; ok && j < n; ++j) {
+    const int vi = 2 * j + 1;
+    ok = landed(vi);
+    if (ok && j + 1 == n && w.keys < n * kKeys) ok = wait(&sm.tail, 0, a.status);
+    bool next = false;  // the next K tile has landed
+    for (int x = 0; ok && x < 2; ++x) {
+      if (j >= w.tiles[x]) continue;
+      ok = wait(&sm.p_full[x], j & 1, a.status);
+      if (!ok) break;
+      tmem_fence_after();
+      const uint64_t vd = v_desc(smem_u32(sm.kv[vi % S::kStages]));
+#pragma unroll
+      for (int i = 0; i < kKeys / 16; ++i)  // 16 keys: 8 columns of P, 2048 bytes of V
+        mma_ts(tmem + kColO + x * D, tmem + x * kKeys + 8 * i, vd + i * (2048 >> 4), kDescO, (j | i) != 0);
+      if (j + 1 < w.tiles[x]) {
+        if (!next) ok = next = landed(vi + 1);
+        if (!ok) break;
+        scores(x, j + 1);
+      } else {
+        mma_commit(&sm.o_full[x]);
+      }
+    }
+    mma_commit(&sm.empty[vi % S::kStages]);
+    if (j + 1 < n) mma_commit(&sm.empty[(vi + 1) % S::kStages]);
+  }
+  mma_commit(&sm.mma_done);  // every MMA is done before TMEM is freed
+  mbar_wait(&sm.mma_done, 0, kWaitNs);
+}
+
+// ------------------------------------------------------------------ softmax (warps 0-7)
+
+template <class T, int D>
+__device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
+  const int x = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
+  const int first = w.r0 + x * kRows;
+  // Q of the tile into the swizzled K-major layout: 16 bytes a thread and round, a row side by side
+  {
+    constexpr int kChunks = D / 8, kStep = 128 / kChunks;
+    const int c = row % kChunks;
+    uint8_t *dst = sm.q[x] + (c >> 3) * (kRows * 128);
+#pragma unroll 8
+    for (int i = row / kChunks; i < kRows; i += kStep) {
+      const int r = first + i;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < w.rows) {
+        const int t = r / a.group, h = r - t * a.group;
+        v = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(w.row0 + t) * a.q_stride +
+                                                  (int64_t(w.kv) * a.group + h) * D) + c);
+        v.x ^= a.flip;
+        v.y ^= a.flip;
+        v.z ^= a.flip;
+        v.w ^= a.flip;
+      }
+      *reinterpret_cast<uint4 *>(dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
+    }
+    fence_proxy_async();
+    mbar_arrive(&sm.q_full);
+  }
+  const int r = first + row;
+  const int limit = key_limit(a, w, r);
+  const uint32_t lanes = uint32_t(warp * 32) << 16;
+  const uint32_t ts = tmem + lanes + x * kKeys, to = tmem + lanes + kColO + x * D;
+  float ref = 0.0f, total = 0.0f;  // the reference in score units
+  bool ok = true;
+  for (int j = 0; j < w.tiles[x]; ++j) {
+    ok = wait(&sm.s_full[x], j & 1, a.status);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (!ok) break;
+    tmem_fence_after();
+    uint32_t s[kKeys];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_wait_ld(s + 32 * i);
+    const int lim = limit - j * kKeys;
+    if (__any_sync(0xFFFFFFFFu, lim < kKeys)) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (i >= lim) s[i] = 0xFF800000u;  // -inf
+    }
+    float mx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+    for (int i = 4; i < kKeys; i += 8)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float u = __uint_as_float(s[i + c]);
+        mx[c] = i + c + 4 < kKeys ? fmaxf(mx[c], fmaxf(u, __uint_as_float(s[i + c + 4]))) : fmaxf(mx[c], u);
+      }
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    if (j == 0) {
+      ref = top == -INFINITY ? 0.0f : top;
+    } else {
+      const bool move = (top - ref) * a.scale2 > kLazy;
+      if (__any_sync(0xFFFFFFFFu, move)) {
+        const float f = move ? exp2_approx((ref - top) * a.scale2) : 1.0f;
+        if (move) ref = top;
+        total *= f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * i, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+          tmem_st32(to + 32 * i, o);
+        }
+      }
+    }
+    const float base = -ref * a.scale2;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t p[kKeys / 2];
+#pragma unroll
+    for (int i = 0; i < kKeys; i += 2) {
+      const float u = exp2_approx(fmaf(__uint_as_float(s[i]), a.scale2, base));
+      const float v = exp2_approx(fmaf(__uint_as_float(s[i + 1]), a.scale2, base));
+      sum[(i >> 1) & 3] += u + v;
+      p[i / 2] = T::pack(u, v);
+    }
+    tmem_st32(ts, p);
+    tmem_st32(ts + 32, p + 32);
+    total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    tmem_wait_st();
+    tmem_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.p_full[x]);
+  }
+  if (!ok) return;
+  if (w.tiles[x] > 0) {
+    ok = wait(&sm.o_full[x], 0, a.status);
+    if (!__all_sync(0xFFFFFFFFu, ok)) return;
+    tmem_fence_after();
+  }
+  const bool real = r < w.rows;
+  const int t = r / a.group, h = w.kv * a.group + r - t * a.group;
+  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  uint16_t *out = a.out + int64_t(w.row0 + t) * a.out_stride + int64_t(h) * D;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    uint32_t o[32];
+    if (w.tiles[x] > 0) {
+      tmem_ld32(to + 32 * i, o);
+      tmem_wait_ld(o);
+    }
+    if (!real) continue;
+    const bool any = limit > 0;  // a row without keys has no accumulator of its own
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = any ? T::pack(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv) : 0u;
+      *reinterpret_cast<uint4 *>(out + 32 * i + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  if (real && a.lse)
+    a.lse[int64_t(w.row0 + t) * a.num_heads + h] =
+        total > 0.0f ? (log2f(total) + ref * a.scale2) * 0.6931471805599453f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                                    const __grid_constant__ CUtensorMap vmap,
+                                                                    const PromptArgs a) {
+  extern __shared__ unsigned char prompt_smem_raw[];
+  using S = Smem<D>;
+  static_assert(sizeof(S) + 1024 <= S::kBytes && S::kBytes <= 227 * 1024, "shared memory budget");
+  S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    const TileAt at = find_tile(a.cu_rows, a.num_seqs, a.num_rows, a.group, 2 * kRows, blockIdx.x, a.status);
+    if (lane == 0) {
+      sm.seq = at.seq;
+      sm.local = at.local;
+      sm.tiles = at.tiles;
+      mbar_init(&sm.q_full, kSoftmaxThreads);
+      for (int i = 0; i < S::kStages; ++i) {
+        mbar_init(&sm.full[i], 1);
+        mbar_init(&sm.empty[i], 1);
+      }
+      mbar_init(&sm.tail, 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&sm.s_full[x], 1);
+        mbar_init(&sm.p_full[x], 4);
+        mbar_init(&sm.o_full[x], 1);
+      }
+      mbar_init(&sm.mma_done, 1);
+      fence_mbar_init();
+    }
+  }
+  __syncthreads();
+  if (sm.seq < 0) return;  // past the last tile: the whole block
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  Work w;
+  const Span rows = seq_span(a.cu_rows, sm.seq, a.num_rows, nullptr);
+  const Span keys = seq_span(a.cu_keys, sm.seq, a.num_keys, a.status);
+  w.row0 = rows.first;
+  w.n = rows.n;
+  w.rows = rows.n * a.group;
+  w.key0 = keys.first;
+  w.keys = keys.n;
+  w.kv = blockIdx.y;
+  w.r0 = (sm.tiles - 1 - sm.local) * (2 * kRows);  // the last rows see the most keys: they start first
+  for (int x = 0; x < 2; ++x) {
+    const int first = w.r0 + x * kRows;
+    w.tiles[x] = first < w.rows ? (key_limit(a, w, min(first + kRows, w.rows) - 1) + kKeys - 1) / kKeys : 0;
+  }
+  const int n = max(w.tiles[0], w.tiles[1]);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  if (warp < kWarpLoad) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax_warps<T, D>(a, sm, w, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (n > 0 && warp == kWarpLoad) load_warp<D>(&kmap, &vmap, a, sm, w, n);
+    if (n > 0 && warp == kWarpMma && lane == 0) mma_lane<T, D>(a, sm, w, n, tmem);
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == kWarpMma)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// ------------------------------------------------------------------ host
+
+// Boxes of 128 keys x 64 values, 128-byte swizzle, over [keys][kv heads * D] with the caller's row stride.
+bool encode(CUtensorMap *map, const void *base, uint64_t keys, uint64_t width, int64_t stride) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {width, keys}, strides[1] = {uint64_t(stride) * 2};
+  const cuuint32_t box[2] = {64, kKeys}, estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int D>
+cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const PromptArgs &a, int kv_heads,
+                   cudaStream_t st) {
+  const int64_t tiles = int64_t(a.num_rows) * a.group / (2 * kRows) + a.num_seqs;
+  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+  // The register split above assumes the launch's share: a build that gave the kernel less must not run.
+  static const bool split = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, attend_prompt_kernel<T, D>) == cudaSuccess && at.numRegs == kRegsLaunch;
+  }();
+  if (!split) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(Smem<D>::kBytes));
+  if (e != cudaSuccess) return e;
+  attend_prompt_kernel<T, D>
+      <<<dim3(unsigned(tiles), unsigned(kv_heads)), kThreads, Smem<D>::kBytes, st>>>(kmap, vmap, a);
+  return cudaGetLastError();
+}
 
 }  // namespace
 
 cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *status, int num_sms, cudaStream_t st) {
-  SimpleArgs a = {};
+  PromptArgs a = {};
   a.q = static_cast<const uint16_t *>(io.q);
   a.q_stride = io.q_stride;
   a.out = static_cast<uint16_t *>(io.out);
   a.out_stride = io.out_stride;
   a.lse = io.lse;
   a.cu_rows = io.cu_rows;
+  a.cu_keys = io.cu_keys;
   a.num_seqs = io.num_seqs;
   a.num_rows = io.num_rows;
+  a.num_keys = io.num_keys;
   a.num_heads = io.num_heads;
-  a.num_kv_heads = io.num_kv_heads;
+  a.group = io.num_heads / io.num_kv_heads;
   a.causal = io.causal;
-  a.scale = io.scale;
+  a.scale2 = fmaxf(fabsf(io.scale) * 1.4426950408889634f, 0x1p-100f);
+  a.flip = io.scale < 0.0f ? 0x80008000u : 0u;
   a.status = status;
-  const auto *k = static_cast<const uint16_t *>(io.k), *v = static_cast<const uint16_t *>(io.v);
-  if (io.dtype == MOE_DTYPE_F16) {
-    const PromptSource<F16> src = {k, v, io.k_stride, io.v_stride, io.cu_keys, io.num_keys};
-    return launch_simple(a, src, io.head_dim, io.dtype, st);
+  CUtensorMap kmap, vmap;
+  memset(&kmap, 0, sizeof kmap);
+  memset(&vmap, 0, sizeof vmap);
+  if (io.num_keys) {
+    const uint64_t width = uint64_t(io.num_kv_heads) * io.head_dim;
+    if (!encode(&kmap, io.k, io.num_keys, width, io.k_stride) || !encode(&vmap, io.v, io.num_keys, width, io.v_stride))
+      return cudaErrorInvalidValue;
   }
-  const PromptSource<Bf16> src = {k, v, io.k_stride, io.v_stride, io.cu_keys, io.num_keys};
-  return launch_simple(a, src, io.head_dim, io.dtype, st);
+  const bool h = io.dtype == MOE_DTYPE_F16;
+  if (io.head_dim == 64)
+    return h ? launch<F16, 64>(kmap, vmap, a, io.num_kv_heads, st) : launch<Bf16, 64>(kmap, vmap, a, io.num_kv_heads, st);
+  return h ? launch<F16, 128>(kmap, vmap, a, io.num_kv_heads, st) : launch<Bf16, 128>(kmap, vmap, a, io.num_kv_heads, st);
 }
 
 }  // namespace moe

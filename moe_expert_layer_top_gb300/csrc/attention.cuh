@@ -20,7 +20,7 @@ __device__ __forceinline__ void out_of_range(int32_t *status) {
 // ------------------------------------------------------------------ 16-bit types
 
 struct Bf16 {
-  using T = __nv_bfloat16;
+  static constexpr uint32_t kMmaType = 1;  // operand type of the tensor-core instruction descriptor
   static __device__ __forceinline__ float lo(uint32_t v) { return __uint_as_float(v << 16); }
   static __device__ __forceinline__ float hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
   static __device__ __forceinline__ uint32_t pack(float a, float b) {  // a in the low half
@@ -30,7 +30,7 @@ struct Bf16 {
 };
 
 struct F16 {
-  using T = __half;
+  static constexpr uint32_t kMmaType = 0;
   static __device__ __forceinline__ float lo(uint32_t v) {
     return __low2float(*reinterpret_cast<const __half2 *>(&v));
   }
@@ -68,6 +68,33 @@ __device__ __forceinline__ int warp_inclusive_sum(int v) {
     if (lane >= d) v += u;
   }
   return v;
+}
+
+// The sequence that tile number `tile` falls into, when sequence b has
+// ceil(n_b * group / rows) tiles of `rows` (row, head) pairs. Called by a whole warp; seq = -1: past the last tile.
+struct TileAt {
+  int seq, local, tiles;  // sequence, tile within it, its tiles
+};
+
+__device__ __forceinline__ TileAt find_tile(const int32_t *cu, int num_seqs, int num_rows, int group, int rows,
+                                            int64_t tile, int32_t *status) {
+  const int lane = threadIdx.x & 31;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < num_seqs; b0 += 32) {
+    const int b = b0 + lane;
+    const int n = b < num_seqs ? seq_span(cu, b, num_rows, status).n : 0;
+    const int tiles = int((int64_t(n) * group + rows - 1) / rows);
+    const int64_t end = base + warp_inclusive_sum(tiles);
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, tile < end);
+    if (hit) {
+      const int w = __ffs(hit) - 1;
+      const int mine = __shfl_sync(0xFFFFFFFFu, tiles, w);
+      const int64_t stop = __shfl_sync(0xFFFFFFFFu, end, w);
+      return {b0 + w, int(tile - (stop - mine)), mine};
+    }
+    base = __shfl_sync(0xFFFFFFFFu, end, 31);
+  }
+  return {-1, 0, 0};
 }
 
 }  // namespace moe

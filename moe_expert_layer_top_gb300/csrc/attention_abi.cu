@@ -68,6 +68,7 @@ moe_status_t paged_sizes_ok(const moe_attend_paged_io_t &io, const moe_kv_cache_
   if (io.num_seqs < 0 || io.num_rows < 0 || io.max_pages < 0 || io.max_rows < 1) return MOE_ERR_INVALID_ARG;
   if (io.num_seqs > kMaxSeqs) return MOE_ERR_UNSUPPORTED;
   if (int64_t(io.max_pages) * c.page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (int64_t(io.num_rows) * io.num_heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -154,7 +155,7 @@ moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_stat
   moe_status_t s = heads_ok(io->num_heads, io->num_kv_heads, io->head_dim, io->dtype);
   if (s != MOE_OK) return s;
   if (io->num_seqs < 0 || io->num_rows < 0 || io->num_keys < 0) return MOE_ERR_INVALID_ARG;
-  if (io->num_seqs > kMaxSeqs) return MOE_ERR_UNSUPPORTED;
+  if (io->num_seqs > kMaxSeqs || int64_t(io->num_rows) * io->num_heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (io->causal != 0 && io->causal != 1) return MOE_ERR_INVALID_ARG;
   if (!finite(io->scale) || !aligned(d_status, 4) || !aligned(io->lse, 4)) return MOE_ERR_INVALID_ARG;
   if (io->num_rows == 0 || io->num_seqs == 0) return MOE_OK;
