@@ -466,8 +466,8 @@ typedef struct moe_attend_paged_io {
   const int32_t *lengths;     /* [num_seqs] tokens of each sequence in the cache, its query rows included */
   const int32_t *cu_rows;     /* [num_seqs + 1] first query row of each sequence, then the end */
   int32_t num_seqs;           /* 0..4096 */
-  int32_t num_rows;           /* rows of q and out */
-  int32_t max_pages;          /* columns of page_table */
+  int32_t num_rows;           /* rows of q and out; num_rows * num_heads < 2^31 */
+  int32_t max_pages;          /* columns of page_table; max_pages * page_size <= 2^30 */
   int32_t max_rows;           /* query rows that a sequence usually has at most: picks the kernel variant; any
                                * value >= 1 gives right results */
   int32_t num_heads;          /* a multiple of the cache's num_kv_heads */
@@ -501,7 +501,7 @@ typedef struct moe_attend_prompt_io {
   const int32_t *cu_rows;     /* [num_seqs + 1] first query row of each sequence, then the end */
   const int32_t *cu_keys;     /* [num_seqs + 1] first key of each sequence, then the end */
   int32_t num_seqs;           /* 0..4096 */
-  int32_t num_rows, num_keys; /* rows of q and out; rows of k and v */
+  int32_t num_rows, num_keys; /* rows of q and out (num_rows * num_heads < 2^31); rows of k and v */
   int32_t num_heads, num_kv_heads, head_dim;
   uint32_t dtype;
   int32_t causal;             /* 1: row i of n sees keys 0 .. m - n + i of its sequence's m; 0: all of them */

@@ -67,7 +67,7 @@ moe_status_t paged_sizes_ok(const moe_attend_paged_io_t &io, const moe_kv_cache_
   if (s != MOE_OK) return s;
   if (io.num_seqs < 0 || io.num_rows < 0 || io.max_pages < 0 || io.max_rows < 1) return MOE_ERR_INVALID_ARG;
   if (io.num_seqs > kMaxSeqs) return MOE_ERR_UNSUPPORTED;
-  if (int64_t(io.max_pages) * c.page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (int64_t(io.max_pages) * c.page_size > 1 << 30) return MOE_ERR_UNSUPPORTED;  // keys are counted in 32 bits
   if (int64_t(io.num_rows) * io.num_heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -100,7 +100,8 @@ def paged_io(**kw):
     (dict(num_seqs=5000), UNSUPPORTED),
     (dict(num_rows=-1), INVALID),
     (dict(max_pages=-1), INVALID),
-    (dict(max_pages=1 << 26), UNSUPPORTED),         # lengths past 2^31
+    (dict(max_pages=1 << 26), UNSUPPORTED),         # lengths past 2^30
+    (dict(num_rows=1 << 27), UNSUPPORTED),          # 2^32 (row, head) pairs
     (dict(max_rows=0), INVALID),
     (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID),
@@ -143,6 +144,7 @@ def prompt_io(**kw):
     (dict(num_seqs=4097), UNSUPPORTED),
     (dict(num_rows=-1), INVALID),
     (dict(num_keys=-1), INVALID),
+    (dict(num_rows=1 << 27), UNSUPPORTED),
     (dict(causal=2), INVALID),
     (dict(scale=float("-inf")), INVALID),
     (dict(q=P + 2), INVALID),
