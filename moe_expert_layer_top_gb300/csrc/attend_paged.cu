@@ -47,14 +47,13 @@
 #include <stdint.h>
 
 #include "attention.cuh"
-#include "tcgen05.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr int kStageKeys = 32;
-constexpr int64_t kWaitNs = 1000000000;  // bound of every wait
+constexpr int kOver = 8;                 // what an item costs beside its stages, in units of one stage
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
 constexpr float kNone = 1e30f;           // minus the reference of a row that has seen no key
 constexpr int kCombineThreads = 256;
@@ -75,35 +74,42 @@ struct PagedArgs {
   int32_t *status;
 };
 
-// A variant: head size, n-tiles of 8 rows, warps (one loads), blocks per SM, ring stages.
-template <int D_, int NT_, int WARPS_, int BLOCKS_, int STAGES_>
+// A variant: head size, n-tiles of 8 rows, warps, blocks per SM, stages of each
+// warp's ring, granules of 16 keys computed at a time.
+template <int D_, int NT_, int W_, int BLOCKS_, int DEPTH_, int U_>
 struct Cfg {
-  static constexpr int D = D_, NT = NT_, W = WARPS_ - 1, BLOCKS = BLOCKS_, STAGES = STAGES_;
-  static constexpr int THREADS = WARPS_ * 32;
+  static constexpr int D = D_, NT = NT_, W = W_, BLOCKS = BLOCKS_, DEPTH = DEPTH_, U = U_;
+  static constexpr int THREADS = W * 32;
   static constexpr int ROWS = 8 * NT;           // (token, head) pairs of a row block
   static constexpr int KS = D / 16;             // k-steps of the score product
   static constexpr int MT = D / 16;             // m-tiles of the value product
+  static constexpr bool QREG = NT == 1;         // query operands stay in registers
   static constexpr int CODES = kStageKeys * D / 2, SCALES = kStageKeys * D / 32;
   static constexpr int STAGE_BYTES = 2 * (CODES + SCALES);
   static constexpr int SLAB = D + 4;            // row stride of the joined accumulators (floats)
   static constexpr int PART = ROWS * (D + 2);   // floats of one partial result
   struct Smem {
-    alignas(128) uint8_t ring[STAGES][STAGE_BYTES];  // K codes, V codes, K scales, V scales
-    float slab[W][8][SLAB];   // accumulators of one n-tile of every warp
-    uint2 q[NT][KS][32];      // query operand registers
-    float mul[ROWS];          // score units to exponents of two
-    int limit[ROWS];          // keys that a row sees
+    union {
+      alignas(128) uint8_t ring[W][DEPTH][STAGE_BYTES];  // K codes, V codes, K scales, V scales
+      float slab[W][8][SLAB];  // accumulators of one n-tile of every warp, once the rings are drained
+    };
+    uint2 q[NT][KS][32];       // query operand registers
+    float mul[ROWS];           // score units to exponents of two
+    int limit[ROWS];           // keys that a row sees
     float ref[W][ROWS], sum[W][ROWS];
-    int64_t before[kMaxSeqs / 32 + 1];  // stages of each 32 sequences, then summed
-    uint64_t full[STAGES], empty[STAGES];
+    int64_t before[kMaxSeqs / 32 + 1];  // units of each 32 sequences, then summed
   };
 };
 
-// ------------------------------------------------------------------ the list of stages
+// ------------------------------------------------------------------ the list of work
+// In units: an item (sequence, kv head, row block) is kOver units for its
+// queries and its join, then one unit for each of its stages of 32 keys.
 
 struct Seq {
   int b, row0, n, len;  // sequence, first row, rows, keys
   int items, steps;     // kv heads x row blocks; stages of each
+
+  __device__ __forceinline__ int64_t units() const { return int64_t(items) * (steps + kOver); }
 };
 
 template <class C>
@@ -126,14 +132,14 @@ __device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b, int32_t *stat
   return s;
 }
 
-// Fills before[] with the stages ahead of every 32 sequences; returns all stages. Whole block.
+// Fills before[] with the units ahead of every 32 sequences; returns all units. Whole block.
 template <class C>
-__device__ int64_t count_stages(const PagedArgs &a, int64_t *before, int64_t *total) {
+__device__ int64_t count_units(const PagedArgs &a, int64_t *before, int64_t *total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (a.num_seqs + 31) / 32;
   for (int c = warp; c < chunks; c += blockDim.x / 32) {
     const Seq s = load_seq<C>(a, c * 32 + lane, nullptr);
-    int64_t v = int64_t(s.items) * s.steps;
+    int64_t v = s.units();
 #pragma unroll
     for (int d = 16; d; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
     if (lane == 0) before[c] = v;
@@ -158,19 +164,19 @@ __device__ int64_t count_stages(const PagedArgs &a, int64_t *before, int64_t *to
   return *total;
 }
 
-// A place in the list: a sequence, and a stage of its items x steps.
+// A place in the list: a unit of an item of a sequence.
 struct Place {
   Seq s;
-  int item, step;
+  int item, unit;
 };
 
-// The place of stage p (0 <= p < all). Whole warp; the same for every lane.
+// The place of unit p (0 <= p < all). Whole warp; the same for every lane.
 template <class C>
-__device__ Place find_stage(const PagedArgs &a, const int64_t *before, int64_t p) {
+__device__ Place find_unit(const PagedArgs &a, const int64_t *before, int64_t p) {
   const int lane = threadIdx.x & 31;
   const int chunks = (a.num_seqs + 31) / 32;
   int c = 0;
-  for (int lo = 0, hi = chunks; lo < hi;) {  // the last chunk with before <= p
+  for (int lo = 0, hi = chunks; lo < hi;) {  // the last chunk with before <= p: earlier ones with that start are empty
     const int mid = (lo + hi) / 2;
     if (before[mid] <= p) {
       c = mid;
@@ -179,9 +185,8 @@ __device__ Place find_stage(const PagedArgs &a, const int64_t *before, int64_t p
       hi = mid;
     }
   }
-  // chunks without stages share their start with the next one: the last is the one with stages
   const Seq mine = load_seq<C>(a, c * 32 + lane, nullptr);
-  const int64_t own = int64_t(mine.items) * mine.steps;
+  const int64_t own = mine.units();
   int64_t end = own;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -194,20 +199,19 @@ __device__ Place find_stage(const PagedArgs &a, const int64_t *before, int64_t p
   const int64_t in = rest - (__shfl_sync(0xFFFFFFFFu, end, w) - __shfl_sync(0xFFFFFFFFu, own, w));
   Place pl;
   pl.s = load_seq<C>(a, c * 32 + w, nullptr);
-  pl.item = int(in / pl.s.steps);
-  pl.step = int(in - int64_t(pl.item) * pl.s.steps);
+  pl.item = int(in / (pl.s.steps + kOver));
+  pl.unit = int(in - int64_t(pl.item) * (pl.s.steps + kOver));
   return pl;
 }
 
-// A run of stages of one item that a block computes.
+// A run of stages of one item that a block computes (count may be 0).
 struct Segment {
   Seq s;
   int kv, r0;       // kv head, first (token, head) pair
   int first, count; // stages
-  bool whole;       // all of the item's stages
 };
 
-// Cuts the next segment off a block's share; `left` stages remain after it.
+// Cuts the next segment off a block's share; `left` units remain after it.
 template <class C>
 __device__ __forceinline__ Segment next_segment(const PagedArgs &a, Place &p, int64_t &left) {
   Segment g;
@@ -215,12 +219,12 @@ __device__ __forceinline__ Segment next_segment(const PagedArgs &a, Place &p, in
   const int blocks = p.s.items / a.num_kv_heads;
   g.kv = p.item / blocks;
   g.r0 = (p.item - g.kv * blocks) * C::ROWS;
-  g.first = p.step;
-  const int64_t room = p.s.steps - p.step;
-  g.count = int(room < left ? room : left);
-  g.whole = g.count == p.s.steps;
-  left -= g.count;
-  p.step = 0;
+  const int64_t room = p.s.steps + kOver - p.unit;
+  const int take = int(room < left ? room : left);
+  g.first = max(0, p.unit - kOver);
+  g.count = max(0, p.unit + take - kOver) - g.first;
+  left -= take;
+  p.unit = 0;
   ++p.item;
   if (left > 0) {
     while (p.item >= p.s.items) {  // the next sequence with rows
@@ -235,63 +239,78 @@ __device__ __forceinline__ Segment next_segment(const PagedArgs &a, Place &p, in
   return g;
 }
 
-// Blocks that share the list: enough stages for each warp of a block to have one.
+// Blocks that share the list: about a stage for each warp at least.
 template <class C>
-__device__ __forceinline__ int64_t active_blocks(int64_t stages, int64_t grid) {
-  const int64_t n = (stages + C::W - 1) / C::W;
+__device__ __forceinline__ int64_t active_blocks(int64_t units, int64_t grid) {
+  const int64_t n = (units + C::W - 1) / C::W;
   return n < grid ? n : grid;
 }
 
-// ------------------------------------------------------------------ copies (the last warp)
+// ------------------------------------------------------------------ copies
+// Every warp copies its own stages (stage i of a segment is warp i mod W's)
+// with cp.async, DEPTH - 1 of them ahead of the one it computes.
+
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <class C>
-__device__ void load_warp(const PagedArgs &a, typename C::Smem &sm, Place p, int64_t left) {
-  const int lane = threadIdx.x & 31;
-  const uint64_t policy = l2_evict_first_policy();
-  int64_t g = 0;
-  bool ok = true;
-  while (ok && left > 0) {
-    const Segment seg = next_segment<C>(a, p, left);
-    const int32_t *table = a.page_table + int64_t(seg.s.b) * a.max_pages;
-    for (int s0 = 0; ok && s0 < seg.count; s0 += 16) {
-      // lane 2 i + u looks up granule u (16 keys) of stage s0 + i
-      const int key = (seg.first + s0) * kStageKeys + lane * 16;
-      int64_t at = -1;  // first cached row of the granule
-      if (s0 + lane / 2 < seg.count && key < seg.s.len) {
-        const int pi = key / a.page_size, page = __ldg(table + pi);
-        if (page < 0 || page >= a.num_pages)
-          out_of_range(a.status);
-        else
-          at = (int64_t(page) * a.num_kv_heads + seg.kv) * a.page_size + (key - pi * a.page_size);
-      }
-      const int batch = min(16, seg.count - s0);
-      for (int i = 0; i < batch; ++i, ++g) {
-        const int slot = int(g % C::STAGES);
-        ok = mbar_wait(&sm.empty[slot], uint32_t((g / C::STAGES) & 1) ^ 1u, kWaitNs);
-        if (!ok) break;
-        // lanes 0-7: (part, granule); both granules carry their own address
-        const int64_t row = __shfl_sync(0xFFFFFFFFu, at, 2 * i + (lane & 1));
-        const unsigned have = __ballot_sync(0xFFFFFFFFu, row >= 0) & 3u;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], uint32_t(__popc(have)) * (C::STAGE_BYTES / 2));
-        __syncwarp();
-        if (lane < 8 && row >= 0) {
-          const int u = lane & 1, part = lane >> 1;
-          const bool scales = part >= 2, value = part & 1;
-          const int bytes = scales ? C::SCALES / 2 : C::CODES / 2;
-          const int64_t width = scales ? C::D / 32 : C::D / 2;
-          const uint8_t *src = (scales ? (value ? a.v_scales : a.k_scales) : (value ? a.v_codes : a.k_codes)) + row * width;
-          uint8_t *dst = sm.ring[slot] + (scales ? 2 * C::CODES + (value ? C::SCALES : 0) : (value ? C::CODES : 0)) +
-                         u * bytes;
-          bulk_g2s(dst, src, uint32_t(bytes), &sm.full[slot], policy);
+struct Copier {
+  const int32_t *table;
+  int64_t at;     // lane 2 j + u: first cached row of granule u (16 keys) of the j-th stage of the batch, -1: none
+  int batch;      // stages copied of the batch (16 are looked up at a time)
+
+  __device__ __forceinline__ void start(const PagedArgs &a, const Segment &seg) {
+    table = a.page_table + int64_t(seg.s.b) * a.max_pages;
+    batch = 16;
+  }
+
+  // Copies stage i of the segment; the next call's is stage i + W.
+  __device__ __forceinline__ void copy(const PagedArgs &a, const Segment &seg, int i, uint8_t *slot) {
+    const int lane = threadIdx.x & 31;
+    if (i < seg.count) {
+      if (batch == 16) {
+        batch = 0;
+        const int step = i + (lane >> 1) * C::W, key = (seg.first + step) * kStageKeys + (lane & 1) * 16;
+        at = -1;
+        if (step < seg.count && key < seg.s.len) {
+          const int pi = key / a.page_size, page = __ldg(table + pi);
+          if (page < 0 || page >= a.num_pages)
+            out_of_range(a.status);
+          else
+            at = (int64_t(page) * a.num_kv_heads + seg.kv) * a.page_size + (key - pi * a.page_size);
         }
       }
+      constexpr int kPer = C::CODES / 512;  // copies of 16 bytes a lane, of the codes of K (and of V)
+      const int64_t r0 = __shfl_sync(0xFFFFFFFFu, at, 2 * batch), r1 = __shfl_sync(0xFFFFFFFFu, at, 2 * batch + 1);
+      ++batch;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        const int64_t r = 2 * c < kPer ? r0 : r1;
+        const int in = (c % (kPer / 2)) * 512 + lane * 16;  // byte within the granule's codes
+        if (r >= 0) {
+          copy16(slot + c * 512 + lane * 16, a.k_codes + r * (C::D / 2) + in);
+          copy16(slot + C::CODES + c * 512 + lane * 16, a.v_codes + r * (C::D / 2) + in);
+        }
+      }
+      constexpr int kLanes = C::SCALES / 32;  // lanes that carry one granule's scales
+      if (lane < 4 * kLanes) {
+        const bool value = lane >= 2 * kLanes;
+        const int l = lane & (2 * kLanes - 1);
+        const int64_t r = l < kLanes ? r0 : r1;
+        if (r >= 0)
+          copy16(slot + 2 * C::CODES + lane * 16,
+                 (value ? a.v_scales : a.k_scales) + r * (C::D / 32) + (l & (kLanes - 1)) * 16);
+      }
     }
+    copy_commit();
   }
-  if (!ok && a.status && lane == 0) report_error(a.status, MOE_ERR_TIMEOUT);
-  // no copy may be in flight when the block exits
-  for (int64_t j = 1; j <= C::STAGES && j <= g; ++j)
-    mbar_wait(&sm.full[(g - j) % C::STAGES], uint32_t(((g - j) / C::STAGES) & 1), kWaitNs);
-}
+};
 
 // ------------------------------------------------------------------ arithmetic
 
@@ -332,40 +351,81 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// 2^-e as binary32, e >= 0 (0 below 2^-126).
-__device__ __forceinline__ float pow2_neg(int e) { return __uint_as_float(uint32_t(max(127 - e, 0)) << 23); }
+// 2^(code - ref) as binary32 (code <= ref); a scale code of 0 (2^-127) counts as zero.
+__device__ __forceinline__ float pow2_rel(uint32_t code, float unit) { return __uint_as_float(code << 23) * unit; }
+// its unit: 2^(127 - ref)
+__device__ __forceinline__ float pow2_unit(int ref) { return ue8m0_to_float(uint32_t(254 - ref)); }
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) { return F16::pack(lo, hi); }
-
-__device__ __forceinline__ int max4(uint32_t w) {  // the largest of four bytes
-  uint32_t m;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(w & 0x00FF00FFu), "r"((w >> 8) & 0x00FF00FFu));
-  return max(int(m & 0xFFFFu), int(m >> 16));
-}
 
 template <class C>
 struct State {
   float o[C::MT][C::NT][4];      // [m-tile][n-tile]: dimension pair x row pair
   float ref[C::NT][2];           // minus the reference of rows 2t, 2t + 1 (exponents of two)
   float sum[C::NT][2];           // this lane's keys only
-  int vref;                      // scale code that this lane's accumulators are relative to
+  int kref, vref;                // scale codes that K and the accumulators are relative to
 };
 
-// One stage of 32 keys. key0: its first key; len: keys of the sequence; masked: some row may not see all of it.
+// U granules (16 U keys) of a stage, the first of them granule u0. key0: the
+// stage's first key; len: keys of the sequence; masked: some row may not see all.
 template <class C, int D = C::D>
-__device__ __forceinline__ void stage(const PagedArgs &a, const typename C::Smem &sm, const uint8_t *ring, State<C> &st,
-                                      const uint2 (&qreg)[C::NT <= 2 ? C::NT : 1][C::NT <= 2 ? C::KS : 1], int key0, int len,
-                                      bool masked) {
-  constexpr int NT = C::NT;
+__device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8_t *ring, State<C> &st,
+                                         const uint2 (&qreg)[C::QREG ? C::NT : 1][C::QREG ? C::KS : 1], int u0, int key0,
+                                         int len, bool masked) {
+  constexpr int NT = C::NT, U = C::U;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint8_t *kc = ring, *vc = ring + C::CODES, *ks = ring + 2 * C::CODES, *vs = ks + C::SCALES;
+  const uint8_t *kc = ring + u0 * 16 * (D / 2), *vc = kc + C::CODES;
+  const uint8_t *ks = ring + 2 * C::CODES + u0 * 16 * (D / 32), *vs = ks + C::SCALES;
+  key0 += 16 * u0;
 
-  // ---- scores: keys 16 u + g + 8 v
-  constexpr int QW = D / 32;  // 32-bit words of a lane's quarter row
-  uint32_t kw[2][2][QW], kf[2][2];
-  float kmul[2][2];
+  // ---- scale codes: K of keys 16 u + g + 8 v, V of keys 16 u + 8 v + 2 t + e
+  uint32_t kcode[U][2], vcode[U][2][2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      kcode[u][v] = ks[(16 * u + 8 * v + g) * (D / 32) + t / (128 / D)];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) vcode[u][v][e] = vs[(16 * u + 8 * v + 2 * t + e) * (D / 32) + g / (256 / D)];
+    }
+  if (masked) {  // past the end there may be anything
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        if (key0 + 16 * u + 8 * v + g >= len) kcode[u][v] = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (key0 + 16 * u + 8 * v + 2 * t + e >= len) vcode[u][v][e] = 0;
+      }
+  }
+  uint32_t ktop = 0, vtop = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      ktop = max(ktop, kcode[u][v]);
+      vtop = max(vtop, max(vcode[u][v][0], vcode[u][v][1]));
+    }
+  if (__any_sync(0xFFFFFFFFu, int(ktop) > st.kref || int(vtop) > st.vref)) {
+    st.kref = max(st.kref, int(__reduce_max_sync(0xFFFFFFFFu, ktop)));
+    const int next = max(st.vref, int(__reduce_max_sync(0xFFFFFFFFu, vtop)));
+    const float f = __uint_as_float(uint32_t(max(127 - (next - st.vref), 0)) << 23);
+    st.vref = next;
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st.o[i][n][c] *= f;
+  }
+
+  // ---- scores
+  constexpr int QW = D / 32;  // 32-bit words of a lane's quarter row
+  uint32_t kw[U][2][QW], kf[U][2];
+  const float kunit = pow2_unit(st.kref);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const int key = 16 * u + 8 * v + g;
@@ -376,24 +436,12 @@ __device__ __forceinline__ void stage(const PagedArgs &a, const typename C::Smem
         const uint2 w = *reinterpret_cast<const uint2 *>(kc + key * (D / 2) + 8 * t);
         kw[u][v][0] = w.x, kw[u][v][1] = w.y;
       }
-      int mine, top;
-      if constexpr (D == 128) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(ks + key * 4);
-        top = max4(w);
-        mine = int((w >> (8 * t)) & 0xFFu);
-      } else {
-        const uint32_t w = *reinterpret_cast<const uint16_t *>(ks + key * 2);
-        const int lo = int(w & 0xFFu), hi = int(w >> 8);
-        top = max(lo, hi);
-        mine = t < 2 ? lo : hi;
-      }
-      const float f = pow2_neg(top - mine);
+      const float f = pow2_rel(kcode[u][v], kunit);
       kf[u][v] = f16x2(f, f);
-      kmul[u][v] = ue8m0_to_float(uint32_t(top));
     }
-  float s[2][NT][4];
+  float s[U][NT][4];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -403,13 +451,13 @@ __device__ __forceinline__ void stage(const PagedArgs &a, const typename C::Smem
     uint2 b[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if constexpr (NT <= 2)
+      if constexpr (C::QREG)
         b[n] = qreg[n][k];
       else
         b[n] = sm.q[n][k][lane];
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < U; ++u) {
       uint32_t r[2][2];
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
@@ -421,37 +469,33 @@ __device__ __forceinline__ void stage(const PagedArgs &a, const typename C::Smem
       for (int n = 0; n < NT; ++n) mma_f16(s[u][n], r[0][0], r[1][0], r[0][1], r[1][1], b[n].x, b[n].y);
     }
   }
-  // to score units; hidden keys to -inf
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[u][n][c] *= kmul[u][c >> 1];
-  if (masked) {
+  if (masked) {  // hidden keys to -inf
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int limit = sm.limit[8 * n + 2 * t + e] - key0 - g;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int v = 0; v < 2; ++v)
             if (16 * u + 8 * v >= limit) s[u][n][2 * v + e] = -INFINITY;
       }
   }
   // ---- reference
-  float top[NT][2], mul[NT][2];
+  const float kscale = ue8m0_to_float(uint32_t(st.kref));
+  float mul[NT][2];
   bool move = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float2 m = *reinterpret_cast<const float2 *>(&sm.mul[8 * n + 2 * t]);
-    mul[n][0] = m.x, mul[n][1] = m.y;
+    mul[n][0] = fmaxf(m.x * kscale, 0x1p-126f), mul[n][1] = fmaxf(m.y * kscale, 0x1p-126f);  // never 0: -inf stays
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      top[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e])) * mul[n][e];
-      move |= top[n][e] + st.ref[n][e] > kLazy;
+      float x = fmaxf(s[0][n][e], s[0][n][2 + e]);
+#pragma unroll
+      for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][n][e], s[u][n][2 + e]));
+      move |= fmaf(x, mul[n][e], st.ref[n][e]) > kLazy;
     }
   }
   if (__any_sync(0xFFFFFFFFu, move)) {
@@ -459,9 +503,12 @@ __device__ __forceinline__ void stage(const PagedArgs &a, const typename C::Smem
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float m = top[n][e];
+        float m = s[0][n][e];
+#pragma unroll
+        for (int u = 0; u < U; ++u) m = fmaxf(m, fmaxf(s[u][n][e], s[u][n][2 + e]));
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        m *= mul[n][e];
         const float next = m + st.ref[n][e] > 0.0f ? -m : st.ref[n][e];
         const float f = exp2_approx(next - st.ref[n][e]);
         st.ref[n][e] = next;
@@ -474,11 +521,11 @@ __device__ __forceinline__ void stage(const PagedArgs &a, const typename C::Smem
       }
   }
   // ---- probabilities, in the operand layout of the second product
-  uint32_t p[2][NT][2];
+  uint32_t p[U][NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const float x = exp2_approx(fmaf(s[u][n][2 * v], mul[n][0], st.ref[n][0]));
@@ -487,34 +534,11 @@ __device__ __forceinline__ void stage(const PagedArgs &a, const typename C::Smem
         st.sum[n][1] += y;
         p[u][n][v] = transpose8x8(f16x2(x, y));
       }
-  // ---- values: keys 16 u + 8 v + 2 t + e
+  // ---- values
   constexpr int VW = D / 64;  // 32-bit words of a lane's eighth of a row
-  int code[2][2][2], vtop = 0;
+  const float vunit = pow2_unit(st.vref);
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int key = 16 * u + 8 * v + 2 * t + e;
-        code[u][v][e] = key0 + key < len ? int(vs[key * (D / 32) + g / (256 / D)]) : 0;  // past the end: anything
-        vtop = max(vtop, code[u][v][e]);
-      }
-  vtop = max(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, 1));
-  vtop = max(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, 2));
-  if (__any_sync(0xFFFFFFFFu, vtop > st.vref)) {
-    const int next = max(vtop, st.vref);
-    const float f = pow2_neg(next - st.vref);
-    st.vref = next;
-#pragma unroll
-    for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) st.o[i][n][c] *= f;
-  }
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < U; ++u) {
     uint32_t lo[2][VW], hi[2][VW], vf[2];  // even and odd dimensions of two keys, interleaved
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
@@ -532,7 +556,7 @@ __device__ __forceinline__ void stage(const PagedArgs &a, const typename C::Smem
         lo[v][w] = (x[w] & 0x0F0F0F0Fu) | ((y[w] << 4) & 0xF0F0F0F0u);
         hi[v][w] = ((x[w] >> 4) & 0x0F0F0F0Fu) | (y[w] & 0xF0F0F0F0u);
       }
-      vf[v] = f16x2(pow2_neg(st.vref - code[u][v][0]), pow2_neg(st.vref - code[u][v][1]));
+      vf[v] = f16x2(pow2_rel(vcode[u][v][0], vunit), pow2_rel(vcode[u][v][1], vunit));
     }
 #pragma unroll
     for (int i = 0; i < C::MT; ++i) {
@@ -572,21 +596,6 @@ __device__ __forceinline__ void store_lse(const PagedArgs &a, const Seq &s, int 
 }
 
 // ------------------------------------------------------------------ main kernel
-
-constexpr int kBarWarps = 1;
-
-__device__ __forceinline__ int bar_and_warps(int threads, int v) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.s32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, %3, p;\n\t"
-      "selp.s32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(v), "n"(kBarWarps), "r"(threads)
-      : "memory");
-  return r;
-}
 
 // The queries of a row block, as operand registers, with their limits and multipliers.
 template <class T, class C>
@@ -630,17 +639,32 @@ __device__ void load_queries(const PagedArgs &a, typename C::Smem &sm, const Seg
 }
 
 template <class T, class C>
-__device__ void compute_warps(const PagedArgs &a, typename C::Smem &sm, Place p, int64_t left, int warp) {
-  constexpr int D = C::D, NT = C::NT, kSync = C::W * 32;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int tid = warp * 32 + lane;
-  int64_t base = 0;  // stages of the block before this segment
+__global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(const PagedArgs a) {
+  constexpr int D = C::D, NT = C::NT;
+  extern __shared__ unsigned char paged_smem_raw[];
+  typename C::Smem &sm =
+      *reinterpret_cast<typename C::Smem *>((reinterpret_cast<uintptr_t>(paged_smem_raw) + 127) & ~uintptr_t(127));
+  __shared__ int64_t total;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  pdl_launch_dependents();
+  if (blockIdx.x == 0)  // what is out of range is reported once
+    for (int b = tid; b < a.num_seqs; b += C::THREADS) load_seq<C>(a, b, a.status);
+  const int64_t all = count_units<C>(a, sm.before, &total);
+  const int64_t blocks = active_blocks<C>(all, gridDim.x);
+  if (int64_t(blockIdx.x) >= blocks) return;
+  const int64_t begin = int64_t(blockIdx.x) * all / blocks, end = (int64_t(blockIdx.x) + 1) * all / blocks;
+  Place place = find_unit<C>(a, sm.before, begin);
+  int64_t left = end - begin;
   bool first = true;
-  int ok = 1;
   while (left > 0) {
-    const Segment seg = next_segment<C>(a, p, left);
+    const Segment seg = next_segment<C>(a, place, left);
+    if (seg.count == 0) continue;
+    Copier<C> copier;
+    copier.start(a, seg);
+#pragma unroll
+    for (int c = 0; c < C::DEPTH - 1; ++c) copier.copy(a, seg, warp + c * C::W, sm.ring[warp][c]);
     load_queries<T, C>(a, sm, seg, warp);
-    if (!bar_and_warps(kSync, ok)) break;
+    __syncthreads();
     State<C> st;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -654,32 +678,28 @@ __device__ void compute_warps(const PagedArgs &a, typename C::Smem &sm, Place p,
 #pragma unroll
         for (int c = 0; c < 4; ++c) st.o[i][n][c] = 0.0f;
     }
-    st.vref = 0;
-    uint2 qreg[NT <= 2 ? NT : 1][NT <= 2 ? C::KS : 1];
-    if constexpr (NT <= 2) {
+    st.kref = st.vref = 0;
+    uint2 qreg[C::QREG ? NT : 1][C::QREG ? C::KS : 1];
+    if constexpr (C::QREG) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < C::KS; ++k) qreg[n][k] = sm.q[n][k][lane];
     }
-    const int clear = max(0, seg.s.len - seg.s.n + 1 + seg.r0 / a.group);  // keys that every row sees
-    // stage g of the block belongs to warp g mod W
-    int i = int((warp - base % C::W + C::W) % C::W);
-    for (; ok && i < seg.count; i += C::W) {
-      const int64_t gs = base + i;
-      const int slot = int(gs % C::STAGES);
-      ok = mbar_wait(&sm.full[slot], uint32_t((gs / C::STAGES) & 1), kWaitNs) ? 1 : 0;
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) {
-        if (a.status && lane == 0) report_error(a.status, MOE_ERR_TIMEOUT);
-        break;
-      }
+    const int clear = min(seg.s.len, max(0, seg.s.len - seg.s.n + 1 + seg.r0 / a.group));  // keys that every row sees
+    int slot = 0;
+    for (int i = warp; i < seg.count; i += C::W) {
+      copy_wait<C::DEPTH - 2>();
+      __syncwarp();  // every lane's copies of this stage are there, and nobody reads the slot that is filled next
+      copier.copy(a, seg, i + (C::DEPTH - 1) * C::W, sm.ring[warp][slot == 0 ? C::DEPTH - 1 : slot - 1]);
       const int key0 = (seg.first + i) * kStageKeys;
-      stage<C>(a, sm, sm.ring[slot], st, qreg, key0, seg.s.len, key0 + kStageKeys > min(clear, seg.s.len));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[slot]);
+      const bool masked = key0 + kStageKeys > clear;
+#pragma unroll 1
+      for (int u = 0; u < 2; u += C::U)
+        granules<C>(sm, sm.ring[warp][slot], st, qreg, u, key0, seg.s.len, masked);
+      slot = slot == C::DEPTH - 1 ? 0 : slot + 1;
     }
-    base += seg.count;
+    copy_wait<0>();
     // ---- join the warps: reference and sum of each row, then the accumulators n-tile by n-tile
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -693,8 +713,9 @@ __device__ void compute_warps(const PagedArgs &a, typename C::Smem &sm, Place p,
           sm.sum[warp][8 * n + 2 * t + e] = l;
         }
       }
-    if (!bar_and_warps(kSync, ok)) break;
+    __syncthreads();  // the rings are drained: the slab takes their place
     const float unit = ue8m0_to_float(uint32_t(st.vref));
+    const bool whole = seg.count == seg.s.steps;
     const int rows = seg.s.n * a.group - seg.r0;  // real rows of the block
     float *part = a.parts + (int64_t(blockIdx.x) * 2 + (first ? 0 : 1)) * C::PART;
 #pragma unroll
@@ -704,17 +725,17 @@ __device__ void compute_warps(const PagedArgs &a, typename C::Smem &sm, Place p,
       for (int e = 0; e < 2; ++e) {
         float m = sm.ref[0][8 * n + 2 * t + e];
         for (int w = 1; w < C::W; ++w) m = fmaxf(m, sm.ref[w][8 * n + 2 * t + e]);
-        f[e] = exp2_approx(-st.ref[n][e] - m);
+        f[e] = exp2_approx(-st.ref[n][e] - m) * unit;
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < C::MT; i += 2)  // dimensions g D/8 + 2 i .. + 3
           *reinterpret_cast<float4 *>(&sm.slab[warp][2 * t + e][g * (D / 8) + 2 * i]) =
-              make_float4(st.o[i][n][e] * f[e] * unit, st.o[i][n][2 + e] * f[e] * unit, st.o[i + 1][n][e] * f[e] * unit,
-                          st.o[i + 1][n][2 + e] * f[e] * unit);
-      bar_and_warps(kSync, 1);
-      for (int idx = tid; idx < 8 * (D / 4); idx += kSync) {
+              make_float4(st.o[i][n][e] * f[e], st.o[i][n][2 + e] * f[e], st.o[i + 1][n][e] * f[e],
+                          st.o[i + 1][n][2 + e] * f[e]);
+      __syncthreads();
+      for (int idx = tid; idx < 8 * (D / 4); idx += C::THREADS) {
         const int row = idx / (D / 4), d = 4 * (idx % (D / 4)), rr = 8 * n + row;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float m = sm.ref[0][rr], l = 0.0f;
@@ -725,12 +746,11 @@ __device__ void compute_warps(const PagedArgs &a, typename C::Smem &sm, Place p,
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
           l += sm.sum[w][rr] * exp2_approx(sm.ref[w][rr] - m);
         }
-        if (seg.whole) {
+        if (whole) {
           if (rr < rows) {
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            const bool any = l != 0.0f;
             store4<T>(a, seg.s, seg.kv, seg.r0 + rr, D, d,
-                      any ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0, 0, 0, 0));
+                      l != 0.0f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0, 0, 0, 0));
             if (d == 0) store_lse(a, seg.s, seg.kv, seg.r0 + rr, m, l);
           }
         } else {
@@ -741,38 +761,10 @@ __device__ void compute_warps(const PagedArgs &a, typename C::Smem &sm, Place p,
           }
         }
       }
-      bar_and_warps(kSync, 1);
+      __syncthreads();
     }
     first = false;
   }
-}
-
-template <class T, class C>
-__global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(const PagedArgs a) {
-  extern __shared__ unsigned char paged_smem_raw[];
-  typename C::Smem &sm =
-      *reinterpret_cast<typename C::Smem *>((reinterpret_cast<uintptr_t>(paged_smem_raw) + 127) & ~uintptr_t(127));
-  __shared__ int64_t total;
-  const int warp = threadIdx.x >> 5;
-  pdl_launch_dependents();
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
-    }
-    fence_mbar_init();
-  }
-  if (blockIdx.x == 0)  // what is out of range is reported once
-    for (int b = threadIdx.x; b < a.num_seqs; b += C::THREADS) load_seq<C>(a, b, a.status);
-  const int64_t all = count_stages<C>(a, sm.before, &total);
-  const int64_t blocks = active_blocks<C>(all, gridDim.x);
-  if (int64_t(blockIdx.x) >= blocks) return;
-  const int64_t begin = int64_t(blockIdx.x) * all / blocks, end = (int64_t(blockIdx.x) + 1) * all / blocks;
-  const Place p = find_stage<C>(a, sm.before, begin);
-  if (warp == C::W)
-    load_warp<C>(a, sm, p, end - begin);
-  else
-    compute_warps<T, C>(a, sm, p, end - begin, warp);
 }
 
 // ------------------------------------------------------------------ joining the blocks
@@ -782,24 +774,25 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
 template <class T, class C>
 __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const PagedArgs a) {
   __shared__ int64_t before[kMaxSeqs / 32 + 1], total;
-  const int64_t all = count_stages<C>(a, before, &total);
+  const int64_t all = count_units<C>(a, before, &total);
   const int64_t blocks = active_blocks<C>(all, gridDim.x);
   const int64_t c = blockIdx.x;
   Place p;
-  int64_t begin = 0, end = 0, item0 = 0, item1 = 0;  // the block's stages, the item's
+  int64_t begin = 0, end = 0, item0 = 0, item1 = 0;  // the block's units, the item's
   if (c + 1 < blocks) {
     begin = c * all / blocks;
     end = (c + 1) * all / blocks;
-    p = find_stage<C>(a, before, end - 1);
-    item0 = end - 1 - p.step;
-    item1 = item0 + p.s.steps;
+    p = find_unit<C>(a, before, end - 1);
+    item0 = end - 1 - p.unit;
+    item1 = item0 + kOver + p.s.steps;
   }
   pdl_wait_primary();  // every block: this kernel must not end before the main one
-  if (item0 < begin || item1 <= end) return;  // begun by an earlier block, or complete
+  // the item's first stage is in a later block, or in an earlier one, or all of them are in this block
+  if (end <= item0 + kOver || begin > item0 + kOver || item1 <= end) return;
   // the blocks that hold parts of it: c, whose part is its last segment, and those after it, whose first it is
   int64_t last = c + 1;
   while ((last + 1) * all / blocks < item1) ++last;
-  const float *part0 = a.parts + (c * 2 + (item0 == begin ? 0 : 1)) * C::PART;
+  const float *part0 = a.parts + (c * 2 + (item0 <= begin ? 0 : 1)) * C::PART;
   const auto part = [&](int64_t b) { return b == c ? part0 : a.parts + b * 2 * C::PART; };
   const int per = p.s.items / a.num_kv_heads, kv = p.item / per, r0 = (p.item - kv * per) * C::ROWS;
   const int rows = min(C::ROWS, p.s.n * a.group - r0);
@@ -859,10 +852,10 @@ template <int D, class F>
 auto pick(int rows, F f) {
   const int blocks = (rows + 31) / 32, tiles = ((rows + blocks - 1) / blocks + 7) / 8;
   switch (tiles) {
-    case 1: return f(Cfg<D, 1, 8, 2, D == 128 ? 16 : 32>());
-    case 2: return f(Cfg<D, 2, 8, 2, D == 128 ? 16 : 32>());
-    case 3: return f(Cfg<D, 3, 12, 1, 32>());
-    default: return f(Cfg<D, 4, 8, 1, 32>());
+    case 1: return f(Cfg<D, 1, 8, 2, D == 128 ? 3 : 5, 2>());
+    case 2: return f(Cfg<D, 2, 8, 2, D == 128 ? 3 : 5, 1>());
+    case 3: return f(Cfg<D, 3, D == 128 ? 12 : 8, D == 128 ? 1 : 2, D == 128 ? 4 : 5, 1>());
+    default: return f(Cfg<D, 4, 8, D == 128 ? 1 : 2, 5, 1>());
   }
 }
 
