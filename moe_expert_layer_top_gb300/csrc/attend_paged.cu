@@ -53,10 +53,11 @@ namespace moe {
 namespace {
 
 constexpr int kStageKeys = 32;
-constexpr int kOver = 8;                 // what an item costs beside its stages, in units of one stage
+constexpr int kOver = 16;                // what an item costs beside its stages, in units of one stage
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
 constexpr float kNone = 1e30f;           // minus the reference of a row that has seen no key
 constexpr int kCombineThreads = 256;
+constexpr int kMaxBlocks = 1024;         // blocks of the main kernel, at most
 
 struct PagedArgs {
   const uint16_t *q;
@@ -262,8 +263,9 @@ __device__ __forceinline__ void copy_wait() {
 template <class C>
 struct Copier {
   const int32_t *table;
-  int64_t at;     // lane 2 j + u: first cached row of granule u (16 keys) of the j-th stage of the batch, -1: none
+  uint32_t at;    // lane 2 j + u: first cached row of granule u (16 keys) of the j-th stage of the batch
   int batch;      // stages copied of the batch (16 are looked up at a time)
+  static constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
   __device__ __forceinline__ void start(const PagedArgs &a, const Segment &seg) {
     table = a.page_table + int64_t(seg.s.b) * a.max_pages;
@@ -277,35 +279,35 @@ struct Copier {
       if (batch == 16) {
         batch = 0;
         const int step = i + (lane >> 1) * C::W, key = (seg.first + step) * kStageKeys + (lane & 1) * 16;
-        at = -1;
+        at = kNoRow;
         if (step < seg.count && key < seg.s.len) {
           const int pi = key / a.page_size, page = __ldg(table + pi);
           if (page < 0 || page >= a.num_pages)
             out_of_range(a.status);
           else
-            at = (int64_t(page) * a.num_kv_heads + seg.kv) * a.page_size + (key - pi * a.page_size);
+            at = (uint32_t(page) * a.num_kv_heads + seg.kv) * a.page_size + (key - pi * a.page_size);
         }
       }
       constexpr int kPer = C::CODES / 512;  // copies of 16 bytes a lane, of the codes of K (and of V)
-      const int64_t r0 = __shfl_sync(0xFFFFFFFFu, at, 2 * batch), r1 = __shfl_sync(0xFFFFFFFFu, at, 2 * batch + 1);
+      const uint32_t r0 = __shfl_sync(0xFFFFFFFFu, at, 2 * batch), r1 = __shfl_sync(0xFFFFFFFFu, at, 2 * batch + 1);
       ++batch;
 #pragma unroll
       for (int c = 0; c < kPer; ++c) {
-        const int64_t r = 2 * c < kPer ? r0 : r1;
+        const uint32_t r = 2 * c < kPer ? r0 : r1;
         const int in = (c % (kPer / 2)) * 512 + lane * 16;  // byte within the granule's codes
-        if (r >= 0) {
-          copy16(slot + c * 512 + lane * 16, a.k_codes + r * (C::D / 2) + in);
-          copy16(slot + C::CODES + c * 512 + lane * 16, a.v_codes + r * (C::D / 2) + in);
+        if (r != kNoRow) {
+          copy16(slot + c * 512 + lane * 16, a.k_codes + in + uint64_t(r) * (C::D / 2));
+          copy16(slot + C::CODES + c * 512 + lane * 16, a.v_codes + in + uint64_t(r) * (C::D / 2));
         }
       }
       constexpr int kLanes = C::SCALES / 32;  // lanes that carry one granule's scales
       if (lane < 4 * kLanes) {
         const bool value = lane >= 2 * kLanes;
         const int l = lane & (2 * kLanes - 1);
-        const int64_t r = l < kLanes ? r0 : r1;
-        if (r >= 0)
+        const uint32_t r = l < kLanes ? r0 : r1;
+        if (r != kNoRow)
           copy16(slot + 2 * C::CODES + lane * 16,
-                 (value ? a.v_scales : a.k_scales) + r * (C::D / 32) + (l & (kLanes - 1)) * 16);
+                 (value ? a.v_scales : a.k_scales) + (l & (kLanes - 1)) * 16 + uint64_t(r) * (C::D / 32));
       }
     }
     copy_commit();
@@ -337,6 +339,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same on accumulators that start at zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -441,12 +451,6 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
     }
   float s[U][NT][4];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[u][n][c] = 0.0f;
-#pragma unroll
   for (int k = 0; k < C::KS; ++k) {
     uint2 b[NT];
 #pragma unroll
@@ -466,7 +470,12 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
         r[v][1] = mul2(k & 1 ? decode2<3>(w) : decode2<1>(w), kf[u][v]);
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma_f16(s[u][n], r[0][0], r[1][0], r[0][1], r[1][1], b[n].x, b[n].y);
+      for (int n = 0; n < NT; ++n) {
+        if (k == 0)
+          mma_f16_first(s[u][n], r[0][0], r[1][0], r[0][1], r[1][1], b[n].x, b[n].y);
+        else
+          mma_f16(s[u][n], r[0][0], r[1][0], r[0][1], r[1][1], b[n].x, b[n].y);
+      }
     }
   }
   if (masked) {  // hidden keys to -inf
@@ -774,6 +783,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
 template <class T, class C>
 __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const PagedArgs a) {
   __shared__ int64_t before[kMaxSeqs / 32 + 1], total;
+  __shared__ float weight[8][kMaxBlocks], top[8], sum[8];
+  static_assert(kCombineThreads == 8 * 32, "a warp for each row's weights");
   const int64_t all = count_units<C>(a, before, &total);
   const int64_t blocks = active_blocks<C>(all, gridDim.x);
   const int64_t c = blockIdx.x;
@@ -792,28 +803,53 @@ __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const Pa
   // the blocks that hold parts of it: c, whose part is its last segment, and those after it, whose first it is
   int64_t last = c + 1;
   while ((last + 1) * all / blocks < item1) ++last;
+  const int parts = int(last - c) + 1;
   const float *part0 = a.parts + (c * 2 + (item0 <= begin ? 0 : 1)) * C::PART;
-  const auto part = [&](int64_t b) { return b == c ? part0 : a.parts + b * 2 * C::PART; };
+  const float *part1 = a.parts + (c + 1) * 2 * C::PART;  // the others, two slots apart
   const int per = p.s.items / a.num_kv_heads, kv = p.item / per, r0 = (p.item - kv * per) * C::ROWS;
-  const int rows = min(C::ROWS, p.s.n * a.group - r0);
   constexpr int D = C::D;
+  const int row0 = 8 * int(blockIdx.y);  // this block's 8 rows of the item
+  // weights of the parts: 2^(reference - largest)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  {
+    const int row = row0 + warp;
+    float m = -kNone;
+    for (int b = lane; b < parts; b += 32)
+      m = fmaxf(m, (b ? part1 + int64_t(b - 1) * 2 * C::PART : part0)[C::ROWS * D + row]);
+#pragma unroll
+    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    float l = 0.0f;
+    for (int b = lane; b < parts; b += 32) {
+      const float *x = (b ? part1 + int64_t(b - 1) * 2 * C::PART : part0) + C::ROWS * D + row;
+      const float f = exp2_approx(x[0] - m);
+      weight[warp][b] = f;
+      l = fmaf(x[C::ROWS], f, l);
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    if (lane == 0) {
+      top[warp] = m;
+      sum[warp] = l;
+    }
+  }
+  __syncthreads();
+  const int rows = min(8, p.s.n * a.group - r0 - row0);
   for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kCombineThreads) {
     const int row = idx / (D / 4), d = 4 * (idx % (D / 4));
-    float m = -kNone;
-    for (int64_t b = c; b <= last; ++b) m = fmaxf(m, part(b)[C::ROWS * D + row]);
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-    for (int64_t b = c; b <= last; ++b) {
-      const float *x = part(b);
-      const float f = exp2_approx(x[C::ROWS * D + row] - m);
-      const float4 o = *reinterpret_cast<const float4 *>(x + row * D + d);
-      v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
-      l = fmaf(x[C::ROWS * D + C::ROWS + row], f, l);
+    const int64_t at = (row0 + row) * D + d;
+    float4 v = *reinterpret_cast<const float4 *>(part0 + at);
+    const float f = weight[row][0];
+    v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll 8
+    for (int b = 1; b < parts; ++b) {
+      const float4 o = *reinterpret_cast<const float4 *>(part1 + int64_t(b - 1) * 2 * C::PART + at);
+      const float w = weight[row][b];
+      v.x = fmaf(o.x, w, v.x), v.y = fmaf(o.y, w, v.y), v.z = fmaf(o.z, w, v.z), v.w = fmaf(o.w, w, v.w);
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    store4<T>(a, p.s, kv, r0 + row, D, d,
+    const float l = sum[row], inv = l > 0.0f ? 1.0f / l : 0.0f;
+    store4<T>(a, p.s, kv, r0 + row0 + row, D, d,
               l != 0.0f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0, 0, 0, 0));
-    if (d == 0) store_lse(a, p.s, kv, r0 + row, m, l);
+    if (d == 0) store_lse(a, p.s, kv, r0 + row0 + row, top[row], l);
   }
 }
 
@@ -825,17 +861,23 @@ constexpr size_t smem_bytes() {
   return sizeof(typename C::Smem) + 128;
 }
 
+template <class C>
+int blocks_of(int num_sms) {
+  const int n = num_sms * C::BLOCKS;
+  return n < kMaxBlocks ? n : kMaxBlocks;
+}
+
 template <class T, class C>
 cudaError_t launch(const PagedArgs &a, int num_sms, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(attend_paged_kernel<T, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(smem_bytes<C>()));
   if (e != cudaSuccess) return e;
-  const unsigned grid = unsigned(num_sms * C::BLOCKS);
+  const unsigned grid = unsigned(blocks_of<C>(num_sms));
   attend_paged_kernel<T, C><<<grid, C::THREADS, smem_bytes<C>(), st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(grid, C::NT);
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -853,9 +895,9 @@ auto pick(int rows, F f) {
   const int blocks = (rows + 31) / 32, tiles = ((rows + blocks - 1) / blocks + 7) / 8;
   switch (tiles) {
     case 1: return f(Cfg<D, 1, 8, 2, D == 128 ? 3 : 5, 2>());
-    case 2: return f(Cfg<D, 2, 8, 2, D == 128 ? 3 : 5, 1>());
-    case 3: return f(Cfg<D, 3, D == 128 ? 12 : 8, D == 128 ? 1 : 2, D == 128 ? 4 : 5, 1>());
-    default: return f(Cfg<D, 4, 8, D == 128 ? 1 : 2, 5, 1>());
+    case 2: return f(Cfg<D, 2, 4, 3, D == 128 ? 3 : 5, 2>());
+    case 3: return f(Cfg<D, 3, 4, D == 128 ? 2 : 3, 5, 2>());
+    default: return f(Cfg<D, 4, 4, D == 128 ? 2 : 3, 5, 1>());
   }
 }
 
@@ -869,7 +911,7 @@ int usual_rows(const moe_attend_paged_io_t &io, const moe_kv_cache_t &c) {
 int64_t attend_paged_workspace(const moe_attend_paged_io_t &io, const moe_kv_cache_t &c, int num_sms) {
   const auto bytes = [&](auto cfg) {
     using C = decltype(cfg);
-    return int64_t(num_sms) * C::BLOCKS * 2 * C::PART * 4;
+    return int64_t(blocks_of<C>(num_sms)) * 2 * C::PART * 4;
   };
   const int rows = usual_rows(io, c);
   return c.head_dim == 64 ? pick<64>(rows, bytes) : pick<128>(rows, bytes);

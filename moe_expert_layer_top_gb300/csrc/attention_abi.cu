@@ -38,6 +38,8 @@ moe_status_t cache_sizes_ok(const moe_kv_cache_t &c) {
   if (c.num_pages < 0 || c.page_size <= 0 || c.num_kv_heads <= 0 || c.head_dim <= 0) return MOE_ERR_INVALID_ARG;
   if (c.page_size % 16 || c.page_size > 1024 || (c.head_dim != 64 && c.head_dim != 128) || c.num_kv_heads > 1024)
     return MOE_ERR_UNSUPPORTED;
+  // cached rows are counted in 32 bits: more of them than a device's memory holds
+  if (int64_t(c.num_pages) * c.page_size > int64_t(0xFFFFFFFFu) / c.num_kv_heads - 1) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
