@@ -4,13 +4,13 @@
 // sum_j exp(s_j - m), one pass over the keys with a reference m and the two
 // sums (see attend_prompt.cu). K_j = 2^(a - 127) k with E2M1 codes k and one
 // scale code a per 32 dimensions; V likewise.
-//   Keys: each code becomes an f16 value (exact), times 2^(a - a_max) with
-//   a_max the largest of the key's scale codes; the score is multiplied by
-//   2^(a_max - 127) after the product. Queries become f16 times a power of two
-//   per row. Both are exact but for parts 2^-24 below the key's (row's) largest.
+//   Keys: codes as f16 (exact); the partial score of each group of 32
+//   dimensions is multiplied by its 2^(a - 127) in binary32. Queries become f16
+//   times a power of two per row: exact but for parts 2^-28 below the row's
+//   largest and smaller.
 //   Values: codes times 2^(b - b_ref) in f16, with b_ref the largest scale code
-//   seen so far in the group of 32 dimensions; like m it moves as the pass goes
-//   on, and the accumulators of the group are rescaled when it does.
+//   that the warp has seen; like m it moves as the pass goes on, and the
+//   accumulators are rescaled when it does. Exact down to 2^-23 of the largest.
 //   Probabilities: f16, at most 2^8 (the lazy reference of attend_prompt.cu).
 // All sums are binary32, on the tensor cores (mma.sync m16n8k16, f16 operands).
 //
@@ -26,9 +26,9 @@
 // Layout. Keys are the MMA's M (scores transposed: 16 keys x 8 rows), so a step
 // of 8 rows wastes nothing on padding. The order of a product's inner dimension
 // is free when both operands share it, so a lane's operand registers are decoded
-// from whole 16-byte (K) and 8-byte (V) pieces of a cached row:
+// from whole 4-byte (K) and 8-byte (V) pieces of a cached row:
 //   S^T = K Q^T   lane (g, t) = (lane / 4, lane % 4) decodes dimensions
-//                 [t D/4, (t + 1) D/4) of keys g and g + 8
+//                 32 j + 8 t .. + 7 of keys g and g + 8, for each group j
 //   O^T = V^T P^T lane (g, t) decodes dimensions [g D/8, (g + 1) D/8) of keys
 //                 2t, 2t + 1, 2t + 8, 2t + 9, two keys' codes interleaved
 // P moves from the first product's result layout to the second's operand
@@ -260,6 +260,14 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Codes lie in shared memory as [key][D/2 bytes], with the 16-byte groups of a
+// key exchanged by key: a lane reads 4 bytes of a group (K) or 8 of a key (V),
+// and the keys that a warp reads at once then fall into different banks.
+template <int D>
+__device__ __forceinline__ int swizzle(int key) {
+  return D == 128 ? (key >> 1) & 3 : (key >> 2) & 1;
+}
+
 template <class C>
 struct Copier {
   const int32_t *table;
@@ -289,6 +297,9 @@ struct Copier {
         }
       }
       constexpr int kPer = C::CODES / 512;  // copies of 16 bytes a lane, of the codes of K (and of V)
+      // 16 bytes are a key's group of 32 codes; see swizzle() for its place
+      constexpr int kGroups = C::D / 32;
+      const int to = (lane / kGroups) * (C::D / 2) + (((lane % kGroups) ^ swizzle<C::D>(lane / kGroups)) << 4);
       const uint32_t r0 = __shfl_sync(0xFFFFFFFFu, at, 2 * batch), r1 = __shfl_sync(0xFFFFFFFFu, at, 2 * batch + 1);
       ++batch;
 #pragma unroll
@@ -296,8 +307,8 @@ struct Copier {
         const uint32_t r = 2 * c < kPer ? r0 : r1;
         const int in = (c % (kPer / 2)) * 512 + lane * 16;  // byte within the granule's codes
         if (r != kNoRow) {
-          copy16(slot + c * 512 + lane * 16, a.k_codes + in + uint64_t(r) * (C::D / 2));
-          copy16(slot + C::CODES + c * 512 + lane * 16, a.v_codes + in + uint64_t(r) * (C::D / 2));
+          copy16(slot + c * 512 + to, a.k_codes + in + uint64_t(r) * (C::D / 2));
+          copy16(slot + C::CODES + c * 512 + to, a.v_codes + in + uint64_t(r) * (C::D / 2));
         }
       }
       constexpr int kLanes = C::SCALES / 32;  // lanes that carry one granule's scales
@@ -373,7 +384,7 @@ struct State {
   float o[C::MT][C::NT][4];      // [m-tile][n-tile]: dimension pair x row pair
   float ref[C::NT][2];           // minus the reference of rows 2t, 2t + 1 (exponents of two)
   float sum[C::NT][2];           // this lane's keys only
-  int kref, vref;                // scale codes that K and the accumulators are relative to
+  int vref;                      // scale code that the accumulators are relative to
 };
 
 // U granules (16 U keys) of a stage, the first of them granule u0. key0: the
@@ -388,37 +399,28 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
   const uint8_t *ks = ring + 2 * C::CODES + u0 * 16 * (D / 32), *vs = ks + C::SCALES;
   key0 += 16 * u0;
 
-  // ---- scale codes: K of keys 16 u + g + 8 v, V of keys 16 u + 8 v + 2 t + e
-  uint32_t kcode[U][2], vcode[U][2][2];
+  // ---- scale codes of V: keys 16 u + 8 v + 2 t + e
+  uint32_t vcode[U][2][2], vtop = 0;
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      kcode[u][v] = ks[(16 * u + 8 * v + g) * (D / 32) + t / (128 / D)];
+    for (int v = 0; v < 2; ++v)
 #pragma unroll
       for (int e = 0; e < 2; ++e) vcode[u][v][e] = vs[(16 * u + 8 * v + 2 * t + e) * (D / 32) + g / (256 / D)];
-    }
   if (masked) {  // past the end there may be anything
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (key0 + 16 * u + 8 * v + g >= len) kcode[u][v] = 0;
+      for (int v = 0; v < 2; ++v)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (key0 + 16 * u + 8 * v + 2 * t + e >= len) vcode[u][v][e] = 0;
-      }
   }
-  uint32_t ktop = 0, vtop = 0;
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      ktop = max(ktop, kcode[u][v]);
-      vtop = max(vtop, max(vcode[u][v][0], vcode[u][v][1]));
-    }
-  if (__any_sync(0xFFFFFFFFu, int(ktop) > st.kref || int(vtop) > st.vref)) {
-    st.kref = max(st.kref, int(__reduce_max_sync(0xFFFFFFFFu, ktop)));
+    for (int v = 0; v < 2; ++v) vtop = max(vtop, max(vcode[u][v][0], vcode[u][v][1]));
+  if (__any_sync(0xFFFFFFFFu, int(vtop) > st.vref)) {
     const int next = max(st.vref, int(__reduce_max_sync(0xFFFFFFFFu, vtop)));
     const float f = __uint_as_float(uint32_t(max(127 - (next - st.vref), 0)) << 23);
     st.vref = next;
@@ -430,51 +432,54 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
         for (int c = 0; c < 4; ++c) st.o[i][n][c] *= f;
   }
 
-  // ---- scores
-  constexpr int QW = D / 32;  // 32-bit words of a lane's quarter row
-  uint32_t kw[U][2][QW], kf[U][2];
-  const float kunit = pow2_unit(st.kref);
+  // ---- scores: keys 16 u + g + 8 v. A lane's word t of each group: two k-steps of a
+  // group, then the group's partial score times its scale, 2^(code - 127), in binary32.
+  constexpr int GR = D / 32;  // groups
+  uint32_t kw[U][2][GR], kscale[U][2];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const int key = 16 * u + 8 * v + g;
-      if constexpr (D == 128) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(kc + key * (D / 2) + 16 * t);
-        kw[u][v][0] = w.x, kw[u][v][1] = w.y, kw[u][v][2] = w.z, kw[u][v][3] = w.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(kc + key * (D / 2) + 8 * t);
-        kw[u][v][0] = w.x, kw[u][v][1] = w.y;
-      }
-      const float f = pow2_rel(kcode[u][v], kunit);
-      kf[u][v] = f16x2(f, f);
+#pragma unroll
+      for (int j = 0; j < GR; ++j)
+        kw[u][v][j] = *reinterpret_cast<const uint32_t *>(kc + key * (D / 2) + ((j ^ swizzle<D>(g)) << 4) + 4 * t);
+      if constexpr (D == 128)
+        kscale[u][v] = *reinterpret_cast<const uint32_t *>(ks + key * 4);
+      else
+        kscale[u][v] = *reinterpret_cast<const uint16_t *>(ks + key * 2);
     }
   float s[U][NT][4];
 #pragma unroll
-  for (int k = 0; k < C::KS; ++k) {
-    uint2 b[NT];
+  for (int j = 0; j < GR; ++j) {
+    uint2 b[2][NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if constexpr (C::QREG)
-        b[n] = qreg[n][k];
-      else
-        b[n] = sm.q[n][k][lane];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t r[2][2];
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint32_t w = kw[u][v][k / 2];
-        r[v][0] = mul2(k & 1 ? decode2<2>(w) : decode2<0>(w), kf[u][v]);
-        r[v][1] = mul2(k & 1 ? decode2<3>(w) : decode2<1>(w), kf[u][v]);
-      }
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (k == 0)
-          mma_f16_first(s[u][n], r[0][0], r[1][0], r[0][1], r[1][1], b[n].x, b[n].y);
+        if constexpr (C::QREG)
+          b[h][n] = qreg[n][2 * j + h];
         else
-          mma_f16(s[u][n], r[0][0], r[1][0], r[0][1], r[1][1], b[n].x, b[n].y);
+          b[h][n] = sm.q[n][2 * j + h][lane];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t x = kw[u][0][j], y = kw[u][1][j];
+      float f[2];
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+        f[v] = __uint_as_float((j == 0   ? kscale[u][v] << 23
+                                : j == 1 ? kscale[u][v] << 15
+                                : j == 2 ? kscale[u][v] << 7
+                                         : kscale[u][v] >> 1) &
+                               0x7F800000u);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float d[4];
+        mma_f16_first(d, decode2<0>(x), decode2<0>(y), decode2<1>(x), decode2<1>(y), b[0][n].x, b[0][n].y);
+        mma_f16(d, decode2<2>(x), decode2<2>(y), decode2<3>(x), decode2<3>(y), b[1][n].x, b[1][n].y);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[u][n][c] = j == 0 ? d[c] * f[c >> 1] : fmaf(d[c], f[c >> 1], s[u][n][c]);
       }
     }
   }
@@ -492,13 +497,12 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
       }
   }
   // ---- reference
-  const float kscale = ue8m0_to_float(uint32_t(st.kref));
   float mul[NT][2];
   bool move = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float2 m = *reinterpret_cast<const float2 *>(&sm.mul[8 * n + 2 * t]);
-    mul[n][0] = fmaxf(m.x * kscale, 0x1p-126f), mul[n][1] = fmaxf(m.y * kscale, 0x1p-126f);  // never 0: -inf stays
+    mul[n][0] = m.x, mul[n][1] = m.y;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float x = fmaxf(s[0][n][e], s[0][n][2 + e]);
@@ -543,15 +547,16 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
         st.sum[n][1] += y;
         p[u][n][v] = transpose8x8(f16x2(x, y));
       }
-  // ---- values
+  // ---- values: even and odd dimensions of two keys, interleaved
   constexpr int VW = D / 64;  // 32-bit words of a lane's eighth of a row
   const float vunit = pow2_unit(st.vref);
+  uint32_t vlo[U][2][VW], vhi[U][2][VW], vf[U][2];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    uint32_t lo[2][VW], hi[2][VW], vf[2];  // even and odd dimensions of two keys, interleaved
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      const uint8_t *row = vc + (16 * u + 8 * v + 2 * t) * (D / 2) + g * (D / 16);
+      const uint8_t *row = vc + (16 * u + 8 * v + 2 * t) * (D / 2) + (((g / (256 / D)) ^ swizzle<D>(2 * t)) << 4) +
+                           g * (D / 16) % 16;
       uint32_t x[VW], y[VW];
       if constexpr (VW == 2) {
         const uint2 xx = *reinterpret_cast<const uint2 *>(row), yy = *reinterpret_cast<const uint2 *>(row + D / 2);
@@ -562,27 +567,30 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
       }
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
-        lo[v][w] = (x[w] & 0x0F0F0F0Fu) | ((y[w] << 4) & 0xF0F0F0F0u);
-        hi[v][w] = ((x[w] >> 4) & 0x0F0F0F0Fu) | (y[w] & 0xF0F0F0F0u);
+        vlo[u][v][w] = (x[w] & 0x0F0F0F0Fu) | ((y[w] << 4) & 0xF0F0F0F0u);
+        vhi[u][v][w] = ((x[w] >> 4) & 0x0F0F0F0Fu) | (y[w] & 0xF0F0F0F0u);
       }
-      vf[v] = f16x2(pow2_rel(vcode[u][v][0], vunit), pow2_rel(vcode[u][v][1], vunit));
+      vf[u][v] = f16x2(pow2_rel(vcode[u][v][0], vunit), pow2_rel(vcode[u][v][1], vunit));
     }
+
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int i = 0; i < C::MT; ++i) {
       uint32_t r[2][2];
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        const uint32_t l = lo[v][i / 4], h = hi[v][i / 4];
+        const uint32_t l = vlo[u][v][i / 4], h = vhi[u][v][i / 4];
         r[v][0] = mul2((i & 3) == 0   ? decode2<0>(l)
                        : (i & 3) == 1 ? decode2<1>(l)
                        : (i & 3) == 2 ? decode2<2>(l)
                                       : decode2<3>(l),
-                       vf[v]);
+                       vf[u][v]);
         r[v][1] = mul2((i & 3) == 0   ? decode2<0>(h)
                        : (i & 3) == 1 ? decode2<1>(h)
                        : (i & 3) == 2 ? decode2<2>(h)
                                       : decode2<3>(h),
-                       vf[v]);
+                       vf[u][v]);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma_f16(st.o[i][n], r[0][0], r[0][1], r[1][0], r[1][1], p[u][n][0], p[u][n][1]);
@@ -609,19 +617,20 @@ __device__ __forceinline__ void store_lse(const PagedArgs &a, const Seq &s, int 
 // The queries of a row block, as operand registers, with their limits and multipliers.
 template <class T, class C>
 __device__ void load_queries(const PagedArgs &a, typename C::Smem &sm, const Segment &seg, int warp) {
-  constexpr int D = C::D, E = D / 4;  // a lane's dimensions
+  constexpr int D = C::D, GR = D / 32;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   for (int n = warp; n < C::NT; n += C::W) {
     const int r = seg.r0 + 8 * n + g;
     const bool real = r < seg.s.n * a.group;
     const int tok = r / a.group, h = seg.kv * a.group + r - tok * a.group;
-    uint4 raw[E / 8];
+    uint4 raw[GR];  // dimensions 32 i + 8 t .. + 7
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E / 8; ++i) {
+    for (int i = 0; i < GR; ++i) {
       raw[i] = make_uint4(0, 0, 0, 0);
       if (real)
-        raw[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(seg.s.row0 + tok) * a.q_stride + int64_t(h) * D + E * t) + i);
+        raw[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(seg.s.row0 + tok) * a.q_stride + int64_t(h) * D +
+                                                       32 * i + 8 * t));
       raw[i].x ^= a.flip, raw[i].y ^= a.flip, raw[i].z ^= a.flip, raw[i].w ^= a.flip;
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
@@ -633,7 +642,7 @@ __device__ void load_queries(const PagedArgs &a, typename C::Smem &sm, const Seg
     const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -100), 126);
     const float up = __uint_as_float(uint32_t(127 + 14 - e > 254 ? 254 : 127 + 14 - e) << 23);
 #pragma unroll
-    for (int i = 0; i < E / 8; ++i) {
+    for (int i = 0; i < GR; ++i) {
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -641,7 +650,7 @@ __device__ void load_queries(const PagedArgs &a, typename C::Smem &sm, const Seg
                                               f16x2(T::lo(w[2 * c + 1]) * up, T::hi(w[2 * c + 1]) * up));
     }
     if (t == 0) {
-      sm.mul[8 * n + g] = a.scale2 / up;
+      sm.mul[8 * n + g] = fmaxf(a.scale2 / up, 0x1p-126f);  // not 0: -inf must stay -inf
       sm.limit[8 * n + g] = real ? min(seg.s.len, max(0, seg.s.len - seg.s.n + tok + 1)) : 0;
     }
   }
@@ -687,7 +696,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
 #pragma unroll
         for (int c = 0; c < 4; ++c) st.o[i][n][c] = 0.0f;
     }
-    st.kref = st.vref = 0;
+    st.vref = 0;
     uint2 qreg[C::QREG ? NT : 1][C::QREG ? C::KS : 1];
     if constexpr (C::QREG) {
 #pragma unroll
