@@ -24,6 +24,7 @@ another stream than the one it was allocated on is kept alive by the caller
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -47,12 +48,12 @@ class KVCacheMXFP4:
 
     def __post_init__(self):
         pages, heads, page, half = _shape(self.k_codes, 4, "k_codes")
-        want = {"k_codes": half, "v_codes": half, "k_scales": half // 16, "v_scales": half // 16}
-        for name, width in want.items():
-            t = getattr(self, name)
-            if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.device != self.k_codes.device:
+        device = self.k_codes.get_device()
+        for name, t, width in (("k_codes", self.k_codes, half), ("k_scales", self.k_scales, half // 16),
+                               ("v_codes", self.v_codes, half), ("v_scales", self.v_scales, half // 16)):
+            if t.dtype is not torch.uint8 or device < 0 or t.get_device() != device or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor on the cache's device")
-            if tuple(t.shape) != (pages, heads, page, width):
+            if t.shape != (pages, heads, page, width):
                 raise ValueError(f"{name} must have shape {(pages, heads, page, width)}, not {tuple(t.shape)}")
 
     @classmethod
@@ -93,42 +94,64 @@ def _shape(t: torch.Tensor, dims: int, name: str):
     return t.shape
 
 
-def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+def _rows(t: torch.Tensor, name: str, device: int, dtype: torch.dtype) -> int:
     """Row stride of a [rows][heads][dim] tensor whose rows are contiguous."""
     rows, heads, dim = _shape(t, 3, name)
-    if not t.is_cuda or t.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be a CUDA tensor in bf16 or fp16")
-    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+    if device < 0 or dtype not in _DTYPES:
+        raise ValueError("q must be a CUDA tensor in bf16 or fp16")
+    if t.get_device() != device or t.dtype is not dtype:
         raise ValueError(f"{name} must have the device and type of q")
+    step, head, one = t.stride()
+    if rows > 1 and heads > 1 and dim > 1:
+        if one != 1 or head != dim:
+            raise ValueError(f"the heads of a row of {name} must be contiguous")
+        return step
     if t.numel() == 0:  # strides of an empty tensor say nothing
         return heads * dim
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    if (dim > 1 and one != 1) or (heads > 1 and head != dim):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return t.stride(0) if rows > 1 else heads * dim
+    return step if rows > 1 else heads * dim
 
 
-def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, like: torch.Tensor) -> torch.Tensor:
-    if t.dtype != dtype or t.device != like.device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: int) -> int:
+    """Address of a contiguous vector."""
+    if t.dtype is not dtype or t.get_device() != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on q's device")
-    return t
+    return t.data_ptr()
 
 
-def _status(t: torch.Tensor | None, like: torch.Tensor):
-    if t is not None and (t.dtype != torch.int32 or t.device != like.device or t.numel() < 1):
+def _status(t: torch.Tensor | None, device: int) -> int | None:
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.get_device() != device or t.numel() < 1:
         raise ValueError("d_status must be an int32 tensor on q's device")
-    return t
+    return t.data_ptr()
 
 
-def _out(out: torch.Tensor | None, q: torch.Tensor) -> torch.Tensor:
+def _out(out: torch.Tensor | None, q: torch.Tensor, device: int, dtype: torch.dtype) -> tuple[torch.Tensor, int]:
+    """The output tensor and its row stride."""
     if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return torch.empty(q.shape, dtype=dtype, device=q.device), q.shape[1] * q.shape[2]
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    return out
+    return out, _rows(out, "out", device, dtype)
 
 
-def _stream(stream, like: torch.Tensor):
-    return stream if stream is not None else torch.cuda.current_stream(like.device)
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)  # current_stream() without its Stream object
+    return abi.stream_ptr(stream)
+
+
+def _on(device: int, name: str, fn, *args):
+    """Calls an entry point with the device current, and checks its status."""
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != abi.MOE_OK:
+        abi.check(name, status)
 
 
 def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: torch.Tensor | None = None,
@@ -147,47 +170,63 @@ def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: 
     Returns {"q"}, plus "k" (rotated keys in 16 bits) with rotated_keys, plus "k_cached" and "v_cached" (the
     values that the 4-bit cache keeps) with cached_values.
     """
-    q_stride, k_stride, v_stride = _rows(q, "q"), _rows(k, "k", q), _rows(v, "v", q)
+    device, dtype = q.get_device(), q.dtype
+    q_stride, k_stride, v_stride = (_rows(q, "q", device, dtype), _rows(k, "k", device, dtype),
+                                    _rows(v, "v", device, dtype))
     T, H, D = q.shape
-    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
-        raise ValueError("k and v must be [T][kv heads][D] with the T and D of q")
     K = k.shape[1]
-    R = 0
+    if k.shape != (T, K, D) or v.shape != (T, K, D):
+        raise ValueError("k and v must be [T][kv heads][D] with the T and D of q")
+    R = table_rows = 0
+    rope_at = positions_at = slots_at = abi_cache = None
     if rope is not None:
-        if rope.dim() != 2 or rope.dtype != torch.float32 or rope.device != q.device or not rope.is_contiguous():
+        if rope.dim() != 2 or rope.dtype is not torch.float32 or rope.get_device() != device or \
+                not rope.is_contiguous():
             raise ValueError("rope must be a contiguous fp32 [positions][rotary_dim] tensor on q's device")
         if positions is None:
             raise ValueError("rope needs positions")
-        _vector(positions, "positions", torch.int32, T, q)
-        R = rope.shape[1]
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None:
-            _vector(w, name, q.dtype, D, q)
+        positions_at = _vector(positions, "positions", torch.int32, T, device)
+        table_rows, R = rope.shape
+        rope_at = rope.data_ptr()
     if (cache is None) != (slots is None):
         raise ValueError("cache and slots go together")
     if cache is not None:
-        if cache.k_codes.device != q.device or (cache.num_kv_heads, cache.head_dim) != (K, D):
+        if cache.k_codes.get_device() != device or (cache.num_kv_heads, cache.head_dim) != (K, D):
             raise ValueError("the cache must be on q's device, with the kv heads and head size of k")
-        _vector(slots, "slots", torch.int64, T, q)
+        slots_at = _vector(slots, "slots", torch.int64, T, device)
+        abi_cache = cache.as_abi()
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != q.device or not q_out.is_contiguous():
+        q_out = torch.empty((T, H, D), dtype=dtype, device=q.device)
+    elif q_out.shape != q.shape or q_out.dtype is not dtype or q_out.get_device() != device or \
+            not q_out.is_contiguous():
         raise ValueError("q_out must be contiguous, with the shape, type and device of q")
     out = {"q": q_out}
-    kv = dict(size=(T, K, D), dtype=q.dtype, device=q.device)
+    k_at = k_cached_at = v_cached_at = None
     if rotated_keys:
-        out["k"] = torch.empty(**kv)
+        out["k"] = torch.empty((T, K, D), dtype=dtype, device=q.device)
+        k_at = out["k"].data_ptr()
     if cached_values:
-        out["k_cached"], out["v_cached"] = torch.empty(**kv), torch.empty(**kv)
-    io = abi.MoeQkvAppendIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, T, H, K, D,
-                            _DTYPES[q.dtype], R, int(interleaved), rope.shape[0] if rope is not None else 0,
-                            abi.ptr(rope), abi.ptr(positions) if R else None, abi.ptr(q_norm), abi.ptr(k_norm), eps,
-                            abi.ptr(slots), q_out.data_ptr(), abi.ptr(out.get("k")), abi.ptr(out.get("k_cached")),
-                            abi.ptr(out.get("v_cached")))
-    with torch.cuda.device(q.device):
-        abi.check("moe_qkv_append", abi.moe_qkv_append(io, cache.as_abi() if cache is not None else None,
-                                                       _status(d_status, q), _stream(stream, q)))
+        out["k_cached"] = torch.empty((T, K, D), dtype=dtype, device=q.device)
+        out["v_cached"] = torch.empty((T, K, D), dtype=dtype, device=q.device)
+        k_cached_at, v_cached_at = out["k_cached"].data_ptr(), out["v_cached"].data_ptr()
+    io = abi.MoeQkvAppendIO(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, T, H, K, D, _DTYPES[dtype], R,
+        int(interleaved), table_rows, rope_at, positions_at,
+        None if q_norm is None else _vector(q_norm, "q_norm", dtype, D, device),
+        None if k_norm is None else _vector(k_norm, "k_norm", dtype, D, device),
+        eps, slots_at, q_out.data_ptr(), k_at, k_cached_at, v_cached_at)
+    _on(device, "moe_qkv_append", abi.moe_qkv_append, io, abi_cache, _status(d_status, device),
+        _raw_stream(stream, device))
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_workspace(device: int, rows: int, max_rows: int, heads: int, kv_heads: int, dim: int) -> int:
+    """Bytes of workspace, which depend on these sizes alone."""
+    io = abi.MoeAttendPagedIO(num_rows=rows, max_rows=max_rows, num_heads=heads)
+    with torch.cuda.device(device):
+        return abi.moe_attend_paged_workspace(
+            io, abi.MoeKvCache(page_size=16, num_kv_heads=kv_heads, head_dim=dim))
 
 
 def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -204,35 +243,32 @@ def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor,
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
-    q_stride = _rows(q, "q")
+    device, dtype = q.get_device(), q.dtype
+    q_stride = _rows(q, "q", device, dtype)
     T, H, D = q.shape
     B = lengths.shape[0] if lengths.dim() == 1 else -1
-    _vector(lengths, "lengths", torch.int32, B, q)
-    _vector(cu_rows, "cu_rows", torch.int32, B + 1, q)
-    if page_table.dtype != torch.int32 or page_table.device != q.device or page_table.dim() != 2 or \
+    lengths_at = _vector(lengths, "lengths", torch.int32, B, device)
+    cu_at = _vector(cu_rows, "cu_rows", torch.int32, B + 1, device)
+    if page_table.dtype is not torch.int32 or page_table.get_device() != device or page_table.dim() != 2 or \
             page_table.shape[0] != B or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 [sequences][pages] tensor on q's device")
-    if cache.k_codes.device != q.device or cache.head_dim != D:
-        raise ValueError("the cache must be on q's device, with q's head size")
-    out = _out(out, q)
-    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
-    io = abi.MoeAttendPagedIO(q.data_ptr(), q_stride, out.data_ptr(), _rows(out, "out", q), abi.ptr(lse),
-                              page_table.data_ptr(), lengths.data_ptr(), cu_rows.data_ptr(), B, T,
-                              page_table.shape[1], max_rows, H, _DTYPES[q.dtype],
-                              D ** -0.5 if scale is None else scale)
     c = cache.as_abi()
-    st = _stream(stream, q)
-    with torch.cuda.device(q.device), torch.cuda.stream(_torch_stream(st, q) if stream is not None else None):
-        n = abi.moe_attend_paged_workspace(io, c)
-        workspace = torch.empty((n,), dtype=torch.uint8, device=q.device) if n else None
-        abi.check("moe_attend_paged", abi.moe_attend_paged(io, c, workspace, n, _status(d_status, q), st))
+    if cache.k_codes.get_device() != device or c.head_dim != D:
+        raise ValueError("the cache must be on q's device, with q's head size")
+    out, out_stride = _out(out, q, device, dtype)
+    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
+    io = abi.MoeAttendPagedIO(q.data_ptr(), q_stride, out.data_ptr(), out_stride,
+                              lse.data_ptr() if return_lse else None, page_table.data_ptr(), lengths_at, cu_at, B, T,
+                              page_table.shape[1], max_rows, H, _DTYPES[dtype], D ** -0.5 if scale is None else scale)
+    n = _paged_workspace(device, T, max_rows, H, c.num_kv_heads, D)
+    if stream is None:
+        workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+    else:  # allocated on the stream that uses it, so that it is not handed out again before the call has run
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+            workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+    _on(device, "moe_attend_paged", abi.moe_attend_paged, io, c, workspace.data_ptr(), n, _status(d_status, device),
+        _raw_stream(stream, device))
     return (out, lse) if return_lse else out
-
-
-def _torch_stream(st, like: torch.Tensor):
-    """The stream as a torch stream: the workspace is allocated on it, so that it is not handed out again before
-    the call has run."""
-    return torch.cuda.ExternalStream(st, device=like.device) if isinstance(st, int) else st
 
 
 def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, cu_keys: torch.Tensor, *,
@@ -245,21 +281,24 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
-    q_stride, k_stride, v_stride = _rows(q, "q"), _rows(k, "k", q), _rows(v, "v", q)
+    device, dtype = q.get_device(), q.dtype
+    q_stride, k_stride, v_stride = (_rows(q, "q", device, dtype), _rows(k, "k", device, dtype),
+                                    _rows(v, "v", device, dtype))
     T, H, D = q.shape
-    if k.shape != v.shape or k.shape[2] != D:
+    N, K = k.shape[:2]
+    if k.shape != (N, K, D) or v.shape != (N, K, D):
         raise ValueError("k and v must be [keys][kv heads][D] with the D of q")
     n = cu_rows.shape[0] if cu_rows.dim() == 1 else 0
     if n < 1:
         raise ValueError("cu_rows needs an entry for each sequence and one for the end")
-    _vector(cu_rows, "cu_rows", torch.int32, n, q)
-    _vector(cu_keys, "cu_keys", torch.int32, n, q)
-    out = _out(out, q)
+    cu_rows_at = _vector(cu_rows, "cu_rows", torch.int32, n, device)
+    cu_keys_at = _vector(cu_keys, "cu_keys", torch.int32, n, device)
+    out, out_stride = _out(out, q, device, dtype)
     lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
-    io = abi.MoeAttendPromptIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, out.data_ptr(),
-                               _rows(out, "out", q), abi.ptr(lse), cu_rows.data_ptr(), cu_keys.data_ptr(), n - 1, T,
-                               k.shape[0], H, k.shape[1], D, _DTYPES[q.dtype], int(causal),
+    io = abi.MoeAttendPromptIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
+                               out.data_ptr(), out_stride, lse.data_ptr() if return_lse else None, cu_rows_at,
+                               cu_keys_at, n - 1, T, N, H, K, D, _DTYPES[dtype], int(causal),
                                D ** -0.5 if scale is None else scale)
-    with torch.cuda.device(q.device):
-        abi.check("moe_attend_prompt", abi.moe_attend_prompt(io, _status(d_status, q), _stream(stream, q)))
+    _on(device, "moe_attend_prompt", abi.moe_attend_prompt, io, _status(d_status, device),
+        _raw_stream(stream, device))
     return (out, lse) if return_lse else out
