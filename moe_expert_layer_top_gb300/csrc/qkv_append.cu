@@ -91,8 +91,9 @@ __device__ __forceinline__ void unpack4(const uint2 &r, float *x) {
 }
 
 template <class T>
-__device__ __forceinline__ uint2 pack4(const float *x) {
-  return make_uint2(T::pack(x[0], x[1]), T::pack(x[2], x[3]));
+__device__ __forceinline__ void unpack8(const uint4 &r, float (&x)[8]) {
+  unpack4<T>(make_uint2(r.x, r.y), x);
+  unpack4<T>(make_uint2(r.z, r.w), x + 4);
 }
 
 template <class T>
@@ -135,16 +136,15 @@ __device__ __forceinline__ Lane make_lane(const moe_qkv_append_io_t &io, int64_t
   return t;
 }
 
-template <class T>
-__device__ __forceinline__ void load_run(const uint16_t *head, const Lane &t, float (&x)[8]) {
-  unpack4<T>(*reinterpret_cast<const uint2 *>(head + t.a), x);
-  unpack4<T>(*reinterpret_cast<const uint2 *>(head + t.b), x + 4);
+// Both runs of the lane, of a head.
+__device__ __forceinline__ uint4 load_runs(const uint16_t *head, const Lane &t) {
+  const uint2 a = *reinterpret_cast<const uint2 *>(head + t.a), b = *reinterpret_cast<const uint2 *>(head + t.b);
+  return make_uint4(a.x, a.y, b.x, b.y);
 }
 
-template <class T>
-__device__ __forceinline__ void store_run(uint16_t *head, const Lane &t, const float (&y)[8]) {
-  *reinterpret_cast<uint2 *>(head + t.a) = pack4<T>(y);
-  *reinterpret_cast<uint2 *>(head + t.b) = pack4<T>(y + 4);
+__device__ __forceinline__ void store_runs(uint16_t *head, const Lane &t, const uint4 &y) {
+  *reinterpret_cast<uint2 *>(head + t.a) = make_uint2(y.x, y.y);
+  *reinterpret_cast<uint2 *>(head + t.b) = make_uint2(y.z, y.w);
 }
 
 // y = the rotated x; the two orders of the pairs differ in which elements they are.
@@ -240,8 +240,7 @@ __device__ __forceinline__ void key_head(const moe_qkv_append_io_t &io, const La
 template <class T>
 __device__ __forceinline__ void quantize_head(const uint4 &raw, uint32_t &codes, uint32_t &scale, uint4 *values) {
   float x[8];
-  unpack4<T>(make_uint2(raw.x, raw.y), x);
-  unpack4<T>(make_uint2(raw.z, raw.w), x + 4);
+  unpack8<T>(raw, x);
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
@@ -304,32 +303,45 @@ __global__ void __launch_bounds__(kThreads) qkv_append_kernel(const AppendArgs a
   const auto *q = static_cast<const uint16_t *>(io.q) + t * io.q_stride;
   const auto *k = static_cast<const uint16_t *>(io.k) + t * io.k_stride;
   const auto *v = static_cast<const uint16_t *>(io.v) + t * io.v_stride;
+  // The next unit's elements are on their way while one is computed.
+  const auto load = [&](int u) {
+    const bool is_k = u < uk, is_q = !is_k && u < uk + uq;
+    const int h = (is_k ? u : is_q ? u - uk : u - uk - uq) * kHeads + sub;
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (u < units && h < (is_q ? nq : nk)) {
+      if (is_q || is_k)
+        r = load_runs((is_q ? q : k) + int64_t(h) * D, hold);
+      else
+        r = reinterpret_cast<const uint4 *>(v + int64_t(h) * D)[l];
+    }
+    return r;
+  };
+  uint4 next = load(part);
   for (int u = part; u < units; u += a.parts) {
     const bool is_k = u < uk, is_q = !is_k && u < uk + uq;
     const int h = (is_k ? u : is_q ? u - uk : u - uk - uq) * kHeads + sub;
     const bool real = h < (is_q ? nq : nk);
+    uint4 raw = next;
+    next = load(u + a.parts);
     if (is_q) {
-      float x[8] = {}, y[8], w[8] = {};
-      if (io.q_norm) load_run<T>(static_cast<const uint16_t *>(io.q_norm), hold, w);
-      if (real) load_run<T>(q + int64_t(h) * D, hold, x);
+      float x[8], y[8], w[8] = {};
+      if (io.q_norm) unpack8<T>(load_runs(static_cast<const uint16_t *>(io.q_norm), hold), w);
+      unpack8<T>(raw, x);
       query_head<D>(io, hold, w, x, y);
-      if (real) store_run<T>(static_cast<uint16_t *>(io.q_out) + (t * nq + h) * D, hold, y);
+      if (real) store_runs(static_cast<uint16_t *>(io.q_out) + (t * nq + h) * D, hold, pack8<T>(y));
       continue;
     }
-    uint4 raw = make_uint4(0, 0, 0, 0);
     const int64_t row = (t * nk + h) * D;
     if (is_k) {
-      float x[8] = {}, y[8], w[8] = {};
-      if (io.k_norm) load_run<T>(static_cast<const uint16_t *>(io.k_norm), hold, w);
-      if (real) load_run<T>(k + int64_t(h) * D, hold, x);
+      float x[8], y[8], w[8] = {};
+      if (io.k_norm) unpack8<T>(load_runs(static_cast<const uint16_t *>(io.k_norm), hold), w);
+      unpack8<T>(raw, x);
       key_head<D>(io, hold, w, x, y);
       __syncwarp();  // the last unit's keys have been read
-      store_run<T>(reinterpret_cast<uint16_t *>(turned[warp]) + sub * D, hold, y);
+      store_runs(reinterpret_cast<uint16_t *>(turned[warp]) + sub * D, hold, pack8<T>(y));
       __syncwarp();
       raw = turned[warp][lane];
       if (io.k_out && real) reinterpret_cast<uint4 *>(static_cast<uint16_t *>(io.k_out) + row)[l] = raw;
-    } else if (real) {
-      raw = reinterpret_cast<const uint4 *>(v + int64_t(h) * D)[l];
     }
     uint32_t codes, scale;
     uint4 values;
