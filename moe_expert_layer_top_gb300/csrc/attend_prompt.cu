@@ -114,6 +114,19 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// One lane of the (whole) warp. The compiler knows that code under this
+// predicate runs in a single lane; under lane == 0 it would loop over lanes
+// around every instruction that takes uniform registers (each MMA).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Descriptor of V as the N-major B operand: 64 values of N (128 bytes) by 8
 // keys is one swizzled block of 1024 bytes; blocks of the next 8 keys follow
 // (stride offset), the next 64 values of N lie a part (128 keys) further
@@ -288,6 +301,37 @@ __device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, int n,
 
 // ------------------------------------------------------------------ softmax (warps 0-7)
 
+// A row's scores of one key tile; keys from lim on are hidden.
+__device__ __forceinline__ void load_scores(uint32_t ts, int lim, uint32_t (&s)[kKeys]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_wait_ld(s + 32 * i);
+  if (__any_sync(0xFFFFFFFFu, lim < kKeys)) {
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i)
+      if (i >= lim) s[i] = 0xFF800000u;  // -inf
+  }
+}
+
+// P = 2^(s scale2 + base) in 16 bits, the row's largest score, and the sum of P before its rounding.
+template <class T>
+__device__ __forceinline__ void exponentials(const uint32_t (&s)[kKeys], uint32_t (&p)[kKeys / 2], float scale2,
+                                             float base, float &top, float &sum) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kKeys; i += 2) {
+    const float x = __uint_as_float(s[i]), y = __uint_as_float(s[i + 1]);
+    const int c = (i >> 1) & 3;
+    mx[c] = fmaxf(mx[c], fmaxf(x, y));
+    const float u = exp2_approx(fmaf(x, scale2, base)), v = exp2_approx(fmaf(y, scale2, base));
+    add[c] += u + v;
+    p[i / 2] = T::pack(u, v);
+  }
+  top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  sum = (add[0] + add[1]) + (add[2] + add[3]);
+}
+
 template <class T, int D>
 __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
@@ -326,37 +370,29 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (!ok) break;
     tmem_fence_after();
-    uint32_t s[kKeys];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_wait_ld(s + 32 * i);
     const int lim = limit - j * kKeys;
-    if (__any_sync(0xFFFFFFFFu, lim < kKeys)) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (i >= lim) s[i] = 0xFF800000u;  // -inf
+    uint32_t s[kKeys], p[kKeys / 2];
+    float top, sum;
+    load_scores(ts, lim, s);
+    bool redo = true;
+    if (j > 0) {  // with the reference as it is; the maximum only says whether that was good enough
+      exponentials<T>(s, p, a.scale2, -ref * a.scale2, top, sum);
+      redo = __any_sync(0xFFFFFFFFu, (top - ref) * a.scale2 > kLazy);
+      if (redo) load_scores(ts, lim, s);  // P is not stored yet: S is still there
     }
-    float mx[4];
+    if (redo) {
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
-#pragma unroll
-    for (int i = 4; i < kKeys; i += 8)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float u = __uint_as_float(s[i + c]);
-        mx[c] = i + c + 4 < kKeys ? fmaxf(mx[c], fmaxf(u, __uint_as_float(s[i + c + 4]))) : fmaxf(mx[c], u);
-      }
-    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    if (j == 0) {
-      ref = top == -INFINITY ? 0.0f : top;
-    } else {
-      const bool move = (top - ref) * a.scale2 > kLazy;
-      if (__any_sync(0xFFFFFFFFu, move)) {
+      for (int i = 0; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+      top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (j == 0) {
+        ref = top == -INFINITY ? 0.0f : top;
+      } else {
+        const bool move = (top - ref) * a.scale2 > kLazy;
         const float f = move ? exp2_approx((ref - top) * a.scale2) : 1.0f;
         if (move) ref = top;
         total *= f;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           uint32_t o[32];
           tmem_ld32(to + 32 * i, o);
@@ -366,20 +402,11 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
           tmem_st32(to + 32 * i, o);
         }
       }
+      exponentials<T>(s, p, a.scale2, -ref * a.scale2, top, sum);
     }
-    const float base = -ref * a.scale2;
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t p[kKeys / 2];
-#pragma unroll
-    for (int i = 0; i < kKeys; i += 2) {
-      const float u = exp2_approx(fmaf(__uint_as_float(s[i]), a.scale2, base));
-      const float v = exp2_approx(fmaf(__uint_as_float(s[i + 1]), a.scale2, base));
-      sum[(i >> 1) & 3] += u + v;
-      p[i / 2] = T::pack(u, v);
-    }
+    total += sum;
     tmem_st32(ts, p);
     tmem_st32(ts + 32, p + 32);
-    total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     tmem_wait_st();
     tmem_fence_before();
     __syncwarp();
@@ -483,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (n > 0 && warp == kWarpLoad) load_warp<D>(&kmap, &vmap, a, sm, w, n);
-    if (n > 0 && warp == kWarpMma && lane == 0) mma_lane<T, D>(a, sm, w, n, tmem);
+    if (n > 0 && warp == kWarpMma && elect_one()) mma_lane<T, D>(a, sm, w, n, tmem);
   }
   __syncwarp();
   tmem_fence_before();
