@@ -22,11 +22,14 @@
 //   warp 8      TMA: K and V tiles of 128 keys into a ring of shared memory;
 //               at the end it zeroes the rows of the last V tile that lie past
 //               the sequence (they belong to the next one, and 0 * NaN is NaN)
-//   warp 9      MMA issuer (one lane): S = Q K^T (both operands from shared memory), then
+//   warp 9      MMA issuer: S = Q K^T (both operands from shared memory), then
 //               O += P V with P from TMEM, where the softmax wrote it over S
-// TMEM: S of A and B (128 columns each), O of A and B (D columns each).
-// The MMAs of one thread run in the order of issue. So when S of tile j + 1 is
-// complete, O holds every tile up to j, and the softmax may rescale it in place.
+// The work is a list of steps (row tile, key tile): A0 B0 A1 B1 ..., then what
+// one of the two has left. TMEM holds O of both and a ring of S: step q has S
+// buffer q mod kBufs, so S of the next steps is computed while the softmax of
+// this one runs (D = 64: three buffers; D = 128 leaves room for two). The MMAs of
+// one thread run in the order of issue: S(q + kBufs) goes after P V of q, which
+// reads the same columns.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -41,14 +44,14 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a tile (MMA M, TMEM lanes)
 constexpr int kKeys = 128;     // keys of a tile
-constexpr int kSoftmaxThreads = 256, kThreads = 384;  // three warpgroups; two warps of the last have no work
+constexpr int kThreads = 384;  // three warpgroups; two warps of the last have no work
 // Registers: 168 a thread at launch (384 x 168 = 64,512). The softmax keeps a
 // row of 128 scores, so the last warpgroup hands most of its share to the other
 // two: 2 x 128 x 224 + 128 x 56 = 64,512.
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 224, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "register split");
 constexpr int kWarpLoad = 8, kWarpMma = 9;
-constexpr uint32_t kTmemCols = 512, kColO = 256;
+constexpr uint32_t kTmemCols = 512;
 constexpr int64_t kWaitNs = 1000000000;  // bound of every wait
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
 
@@ -69,18 +72,20 @@ template <int D>
 struct Smem {
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of Q, K or V: D/64 parts of 128 rows x 128 bytes
+  static constexpr int kBufs = D == 128 ? 2 : 3;  // S tiles in TMEM
+  static constexpr uint32_t kColO = kBufs * kKeys;
+  static_assert(kColO + 2 * D <= kTmemCols && kBufs <= 3, "TMEM budget");
   uint8_t q[2][kTileBytes];
   uint8_t kv[kStages][kTileBytes];
-  uint64_t q_full;           // 256 arrivals
   uint64_t full[kStages];    // a K or V tile landed
   uint64_t empty[kStages];   // the MMAs that read it are done
   uint64_t tail;             // the last V tile is zeroed past the sequence's end
-  uint64_t s_full[2];        // S of a tile complete
-  uint64_t p_full[2];        // P written (4 warps)
-  uint64_t o_full[2];        // the last MMA into O of a tile is done
+  uint64_t s_full[2][2];     // S of (row tile, key tile j) complete, by j mod 2: its waiters see every phase
+  uint64_t p_full[kBufs];    // P of a step written (4 warps)
+  uint64_t pv_done[2][2];    // P V of (row tile, key tile j) is in O, by j mod 2
+  uint64_t o_full[2];        // the row tile's last P V is in O
   uint64_t mma_done;
   uint32_t tmem_base;
-  int seq, local, tiles;
   static constexpr size_t kBytes = 2 * kTileBytes + kStages * kTileBytes + 512 + 1024;
 };
 
@@ -186,7 +191,13 @@ struct Work {
   int n;             // its query rows
   int r0;            // the block's first (row, head) pair
   int kv;            // kv head
-  int tiles[2];      // key tiles of row tiles A and B
+  int tiles0, tiles1;  // key tiles of row tiles A and B
+
+  __device__ __forceinline__ int tiles(int x) const { return x ? tiles1 : tiles0; }
+  __device__ __forceinline__ int both() const { return min(tiles0, tiles1); }  // key tiles that both have
+  __device__ __forceinline__ int all() const { return max(tiles0, tiles1); }
+  // the place of (row tile x, key tile j) in the list of steps
+  __device__ __forceinline__ int step(int x, int j) const { return j < both() ? 2 * j + x : both() + j; }
 };
 
 // Keys that pair r sees.
@@ -196,7 +207,15 @@ __device__ __forceinline__ int key_limit(const PromptArgs &a, const Work &w, int
 }
 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *status) {
-  if (mbar_wait(bar, parity, kWaitNs)) return true;
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (done || mbar_wait(bar, parity, kWaitNs)) return true;
   if (status) report_error(status, MOE_ERR_TIMEOUT);
   return false;
 }
@@ -205,11 +224,11 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *st
 
 template <int D>
 __device__ void load_warp(const CUtensorMap *kmap, const CUtensorMap *vmap, const PromptArgs &a, Smem<D> &sm,
-                          const Work &w, int n) {
+                          const Work &w) {
   using S = Smem<D>;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, n = w.all();
   int issued = 0;
-  if (lane == 0) {
+  if (elect_one()) {
     for (int i = 0; i < 2 * n; ++i) {  // K 0, V 0, K 1, V 1, ...
       const int s = i % S::kStages;
       if (!wait(&sm.empty[s], ((i / S::kStages) & 1) ^ 1, a.status)) break;
@@ -221,7 +240,7 @@ __device__ void load_warp(const CUtensorMap *kmap, const CUtensorMap *vmap, cons
       ++issued;
     }
   }
-  issued = __shfl_sync(0xFFFFFFFFu, issued, 0);
+  issued = __reduce_max_sync(0xFFFFFFFFu, unsigned(issued));
   const int cut = w.keys - (n - 1) * kKeys;  // keys of the last tile
   if (issued == 2 * n && cut < kKeys) {
     const int i = 2 * n - 1, s = i % S::kStages;
@@ -244,56 +263,81 @@ __device__ void load_warp(const CUtensorMap *kmap, const CUtensorMap *vmap, cons
 // ------------------------------------------------------------------ MMA issuer (one lane of warp 9)
 
 template <class T, int D>
-__device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, int n, uint32_t tmem) {
+__device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
   using S = Smem<D>;
   constexpr uint32_t kType = T::kMmaType;
   constexpr uint32_t kBase = (1u << 4) | (kType << 7) | (kType << 10) | (uint32_t(kRows >> 4) << 24);
   constexpr uint32_t kDescS = kBase | (uint32_t(kKeys >> 3) << 17);
   constexpr uint32_t kDescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);  // B is N-major
-  bool ok = wait(&sm.q_full, 0, a.status);
-  const auto landed = [&](int i) { return wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, a.status); };
-  const auto scores = [&](int x, int j) {  // S of row tile x, key tile j
-    const uint32_t q = smem_u32(sm.q[x]), k = smem_u32(sm.kv[(2 * j) % S::kStages]);
-#pragma unroll
-    for (int p = 0; p < D / 64; ++p) {
-      const uint64_t qd = sw128_desc(q + p * (kRows * 128)), kd = sw128_desc(k + p * (kKeys * 128));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // 16 values are 32 bytes: 2 in the descriptor's address field
-        mma_ss(tmem + x * kKeys, qd + 2 * i, kd + 2 * i, kDescS, (p | i) != 0);
-    }
-    mma_commit(&sm.s_full[x]);
-  };
-  if (ok) ok = landed(0);
-  if (ok) {
+  const int n = w.all(), m = w.both(), longer = w.tiles1 > w.tiles0 ? 1 : 0;
+  const int steps = w.tiles0 + w.tiles1;
+  // Two places in the list of steps, the next S to issue (k...) and the next P V (v...): row tile, key tile, the
+  // ring slot and phase of its K or V tile, the S buffer. Kept by increments, in registers: this lane's own latency
+  // is on the critical path.
+  int kx = m > 0 ? 0 : longer, kj = 0, kslot = 0, kbuf = 0, vx = kx, vj = 0, vslot = 1, vbuf = 0, issued = 0;
+  uint32_t kphase = 0, vphase = 0, pphase = 0;  // pphase: of the P buffers, flips when their ring starts over
+  bool kfresh = true, vfresh = true;            // the first step of its key tile
+  const uint64_t qd0 = sw128_desc(smem_u32(sm.q[0])), kd0 = sw128_desc(smem_u32(sm.kv[0])), vd0 = v_desc(smem_u32(sm.kv[0]));
+  constexpr uint32_t kTile = S::kTileBytes >> 4;  // in a descriptor's address field
+  const auto scores = [&] {                       // S of the next step into its buffer
+    if (kfresh && !wait(&sm.full[kslot], kphase, a.status)) return false;
     tmem_fence_after();
-    for (int x = 0; x < 2; ++x)
-      if (w.tiles[x] > 0) scores(x, 0);
-    mma_commit(&sm.empty[0]);
-  }
-  for (int j = 0; ok && j < n; ++j) {
-    const int vi = 2 * j + 1;
-    ok = landed(vi);
-    if (ok && j + 1 == n && w.keys < n * kKeys) ok = wait(&sm.tail, 0, a.status);
-    bool next = false;  // the next K tile has landed
-    for (int x = 0; ok && x < 2; ++x) {
-      if (j >= w.tiles[x]) continue;
-      ok = wait(&sm.p_full[x], j & 1, a.status);
-      if (!ok) break;
-      tmem_fence_after();
-      const uint64_t vd = v_desc(smem_u32(sm.kv[vi % S::kStages]));
+    const uint64_t qd = qd0 + (kx ? kTile : 0u), kd = kd0 + uint32_t(kslot) * kTile;
+    const uint32_t d = tmem + kbuf * kKeys;
 #pragma unroll
-      for (int i = 0; i < kKeys / 16; ++i)  // 16 keys: 8 columns of P, 2048 bytes of V
-        mma_ts(tmem + kColO + x * D, tmem + x * kKeys + 8 * i, vd + i * (2048 >> 4), kDescO, (j | i) != 0);
-      if (j + 1 < w.tiles[x]) {
-        if (!next) ok = next = landed(vi + 1);
-        if (!ok) break;
-        scores(x, j + 1);
-      } else {
-        mma_commit(&sm.o_full[x]);
+    for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)  // 16 values are 32 bytes: 2 in the address field
+        mma_ss(d, qd + p * (kRows * 128 >> 4) + 2 * c, kd + p * (kKeys * 128 >> 4) + 2 * c, kDescS, (p | c) != 0);
+    mma_commit(&sm.s_full[kx][kj & 1]);
+    kfresh = kx == 1 || kj >= m;  // the last step that reads this K tile
+    if (kfresh) {
+      mma_commit(&sm.empty[kslot]);
+      ++kj;
+      kx = kj < m ? 0 : longer;
+      kslot += 2;
+      if (kslot >= S::kStages) {
+        kslot -= S::kStages;
+        kphase ^= 1;
       }
+    } else {
+      kx = 1;
     }
-    mma_commit(&sm.empty[vi % S::kStages]);
-    if (j + 1 < n) mma_commit(&sm.empty[(vi + 1) % S::kStages]);
+    kbuf = kbuf + 1 == S::kBufs ? 0 : kbuf + 1;
+    ++issued;
+    return true;
+  };
+  bool ok = true;
+  while (ok && issued < S::kBufs && issued < steps) ok = scores();
+  for (int q = 0; ok && q < steps; ++q) {
+    if (vfresh)
+      ok = wait(&sm.full[vslot], vphase, a.status) && (vj + 1 < n || w.keys >= n * kKeys || wait(&sm.tail, 0, a.status));
+    ok = ok && wait(&sm.p_full[vbuf], pphase, a.status);
+    if (!ok) break;
+    tmem_fence_after();
+    const uint64_t vd = vd0 + uint32_t(vslot) * kTile;
+    const uint32_t pa = tmem + vbuf * kKeys, d = tmem + S::kColO + (vx ? D : 0);
+#pragma unroll
+    for (int c = 0; c < kKeys / 16; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
+      mma_ts(d, pa + 8 * c, vd + c * (2048 >> 4), kDescO, (vj | c) != 0);
+    if (issued < steps) ok = scores();
+    mma_commit(&sm.pv_done[vx][vj & 1]);
+    if (vj + 1 == w.tiles(vx)) mma_commit(&sm.o_full[vx]);
+    vfresh = vx == 1 || vj >= m;
+    if (vfresh) {
+      mma_commit(&sm.empty[vslot]);
+      ++vj;
+      vx = vj < m ? 0 : longer;
+      vslot += 2;
+      if (vslot >= S::kStages) {
+        vslot -= S::kStages;
+        vphase ^= 1;
+      }
+    } else {
+      vx = 1;
+    }
+    vbuf = vbuf + 1 == S::kBufs ? 0 : vbuf + 1;
+    if (vbuf == 0) pphase ^= 1;
   }
   mma_commit(&sm.mma_done);  // every MMA is done before TMEM is freed
   mbar_wait(&sm.mma_done, 0, kWaitNs);
@@ -332,42 +376,44 @@ __device__ __forceinline__ void exponentials(const uint32_t (&s)[kKeys], uint32_
   sum = (add[0] + add[1]) + (add[2] + add[3]);
 }
 
+// Q of the block into the swizzled K-major layout: 16 bytes a thread and round, a row side by side.
+template <int D>
+__device__ void load_queries(const PromptArgs &a, Smem<D> &sm, const Work &w) {
+  constexpr int kChunks = D / 8, kStep = 128 / kChunks;
+  const int x = threadIdx.x >> 7, row = threadIdx.x & 127, first = w.r0 + x * kRows, c = row % kChunks;
+  uint8_t *dst = sm.q[x] + (c >> 3) * (kRows * 128);
+#pragma unroll 8
+  for (int i = row / kChunks; i < kRows; i += kStep) {
+    const int r = first + i;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < w.rows) {
+      const int t = r / a.group, h = r - t * a.group;
+      v = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(w.row0 + t) * a.q_stride +
+                                                (int64_t(w.kv) * a.group + h) * D) + c);
+      v.x ^= a.flip;
+      v.y ^= a.flip;
+      v.z ^= a.flip;
+      v.w ^= a.flip;
+    }
+    *reinterpret_cast<uint4 *>(dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
+  }
+  fence_proxy_async();
+}
+
 template <class T, int D>
 __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
+  using S = Smem<D>;
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
-  const int first = w.r0 + x * kRows;
-  // Q of the tile into the swizzled K-major layout: 16 bytes a thread and round, a row side by side
-  {
-    constexpr int kChunks = D / 8, kStep = 128 / kChunks;
-    const int c = row % kChunks;
-    uint8_t *dst = sm.q[x] + (c >> 3) * (kRows * 128);
-#pragma unroll 8
-    for (int i = row / kChunks; i < kRows; i += kStep) {
-      const int r = first + i;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < w.rows) {
-        const int t = r / a.group, h = r - t * a.group;
-        v = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(w.row0 + t) * a.q_stride +
-                                                  (int64_t(w.kv) * a.group + h) * D) + c);
-        v.x ^= a.flip;
-        v.y ^= a.flip;
-        v.z ^= a.flip;
-        v.w ^= a.flip;
-      }
-      *reinterpret_cast<uint4 *>(dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
-    }
-    fence_proxy_async();
-    mbar_arrive(&sm.q_full);
-  }
-  const int r = first + row;
+  const int r = w.r0 + x * kRows + row;
   const int limit = key_limit(a, w, r);
   const uint32_t lanes = uint32_t(warp * 32) << 16;
-  const uint32_t ts = tmem + lanes + x * kKeys, to = tmem + lanes + kColO + x * D;
+  const uint32_t to = tmem + lanes + S::kColO + x * D;
   float ref = 0.0f, total = 0.0f;  // the reference in score units
   bool ok = true;
-  for (int j = 0; j < w.tiles[x]; ++j) {
-    ok = wait(&sm.s_full[x], j & 1, a.status);
-    ok = __all_sync(0xFFFFFFFFu, ok);
+  for (int j = 0; j < w.tiles(x); ++j) {
+    const int q = w.step(x, j), b = q % S::kBufs;
+    const uint32_t ts = tmem + lanes + b * kKeys;
+    ok = __all_sync(0xFFFFFFFFu, wait(&sm.s_full[x][j & 1], (j >> 1) & 1, a.status));
     if (!ok) break;
     tmem_fence_after();
     const int lim = limit - j * kKeys;
@@ -388,6 +434,11 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
       if (j == 0) {
         ref = top == -INFINITY ? 0.0f : top;
       } else {
+        // O has to hold every tile before this one. S of this step went after P V of step q - 3 at the latest, so
+        // key tile j - 3 is in O and the barrier's phase is that of j - 1.
+        ok = __all_sync(0xFFFFFFFFu, wait(&sm.pv_done[x][(j - 1) & 1], ((j - 1) >> 1) & 1, a.status));
+        if (!ok) break;
+        tmem_fence_after();
         const bool move = (top - ref) * a.scale2 > kLazy;
         const float f = move ? exp2_approx((ref - top) * a.scale2) : 1.0f;
         if (move) ref = top;
@@ -410,12 +461,11 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
     tmem_wait_st();
     tmem_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.p_full[x]);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.p_full[b]);
   }
   if (!ok) return;
-  if (w.tiles[x] > 0) {
-    ok = wait(&sm.o_full[x], 0, a.status);
-    if (!__all_sync(0xFFFFFFFFu, ok)) return;
+  if (w.tiles(x) > 0) {
+    if (!__all_sync(0xFFFFFFFFu, wait(&sm.o_full[x], 0, a.status))) return;
     tmem_fence_after();
   }
   const bool real = r < w.rows;
@@ -425,7 +475,7 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     uint32_t o[32];
-    if (w.tiles[x] > 0) {
+    if (w.tiles(x) > 0) {
       tmem_ld32(to + 32 * i, o);
       tmem_wait_ld(o);
     }
@@ -455,51 +505,52 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   using S = Smem<D>;
   static_assert(sizeof(S) + 1024 <= S::kBytes && S::kBytes <= 227 * 1024, "shared memory budget");
   S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    const TileAt at = find_tile(a.cu_rows, a.num_seqs, a.num_rows, a.group, 2 * kRows, blockIdx.x, a.status);
-    if (lane == 0) {
-      sm.seq = at.seq;
-      sm.local = at.local;
-      sm.tiles = at.tiles;
-      mbar_init(&sm.q_full, kSoftmaxThreads);
-      for (int i = 0; i < S::kStages; ++i) {
-        mbar_init(&sm.full[i], 1);
-        mbar_init(&sm.empty[i], 1);
-      }
-      mbar_init(&sm.tail, 1);
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(&sm.s_full[x], 1);
-        mbar_init(&sm.p_full[x], 4);
-        mbar_init(&sm.o_full[x], 1);
-      }
-      mbar_init(&sm.mma_done, 1);
-      fence_mbar_init();
-    }
-  }
-  __syncthreads();
-  if (sm.seq < 0) return;  // past the last tile: the whole block
-  if (warp == kWarpMma) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  const int warp = threadIdx.x >> 5;
+  // every warp finds the block's tile for itself: nothing to wait for
+  const TileAt at = find_tile(a.cu_rows, a.num_seqs, a.num_rows, a.group, 2 * kRows, blockIdx.x,
+                              warp == 0 ? a.status : nullptr);
+  if (at.seq < 0) return;  // past the last tile: the whole block
   Work w;
-  const Span rows = seq_span(a.cu_rows, sm.seq, a.num_rows, nullptr);
-  const Span keys = seq_span(a.cu_keys, sm.seq, a.num_keys, a.status);
+  const Span rows = seq_span(a.cu_rows, at.seq, a.num_rows, nullptr);
+  const Span keys = seq_span(a.cu_keys, at.seq, a.num_keys, a.status);
   w.row0 = rows.first;
   w.n = rows.n;
   w.rows = rows.n * a.group;
   w.key0 = keys.first;
   w.keys = keys.n;
   w.kv = blockIdx.y;
-  w.r0 = (sm.tiles - 1 - sm.local) * (2 * kRows);  // the last rows see the most keys: they start first
-  for (int x = 0; x < 2; ++x) {
-    const int first = w.r0 + x * kRows;
-    w.tiles[x] = first < w.rows ? (key_limit(a, w, min(first + kRows, w.rows) - 1) + kKeys - 1) / kKeys : 0;
+  w.r0 = (at.tiles - 1 - at.local) * (2 * kRows);  // the last rows see the most keys: they start first
+  const auto key_tiles = [&](int first) {
+    return first < w.rows ? (key_limit(a, w, min(first + kRows, w.rows) - 1) + kKeys - 1) / kKeys : 0;
+  };
+  w.tiles0 = key_tiles(w.r0);
+  w.tiles1 = key_tiles(w.r0 + kRows);
+  if (warp < kWarpLoad) {
+    load_queries<D>(a, sm, w);
+  } else if (warp == kWarpLoad) {
+    if (elect_one()) {
+      for (int i = 0; i < S::kStages; ++i) {
+        mbar_init(&sm.full[i], 1);
+        mbar_init(&sm.empty[i], 1);
+      }
+      mbar_init(&sm.tail, 1);
+      for (int i = 0; i < S::kBufs; ++i) mbar_init(&sm.p_full[i], 4);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&sm.s_full[x][0], 1);
+        mbar_init(&sm.s_full[x][1], 1);
+        mbar_init(&sm.pv_done[x][0], 1);
+        mbar_init(&sm.pv_done[x][1], 1);
+        mbar_init(&sm.o_full[x], 1);
+      }
+      mbar_init(&sm.mma_done, 1);
+      fence_mbar_init();
+    }
+  } else if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  const int n = max(w.tiles[0], w.tiles[1]);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -509,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
     softmax_warps<T, D>(a, sm, w, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (n > 0 && warp == kWarpLoad) load_warp<D>(&kmap, &vmap, a, sm, w, n);
-    if (n > 0 && warp == kWarpMma && elect_one()) mma_lane<T, D>(a, sm, w, n, tmem);
+    if (w.all() > 0 && warp == kWarpLoad) load_warp<D>(&kmap, &vmap, a, sm, w);
+    if (w.all() > 0 && warp == kWarpMma && elect_one()) mma_lane<T, D>(a, sm, w, tmem);
   }
   __syncwarp();
   tmem_fence_before();
