@@ -82,7 +82,6 @@ struct Smem {
   uint64_t tail;             // the last V tile is zeroed past the sequence's end
   uint64_t s_full[2][2];     // S of (row tile, key tile j) complete, by j mod 2: its waiters see every phase
   uint64_t p_full[kBufs];    // P of a step written (4 warps)
-  uint64_t pv_done[2][2];    // P V of (row tile, key tile j) is in O, by j mod 2
   uint64_t o_full[2];        // the row tile's last P V is in O
   uint64_t mma_done;
   uint32_t tmem_base;
@@ -321,7 +320,6 @@ __device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32
     for (int c = 0; c < kKeys / 16; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
       mma_ts(d, pa + 8 * c, vd + c * (2048 >> 4), kDescO, (vj | c) != 0);
     if (issued < steps) ok = scores();
-    mma_commit(&sm.pv_done[vx][vj & 1]);
     if (vj + 1 == w.tiles(vx)) mma_commit(&sm.o_full[vx]);
     vfresh = vx == 1 || vj >= m;
     if (vfresh) {
@@ -434,9 +432,10 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
       if (j == 0) {
         ref = top == -INFINITY ? 0.0f : top;
       } else {
-        // O has to hold every tile before this one. S of this step went after P V of step q - 3 at the latest, so
-        // key tile j - 3 is in O and the barrier's phase is that of j - 1.
-        ok = __all_sync(0xFFFFFFFFu, wait(&sm.pv_done[x][(j - 1) & 1], ((j - 1) >> 1) & 1, a.status));
+        // O has to hold every tile before this one: then V of key tile j - 1 has been released. (Its slot is not
+        // released again before this step is done, and was not in an older phase when S of this step was issued.)
+        const int i = 2 * j - 1;
+        ok = __all_sync(0xFFFFFFFFu, wait(&sm.empty[i % S::kStages], (i / S::kStages) & 1, a.status));
         if (!ok) break;
         tmem_fence_after();
         const bool move = (top - ref) * a.scale2 > kLazy;
@@ -538,8 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       for (int x = 0; x < 2; ++x) {
         mbar_init(&sm.s_full[x][0], 1);
         mbar_init(&sm.s_full[x][1], 1);
-        mbar_init(&sm.pv_done[x][0], 1);
-        mbar_init(&sm.pv_done[x][1], 1);
         mbar_init(&sm.o_full[x], 1);
       }
       mbar_init(&sm.mma_done, 1);
