@@ -221,21 +221,30 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *st
 
 // ------------------------------------------------------------------ TMA (warp 8)
 
+// Entry i of the list K 0, V 0, K 1, V 1, ... into its ring slot (one lane).
+template <int D>
+__device__ __forceinline__ void load_tile(const CUtensorMap *kmap, const CUtensorMap *vmap, Smem<D> &sm, const Work &w,
+                                          int i) {
+  using S = Smem<D>;
+  const int s = i % S::kStages;
+  mbar_arrive_expect_tx(&sm.full[s], S::kTileBytes);
+  const CUtensorMap *map = i & 1 ? vmap : kmap;
+#pragma unroll
+  for (int p = 0; p < D / 64; ++p)
+    tma_load(sm.kv[s] + p * (kKeys * 128), map, w.kv * D + 64 * p, w.key0 + (i >> 1) * kKeys, &sm.full[s]);
+}
+
+// The first entries, as many as the ring has slots, went out with the barriers' initialisation.
 template <int D>
 __device__ void load_warp(const CUtensorMap *kmap, const CUtensorMap *vmap, const PromptArgs &a, Smem<D> &sm,
                           const Work &w) {
   using S = Smem<D>;
   const int lane = threadIdx.x & 31, n = w.all();
-  int issued = 0;
+  int issued = min(2 * n, S::kStages);
   if (elect_one()) {
-    for (int i = 0; i < 2 * n; ++i) {  // K 0, V 0, K 1, V 1, ...
-      const int s = i % S::kStages;
-      if (!wait(&sm.empty[s], ((i / S::kStages) & 1) ^ 1, a.status)) break;
-      mbar_arrive_expect_tx(&sm.full[s], S::kTileBytes);
-      const CUtensorMap *map = i & 1 ? vmap : kmap;
-#pragma unroll
-      for (int p = 0; p < D / 64; ++p)
-        tma_load(sm.kv[s] + p * (kKeys * 128), map, w.kv * D + 64 * p, w.key0 + (i >> 1) * kKeys, &sm.full[s]);
+    for (int i = issued; i < 2 * n; ++i) {
+      if (!wait(&sm.empty[i % S::kStages], ((i / S::kStages) & 1) ^ 1, a.status)) break;
+      load_tile<D>(kmap, vmap, sm, w, i);
       ++issued;
     }
   }
@@ -380,20 +389,25 @@ __device__ void load_queries(const PromptArgs &a, Smem<D> &sm, const Work &w) {
   constexpr int kChunks = D / 8, kStep = 128 / kChunks;
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127, first = w.r0 + x * kRows, c = row % kChunks;
   uint8_t *dst = sm.q[x] + (c >> 3) * (kRows * 128);
-#pragma unroll 8
-  for (int i = row / kChunks; i < kRows; i += kStep) {
-    const int r = first + i;
-    uint4 v = make_uint4(0, 0, 0, 0);
+  uint4 v[kChunks];  // all of a thread's pieces in flight at once
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    const int r = first + row / kChunks + k * kStep;
+    v[k] = make_uint4(0, 0, 0, 0);
     if (r < w.rows) {
       const int t = r / a.group, h = r - t * a.group;
-      v = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(w.row0 + t) * a.q_stride +
-                                                (int64_t(w.kv) * a.group + h) * D) + c);
-      v.x ^= a.flip;
-      v.y ^= a.flip;
-      v.z ^= a.flip;
-      v.w ^= a.flip;
+      v[k] = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(w.row0 + t) * a.q_stride +
+                                                   (int64_t(w.kv) * a.group + h) * D) + c);
     }
-    *reinterpret_cast<uint4 *>(dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
+  }
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    const int i = row / kChunks + k * kStep;
+    v[k].x ^= a.flip;
+    v[k].y ^= a.flip;
+    v[k].z ^= a.flip;
+    v[k].w ^= a.flip;
+    *reinterpret_cast<uint4 *>(dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v[k];
   }
   fence_proxy_async();
 }
@@ -541,6 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       }
       mbar_init(&sm.mma_done, 1);
       fence_mbar_init();
+      fence_proxy_async();  // the copies' completions go to these barriers
+      for (int i = 0; i < S::kStages && i < 2 * w.all(); ++i) load_tile<D>(&kmap, &vmap, sm, w, i);
     }
   } else if (warp == kWarpMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
