@@ -390,14 +390,18 @@ __device__ void load_queries(const PromptArgs &a, Smem<D> &sm, const Work &w) {
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127, first = w.r0 + x * kRows, c = row % kChunks;
   uint8_t *dst = sm.q[x] + (c >> 3) * (kRows * 128);
   uint4 v[kChunks];  // all of a thread's pieces in flight at once
+  const int r = first + row / kChunks, dt = kStep / a.group, dh = kStep - dt * a.group;
+  int t = r / a.group, h = r - t * a.group;
+  const uint16_t *head = a.q + int64_t(w.row0) * a.q_stride + int64_t(w.kv) * a.group * D + 8 * c;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
-    const int r = first + row / kChunks + k * kStep;
     v[k] = make_uint4(0, 0, 0, 0);
-    if (r < w.rows) {
-      const int t = r / a.group, h = r - t * a.group;
-      v[k] = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(w.row0 + t) * a.q_stride +
-                                                   (int64_t(w.kv) * a.group + h) * D) + c);
+    if (r + k * kStep < w.rows) v[k] = __ldg(reinterpret_cast<const uint4 *>(head + t * a.q_stride + h * D));
+    t += dt;
+    h += dh;
+    if (h >= a.group) {
+      h -= a.group;
+      ++t;
     }
   }
 #pragma unroll
@@ -481,10 +485,13 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
     if (!__all_sync(0xFFFFFFFFu, wait(&sm.o_full[x], 0, a.status))) return;
     tmem_fence_after();
   }
-  const bool real = r < w.rows;
-  const int t = r / a.group, h = w.kv * a.group + r - t * a.group;
+  // O / sum into this warp's 32 rows of the tile's Q, which nothing reads any more (every S is done), then out by
+  // whole rows. 16-byte pieces of a row are exchanged by row, against bank conflicts.
   const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-  uint16_t *out = a.out + int64_t(w.row0 + t) * a.out_stride + int64_t(h) * D;
+  const bool any = limit > 0;  // a row without keys has no accumulator of its own
+  constexpr int kChunks = D / 8;
+  uint8_t *stage = sm.q[x] + warp * 32 * (2 * D);
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     uint32_t o[32];
@@ -492,20 +499,41 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
       tmem_ld32(to + 32 * i, o);
       tmem_wait_ld(o);
     }
-    if (!real) continue;
-    const bool any = limit > 0;  // a row without keys has no accumulator of its own
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         v[e] = any ? T::pack(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv) : 0u;
-      *reinterpret_cast<uint4 *>(out + 32 * i + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4 *>(stage + lane * (2 * D) + (((4 * i + c) ^ (lane & 7)) << 4)) =
+          make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
-  if (real && a.lse)
-    a.lse[int64_t(w.row0 + t) * a.num_heads + h] =
+  __syncwarp();
+  const int first = w.r0 + x * kRows + warp * 32;  // the warp's first pair
+  {
+    constexpr int kStep = 32 / kChunks;
+    const int c = lane % kChunks, l = lane / kChunks, dt = kStep / a.group, dh = kStep - dt * a.group;
+    int t = (first + l) / a.group, h = first + l - t * a.group;
+    uint16_t *out = a.out + int64_t(w.row0) * a.out_stride + int64_t(w.kv) * a.group * D + 8 * c;
+#pragma unroll 4
+    for (int i = l; i < 32; i += kStep) {
+      if (first + i < w.rows)
+        *reinterpret_cast<uint4 *>(out + t * a.out_stride + h * D) =
+            *reinterpret_cast<const uint4 *>(stage + i * (2 * D) + ((c ^ (i & 7)) << 4));
+      t += dt;
+      h += dh;
+      if (h >= a.group) {
+        h -= a.group;
+        ++t;
+      }
+    }
+  }
+  if (r < w.rows && a.lse) {
+    const int t = r / a.group;
+    a.lse[int64_t(w.row0 + t) * a.num_heads + w.kv * a.group + r - t * a.group] =
         total > 0.0f ? (log2f(total) + ref * a.scale2) * 0.6931471805599453f : -INFINITY;
+  }
 }
 
 // ------------------------------------------------------------------ kernel
@@ -520,12 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   // every warp finds the block's tile for itself: nothing to wait for
-  const TileAt at = find_tile(a.cu_rows, a.num_seqs, a.num_rows, a.group, 2 * kRows, blockIdx.x,
+  const TileAt at = find_tile(a.cu_rows, a.num_rows, a.cu_keys, a.num_keys, a.num_seqs, a.group, 2 * kRows, blockIdx.x,
                               warp == 0 ? a.status : nullptr);
   if (at.seq < 0) return;  // past the last tile: the whole block
   Work w;
-  const Span rows = seq_span(a.cu_rows, at.seq, a.num_rows, nullptr);
-  const Span keys = seq_span(a.cu_keys, at.seq, a.num_keys, a.status);
+  const Span rows = at.rows, keys = at.keys;
   w.row0 = rows.first;
   w.n = rows.n;
   w.rows = rows.n * a.group;

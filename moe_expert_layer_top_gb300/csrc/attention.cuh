@@ -74,27 +74,36 @@ __device__ __forceinline__ int warp_inclusive_sum(int v) {
 // ceil(n_b * group / rows) tiles of `rows` (row, head) pairs. Called by a whole warp; seq = -1: past the last tile.
 struct TileAt {
   int seq, local, tiles;  // sequence, tile within it, its tiles
+  Span rows, keys;        // of the sequence
 };
 
-__device__ __forceinline__ TileAt find_tile(const int32_t *cu, int num_seqs, int num_rows, int group, int rows,
-                                            int64_t tile, int32_t *status) {
+__device__ __forceinline__ TileAt find_tile(const int32_t *cu_rows, int num_rows, const int32_t *cu_keys, int num_keys,
+                                            int num_seqs, int group, int rows, int64_t tile, int32_t *status) {
   const int lane = threadIdx.x & 31;
   int64_t base = 0;
   for (int b0 = 0; b0 < num_seqs; b0 += 32) {
     const int b = b0 + lane;
-    const int n = b < num_seqs ? seq_span(cu, b, num_rows, status).n : 0;
-    const int tiles = int((int64_t(n) * group + rows - 1) / rows);
+    Span r = {0, 0}, k = {0, 0};
+    if (b < num_seqs) {
+      r = seq_span(cu_rows, b, num_rows, status);
+      k = seq_span(cu_keys, b, num_keys, status);
+    }
+    const int tiles = int((int64_t(r.n) * group + rows - 1) / rows);
     const int64_t end = base + warp_inclusive_sum(tiles);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, tile < end);
     if (hit) {
       const int w = __ffs(hit) - 1;
-      const int mine = __shfl_sync(0xFFFFFFFFu, tiles, w);
-      const int64_t stop = __shfl_sync(0xFFFFFFFFu, end, w);
-      return {b0 + w, int(tile - (stop - mine)), mine};
+      TileAt at;
+      at.seq = b0 + w;
+      at.tiles = __shfl_sync(0xFFFFFFFFu, tiles, w);
+      at.local = int(tile - (__shfl_sync(0xFFFFFFFFu, end, w) - at.tiles));
+      at.rows = {__shfl_sync(0xFFFFFFFFu, r.first, w), __shfl_sync(0xFFFFFFFFu, r.n, w)};
+      at.keys = {__shfl_sync(0xFFFFFFFFu, k.first, w), __shfl_sync(0xFFFFFFFFu, k.n, w)};
+      return at;
     }
     base = __shfl_sync(0xFFFFFFFFu, end, 31);
   }
-  return {-1, 0, 0};
+  return {-1, 0, 0, {0, 0}, {0, 0}};
 }
 
 }  // namespace moe
