@@ -14,12 +14,13 @@
 //
 // Layout. A row of the tile is a (token, head) pair: the G heads of a kv head's
 // group are packed, r = token * G + head, so one key tile serves all of them and
-// short prompts still fill the 128 rows of an MMA. A block takes two row tiles A
-// and B of 128. While the tensor cores work for one, the softmax of the other
+// short prompts still fill the 128 rows of an MMA (floor(128 / G) G of them; a
+// group of more than 128 heads is cut into equal parts). A block takes two such row
+// tiles A and B. While the tensor cores work for one, the softmax of the other
 // runs on the CUDA cores:
 //   warps 0-3   softmax of tile A, one row (TMEM lane) a thread
 //   warps 4-7   softmax of tile B
-//   warp 8      TMA: K and V tiles of 128 keys into a ring of shared memory;
+//   warp 8      TMA: Q, then K and V tiles of 128 keys into a ring of shared memory;
 //               at the end it zeroes the rows of the last V tile that lie past
 //               the sequence (they belong to the next one, and 0 * NaN is NaN)
 //   warp 9      MMA issuer: S = Q K^T (both operands from shared memory), then
@@ -56,15 +57,17 @@ constexpr int64_t kWaitNs = 1000000000;  // bound of every wait
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
 
 struct PromptArgs {
-  const uint16_t *q;
-  int64_t q_stride;
   uint16_t *out;
   int64_t out_stride;
   float *lse;
   const int32_t *cu_rows, *cu_keys;
-  int num_seqs, num_rows, num_keys, num_heads, group, causal;
+  int num_seqs, num_rows, num_keys, num_heads, causal;
+  int group;       // heads packed into a row tile
+  int groups;      // such groups of a kv head
+  int all_groups;  // and of all heads
+  int tokens;      // tokens of a row tile
   float scale2;    // |scale| log2 e, at least 2^-100: scores times this are exponents of two
-  uint32_t flip;   // 0x80008000 with a negative scale: the queries are negated
+  bool negative;   // the scale is: scores change sign
   int32_t *status;
 };
 
@@ -77,6 +80,7 @@ struct Smem {
   static_assert(kColO + 2 * D <= kTmemCols && kBufs <= 3, "TMEM budget");
   uint8_t q[2][kTileBytes];
   uint8_t kv[kStages][kTileBytes];
+  uint64_t q_full;           // Q landed
   uint64_t full[kStages];    // a K or V tile landed
   uint64_t empty[kStages];   // the MMAs that read it are done
   uint64_t tail;             // the last V tile is zeroed past the sequence's end
@@ -90,11 +94,11 @@ struct Smem {
 
 // ------------------------------------------------------------------ PTX wrappers
 
-__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -185,11 +189,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // ------------------------------------------------------------------ the block's work
 
 struct Work {
-  int row0, rows;    // the sequence's first row, its rows times group
+  int row0, n;       // the sequence's first row, its rows
   int key0, keys;    // its first key, its keys
-  int n;             // its query rows
-  int r0;            // the block's first (row, head) pair
-  int kv;            // kv head
+  int t0;            // the block's first row within the sequence
+  int kv, head0;     // kv head, the first of the block's heads
   int tiles0, tiles1;  // key tiles of row tiles A and B
 
   __device__ __forceinline__ int tiles(int x) const { return x ? tiles1 : tiles0; }
@@ -199,10 +202,9 @@ struct Work {
   __device__ __forceinline__ int step(int x, int j) const { return j < both() ? 2 * j + x : both() + j; }
 };
 
-// Keys that pair r sees.
-__device__ __forceinline__ int key_limit(const PromptArgs &a, const Work &w, int r) {
-  if (r >= w.rows) return 0;
-  return a.causal ? min(w.keys, max(0, w.keys - w.n + r / a.group + 1)) : w.keys;
+// Keys that row t of the sequence sees.
+__device__ __forceinline__ int key_limit(const PromptArgs &a, const Work &w, int t) {
+  return a.causal ? min(w.keys, max(0, w.keys - w.n + t + 1)) : w.keys;
 }
 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *status) {
@@ -231,7 +233,7 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *kmap, const CUtenso
   const CUtensorMap *map = i & 1 ? vmap : kmap;
 #pragma unroll
   for (int p = 0; p < D / 64; ++p)
-    tma_load(sm.kv[s] + p * (kKeys * 128), map, w.kv * D + 64 * p, w.key0 + (i >> 1) * kKeys, &sm.full[s]);
+    tma_load(sm.kv[s] + p * (kKeys * 128), map, 64 * p, w.kv, w.key0 + (i >> 1) * kKeys, &sm.full[s]);
 }
 
 // The first entries, as many as the ring has slots, went out with the barriers' initialisation.
@@ -262,6 +264,7 @@ __device__ void load_warp(const CUtensorMap *kmap, const CUtensorMap *vmap, cons
     }
   }
   // no copy may be in flight when the block exits
+  mbar_wait(&sm.q_full, 0, kWaitNs);
   for (int j = 1; j <= S::kStages && j <= issued; ++j) {
     const int i = issued - j;
     mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, kWaitNs);
@@ -315,7 +318,7 @@ __device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32
     ++issued;
     return true;
   };
-  bool ok = true;
+  bool ok = wait(&sm.q_full, 0, a.status);
   while (ok && issued < S::kBufs && issued < steps) ok = scores();
   for (int q = 0; ok && q < steps; ++q) {
     if (vfresh)
@@ -353,11 +356,15 @@ __device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32
 // ------------------------------------------------------------------ softmax (warps 0-7)
 
 // A row's scores of one key tile; keys from lim on are hidden.
-__device__ __forceinline__ void load_scores(uint32_t ts, int lim, uint32_t (&s)[kKeys]) {
+__device__ __forceinline__ void load_scores(uint32_t ts, int lim, bool negative, uint32_t (&s)[kKeys]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
 #pragma unroll
   for (int i = 0; i < 4; ++i) tmem_wait_ld(s + 32 * i);
+  if (negative) {
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) s[i] ^= 0x80000000u;
+  }
   if (__any_sync(0xFFFFFFFFu, lim < kKeys)) {
 #pragma unroll
     for (int i = 0; i < kKeys; ++i)
@@ -383,45 +390,14 @@ __device__ __forceinline__ void exponentials(const uint32_t (&s)[kKeys], uint32_
   sum = (add[0] + add[1]) + (add[2] + add[3]);
 }
 
-// Q of the block into the swizzled K-major layout: 16 bytes a thread and round, a row side by side.
-template <int D>
-__device__ void load_queries(const PromptArgs &a, Smem<D> &sm, const Work &w) {
-  constexpr int kChunks = D / 8, kStep = 128 / kChunks;
-  const int x = threadIdx.x >> 7, row = threadIdx.x & 127, first = w.r0 + x * kRows, c = row % kChunks;
-  uint8_t *dst = sm.q[x] + (c >> 3) * (kRows * 128);
-  uint4 v[kChunks];  // all of a thread's pieces in flight at once
-  const int r = first + row / kChunks, dt = kStep / a.group, dh = kStep - dt * a.group;
-  int t = r / a.group, h = r - t * a.group;
-  const uint16_t *head = a.q + int64_t(w.row0) * a.q_stride + int64_t(w.kv) * a.group * D + 8 * c;
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k) {
-    v[k] = make_uint4(0, 0, 0, 0);
-    if (r + k * kStep < w.rows) v[k] = __ldg(reinterpret_cast<const uint4 *>(head + t * a.q_stride + h * D));
-    t += dt;
-    h += dh;
-    if (h >= a.group) {
-      h -= a.group;
-      ++t;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k) {
-    const int i = row / kChunks + k * kStep;
-    v[k].x ^= a.flip;
-    v[k].y ^= a.flip;
-    v[k].z ^= a.flip;
-    v[k].w ^= a.flip;
-    *reinterpret_cast<uint4 *>(dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v[k];
-  }
-  fence_proxy_async();
-}
-
 template <class T, int D>
 __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
   using S = Smem<D>;
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
-  const int r = w.r0 + x * kRows + row;
-  const int limit = key_limit(a, w, r);
+  // the thread's row of the sequence and its head; rows past the tile's tokens or the sequence see nothing
+  const int t = w.t0 + x * a.tokens + row / a.group, h = w.head0 + row % a.group;
+  const bool real = row < a.tokens * a.group && t < w.n;
+  const int limit = real ? key_limit(a, w, t) : 0;
   const uint32_t lanes = uint32_t(warp * 32) << 16;
   const uint32_t to = tmem + lanes + S::kColO + x * D;
   float ref = 0.0f, total = 0.0f;  // the reference in score units
@@ -435,12 +411,12 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
     const int lim = limit - j * kKeys;
     uint32_t s[kKeys], p[kKeys / 2];
     float top, sum;
-    load_scores(ts, lim, s);
+    load_scores(ts, lim, a.negative, s);
     bool redo = true;
     if (j > 0) {  // with the reference as it is; the maximum only says whether that was good enough
       exponentials<T>(s, p, a.scale2, -ref * a.scale2, top, sum);
       redo = __any_sync(0xFFFFFFFFu, (top - ref) * a.scale2 > kLazy);
-      if (redo) load_scores(ts, lim, s);  // P is not stored yet: S is still there
+      if (redo) load_scores(ts, lim, a.negative, s);  // P is not stored yet: S is still there
     }
     if (redo) {
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -510,36 +486,40 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
     }
   }
   __syncwarp();
-  const int first = w.r0 + x * kRows + warp * 32;  // the warp's first pair
   {
-    constexpr int kStep = 32 / kChunks;
+    constexpr int kStep = 32 / kChunks;  // rows that a warp stores at once
     const int c = lane % kChunks, l = lane / kChunks, dt = kStep / a.group, dh = kStep - dt * a.group;
-    int t = (first + l) / a.group, h = first + l - t * a.group;
-    uint16_t *out = a.out + int64_t(w.row0) * a.out_stride + int64_t(w.kv) * a.group * D + 8 * c;
-#pragma unroll 4
-    for (int i = l; i < 32; i += kStep) {
-      if (first + i < w.rows)
-        *reinterpret_cast<uint4 *>(out + t * a.out_stride + h * D) =
-            *reinterpret_cast<const uint4 *>(stage + i * (2 * D) + ((c ^ (i & 7)) << 4));
-      t += dt;
-      h += dh;
-      if (h >= a.group) {
-        h -= a.group;
-        ++t;
+    int rr = warp * 32 + l, tt = w.t0 + x * a.tokens + rr / a.group, hh = rr % a.group;
+    uint16_t *out = a.out + int64_t(w.row0 + tt) * a.out_stride + int64_t(w.head0 + hh) * D + 8 * c;
+    const int64_t step = dt * a.out_stride + dh * D, wrap = a.out_stride - a.group * D;
+    const uint8_t *from = stage + l * (2 * D);
+    const int rows = a.tokens * a.group;
+#pragma unroll
+    for (int i = 0; i < 32; i += kStep) {
+      if (rr < rows && tt < w.n)
+        *reinterpret_cast<uint4 *>(out) =
+            *reinterpret_cast<const uint4 *>(from + i * (2 * D) + ((c ^ ((l + i) & 7)) << 4));
+      rr += kStep;
+      tt += dt;
+      hh += dh;
+      out += step;
+      if (hh >= a.group) {
+        hh -= a.group;
+        ++tt;
+        out += wrap;
       }
     }
   }
-  if (r < w.rows && a.lse) {
-    const int t = r / a.group;
-    a.lse[int64_t(w.row0 + t) * a.num_heads + w.kv * a.group + r - t * a.group] =
+  if (real && a.lse)
+    a.lse[int64_t(w.row0 + t) * a.num_heads + h] =
         total > 0.0f ? (log2f(total) + ref * a.scale2) * 0.6931471805599453f : -INFINITY;
-  }
 }
 
 // ------------------------------------------------------------------ kernel
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ CUtensorMap kmap,
+__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ CUtensorMap qmap,
+                                                                    const __grid_constant__ CUtensorMap kmap,
                                                                     const __grid_constant__ CUtensorMap vmap,
                                                                     const PromptArgs a) {
   extern __shared__ unsigned char prompt_smem_raw[];
@@ -548,27 +528,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   // every warp finds the block's tile for itself: nothing to wait for
-  const TileAt at = find_tile(a.cu_rows, a.num_rows, a.cu_keys, a.num_keys, a.num_seqs, a.group, 2 * kRows, blockIdx.x,
+  // (Heads run fastest: the heads of a sequence's long tiles start before its short ones.)
+  const uint32_t tile = blockIdx.x / a.all_groups, head = blockIdx.x - tile * a.all_groups;
+  const TileAt at = find_tile(a.cu_rows, a.num_rows, a.cu_keys, a.num_keys, a.num_seqs, 2 * a.tokens, tile,
                               warp == 0 ? a.status : nullptr);
   if (at.seq < 0) return;  // past the last tile: the whole block
   Work w;
-  const Span rows = at.rows, keys = at.keys;
-  w.row0 = rows.first;
-  w.n = rows.n;
-  w.rows = rows.n * a.group;
-  w.key0 = keys.first;
-  w.keys = keys.n;
-  w.kv = blockIdx.y;
-  w.r0 = (at.tiles - 1 - at.local) * (2 * kRows);  // the last rows see the most keys: they start first
+  w.row0 = at.rows.first;
+  w.n = at.rows.n;
+  w.key0 = at.keys.first;
+  w.keys = at.keys.n;
+  w.kv = head / a.groups;
+  w.head0 = head * a.group;
+  w.t0 = (at.tiles - 1 - at.local) * (2 * a.tokens);  // the last rows see the most keys: they start first
   const auto key_tiles = [&](int first) {
-    return first < w.rows ? (key_limit(a, w, min(first + kRows, w.rows) - 1) + kKeys - 1) / kKeys : 0;
+    return first < w.n ? (key_limit(a, w, min(first + a.tokens, w.n) - 1) + kKeys - 1) / kKeys : 0;
   };
-  w.tiles0 = key_tiles(w.r0);
-  w.tiles1 = key_tiles(w.r0 + kRows);
-  if (warp < kWarpLoad) {
-    load_queries<D>(a, sm, w);
-  } else if (warp == kWarpLoad) {
+  w.tiles0 = key_tiles(w.t0);
+  w.tiles1 = key_tiles(w.t0 + a.tokens);
+  if (warp == kWarpLoad) {
     if (elect_one()) {
+      mbar_init(&sm.q_full, 1);
       for (int i = 0; i < S::kStages; ++i) {
         mbar_init(&sm.full[i], 1);
         mbar_init(&sm.empty[i], 1);
@@ -583,6 +563,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       mbar_init(&sm.mma_done, 1);
       fence_mbar_init();
       fence_proxy_async();  // the copies' completions go to these barriers
+      if (w.all() > 0) {
+        // rows past the sequence are another one's, or zeros past the last: their scores are hidden
+        const int tiles = w.tiles1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(&sm.q_full, uint32_t(tiles * a.tokens * a.group * D * 2));
+        for (int x = 0; x < tiles; ++x)
+          for (int p = 0; p < D / 64; ++p)
+            tma_load(sm.q[x] + p * (kRows * 128), &qmap, 64 * p, w.head0, w.row0 + w.t0 + x * a.tokens, &sm.q_full);
+      }
       for (int i = 0; i < S::kStages && i < 2 * w.all(); ++i) load_tile<D>(&kmap, &vmap, sm, w, i);
     }
   } else if (warp == kWarpMma) {
@@ -613,22 +601,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
 
 // ------------------------------------------------------------------ host
 
-// Boxes of 128 keys x 64 values, 128-byte swizzle, over [keys][kv heads * D] with the caller's row stride.
-bool encode(CUtensorMap *map, const void *base, uint64_t keys, uint64_t width, int64_t stride) {
+// Boxes of 64 values x `heads` heads x `rows` rows, 128-byte swizzle, over [total][all_heads][dim] with the caller's row stride.
+bool encode(CUtensorMap *map, const void *base, int dim, int all_heads, int64_t total, int64_t stride, int heads, int rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[2] = {width, keys}, strides[1] = {uint64_t(stride) * 2};
-  const cuuint32_t box[2] = {64, kKeys}, estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+  const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(all_heads), cuuint64_t(total)};
+  const cuuint64_t strides[2] = {cuuint64_t(dim) * 2, cuuint64_t(stride) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(heads), cuuint32_t(rows)}, estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
 template <class T, int D>
-cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const PromptArgs &a, int kv_heads,
-                   cudaStream_t st) {
-  const int64_t tiles = int64_t(a.num_rows) * a.group / (2 * kRows) + a.num_seqs;
-  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+cudaError_t launch(const Maps &maps, const PromptArgs &a, cudaStream_t st) {
+  const int64_t blocks = (int64_t(a.num_rows) / (2 * a.tokens) + a.num_seqs) * a.all_groups;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   // The register split above assumes the launch's share: a build that gave the kernel less must not run.
   static const bool split = [] {
     cudaFuncAttributes at;
@@ -638,8 +630,8 @@ cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const Promp
   const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              int(Smem<D>::kBytes));
   if (e != cudaSuccess) return e;
-  attend_prompt_kernel<T, D>
-      <<<dim3(unsigned(tiles), unsigned(kv_heads)), kThreads, Smem<D>::kBytes, st>>>(kmap, vmap, a);
+  attend_prompt_kernel<T, D><<<unsigned(blocks), kThreads, Smem<D>::kBytes, st>>>(
+      maps.q, maps.k, maps.v, a);
   return cudaGetLastError();
 }
 
@@ -647,8 +639,6 @@ cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const Promp
 
 cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *status, int num_sms, cudaStream_t st) {
   PromptArgs a = {};
-  a.q = static_cast<const uint16_t *>(io.q);
-  a.q_stride = io.q_stride;
   a.out = static_cast<uint16_t *>(io.out);
   a.out_stride = io.out_stride;
   a.lse = io.lse;
@@ -658,23 +648,26 @@ cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *stat
   a.num_rows = io.num_rows;
   a.num_keys = io.num_keys;
   a.num_heads = io.num_heads;
-  a.group = io.num_heads / io.num_kv_heads;
+  const int group = io.num_heads / io.num_kv_heads;
+  a.group = group < kRows ? group : kRows;
+  while (group % a.group) --a.group;
+  a.groups = group / a.group;
+  a.all_groups = io.num_heads / a.group;
+  a.tokens = kRows / a.group;
   a.causal = io.causal;
   a.scale2 = fmaxf(fabsf(io.scale) * 1.4426950408889634f, 0x1p-100f);
-  a.flip = io.scale < 0.0f ? 0x80008000u : 0u;
+  a.negative = io.scale < 0.0f;
   a.status = status;
-  CUtensorMap kmap, vmap;
-  memset(&kmap, 0, sizeof kmap);
-  memset(&vmap, 0, sizeof vmap);
-  if (io.num_keys) {
-    const uint64_t width = uint64_t(io.num_kv_heads) * io.head_dim;
-    if (!encode(&kmap, io.k, io.num_keys, width, io.k_stride) || !encode(&vmap, io.v, io.num_keys, width, io.v_stride))
-      return cudaErrorInvalidValue;
-  }
+  const int D = io.head_dim;
+  Maps maps;
+  memset(&maps, 0, sizeof maps);
+  if (!encode(&maps.q, io.q, D, io.num_heads, io.num_rows, io.q_stride, a.group, a.tokens)) return cudaErrorInvalidValue;
+  if (io.num_keys && (!encode(&maps.k, io.k, D, io.num_kv_heads, io.num_keys, io.k_stride, 1, kKeys) ||
+                      !encode(&maps.v, io.v, D, io.num_kv_heads, io.num_keys, io.v_stride, 1, kKeys)))
+    return cudaErrorInvalidValue;
   const bool h = io.dtype == MOE_DTYPE_F16;
-  if (io.head_dim == 64)
-    return h ? launch<F16, 64>(kmap, vmap, a, io.num_kv_heads, st) : launch<Bf16, 64>(kmap, vmap, a, io.num_kv_heads, st);
-  return h ? launch<F16, 128>(kmap, vmap, a, io.num_kv_heads, st) : launch<Bf16, 128>(kmap, vmap, a, io.num_kv_heads, st);
+  if (D == 64) return h ? launch<F16, 64>(maps, a, st) : launch<Bf16, 64>(maps, a, st);
+  return h ? launch<F16, 128>(maps, a, st) : launch<Bf16, 128>(maps, a, st);
 }
 
 }  // namespace moe

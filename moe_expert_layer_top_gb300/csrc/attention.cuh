@@ -71,14 +71,14 @@ __device__ __forceinline__ int warp_inclusive_sum(int v) {
 }
 
 // The sequence that tile number `tile` falls into, when sequence b has
-// ceil(n_b * group / rows) tiles of `rows` (row, head) pairs. Called by a whole warp; seq = -1: past the last tile.
+// ceil(n_b / rows) tiles of `rows` rows. Called by a whole warp; seq = -1: past the last tile.
 struct TileAt {
   int seq, local, tiles;  // sequence, tile within it, its tiles
   Span rows, keys;        // of the sequence
 };
 
 __device__ __forceinline__ TileAt find_tile(const int32_t *cu_rows, int num_rows, const int32_t *cu_keys, int num_keys,
-                                            int num_seqs, int group, int rows, int64_t tile, int32_t *status) {
+                                            int num_seqs, int rows, int64_t tile, int32_t *status) {
   const int lane = threadIdx.x & 31;
   int64_t base = 0;
   for (int b0 = 0; b0 < num_seqs; b0 += 32) {
@@ -88,7 +88,7 @@ __device__ __forceinline__ TileAt find_tile(const int32_t *cu_rows, int num_rows
       r = seq_span(cu_rows, b, num_rows, status);
       k = seq_span(cu_keys, b, num_keys, status);
     }
-    const int tiles = int((int64_t(r.n) * group + rows - 1) / rows);
+    const int tiles = (r.n + rows - 1) / rows;
     const int64_t end = base + warp_inclusive_sum(tiles);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, tile < end);
     if (hit) {
