@@ -133,77 +133,96 @@ __device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b, int32_t *stat
   return s;
 }
 
-// Fills before[] with the units ahead of every 32 sequences; returns all units. Whole block.
-template <class C>
-__device__ int64_t count_units(const PagedArgs &a, int64_t *before, int64_t *total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int chunks = (a.num_seqs + 31) / 32;
-  for (int c = warp; c < chunks; c += blockDim.x / 32) {
-    const Seq s = load_seq<C>(a, c * 32 + lane, nullptr);
-    int64_t v = s.units();
-#pragma unroll
-    for (int d = 16; d; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    if (lane == 0) before[c] = v;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int64_t base = 0;
-    for (int c0 = 0; c0 < chunks; c0 += 32) {
-      const int64_t v = c0 + lane < chunks ? before[c0 + lane] : 0;
-      int64_t s = v;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, s, d);
-        if (lane >= d) s += u;
-      }
-      if (c0 + lane < chunks) before[c0 + lane] = base + s - v;
-      base += __shfl_sync(0xFFFFFFFFu, s, 31);
-    }
-    if (lane == 0) *total = base;
-  }
-  __syncthreads();
-  return *total;
-}
-
 // A place in the list: a unit of an item of a sequence.
 struct Place {
   Seq s;
   int item, unit;
 };
 
-// The place of unit p (0 <= p < all). Whole warp; the same for every lane.
-template <class C>
-__device__ Place find_unit(const PagedArgs &a, const int64_t *before, int64_t p) {
+__device__ __forceinline__ int64_t warp_sums(int64_t v) {  // inclusive
   const int lane = threadIdx.x & 31;
-  const int chunks = (a.num_seqs + 31) / 32;
-  int c = 0;
-  for (int lo = 0, hi = chunks; lo < hi;) {  // the last chunk with before <= p: earlier ones with that start are empty
-    const int mid = (lo + hi) / 2;
-    if (before[mid] <= p) {
-      c = mid;
-      lo = mid + 1;
-    } else {
-      hi = mid;
-    }
-  }
-  const Seq mine = load_seq<C>(a, c * 32 + lane, nullptr);
-  const int64_t own = mine.units();
-  int64_t end = own;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, end, d);
-    if (lane >= d) end += u;
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += u;
   }
-  const int64_t rest = p - before[c];
-  const unsigned hit = __ballot_sync(0xFFFFFFFFu, rest < end);
-  const int w = hit ? __ffs(hit) - 1 : 31;
-  const int64_t in = rest - (__shfl_sync(0xFFFFFFFFu, end, w) - __shfl_sync(0xFFFFFFFFu, own, w));
-  Place pl;
-  pl.s = load_seq<C>(a, c * 32 + w, nullptr);
-  pl.item = int(in / (pl.s.steps + kOver));
-  pl.unit = int(in - int64_t(pl.item) * (pl.s.steps + kOver));
-  return pl;
+  return v;
 }
+
+// The list of all work, as a warp sees it: the 32 sequences of a chunk, one a
+// lane, and (more than 32 sequences) the units ahead of each chunk in shared memory.
+template <class C>
+struct List {
+  const PagedArgs &a;
+  int64_t *before;
+  int64_t all;    // units of all sequences
+  Seq mine;       // sequence of this lane in chunk 0 (up to 32 sequences)
+  int64_t end;    // units up to and with it
+
+  // Whole block.
+  __device__ List(const PagedArgs &args, int64_t *shared, int64_t *total) : a(args), before(shared) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int chunks = (a.num_seqs + 31) / 32;
+    if (chunks <= 1) {  // every warp for itself: one round of loads, no barrier
+      mine = load_seq<C>(a, lane, nullptr);
+      end = warp_sums(mine.units());
+      all = __shfl_sync(0xFFFFFFFFu, end, 31);
+      return;
+    }
+    for (int c = warp; c < chunks; c += blockDim.x / 32) {
+      const int64_t v = warp_sums(load_seq<C>(a, c * 32 + lane, nullptr).units());
+      if (lane == 31) before[c] = v;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int64_t base = 0;
+      for (int c0 = 0; c0 < chunks; c0 += 32) {
+        const int64_t v = c0 + lane < chunks ? before[c0 + lane] : 0, s = warp_sums(v);
+        if (c0 + lane < chunks) before[c0 + lane] = base + s - v;
+        base += __shfl_sync(0xFFFFFFFFu, s, 31);
+      }
+      if (lane == 0) *total = base;
+    }
+    __syncthreads();
+    all = *total;
+  }
+
+  // The place of unit p (0 <= p < all). Whole warp; the same for every lane.
+  __device__ Place find(int64_t p) const {
+    const int lane = threadIdx.x & 31;
+    const int chunks = (a.num_seqs + 31) / 32;
+    int c = 0;
+    Seq s = mine;
+    int64_t stop = end, rest = p;
+    if (chunks > 1) {
+      for (int lo = 0, hi = chunks; lo < hi;) {  // the last chunk with before <= p: earlier ones with that start are empty
+        const int mid = (lo + hi) / 2;
+        if (before[mid] <= p) {
+          c = mid;
+          lo = mid + 1;
+        } else {
+          hi = mid;
+        }
+      }
+      s = load_seq<C>(a, c * 32 + lane, nullptr);
+      stop = warp_sums(s.units());
+      rest = p - before[c];
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, rest < stop);
+    const int w = hit ? __ffs(hit) - 1 : 31;
+    const int64_t in = rest - (__shfl_sync(0xFFFFFFFFu, stop, w) - __shfl_sync(0xFFFFFFFFu, s.units(), w));
+    Place pl;
+    pl.s.b = c * 32 + w;
+    pl.s.row0 = __shfl_sync(0xFFFFFFFFu, s.row0, w);
+    pl.s.n = __shfl_sync(0xFFFFFFFFu, s.n, w);
+    pl.s.len = __shfl_sync(0xFFFFFFFFu, s.len, w);
+    pl.s.items = __shfl_sync(0xFFFFFFFFu, s.items, w);
+    pl.s.steps = __shfl_sync(0xFFFFFFFFu, s.steps, w);
+    pl.item = int(in / (pl.s.steps + kOver));
+    pl.unit = int(in - int64_t(pl.item) * (pl.s.steps + kOver));
+    return pl;
+  }
+};
 
 // A run of stages of one item that a block computes (count may be 0).
 struct Segment {
@@ -667,11 +686,11 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
   pdl_launch_dependents();
   if (blockIdx.x == 0)  // what is out of range is reported once
     for (int b = tid; b < a.num_seqs; b += C::THREADS) load_seq<C>(a, b, a.status);
-  const int64_t all = count_units<C>(a, sm.before, &total);
-  const int64_t blocks = active_blocks<C>(all, gridDim.x);
+  const List<C> list(a, sm.before, &total);
+  const int64_t all = list.all, blocks = active_blocks<C>(all, gridDim.x);
   if (int64_t(blockIdx.x) >= blocks) return;
   const int64_t begin = int64_t(blockIdx.x) * all / blocks, end = (int64_t(blockIdx.x) + 1) * all / blocks;
-  Place place = find_unit<C>(a, sm.before, begin);
+  Place place = list.find(begin);
   int64_t left = end - begin;
   bool first = true;
   while (left > 0) {
@@ -794,15 +813,15 @@ __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const Pa
   __shared__ int64_t before[kMaxSeqs / 32 + 1], total;
   __shared__ float weight[8][kMaxBlocks], top[8], sum[8];
   static_assert(kCombineThreads == 8 * 32, "a warp for each row's weights");
-  const int64_t all = count_units<C>(a, before, &total);
-  const int64_t blocks = active_blocks<C>(all, gridDim.x);
+  const List<C> list(a, before, &total);
+  const int64_t all = list.all, blocks = active_blocks<C>(all, gridDim.x);
   const int64_t c = blockIdx.x;
   Place p;
   int64_t begin = 0, end = 0, item0 = 0, item1 = 0;  // the block's units, the item's
   if (c + 1 < blocks) {
     begin = c * all / blocks;
     end = (c + 1) * all / blocks;
-    p = find_unit<C>(a, before, end - 1);
+    p = list.find(end - 1);
     item0 = end - 1 - p.unit;
     item1 = item0 + kOver + p.s.steps;
   }
