@@ -139,6 +139,11 @@ struct Place {
   int item, unit;
 };
 
+// a / b for 0 <= a, 0 < b; in 32 bits where that is enough (a 64-bit division is about 100 instructions).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return uint64_t(a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
+
 __device__ __forceinline__ int64_t warp_sums(int64_t v) {  // inclusive
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -218,7 +223,7 @@ struct List {
     pl.s.len = __shfl_sync(0xFFFFFFFFu, s.len, w);
     pl.s.items = __shfl_sync(0xFFFFFFFFu, s.items, w);
     pl.s.steps = __shfl_sync(0xFFFFFFFFu, s.steps, w);
-    pl.item = int(in / (pl.s.steps + kOver));
+    pl.item = int(divide(in, pl.s.steps + kOver));
     pl.unit = int(in - int64_t(pl.item) * (pl.s.steps + kOver));
     return pl;
   }
@@ -259,11 +264,20 @@ __device__ __forceinline__ Segment next_segment(const PagedArgs &a, Place &p, in
   return g;
 }
 
-// Blocks that share the list: about a stage for each warp at least.
+// The blocks' shares of the list: about a stage for each warp at least, and equal to one unit.
+struct Shares {
+  int64_t blocks, each, more;  // the first `more` blocks have each + 1 units
+
+  __device__ __forceinline__ int64_t begin(int64_t b) const { return b * each + (b < more ? b : more); }
+};
+
 template <class C>
-__device__ __forceinline__ int64_t active_blocks(int64_t units, int64_t grid) {
-  const int64_t n = (units + C::W - 1) / C::W;
-  return n < grid ? n : grid;
+__device__ __forceinline__ Shares make_shares(int64_t units, int64_t grid) {
+  Shares s;
+  s.blocks = units < grid * C::W ? (units + C::W - 1) / C::W : grid;
+  s.each = s.blocks ? divide(units, s.blocks) : 0;
+  s.more = units - s.each * s.blocks;
+  return s;
 }
 
 // ------------------------------------------------------------------ copies
@@ -633,47 +647,65 @@ __device__ __forceinline__ void store_lse(const PagedArgs &a, const Seq &s, int 
 
 // ------------------------------------------------------------------ main kernel
 
-// The queries of a row block, as operand registers, with their limits and multipliers.
+// The queries of a row block: loaded first, made into operand registers (with their limits and multipliers) when
+// the copies of keys are on their way.
 template <class T, class C>
-__device__ void load_queries(const PagedArgs &a, typename C::Smem &sm, const Segment &seg, int warp) {
-  constexpr int D = C::D, GR = D / 32;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  for (int n = warp; n < C::NT; n += C::W) {
-    const int r = seg.r0 + 8 * n + g;
-    const bool real = r < seg.s.n * a.group;
-    const int tok = r / a.group, h = seg.kv * a.group + r - tok * a.group;
-    uint4 raw[GR];  // dimensions 32 i + 8 t .. + 7
-    float amax = 0.0f;
+struct Queries {
+  static constexpr int D = C::D, GR = D / 32, PER = (C::NT + C::W - 1) / C::W;  // n-tiles of a warp
+  uint4 raw[PER][GR];  // dimensions 32 i + 8 t .. + 7 of row g
+
+  __device__ __forceinline__ void load(const PagedArgs &a, const Segment &seg, int warp) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (real)
-        raw[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(seg.s.row0 + tok) * a.q_stride + int64_t(h) * D +
-                                                       32 * i + 8 * t));
-      raw[i].x ^= a.flip, raw[i].y ^= a.flip, raw[i].z ^= a.flip, raw[i].w ^= a.flip;
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    for (int k = 0; k < PER; ++k) {
+      const int n = warp + k * C::W, r = seg.r0 + 8 * n + g;
+      const int tok = r / a.group, h = seg.kv * a.group + r - tok * a.group;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) amax = fmaxf(amax, fmaxf(fabsf(T::lo(w[c])), fabsf(T::hi(w[c]))));
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    // times 2^(14 - e): the largest lies in [2^14, 2^15), parts down to 2^-28 of it keep all their bits
-    const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -100), 126);
-    const float up = __uint_as_float(uint32_t(127 + 14 - e > 254 ? 254 : 127 + 14 - e) << 23);
-#pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        sm.q[n][2 * i + c][lane] = make_uint2(f16x2(T::lo(w[2 * c]) * up, T::hi(w[2 * c]) * up),
-                                              f16x2(T::lo(w[2 * c + 1]) * up, T::hi(w[2 * c + 1]) * up));
-    }
-    if (t == 0) {
-      sm.mul[8 * n + g] = fmaxf(a.scale2 / up, 0x1p-126f);  // not 0: -inf must stay -inf
-      sm.limit[8 * n + g] = real ? min(seg.s.len, max(0, seg.s.len - seg.s.n + tok + 1)) : 0;
+      for (int i = 0; i < GR; ++i) {
+        raw[k][i] = make_uint4(0, 0, 0, 0);
+        if (n < C::NT && r < seg.s.n * a.group)
+          raw[k][i] = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(seg.s.row0 + tok) * a.q_stride +
+                                                            int64_t(h) * D + 32 * i + 8 * t));
+      }
     }
   }
-}
+
+  __device__ __forceinline__ void store(const PagedArgs &a, typename C::Smem &sm, const Segment &seg, int warp) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int n = warp + k * C::W, r = seg.r0 + 8 * n + g;
+      if (n >= C::NT) break;
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        uint4 &v = raw[k][i];
+        v.x ^= a.flip, v.y ^= a.flip, v.z ^= a.flip, v.w ^= a.flip;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) amax = fmaxf(amax, fmaxf(fabsf(T::lo(w[c])), fabsf(T::hi(w[c]))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      // times 2^(14 - e): the largest lies in [2^14, 2^15), parts down to 2^-28 of it keep all their bits
+      const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -100), 126);
+      const float up = __uint_as_float(uint32_t(127 + 14 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        const uint32_t w[4] = {raw[k][i].x, raw[k][i].y, raw[k][i].z, raw[k][i].w};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          sm.q[n][2 * i + c][lane] = make_uint2(f16x2(T::lo(w[2 * c]) * up, T::hi(w[2 * c]) * up),
+                                                f16x2(T::lo(w[2 * c + 1]) * up, T::hi(w[2 * c + 1]) * up));
+      }
+      if (t == 0) {
+        const bool real = r < seg.s.n * a.group;
+        sm.mul[8 * n + g] = fmaxf(a.scale2 / up, 0x1p-126f);  // not 0: -inf must stay -inf
+        sm.limit[8 * n + g] = real ? min(seg.s.len, max(0, seg.s.len - seg.s.n + r / a.group + 1)) : 0;
+      }
+    }
+  }
+};
 
 template <class T, class C>
 __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(const PagedArgs a) {
@@ -687,20 +719,22 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
   if (blockIdx.x == 0)  // what is out of range is reported once
     for (int b = tid; b < a.num_seqs; b += C::THREADS) load_seq<C>(a, b, a.status);
   const List<C> list(a, sm.before, &total);
-  const int64_t all = list.all, blocks = active_blocks<C>(all, gridDim.x);
-  if (int64_t(blockIdx.x) >= blocks) return;
-  const int64_t begin = int64_t(blockIdx.x) * all / blocks, end = (int64_t(blockIdx.x) + 1) * all / blocks;
+  const Shares shares = make_shares<C>(list.all, gridDim.x);
+  if (int64_t(blockIdx.x) >= shares.blocks) return;
+  const int64_t begin = shares.begin(blockIdx.x), end = shares.begin(int64_t(blockIdx.x) + 1);
   Place place = list.find(begin);
   int64_t left = end - begin;
   bool first = true;
   while (left > 0) {
     const Segment seg = next_segment<C>(a, place, left);
     if (seg.count == 0) continue;
+    Queries<T, C> queries;
+    queries.load(a, seg, warp);
     Copier<C> copier;
     copier.start(a, seg);
 #pragma unroll
     for (int c = 0; c < C::DEPTH - 1; ++c) copier.copy(a, seg, warp + c * C::W, sm.ring[warp][c]);
-    load_queries<T, C>(a, sm, seg, warp);
+    queries.store(a, sm, seg, warp);
     __syncthreads();
     State<C> st;
 #pragma unroll
@@ -811,74 +845,83 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
 template <class T, class C>
 __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const PagedArgs a) {
   __shared__ int64_t before[kMaxSeqs / 32 + 1], total;
-  __shared__ float weight[8][kMaxBlocks], top[8], sum[8];
+  __shared__ float weight[8][kMaxBlocks], top[8], sum[8];  // by row
   static_assert(kCombineThreads == 8 * 32, "a warp for each row's weights");
   const List<C> list(a, before, &total);
-  const int64_t all = list.all, blocks = active_blocks<C>(all, gridDim.x);
+  const Shares shares = make_shares<C>(list.all, gridDim.x);
   const int64_t c = blockIdx.x;
   Place p;
-  int64_t begin = 0, end = 0, item0 = 0, item1 = 0;  // the block's units, the item's
-  if (c + 1 < blocks) {
-    begin = c * all / blocks;
-    end = (c + 1) * all / blocks;
+  int64_t begin = 0, end = 0, item0 = 0, item1 = 0, last = c + 1;  // the block's units, the item's, its last block
+  if (c + 1 < shares.blocks) {
+    begin = shares.begin(c);
+    end = shares.begin(c + 1);
     p = list.find(end - 1);
     item0 = end - 1 - p.unit;
     item1 = item0 + kOver + p.s.steps;
+    while (shares.begin(last + 1) < item1) ++last;
   }
+  // the item's first stage is in a later block, or in an earlier one, or all of them are in this block: nothing to join
+  const bool none = end <= item0 + kOver || begin > item0 + kOver || item1 <= end;
   pdl_wait_primary();  // every block: this kernel must not end before the main one
-  // the item's first stage is in a later block, or in an earlier one, or all of them are in this block
-  if (end <= item0 + kOver || begin > item0 + kOver || item1 <= end) return;
+  if (none) return;
   // the blocks that hold parts of it: c, whose part is its last segment, and those after it, whose first it is
-  int64_t last = c + 1;
-  while ((last + 1) * all / blocks < item1) ++last;
+  constexpr int D = C::D, kAhead = 16;
+  static_assert(8 * (D / 4) <= kCombineThreads, "one thread for four dimensions of a row");
   const int parts = int(last - c) + 1;
-  const float *part0 = a.parts + (c * 2 + (item0 <= begin ? 0 : 1)) * C::PART;
-  const float *part1 = a.parts + (c + 1) * 2 * C::PART;  // the others, two slots apart
-  const int per = p.s.items / a.num_kv_heads, kv = p.item / per, r0 = (p.item - kv * per) * C::ROWS;
-  constexpr int D = C::D;
   const int row0 = 8 * int(blockIdx.y);  // this block's 8 rows of the item
-  // weights of the parts: 2^(reference - largest)
+  const float *part0 = a.parts + (c * 2 + (item0 <= begin ? 0 : 1)) * C::PART;
+  const float *part1 = a.parts + c * 2 * C::PART;  // the others: part b is 2 b slots on
+  const auto part = [&](int b) { return b ? part1 + int64_t(b) * 2 * C::PART : part0; };
+  const int row = threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4)), at = (row0 + row) * D + d;
+  const bool mine = row < 8;
+  float4 v[kAhead];  // the first parts are on their way while the weights are made
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) {
+    v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (mine && b < parts) v[b] = *reinterpret_cast<const float4 *>(part(b) + at);
+  }
+  // weights of the parts: 2^(reference - largest), a warp for each row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   {
-    const int row = row0 + warp;
-    float m = -kNone;
-    for (int b = lane; b < parts; b += 32)
-      m = fmaxf(m, (b ? part1 + int64_t(b - 1) * 2 * C::PART : part0)[C::ROWS * D + row]);
+    const int head = C::ROWS * D + row0 + warp;
+    float m0 = -kNone, l0 = 0.0f;
+    if (lane < parts) {
+      m0 = part(lane)[head];
+      l0 = part(lane)[head + C::ROWS];
+    }
+    float m = m0;
+    for (int b = lane + 32; b < parts; b += 32) m = fmaxf(m, part(b)[head]);
 #pragma unroll
-    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    for (int k = 16; k; k /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
     float l = 0.0f;
     for (int b = lane; b < parts; b += 32) {
-      const float *x = (b ? part1 + int64_t(b - 1) * 2 * C::PART : part0) + C::ROWS * D + row;
-      const float f = exp2_approx(x[0] - m);
+      const float f = exp2_approx((b == lane ? m0 : part(b)[head]) - m);
       weight[warp][b] = f;
-      l = fmaf(x[C::ROWS], f, l);
+      l = fmaf(b == lane ? l0 : part(b)[head + C::ROWS], f, l);
     }
 #pragma unroll
-    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    for (int k = 16; k; k /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, k);
     if (lane == 0) {
       top[warp] = m;
       sum[warp] = l;
     }
   }
   __syncthreads();
-  const int rows = min(8, p.s.n * a.group - r0 - row0);
-  for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kCombineThreads) {
-    const int row = idx / (D / 4), d = 4 * (idx % (D / 4));
-    const int64_t at = (row0 + row) * D + d;
-    float4 v = *reinterpret_cast<const float4 *>(part0 + at);
-    const float f = weight[row][0];
-    v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+  const int per = p.s.items / a.num_kv_heads, kv = p.item / per, r0 = (p.item - kv * per) * C::ROWS;
+  if (!mine || r0 + row0 + row >= p.s.n * a.group) return;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const auto add = [&](const float4 &x, float w) {
+    o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
+  };
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b)
+    if (b < parts) add(v[b], weight[row][b]);
 #pragma unroll 8
-    for (int b = 1; b < parts; ++b) {
-      const float4 o = *reinterpret_cast<const float4 *>(part1 + int64_t(b - 1) * 2 * C::PART + at);
-      const float w = weight[row][b];
-      v.x = fmaf(o.x, w, v.x), v.y = fmaf(o.y, w, v.y), v.z = fmaf(o.z, w, v.z), v.w = fmaf(o.w, w, v.w);
-    }
-    const float l = sum[row], inv = l > 0.0f ? 1.0f / l : 0.0f;
-    store4<T>(a, p.s, kv, r0 + row0 + row, D, d,
-              l != 0.0f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0, 0, 0, 0));
-    if (d == 0) store_lse(a, p.s, kv, r0 + row0 + row, top[row], l);
-  }
+  for (int b = kAhead; b < parts; ++b) add(*reinterpret_cast<const float4 *>(part(b) + at), weight[row][b]);
+  const float l = sum[row], inv = l > 0.0f ? 1.0f / l : 0.0f;
+  store4<T>(a, p.s, kv, r0 + row0 + row, D, d,
+            l != 0.0f ? make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv) : make_float4(0, 0, 0, 0));
+  if (d == 0) store_lse(a, p.s, kv, r0 + row0 + row, top[row], l);
 }
 
 // ------------------------------------------------------------------ host
