@@ -25,7 +25,6 @@ another stream than the one it was allocated on is kept alive by the caller
 from __future__ import annotations
 
 import functools
-from dataclasses import dataclass
 
 import torch
 
@@ -34,27 +33,33 @@ from . import abi
 _DTYPES = {torch.bfloat16: abi.MOE_DTYPE_BF16, torch.float16: abi.MOE_DTYPE_F16}
 
 
-@dataclass
 class KVCacheMXFP4:
-    """A paged key/value cache in MXFP4 (uint8 tensors, contiguous, on one CUDA device).
+    """A paged key/value cache in MXFP4 (uint8 tensors, contiguous, on one CUDA device; the four stay the same).
 
     k_codes, v_codes:   [pages][kv heads][page size][head_dim/2], two E2M1 codes per byte (element 2i low)
     k_scales, v_scales: [pages][kv heads][page size][head_dim/32], UE8M0
     """
-    k_codes: torch.Tensor
-    k_scales: torch.Tensor
-    v_codes: torch.Tensor
-    v_scales: torch.Tensor
+    __slots__ = ("_parts", "_abi", "device", "num_kv_heads", "head_dim")
 
-    def __post_init__(self):
-        pages, heads, page, half = _shape(self.k_codes, 4, "k_codes")
-        device = self.k_codes.get_device()
-        for name, t, width in (("k_codes", self.k_codes, half), ("k_scales", self.k_scales, half // 16),
-                               ("v_codes", self.v_codes, half), ("v_scales", self.v_scales, half // 16)):
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor):
+        pages, heads, page, half = shape = _shape(k_codes, 4, "k_codes")
+        device, scales = k_codes.get_device(), (pages, heads, page, half // 16)
+        parts = (k_codes, k_scales, v_codes, v_scales)
+        for name, t, want in zip(("k_codes", "k_scales", "v_codes", "v_scales"), parts, (shape, scales, shape, scales)):
             if t.dtype is not torch.uint8 or device < 0 or t.get_device() != device or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor on the cache's device")
-            if t.shape != (pages, heads, page, width):
-                raise ValueError(f"{name} must have shape {(pages, heads, page, width)}, not {tuple(t.shape)}")
+            if t.shape != want:
+                raise ValueError(f"{name} must have shape {tuple(want)}, not {tuple(t.shape)}")
+        self._parts = parts
+        self.device, self.num_kv_heads, self.head_dim = device, heads, 2 * half
+        self._abi = abi.MoeKvCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                                   pages, page, heads, 2 * half)
+
+    k_codes = property(lambda self: self._parts[0])
+    k_scales = property(lambda self: self._parts[1])
+    v_codes = property(lambda self: self._parts[2])
+    v_scales = property(lambda self: self._parts[3])
+    page_size = property(lambda self: self._parts[0].shape[2])
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, device="cuda") -> "KVCacheMXFP4":
@@ -62,22 +67,8 @@ class KVCacheMXFP4:
             return torch.empty((num_pages, num_kv_heads, page_size, width), dtype=torch.uint8, device=device)
         return cls(make(head_dim // 2), make(head_dim // 32), make(head_dim // 2), make(head_dim // 32))
 
-    @property
-    def head_dim(self) -> int:
-        return 2 * self.k_codes.shape[3]
-
-    @property
-    def num_kv_heads(self) -> int:
-        return self.k_codes.shape[1]
-
-    @property
-    def page_size(self) -> int:
-        return self.k_codes.shape[2]
-
     def as_abi(self) -> abi.MoeKvCache:
-        pages, heads, page, half = self.k_codes.shape
-        return abi.MoeKvCache(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
-                              self.v_scales.data_ptr(), pages, page, heads, 2 * half)
+        return self._abi
 
 
 def rope_table(positions: int, rotary_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -95,22 +86,23 @@ def _shape(t: torch.Tensor, dims: int, name: str):
 
 
 def _rows(t: torch.Tensor, name: str, device: int, dtype: torch.dtype) -> int:
-    """Row stride of a [rows][heads][dim] tensor whose rows are contiguous."""
+    """Row stride of a [rows][heads][dim] tensor whose rows are contiguous, on the device and in the type of q."""
     rows, heads, dim = _shape(t, 3, name)
-    if device < 0 or dtype not in _DTYPES:
-        raise ValueError("q must be a CUDA tensor in bf16 or fp16")
     if t.get_device() != device or t.dtype is not dtype:
         raise ValueError(f"{name} must have the device and type of q")
     step, head, one = t.stride()
-    if rows > 1 and heads > 1 and dim > 1:
-        if one != 1 or head != dim:
-            raise ValueError(f"the heads of a row of {name} must be contiguous")
-        return step
-    if t.numel() == 0:  # strides of an empty tensor say nothing
-        return heads * dim
-    if (dim > 1 and one != 1) or (heads > 1 and head != dim):
+    if (one != 1 or head != dim) and t.numel() and ((dim > 1 and one != 1) or (heads > 1 and head != dim)):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
     return step if rows > 1 else heads * dim
+
+
+def _queries(q: torch.Tensor) -> tuple[int, torch.dtype, int]:
+    """Device and type of q, which the other tensors share, and the type's code."""
+    _shape(q, 3, "q")
+    device, dtype = q.get_device(), q.dtype
+    if device < 0 or dtype not in _DTYPES:
+        raise ValueError("q must be a CUDA tensor in bf16 or fp16")
+    return device, dtype, _DTYPES[dtype]
 
 
 def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: int) -> int:
@@ -131,7 +123,8 @@ def _status(t: torch.Tensor | None, device: int) -> int | None:
 def _out(out: torch.Tensor | None, q: torch.Tensor, device: int, dtype: torch.dtype) -> tuple[torch.Tensor, int]:
     """The output tensor and its row stride."""
     if out is None:
-        return torch.empty(q.shape, dtype=dtype, device=q.device), q.shape[1] * q.shape[2]
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        return out, q.shape[1] * q.shape[2]
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     return out, _rows(out, "out", device, dtype)
@@ -170,7 +163,7 @@ def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: 
     Returns {"q"}, plus "k" (rotated keys in 16 bits) with rotated_keys, plus "k_cached" and "v_cached" (the
     values that the 4-bit cache keeps) with cached_values.
     """
-    device, dtype = q.get_device(), q.dtype
+    device, dtype, code = _queries(q)
     q_stride, k_stride, v_stride = (_rows(q, "q", device, dtype), _rows(k, "k", device, dtype),
                                     _rows(v, "v", device, dtype))
     T, H, D = q.shape
@@ -191,7 +184,7 @@ def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: 
     if (cache is None) != (slots is None):
         raise ValueError("cache and slots go together")
     if cache is not None:
-        if cache.k_codes.get_device() != device or (cache.num_kv_heads, cache.head_dim) != (K, D):
+        if cache.device != device or cache.num_kv_heads != K or cache.head_dim != D:
             raise ValueError("the cache must be on q's device, with the kv heads and head size of k")
         slots_at = _vector(slots, "slots", torch.int64, T, device)
         abi_cache = cache.as_abi()
@@ -210,7 +203,7 @@ def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: 
         out["v_cached"] = torch.empty((T, K, D), dtype=dtype, device=q.device)
         k_cached_at, v_cached_at = out["k_cached"].data_ptr(), out["v_cached"].data_ptr()
     io = abi.MoeQkvAppendIO(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, T, H, K, D, _DTYPES[dtype], R,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, T, H, K, D, code, R,
         int(interleaved), table_rows, rope_at, positions_at,
         None if q_norm is None else _vector(q_norm, "q_norm", dtype, D, device),
         None if k_norm is None else _vector(k_norm, "k_norm", dtype, D, device),
@@ -243,7 +236,7 @@ def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor,
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
-    device, dtype = q.get_device(), q.dtype
+    device, dtype, code = _queries(q)
     q_stride = _rows(q, "q", device, dtype)
     T, H, D = q.shape
     B = lengths.shape[0] if lengths.dim() == 1 else -1
@@ -253,14 +246,14 @@ def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor,
             page_table.shape[0] != B or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 [sequences][pages] tensor on q's device")
     c = cache.as_abi()
-    if cache.k_codes.get_device() != device or c.head_dim != D:
+    if cache.device != device or cache.head_dim != D:
         raise ValueError("the cache must be on q's device, with q's head size")
     out, out_stride = _out(out, q, device, dtype)
     lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
     io = abi.MoeAttendPagedIO(q.data_ptr(), q_stride, out.data_ptr(), out_stride,
                               lse.data_ptr() if return_lse else None, page_table.data_ptr(), lengths_at, cu_at, B, T,
-                              page_table.shape[1], max_rows, H, _DTYPES[dtype], D ** -0.5 if scale is None else scale)
-    n = _paged_workspace(device, T, max_rows, H, c.num_kv_heads, D)
+                              page_table.shape[1], max_rows, H, code, D ** -0.5 if scale is None else scale)
+    n = _paged_workspace(device, T, max_rows, H, cache.num_kv_heads, D)
     if stream is None:
         workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
     else:  # allocated on the stream that uses it, so that it is not handed out again before the call has run
@@ -281,7 +274,7 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
-    device, dtype = q.get_device(), q.dtype
+    device, dtype, code = _queries(q)
     q_stride, k_stride, v_stride = (_rows(q, "q", device, dtype), _rows(k, "k", device, dtype),
                                     _rows(v, "v", device, dtype))
     T, H, D = q.shape
@@ -297,7 +290,7 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
     lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
     io = abi.MoeAttendPromptIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
                                out.data_ptr(), out_stride, lse.data_ptr() if return_lse else None, cu_rows_at,
-                               cu_keys_at, n - 1, T, N, H, K, D, _DTYPES[dtype], int(causal),
+                               cu_keys_at, n - 1, T, N, H, K, D, code, int(causal),
                                D ** -0.5 if scale is None else scale)
     _on(device, "moe_attend_prompt", abi.moe_attend_prompt, io, _status(d_status, device),
         _raw_stream(stream, device))
