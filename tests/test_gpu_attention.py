@@ -271,6 +271,40 @@ def test_prompt_offsets_past_32_bits():
     assert torch.equal(out[a:b], want) and not out[b:].any() and not out[a - 200:a].any()
 
 
+@pytest.mark.parametrize("D,H,K,dtype", [(64, 2, 1, "bf16"), (128, 2, 1, "fp16"), (64, 1, 1, "fp16"), (128, 4, 1, "bf16")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_rising_scores(D, H, K, dtype, causal):
+    """Scores that rise by 12 in the exponent from 100 keys to the next in one row and fall or stay in others: the
+    references move in several key tiles, in both row tiles and in a lone one."""
+    rng = np.random.default_rng(D + H)
+    n = 700
+    q = ac.rows16(rng, (n, H, D), dtype, 0.05)
+    k = ac.rows16(rng, (n, K, D), dtype, 0.05)
+    v = ac.rows16(rng, (n, K, D), dtype)
+    step = (np.arange(n) // 100)[:, None]
+    k[:, :, 0] = step * 8.0
+    q[:, :, 0] = np.array([1.0, -1.0, 0.0, 2.0])[np.arange(n) % 4][:, None]
+    for rows in (n, 90):  # several row tiles; a lone one at the end of the keys
+        cr, ck = ac.i32([0, rows]), ac.i32([0, n])
+        x = q[n - rows:]
+        out, lse = attention.attend_prompt(ac.dev(x, dtype), ac.dev(k, dtype), ac.dev(v, dtype), cr, ck, causal=causal,
+                                           scale=1.0, return_lse=True)
+        ac.check_attention(out, lse, x, k, v, 1.0, dtype, dtype, causal)
+
+
+@pytest.mark.parametrize("H,K,D", [(96, 2, 64), (200, 1, 64), (130, 1, 128), (56, 8, 128), (1024, 1024, 64), (1024, 1, 64)])
+def test_prompt_groups(H, K, D):
+    """Groups that do not divide a row tile, and larger than one."""
+    run_prompt([(5, 9), (11, 140)] if H < 1000 else [(3, 150)], H, K, D, "bf16", True, seed=H)
+
+
+@pytest.mark.parametrize("B,longest", [(33, 60), (70, 200), (1100, 12)])
+def test_prompt_many_sequences(B, longest):
+    rng = np.random.default_rng(B)
+    rows = rng.integers(0, longest, B)
+    run_prompt([(int(n), int(n + x)) for n, x in zip(rows, rng.integers(0, 9, B))], 2, 1, 64, "fp16", True, seed=B)
+
+
 # ------------------------------------------------------------------ paged cache
 
 PAGED = [
@@ -401,6 +435,80 @@ def test_paged_offsets_past_32_bits():
     assert torch.equal(c.v_codes[-1, :, -1], codes[0]) and torch.equal(c.v_scales[-1, :, -1], scales[0])
 
 
+@pytest.mark.parametrize("case", [
+    ([(4, 500), (2, 33)], 8, 2, 64, 16, "bf16", 4),       # 16 rows
+    ([(4, 700), (3, 95)], 8, 2, 128, 64, "fp16", 4),
+    ([(6, 300), (5, 1000), (6, 31)], 16, 2, 128, 32, "bf16", 6),  # 48 rows: two blocks of 24
+    ([(8, 260), (8, 77)], 8, 2, 128, 16, "fp16", 8),      # 32 rows
+    ([(8, 260), (7, 777)], 16, 4, 64, 64, "bf16", 8),
+    ([(1, 333), (1, 2)], 8, 1, 64, 32, "fp16", 1),        # 8 rows
+    ([(3, 500)], 130, 1, 64, 16, "bf16", 3),              # 390 rows of a head
+], ids=lambda c: f"H{c[1]}_D{c[3]}_r{c[6]}_{c[5]}")
+def test_paged_row_block_sizes(case):
+    run_paged(*case, seed=case[1])
+
+
+@pytest.mark.parametrize("B,longest,D,H,K,rows", [(33, 200, 64, 4, 2, 3), (70, 300, 128, 4, 1, 2), (1100, 40, 64, 2, 1, 2)])
+def test_paged_many_sequences(B, longest, D, H, K, rows):
+    """More sequences than a warp has lanes, and than a warp has lanes times lanes; some without rows or keys."""
+    rng = np.random.default_rng(B)
+    seqs = [(int(n), int(m)) for n, m in zip(rng.integers(0, rows + 1, B), rng.integers(0, longest, B))]
+    run_paged(seqs, H, K, D, 16, "bf16", rows, seed=B)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 2.0])
+def test_paged_other_scales(scale):
+    rng = np.random.default_rng(27)
+    n, H, K, D = 200, 6, 2, 64
+    c = ac.Cache(rng, [n], K, D, 32)
+    q = ac.rows16(rng, (2, H, D), "fp16", 1.5)
+    out, lse = attention.attend_paged(ac.dev(q, "fp16"), c.cache, c.table, ac.i32([n]), ac.i32([0, 2]), scale=scale,
+                                      max_rows=2, return_lse=True)
+    ac.check_attention(out, lse, q, c.k[0], c.v[0], scale, "fp16", "fp16")
+
+
+def test_paged_rising_scores():
+    """Scores that rise by 2^4 in the exponent from stage to stage, and values whose scales do: every move of the
+    references."""
+    rng = np.random.default_rng(28)
+    n, H, K, D = 1000, 8, 1, 128
+    c = ac.Cache(rng, [n], K, D, 16, sigma=0.125)
+    table = c.table[0].long()
+    one = np.full((1, D // 2), 0x22, dtype=np.uint8)  # every code 1.0
+    for j in range(n):  # keys: a constant row of 2^e with e rising, so that q . k rises
+        page, at = table[j // 16], j % 16
+        c.cache.k_codes[page, :, at] = torch.from_numpy(one).cuda()
+        e = min(j // 64, 10)
+        c.cache.k_scales[page, :, at] = 127 - 6 + e
+        c.cache.v_scales[page, :, at] += j // 100
+        c.k[0][j] = 2.0 ** (e - 6)
+        c.v[0][j] *= 2.0 ** (j // 100)
+    q = np.zeros((3, H, D))
+    for r in range(3):
+        for h in range(H):
+            q[r, h, : 8 * (h + 1)] = (1, -1, 0.25)[r]
+    out, lse = attention.attend_paged(ac.dev(q, "bf16"), c.cache, c.table, ac.i32([n]), ac.i32([0, 3]), max_rows=3,
+                                      return_lse=True)
+    ac.check_attention(out, lse, q, c.k[0], c.v[0], D ** -0.5, "bf16", "fp16")
+
+
+def test_paged_sequences_that_share_pages():
+    """One prefix in the tables of three sequences, and the same page twice in one table."""
+    rng = np.random.default_rng(29)
+    H, K, D, page = 8, 2, 64, 16
+    c = ac.Cache(rng, [100], K, D, page)
+    t = c.table[0].tolist()
+    table = [t, t[:3] + [t[0], t[0]] + t[5:], t]
+    lens = [100, 80, 37]
+    q = ac.rows16(rng, (6, H, D), "bf16", 1.5)
+    out, lse = attention.attend_paged(ac.dev(q, "bf16"), c.cache, ac.i32(table), ac.i32(lens), ac.i32([0, 2, 4, 6]),
+                                      max_rows=2, return_lse=True)
+    for b in range(3):
+        at = np.array([t.index(table[b][j // page]) * page + j % page for j in range(lens[b])])
+        r = slice(2 * b, 2 * b + 2)
+        ac.check_attention(out[r], lse[r], q[r], c.k[0][at], c.v[0][at], D ** -0.5, "bf16", "fp16")
+
+
 # ------------------------------------------------------------------ streams, graphs, a run of all
 
 def test_other_streams_and_concurrent_calls():
@@ -459,6 +567,60 @@ def test_prompt_in_a_graph():
     out.zero_()
     g.replay()
     assert torch.equal(out, want)
+
+
+def test_prompt_calls_at_once():
+    cases = []
+    for n, gen in ((400, 1), (90, 2)):
+        x = torch.randn(n, 6, 64, device="cuda", generator=torch.Generator("cuda").manual_seed(gen)).half()
+        cases.append((x[:, :4], x[:, 4:5], x[:, 5:], ac.i32([0, n // 3, n]), ac.i32([0, n // 3, n])))
+    want = [attention.attend_prompt(*c) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [torch.zeros_like(w) for w in want]
+        torch.cuda.synchronize()
+        for c, s, o in zip(cases, streams, outs):
+            attention.attend_prompt(*c, out=o, stream=s)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
+def test_append_in_a_graph_and_on_another_stream():
+    """A captured append follows the positions and slots of its replay; one on another stream writes the same."""
+    T, H, K, D, page = 12, 4, 2, 128, 16
+    x = torch.randn(T, H + 2 * K, D, device="cuda", generator=torch.Generator("cuda").manual_seed(50)).bfloat16()
+    rope = attention.rope_table(100, D)
+    pos, slots = ac.i32(list(range(T))), torch.arange(T, device="cuda")
+    parts = ("k_codes", "k_scales", "v_codes", "v_scales")
+    caches = [attention.KVCacheMXFP4.empty(4, page, K, D) for _ in range(3)]
+
+    def call(c, **kw):
+        return attention.qkv_append(x[:, :H], x[:, H:H + K], x[:, H + K:], positions=pos, rope=rope, cache=c, slots=slots,
+                                    **kw)["q"]
+
+    call(caches[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q = call(caches[0])
+    pos.copy_(torch.arange(T, dtype=torch.int32) * 7)
+    slots.copy_(torch.arange(T).flip(0) * 5)
+    for c in caches:
+        for part in parts:
+            getattr(c, part).zero_()
+    want = call(caches[1])
+    torch.cuda.synchronize()
+    g.replay()
+    stream = torch.cuda.Stream()
+    other = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    call(caches[2], q_out=other, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(q, want) and torch.equal(other, want)
+    for part in parts:
+        w = getattr(caches[1], part)
+        assert w.any() and torch.equal(getattr(caches[0], part), w) and torch.equal(getattr(caches[2], part), w)
 
 
 def test_layer_prompt_then_verify_steps():
