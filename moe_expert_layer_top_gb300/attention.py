@@ -17,8 +17,9 @@ set to MOE_OK, and look at it when convenient (MOE_ERR_DEVICE_BOUNDS: something
 was out of range and was not accessed).
 
 The calls run on the tensors' device and on its current stream unless ``stream``
-is given. Outputs and workspaces come from PyTorch's allocator, so calls on
-several streams and captured graphs do not share any. A tensor that is used on
+is given. Outputs and workspaces come from PyTorch's allocator, on the stream
+of the call, so calls on several streams and captured graphs do not share any
+and none is handed out again before the call has run. A tensor that is used on
 another stream than the one it was allocated on is kept alive by the caller
 (``Tensor.record_stream``), as for any PyTorch operator.
 """
@@ -120,11 +121,18 @@ def _status(t: torch.Tensor | None, device: int) -> int | None:
     return t.data_ptr()
 
 
-def _out(out: torch.Tensor | None, q: torch.Tensor, device: int, dtype: torch.dtype) -> tuple[torch.Tensor, int]:
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """A tensor that belongs to the stream of the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(out: torch.Tensor | None, q: torch.Tensor, device: int, dtype: torch.dtype, stream) -> tuple[torch.Tensor, int]:
     """The output tensor and its row stride."""
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=q.device)
-        return out, q.shape[1] * q.shape[2]
+        return _empty(q.shape, dtype, q.device, stream), q.shape[1] * q.shape[2]
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     return out, _rows(out, "out", device, dtype)
@@ -189,18 +197,18 @@ def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: 
         slots_at = _vector(slots, "slots", torch.int64, T, device)
         abi_cache = cache.as_abi()
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=dtype, device=q.device)
+        q_out = _empty((T, H, D), dtype, q.device, stream)
     elif q_out.shape != q.shape or q_out.dtype is not dtype or q_out.get_device() != device or \
             not q_out.is_contiguous():
         raise ValueError("q_out must be contiguous, with the shape, type and device of q")
     out = {"q": q_out}
     k_at = k_cached_at = v_cached_at = None
     if rotated_keys:
-        out["k"] = torch.empty((T, K, D), dtype=dtype, device=q.device)
+        out["k"] = _empty((T, K, D), dtype, q.device, stream)
         k_at = out["k"].data_ptr()
     if cached_values:
-        out["k_cached"] = torch.empty((T, K, D), dtype=dtype, device=q.device)
-        out["v_cached"] = torch.empty((T, K, D), dtype=dtype, device=q.device)
+        out["k_cached"] = _empty((T, K, D), dtype, q.device, stream)
+        out["v_cached"] = _empty((T, K, D), dtype, q.device, stream)
         k_cached_at, v_cached_at = out["k_cached"].data_ptr(), out["v_cached"].data_ptr()
     io = abi.MoeQkvAppendIO(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, T, H, K, D, code, R,
@@ -248,17 +256,13 @@ def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor,
     c = cache.as_abi()
     if cache.device != device or cache.head_dim != D:
         raise ValueError("the cache must be on q's device, with q's head size")
-    out, out_stride = _out(out, q, device, dtype)
-    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
+    out, out_stride = _out(out, q, device, dtype, stream)
+    lse = _empty((T, H), torch.float32, q.device, stream) if return_lse else None
     io = abi.MoeAttendPagedIO(q.data_ptr(), q_stride, out.data_ptr(), out_stride,
                               lse.data_ptr() if return_lse else None, page_table.data_ptr(), lengths_at, cu_at, B, T,
                               page_table.shape[1], max_rows, H, code, D ** -0.5 if scale is None else scale)
     n = _paged_workspace(device, T, max_rows, H, cache.num_kv_heads, D)
-    if stream is None:
-        workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
-    else:  # allocated on the stream that uses it, so that it is not handed out again before the call has run
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
-            workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+    workspace = _empty((n,), torch.uint8, q.device, stream)
     _on(device, "moe_attend_paged", abi.moe_attend_paged, io, c, workspace.data_ptr(), n, _status(d_status, device),
         _raw_stream(stream, device))
     return (out, lse) if return_lse else out
@@ -286,8 +290,8 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
         raise ValueError("cu_rows needs an entry for each sequence and one for the end")
     cu_rows_at = _vector(cu_rows, "cu_rows", torch.int32, n, device)
     cu_keys_at = _vector(cu_keys, "cu_keys", torch.int32, n, device)
-    out, out_stride = _out(out, q, device, dtype)
-    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
+    out, out_stride = _out(out, q, device, dtype, stream)
+    lse = _empty((T, H), torch.float32, q.device, stream) if return_lse else None
     io = abi.MoeAttendPromptIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
                                out.data_ptr(), out_stride, lse.data_ptr() if return_lse else None, cu_rows_at,
                                cu_keys_at, n - 1, T, N, H, K, D, code, int(causal),

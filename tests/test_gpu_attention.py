@@ -623,6 +623,25 @@ def test_append_in_a_graph_and_on_another_stream():
         assert w.any() and torch.equal(getattr(caches[0], part), w) and torch.equal(getattr(caches[2], part), w)
 
 
+def test_streams_as_handles():
+    """A raw handle, the legacy default stream's 0 among them; outputs belong to the call's stream."""
+    x = torch.randn(40, 6, 64, device="cuda", generator=torch.Generator("cuda").manual_seed(51)).bfloat16()
+    cu = ac.i32([0, 40])
+    c = ac.Cache(np.random.default_rng(52), [40], 1, 64, 16)
+    args = x[:, :4], x[:, 4:5], x[:, 5:]
+    want = (attention.qkv_append(*args)["q"], attention.attend_prompt(*args, cu, cu),
+            attention.attend_paged(args[0], c.cache, c.table, ac.i32([40]), cu))
+    lens = ac.i32([40])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for handle in (s.cuda_stream, 0, s):
+        got = (attention.qkv_append(*args, stream=handle)["q"], attention.attend_prompt(*args, cu, cu, stream=handle),
+               attention.attend_paged(args[0], c.cache, c.table, lens, cu, stream=handle))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
 def test_layer_prompt_then_verify_steps():
     """A layer as a server runs it: a prompt through append and prompt attention, then steps of six rows through
     append, paged attention and the MoE step; the paged rows equal prompt attention over the cached values."""
