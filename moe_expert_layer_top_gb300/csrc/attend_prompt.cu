@@ -73,7 +73,7 @@ struct PromptArgs {
 
 template <int D>
 struct Smem {
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of Q, K or V: D/64 parts of 128 rows x 128 bytes
   static constexpr int kBufs = D == 128 ? 2 : 3;  // S tiles in TMEM
   static constexpr uint32_t kColO = kBufs * kKeys;
@@ -84,7 +84,7 @@ struct Smem {
   uint64_t full[kStages];    // a K or V tile landed
   uint64_t empty[kStages];   // the MMAs that read it are done
   uint64_t tail;             // the last V tile is zeroed past the sequence's end
-  uint64_t s_full[2][2];     // S of (row tile, key tile j) complete, by j mod 2: its waiters see every phase
+  uint64_t s_full[2][kBufs]; // S of (row tile, key tile j) complete, by j mod kBufs: no phase ends unseen
   uint64_t p_full[kBufs];    // P of a step written (4 warps)
   uint64_t o_full[2];        // the row tile's last P V is in O
   uint64_t mma_done;
@@ -300,7 +300,7 @@ __device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32
 #pragma unroll
       for (int c = 0; c < 4; ++c)  // 16 values are 32 bytes: 2 in the address field
         mma_ss(d, qd + p * (kRows * 128 >> 4) + 2 * c, kd + p * (kKeys * 128 >> 4) + 2 * c, kDescS, (p | c) != 0);
-    mma_commit(&sm.s_full[kx][kj & 1]);
+    mma_commit(&sm.s_full[kx][kj % S::kBufs]);
     kfresh = kx == 1 || kj >= m;  // the last step that reads this K tile
     if (kfresh) {
       mma_commit(&sm.empty[kslot]);
@@ -405,7 +405,7 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
   for (int j = 0; j < w.tiles(x); ++j) {
     const int q = w.step(x, j), b = q % S::kBufs;
     const uint32_t ts = tmem + lanes + b * kKeys;
-    ok = __all_sync(0xFFFFFFFFu, wait(&sm.s_full[x][j & 1], (j >> 1) & 1, a.status));
+    ok = __all_sync(0xFFFFFFFFu, wait(&sm.s_full[x][j % S::kBufs], (j / S::kBufs) & 1, a.status));
     if (!ok) break;
     tmem_fence_after();
     const int lim = limit - j * kKeys;
@@ -556,8 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       mbar_init(&sm.tail, 1);
       for (int i = 0; i < S::kBufs; ++i) mbar_init(&sm.p_full[i], 4);
       for (int x = 0; x < 2; ++x) {
-        mbar_init(&sm.s_full[x][0], 1);
-        mbar_init(&sm.s_full[x][1], 1);
+        for (int i = 0; i < S::kBufs; ++i) mbar_init(&sm.s_full[x][i], 1);
         mbar_init(&sm.o_full[x], 1);
       }
       mbar_init(&sm.mma_done, 1);
