@@ -411,7 +411,8 @@ moe_status_t moe_forward_static_scratch(const moe_config_t *config, const moe_we
  *   codes  uint8 [num_pages][num_kv_heads][page_size][head_dim/2]
  *   scales uint8 [num_pages][num_kv_heads][page_size][head_dim/32]
  * 16-byte aligned device memory, owned by the caller. Tokens that were never
- * appended may hold anything: no call reads past a sequence's length. */
+ * appended may hold anything: what lies past a sequence's length has no effect.
+ * Sequences may share pages. num_pages * page_size * num_kv_heads < 2^32 - 1. */
 typedef struct moe_kv_cache {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
   int32_t num_pages;
@@ -486,9 +487,15 @@ moe_status_t moe_attend_paged_workspace(const moe_attend_paged_io_t *io, const m
  *   s_j = scale * (q . K_j),  out = sum_j softmax(s)_j V_j,  lse = log sum_j exp s_j
  * with K, V the values the cache stands for. A row that sees no key (L < n)
  * gets out = 0 and lse = -inf. Rows of q past cu_rows[num_seqs] are not
- * touched. workspace: 16-byte aligned device memory of at least the size
+ * touched. Sums and statistics are binary32, probabilities f16. A scale code of
+ * 0 counts as zero; of the values (and of a query row) parts below 2^-23 of the
+ * largest may lose bits. A NaN among the values of a key can reach earlier rows of
+ * its own sequence (their weight of it is 0, and 0 * NaN is NaN). A sequence with a
+ * page, length or offset out of range has unspecified results; the others have
+ * theirs. workspace: 16-byte aligned device memory of at least the size
  * above; its content before the call does not matter, and calls that may
- * overlap on the GPU need one each. */
+ * overlap on the GPU need one each. Results do not depend on timing: the same
+ * call gives the same bits. */
 moe_status_t moe_attend_paged(const moe_attend_paged_io_t *io, const moe_kv_cache_t *cache, void *workspace,
                               int64_t workspace_bytes, int32_t *d_status, void *cuda_stream);
 
@@ -510,8 +517,13 @@ typedef struct moe_attend_prompt_io {
 
 /* Attention over packed prompts, or over chunks of prompts with the keys that
  * precede them (m > n). Formula and empty rows as for moe_attend_paged. The
- * rows behind the last sequence are not touched. A NaN or infinity in a key or
- * value of one sequence never reaches another sequence. */
+ * rows behind the last sequence are not touched. Sums and statistics are
+ * binary32, probabilities are rounded to the inputs' type. A NaN or infinity in
+ * a key or value of one sequence never reaches another sequence, and one in a key
+ * that a row does not see never reaches the row; one in a value of a later key
+ * can reach earlier rows of its own sequence (0 * NaN is NaN). A sequence with an
+ * offset out of range gets no result; the others have theirs. out must not
+ * overlap the inputs. */
 moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_status, void *cuda_stream);
 
 /* Teardown: frees the plan's device memory and events, after a device-wide

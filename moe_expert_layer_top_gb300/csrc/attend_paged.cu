@@ -16,12 +16,17 @@
 //
 // Bound. A cached token and kv head is D + D/16 bytes against 4 D flops per row
 // and head: HBM for single tokens. Decoding the 4-bit codes is CUDA-core work
-// whatever multiplies them (2 D conversions a token), and keeps the
-// conversion pipe about 3/4 busy at the HBM rate. The codes go from shared
-// memory straight into the registers that the MMA reads: tcgen05 would need K
-// and V in 16 bits in shared memory first, and writing and reading those (for
-// D = 128: 48 KB per 128 tokens beside 17 KB of codes in and out) would make
-// shared memory the bound.
+// whatever multiplies them (2 D conversions a token, at half rate). 128 single
+// tokens of 4,000 to 16,000 (D = 128, 32 + 8 heads) take 243 us, 4.83 TB/s or 71 %
+// of the copy bandwidth: issue slots are 63 % busy, the ALU pipe 56 %. With 24
+// rows of a kv head (steps of six rows, 64 sequences of 1,024 to 5,120, 82 us) it
+// is neither: two warps a scheduler (the accumulators take the registers) wait on
+// fixed latencies; tensor pipe 36 %, issue 44 %, HBM 30 %. One token over 4,096:
+// 10.7 us, launches and the chain lookup - load - join.
+// The codes go from shared memory straight into the registers that the MMA
+// reads: tcgen05 would need K and V in 16 bits in shared memory first, and
+// writing and reading those (for D = 128: 48 KB per 128 tokens beside 17 KB of
+// codes in and out) would make shared memory the bound.
 //
 // Layout. Keys are the MMA's M (scores transposed: 16 keys x 8 rows), so a step
 // of 8 rows wastes nothing on padding. The order of a product's inner dimension
@@ -34,15 +39,19 @@
 // P moves from the first product's result layout to the second's operand
 // layout by movmatrix. Rows are (token, head) pairs of one kv head's group.
 //
-// Schedule. The work is a list of stages of 32 keys: sequence by sequence, kv head
-// by kv head, row block by row block. Every block takes an equal, contiguous
-// share of the list, so one long sequence spreads over all SMs and a batch of
-// ragged ones stays balanced. One warp copies stages into a ring of shared
-// memory (plain bulk copies; a page is contiguous per kv head); the other warps
-// take stages in turn and meet only where a (sequence, kv head, row block) ends.
-// What a block holds of an item it shares with other blocks goes to the
-// workspace; a second kernel, launched with programmatic dependent launch, joins
-// these in a fixed order. Results do not depend on timing.
+// Schedule. The work is a list of items (sequence, kv head, row block), each of
+// kOver units for its queries and its join and one for each stage of 32 keys.
+// Every block takes an equal, contiguous share of the units, so one long sequence
+// spreads over all SMs and a batch of ragged ones stays balanced. Within its share
+// of an item a block's warps take the stages in turn. Each copies its own ahead of
+// time into a ring of its own (cp.async), so they meet only where an item ends:
+// there the accumulators of all warps are joined through shared memory, which the
+// drained rings leave free. What a block holds of an item that it shares with
+// other blocks goes to the workspace; a second kernel, launched with programmatic
+// dependent launch, joins these in a fixed order. Results do not depend on timing.
+// Tried and slower: one copying warp with bulk copies (128 tokens 479 us against
+// 244), the next granule's scores between this one's exponentials and products
+// (six rows 94 us against 82), whose registers cost more than the wait.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -53,7 +62,9 @@ namespace moe {
 namespace {
 
 constexpr int kStageKeys = 32;
-constexpr int kOver = 16;                // what an item costs beside its stages, in units of one stage
+// What an item costs beside its stages, in units of one stage. 24 ragged sequences with D = 64: 25.5 us with 16, 41 with
+// 1; 64 steps of six rows 82 against 91. 10 and 24 are no better than 16.
+constexpr int kOver = 16;
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
 constexpr float kNone = 1e30f;           // minus the reference of a row that has seen no key
 constexpr int kCombineThreads = 256;
@@ -960,7 +971,14 @@ cudaError_t launch(const PagedArgs &a, int num_sms, cudaStream_t st) {
 }
 
 // The variants: as few row blocks of at most 32 rows as the usual rows of a
-// sequence need, and as few n-tiles a block as those leave.
+// sequence need, and as few n-tiles a block as those leave. 64 sequences of 1,024
+// to 5,120 (D = 128, groups of 4): 1 to 2 rows of a sequence take 49 us, 4 rows
+// 67 (109 in the variant of 32), 6 rows 82 (110 there), 8 rows 112.
+// Warps and blocks follow the registers: 16, 12 and 8 warps an SM with 128, 168
+// and 255 (D = 64: 12). 8 rows: blocks of 4 warps instead of 8 gain 3 % with 128
+// sequences (236 us against 243) and lose 7 % with one (11.4 against 10.7), whose
+// parts to join are then twice as many. 24 rows: 12 or 10 warps an SM spill or halve
+// the granules computed at once, 88 to 114 us against 65 (one long sequence) and 82.
 template <int D, class F>
 auto pick(int rows, F f) {
   const int blocks = (rows + 31) / 32, tiles = ((rows + blocks - 1) / blocks + 7) / 8;
