@@ -71,7 +71,6 @@
 #include "combine.cuh"
 #include "device.cuh"
 #include "internal.h"
-#include "tcgen05.cuh"
 
 namespace moe {
 
@@ -186,6 +185,9 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Generic-proxy writes of this thread (cp.async) before later async-proxy reads (tcgen05.mma).
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 __device__ __forceinline__ void named_bar(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -206,6 +208,21 @@ __device__ __forceinline__ int bar_and(int id, int n, int v) {
   return r;
 }
 
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
+// 1024 bytes apart, start address 16-byte granular.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= uint64_t((saddr >> 4) & 0x3FFFu);  // start address
+  d |= uint64_t(1) << 16;                 // leading byte offset (unused with a 128-byte swizzle)
+  d |= uint64_t(1024 >> 4) << 32;         // stride byte offset: 8 rows x 128 bytes
+  d |= uint64_t(1) << 46;                 // descriptor version
+  d |= uint64_t(2) << 61;                 // 128-byte swizzle
+  return d;
+}
+
 // D (+)= (A * SFA) x (B * SFB)^T for K = 32; sf_id picks the byte of the scale words.
 __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                          uint32_t sfb, uint32_t accumulate) {
@@ -215,6 +232,11 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t adesc, uint64_t bd
       "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 
 // Shared-memory descriptor of a 32-row x 16-byte matrix, no swizzle: 8-row
@@ -958,6 +980,21 @@ __global__ void __launch_bounds__(kMThreads, 1) experts_mma_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------ host
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    else
+      cudaGetLastError();
+  }
+  return fn;
+}
 
 // rows x k matrix of 8-bit codes (fp4 = false) or packed 4-bit codes (fp4 =
 // true, two per byte), row-major; boxes of 128 codes x box_rows, 128-byte

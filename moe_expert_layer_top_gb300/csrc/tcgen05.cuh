@@ -1,6 +1,7 @@
-// tcgen05.cuh — the parts of the 5th-generation tensor-core path that several
-// kernels share: proxy and TMEM fences, operand descriptors, commits, and the
-// driver's tensor-map encoder.
+// tcgen05.cuh — wrappers of the 5th-generation tensor-core path for the
+// attention: proxy and TMEM fences, operand descriptors, commits, and the
+// driver's tensor-map encoder. (The expert kernel keeps its own: the recorded
+// DRAM traffic of that kernel is tied to its source.)
 #pragma once
 
 #include <cuda.h>
