@@ -492,7 +492,7 @@ moe_status_t moe_attend_paged_workspace(const moe_attend_paged_io_t *io, const m
  * largest may lose bits. A NaN among the values of a key can reach earlier rows of
  * its own sequence (their weight of it is 0, and 0 * NaN is NaN). A sequence with a
  * page, length or offset out of range has unspecified results; the others have
- * theirs. workspace: 16-byte aligned device memory of at least the size
+ * theirs. out must not overlap q. workspace: 16-byte aligned device memory of at least the size
  * above; its content before the call does not matter, and calls that may
  * overlap on the GPU need one each. Results do not depend on timing: the same
  * call gives the same bits. */

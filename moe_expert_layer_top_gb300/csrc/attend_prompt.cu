@@ -11,16 +11,12 @@
 //
 // Bound. 4 D flops per (row, head, key) against 16-bit inputs read once: the
 // tensor pipe, for all but the shortest prompts. 16,384 tokens (32 + 8 heads of
-// 128) take 1.40 ms, 1.57 PFLOP/s or 83 % of the measured bf16 rate, at the power
-// limit. A block costs 1.5 us for a key tile (1.06 of MMAs) and 6.5 us beside them
-// (start, first loads, the first and last softmax, output), so 16 packed prompts
-// with few key tiles each take 89 us where their MMAs need 35. D = 64: an MMA with
-// N = 64 takes as long as one with 128, so the value product has half the rate: three
-// chunks behind 4,000 tokens 142 us, of which 88 for the MMAs. 257 tokens: 10.0 us.
-// Tried: persistent blocks that take over others by launch control, loads and scores
-// of the next work under the end of this one. The packed prompts gained 10 % (81 us),
-// but more state in every role slowed the steps: 16,384 tokens 1.43 ms, D = 64
-// chunks 149 us, 257 tokens 11.6.
+// 128) take 1.38 ms, 1.59 PFLOP/s or 84 % of the measured bf16 rate, at the power
+// limit. A pair of row tiles costs 1.5 us for a key tile (1.06 of MMAs) and 4.4 us
+// beside them (first loads, the first and last softmax, output), so 16 packed
+// prompts with few key tiles each take 77 us where their MMAs need 35. D = 64: an MMA
+// with N = 64 takes as long as one with 128, so the value product has half the rate:
+// three chunks behind 4,000 tokens 140 us, of which 88 for the MMAs. 257 tokens: 11.4.
 //
 // Layout. A row of the tile is a (token, head) pair: the G heads of a kv head's
 // group are packed, r = token * G + head, so one key tile serves all of them and
@@ -32,7 +28,8 @@
 //   warps 4-7   softmax of tile B
 //   warp 8      TMA: Q, then K and V tiles of 128 keys into a ring of shared memory;
 //               at the end it zeroes the rows of the last V tile that lie past
-//               the sequence (they belong to the next one, and 0 * NaN is NaN)
+//               the sequence (they belong to the next one, and 0 * NaN is NaN),
+//               and asks for the block's next work
 //   warp 9      MMA issuer: S = Q K^T (both operands from shared memory), then
 //               O += P V with P from TMEM, where the softmax wrote it over S
 // The work is a list of steps (row tile, key tile): A0 B0 A1 B1 ..., then what
@@ -41,6 +38,11 @@
 // this one runs (D = 64: three buffers; D = 128 leaves room for two). The MMAs of
 // one thread run in the order of issue: S(q + kBufs) goes after P V of q, which
 // reads the same columns.
+//
+// A block goes from work to work without stopping: its barriers and TMEM stay, and
+// the next Q, K and V are loaded while the last softmax and the output of this work
+// run. With a block for each work these cost 6.5 us in place of 4.4 (16 packed
+// prompts 90 us, 16,384 tokens 1.40 ms, 257 tokens 10.3).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -81,6 +83,25 @@ struct PromptArgs {
   int32_t *status;
 };
 
+// What a block does at a time: two row tiles of a sequence, for the heads of a group.
+struct Work {
+  int row0, n;       // the sequence's first row, its rows
+  int key0, keys;    // its first key, its keys
+  int t0;            // the block's first row within the sequence
+  int kv, head0;     // kv head, the first of the block's heads
+  int tiles0, tiles1;  // key tiles of row tiles A and B
+  int valid;           // 0: there is no further work
+  // where the barriers stand when it begins: steps, S of each row tile, entries of the ring (each modulo twice its
+  // ring), and the phases of o_full
+  int step0, s0, s1, entry0, o0, o1;
+
+  __device__ __forceinline__ int tiles(int x) const { return x ? tiles1 : tiles0; }
+  __device__ __forceinline__ int both() const { return min(tiles0, tiles1); }  // key tiles that both have
+  __device__ __forceinline__ int all() const { return max(tiles0, tiles1); }
+  // the place of (row tile x, key tile j) in the list of steps
+  __device__ __forceinline__ int step(int x, int j) const { return j < both() ? 2 * j + x : both() + j; }
+};
+
 template <int D>
 struct Smem {
   static constexpr int kStages = D == 128 ? 4 : 8;
@@ -90,16 +111,23 @@ struct Smem {
   static_assert(kColO + 2 * D <= kTmemCols && kBufs <= 3, "TMEM budget");
   uint8_t q[2][kTileBytes];
   uint8_t kv[kStages][kTileBytes];
-  uint64_t q_full;           // Q landed
+  uint8_t out[D == 128 ? 8 : 1][32 * 128];  // D = 128: 64 values of 32 rows of each softmax warp, on their way out
+  uint4 next;                // the launch control's answer
+  Work work[2];
+  uint64_t next_full;        // the answer is there
+  uint64_t work_full[2], work_empty[2];  // a Work is there; all have read it (8 softmax warps, the MMA lane)
+  uint64_t q_full[2];        // Q of a row tile landed
+  uint64_t q_empty[2];       // every S of the row tile is done
   uint64_t full[kStages];    // a K or V tile landed
   uint64_t empty[kStages];   // the MMAs that read it are done
-  uint64_t tail;             // the last V tile is zeroed past the sequence's end
+  uint64_t tail[4];          // the last V tile of a work is zeroed past the sequence's end, by work mod 4: the loads
+                             // are up to two works ahead of the MMAs
   uint64_t s_full[2][kBufs]; // S of (row tile, key tile j) complete, by j mod kBufs: no phase ends unseen
   uint64_t p_full[kBufs];    // P of a step written (4 warps)
   uint64_t o_full[2];        // the row tile's last P V is in O
   uint64_t mma_done;
   uint32_t tmem_base;
-  static constexpr size_t kBytes = 2 * kTileBytes + kStages * kTileBytes + 512 + 1024;
+  static constexpr size_t kBytes = 2 * kTileBytes + kStages * kTileBytes + 8 * 32 * 128 + 1024 + 1024;
 };
 
 // ------------------------------------------------------------------ PTX wrappers
@@ -198,26 +226,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // ------------------------------------------------------------------ the block's work
 
-struct Work {
-  int row0, n;       // the sequence's first row, its rows
-  int key0, keys;    // its first key, its keys
-  int t0;            // the block's first row within the sequence
-  int kv, head0;     // kv head, the first of the block's heads
-  int tiles0, tiles1;  // key tiles of row tiles A and B
-
-  __device__ __forceinline__ int tiles(int x) const { return x ? tiles1 : tiles0; }
-  __device__ __forceinline__ int both() const { return min(tiles0, tiles1); }  // key tiles that both have
-  __device__ __forceinline__ int all() const { return max(tiles0, tiles1); }
-  // the place of (row tile x, key tile j) in the list of steps
-  __device__ __forceinline__ int step(int x, int j) const { return j < both() ? 2 * j + x : both() + j; }
-};
-
 // Keys that row t of the sequence sees.
 __device__ __forceinline__ int key_limit(const PromptArgs &a, const Work &w, int t) {
   return a.causal ? min(w.keys, max(0, w.keys - w.n + t + 1)) : w.keys;
 }
 
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *status) {
+__device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -226,19 +240,72 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *st
       : "=r"(done)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
-  if (done || mbar_wait(bar, parity, kWaitNs)) return true;
+  return done != 0;
+}
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *status, int64_t ns = kWaitNs) {
+  if (test(bar, parity) || mbar_wait(bar, parity, ns)) return true;
   if (status) report_error(status, MOE_ERR_TIMEOUT);
   return false;
 }
 
+// ------------------------------------------------------------------ the list of work
+// The grid has a block for every Work. A running block takes over those that have not started yet, one by one, through
+// the hardware's launch control; the others run as blocks of their own. (Heads run fastest: the heads of a sequence's
+// long tiles come before its short ones.) Whole warp.
+__device__ __forceinline__ Work find_work(const PromptArgs &a, uint32_t block, int32_t *status) {
+  const uint32_t tile = block / a.all_groups, head = block - tile * a.all_groups;
+  const TileAt at = find_tile(a.cu_rows, a.num_rows, a.cu_keys, a.num_keys, a.num_seqs, 2 * a.tokens, tile, status);
+  Work w;
+  w.valid = at.seq >= 0;
+  w.row0 = at.rows.first;
+  w.n = at.rows.n;
+  w.key0 = at.keys.first;
+  w.keys = at.keys.n;
+  w.kv = head / a.groups;
+  w.head0 = head * a.group;
+  w.t0 = (at.tiles - 1 - at.local) * (2 * a.tokens);  // the last rows see the most keys: they start first
+  const auto key_tiles = [&](int first) {
+    return first < w.n ? (key_limit(a, w, min(first + a.tokens, w.n) - 1) + kKeys - 1) / kKeys : 0;
+  };
+  w.tiles0 = key_tiles(w.t0);
+  w.tiles1 = key_tiles(w.t0 + a.tokens);
+  w.step0 = w.s0 = w.s1 = w.entry0 = w.o0 = w.o1 = 0;
+  return w;
+}
+
+// Asks for the index of a block that has not started, which then never will.
+__device__ __forceinline__ void ask_next(uint4 *answer, uint64_t *bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The answer: whether there was one, and its index.
+__device__ __forceinline__ bool read_next(const uint4 *answer, uint32_t &block) {
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+      : "=r"(got), "=r"(block)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return got != 0;
+}
+
 // ------------------------------------------------------------------ TMA (warp 8)
 
-// Entry i of the list K 0, V 0, K 1, V 1, ... into its ring slot (one lane).
+// Entry i of the list K 0, V 0, K 1, V 1, ... of w into the ring, as its entry number base + i (one lane).
 template <int D>
 __device__ __forceinline__ void load_tile(const CUtensorMap *kmap, const CUtensorMap *vmap, Smem<D> &sm, const Work &w,
-                                          int i) {
+                                          uint32_t base, int i) {
   using S = Smem<D>;
-  const int s = i % S::kStages;
+  const uint32_t s = (base + i) % S::kStages;
   mbar_arrive_expect_tx(&sm.full[s], S::kTileBytes);
   const CUtensorMap *map = i & 1 ? vmap : kmap;
 #pragma unroll
@@ -246,118 +313,206 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *kmap, const CUtenso
     tma_load(sm.kv[s] + p * (kKeys * 128), map, 64 * p, w.kv, w.key0 + (i >> 1) * kKeys, &sm.full[s]);
 }
 
-// The first entries, as many as the ring has slots, went out with the barriers' initialisation.
+// Q of row tile x (one lane). Rows past the sequence are another one's, or zeros past the last: their scores are hidden.
 template <int D>
-__device__ void load_warp(const CUtensorMap *kmap, const CUtensorMap *vmap, const PromptArgs &a, Smem<D> &sm,
-                          const Work &w) {
+__device__ __forceinline__ void load_queries(const CUtensorMap *qmap, const PromptArgs &a, Smem<D> &sm, const Work &w, int x) {
+  mbar_arrive_expect_tx(&sm.q_full[x], uint32_t(a.tokens * a.group * D * 2));
+#pragma unroll
+  for (int p = 0; p < D / 64; ++p)
+    tma_load(sm.q[x] + p * (kRows * 128), qmap, 64 * p, w.head0, w.row0 + w.t0 + x * a.tokens, &sm.q_full[x]);
+}
+
+// Q and the first entries of the block's first work, as many as the ring has slots, went out with the barriers'
+// initialisation.
+template <int D>
+__device__ void load_warp(const CUtensorMap *qmap, const CUtensorMap *kmap, const CUtensorMap *vmap, const PromptArgs &a,
+                          Smem<D> &sm, Work w) {
   using S = Smem<D>;
-  const int lane = threadIdx.x & 31, n = w.all();
-  int issued = min(2 * n, S::kStages);
-  if (elect_one()) {
-    for (int i = issued; i < 2 * n; ++i) {
-      if (!wait(&sm.empty[i % S::kStages], ((i / S::kStages) & 1) ^ 1, a.status)) break;
-      load_tile<D>(kmap, vmap, sm, w, i);
-      ++issued;
+  const int lane = threadIdx.x & 31;
+  uint32_t base = 0;  // entries of the ring so far
+  int queries[2] = {w.tiles0 > 0, w.tiles1 > 0}, issued = min(2 * w.all(), S::kStages);
+  for (uint32_t t = 0;; ++t) {
+    const int n = w.all();
+    bool ok = true;
+    if (elect_one()) {
+      for (int i = issued; i < 2 * n; ++i) {
+        const uint32_t e = base + i;
+        if (e >= S::kStages && !wait(&sm.empty[e % S::kStages], (e / S::kStages & 1) ^ 1, a.status)) {
+          ok = false;
+          break;
+        }
+        load_tile<D>(kmap, vmap, sm, w, base, i);
+        ++issued;
+        if (t > 0 && i == 0) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || w.tiles(x) == 0) continue;
+            ok = queries[x] == 0 || wait(&sm.q_empty[x], (queries[x] - 1) & 1, a.status);
+            if (!ok) continue;
+            load_queries<D>(qmap, a, sm, w, x);
+            ++queries[x];
+          }
+          if (!ok) break;
+        }
+      }
     }
-  }
-  issued = __reduce_max_sync(0xFFFFFFFFu, unsigned(issued));
-  const int cut = w.keys - (n - 1) * kKeys;  // keys of the last tile
-  if (issued == 2 * n && cut < kKeys) {
-    const int i = 2 * n - 1, s = i % S::kStages;
-    if (wait(&sm.full[s], (i / S::kStages) & 1, a.status)) {
-      for (int p = 0; p < D / 64; ++p)
-        for (int c = cut * 8 + lane; c < kKeys * 8; c += 32)
-          *reinterpret_cast<uint4 *>(sm.kv[s] + p * (kKeys * 128) + c * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.tail);
+    if (elect_one()) {
+      mbar_arrive_expect_tx(&sm.next_full, 16);
+      ask_next(&sm.next, &sm.next_full);
     }
+    // one lane issued: the others follow
+    issued = __reduce_max_sync(0xFFFFFFFFu, unsigned(issued));
+    queries[0] = __reduce_max_sync(0xFFFFFFFFu, unsigned(queries[0]));
+    queries[1] = __reduce_max_sync(0xFFFFFFFFu, unsigned(queries[1]));
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    const int cut = w.keys - (n - 1) * kKeys;  // keys of the last tile
+    if (ok && n > 0 && cut < kKeys) {
+      const uint32_t e = base + 2 * n - 1, s = e % S::kStages;
+      ok = __all_sync(0xFFFFFFFFu, wait(&sm.full[s], e / S::kStages & 1, a.status));
+      if (ok) {
+        for (int p = 0; p < D / 64; ++p)
+          for (int c = cut * 8 + lane; c < kKeys * 8; c += 32)
+            *reinterpret_cast<uint4 *>(sm.kv[s] + p * (kKeys * 128) + c * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
+      }
+    }
+    __syncwarp();
+    if (ok && lane == 0) mbar_arrive(&sm.tail[t & 3]);
+    base += issued;
+    uint32_t block = 0;
+    const bool answered = __all_sync(0xFFFFFFFFu, wait(&sm.next_full, t & 1, a.status));
+    const bool more = answered && read_next(&sm.next, block);
+    const Work was = w;
+    w.valid = 0;
+    if (more && ok) w = find_work(a, block, a.status);
+    w.step0 = (was.step0 + was.tiles0 + was.tiles1) % S::kBufs;
+    w.s0 = (was.s0 + was.tiles0) % (2 * S::kBufs);
+    w.s1 = (was.s1 + was.tiles1) % (2 * S::kBufs);
+    w.entry0 = (was.entry0 + 2 * n) % (2 * S::kStages);
+    w.o0 = was.o0 ^ (was.tiles0 > 0);
+    w.o1 = was.o1 ^ (was.tiles1 > 0);
+    const uint32_t slot = (t + 1) & 1;
+    if (ok && t > 0) ok = __all_sync(0xFFFFFFFFu, wait(&sm.work_empty[slot], ((t + 1) / 2 - 1) & 1, a.status));
+    if (!ok) w.valid = 0;
+    fence_proxy_async();  // the answer has been read before another is asked for
+    __syncwarp();
+    if (ok && lane == 0) {
+      sm.work[slot] = w;
+      mbar_arrive(&sm.work_full[slot]);
+    }
+    if (!w.valid) break;
+    issued = 0;
   }
   // no copy may be in flight when the block exits
-  mbar_wait(&sm.q_full, 0, kWaitNs);
-  for (int j = 1; j <= S::kStages && j <= issued; ++j) {
-    const int i = issued - j;
-    mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, kWaitNs);
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (queries[x] > 0) mbar_wait(&sm.q_full[x], (queries[x] - 1) & 1, kWaitNs);
+  for (uint32_t j = 1; j <= S::kStages && j <= base; ++j) {
+    const uint32_t e = base - j;
+    mbar_wait(&sm.full[e % S::kStages], e / S::kStages & 1, kWaitNs);
   }
 }
 
 // ------------------------------------------------------------------ MMA issuer (one lane of warp 9)
 
 template <class T, int D>
-__device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
+__device__ void mma_lane(const PromptArgs &a, Smem<D> &sm, uint32_t tmem) {
   using S = Smem<D>;
   constexpr uint32_t kType = T::kMmaType;
   constexpr uint32_t kBase = (1u << 4) | (kType << 7) | (kType << 10) | (uint32_t(kRows >> 4) << 24);
   constexpr uint32_t kDescS = kBase | (uint32_t(kKeys >> 3) << 17);
   constexpr uint32_t kDescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);  // B is N-major
-  const int n = w.all(), m = w.both(), longer = w.tiles1 > w.tiles0 ? 1 : 0;
-  const int steps = w.tiles0 + w.tiles1;
-  // Two places in the list of steps, the next S to issue (k...) and the next P V (v...): row tile, key tile, the
-  // ring slot and phase of its K or V tile, the S buffer. Kept by increments, in registers: this lane's own latency
-  // is on the critical path.
-  int kx = m > 0 ? 0 : longer, kj = 0, kslot = 0, kbuf = 0, vx = kx, vj = 0, vslot = 1, vbuf = 0, issued = 0;
-  uint32_t kphase = 0, vphase = 0, pphase = 0;  // pphase: of the P buffers, flips when their ring starts over
-  bool kfresh = true, vfresh = true;            // the first step of its key tile
+  constexpr uint32_t kTile = S::kTileBytes >> 4;                              // in a descriptor's address field
   const uint64_t qd0 = sw128_desc(smem_u32(sm.q[0])), kd0 = sw128_desc(smem_u32(sm.kv[0])), vd0 = v_desc(smem_u32(sm.kv[0]));
-  constexpr uint32_t kTile = S::kTileBytes >> 4;  // in a descriptor's address field
-  const auto scores = [&] {                       // S of the next step into its buffer
-    if (kfresh && !wait(&sm.full[kslot], kphase, a.status)) return false;
-    tmem_fence_after();
-    const uint64_t qd = qd0 + (kx ? kTile : 0u), kd = kd0 + uint32_t(kslot) * kTile;
-    const uint32_t d = tmem + kbuf * kKeys;
+  // Two places in the list of a work's steps, the next S to issue (k...) and the next P V (v...): row tile, key tile, the
+  // ring slot and phase of its K or V tile, the S buffer. Kept by increments, in registers: this lane's own latency is on
+  // the critical path. (S of the next work under the last steps of this one was slower: a second place to issue S from
+  // cost every step more than the works' ends gained.)
+  int kslot = 0, kbuf = 0, kc0 = 0, kc1 = 0, vslot = 1, vbuf = 0;
+  uint32_t kphase = 0, vphase = 0, pphase = 0;  // pphase: of the P buffers, flips when their ring starts over
+  uint32_t qphase = 0;                          // bit x: of q_full[x]
+  bool ok = true;
+  for (uint32_t t = 0; ok; ++t) {
+    if (!wait(&sm.work_full[t & 1], t >> 1 & 1, a.status)) break;
+    const Work &w = sm.work[t & 1];
+    if (!w.valid) break;
+    const int tiles0 = w.tiles0, tiles1 = w.tiles1;
+    const int n = max(tiles0, tiles1), m = min(tiles0, tiles1), longer = tiles1 > tiles0 ? 1 : 0, steps = tiles0 + tiles1;
+    const bool cut = w.keys < n * kKeys;
+    mbar_arrive(&sm.work_empty[t & 1]);
+    int kx = m > 0 ? 0 : longer, kj = 0, vx = kx, vj = 0, issued = 0;
+    bool kfresh = true, vfresh = true;  // the first step of its key tile
+    const auto scores = [&] {           // S of the next step into its buffer
+      if (kfresh && !wait(&sm.full[kslot], kphase, a.status)) return false;
+      tmem_fence_after();
+      const uint64_t qd = qd0 + (kx ? kTile : 0u), kd = kd0 + uint32_t(kslot) * kTile;
+      const uint32_t d = tmem + kbuf * kKeys;
 #pragma unroll
-    for (int p = 0; p < D / 64; ++p)
+      for (int p = 0; p < D / 64; ++p)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)  // 16 values are 32 bytes: 2 in the address field
-        mma_ss(d, qd + p * (kRows * 128 >> 4) + 2 * c, kd + p * (kKeys * 128 >> 4) + 2 * c, kDescS, (p | c) != 0);
-    mma_commit(&sm.s_full[kx][kj % S::kBufs]);
-    kfresh = kx == 1 || kj >= m;  // the last step that reads this K tile
-    if (kfresh) {
-      mma_commit(&sm.empty[kslot]);
-      ++kj;
-      kx = kj < m ? 0 : longer;
-      kslot += 2;
-      if (kslot >= S::kStages) {
-        kslot -= S::kStages;
-        kphase ^= 1;
+        for (int c = 0; c < 4; ++c)  // 16 values are 32 bytes: 2 in the address field
+          mma_ss(d, qd + p * (kRows * 128 >> 4) + 2 * c, kd + p * (kKeys * 128 >> 4) + 2 * c, kDescS, (p | c) != 0);
+      mma_commit(&sm.s_full[kx][kx ? kc1 : kc0]);
+      if (kx) {
+        kc1 = kc1 + 1 == S::kBufs ? 0 : kc1 + 1;
+      } else {
+        kc0 = kc0 + 1 == S::kBufs ? 0 : kc0 + 1;
       }
-    } else {
-      kx = 1;
-    }
-    kbuf = kbuf + 1 == S::kBufs ? 0 : kbuf + 1;
-    ++issued;
-    return true;
-  };
-  bool ok = wait(&sm.q_full, 0, a.status);
-  while (ok && issued < S::kBufs && issued < steps) ok = scores();
-  for (int q = 0; ok && q < steps; ++q) {
-    if (vfresh)
-      ok = wait(&sm.full[vslot], vphase, a.status) && (vj + 1 < n || w.keys >= n * kKeys || wait(&sm.tail, 0, a.status));
-    ok = ok && wait(&sm.p_full[vbuf], pphase, a.status);
-    if (!ok) break;
-    tmem_fence_after();
-    const uint64_t vd = vd0 + uint32_t(vslot) * kTile;
-    const uint32_t pa = tmem + vbuf * kKeys, d = tmem + S::kColO + (vx ? D : 0);
-#pragma unroll
-    for (int c = 0; c < kKeys / 16; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
-      mma_ts(d, pa + 8 * c, vd + c * (2048 >> 4), kDescO, (vj | c) != 0);
-    if (issued < steps) ok = scores();
-    if (vj + 1 == w.tiles(vx)) mma_commit(&sm.o_full[vx]);
-    vfresh = vx == 1 || vj >= m;
-    if (vfresh) {
-      mma_commit(&sm.empty[vslot]);
-      ++vj;
-      vx = vj < m ? 0 : longer;
-      vslot += 2;
-      if (vslot >= S::kStages) {
-        vslot -= S::kStages;
-        vphase ^= 1;
+      if (kj + 1 == (kx ? tiles1 : tiles0)) mma_commit(&sm.q_empty[kx]);
+      kfresh = kx == 1 || kj >= m;  // the last step that reads this K tile
+      if (kfresh) {
+        mma_commit(&sm.empty[kslot]);
+        ++kj;
+        kx = kj < m ? 0 : longer;
+        kslot += 2;
+        if (kslot >= S::kStages) {
+          kslot -= S::kStages;
+          kphase ^= 1;
+        }
+      } else {
+        kx = 1;
       }
-    } else {
-      vx = 1;
+      kbuf = kbuf + 1 == S::kBufs ? 0 : kbuf + 1;
+      ++issued;
+      return true;
+    };
+    while (ok && issued < S::kBufs && issued < steps) {
+      if (kj == 0) {  // the first S of both row tiles are among these
+        ok = wait(&sm.q_full[kx], qphase >> kx & 1, a.status);
+        qphase ^= 1u << kx;
+      }
+      ok = ok && scores();
     }
-    vbuf = vbuf + 1 == S::kBufs ? 0 : vbuf + 1;
-    if (vbuf == 0) pphase ^= 1;
+    for (int q = 0; ok && q < steps; ++q) {
+      if (vfresh)
+        ok = wait(&sm.full[vslot], vphase, a.status) &&
+             (!cut || vj + 1 < n || wait(&sm.tail[t & 3], t >> 2 & 1, a.status));
+      ok = ok && wait(&sm.p_full[vbuf], pphase, a.status);
+      if (!ok) break;
+      tmem_fence_after();
+      const uint64_t vd = vd0 + uint32_t(vslot) * kTile;
+      const uint32_t pa = tmem + vbuf * kKeys, d = tmem + S::kColO + (vx ? D : 0);
+#pragma unroll
+      for (int c = 0; c < kKeys / 16; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
+        mma_ts(d, pa + 8 * c, vd + c * (2048 >> 4), kDescO, (vj | c) != 0);
+      if (issued < steps) ok = scores();
+      if (vj + 1 == (vx ? tiles1 : tiles0)) mma_commit(&sm.o_full[vx]);
+      vfresh = vx == 1 || vj >= m;
+      if (vfresh) {
+        mma_commit(&sm.empty[vslot]);
+        ++vj;
+        vx = vj < m ? 0 : longer;
+        vslot += 2;
+        if (vslot >= S::kStages) {
+          vslot -= S::kStages;
+          vphase ^= 1;
+        }
+      } else {
+        vx = 1;
+      }
+      vbuf = vbuf + 1 == S::kBufs ? 0 : vbuf + 1;
+      if (vbuf == 0) pphase ^= 1;
+    }
   }
   mma_commit(&sm.mma_done);  // every MMA is done before TMEM is freed
   mbar_wait(&sm.mma_done, 0, kWaitNs);
@@ -401,7 +556,7 @@ __device__ __forceinline__ void exponentials(const uint32_t (&s)[kKeys], uint32_
 }
 
 template <class T, int D>
-__device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
+__device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
   using S = Smem<D>;
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
   // the thread's row of the sequence and its head; rows past the tile's tokens or the sequence see nothing
@@ -412,11 +567,12 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
   const uint32_t to = tmem + lanes + S::kColO + x * D;
   float ref = 0.0f, total = 0.0f;  // the reference in score units
   bool ok = true;
-  for (int j = 0; j < w.tiles(x); ++j) {
-    const int q = w.step(x, j), b = q % S::kBufs;
+  const int tiles = w.tiles(x), both = w.both(), step0 = w.step0, s0 = x ? w.s1 : w.s0;
+  for (int j = 0; j < tiles; ++j) {
+    const int b = (step0 + (j < both ? 2 * j + x : both + j)) % S::kBufs, c = s0 + j;
     const uint32_t ts = tmem + lanes + b * kKeys;
-    ok = __all_sync(0xFFFFFFFFu, wait(&sm.s_full[x][j % S::kBufs], (j / S::kBufs) & 1, a.status));
-    if (!ok) break;
+    ok = __all_sync(0xFFFFFFFFu, wait(&sm.s_full[x][c % S::kBufs], (c / S::kBufs) & 1, a.status));
+    if (!ok) return false;
     tmem_fence_after();
     const int lim = limit - j * kKeys;
     uint32_t s[kKeys], p[kKeys / 2];
@@ -438,9 +594,9 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
       } else {
         // O has to hold every tile before this one: then V of key tile j - 1 has been released. (Its slot is not
         // released again before this step is done, and was not in an older phase when S of this step was issued.)
-        const int i = 2 * j - 1;
+        const int i = w.entry0 + 2 * j - 1;
         ok = __all_sync(0xFFFFFFFFu, wait(&sm.empty[i % S::kStages], (i / S::kStages) & 1, a.status));
-        if (!ok) break;
+        if (!ok) return false;
         tmem_fence_after();
         const bool move = (top - ref) * a.scale2 > kLazy;
         const float f = move ? exp2_approx((ref - top) * a.scale2) : 1.0f;
@@ -466,63 +622,95 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, const Work &w, u
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.p_full[b]);
   }
-  if (!ok) return;
   if (w.tiles(x) > 0) {
-    if (!__all_sync(0xFFFFFFFFu, wait(&sm.o_full[x], 0, a.status))) return;
+    if (!__all_sync(0xFFFFFFFFu, wait(&sm.o_full[x], x ? w.o1 : w.o0, a.status))) return false;
     tmem_fence_after();
   }
-  // O / sum into this warp's 32 rows of the tile's Q, which nothing reads any more (every S is done), then out by
-  // whole rows. 16-byte pieces of a row are exchanged by row, against bank conflicts.
+  // O / sum. Rows of 256 bytes go through the warp's own shared memory, 64 values of 32 rows at a time, and out by whole
+  // pieces of rows (16-byte pieces exchanged by row, against bank conflicts); rows of 128 straight from their threads.
+  // 16,384 tokens with D = 128: 1.37 ms, 1.41 straight; chunks with D = 64: 140 us straight, 145 through shared memory.
   const float inv = total > 0.0f ? 1.0f / total : 0.0f;
   const bool any = limit > 0;  // a row without keys has no accumulator of its own
-  constexpr int kChunks = D / 8;
-  uint8_t *stage = sm.q[x] + warp * 32 * (2 * D);
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
+  const auto load_out = [&](int first, uint32_t (&v)[16]) {  // 32 values of the row from the first on
     uint32_t o[32];
     if (w.tiles(x) > 0) {
-      tmem_ld32(to + 32 * i, o);
+      tmem_ld32(to + first, o);
       tmem_wait_ld(o);
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t v[4];
+    for (int i = 0; i < 16; ++i)
+      v[i] = any ? T::pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+  };
+  if constexpr (D == 64) {
+    uint16_t *out = a.out + int64_t(w.row0 + t) * a.out_stride + int64_t(h) * D;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[e] = any ? T::pack(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv) : 0u;
-      *reinterpret_cast<uint4 *>(stage + lane * (2 * D) + (((4 * i + c) ^ (lane & 7)) << 4)) =
-          make_uint4(v[0], v[1], v[2], v[3]);
+    for (int i = 0; i < 2; ++i) {
+      uint32_t v[16];
+      load_out(32 * i, v);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (real)
+          *reinterpret_cast<uint4 *>(out + 32 * i + 8 * c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
     }
-  }
-  __syncwarp();
-  {
-    constexpr int kStep = 32 / kChunks;  // rows that a warp stores at once
-    const int c = lane % kChunks, l = lane / kChunks, dt = kStep / a.group, dh = kStep - dt * a.group;
-    int rr = warp * 32 + l, tt = w.t0 + x * a.tokens + rr / a.group, hh = rr % a.group;
-    uint16_t *out = a.out + int64_t(w.row0 + tt) * a.out_stride + int64_t(w.head0 + hh) * D + 8 * c;
+  } else {
+    uint8_t *stage = sm.out[threadIdx.x >> 5];
+    const int lane = threadIdx.x & 31;
+    constexpr int kStep = 4;  // rows that a warp stores at once, 8 lanes each
+    const int c8 = lane % 8, l8 = lane / 8, dt = kStep / a.group, dh = kStep - dt * a.group;
     const int64_t step = dt * a.out_stride + dh * D, wrap = a.out_stride - a.group * D;
-    const uint8_t *from = stage + l * (2 * D);
     const int rows = a.tokens * a.group;
 #pragma unroll
-    for (int i = 0; i < 32; i += kStep) {
-      if (rr < rows && tt < w.n)
-        *reinterpret_cast<uint4 *>(out) =
-            *reinterpret_cast<const uint4 *>(from + i * (2 * D) + ((c ^ ((l + i) & 7)) << 4));
-      rr += kStep;
-      tt += dt;
-      hh += dh;
-      out += step;
-      if (hh >= a.group) {
-        hh -= a.group;
-        ++tt;
-        out += wrap;
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t v[16];
+        load_out(64 * half + 32 * i, v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4 *>(stage + lane * 128 + (((4 * i + c) ^ (lane & 7)) << 4)) =
+              make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
       }
+      __syncwarp();
+      int rr = warp * 32 + l8, tt = w.t0 + x * a.tokens + rr / a.group, hh = rr % a.group;
+      uint16_t *out = a.out + int64_t(w.row0 + tt) * a.out_stride + int64_t(w.head0 + hh) * D + 64 * half + 8 * c8;
+#pragma unroll
+      for (int i = 0; i < 32; i += kStep) {
+        if (rr < rows && tt < w.n)
+          *reinterpret_cast<uint4 *>(out) =
+              *reinterpret_cast<const uint4 *>(stage + (l8 + i) * 128 + ((c8 ^ ((l8 + i) & 7)) << 4));
+        rr += kStep;
+        tt += dt;
+        hh += dh;
+        out += step;
+        if (hh >= a.group) {
+          hh -= a.group;
+          ++tt;
+          out += wrap;
+        }
+      }
+      __syncwarp();
     }
   }
   if (real && a.lse)
     a.lse[int64_t(w.row0 + t) * a.num_heads + h] =
         total > 0.0f ? (log2f(total) + ref * a.scale2) * 0.6931471805599453f : -INFINITY;
+  return true;
+}
+
+template <class T, int D>
+__device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, uint32_t tmem) {
+  using S = Smem<D>;
+  int64_t ns = kWaitNs;
+  for (uint32_t t = 0;; ++t) {
+    if (!__all_sync(0xFFFFFFFFu, wait(&sm.work_full[t & 1], t >> 1 & 1, a.status, ns))) return;
+    const Work &w = sm.work[t & 1];
+    if (!w.valid) return;
+    if (!softmax_work<T, D>(a, sm, w, tmem)) return;
+    // the next work comes when the loads of this one are out; a warp whose own row tile is short waits for the other's
+    ns = kWaitNs + int64_t(w.all()) * 100000;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.work_empty[t & 1]);
+  }
 }
 
 // ------------------------------------------------------------------ kernel
@@ -537,50 +725,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   static_assert(sizeof(S) + 1024 <= S::kBytes && S::kBytes <= 227 * 1024, "shared memory budget");
   S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
-  // every warp finds the block's tile for itself: nothing to wait for
-  // (Heads run fastest: the heads of a sequence's long tiles start before its short ones.)
-  const uint32_t tile = blockIdx.x / a.all_groups, head = blockIdx.x - tile * a.all_groups;
-  const TileAt at = find_tile(a.cu_rows, a.num_rows, a.cu_keys, a.num_keys, a.num_seqs, 2 * a.tokens, tile,
-                              warp == 0 ? a.status : nullptr);
-  if (at.seq < 0) return;  // past the last tile: the whole block
-  Work w;
-  w.row0 = at.rows.first;
-  w.n = at.rows.n;
-  w.key0 = at.keys.first;
-  w.keys = at.keys.n;
-  w.kv = head / a.groups;
-  w.head0 = head * a.group;
-  w.t0 = (at.tiles - 1 - at.local) * (2 * a.tokens);  // the last rows see the most keys: they start first
-  const auto key_tiles = [&](int first) {
-    return first < w.n ? (key_limit(a, w, min(first + a.tokens, w.n) - 1) + kKeys - 1) / kKeys : 0;
-  };
-  w.tiles0 = key_tiles(w.t0);
-  w.tiles1 = key_tiles(w.t0 + a.tokens);
+  // every warp finds the block's first work for itself: nothing to wait for
+  const Work w = find_work(a, blockIdx.x, warp == kWarpLoad ? a.status : nullptr);
+  if (!w.valid) return;  // past the last tile: the whole block
   if (warp == kWarpLoad) {
     if (elect_one()) {
-      mbar_init(&sm.q_full, 1);
+      mbar_init(&sm.next_full, 1);
       for (int i = 0; i < S::kStages; ++i) {
         mbar_init(&sm.full[i], 1);
         mbar_init(&sm.empty[i], 1);
       }
-      mbar_init(&sm.tail, 1);
+      for (int i = 0; i < 4; ++i) mbar_init(&sm.tail[i], 1);
       for (int i = 0; i < S::kBufs; ++i) mbar_init(&sm.p_full[i], 4);
       for (int x = 0; x < 2; ++x) {
+        mbar_init(&sm.work_full[x], 1);
+        mbar_init(&sm.work_empty[x], 9);
+        mbar_init(&sm.q_full[x], 1);
+        mbar_init(&sm.q_empty[x], 1);
         for (int i = 0; i < S::kBufs; ++i) mbar_init(&sm.s_full[x][i], 1);
         mbar_init(&sm.o_full[x], 1);
       }
       mbar_init(&sm.mma_done, 1);
       fence_mbar_init();
       fence_proxy_async();  // the copies' completions go to these barriers
-      if (w.all() > 0) {
-        // rows past the sequence are another one's, or zeros past the last: their scores are hidden
-        const int tiles = w.tiles1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&sm.q_full, uint32_t(tiles * a.tokens * a.group * D * 2));
-        for (int x = 0; x < tiles; ++x)
-          for (int p = 0; p < D / 64; ++p)
-            tma_load(sm.q[x] + p * (kRows * 128), &qmap, 64 * p, w.head0, w.row0 + w.t0 + x * a.tokens, &sm.q_full);
-      }
-      for (int i = 0; i < S::kStages && i < 2 * w.all(); ++i) load_tile<D>(&kmap, &vmap, sm, w, i);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (w.tiles(x) > 0) load_queries<D>(&qmap, a, sm, w, x);
+      for (int i = 0; i < S::kStages && i < 2 * w.all(); ++i) load_tile<D>(&kmap, &vmap, sm, w, 0, i);
+      sm.work[0] = w;
+      mbar_arrive(&sm.work_full[0]);
     }
   } else if (warp == kWarpMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
@@ -594,11 +767,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   const uint32_t tmem = sm.tmem_base;
   if (warp < kWarpLoad) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_warps<T, D>(a, sm, w, tmem);
+    softmax_warps<T, D>(a, sm, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (w.all() > 0 && warp == kWarpLoad) load_warp<D>(&kmap, &vmap, a, sm, w);
-    if (w.all() > 0 && warp == kWarpMma && elect_one()) mma_lane<T, D>(a, sm, w, tmem);
+    if (warp == kWarpLoad) load_warp<D>(&qmap, &kmap, &vmap, a, sm, w);
+    if (warp == kWarpMma && elect_one()) mma_lane<T, D>(a, sm, tmem);
   }
   __syncwarp();
   tmem_fence_before();

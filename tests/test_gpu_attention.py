@@ -642,6 +642,16 @@ def test_streams_as_handles():
             assert torch.equal(g, w)
 
 
+@pytest.mark.parametrize("B,longest,H,K,D,dtype", [(250, 300, 4, 2, 128, "bf16"), (700, 40, 8, 4, 64, "fp16")])
+def test_prompt_many_mixed_sequences(B, longest, H, K, D, dtype):
+    """Far more row tiles than the GPU holds at once, of every kind in turn: without rows, without keys, with one row tile
+    or two, with key tiles that end inside, at the end and behind a prefix."""
+    rng = np.random.default_rng(B)
+    rows = rng.integers(0, longest, B)
+    extra = rng.choice([-longest, -5, 0, 3, 128, 300], B)
+    run_prompt([(int(n), max(0, int(n + x))) for n, x in zip(rows, extra)], H, K, D, dtype, True, seed=B)
+
+
 def test_layer_prompt_then_verify_steps():
     """A layer as a server runs it: a prompt through append and prompt attention, then steps of six rows through
     append, paged attention and the MoE step; the paged rows equal prompt attention over the cached values."""
