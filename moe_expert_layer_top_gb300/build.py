@@ -6,6 +6,8 @@
   bounds-checked build (every kernel index checked; a miss is reported as
   MOE_ERR_DEVICE_BOUNDS and the access skipped), loaded instead of libmoe.so
   when the environment sets MOE_DEBUG_BOUNDS=1;
+* ``csrc/attention_torch.cpp`` -> ``_build/attention_torch.so``, the Python module
+  that passes PyTorch tensors to the attention calls (host code, g++);
 * ``synth/synth.cu`` -> ``synth/_build/libmoe_synth.so``, the device side of the
   seeded input generator.
 The translation units are compiled in parallel, each with one ``-gencode``.
@@ -25,6 +27,8 @@ LIB_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe.so")
 DEBUG_DIR = os.path.join(LIB_DIR, "debug")
 DEBUG_LIB_PATH = os.path.join(LIB_DIR, "libmoe_debug.so")
+TORCH_SRC = os.path.join(CSRC, "attention_torch.cpp")
+TORCH_LIB_PATH = os.path.join(LIB_DIR, "attention_torch.so")
 SYNTH_DIR = os.path.join(ROOT, "synth")
 SYNTH_LIB_DIR = os.path.join(SYNTH_DIR, "_build")
 SYNTH_LIB_PATH = os.path.join(SYNTH_LIB_DIR, "libmoe_synth.so")
@@ -49,6 +53,20 @@ def _run(cmd):
 
 def _compile(src: str, obj: str, extra=()):
     return _run([nvcc(), *ARCH, *FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj])
+
+
+def _build_torch_module():
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    tmp = TORCH_LIB_PATH + ".tmp"
+    _run([os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+          "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+          "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"), TORCH_SRC,
+          "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"])
+    os.replace(tmp, TORCH_LIB_PATH)
 
 
 def _stale(target: str, sources) -> bool:
@@ -77,8 +95,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         jobs.append(("synth", [synth_src], [os.path.join(SYNTH_LIB_DIR, "synth.o")], SYNTH_LIB_PATH, ()))
     work = [(s, o, tuple(flags) + (("-Xptxas", "-v") if verbose else ()))
             for _, srcs, objs, _, flags in jobs for s, o in zip(srcs, objs)]
-    with ThreadPoolExecutor(max_workers=max(1, min(len(work), os.cpu_count() or 4))) as ex:
+    module = force or _stale(TORCH_LIB_PATH, [TORCH_SRC, os.path.join(INCLUDE, "moe.h")])
+    with ThreadPoolExecutor(max_workers=max(1, min(len(work) + 1, os.cpu_count() or 4))) as ex:
+        pending = [ex.submit(_build_torch_module)] if module else []
         logs = list(ex.map(lambda a: _compile(*a), work))
+        for p in pending:
+            p.result()
     if verbose:
         for log in logs:
             print(log)

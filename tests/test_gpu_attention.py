@@ -652,6 +652,55 @@ def test_prompt_many_mixed_sequences(B, longest, H, K, D, dtype):
     run_prompt([(int(n), max(0, int(n + x))) for n, x in zip(rows, extra)], H, K, D, dtype, True, seed=B)
 
 
+def test_wrapper_refusals():
+    """What the wrappers and entry points refuse, before anything runs on the GPU."""
+    z = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype, device="cuda")
+    q, k = z(4, 8, 64), z(4, 2, 64)
+    cu, pos, slots = ac.i32([0, 4]), ac.i32([0, 1, 2, 3]), torch.arange(4, device="cuda")
+    rope, cache, table, lens = attention.rope_table(8, 64), attention.KVCacheMXFP4.empty(2, 16, 2, 64), ac.i32([[0, 1]]), ac.i32([4])
+    wrong = ValueError
+    for error, match, call in (
+        (wrong, "type of q", lambda: attention.qkv_append(q, k.half(), k)),
+        (wrong, "contiguous", lambda: attention.qkv_append(q, k.transpose(1, 2).contiguous().transpose(1, 2), k)),
+        (wrong, "k and v", lambda: attention.qkv_append(q, k[:3], k[:3])),
+        (wrong, "together", lambda: attention.qkv_append(q, k, k, rope=rope)),
+        (wrong, "together", lambda: attention.qkv_append(q, k, k, cache=cache)),
+        (wrong, "positions", lambda: attention.qkv_append(q, k, k, rope=rope, positions=pos.long())),
+        (wrong, "positions", lambda: attention.qkv_append(q, k, k, rope=rope, positions=pos[:3])),
+        (wrong, "rope", lambda: attention.qkv_append(q, k, k, rope=rope.double(), positions=pos)),
+        (wrong, "slots", lambda: attention.qkv_append(q, k, k, cache=cache, slots=slots.int())),
+        (wrong, "slots", lambda: attention.qkv_append(q, k, k, cache=cache, slots=slots.cpu())),
+        (wrong, "q_norm", lambda: attention.qkv_append(q, k, k, q_norm=z(32))),
+        (wrong, "q_out", lambda: attention.qkv_append(q, k, k, q_out=z(4, 9, 64)[:, :8])),
+        (wrong, "cache", lambda: attention.qkv_append(q, z(4, 4, 64), z(4, 4, 64), cache=cache, slots=slots)),
+        (wrong, "d_status", lambda: attention.qkv_append(q, k, k, d_status=slots)),
+        (wrong, "bf16 or fp16", lambda: attention.qkv_append(q.float(), k, k)),
+        (TypeError, "tensor", lambda: attention.qkv_append(q, k, [1])),
+        (abi.MoeError, None, lambda: attention.qkv_append(q, k, k, eps=float("nan"))),
+        (abi.MoeError, None, lambda: attention.qkv_append(z(4, 8, 96), z(4, 2, 96), z(4, 2, 96))),
+        (abi.MoeError, None, lambda: attention.qkv_append(q, z(4, 3, 64), z(4, 3, 64))),
+        (wrong, "lengths", lambda: attention.attend_paged(q, cache, table, lens.long(), cu)),
+        (wrong, "cu_rows", lambda: attention.attend_paged(q, cache, table, lens, ac.i32([0, 2, 4]))),
+        (wrong, "page_table", lambda: attention.attend_paged(q, cache, table[0], lens, cu)),
+        (wrong, "page_table", lambda: attention.attend_paged(q, cache, ac.i32([[0, 1], [0, 1]]), lens, cu)),
+        (wrong, "cache", lambda: attention.attend_paged(z(4, 8, 128), cache, table, lens, cu)),
+        (AttributeError, None, lambda: attention.attend_paged(q, k, table, lens, cu)),
+        (wrong, "32 bits", lambda: attention.attend_paged(q, cache, table, lens, cu, max_rows=2 ** 40)),
+        (abi.MoeError, None, lambda: attention.attend_paged(q, cache, table, lens, cu, max_rows=0)),
+        (abi.MoeError, None, lambda: attention.attend_paged(q, cache, table, lens, cu, scale=1e300)),
+        (TypeError, None, lambda: attention.attend_paged(q, cache, table, lens, cu, scale="1")),
+        (wrong, "out", lambda: attention.attend_prompt(q, k, k, cu, cu, out=z(4, 8, 128))),
+        (wrong, "cu_keys", lambda: attention.attend_prompt(q, k, k, cu, pos)),
+        (wrong, "cu_rows", lambda: attention.attend_prompt(q, k, k, cu[:0], cu[:0])),
+        (wrong, "k and v", lambda: attention.attend_prompt(q, k, k[:3], cu, cu)),
+        (abi.MoeError, None, lambda: attention.attend_prompt(z(4, 516)[:, :512].view(4, 8, 64), k, k, cu, cu)),  # row stride
+        (wrong, "k_scales", lambda: attention.KVCacheMXFP4(cache.k_codes, cache.k_codes, cache.v_codes, cache.v_scales)),
+        (wrong, "dimensions", lambda: attention.KVCacheMXFP4(cache.k_codes[0], cache.k_scales, cache.v_codes, cache.v_scales)),
+    ):
+        with pytest.raises(error, match=match):
+            call()
+
+
 def test_layer_prompt_then_verify_steps():
     """A layer as a server runs it: a prompt through append and prompt attention, then steps of six rows through
     append, paged attention and the MoE step; the paged rows equal prompt attention over the cached values."""
