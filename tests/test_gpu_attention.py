@@ -701,6 +701,32 @@ def test_wrapper_refusals():
             call()
 
 
+def test_calls_from_threads():
+    """Three threads, each with its stream and its call, many times over."""
+    import threading
+    x = torch.randn(40, 6, 64, device="cuda", generator=torch.Generator("cuda").manual_seed(53)).bfloat16()
+    args, cu, lens = (x[:, :4], x[:, 4:5], x[:, 5:]), ac.i32([0, 40]), ac.i32([90])
+    c = ac.Cache(np.random.default_rng(54), [90], 1, 64, 16)
+    calls = [lambda: attention.qkv_append(*args)["q"], lambda: attention.attend_prompt(*args, cu, cu),
+             lambda: attention.attend_paged(args[0], c.cache, c.table, lens, cu)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    got = [None] * 3
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()) as _:
+            got[i] = [calls[i]() for _ in range(100)]
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g, w in zip(got, want):
+        assert len(g) == 100 and all(torch.equal(y, w) for y in g)
+
+
 def test_layer_prompt_then_verify_steps():
     """A layer as a server runs it: a prompt through append and prompt attention, then steps of six rows through
     append, paged attention and the MoE step; the paged rows equal prompt attention over the cached values."""
