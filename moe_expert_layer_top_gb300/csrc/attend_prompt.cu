@@ -253,9 +253,10 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *st
 // The grid has a block for every Work. A running block takes over those that have not started yet, one by one, through
 // the hardware's launch control; the others run as blocks of their own. (Heads run fastest: the heads of a sequence's
 // long tiles come before its short ones.) Whole warp.
-__device__ __forceinline__ Work find_work(const PromptArgs &a, uint32_t block, int32_t *status) {
+__device__ __forceinline__ Work find_work(const PromptArgs &a, TileCursor &cursor, uint32_t block, int32_t *status) {
   const uint32_t tile = block / a.all_groups, head = block - tile * a.all_groups;
-  const TileAt at = find_tile(a.cu_rows, a.num_rows, a.cu_keys, a.num_keys, a.num_seqs, 2 * a.tokens, tile, status);
+  const TileAt at =
+      find_tile(cursor, a.cu_rows, a.num_rows, a.cu_keys, a.num_keys, a.num_seqs, 2 * a.tokens, tile, status);
   Work w;
   w.valid = at.seq >= 0;
   w.row0 = at.rows.first;
@@ -329,7 +330,8 @@ __device__ void load_warp(const CUtensorMap *qmap, const CUtensorMap *kmap, cons
                           Smem<D> &sm, Work w) {
   using S = Smem<D>;
   const int lane = threadIdx.x & 31;
-  uint32_t base = 0;  // entries of the ring so far
+  TileCursor cursor;
+  uint32_t base = 0, asked = 0;  // entries of the ring so far; questions for further work
   int queries[2] = {w.tiles0 > 0, w.tiles1 > 0}, issued = min(2 * w.all(), S::kStages);
   for (uint32_t t = 0;; ++t) {
     const int n = w.all();
@@ -356,10 +358,14 @@ __device__ void load_warp(const CUtensorMap *qmap, const CUtensorMap *kmap, cons
         }
       }
     }
-    if (elect_one()) {
-      mbar_arrive_expect_tx(&sm.next_full, 16);
-      ask_next(&sm.next, &sm.next_full);
-    }
+    const auto ask = [&] {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sm.next_full, 16);
+        ask_next(&sm.next, &sm.next_full);
+      }
+      ++asked;
+    };
+    ask();
     // one lane issued: the others follow
     issued = __reduce_max_sync(0xFFFFFFFFu, unsigned(issued));
     queries[0] = __reduce_max_sync(0xFFFFFFFFu, unsigned(queries[0]));
@@ -379,12 +385,15 @@ __device__ void load_warp(const CUtensorMap *qmap, const CUtensorMap *kmap, cons
     __syncwarp();
     if (ok && lane == 0) mbar_arrive(&sm.tail[t & 3]);
     base += issued;
-    uint32_t block = 0;
-    const bool answered = __all_sync(0xFFFFFFFFu, wait(&sm.next_full, t & 1, a.status));
-    const bool more = answered && read_next(&sm.next, block);
     const Work was = w;
     w.valid = 0;
-    if (more && ok) w = find_work(a, block, a.status);
+    for (uint32_t block; __all_sync(0xFFFFFFFFu, wait(&sm.next_full, (asked - 1) & 1, a.status)) && read_next(&sm.next, block);) {
+      if (ok) w = find_work(a, cursor, block, a.status);
+      if (w.valid || !ok) break;
+      fence_proxy_async();
+      __syncwarp();
+      ask();  // the grid is as large as it can be for these sizes: blocks past the last tile are taken over for nothing
+    }
     w.step0 = (was.step0 + was.tiles0 + was.tiles1) % S::kBufs;
     w.s0 = (was.s0 + was.tiles0) % (2 * S::kBufs);
     w.s1 = (was.s1 + was.tiles1) % (2 * S::kBufs);
@@ -726,7 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   // every warp finds the block's first work for itself: nothing to wait for
-  const Work w = find_work(a, blockIdx.x, warp == kWarpLoad ? a.status : nullptr);
+  TileCursor cursor;
+  const Work w = find_work(a, cursor, blockIdx.x, warp == kWarpLoad ? a.status : nullptr);
   if (!w.valid) return;  // past the last tile: the whole block
   if (warp == kWarpLoad) {
     if (elect_one()) {

@@ -77,31 +77,40 @@ struct TileAt {
   Span rows, keys;        // of the sequence
 };
 
-__device__ __forceinline__ TileAt find_tile(const int32_t *cu_rows, int num_rows, const int32_t *cu_keys, int num_keys,
-                                            int num_seqs, int rows, int64_t tile, int32_t *status) {
-  const int lane = threadIdx.x & 31;
+// Where a search may begin: `base` tiles lie before sequence b0. A search that goes on where the last one ended makes
+// all searches of a block one pass over the sequences (4,096 prompts of 30 tokens: 1.09 ms; 11.4 with searches from the
+// start and without taking over the blocks past the last tile).
+struct TileCursor {
+  int b0 = 0;
   int64_t base = 0;
-  for (int b0 = 0; b0 < num_seqs; b0 += 32) {
-    const int b = b0 + lane;
+};
+
+__device__ __forceinline__ TileAt find_tile(TileCursor &from, const int32_t *cu_rows, int num_rows, const int32_t *cu_keys,
+                                            int num_keys, int num_seqs, int rows, int64_t tile, int32_t *status) {
+  const int lane = threadIdx.x & 31;
+  if (tile < from.base) from = TileCursor();
+  while (from.b0 < num_seqs) {
+    const int b = from.b0 + lane;
     Span r = {0, 0}, k = {0, 0};
     if (b < num_seqs) {
       r = seq_span(cu_rows, b, num_rows, status);
       k = seq_span(cu_keys, b, num_keys, status);
     }
     const int tiles = (r.n + rows - 1) / rows;
-    const int64_t end = base + warp_inclusive_sum(tiles);
+    const int64_t end = from.base + warp_inclusive_sum(tiles);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, tile < end);
     if (hit) {
       const int w = __ffs(hit) - 1;
       TileAt at;
-      at.seq = b0 + w;
+      at.seq = from.b0 + w;
       at.tiles = __shfl_sync(0xFFFFFFFFu, tiles, w);
       at.local = int(tile - (__shfl_sync(0xFFFFFFFFu, end, w) - at.tiles));
       at.rows = {__shfl_sync(0xFFFFFFFFu, r.first, w), __shfl_sync(0xFFFFFFFFu, r.n, w)};
       at.keys = {__shfl_sync(0xFFFFFFFFu, k.first, w), __shfl_sync(0xFFFFFFFFu, k.n, w)};
       return at;
     }
-    base = __shfl_sync(0xFFFFFFFFu, end, 31);
+    from.base = __shfl_sync(0xFFFFFFFFu, end, 31);
+    from.b0 += 32;
   }
   return {-1, 0, 0, {0, 0}, {0, 0}};
 }

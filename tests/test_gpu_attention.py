@@ -652,6 +652,16 @@ def test_prompt_many_mixed_sequences(B, longest, H, K, D, dtype):
     run_prompt([(int(n), max(0, int(n + x))) for n, x in zip(rows, extra)], H, K, D, dtype, True, seed=B)
 
 
+def test_prompt_mostly_empty_sequences():
+    """4,096 sequences of which few have rows: searches far into the list, and many blocks past the last tile."""
+    rng = np.random.default_rng(60)
+    seqs = [(0, int(x)) for x in rng.integers(0, 3, 4096)]
+    for b in rng.choice(4096, 30, replace=False):
+        seqs[b] = (int(rng.integers(1, 90)), int(rng.integers(0, 200)))
+    seqs[4095] = (33, 40)
+    run_prompt(seqs, 4, 2, 64, "bf16", True, seed=61)
+
+
 def test_wrapper_refusals():
     """What the wrappers and entry points refuse, before anything runs on the GPU."""
     z = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype, device="cuda")
