@@ -513,7 +513,15 @@ typedef struct moe_attend_prompt_io {
   uint32_t dtype;
   int32_t causal;             /* 1: row i of n sees keys 0 .. m - n + i of its sequence's m; 0: all of them */
   float scale;
+  void *workspace;            /* optional, 16-byte aligned device memory: lets few rows over many keys spread over the
+                               * GPU (the keys are split and the parts joined); NULL: each row's keys in one pass */
+  int64_t workspace_bytes;
 } moe_attend_prompt_io_t;
+
+/* Bytes of workspace that moe_attend_prompt can use for these sizes (the
+ * pointers are not looked at), the same for every content of the device
+ * arrays; 0 where it has no use for one. It depends on the current device. */
+moe_status_t moe_attend_prompt_workspace(const moe_attend_prompt_io_t *io, int64_t *bytes_out);
 
 /* Attention over packed prompts, or over chunks of prompts with the keys that
  * precede them (m > n). Formula and empty rows as for moe_attend_paged. The
@@ -523,7 +531,8 @@ typedef struct moe_attend_prompt_io {
  * that a row does not see never reaches the row; one in a value of a later key
  * can reach earlier rows of its own sequence (0 * NaN is NaN). A sequence with an
  * offset out of range gets no result; the others have theirs. out must not
- * overlap the inputs. */
+ * overlap the inputs. A workspace smaller than moe_attend_prompt_workspace says
+ * is MOE_ERR_INVALID_ARG; calls that may overlap on the GPU need one each. */
 moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_status, void *cuda_stream);
 
 /* Teardown: frees the plan's device memory and events, after a device-wide

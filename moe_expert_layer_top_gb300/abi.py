@@ -52,6 +52,7 @@ EXPORTED = (
     "moe_qkv_append",
     "moe_attend_paged_workspace",
     "moe_attend_paged",
+    "moe_attend_prompt_workspace",
     "moe_attend_prompt",
     "moe_destroy",
 )
@@ -173,6 +174,8 @@ class MoeAttendPromptIO(ctypes.Structure):
         ("dtype", ctypes.c_uint32),
         ("causal", ctypes.c_int32),
         ("scale", ctypes.c_float),
+        ("workspace", _P),
+        ("workspace_bytes", ctypes.c_int64),
     ]
 
 
@@ -229,6 +232,8 @@ def load(path: str | None = None):
     lib.moe_attend_paged.restype = ctypes.c_int
     lib.moe_attend_paged.argtypes = [ctypes.POINTER(MoeAttendPagedIO), ctypes.POINTER(MoeKvCache), _P,
                                      ctypes.c_int64, _P, _P]
+    lib.moe_attend_prompt_workspace.restype = ctypes.c_int
+    lib.moe_attend_prompt_workspace.argtypes = [ctypes.POINTER(MoeAttendPromptIO), ctypes.POINTER(ctypes.c_int64)]
     lib.moe_attend_prompt.restype = ctypes.c_int
     lib.moe_attend_prompt.argtypes = [ctypes.POINTER(MoeAttendPromptIO), _P, _P]
     lib.moe_destroy.restype = ctypes.c_int
@@ -385,6 +390,14 @@ def moe_attend_paged(io: MoeAttendPagedIO, cache: MoeKvCache, workspace, workspa
     lib = load()
     return lib.moe_attend_paged(ctypes.byref(io), ctypes.byref(cache), ptr(workspace), workspace_bytes,
                                 ptr(d_status), stream_ptr(stream))
+
+
+def moe_attend_prompt_workspace(io: MoeAttendPromptIO) -> int:
+    """Bytes of workspace that moe_attend_prompt can use for these sizes (0: none)."""
+    lib = load()
+    n = ctypes.c_int64()
+    check("moe_attend_prompt_workspace", lib.moe_attend_prompt_workspace(ctypes.byref(io), ctypes.byref(n)))
+    return n.value
 
 
 def moe_attend_prompt(io: MoeAttendPromptIO, d_status=None, stream=None) -> int:

@@ -47,7 +47,8 @@ def _native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-            "moe_qkv_append", "moe_attend_paged_workspace", "moe_attend_paged", "moe_attend_prompt")))
+            "moe_qkv_append", "moe_attend_paged_workspace", "moe_attend_paged", "moe_attend_prompt_workspace",
+            "moe_attend_prompt")))
         _module = module
     return _module
 

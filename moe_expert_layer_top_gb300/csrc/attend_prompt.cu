@@ -67,6 +67,8 @@ constexpr int kWarpLoad = 8, kWarpMma = 9;
 constexpr uint32_t kTmemCols = 512;
 constexpr int64_t kWaitNs = 1000000000;  // bound of every wait
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
+constexpr int kSplitTiles = 8;           // key tiles of a part, at least
+constexpr int kMaxSplits = 16;
 
 struct PromptArgs {
   uint16_t *out;
@@ -81,6 +83,8 @@ struct PromptArgs {
   float scale2;    // |scale| log2 e, at least 2^-100: scores times this are exponents of two
   bool negative;   // the scale is: scores change sign
   int32_t *status;
+  int splits;    // parts that a work's keys may be split into
+  float *parts;  // workspace: of each part, O and (reference, sum) of its 256 rows
 };
 
 // What a block does at a time: two row tiles of a sequence, for the heads of a group.
@@ -91,6 +95,7 @@ struct Work {
   int kv, head0;     // kv head, the first of the block's heads
   int tiles0, tiles1;  // key tiles of row tiles A and B
   int valid;           // 0: there is no further work
+  int skip, parts, slot;  // keys of the sequence before key0; parts of this tile, and where this one goes
   // where the barriers stand when it begins: steps, S of each row tile, entries of the ring (each modulo twice its
   // ring), and the phases of o_full
   int step0, s0, s1, entry0, o0, o1;
@@ -98,8 +103,6 @@ struct Work {
   __device__ __forceinline__ int tiles(int x) const { return x ? tiles1 : tiles0; }
   __device__ __forceinline__ int both() const { return min(tiles0, tiles1); }  // key tiles that both have
   __device__ __forceinline__ int all() const { return max(tiles0, tiles1); }
-  // the place of (row tile x, key tile j) in the list of steps
-  __device__ __forceinline__ int step(int x, int j) const { return j < both() ? 2 * j + x : both() + j; }
 };
 
 template <int D>
@@ -227,8 +230,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // ------------------------------------------------------------------ the block's work
 
 // Keys that row t of the sequence sees.
-__device__ __forceinline__ int key_limit(const PromptArgs &a, const Work &w, int t) {
-  return a.causal ? min(w.keys, max(0, w.keys - w.n + t + 1)) : w.keys;
+__device__ __forceinline__ int key_limit(const PromptArgs &a, int keys, int n, int t) {
+  return a.causal ? min(keys, max(0, keys - n + t + 1)) : keys;
 }
 
 __device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity) {
@@ -253,7 +256,14 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *st
 // The grid has a block for every Work. A running block takes over those that have not started yet, one by one, through
 // the hardware's launch control; the others run as blocks of their own. (Heads run fastest: the heads of a sequence's
 // long tiles come before its short ones.) Whole warp.
+template <bool SPLIT>
 __device__ __forceinline__ Work find_work(const PromptArgs &a, TileCursor &cursor, uint32_t block, int32_t *status) {
+  int part = 0;
+  const int slot = int(block);
+  if constexpr (SPLIT) {
+    part = int(block % uint32_t(a.splits));
+    block /= uint32_t(a.splits);
+  }
   const uint32_t tile = block / a.all_groups, head = block - tile * a.all_groups;
   const TileAt at =
       find_tile(cursor, a.cu_rows, a.num_rows, a.cu_keys, a.num_keys, a.num_seqs, 2 * a.tokens, tile, status);
@@ -267,11 +277,22 @@ __device__ __forceinline__ Work find_work(const PromptArgs &a, TileCursor &curso
   w.head0 = head * a.group;
   w.t0 = (at.tiles - 1 - at.local) * (2 * a.tokens);  // the last rows see the most keys: they start first
   const auto key_tiles = [&](int first) {
-    return first < w.n ? (key_limit(a, w, min(first + a.tokens, w.n) - 1) + kKeys - 1) / kKeys : 0;
+    return first < w.n ? (key_limit(a, w.keys, w.n, min(first + a.tokens, w.n) - 1) + kKeys - 1) / kKeys : 0;
   };
   w.tiles0 = key_tiles(w.t0);
   w.tiles1 = key_tiles(w.t0 + a.tokens);
   w.step0 = w.s0 = w.s1 = w.entry0 = w.o0 = w.o1 = 0;
+  w.skip = 0, w.parts = 1, w.slot = slot;
+  if constexpr (SPLIT) {  // equal parts, of kSplitTiles key tiles at least
+    const int all = w.all(), per = max(1, (all + min(a.splits, max(1, all / kSplitTiles)) - 1) / min(a.splits, max(1, all / kSplitTiles)));
+    w.parts = max(1, (all + per - 1) / per);
+    if (part >= w.parts) w.valid = 0;
+    w.skip = part * per * kKeys;
+    w.key0 += w.skip;
+    w.keys -= w.skip;
+    w.tiles0 = min(max(w.tiles0 - part * per, 0), per);
+    w.tiles1 = min(max(w.tiles1 - part * per, 0), per);
+  }
   return w;
 }
 
@@ -325,7 +346,7 @@ __device__ __forceinline__ void load_queries(const CUtensorMap *qmap, const Prom
 
 // Q and the first entries of the block's first work, as many as the ring has slots, went out with the barriers'
 // initialisation.
-template <int D>
+template <int D, bool SPLIT>
 __device__ void load_warp(const CUtensorMap *qmap, const CUtensorMap *kmap, const CUtensorMap *vmap, const PromptArgs &a,
                           Smem<D> &sm, Work w) {
   using S = Smem<D>;
@@ -388,7 +409,7 @@ __device__ void load_warp(const CUtensorMap *qmap, const CUtensorMap *kmap, cons
     const Work was = w;
     w.valid = 0;
     for (uint32_t block; __all_sync(0xFFFFFFFFu, wait(&sm.next_full, (asked - 1) & 1, a.status)) && read_next(&sm.next, block);) {
-      if (ok) w = find_work(a, cursor, block, a.status);
+      if (ok) w = find_work<SPLIT>(a, cursor, block, a.status);
       if (w.valid || !ok) break;
       fence_proxy_async();
       __syncwarp();
@@ -564,14 +585,15 @@ __device__ __forceinline__ void exponentials(const uint32_t (&s)[kKeys], uint32_
   sum = (add[0] + add[1]) + (add[2] + add[3]);
 }
 
-template <class T, int D>
+template <class T, int D, bool SPLIT>
 __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, const Work &w, uint32_t tmem) {
   using S = Smem<D>;
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
   // the thread's row of the sequence and its head; rows past the tile's tokens or the sequence see nothing
   const int t = w.t0 + x * a.tokens + row / a.group, h = w.head0 + row % a.group;
   const bool real = row < a.tokens * a.group && t < w.n;
-  const int limit = real ? key_limit(a, w, t) : 0;
+  const int skip = SPLIT ? w.skip : 0;
+  const int limit = real ? key_limit(a, w.keys + skip, w.n, t) - skip : 0;
   const uint32_t lanes = uint32_t(warp * 32) << 16;
   const uint32_t to = tmem + lanes + S::kColO + x * D;
   float ref = 0.0f, total = 0.0f;  // the reference in score units
@@ -634,6 +656,30 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
   if (w.tiles(x) > 0) {
     if (!__all_sync(0xFFFFFFFFu, wait(&sm.o_full[x], x ? w.o1 : w.o0, a.status))) return false;
     tmem_fence_after();
+  }
+  if constexpr (SPLIT) {
+    if (w.parts > 1) {  // as it is, for the join
+      float *const part = a.parts + (int64_t(w.slot) * 2 + x) * kRows * (D + 2);
+      if (real) {
+        part[kRows * D + row] = total != 0.0f ? ref * a.scale2 : -1e30f;
+        part[kRows * D + kRows + row] = total;
+      }
+      if (tiles > 0) {
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * i, o);
+          tmem_wait_ld(o);
+          if (real) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4 *>(part + row * D + 32 * i + 4 * c) =
+                  make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          }
+        }
+      }
+      return true;
+    }
   }
   // O / sum. Rows of 256 bytes go through the warp's own shared memory, 64 values of 32 rows at a time, and out by whole
   // pieces of rows (16-byte pieces exchanged by row, against bank conflicts); rows of 128 straight from their threads.
@@ -706,7 +752,7 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
   return true;
 }
 
-template <class T, int D>
+template <class T, int D, bool SPLIT>
 __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, uint32_t tmem) {
   using S = Smem<D>;
   int64_t ns = kWaitNs;
@@ -714,7 +760,7 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, uint32_t tmem) {
     if (!__all_sync(0xFFFFFFFFu, wait(&sm.work_full[t & 1], t >> 1 & 1, a.status, ns))) return;
     const Work &w = sm.work[t & 1];
     if (!w.valid) return;
-    if (!softmax_work<T, D>(a, sm, w, tmem)) return;
+    if (!softmax_work<T, D, SPLIT>(a, sm, w, tmem)) return;
     // the next work comes when the loads of this one are out; a warp whose own row tile is short waits for the other's
     ns = kWaitNs + int64_t(w.all()) * 100000;
     __syncwarp();
@@ -724,7 +770,7 @@ __device__ void softmax_warps(const PromptArgs &a, Smem<D> &sm, uint32_t tmem) {
 
 // ------------------------------------------------------------------ kernel
 
-template <class T, int D>
+template <class T, int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ CUtensorMap qmap,
                                                                     const __grid_constant__ CUtensorMap kmap,
                                                                     const __grid_constant__ CUtensorMap vmap,
@@ -736,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   const int warp = threadIdx.x >> 5;
   // every warp finds the block's first work for itself: nothing to wait for
   TileCursor cursor;
-  const Work w = find_work(a, cursor, blockIdx.x, warp == kWarpLoad ? a.status : nullptr);
+  const Work w = find_work<SPLIT>(a, cursor, blockIdx.x, warp == kWarpLoad ? a.status : nullptr);
   if (!w.valid) return;  // past the last tile: the whole block
   if (warp == kWarpLoad) {
     if (elect_one()) {
@@ -777,10 +823,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   const uint32_t tmem = sm.tmem_base;
   if (warp < kWarpLoad) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_warps<T, D>(a, sm, tmem);
+    softmax_warps<T, D, SPLIT>(a, sm, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kWarpLoad) load_warp<D>(&qmap, &kmap, &vmap, a, sm, w);
+    if (warp == kWarpLoad) load_warp<D, SPLIT>(&qmap, &kmap, &vmap, a, sm, w);
     if (warp == kWarpMma && elect_one()) mma_lane<T, D>(a, sm, tmem);
   }
   __syncwarp();
@@ -789,6 +835,52 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   tmem_fence_after();
   if (warp == kWarpMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// ------------------------------------------------------------------ joining the parts of split keys
+// A block for 32 rows of a tile, a warp for a row at a time: the parts' references and sums a lane each, then O.
+constexpr int kJoinThreads = 256, kJoinRows = 32;
+
+template <class T, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const PromptArgs a) {
+  static_assert(kMaxSplits <= 32, "a lane for each part");
+  TileCursor cursor;
+  const Work w = find_work<true>(a, cursor, blockIdx.x * uint32_t(a.splits), nullptr);
+  if (!w.valid || w.parts == 1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int64_t kPart = 2 * kRows * (D + 2);
+  for (int i = 0; i < kJoinRows / (kJoinThreads / 32); ++i) {
+    const int r = int(blockIdx.y) * kJoinRows + i * (kJoinThreads / 32) + warp, x = r / kRows, row = r % kRows;
+    const int t = w.t0 + x * a.tokens + row / a.group, h = w.head0 + row % a.group;
+    if (row >= a.tokens * a.group || t >= w.n) continue;
+    const float *const from = a.parts + w.slot * kPart + int64_t(x) * kRows * (D + 2);
+    float ref = -1e30f, sum = 0.0f;
+    if (lane < w.parts) {
+      ref = from[lane * kPart + kRows * D + row];
+      sum = from[lane * kPart + kRows * D + kRows + row];
+    }
+    float top = ref;
+#pragma unroll
+    for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const float weight = sum != 0.0f ? exp2_approx(ref - top) : 0.0f;  // a part in which the row sees no key has no O
+    float total = weight * sum;
+#pragma unroll
+    for (int d = 16; d; d /= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p = 0; p < w.parts; ++p) {
+      const float f = __shfl_sync(0xFFFFFFFFu, weight, p);
+      if (f == 0.0f || lane >= D / 4) continue;
+      const float4 v = *reinterpret_cast<const float4 *>(from + p * kPart + row * D + 4 * lane);
+      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    }
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+    if (lane < D / 4)
+      *reinterpret_cast<uint2 *>(a.out + int64_t(w.row0 + t) * a.out_stride + int64_t(h) * D + 4 * lane) =
+          total != 0.0f ? make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+    if (lane == 0 && a.lse)
+      a.lse[int64_t(w.row0 + t) * a.num_heads + h] =
+          total > 0.0f ? (log2f(total) + top) * 0.6931471805599453f : -INFINITY;
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -809,25 +901,63 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
-template <class T, int D>
+// The most works that these sizes can have.
+int64_t works_bound(const PromptArgs &a) { return (int64_t(a.num_rows) / (2 * a.tokens) + a.num_seqs) * a.all_groups; }
+
+// Heads that share a row tile, and what follows from them.
+void set_groups(const moe_attend_prompt_io_t &io, PromptArgs &a) {
+  const int group = io.num_heads / io.num_kv_heads;
+  a.group = group < kRows ? group : kRows;
+  while (group % a.group) --a.group;
+  a.groups = group / a.group;
+  a.all_groups = io.num_heads / a.group;
+  a.tokens = kRows / a.group;
+  a.num_rows = io.num_rows;
+  a.num_seqs = io.num_seqs;
+}
+
+// The keys are split where the works alone leave half of the GPU idle and the keys suffice for two parts.
+int splits_of(const PromptArgs &a, int num_keys, int num_sms) {
+  const int64_t works = works_bound(a);
+  if (works < 1) return 1;
+  int64_t s = num_sms / works;
+  s = s < kMaxSplits ? s : kMaxSplits;
+  s = s < num_keys / (kSplitTiles * kKeys) ? s : num_keys / (kSplitTiles * kKeys);
+  return s < 1 ? 1 : int(s);
+}
+
+template <class T, int D, bool SPLIT>
 cudaError_t launch(const Maps &maps, const PromptArgs &a, cudaStream_t st) {
-  const int64_t blocks = (int64_t(a.num_rows) / (2 * a.tokens) + a.num_seqs) * a.all_groups;
+  const int64_t works = works_bound(a), blocks = works * (SPLIT ? a.splits : 1);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   // The register split above assumes the launch's share: a build that gave the kernel less must not run.
   static const bool split = [] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, attend_prompt_kernel<T, D>) == cudaSuccess && at.numRegs == kRegsLaunch;
+    return cudaFuncGetAttributes(&at, attend_prompt_kernel<T, D, SPLIT>) == cudaSuccess && at.numRegs == kRegsLaunch;
   }();
   if (!split) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              int(Smem<D>::kBytes));
   if (e != cudaSuccess) return e;
-  attend_prompt_kernel<T, D><<<unsigned(blocks), kThreads, Smem<D>::kBytes, st>>>(
+  attend_prompt_kernel<T, D, SPLIT><<<unsigned(blocks), kThreads, Smem<D>::kBytes, st>>>(
       maps.q, maps.k, maps.v, a);
+  if constexpr (SPLIT) {
+    const cudaError_t launched = cudaGetLastError();
+    if (launched != cudaSuccess) return launched;
+    join_prompt_kernel<T, D><<<dim3(unsigned(works), 2 * kRows / kJoinRows), kJoinThreads, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 
 }  // namespace
+
+int64_t attend_prompt_workspace(const moe_attend_prompt_io_t &io, int num_sms) {
+  if (io.num_rows == 0 || io.num_seqs == 0) return 0;
+  PromptArgs a = {};
+  set_groups(io, a);
+  const int splits = splits_of(a, io.num_keys, num_sms);
+  return splits > 1 ? works_bound(a) * splits * 2 * kRows * (io.head_dim + 2) * 4 : 0;
+}
 
 cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *status, int num_sms, cudaStream_t st) {
   PromptArgs a = {};
@@ -840,12 +970,9 @@ cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *stat
   a.num_rows = io.num_rows;
   a.num_keys = io.num_keys;
   a.num_heads = io.num_heads;
-  const int group = io.num_heads / io.num_kv_heads;
-  a.group = group < kRows ? group : kRows;
-  while (group % a.group) --a.group;
-  a.groups = group / a.group;
-  a.all_groups = io.num_heads / a.group;
-  a.tokens = kRows / a.group;
+  set_groups(io, a);
+  a.splits = io.workspace ? splits_of(a, io.num_keys, num_sms) : 1;
+  a.parts = static_cast<float *>(io.workspace);
   a.causal = io.causal;
   a.scale2 = fmaxf(fabsf(io.scale) * 1.4426950408889634f, 0x1p-100f);
   a.negative = io.scale < 0.0f;
@@ -858,8 +985,12 @@ cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *stat
                       !encode(&maps.v, io.v, D, io.num_kv_heads, io.num_keys, io.v_stride, 1, kKeys)))
     return cudaErrorInvalidValue;
   const bool h = io.dtype == MOE_DTYPE_F16;
-  if (D == 64) return h ? launch<F16, 64>(maps, a, st) : launch<Bf16, 64>(maps, a, st);
-  return h ? launch<F16, 128>(maps, a, st) : launch<Bf16, 128>(maps, a, st);
+  if (a.splits > 1) {
+    if (D == 64) return h ? launch<F16, 64, true>(maps, a, st) : launch<Bf16, 64, true>(maps, a, st);
+    return h ? launch<F16, 128, true>(maps, a, st) : launch<Bf16, 128, true>(maps, a, st);
+  }
+  if (D == 64) return h ? launch<F16, 64, false>(maps, a, st) : launch<Bf16, 64, false>(maps, a, st);
+  return h ? launch<F16, 128, false>(maps, a, st) : launch<Bf16, 128, false>(maps, a, st);
 }
 
 }  // namespace moe

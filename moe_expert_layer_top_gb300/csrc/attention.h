@@ -15,6 +15,7 @@ cudaError_t launch_qkv_append(const moe_qkv_append_io_t &io, const moe_kv_cache_
 int64_t attend_paged_workspace(const moe_attend_paged_io_t &io, const moe_kv_cache_t &c, int num_sms);
 cudaError_t launch_attend_paged(const moe_attend_paged_io_t &io, const moe_kv_cache_t &c, void *workspace,
                                 int32_t *status, int num_sms, cudaStream_t st);
+int64_t attend_prompt_workspace(const moe_attend_prompt_io_t &io, int num_sms);
 cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *status, int num_sms, cudaStream_t st);
 
 }  // namespace moe

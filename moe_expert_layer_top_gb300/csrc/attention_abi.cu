@@ -74,6 +74,14 @@ moe_status_t paged_sizes_ok(const moe_attend_paged_io_t &io, const moe_kv_cache_
   return MOE_OK;
 }
 
+moe_status_t prompt_sizes_ok(const moe_attend_prompt_io_t &io) {
+  const moe_status_t s = heads_ok(io.num_heads, io.num_kv_heads, io.head_dim, io.dtype);
+  if (s != MOE_OK) return s;
+  if (io.num_seqs < 0 || io.num_rows < 0 || io.num_keys < 0) return MOE_ERR_INVALID_ARG;
+  if (io.num_seqs > kMaxSeqs || int64_t(io.num_rows) * io.num_heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -151,13 +159,22 @@ moe_status_t moe_attend_paged(const moe_attend_paged_io_t *io, const moe_kv_cach
              : MOE_ERR_CUDA;
 }
 
+moe_status_t moe_attend_prompt_workspace(const moe_attend_prompt_io_t *io, int64_t *bytes_out) {
+  if (!io || !bytes_out) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = prompt_sizes_ok(*io);
+  if (s != MOE_OK) return s;
+  int sms = 0;
+  s = device_sms(&sms);
+  if (s != MOE_OK) return s;
+  *bytes_out = attend_prompt_workspace(*io, sms);
+  return MOE_OK;
+}
+
 moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_status, void *cuda_stream) {
   const NvtxRange nvtx_range("moe_attend_prompt");
   if (!io) return MOE_ERR_INVALID_ARG;
-  moe_status_t s = heads_ok(io->num_heads, io->num_kv_heads, io->head_dim, io->dtype);
+  moe_status_t s = prompt_sizes_ok(*io);
   if (s != MOE_OK) return s;
-  if (io->num_seqs < 0 || io->num_rows < 0 || io->num_keys < 0) return MOE_ERR_INVALID_ARG;
-  if (io->num_seqs > kMaxSeqs || int64_t(io->num_rows) * io->num_heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (io->causal != 0 && io->causal != 1) return MOE_ERR_INVALID_ARG;
   if (!finite(io->scale) || !aligned(d_status, 4) || !aligned(io->lse, 4)) return MOE_ERR_INVALID_ARG;
   if (io->num_rows == 0 || io->num_seqs == 0) return MOE_OK;
@@ -172,6 +189,8 @@ moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_stat
   int sms = 0;
   s = device_sms(&sms);
   if (s != MOE_OK) return s;
+  if (io->workspace && (!aligned(io->workspace, 16) || io->workspace_bytes < attend_prompt_workspace(*io, sms)))
+    return MOE_ERR_INVALID_ARG;
   return launch_attend_prompt(*io, d_status, sms, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;

@@ -26,6 +26,7 @@ namespace {
 decltype(&moe_qkv_append) qkv_append = nullptr;
 decltype(&moe_attend_paged_workspace) attend_paged_workspace = nullptr;
 decltype(&moe_attend_paged) attend_paged = nullptr;
+decltype(&moe_attend_prompt_workspace) attend_prompt_workspace = nullptr;
 decltype(&moe_attend_prompt) attend_prompt = nullptr;
 
 struct Refused : std::runtime_error {  // becomes a ValueError
@@ -181,18 +182,19 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t expect, F f) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of the four entry points)
+// bind(addresses of the five entry points)
 PyObject *py_bind(PyObject *, PyObject *const *arg, Py_ssize_t n) {
-  return guarded(n, 4, [&]() -> PyObject * {
-    void *p[4];
-    for (int i = 0; i < 4; ++i) {
+  return guarded(n, 5, [&]() -> PyObject * {
+    void *p[5];
+    for (int i = 0; i < 5; ++i) {
       p[i] = PyLong_AsVoidPtr(arg[i]);
       if (!p[i]) throw std::runtime_error("no address");
     }
     qkv_append = reinterpret_cast<decltype(qkv_append)>(p[0]);
     attend_paged_workspace = reinterpret_cast<decltype(attend_paged_workspace)>(p[1]);
     attend_paged = reinterpret_cast<decltype(attend_paged)>(p[2]);
-    attend_prompt = reinterpret_cast<decltype(attend_prompt)>(p[3]);
+    attend_prompt_workspace = reinterpret_cast<decltype(attend_prompt_workspace)>(p[3]);
+    attend_prompt = reinterpret_cast<decltype(attend_prompt)>(p[4]);
     Py_RETURN_NONE;
   });
 }
@@ -378,18 +380,25 @@ PyObject *py_prompt(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     io.scale = arg[6] == Py_None ? float(1.0 / std::sqrt(double(D))) : float(number(arg[6]));
     const at::Tensor *given = optional_tensor(arg[7], "out");
     const bool return_lse = flag(arg[8]);
-    at::Tensor out, lse;
+    at::Tensor out, lse, workspace;
     moe_status_t s;
     {
       const WithoutGil free;
       const c10::cuda::CUDAGuard guard(kind.device);
-      out = output(given, q, kind, io.out_stride);
-      if (return_lse) {
-        lse = make({T, H}, at::kFloat, kind);
-        io.lse = static_cast<float *>(lse.data_ptr());
+      s = attend_prompt_workspace(&io, &io.workspace_bytes);
+      if (s == MOE_OK) {
+        out = output(given, q, kind, io.out_stride);
+        if (return_lse) {
+          lse = make({T, H}, at::kFloat, kind);
+          io.lse = static_cast<float *>(lse.data_ptr());
+        }
+        if (io.workspace_bytes > 0) {
+          workspace = make({io.workspace_bytes}, at::kByte, kind);
+          io.workspace = workspace.data_ptr();
+        }
+        io.q = q.data_ptr(), io.k = k.data_ptr(), io.v = v.data_ptr(), io.out = out.data_ptr();
+        s = attend_prompt(&io, word, stream_of(kind));
       }
-      io.q = q.data_ptr(), io.k = k.data_ptr(), io.v = v.data_ptr(), io.out = out.data_ptr();
-      s = attend_prompt(&io, word, stream_of(kind));
     }
     return s != MOE_OK ? PyLong_FromLong(s) : outputs(out, lse);
   });

@@ -662,6 +662,46 @@ def test_prompt_mostly_empty_sequences():
     run_prompt(seqs, 4, 2, 64, "bf16", True, seed=61)
 
 
+@pytest.mark.parametrize("seqs,H,K,D,dtype,causal", [
+    ([(1, 2100)], 1, 1, 128, "bf16", True),
+    ([(7, 5000)], 8, 2, 64, "fp16", True),
+    ([(70, 3333)], 4, 1, 128, "fp16", True),                         # two row tiles
+    ([(130, 2300)], 2, 2, 128, "bf16", False),
+    ([(3, 4096), (0, 50), (5, 0), (9, 60), (2, 1500)], 4, 2, 64, "bf16", True),  # parts of one, two and more
+    ([(2200, 2200)], 1, 1, 64, "bf16", True),                        # rows that see no key of the later parts
+    ([(20, 2500)], 130, 1, 64, "bf16", True),
+])
+def test_prompt_few_rows_many_keys(seqs, H, K, D, dtype, causal):
+    """The keys split over the GPU, and the same without a workspace."""
+    run_prompt(seqs, H, K, D, dtype, causal, seed=H + D)
+    gen = torch.Generator("cuda").manual_seed(70)
+    n, m = sum(s[0] for s in seqs), sum(s[1] for s in seqs)
+    make = lambda r, h: torch.randn(r, h, D, device="cuda", generator=gen).to(ac.TORCH[dtype])
+    q, k, v = make(n, H), make(m, K), make(m, K)
+    cu = [ac.i32(ac.offsets([s[i] for s in seqs])) for i in range(2)]
+    st = status()
+    split, z = attention.attend_prompt(q, k, v, *cu, causal=causal, return_lse=True, d_status=st)
+    for _ in range(3):
+        again = attention.attend_prompt(q, k, v, *cu, causal=causal, d_status=st)
+        assert torch.equal(again, split)
+    out, lse = torch.full_like(q, 3.0), torch.zeros(n, H, device="cuda")
+    io = abi.MoeAttendPromptIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), H * D, K * D, K * D, out.data_ptr(), H * D,
+                               lse.data_ptr(), cu[0].data_ptr(), cu[1].data_ptr(), len(seqs), n, m, H, K, D,
+                               abi.MOE_DTYPE_BF16 if dtype == "bf16" else abi.MOE_DTYPE_F16, int(causal), D ** -0.5)
+    bytes = abi.moe_attend_prompt_workspace(io)
+    assert bytes > 0
+    assert abi.moe_attend_prompt(io, st, torch.cuda.current_stream()) == abi.MOE_OK and st.item() == abi.MOE_OK
+    # both are within their bounds of one result: two roundings of o, and the probabilities' roundings of values of
+    # about 1 (at most half a step of each value's weight, twice)
+    half = ac.HALF_STEP[dtype]
+    v_top = v.float().abs().max().item()
+    assert ((out.float() - split.float()).abs() <= 2 * half * (out.float().abs() + 1.1 * v_top)).all()
+    assert ((lse - z).abs()[torch.isfinite(z)] <= 1e-4).all() and torch.equal(torch.isinf(lse), torch.isinf(z))
+    small = torch.empty(bytes - 4, dtype=torch.uint8, device="cuda")
+    io.workspace, io.workspace_bytes = small.data_ptr(), bytes - 4
+    assert abi.moe_attend_prompt(io, st, torch.cuda.current_stream()) == abi.MOE_ERR_INVALID_ARG
+
+
 def test_wrapper_refusals():
     """What the wrappers and entry points refuse, before anything runs on the GPU."""
     z = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype, device="cuda")
