@@ -11,12 +11,12 @@
 //
 // Bound. 4 D flops per (row, head, key) against 16-bit inputs read once: the
 // tensor pipe, for all but the shortest prompts. 16,384 tokens (32 + 8 heads of
-// 128) take 1.38 ms, 1.59 PFLOP/s or 84 % of the measured bf16 rate, at the power
+// 128) take 1.40 ms, 1.57 PFLOP/s or 83 % of the measured bf16 rate, at the power
 // limit. A pair of row tiles costs 1.5 us for a key tile (1.06 of MMAs) and 4.4 us
 // beside them (first loads, the first and last softmax, output), so 16 packed
-// prompts with few key tiles each take 77 us where their MMAs need 35. D = 64: an MMA
+// prompts with few key tiles each take 78 us where their MMAs need 35. D = 64: an MMA
 // with N = 64 takes as long as one with 128, so the value product has half the rate:
-// three chunks behind 4,000 tokens 140 us, of which 88 for the MMAs. 257 tokens: 11.4.
+// three chunks behind 4,000 tokens 139 us, of which 88 for the MMAs. 257 tokens: 11.4.
 //
 // Layout. A row of the tile is a (token, head) pair: the G heads of a kv head's
 // group are packed, r = token * G + head, so one key tile serves all of them and
@@ -46,7 +46,7 @@
 // A block goes from work to work without stopping: its barriers and TMEM stay, and
 // the next Q, K and V are loaded while the last softmax and the output of this work
 // run. With a block for each work these cost 6.5 us in place of 4.4 (16 packed
-// prompts 90 us, 16,384 tokens 1.40 ms, 257 tokens 10.3).
+// prompts 90 us, 4,096 prompts of 30 tokens 11.4 ms against 1.09, 257 tokens 10.3).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -100,10 +100,10 @@ struct Work {
   int kv, head0;     // kv head, the first of the block's heads
   int tiles0, tiles1;  // key tiles of row tiles A and B
   int valid;           // 0: there is no further work
-  int skip, parts, slot;  // keys of the sequence before key0; parts of this tile, and where this one goes
   // where the barriers stand when it begins: steps, S of each row tile, entries of the ring (each modulo twice its
   // ring), and the phases of o_full
   int step0, s0, s1, entry0, o0, o1;
+  int skip, parts, slot;  // keys of the sequence before key0; parts of this tile, and where this one goes
 
   __device__ __forceinline__ int tiles(int x) const { return x ? tiles1 : tiles0; }
   __device__ __forceinline__ int both() const { return min(tiles0, tiles1); }  // key tiles that both have
@@ -287,9 +287,9 @@ __device__ __forceinline__ Work find_work(const PromptArgs &a, TileCursor &curso
   w.tiles0 = key_tiles(w.t0);
   w.tiles1 = key_tiles(w.t0 + a.tokens);
   w.step0 = w.s0 = w.s1 = w.entry0 = w.o0 = w.o1 = 0;
-  w.skip = 0, w.parts = 1, w.slot = slot;
   if constexpr (SPLIT) {  // equal parts, of kSplitTiles key tiles at least
     const int all = w.all(), most = min(a.splits, max(1, all / kSplitTiles)), per = max(1, (all + most - 1) / most);
+    w.slot = slot;
     w.parts = max(1, (all + per - 1) / per);
     if (part >= w.parts) w.valid = 0;
     w.skip = part * per * kKeys;
@@ -688,7 +688,7 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
   }
   // O / sum. Rows of 256 bytes go through the warp's own shared memory, 64 values of 32 rows at a time, and out by whole
   // pieces of rows (16-byte pieces exchanged by row, against bank conflicts); rows of 128 straight from their threads.
-  // 16,384 tokens with D = 128: 1.37 ms, 1.41 straight; chunks with D = 64: 140 us straight, 145 through shared memory.
+  // 16 packed prompts with D = 128: 77 us, 81 straight; chunks with D = 64: 140 us straight, 145 through shared memory.
   const float inv = total > 0.0f ? 1.0f / total : 0.0f;
   const bool any = limit > 0;  // a row without keys has no accumulator of its own
   const auto load_out = [&](int first, uint32_t (&v)[16]) {  // 32 values of the row from the first on
