@@ -153,6 +153,7 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
 
     q [rows][heads][D], k and v [keys][kv heads][D]; cu_rows, cu_keys int32 [sequences + 1]. Row i of a sequence
     with n rows and m keys sees keys 0 .. m - n + i (causal), or all m. Rows that see no key give 0 and lse -inf.
+    Few rows over many keys are computed in parts (the sizes of the tensors decide, not their contents).
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """

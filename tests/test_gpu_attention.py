@@ -702,6 +702,34 @@ def test_prompt_few_rows_many_keys(seqs, H, K, D, dtype, causal):
     assert abi.moe_attend_prompt(io, st, torch.cuda.current_stream()) == abi.MOE_ERR_INVALID_ARG
 
 
+def test_split_prompts_in_graphs_and_on_streams():
+    """Two captured calls with split keys replayed at once, following the offsets of their replay."""
+    gen = torch.Generator("cuda").manual_seed(71)
+    calls = []
+    for n, m in ((5, 3000), (40, 2500)):
+        x = torch.randn(m, 4, 64, device="cuda", generator=gen).bfloat16()
+        calls.append((x[:n, :2], x[:, 2:3], x[:, 3:], ac.i32([0, n]), ac.i32([0, m])))
+    graphs, outs = [], []
+    for c in calls:
+        attention.attend_prompt(*c)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(attention.attend_prompt(*c))
+        graphs.append(g)
+    for ends in ((3000, 2500), (1700, 900), (3, 2500)):
+        for c, m in zip(calls, ends):
+            c[4].copy_(torch.tensor([0, m], dtype=torch.int32))
+        want = [attention.attend_prompt(*c) for c in calls]
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
 def test_wrapper_refusals():
     """What the wrappers and entry points refuse, before anything runs on the GPU."""
     z = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype, device="cuda")
