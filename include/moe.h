@@ -486,8 +486,9 @@ moe_status_t moe_attend_paged_workspace(const moe_attend_paged_io_t *io, const m
  * length L sees the keys 0 .. L - n + i (the rows are its last n tokens):
  *   s_j = scale * (q . K_j),  out = sum_j softmax(s)_j V_j,  lse = log sum_j exp s_j
  * with K, V the values the cache stands for. A row that sees no key (L < n)
- * gets out = 0 and lse = -inf. Rows of q past cu_rows[num_seqs] are not
- * touched. Sums and statistics are binary32, probabilities f16. A scale code of
+ * gets out = 0 and lse = -inf, and so does one whose scores are all -inf. A NaN
+ * or +inf among a row's scores (or a score past binary32) makes its out and lse
+ * NaN. Rows of q past cu_rows[num_seqs] are not touched. Sums and statistics are binary32, probabilities f16. A scale code of
  * 0 counts as zero; of the values (and of a query row) parts below 2^-23 of the
  * largest may lose bits. A NaN among the values of a key can reach earlier rows of
  * its own sequence (their weight of it is 0, and 0 * NaN is NaN). A sequence with a

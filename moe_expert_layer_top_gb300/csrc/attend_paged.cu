@@ -653,7 +653,7 @@ __device__ __forceinline__ void store4(const PagedArgs &a, const Seq &s, int kv,
 __device__ __forceinline__ void store_lse(const PagedArgs &a, const Seq &s, int kv, int r, float ref, float sum) {
   if (!a.lse) return;
   const int tok = r / a.group, h = kv * a.group + r - tok * a.group;
-  a.lse[int64_t(s.row0 + tok) * a.num_heads + h] = sum > 0.0f ? (log2f(sum) + ref) * 0.6931471805599453f : -INFINITY;
+  a.lse[int64_t(s.row0 + tok) * a.num_heads + h] = sum != 0.0f ? (log2f(sum) + ref) * 0.6931471805599453f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ main kernel
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
         }
         if (whole) {
           if (rr < rows) {
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
             store4<T>(a, seg.s, seg.kv, seg.r0 + rr, D, d,
                       l != 0.0f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0, 0, 0, 0));
             if (d == 0) store_lse(a, seg.s, seg.kv, seg.r0 + rr, m, l);
@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const Pa
     if (b < parts) add(v[b], weight[row][b]);
 #pragma unroll 8
   for (int b = kAhead; b < parts; ++b) add(*reinterpret_cast<const float4 *>(part(b) + at), weight[row][b]);
-  const float l = sum[row], inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float l = sum[row], inv = l != 0.0f ? 1.0f / l : 0.0f;
   store4<T>(a, p.s, kv, r0 + row0 + row, D, d,
             l != 0.0f ? make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv) : make_float4(0, 0, 0, 0));
   if (d == 0) store_lse(a, p.s, kv, r0 + row0 + row, top[row], l);

@@ -689,7 +689,7 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
   // O / sum. Rows of 256 bytes go through the warp's own shared memory, 64 values of 32 rows at a time, and out by whole
   // pieces of rows (16-byte pieces exchanged by row, against bank conflicts); rows of 128 straight from their threads.
   // 16 packed prompts with D = 128: 77 us, 81 straight; chunks with D = 64: 140 us straight, 145 through shared memory.
-  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  const float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a NaN stays one
   const bool any = limit > 0;  // a row without keys has no accumulator of its own
   const auto load_out = [&](int first, uint32_t (&v)[16]) {  // 32 values of the row from the first on
     uint32_t o[32];
@@ -753,7 +753,7 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
   }
   if (real && a.lse)
     a.lse[int64_t(w.row0 + t) * a.num_heads + h] =
-        total > 0.0f ? (log2f(total) + ref * a.scale2) * 0.6931471805599453f : -INFINITY;
+        total != 0.0f ? (log2f(total) + ref * a.scale2) * 0.6931471805599453f : -INFINITY;
   return true;
 }
 
@@ -878,13 +878,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const PromptA
       const float4 v = *reinterpret_cast<const float4 *>(from + p * kPart + row * D + 4 * lane);
       o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
     }
-    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+    const float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a NaN stays one, also of a part whose O has no weight
     if (lane < D / 4)
       *reinterpret_cast<uint2 *>(a.out + int64_t(w.row0 + t) * a.out_stride + int64_t(h) * D + 4 * lane) =
           total != 0.0f ? make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)) : make_uint2(0, 0);
     if (lane == 0 && a.lse)
       a.lse[int64_t(w.row0 + t) * a.num_heads + h] =
-          total > 0.0f ? (log2f(total) + top) * 0.6931471805599453f : -INFINITY;
+          total != 0.0f ? (log2f(total) + top) * 0.6931471805599453f : -INFINITY;
   }
 }
 
