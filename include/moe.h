@@ -492,8 +492,8 @@ moe_status_t moe_attend_paged_workspace(const moe_attend_paged_io_t *io, const m
  * 0 counts as zero; of the values (and of a query row) parts below 2^-23 of the
  * largest may lose bits. A NaN among the values of a key can reach earlier rows of
  * its own sequence (their weight of it is 0, and 0 * NaN is NaN). A sequence with a
- * page, length or offset out of range has unspecified results; the others have
- * theirs. out must not overlap q. workspace: 16-byte aligned device memory of at least the size
+ * page, length or offset out of range, or whose rows overlap another one's (possible
+ * only where cu_rows decreases), has unspecified results; the others have theirs. out must not overlap q. workspace: 16-byte aligned device memory of at least the size
  * above; its content before the call does not matter, and calls that may
  * overlap on the GPU need one each. Results do not depend on timing: the same
  * call gives the same bits. */
@@ -531,8 +531,10 @@ moe_status_t moe_attend_prompt_workspace(const moe_attend_prompt_io_t *io, int64
  * a key or value of one sequence never reaches another sequence, and one in a key
  * that a row does not see never reaches the row; one in a value of a later key
  * can reach earlier rows of its own sequence (0 * NaN is NaN). A sequence with an
- * offset out of range gets no result; the others have theirs. out must not
- * overlap the inputs. A workspace smaller than moe_attend_prompt_workspace says
+ * offset of its rows or keys out of range or out of order gets no result: its rows
+ * are not touched. The others have theirs, unless two of them overlap (possible only
+ * where cu_rows decreases): the rows of both are unspecified then, and rows of later
+ * sequences may be left as they were. out must not overlap the inputs. A workspace smaller than moe_attend_prompt_workspace says
  * is MOE_ERR_INVALID_ARG; calls that may overlap on the GPU need one each. */
 moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_status, void *cuda_stream);
 

@@ -129,9 +129,9 @@ __device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b, int32_t *stat
   Seq s = {b, 0, 0, 0, 0, 0};
   if (b >= a.num_seqs) return s;
   const Span r = seq_span(a.cu_rows, b, a.num_rows, status);
+  if (r.n <= 0) return s;
   s.row0 = r.first;
   s.n = r.n;
-  if (r.n == 0) return s;
   const int cap = a.max_pages * a.page_size;
   int len = __ldg(a.lengths + b);
   if (len < 0 || len > cap) {

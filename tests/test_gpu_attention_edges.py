@@ -95,3 +95,55 @@ def test_paged_lse_of_a_poisoned_query(D, dtype, rows, length, poison):
     hit[rows - 1, 1] = True
     assert torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
     assert torch.equal(lse[~hit], z[~hit]) and torch.equal(out[~hit], want[~hit])
+
+
+# ------------------------------------------------------------------ offsets out of order
+
+ORDERED = [5 * b for b in range(101)]
+
+
+def offset_cases():
+    yield [0, 100, 2 ** 30, 300, 400, 500], ORDERED[:5] + [500]     # far out of range: two sequences are without rows
+    yield [-5, 300, 300, 400, 500], [0, 300, 300, 400, 500]
+    yield [0, 300, 300, 400, 500], [0, 300, 200, 450, 500]          # the keys' alone
+    for at in (3, 31, 32, 33, 64, 97):                              # in, at the end of and behind a warp's 32 sequences
+        for wrong in (-1, 501, 2 ** 31 - 1):
+            yield ORDERED[:at] + [wrong] + ORDERED[at + 1:], ORDERED
+        yield ORDERED, ORDERED[:at] + [-1] + ORDERED[at + 1:]
+
+
+@pytest.mark.parametrize("keys_behind", [0, 3000])  # with split keys too
+def test_prompt_with_an_offset_out_of_order(keys_behind):
+    """The sequences in order have the results that they have alone, the rows of the others are not touched."""
+    H, K, D, T = 8, 2, 64, 500
+    m = T + keys_behind
+    q, k, v = seeded(20, T, H, D).bfloat16(), seeded(21, m, K, D).bfloat16(), seeded(22, m, K, D).bfloat16()
+    top = v.float().abs().max()
+    for rows, keys in offset_cases():
+        keys = keys[:-1] + [keys[-1] + keys_behind]
+        out = torch.full((T, H, D), 7.0, device="cuda").bfloat16()
+        st = status()
+        attention.attend_prompt(q, k, v, ac.i32(rows), ac.i32(keys), out=out, d_status=st)
+        assert st.item() == abi.MOE_ERR_DEVICE_BOUNDS
+        want = torch.full_like(out, 7.0)
+        for b in range(len(rows) - 1):
+            if not (0 <= rows[b] < rows[b + 1] <= T and 0 <= keys[b] <= keys[b + 1] <= m):
+                continue
+            x, y = slice(rows[b], rows[b + 1]), slice(keys[b], keys[b + 1])
+            got = attention.attend_prompt(q[x], k[y], v[y], ac.i32([0, x.stop - x.start]), ac.i32([0, y.stop - y.start]))
+            # alone, the keys may be split otherwise: both are within their bounds of one result
+            assert ((out[x].float() - got.float()).abs() <= 2 * 2.0 ** -8 * (got.float().abs() + 1.1 * top)).all()
+            assert not (out[x] == 7).all(-1).any()
+            want[x] = out[x]
+        assert torch.equal(out, want), (rows, keys)
+
+
+def test_prompt_with_overlapping_sequences():
+    """More tiles than the grid is made for: reported, and nothing outside of the sequences' rows is touched."""
+    H, K, D, T = 4, 1, 64, 520
+    q, k, v = seeded(23, T, H, D).bfloat16(), seeded(24, T, K, D).bfloat16(), seeded(25, T, K, D).bfloat16()
+    cu = ac.i32([0, 300, 100, 400, 500])
+    out, st = torch.full((T, H, D), 7.0, device="cuda").bfloat16(), status()
+    attention.attend_prompt(q, k, v, cu, ac.i32([0, 300, 300, 400, 500]), out=out, d_status=st)
+    assert st.item() == abi.MOE_ERR_DEVICE_BOUNDS
+    assert (out[500:] == 7).all() and not (out[:100] == 7).all(-1).any()
