@@ -33,24 +33,32 @@ import torch
 from . import abi, build
 
 _module = None
+_bound = None  # the library (abi.load()) whose entry points the module calls
 
 
 def _native():
-    """The module that takes the tensors apart (csrc/attention_torch.cpp), bound to the loaded library."""
-    global _module
-    if _module is None:
+    """The module that takes the tensors apart (csrc/attention_torch.cpp), bound to the library that abi has loaded:
+    after a change to another one (the bounds-checked build) the next call goes there."""
+    global _bound
+    lib = abi._lib or abi.load()
+    if lib is not _bound:
         import ctypes
-        lib = abi.load()
-        if not os.path.exists(build.TORCH_LIB_PATH):
-            raise RuntimeError(f"not built: {build.TORCH_LIB_PATH} (run __graft_entry__.build())")
-        spec = importlib.util.spec_from_file_location("attention_torch", build.TORCH_LIB_PATH)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        (_module or _load()).bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "moe_qkv_append", "moe_attend_paged_workspace", "moe_attend_paged", "moe_attend_prompt_workspace",
             "moe_attend_prompt")))
-        _module = module
+        _bound = lib
     return _module
+
+
+def _load():
+    global _module
+    if not os.path.exists(build.TORCH_LIB_PATH):
+        raise RuntimeError(f"not built: {build.TORCH_LIB_PATH} (run __graft_entry__.build())")
+    spec = importlib.util.spec_from_file_location("attention_torch", build.TORCH_LIB_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _module = module
+    return module
 
 
 class KVCacheMXFP4:
@@ -62,7 +70,7 @@ class KVCacheMXFP4:
     __slots__ = ("_parts",)
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor):
-        (_module or _native()).check_cache(k_codes, k_scales, v_codes, v_scales)
+        _native().check_cache(k_codes, k_scales, v_codes, v_scales)
         self._parts = (k_codes, k_scales, v_codes, v_scales)
 
     k_codes = property(lambda self: self._parts[0])
@@ -124,7 +132,7 @@ def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: 
     Returns {"q"}, plus "k" (rotated keys in 16 bits) with rotated_keys, plus "k_cached" and "v_cached" (the
     values that the 4-bit cache keeps) with cached_values.
     """
-    return _call("moe_qkv_append", (_module or _native()).append, stream, q, k, v, positions, rope, interleaved, q_norm,
+    return _call("moe_qkv_append", _native().append, stream, q, k, v, positions, rope, interleaved, q_norm,
                  k_norm, eps, cache, slots, q_out, rotated_keys, cached_values, d_status)
 
 
@@ -142,7 +150,7 @@ def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor,
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
-    return _call("moe_attend_paged", (_module or _native()).paged, stream, q, cache, page_table, lengths, cu_rows,
+    return _call("moe_attend_paged", _native().paged, stream, q, cache, page_table, lengths, cu_rows,
                  max_rows, scale, out, return_lse, d_status)
 
 
@@ -157,5 +165,5 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
-    return _call("moe_attend_prompt", (_module or _native()).prompt, stream, q, k, v, cu_rows, cu_keys, causal, scale,
+    return _call("moe_attend_prompt", _native().prompt, stream, q, k, v, cu_rows, cu_keys, causal, scale,
                  out, return_lse, d_status)

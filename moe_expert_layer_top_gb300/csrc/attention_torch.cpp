@@ -6,7 +6,8 @@
 // fifteen tensors. Here a call takes 8 to 12 us: about 1 us of checks, 1.5 for
 // letting go of the interpreter lock, the rest allocations and launches.
 // The entry points' addresses come from the loaded library (normal or
-// bounds-checked); nothing is kept between calls.
+// bounds-checked) and change when another one is loaded; nothing else is kept
+// between calls.
 #include <Python.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>

@@ -1,0 +1,41 @@
+"""The attention's PyTorch module and the library that it calls. No GPU is needed."""
+import ctypes
+import types
+
+import pytest
+
+import moe_expert_layer_top_gb300 as pkg
+from moe_expert_layer_top_gb300 import abi, attention
+
+ENTRIES = ("moe_qkv_append", "moe_attend_paged_workspace", "moe_attend_paged", "moe_attend_prompt_workspace",
+           "moe_attend_prompt")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    pkg.build.build()
+
+
+def addresses(lib):
+    return tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in ENTRIES)
+
+
+def test_calls_follow_a_change_of_the_library(monkeypatch):
+    """A process that goes on to the bounds-checked library, and back, does not stay with the first one's kernels."""
+    bound = []
+    fake = types.SimpleNamespace(bind=lambda *a: bound.append(a))
+    monkeypatch.setattr(attention, "_module", fake)
+    monkeypatch.setattr(attention, "_bound", None, raising=False)
+    want = []
+    for debug in ("0", "1", "0"):
+        monkeypatch.setenv("MOE_DEBUG_BOUNDS", debug)
+        monkeypatch.setattr(abi, "_lib", None)
+        lib = abi.load()
+        assert attention._native() is fake and attention._native() is fake
+        want.append(addresses(lib))
+    assert want[0] != want[1]
+    assert bound == want  # once for each change
+
+
+def test_the_module_loads_once():
+    assert attention._native() is attention._native()
