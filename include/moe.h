@@ -67,7 +67,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 4
+#define MOE_ABI_VERSION 5
 
 typedef enum {
   MOE_OK = 0,
@@ -103,7 +103,10 @@ typedef enum {
  * The down units of that tile then give
  * up after wait_timeout_ns, and MOE_ERR_TIMEOUT appears in *d_status; y is
  * undefined for that step. The GPU does not fault or hang, and the next
- * moe_forward on a plan without this flag is unaffected. */
+ * moe_forward on a plan without this flag is unaffected.
+ * In moe_attend_prompt: the mark that a sequence's last, partial tile of values
+ * is ready is never set. The products that wait for it give up, with the same
+ * consequences. */
 
 #define MOE_FLAG_TEST_BOUNDS (1u << 9)
 /* Test hook of the bounds-checked build (libmoe_debug.so, compiled with
@@ -391,7 +394,8 @@ moe_status_t moe_forward_static_scratch(const moe_config_t *config, const moe_we
  *
  * Sizes that live in device memory (lengths, offsets, pages, slots,
  * positions) are checked by the kernels. What is out of range is not accessed,
- * and MOE_ERR_DEVICE_BOUNDS is stored in *d_status. Unlike the plan's calls,
+ * and MOE_ERR_DEVICE_BOUNDS is stored in *d_status (moe_attend_prompt may also
+ * store MOE_ERR_TIMEOUT). Unlike the plan's calls,
  * these never store MOE_OK: the caller sets the word to MOE_OK once, and a
  * later check covers every call made until then. d_status NULL: such errors
  * are not reported.
@@ -485,18 +489,20 @@ moe_status_t moe_attend_paged_workspace(const moe_attend_paged_io_t *io, const m
 /* Attention over the paged MXFP4 cache. Row i of the n rows of a sequence of
  * length L sees the keys 0 .. L - n + i (the rows are its last n tokens):
  *   s_j = scale * (q . K_j),  out = sum_j softmax(s)_j V_j,  lse = log sum_j exp s_j
- * with K, V the values the cache stands for. A row that sees no key (L < n)
- * gets out = 0 and lse = -inf, and so does one whose scores are all -inf. A NaN
- * or +inf among a row's scores (or a score past binary32) makes its out and lse
- * NaN. Rows of q past cu_rows[num_seqs] are not touched. Sums and statistics are binary32, probabilities f16. A scale code of
- * 0 counts as zero; of the values (and of a query row) parts below 2^-23 of the
- * largest may lose bits. A NaN among the values of a key can reach earlier rows of
- * its own sequence (their weight of it is 0, and 0 * NaN is NaN). A sequence with a
- * page, length or offset out of range, or whose rows overlap another one's (possible
- * only where cu_rows decreases), has unspecified results; the others have theirs. out must not overlap q. workspace: 16-byte aligned device memory of at least the size
- * above; its content before the call does not matter, and calls that may
- * overlap on the GPU need one each. Results do not depend on timing: the same
- * call gives the same bits. */
+ * with K, V the values the cache stands for. A row that sees no key (L < n) gets
+ * out = 0 and lse = -inf, and so does one whose scores are all -inf. A NaN or
+ * +inf among a row's scores (or a score past binary32) makes its out and lse
+ * NaN. Rows of q past cu_rows[num_seqs] are not touched. Sums and statistics are
+ * binary32, probabilities f16. A scale code of 0 counts as zero; of the values
+ * (and of a query row) parts below 2^-23 of the largest may lose bits. A NaN
+ * among the values of a key can reach earlier rows of its own sequence (their
+ * weight of it is 0, and 0 * NaN is NaN). A sequence with a page, length or
+ * offset out of range, or whose rows overlap another one's (possible only where
+ * cu_rows decreases), has unspecified results; the others have theirs. out must
+ * not overlap q. workspace: 16-byte aligned device memory of at least the size
+ * above; its content before the call does not matter, and calls that may overlap
+ * on the GPU need one each. Results do not depend on timing: the same call gives
+ * the same bits. */
 moe_status_t moe_attend_paged(const moe_attend_paged_io_t *io, const moe_kv_cache_t *cache, void *workspace,
                               int64_t workspace_bytes, int32_t *d_status, void *cuda_stream);
 
@@ -517,6 +523,7 @@ typedef struct moe_attend_prompt_io {
   void *workspace;            /* optional, 16-byte aligned device memory: lets few rows over many keys spread over the
                                * GPU (the keys are split and the parts joined); NULL: each row's keys in one pass */
   int64_t workspace_bytes;
+  uint32_t flags;             /* 0, or MOE_FLAG_TEST_SKIP_READY */
 } moe_attend_prompt_io_t;
 
 /* Bytes of workspace that moe_attend_prompt can use for these sizes (the
@@ -525,16 +532,20 @@ typedef struct moe_attend_prompt_io {
 moe_status_t moe_attend_prompt_workspace(const moe_attend_prompt_io_t *io, int64_t *bytes_out);
 
 /* Attention over packed prompts, or over chunks of prompts with the keys that
- * precede them (m > n). Formula and empty rows as for moe_attend_paged. The
- * rows behind the last sequence are not touched. Sums and statistics are
- * binary32, probabilities are rounded to the inputs' type. A NaN or infinity in
- * a key or value of one sequence never reaches another sequence, and one in a key
- * that a row does not see never reaches the row; one in a value of a later key
- * can reach earlier rows of its own sequence (0 * NaN is NaN). A sequence with an
- * offset of its rows or keys out of range or out of order gets no result: its rows
- * are not touched. The others have theirs, unless two of them overlap (possible only
- * where cu_rows decreases): the rows of both are unspecified then, and rows of later
- * sequences may be left as they were. out must not overlap the inputs. A workspace smaller than moe_attend_prompt_workspace says
+ * precede them (m > n). Formula and empty rows as for moe_attend_paged. The rows
+ * behind the last sequence are not touched. Sums and statistics are binary32,
+ * probabilities are rounded to the inputs' type. A NaN or infinity in a key or
+ * value of one sequence never reaches another sequence, and one in a key that a
+ * row does not see never reaches the row; one in a value of a later key can
+ * reach earlier rows of its own sequence (0 * NaN is NaN). A sequence with an
+ * offset of its rows or keys out of range or out of order gets no result: its
+ * rows are not touched. The others have theirs, unless two of them overlap
+ * (possible only where cu_rows decreases): the rows of both are unspecified
+ * then, and rows of later sequences may be left as they were. The kernel's parts
+ * wait for one another; if such a wait does not end within a second,
+ * MOE_ERR_TIMEOUT is stored in *d_status, the kernel ends by itself, and the
+ * call's results are unspecified (the next call is not affected). out must not
+ * overlap the inputs. A workspace smaller than moe_attend_prompt_workspace says
  * is MOE_ERR_INVALID_ARG; calls that may overlap on the GPU need one each. */
 moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_status, void *cuda_stream);
 

@@ -12,7 +12,7 @@ import os
 
 from . import build as _build
 
-MOE_ABI_VERSION = 4
+MOE_ABI_VERSION = 5
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = 1
@@ -176,6 +176,7 @@ class MoeAttendPromptIO(ctypes.Structure):
         ("scale", ctypes.c_float),
         ("workspace", _P),
         ("workspace_bytes", ctypes.c_int64),
+        ("flags", ctypes.c_uint32),
     ]
 
 

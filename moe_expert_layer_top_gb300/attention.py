@@ -14,7 +14,8 @@ PyTorch only supplies device memory and streams here; every step runs in
 libmoe.so, and a failed call raises. Sizes that live on the device (lengths,
 pages, slots, positions) are checked there: pass ``d_status``, an int32 tensor
 set to MOE_OK, and look at it when convenient (MOE_ERR_DEVICE_BOUNDS: something
-was out of range and was not accessed).
+was out of range and was not accessed; MOE_ERR_TIMEOUT: a wait inside the prompt
+kernel did not end within a second, and the results are unspecified).
 
 The calls run on the tensors' device and on its current stream unless ``stream``
 is given. Outputs and workspaces come from PyTorch's allocator, on the stream

@@ -69,7 +69,9 @@ constexpr int kRegsLaunch = 168, kRegsSoftmax = 224, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "register split");
 constexpr int kWarpLoad = 8, kWarpMma = 9;
 constexpr uint32_t kTmemCols = 512;
-constexpr int64_t kWaitNs = 1000000000;  // bound of every wait
+// Bound of every wait. A constant: with one from the caller 16,384 tokens took 1.54 ms in place of 1.50, 16 packed prompts
+// 82.2 us in place of 80.9.
+constexpr int64_t kWaitNs = 1000000000;
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
 // Key tiles of a part, at least. 64 rows over 4,096 keys: 29 us with 4 (or 2), 32 with 8, 43 with 16, 58 in one part.
 constexpr int kSplitTiles = 4;
@@ -88,6 +90,7 @@ struct PromptArgs {
   float scale2;    // |scale| log2 e, at least 2^-100: scores times this are exponents of two
   bool negative;   // the scale is: scores change sign
   int32_t *status;
+  bool skip_tail;  // test hook: the mark of a zeroed last V tile is never set
   int splits;    // parts that a work's keys may be split into
   float *parts;  // workspace: of each part, O and (reference, sum) of its 256 rows
 };
@@ -409,7 +412,7 @@ __device__ void load_warp(const CUtensorMap *qmap, const CUtensorMap *kmap, cons
       }
     }
     __syncwarp();
-    if (ok && lane == 0) mbar_arrive(&sm.tail[t & 3]);
+    if (ok && lane == 0 && !a.skip_tail) mbar_arrive(&sm.tail[t & 3]);
     base += issued;
     const Work was = w;
     w.valid = 0;
@@ -981,6 +984,7 @@ cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *stat
   a.splits = io.workspace ? splits_of(a, io.num_keys, num_sms) : 1;
   a.parts = static_cast<float *>(io.workspace);
   a.causal = io.causal;
+  a.skip_tail = io.flags & MOE_FLAG_TEST_SKIP_READY;
   a.scale2 = fmaxf(fabsf(io.scale) * 1.4426950408889634f, 0x1p-100f);
   a.negative = io.scale < 0.0f;
   a.status = status;

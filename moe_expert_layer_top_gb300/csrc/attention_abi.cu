@@ -175,7 +175,7 @@ moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_stat
   if (!io) return MOE_ERR_INVALID_ARG;
   moe_status_t s = prompt_sizes_ok(*io);
   if (s != MOE_OK) return s;
-  if (io->causal != 0 && io->causal != 1) return MOE_ERR_INVALID_ARG;
+  if ((io->causal != 0 && io->causal != 1) || io->flags & ~MOE_FLAG_TEST_SKIP_READY) return MOE_ERR_INVALID_ARG;
   if (!finite(io->scale) || !aligned(d_status, 4) || !aligned(io->lse, 4)) return MOE_ERR_INVALID_ARG;
   if (io->num_rows == 0 || io->num_seqs == 0) return MOE_OK;
   const int64_t D = io->head_dim;

@@ -39,3 +39,12 @@ def test_calls_follow_a_change_of_the_library(monkeypatch):
 
 def test_the_module_loads_once():
     assert attention._native() is attention._native()
+
+
+def test_prompt_flags():
+    io = abi.MoeAttendPromptIO(num_heads=8, num_kv_heads=2, head_dim=64, causal=1, scale=0.1)  # no rows: nothing runs
+    assert abi.moe_attend_prompt(io) == abi.MOE_OK
+    io.flags = abi.MOE_FLAG_TEST_SKIP_READY
+    assert abi.moe_attend_prompt(io) == abi.MOE_OK
+    io.flags = 1
+    assert abi.moe_attend_prompt(io) == abi.MOE_ERR_INVALID_ARG

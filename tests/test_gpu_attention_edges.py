@@ -147,3 +147,30 @@ def test_prompt_with_overlapping_sequences():
     attention.attend_prompt(q, k, v, cu, ac.i32([0, 300, 300, 400, 500]), out=out, d_status=st)
     assert st.item() == abi.MOE_ERR_DEVICE_BOUNDS
     assert (out[500:] == 7).all() and not (out[:100] == 7).all(-1).any()
+
+
+# ------------------------------------------------------------------ waits
+
+
+def prompt_io(q, k, v, out, lse, cr, ck, **kw):
+    (n, H, D), (m, K) = q.shape, k.shape[:2]
+    return abi.MoeAttendPromptIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), H * D, K * D, K * D, out.data_ptr(), H * D,
+                                 lse.data_ptr(), cr.data_ptr(), ck.data_ptr(), len(cr) - 1, n, m, H, K, D,
+                                 abi.MOE_DTYPE_BF16, 1, D ** -0.5, **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seqs", [[70], [70] * 200])  # one work, and several a block
+def test_prompt_wait_that_runs_out_is_reported(D, seqs):
+    """The mark that nothing sets: the waits end at their bound (a second), the status says so, the next call is right."""
+    T, H, K = sum(seqs), 8, 2
+    q, k, v = seeded(30, T, H, D).bfloat16(), seeded(31, T, K, D).bfloat16(), seeded(32, T, K, D).bfloat16()
+    cu = ac.i32(ac.offsets(seqs))
+    want, z = attention.attend_prompt(q, k, v, cu, cu, return_lse=True)
+    out, lse = torch.zeros_like(q), torch.zeros(T, H, device="cuda")
+    for flags, code in ((abi.MOE_FLAG_TEST_SKIP_READY, abi.MOE_ERR_TIMEOUT), (0, abi.MOE_OK)):
+        io, st = prompt_io(q, k, v, out, lse, cu, cu, flags=flags), status()
+        assert abi.moe_attend_prompt(io, st, torch.cuda.current_stream()) == abi.MOE_OK
+        torch.cuda.synchronize()
+        assert st.item() == code
+    assert torch.equal(out, want) and torch.equal(lse, z)
