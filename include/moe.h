@@ -115,7 +115,9 @@ typedef enum {
  * check trips at an index that is still inside the buffer, and the step
  * reports MOE_ERR_DEVICE_BOUNDS (site 6 in the
  * diagnostics). It shows the checks are live without any access out of
- * bounds; y is undefined for that step. No effect in the normal build. */
+ * bounds; y is undefined for that step. No effect in the normal build.
+ * The attention calls: half of the cached rows (moe_qkv_append) and half of the
+ * workspace (moe_attend_paged, moe_attend_prompt); without diagnostics. */
 
 /* moe_config_t.weight_format */
 #define MOE_WEIGHTS_MXFP8 0u  /* E4M3 elements, UE8M0 scale per 32 along K */
@@ -444,6 +446,7 @@ typedef struct moe_qkv_append_io {
   void *k_out;                       /* optional [T][num_kv_heads][D]: the rotated keys before 4 bits */
   void *k_cached, *v_cached;         /* optional [T][num_kv_heads][D]: the values that 4 bits keep, whether or not
                                       * the token is cached: attention over them equals attention over the cache */
+  uint32_t flags;                    /* 0, or MOE_FLAG_TEST_BOUNDS */
 } moe_qkv_append_io_t;
 
 /* Norm, rotation and append in one pass over one projection's output:
@@ -478,6 +481,7 @@ typedef struct moe_attend_paged_io {
   int32_t num_heads;          /* a multiple of the cache's num_kv_heads */
   uint32_t dtype;             /* MOE_DTYPE_*: of q and out */
   float scale;                /* of the scores, finite */
+  uint32_t flags;             /* 0, or MOE_FLAG_TEST_BOUNDS */
 } moe_attend_paged_io_t;
 
 /* Bytes of device workspace that moe_attend_paged needs for these sizes (the
@@ -523,7 +527,7 @@ typedef struct moe_attend_prompt_io {
   void *workspace;            /* optional, 16-byte aligned device memory: lets few rows over many keys spread over the
                                * GPU (the keys are split and the parts joined); NULL: each row's keys in one pass */
   int64_t workspace_bytes;
-  uint32_t flags;             /* 0, or MOE_FLAG_TEST_SKIP_READY */
+  uint32_t flags;             /* 0, or MOE_FLAG_TEST_* */
 } moe_attend_prompt_io_t;
 
 /* Bytes of workspace that moe_attend_prompt can use for these sizes (the

@@ -136,6 +136,7 @@ class MoeQkvAppendIO(ctypes.Structure):
         ("q_out", _P),
         ("k_out", _P),
         ("k_cached", _P), ("v_cached", _P),
+        ("flags", ctypes.c_uint32),
     ]
 
 
@@ -156,6 +157,7 @@ class MoeAttendPagedIO(ctypes.Structure):
         ("num_heads", ctypes.c_int32),
         ("dtype", ctypes.c_uint32),
         ("scale", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
     ]
 
 

@@ -83,6 +83,7 @@ struct PagedArgs {
   float scale2;    // |scale| log2 e, at least 2^-100
   uint32_t flip;   // 0x80008000 with a negative scale
   float *parts;    // workspace: two partial results a block
+  int64_t part_cap, cached_rows;  // partial results that it holds, rows of the cache: for the checks
   int32_t *status;
 };
 
@@ -187,7 +188,7 @@ struct List {
     }
     for (int c = warp; c < chunks; c += blockDim.x / 32) {
       const int64_t v = warp_sums(load_seq<C>(a, c * 32 + lane, nullptr).units());
-      if (lane == 31) before[c] = v;
+      if (lane == 31 && index_ok(a.status, c, kMaxSeqs / 32 + 1)) before[c] = v;
     }
     __syncthreads();
     if (warp == 0) {
@@ -333,11 +334,13 @@ struct Copier {
         const int step = i + (lane >> 1) * C::W, key = (seg.first + step) * kStageKeys + (lane & 1) * 16;
         at = kNoRow;
         if (step < seg.count && key < seg.s.len) {
-          const int pi = key / a.page_size, page = __ldg(table + pi);
+          const int pi = key / a.page_size;
+          const int page = index_ok(a.status, pi, a.max_pages) ? __ldg(table + pi) : 0;
           if (page < 0 || page >= a.num_pages)
             out_of_range(a.status);
           else
             at = (uint32_t(page) * a.num_kv_heads + seg.kv) * a.page_size + (key - pi * a.page_size);
+          if (at != kNoRow && !index_ok(a.status, int64_t(at) + 15, a.cached_rows)) at = kNoRow;
         }
       }
       constexpr int kPer = C::CODES / 512;  // copies of 16 bytes a lane, of the codes of K (and of V)
@@ -642,10 +645,15 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
   }
 }
 
+__device__ __forceinline__ bool row_ok(const PagedArgs &a, int row, int head) {
+  return index_ok(a.status, row, a.num_rows) && index_ok(a.status, head, a.num_heads);
+}
+
 // Writes row (token, head) pair r of an item: 4 dimensions from d on, or (d < 0) its log sum exp.
 template <class T>
 __device__ __forceinline__ void store4(const PagedArgs &a, const Seq &s, int kv, int r, int dims, int d, float4 v) {
   const int tok = r / a.group, h = kv * a.group + r - tok * a.group;
+  if (!row_ok(a, s.row0 + tok, h)) return;
   uint16_t *dst = a.out + int64_t(s.row0 + tok) * a.out_stride + int64_t(h) * dims + d;
   *reinterpret_cast<uint2 *>(dst) = make_uint2(T::pack(v.x, v.y), T::pack(v.z, v.w));
 }
@@ -653,6 +661,7 @@ __device__ __forceinline__ void store4(const PagedArgs &a, const Seq &s, int kv,
 __device__ __forceinline__ void store_lse(const PagedArgs &a, const Seq &s, int kv, int r, float ref, float sum) {
   if (!a.lse) return;
   const int tok = r / a.group, h = kv * a.group + r - tok * a.group;
+  if (!row_ok(a, s.row0 + tok, h)) return;
   a.lse[int64_t(s.row0 + tok) * a.num_heads + h] = sum != 0.0f ? (log2f(sum) + ref) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -674,7 +683,7 @@ struct Queries {
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         raw[k][i] = make_uint4(0, 0, 0, 0);
-        if (n < C::NT && r < seg.s.n * a.group)
+        if (n < C::NT && r < seg.s.n * a.group && row_ok(a, seg.s.row0 + tok, h))
           raw[k][i] = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(seg.s.row0 + tok) * a.q_stride +
                                                             int64_t(h) * D + 32 * i + 8 * t));
       }
@@ -799,7 +808,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
     const float unit = ue8m0_to_float(uint32_t(st.vref));
     const bool whole = seg.count == seg.s.steps;
     const int rows = seg.s.n * a.group - seg.r0;  // real rows of the block
-    float *part = a.parts + (int64_t(blockIdx.x) * 2 + (first ? 0 : 1)) * C::PART;
+    const int64_t slot_of = int64_t(blockIdx.x) * 2 + (first ? 0 : 1);
+    float *part = a.parts + slot_of * C::PART;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float f[2];
@@ -835,7 +845,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
                       l != 0.0f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0, 0, 0, 0));
             if (d == 0) store_lse(a, seg.s, seg.kv, seg.r0 + rr, m, l);
           }
-        } else {
+        } else if (index_ok(a.status, slot_of, a.part_cap)) {
           *reinterpret_cast<float4 *>(part + rr * D + d) = v;
           if (d == 0) {
             part[C::ROWS * D + rr] = m;
@@ -879,6 +889,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const Pa
   constexpr int D = C::D, kAhead = 16;
   static_assert(8 * (D / 4) <= kCombineThreads, "one thread for four dimensions of a row");
   const int parts = int(last - c) + 1;
+  if (!index_ok(a.status, parts - 1, kMaxBlocks) || !index_ok(a.status, 2 * last + 1, a.part_cap)) return;
   const int row0 = 8 * int(blockIdx.y);  // this block's 8 rows of the item
   const float *part0 = a.parts + (c * 2 + (item0 <= begin ? 0 : 1)) * C::PART;
   const float *part1 = a.parts + c * 2 * C::PART;  // the others: part b is 2 b slots on
@@ -1007,7 +1018,7 @@ int64_t attend_paged_workspace(const moe_attend_paged_io_t &io, const moe_kv_cac
 }
 
 cudaError_t launch_attend_paged(const moe_attend_paged_io_t &io, const moe_kv_cache_t &c, void *workspace,
-                                int32_t *status, int num_sms, cudaStream_t st) {
+                                int64_t workspace_bytes, int32_t *status, int num_sms, cudaStream_t st) {
   PagedArgs a = {};
   a.q = static_cast<const uint16_t *>(io.q);
   a.q_stride = io.q_stride;
@@ -1029,6 +1040,7 @@ cudaError_t launch_attend_paged(const moe_attend_paged_io_t &io, const moe_kv_ca
   a.v_scales = c.v_scales;
   a.num_pages = c.num_pages;
   a.page_size = c.page_size;
+  a.cached_rows = int64_t(c.num_pages) * c.page_size * c.num_kv_heads;
   a.scale2 = fmaxf(fabsf(io.scale) * 1.4426950408889634f, 0x1p-100f);
   a.flip = io.scale < 0.0f ? 0x80008000u : 0u;
   a.parts = static_cast<float *>(workspace);
@@ -1036,6 +1048,7 @@ cudaError_t launch_attend_paged(const moe_attend_paged_io_t &io, const moe_kv_ca
   const bool h = io.dtype == MOE_DTYPE_F16;
   const auto go = [&](auto cfg) {
     using C = decltype(cfg);
+    a.part_cap = checked_capacity(workspace_bytes / (C::PART * 4), io.flags);
     return h ? launch<F16, C>(a, num_sms, st) : launch<Bf16, C>(a, num_sms, st);
   };
   const int rows = usual_rows(io, c);

@@ -93,6 +93,7 @@ struct PromptArgs {
   bool skip_tail;  // test hook: the mark of a zeroed last V tile is never set
   int splits;    // parts that a work's keys may be split into
   float *parts;  // workspace: of each part, O and (reference, sum) of its 256 rows
+  int64_t part_cap;  // row tiles of parts that it holds, for the checks
 };
 
 // What a block does at a time: two row tiles of a sequence, for the heads of a group.
@@ -330,12 +331,18 @@ __device__ __forceinline__ bool read_next(const uint4 *answer, uint32_t &block) 
 
 // ------------------------------------------------------------------ TMA (warp 8)
 
+__device__ __forceinline__ bool row_ok(const PromptArgs &a, int row, int head) {
+  return index_ok(a.status, row, a.num_rows) && index_ok(a.status, head, a.num_heads);
+}
+
 // Entry i of the list K 0, V 0, K 1, V 1, ... of w into the ring, as its entry number base + i (one lane).
 template <int D>
-__device__ __forceinline__ void load_tile(const CUtensorMap *kmap, const CUtensorMap *vmap, Smem<D> &sm, const Work &w,
-                                          uint32_t base, int i) {
+__device__ __forceinline__ void load_tile(const CUtensorMap *kmap, const CUtensorMap *vmap, const PromptArgs &a, Smem<D> &sm,
+                                          const Work &w, uint32_t base, int i) {
   using S = Smem<D>;
   const uint32_t s = (base + i) % S::kStages;
+  if (!index_ok(a.status, w.key0 + (i >> 1) * kKeys, a.num_keys) || !index_ok(a.status, w.kv, a.all_groups / a.groups))
+    return;  // who waits for it reports that too
   mbar_arrive_expect_tx(&sm.full[s], S::kTileBytes);
   const CUtensorMap *map = i & 1 ? vmap : kmap;
 #pragma unroll
@@ -346,6 +353,7 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *kmap, const CUtenso
 // Q of row tile x (one lane). Rows past the sequence are another one's, or zeros past the last: their scores are hidden.
 template <int D>
 __device__ __forceinline__ void load_queries(const CUtensorMap *qmap, const PromptArgs &a, Smem<D> &sm, const Work &w, int x) {
+  if (!row_ok(a, w.row0 + w.t0 + x * a.tokens, w.head0 + a.group - 1)) return;
   mbar_arrive_expect_tx(&sm.q_full[x], uint32_t(a.tokens * a.group * D * 2));
 #pragma unroll
   for (int p = 0; p < D / 64; ++p)
@@ -372,7 +380,7 @@ __device__ void load_warp(const CUtensorMap *qmap, const CUtensorMap *kmap, cons
           ok = false;
           break;
         }
-        load_tile<D>(kmap, vmap, sm, w, base, i);
+        load_tile<D>(kmap, vmap, a, sm, w, base, i);
         ++issued;
         if (t > 0 && i == 0) {
 #pragma unroll
@@ -599,7 +607,8 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
   // the thread's row of the sequence and its head; rows past the tile's tokens or the sequence see nothing
   const int t = w.t0 + x * a.tokens + row / a.group, h = w.head0 + row % a.group;
-  const bool real = row < a.tokens * a.group && t < w.n;
+  bool real = row < a.tokens * a.group && t < w.n;
+  if (real) real = row_ok(a, w.row0 + t, h);
   const int skip = SPLIT ? w.skip : 0;
   const int limit = real ? key_limit(a, w.keys + skip, w.n, t) - skip : 0;
   const uint32_t lanes = uint32_t(warp * 32) << 16;
@@ -667,6 +676,7 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
   }
   if constexpr (SPLIT) {
     if (w.parts > 1) {  // as it is, for the join
+      if (real) real = index_ok(a.status, int64_t(w.slot) * 2 + x, a.part_cap);
       float *const part = a.parts + (int64_t(w.slot) * 2 + x) * kRows * (D + 2);
       if (real) {
         part[kRows * D + row] = total != 0.0f ? ref * a.scale2 : -1e30f;
@@ -738,7 +748,7 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
       uint16_t *out = a.out + int64_t(w.row0 + tt) * a.out_stride + int64_t(w.head0 + hh) * D + 64 * half + 8 * c8;
 #pragma unroll
       for (int i = 0; i < 32; i += kStep) {
-        if (rr < rows && tt < w.n)
+        if (rr < rows && tt < w.n && row_ok(a, w.row0 + tt, w.head0 + hh))
           *reinterpret_cast<uint4 *>(out) =
               *reinterpret_cast<const uint4 *>(stage + (l8 + i) * 128 + ((c8 ^ ((l8 + i) & 7)) << 4));
         rr += kStep;
@@ -815,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if (w.tiles(x) > 0) load_queries<D>(&qmap, a, sm, w, x);
-      for (int i = 0; i < S::kStages && i < 2 * w.all(); ++i) load_tile<D>(&kmap, &vmap, sm, w, 0, i);
+      for (int i = 0; i < S::kStages && i < 2 * w.all(); ++i) load_tile<D>(&kmap, &vmap, a, sm, w, 0, i);
       sm.work[0] = w;
       mbar_arrive(&sm.work_full[0]);
     }
@@ -861,6 +871,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const PromptA
     const int r = int(blockIdx.y) * kJoinRows + i * (kJoinThreads / 32) + warp, x = r / kRows, row = r % kRows;
     const int t = w.t0 + x * a.tokens + row / a.group, h = w.head0 + row % a.group;
     if (row >= a.tokens * a.group || t >= w.n) continue;
+    if (!row_ok(a, w.row0 + t, h) || !index_ok(a.status, w.parts - 1, kMaxSplits) ||
+        !index_ok(a.status, int64_t(w.slot + w.parts - 1) * 2 + x, a.part_cap))
+      continue;
     const float *const from = a.parts + w.slot * kPart + int64_t(x) * kRows * (D + 2);
     float ref = -1e30f, sum = 0.0f;
     if (lane < w.parts) {
@@ -983,6 +996,7 @@ cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *stat
   set_groups(io, a);
   a.splits = io.workspace ? splits_of(a, io.num_keys, num_sms) : 1;
   a.parts = static_cast<float *>(io.workspace);
+  a.part_cap = checked_capacity(io.workspace ? io.workspace_bytes / (int64_t(kRows) * (io.head_dim + 2) * 4) : 0, io.flags);
   a.causal = io.causal;
   a.skip_tail = io.flags & MOE_FLAG_TEST_SKIP_READY;
   a.scale2 = fmaxf(fabsf(io.scale) * 1.4426950408889634f, 0x1p-100f);

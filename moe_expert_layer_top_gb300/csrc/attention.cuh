@@ -17,6 +17,18 @@ __device__ __forceinline__ void out_of_range(int32_t *status) {
   if (status) report_error(status, MOE_ERR_DEVICE_BOUNDS);
 }
 
+// In the bounds-checked build (see in_bounds): whether 0 <= i < n. If not, that is reported and the caller skips the
+// access. Constantly true in the normal build.
+__device__ __forceinline__ bool index_ok(int32_t *status, int64_t i, int64_t n) {
+  if constexpr (kBoundsChecked) {
+    if (i < 0 || i >= n) {
+      out_of_range(status);
+      return false;
+    }
+  }
+  return true;
+}
+
 // ------------------------------------------------------------------ 16-bit types
 
 struct Bf16 {

@@ -89,7 +89,7 @@ extern "C" {
 moe_status_t moe_qkv_append(const moe_qkv_append_io_t *io, const moe_kv_cache_t *cache, int32_t *d_status,
                             void *cuda_stream) {
   const NvtxRange nvtx_range("moe_qkv_append");
-  if (!io || io->num_tokens < 0) return MOE_ERR_INVALID_ARG;
+  if (!io || io->num_tokens < 0 || io->flags & ~MOE_FLAG_TEST_BOUNDS) return MOE_ERR_INVALID_ARG;
   moe_status_t s = heads_ok(io->num_heads, io->num_kv_heads, io->head_dim, io->dtype);
   if (s != MOE_OK) return s;
   const int64_t D = io->head_dim;
@@ -142,6 +142,7 @@ moe_status_t moe_attend_paged(const moe_attend_paged_io_t *io, const moe_kv_cach
   if (s == MOE_OK) s = cache_ok(*cache);
   if (s != MOE_OK) return s;
   if (!finite(io->scale) || !aligned(d_status, 4) || !aligned(io->lse, 4)) return MOE_ERR_INVALID_ARG;
+  if (io->flags & ~MOE_FLAG_TEST_BOUNDS) return MOE_ERR_INVALID_ARG;
   if (io->num_rows == 0 || io->num_seqs == 0) return MOE_OK;
   const int64_t width = int64_t(io->num_heads) * cache->head_dim;
   if (!good(io->q, 16) || !good(io->out, 16) || !stride_ok(io->q_stride, width) || !stride_ok(io->out_stride, width))
@@ -153,8 +154,8 @@ moe_status_t moe_attend_paged(const moe_attend_paged_io_t *io, const moe_kv_cach
   if (s != MOE_OK) return s;
   const int64_t need = attend_paged_workspace(*io, *cache, sms);
   if (workspace_bytes < need || (need && !good(workspace, 16))) return MOE_ERR_INVALID_ARG;
-  return launch_attend_paged(*io, *cache, workspace, d_status, sms, static_cast<cudaStream_t>(cuda_stream)) ==
-                 cudaSuccess
+  return launch_attend_paged(*io, *cache, workspace, workspace_bytes, d_status, sms,
+                             static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -175,7 +176,8 @@ moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_stat
   if (!io) return MOE_ERR_INVALID_ARG;
   moe_status_t s = prompt_sizes_ok(*io);
   if (s != MOE_OK) return s;
-  if ((io->causal != 0 && io->causal != 1) || io->flags & ~MOE_FLAG_TEST_SKIP_READY) return MOE_ERR_INVALID_ARG;
+  if ((io->causal != 0 && io->causal != 1) || io->flags & ~(MOE_FLAG_TEST_SKIP_READY | MOE_FLAG_TEST_BOUNDS))
+    return MOE_ERR_INVALID_ARG;
   if (!finite(io->scale) || !aligned(d_status, 4) || !aligned(io->lse, 4)) return MOE_ERR_INVALID_ARG;
   if (io->num_rows == 0 || io->num_seqs == 0) return MOE_OK;
   const int64_t D = io->head_dim;

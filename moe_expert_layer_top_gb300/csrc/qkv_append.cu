@@ -40,6 +40,7 @@ struct AppendArgs {
   int64_t slots_total;                               // num_pages * page_size
   int page_size;
   int parts;  // warps per token
+  int64_t cached_rows;  // of all pages and kv heads, for the checks
   int32_t *status;
 };
 
@@ -332,10 +333,12 @@ __global__ void __launch_bounds__(kThreads) qkv_append_kernel(const AppendArgs a
       if (io.q_norm) unpack8<T>(load_runs(static_cast<const uint16_t *>(io.q_norm), hold), w);
       unpack8<T>(raw, x);
       query_head<D>(io, hold, w, x, y);
-      if (real) store_runs(static_cast<uint16_t *>(io.q_out) + (t * nq + h) * D, hold, pack8<T>(y));
+      if (real && index_ok(a.status, t * nq + h, int64_t(io.num_tokens) * nq))
+        store_runs(static_cast<uint16_t *>(io.q_out) + (t * nq + h) * D, hold, pack8<T>(y));
       continue;
     }
     const int64_t row = (t * nk + h) * D;
+    const bool inside = index_ok(a.status, real ? t * nk + h : 0, int64_t(io.num_tokens) * nk);
     if (is_k) {
       float x[8], y[8], w[8] = {};
       if (io.k_norm) unpack8<T>(load_runs(static_cast<const uint16_t *>(io.k_norm), hold), w);
@@ -345,16 +348,17 @@ __global__ void __launch_bounds__(kThreads) qkv_append_kernel(const AppendArgs a
       store_runs(reinterpret_cast<uint16_t *>(turned[warp]) + sub * D, hold, pack8<T>(y));
       __syncwarp();
       raw = turned[warp][lane];
-      if (io.k_out && real) reinterpret_cast<uint4 *>(static_cast<uint16_t *>(io.k_out) + row)[l] = raw;
+      if (io.k_out && real && inside) reinterpret_cast<uint4 *>(static_cast<uint16_t *>(io.k_out) + row)[l] = raw;
     }
     uint32_t codes, scale;
     uint4 values;
     void *kept = is_k ? io.k_cached : io.v_cached;
     quantize_head<T>(raw, codes, scale, kept ? &values : nullptr);
     if (!real) continue;
-    if (kept) reinterpret_cast<uint4 *>(static_cast<uint16_t *>(kept) + row)[l] = values;
+    if (kept && inside) reinterpret_cast<uint4 *>(static_cast<uint16_t *>(kept) + row)[l] = values;
     if (place != kNoPlace) {
       const uint64_t at = place + uint32_t(h) * a.page_size;
+      if (!index_ok(a.status, at, a.cached_rows)) continue;
       reinterpret_cast<uint32_t *>((is_k ? a.k_codes : a.v_codes) + at * (D / 2))[l] = codes;
       if ((l & 3) == 0) ((is_k ? a.k_scales : a.v_scales) + at * (D / 32))[l >> 2] = uint8_t(scale);
     }
@@ -385,6 +389,7 @@ cudaError_t launch_qkv_append(const moe_qkv_append_io_t &io, const moe_kv_cache_
     a.v_scales = cache->v_scales;
     a.page_size = cache->page_size;
     a.slots_total = int64_t(cache->num_pages) * cache->page_size;
+    a.cached_rows = checked_capacity(a.slots_total * cache->num_kv_heads, io.flags);
   }
   const int heads = 256 / io.head_dim;  // of a unit
   const int units = 2 * ((io.num_kv_heads + heads - 1) / heads) + (io.num_heads + heads - 1) / heads;

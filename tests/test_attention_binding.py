@@ -48,3 +48,14 @@ def test_prompt_flags():
     assert abi.moe_attend_prompt(io) == abi.MOE_OK
     io.flags = 1
     assert abi.moe_attend_prompt(io) == abi.MOE_ERR_INVALID_ARG
+
+
+def test_append_and_paged_flags():
+    cache = abi.MoeKvCache(num_pages=0, page_size=16, num_kv_heads=2, head_dim=64)
+    for io, call in ((abi.MoeQkvAppendIO(num_heads=8, num_kv_heads=2, head_dim=64), abi.moe_qkv_append),
+                     (abi.MoeAttendPagedIO(num_heads=8, max_rows=1, scale=0.1),
+                      lambda io, c: abi.moe_attend_paged(io, c, None, 0))):
+        for flags, code in ((0, abi.MOE_OK), (abi.MOE_FLAG_TEST_BOUNDS, abi.MOE_OK), (1, abi.MOE_ERR_INVALID_ARG),
+                            (abi.MOE_FLAG_TEST_SKIP_READY, abi.MOE_ERR_INVALID_ARG)):
+            io.flags = flags
+            assert call(io, cache) == code
