@@ -7,16 +7,20 @@
   MOE_ERR_DEVICE_BOUNDS and the access skipped), loaded instead of libmoe.so
   when the environment sets MOE_DEBUG_BOUNDS=1;
 * ``csrc/attention_torch.cpp`` -> ``_build/attention_torch.so``, the Python module
-  that passes PyTorch tensors to the attention calls (host code, g++);
+  that passes PyTorch tensors to the attention calls (host code, g++; only where
+  PyTorch is installed, anew for another one, and after the libraries, which need
+  nvcc alone);
 * ``synth/synth.cu`` -> ``synth/_build/libmoe_synth.so``, the device side of the
   seeded input generator.
 The translation units are compiled in parallel, each with one ``-gencode``.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +33,7 @@ DEBUG_DIR = os.path.join(LIB_DIR, "debug")
 DEBUG_LIB_PATH = os.path.join(LIB_DIR, "libmoe_debug.so")
 TORCH_SRC = os.path.join(CSRC, "attention_torch.cpp")
 TORCH_LIB_PATH = os.path.join(LIB_DIR, "attention_torch.so")
+TORCH_STAMP_PATH = os.path.join(LIB_DIR, "attention_torch.stamp")
 SYNTH_DIR = os.path.join(ROOT, "synth")
 SYNTH_LIB_DIR = os.path.join(SYNTH_DIR, "_build")
 SYNTH_LIB_PATH = os.path.join(SYNTH_LIB_DIR, "libmoe_synth.so")
@@ -55,10 +60,28 @@ def _compile(src: str, obj: str, extra=()):
     return _run([nvcc(), *ARCH, *FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj])
 
 
-def _build_torch_module():
+def _torch_home() -> str | None:
+    """Directory of the installed PyTorch, without importing it; None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _torch_stamp(home: str) -> str:
+    """What the module was built against: it fits no other interpreter or PyTorch."""
+    with open(os.path.join(home, "version.py")) as f:
+        return f"{sys.version}\n{home}\n{f.read()}"
+
+
+def _torch_module_stale(home: str) -> bool:
+    if _stale(TORCH_LIB_PATH, [TORCH_SRC, os.path.join(INCLUDE, "moe.h")]) or not os.path.exists(TORCH_STAMP_PATH):
+        return True
+    with open(TORCH_STAMP_PATH) as f:
+        return f.read() != _torch_stamp(home)
+
+
+def _build_torch_module(home: str):
     import sysconfig
     import torch
-    home = os.path.dirname(torch.__file__)
     lib = os.path.join(home, "lib")
     tmp = TORCH_LIB_PATH + ".tmp"
     _run([os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -67,6 +90,8 @@ def _build_torch_module():
           "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"), TORCH_SRC,
           "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"])
     os.replace(tmp, TORCH_LIB_PATH)
+    with open(TORCH_STAMP_PATH, "w") as f:
+        f.write(_torch_stamp(home))
 
 
 def _stale(target: str, sources) -> bool:
@@ -95,22 +120,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
         jobs.append(("synth", [synth_src], [os.path.join(SYNTH_LIB_DIR, "synth.o")], SYNTH_LIB_PATH, ()))
     work = [(s, o, tuple(flags) + (("-Xptxas", "-v") if verbose else ()))
             for _, srcs, objs, _, flags in jobs for s, o in zip(srcs, objs)]
-    module = force or _stale(TORCH_LIB_PATH, [TORCH_SRC, os.path.join(INCLUDE, "moe.h")])
+    home = _torch_home()
+    module = home is not None and (force or _torch_module_stale(home))
     with ThreadPoolExecutor(max_workers=max(1, min(len(work) + 1, os.cpu_count() or 4))) as ex:
-        pending = [ex.submit(_build_torch_module)] if module else []
+        pending = [ex.submit(_build_torch_module, home)] if module else []
         logs = list(ex.map(lambda a: _compile(*a), work))
-        for p in pending:
+        if verbose:
+            for log in logs:
+                print(log)
+        for _, _, objs, lib, _ in jobs:
+            tmp = lib + ".tmp"
+            _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs])
+            os.replace(tmp, lib)
+        for p in pending:  # last: the libraries are there whatever becomes of it
             p.result()
-    if verbose:
-        for log in logs:
-            print(log)
-    for _, _, objs, lib, _ in jobs:
-        tmp = lib + ".tmp"
-        _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs])
-        os.replace(tmp, lib)
     return LIB_PATH
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
