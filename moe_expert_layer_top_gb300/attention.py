@@ -17,6 +17,9 @@ set to MOE_OK, and look at it when convenient (MOE_ERR_DEVICE_BOUNDS: something
 was out of range and was not accessed; MOE_ERR_TIMEOUT: a wait inside the prompt
 kernel did not end within a second, and the results are unspecified).
 
+The calls serve only: they have no backward pass, and refuse inputs that require
+a gradient unless gradients are off (``torch.no_grad()``).
+
 The calls run on the tensors' device and on its current stream unless ``stream``
 is given. Outputs and workspaces come from PyTorch's allocator, on the stream
 of the call, so calls on several streams and captured graphs do not share any

@@ -12,6 +12,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -69,6 +70,19 @@ int32_t size32(int64_t v, const char *name) {
   return int32_t(v);
 }
 
+// The calls have no backward pass: a result without a gradient must not come of an input that wants one.
+void no_gradients(std::initializer_list<const at::Tensor *> inputs) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const at::Tensor *t : inputs)
+    if (t && t->requires_grad())
+      refuse("an input requires a gradient, and the call has no backward pass: make it under torch.no_grad()");
+}
+
+// A tensor that a call has written: autograd may hold it for a backward pass, which then has to see that.
+void written(const at::Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Device and type of q, which the other tensors share.
 struct Kind {
   at::Device device = at::Device(at::kCPU);
@@ -123,8 +137,8 @@ at::Tensor output(const at::Tensor *out, const at::Tensor &q, const Kind &kind, 
   return *out;
 }
 
-// The parts of a KVCacheMXFP4, which were checked when it was made.
-moe_kv_cache_t kv_cache(PyObject *cache, const Kind &kind, at::Device &device) {
+// The parts of a KVCacheMXFP4, which were checked when it was made. append: they are about to be written.
+moe_kv_cache_t kv_cache(PyObject *cache, at::Device &device, bool append) {
   PyObject *parts = PyObject_GetAttrString(cache, "_parts");
   if (!parts) throw Raised();
   if (!PyTuple_Check(parts) || PyTuple_GET_SIZE(parts) != 4) {
@@ -140,6 +154,8 @@ moe_kv_cache_t kv_cache(PyObject *cache, const Kind &kind, at::Device &device) {
   c.num_kv_heads = int32_t(k.size(1));
   c.page_size = int32_t(k.size(2));
   c.head_dim = int32_t(2 * k.size(3));
+  if (append)
+    for (int i = 0; i < 4; ++i) written(THPVariable_Unpack(PyTuple_GET_ITEM(parts, i)));
   Py_DECREF(parts);  // the cache, which the caller holds, holds them
   return c;
 }
@@ -224,6 +240,8 @@ PyObject *py_check_cache(PyObject *, PyObject *const *arg, Py_ssize_t n) {
 PyObject *py_append(PyObject *, PyObject *const *arg, Py_ssize_t n) {
   return guarded(n, 15, [&]() -> PyObject * {
     const at::Tensor &q = tensor(arg[0], "q"), &k = tensor(arg[1], "k"), &v = tensor(arg[2], "v");
+    no_gradients({&q, &k, &v, optional_tensor(arg[4], "rope"), optional_tensor(arg[6], "q_norm"),
+                  optional_tensor(arg[7], "k_norm"), optional_tensor(arg[11], "q_out")});
     const Kind kind(q);
     moe_qkv_append_io_t io = {};
     io.q_stride = rows(q, "q", kind);
@@ -252,7 +270,7 @@ PyObject *py_append(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     moe_kv_cache_t cache = {};
     if (slots) {
       at::Device device(at::kCPU);
-      cache = kv_cache(arg[9], kind, device);
+      cache = kv_cache(arg[9], device, true);
       if (device != kind.device || cache.num_kv_heads != K || cache.head_dim != D)
         refuse("the cache must be on q's device, with the kv heads and head size of k");
       io.slots = vector<int64_t>(*slots, "slots", at::kLong, T, kind);
@@ -288,6 +306,7 @@ PyObject *py_append(PyObject *, PyObject *const *arg, Py_ssize_t n) {
       s = qkv_append(&io, slots ? &cache : nullptr, word, stream_of(kind));
     }
     if (s != MOE_OK) return PyLong_FromLong(s);
+    if (given) written(*given);
     PyObject *dict = PyDict_New();
     if (!dict) return nullptr;
     put(dict, "q", q_out);
@@ -305,6 +324,7 @@ PyObject *py_paged(PyObject *, PyObject *const *arg, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject * {
     const at::Tensor &q = tensor(arg[0], "q"), &table = tensor(arg[2], "page_table");
     const at::Tensor &lengths = tensor(arg[3], "lengths"), &cu_rows = tensor(arg[4], "cu_rows");
+    no_gradients({&q, optional_tensor(arg[7], "out")});
     const Kind kind(q);
     moe_attend_paged_io_t io = {};
     io.q_stride = rows(q, "q", kind);
@@ -315,7 +335,7 @@ PyObject *py_paged(PyObject *, PyObject *const *arg, Py_ssize_t n) {
         !table.is_contiguous())
       refuse("page_table must be a contiguous int32 [sequences][pages] tensor on q's device");
     at::Device device(at::kCPU);
-    const moe_kv_cache_t cache = kv_cache(arg[1], kind, device);
+    const moe_kv_cache_t cache = kv_cache(arg[1], device, false);
     if (device != kind.device || cache.head_dim != D) refuse("the cache must be on q's device, with q's head size");
     const int64_t max_rows = PyLong_AsLongLong(arg[5]);
     if (max_rows == -1 && PyErr_Occurred()) return nullptr;
@@ -349,7 +369,9 @@ PyObject *py_paged(PyObject *, PyObject *const *arg, Py_ssize_t n) {
         s = attend_paged(&io, &cache, workspace.data_ptr(), bytes, word, stream_of(kind));
       }
     }
-    return s != MOE_OK ? PyLong_FromLong(s) : outputs(out, lse);
+    if (s != MOE_OK) return PyLong_FromLong(s);
+    if (given) written(*given);
+    return outputs(out, lse);
   });
 }
 
@@ -358,6 +380,7 @@ PyObject *py_prompt(PyObject *, PyObject *const *arg, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject * {
     const at::Tensor &q = tensor(arg[0], "q"), &k = tensor(arg[1], "k"), &v = tensor(arg[2], "v");
     const at::Tensor &cu_rows = tensor(arg[3], "cu_rows"), &cu_keys = tensor(arg[4], "cu_keys");
+    no_gradients({&q, &k, &v, optional_tensor(arg[7], "out")});
     const Kind kind(q);
     moe_attend_prompt_io_t io = {};
     io.q_stride = rows(q, "q", kind);
@@ -401,7 +424,9 @@ PyObject *py_prompt(PyObject *, PyObject *const *arg, Py_ssize_t n) {
         s = attend_prompt(&io, word, stream_of(kind));
       }
     }
-    return s != MOE_OK ? PyLong_FromLong(s) : outputs(out, lse);
+    if (s != MOE_OK) return PyLong_FromLong(s);
+    if (given) written(*given);
+    return outputs(out, lse);
   });
 }
 

@@ -3,6 +3,7 @@ import ctypes
 import types
 
 import pytest
+import torch
 
 import moe_expert_layer_top_gb300 as pkg
 from moe_expert_layer_top_gb300 import abi, attention
@@ -59,3 +60,31 @@ def test_append_and_paged_flags():
                             (abi.MOE_FLAG_TEST_SKIP_READY, abi.MOE_ERR_INVALID_ARG)):
             io.flags = flags
             assert call(io, cache) == code
+
+
+def test_inputs_that_require_gradients_are_refused():
+    x = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16)
+    q, k, cu = x(4, 8, 64), x(4, 2, 64), torch.tensor([0, 4], dtype=torch.int32)
+    rope, pos = torch.zeros(4, 64), torch.zeros(4, dtype=torch.int32)
+
+    def wants(t):
+        return t.clone().requires_grad_()
+
+    calls = [lambda: attention.qkv_append(wants(q), k, k),
+             lambda: attention.qkv_append(q, wants(k), k),
+             lambda: attention.qkv_append(q, k, wants(k)),
+             lambda: attention.qkv_append(q, k, k, rope=wants(rope), positions=pos),
+             lambda: attention.qkv_append(q, k, k, q_norm=wants(x(64))),
+             lambda: attention.qkv_append(q, k, k, k_norm=wants(x(64))),
+             lambda: attention.qkv_append(q, k, k, q_out=wants(q)),
+             lambda: attention.attend_paged(wants(q), None, cu[None], cu[:1], cu),
+             lambda: attention.attend_paged(q, None, cu[None], cu[:1], cu, out=wants(q)),
+             lambda: attention.attend_prompt(wants(q), k, k, cu, cu),
+             lambda: attention.attend_prompt(q, wants(k), k, cu, cu),
+             lambda: attention.attend_prompt(q, k, wants(k), cu, cu),
+             lambda: attention.attend_prompt(q, k, k, cu, cu, out=wants(q))]
+    for call in calls:
+        with pytest.raises(ValueError, match="no backward pass"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # these are host tensors
+            call()

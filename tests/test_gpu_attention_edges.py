@@ -174,3 +174,47 @@ def test_prompt_wait_that_runs_out_is_reported(D, seqs):
         torch.cuda.synchronize()
         assert st.item() == code
     assert torch.equal(out, want) and torch.equal(lse, z)
+
+
+# ------------------------------------------------------------------ PyTorch's view of the calls
+
+def test_outputs_that_are_given_and_the_cache_count_as_written():
+    """A tensor that autograd holds for a backward pass and a call then writes is noticed there."""
+    H, K, D, n = 4, 2, 64, 20
+    q, k, v, cu = seeded(40, n, H, D).bfloat16(), seeded(41, n, K, D).bfloat16(), seeded(42, n, K, D).bfloat16(), ac.i32([0, n])
+    c = attention.KVCacheMXFP4.empty(2, 16, K, D)
+    parts = (c.k_codes, c.k_scales, c.v_codes, c.v_scales)
+    slots, lens = torch.arange(n, device="cuda"), ac.i32([n])
+    for given, call in (
+        (parts, lambda out: attention.qkv_append(q, k, v, cache=c, slots=slots)),
+        (None, lambda out: attention.qkv_append(q, k, v, q_out=out)["q"]),
+        (None, lambda out: attention.attend_prompt(q, k, v, cu, cu, out=out)),
+        (None, lambda out: attention.attend_paged(q, c, ac.i32([[0, 1]]), lens, cu, max_rows=n, out=out)),
+    ):
+        out = torch.empty_like(q)
+        tensors = given or (out,)
+        before = [t._version for t in tensors]
+        call(out)
+        assert [t._version for t in tensors] == [b + 1 for b in before]
+    weight = torch.ones(n, H, D, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    held = torch.ones_like(q)
+    loss = (weight * held).sum()
+    attention.attend_prompt(q, k, v, cu, cu, out=held)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_calls_in_inference_mode_and_without_gradients():
+    H, K, D, n = 4, 2, 64, 20
+    q, k, v, cu = seeded(43, n, H, D).bfloat16(), seeded(44, n, K, D).bfloat16(), seeded(45, n, K, D).bfloat16(), ac.i32([0, n])
+    want = attention.attend_prompt(q, k, v, cu, cu)
+    with torch.no_grad():
+        got = attention.attend_prompt(q.clone().requires_grad_(), k, v, cu, cu)
+        assert torch.equal(got, want) and not got.requires_grad
+    with torch.inference_mode():
+        out = torch.empty_like(q)
+        assert torch.equal(attention.attend_prompt(q.clone(), k, v, cu, cu, out=out), want)
+        c = attention.KVCacheMXFP4.empty(2, 16, K, D)
+        attention.qkv_append(q, k, v, cache=c, slots=torch.arange(n, device="cuda"))
+    attention.attend_prompt(q, k, v, cu, cu, out=out)  # an inference tensor outside of it
+    assert torch.equal(out, want)
