@@ -52,6 +52,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "attention.cuh"
 #include "tcgen05.cuh"
 
@@ -953,12 +955,16 @@ template <class T, int D, bool SPLIT>
 cudaError_t launch(const Maps &maps, const PromptArgs &a, cudaStream_t st) {
   const int64_t works = works_bound(a), blocks = works * (SPLIT ? a.splits : 1);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  // The register split above assumes the launch's share: a build that gave the kernel less must not run.
-  static const bool split = [] {
+  // The register split above assumes the launch's share: a build that gave the kernel less must not run. Only the answer
+  // is remembered, not a query that failed.
+  static std::atomic<int> regs{0};
+  if (!regs.load(std::memory_order_relaxed)) {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, attend_prompt_kernel<T, D, SPLIT>) == cudaSuccess && at.numRegs == kRegsLaunch;
-  }();
-  if (!split) return cudaErrorInvalidConfiguration;
+    const cudaError_t asked = cudaFuncGetAttributes(&at, attend_prompt_kernel<T, D, SPLIT>);
+    if (asked != cudaSuccess) return asked;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kRegsLaunch) return cudaErrorInvalidConfiguration;
   const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              int(Smem<D>::kBytes));
   if (e != cudaSuccess) return e;

@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "device.cuh"
 
 namespace moe {
@@ -38,17 +40,21 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 
 // ------------------------------------------------------------------ host
 
+// Asked for until there is an answer; any thread's will do, they are the same.
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_relaxed);
   if (!fn) {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
             cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
+        q == cudaDriverEntryPointSuccess) {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    else
+      known.store(fn, std::memory_order_relaxed);
+    } else {
       cudaGetLastError();
+    }
   }
   return fn;
 }

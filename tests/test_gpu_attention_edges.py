@@ -218,3 +218,41 @@ def test_calls_in_inference_mode_and_without_gradients():
         attention.qkv_append(q, k, v, cache=c, slots=torch.arange(n, device="cuda"))
     attention.attend_prompt(q, k, v, cu, cu, out=out)  # an inference tensor outside of it
     assert torch.equal(out, want)
+
+
+FIRST_CALLS = """
+import threading
+import torch
+from moe_expert_layer_top_gb300 import attention
+x = torch.randn(60, 6, 64, device="cuda").bfloat16()
+cu = torch.tensor([0, 60], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+start, got = threading.Barrier(8), [None] * 8
+
+def work(i):
+    with torch.cuda.stream(torch.cuda.Stream()):
+        start.wait()
+        y = x if i % 2 else x.half()
+        got[i] = attention.attend_prompt(y[:, :4], y[:, 4:5], y[:, 5:], cu, cu)
+        torch.cuda.current_stream().synchronize()
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+for i in range(8):
+    y = x if i % 2 else x.half()
+    assert torch.equal(got[i], attention.attend_prompt(y[:, :4], y[:, 4:5], y[:, 5:], cu, cu))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_from_threads():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=120)
+        assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr
