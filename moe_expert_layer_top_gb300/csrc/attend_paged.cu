@@ -11,7 +11,8 @@
 //   Values: codes times 2^(b - b_ref) in f16, with b_ref the largest scale code
 //   that the warp has seen; like m it moves as the pass goes on, and the
 //   accumulators are rescaled when it does. Exact down to 2^-23 of the largest.
-//   Probabilities: f16, at most 2^8 (the lazy reference of attend_prompt.cu).
+//   Probabilities: f16, at most 2^15 (the lazy reference of attend_prompt.cu, less
+//   2^7 so that small ones keep their bits: exact to 2^-32 of the row's largest).
 // All sums are binary32, on the tensor cores (mma.sync m16n8k16, f16 operands).
 //
 // Bound. A cached token and kv head is D + D/16 bytes against 4 D flops per row
@@ -429,7 +430,7 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) { return F16::pack
 template <class C>
 struct State {
   float o[C::MT][C::NT][4];      // [m-tile][n-tile]: dimension pair x row pair
-  float ref[C::NT][2];           // minus the reference of rows 2t, 2t + 1 (exponents of two)
+  float ref[C::NT][2];           // F16::kWeightUp minus the maximum that rows 2t, 2t + 1 refer to (exponents of two)
   float sum[C::NT][2];           // this lane's keys only
   int vref;                      // scale code that the accumulators are relative to
 };
@@ -555,7 +556,7 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
       float x = fmaxf(s[0][n][e], s[0][n][2 + e]);
 #pragma unroll
       for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][n][e], s[u][n][2 + e]));
-      move |= fmaf(x, mul[n][e], st.ref[n][e]) > kLazy;
+      move |= fmaf(x, mul[n][e], st.ref[n][e]) > kLazy + F16::kWeightUp;
     }
   }
   if (__any_sync(0xFFFFFFFFu, move)) {
@@ -569,7 +570,7 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
         m *= mul[n][e];
-        const float next = m + st.ref[n][e] > 0.0f ? -m : st.ref[n][e];
+        const float next = m + st.ref[n][e] > F16::kWeightUp ? F16::kWeightUp - m : st.ref[n][e];
         const float f = exp2_approx(next - st.ref[n][e]);
         st.ref[n][e] = next;
         st.sum[n][e] *= f;

@@ -33,6 +33,7 @@ __device__ __forceinline__ bool index_ok(int32_t *status, int64_t i, int64_t n) 
 
 struct Bf16 {
   static constexpr uint32_t kMmaType = 1;  // operand type of the tensor-core instruction descriptor
+  static constexpr float kWeightUp = 0.0f;
   static __device__ __forceinline__ float lo(uint32_t v) { return __uint_as_float(v << 16); }
   static __device__ __forceinline__ float hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
   static __device__ __forceinline__ uint32_t pack(float a, float b) {  // a in the low half
@@ -43,6 +44,10 @@ struct Bf16 {
 
 struct F16 {
   static constexpr uint32_t kMmaType = 0;
+  // Softmax weights are held times 2^kWeightUp (sum and product alike, so it drops out): with the reference up to 2^8
+  // behind they reach 2^15, and the smallest step of f16, 2^-24, is 2^-31 of the reference's weight. Without it, of 65,536
+  // keys with 2^-26 of the largest weight each (2^-10 in all) nothing is left in the product but all in the sum.
+  static constexpr float kWeightUp = 7.0f;
   static __device__ __forceinline__ float lo(uint32_t v) {
     return __low2float(*reinterpret_cast<const __half2 *>(&v));
   }

@@ -152,11 +152,11 @@ def test_prompt_with_overlapping_sequences():
 # ------------------------------------------------------------------ waits
 
 
-def prompt_io(q, k, v, out, lse, cr, ck, **kw):
+def prompt_io(q, k, v, out, lse, cr, ck, dtype=abi.MOE_DTYPE_BF16, scale=None, **kw):
     (n, H, D), (m, K) = q.shape, k.shape[:2]
     return abi.MoeAttendPromptIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), H * D, K * D, K * D, out.data_ptr(), H * D,
                                  lse.data_ptr(), cr.data_ptr(), ck.data_ptr(), len(cr) - 1, n, m, H, K, D,
-                                 abi.MOE_DTYPE_BF16, 1, D ** -0.5, **kw)
+                                 dtype, 1, D ** -0.5 if scale is None else scale, **kw)
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -256,3 +256,84 @@ def test_first_calls_of_a_process_from_threads():
     for _ in range(3):
         r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=120)
         assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr
+
+
+# ------------------------------------------------------------------ many small weights
+
+def check_small_weights(out, lse, q, k, v, scale, dtype):
+    """As attention_cases.check_attention, but a weight (in f16, times 2^7 of the reference's, which is not above the
+    row's largest) loses no more than half of f16's smallest step, 2^-25, in absolute terms: 2^-32 of the row's largest.
+    Divided by the sum of the weights relative to the largest that is the part of |v| that may be lost."""
+    n, H, D = q.shape
+    m = len(k)
+    o, z, spread, reach = oa.attend(q, k, v, scale)
+    delta = (D + 8) * 2.0 ** -24 * reach + 2.0 ** -21
+    top = np.stack([(k[:, h // (H // k.shape[1])] @ q[:, h].T * scale).max(0) for h in range(H)], axis=1)  # one row: sees all
+    lost = 2.0 ** -32 / np.exp(z - top)
+    bound = ac.HALF_STEP[dtype] * np.abs(o) + 1.05 * (2.0 ** -11 + 2 * delta + 2 * m * 2.0 ** -24)[..., None] * spread
+    bound += ac.HALF_TINY[dtype] + lost[..., None] * np.repeat(np.abs(v).sum(0)[None], H // k.shape[1], axis=1)
+    err = np.abs(ac.f64(out) - o)
+    assert (err <= bound).all(), f"{(err / bound).max():.2f} of its bound; {np.abs(err / o).max():.3f} of the result"
+    assert (np.abs(ac.f64(lse) - z) <= delta + m * 2.0 ** -24 + 4 * 2.0 ** -24 * (np.abs(z) + reach)).all()
+
+
+@pytest.mark.parametrize("below", [20.0, 24.0, 25.5, 26.0])  # binary orders of a weak key's weight below the strong one's
+@pytest.mark.parametrize("split", [False, True])
+def test_prompt_keeps_many_small_weights(below, split):
+    """One strong key with value 0 in front of 65,536 weak ones with values of about 1, in fp16."""
+    rng = np.random.default_rng(int(below))
+    n, H, D = 65537, 2, 64
+    k, v = ac.rows16(rng, (n, 1, D), "fp16", 0.01), 1 + ac.rows16(rng, (n, 1, D), "fp16", 0.25)
+    v = oa.round16(v, "fp16")
+    q = ac.rows16(rng, (1, H, D), "fp16", 0.25)
+    q[:, :, 0], k[:, :, 0] = 1.0, 0.0
+    k[0, :, 0], v[0] = oa.round16(below * np.log(2.0), "fp16"), 0.0
+    t = [ac.dev(x, "fp16") for x in (q, k, v)]
+    cu = ac.i32([0, 1]), ac.i32([0, n])
+    if split:
+        out, lse = attention.attend_prompt(*t, *cu, scale=1.0, return_lse=True)
+    else:
+        out, lse, st = torch.empty_like(t[0]), torch.empty(1, H, device="cuda"), status()
+        io = prompt_io(*t, out, lse, *cu, dtype=abi.MOE_DTYPE_F16, scale=1.0)
+        assert abi.moe_attend_prompt(io, st, torch.cuda.current_stream()) == abi.MOE_OK and st.item() == abi.MOE_OK
+    check_small_weights(out, lse, q, k, v, 1.0, "fp16")
+
+
+@pytest.mark.parametrize("below", [20.0, 24.0, 25.5, 26.0])
+@pytest.mark.parametrize("rows", [1, 6])
+def test_paged_keeps_many_small_weights(below, rows):
+    """A strong key with value 0 among every 32 (each warp's stage has one), the others weak with values of about 1."""
+    rng = np.random.default_rng(int(below) + rows)
+    n, H, D, page = 8192, 4, 64, 64
+    k, v = ac.rows16(rng, (n, 1, D), "bf16", 0.01), oa.round16(1 + ac.rows16(rng, (n, 1, D), "bf16", 0.25), "bf16")
+    q = ac.rows16(rng, (rows, H, D), "bf16", 0.25)
+    q[:, :, 0], k[:, :, 0] = oa.round16(below * np.log(2.0) / 6.0, "bf16"), 0.0
+    k[5::32], v[5::32] = 0.0, 0.0
+    k[5::32, :, 0] = 6.0
+    c = attention.KVCacheMXFP4.empty(n // page, page, 1, D)
+    kept = attention.qkv_append(ac.dev(q[:1].repeat(n, 0), "bf16"), ac.dev(k, "bf16"), ac.dev(v, "bf16"), cache=c,
+                                slots=torch.arange(n, device="cuda"), cached_values=True)
+    kk, vv = ac.f64(kept["k_cached"]), ac.f64(kept["v_cached"])
+    table, lens, cu = ac.i32([list(range(n // page))]), ac.i32([n]), ac.i32([0, rows])
+    out, lse = attention.attend_paged(ac.dev(q, "bf16"), c, table, lens, cu, max_rows=rows, scale=1.0, return_lse=True)
+    for i in range(rows):
+        end = n - rows + i + 1
+        check_small_weights(out[i:i + 1], lse[i:i + 1], q[i:i + 1], kk[:end], vv[:end], 1.0, "bf16")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sigma,scale", [(30.0, 0.1), (1.0, 0.0), (1.0, -0.2), (2.0 ** -6, 0.1), (1.0, 3.0), (1.0, 1e-30), (0.01, 1e4)])
+def test_prompt_scales_in_fp16(D, sigma, scale):
+    """The reference stands 2^7 below the maximum: also where the scores in between are far apart, or all one."""
+    rng = np.random.default_rng(D)
+    H, K, seqs = 2, 1, [(150, 150), (10, 400)]
+    cr, ck = ac.offsets([s[0] for s in seqs]), ac.offsets([s[1] for s in seqs])
+    q, k = ac.rows16(rng, (cr[-1], H, D), "fp16", sigma), ac.rows16(rng, (ck[-1], K, D), "fp16", sigma)
+    v = ac.rows16(rng, (ck[-1], K, D), "fp16")
+    st = status()
+    out, lse = attention.attend_prompt(ac.dev(q, "fp16"), ac.dev(k, "fp16"), ac.dev(v, "fp16"), ac.i32(cr), ac.i32(ck),
+                                       scale=scale, return_lse=True, d_status=st)
+    assert st.item() == abi.MOE_OK
+    for b in range(2):
+        r, s = slice(cr[b], cr[b + 1]), slice(ck[b], ck[b + 1])
+        ac.check_attention(out[r], lse[r], q[r], k[s], v[s], scale, "fp16", "fp16")
