@@ -337,3 +337,29 @@ def test_prompt_scales_in_fp16(D, sigma, scale):
     for b in range(2):
         r, s = slice(cr[b], cr[b + 1]), slice(ck[b], ck[b + 1])
         ac.check_attention(out[r], lse[r], q[r], k[s], v[s], scale, "fp16", "fp16")
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "fp16"), (128, "bf16")])
+@pytest.mark.parametrize("rows,keys,gone", [(40, 400, (0, 200)), (3, 5000, (0, 700)), (3, 5000, (1024, 1800)), (300, 300, (0, 140))])
+@pytest.mark.parametrize("scale", [0.1, 2.0 ** -40, 1e9])
+def test_prompt_key_tiles_without_a_weight(D, dtype, rows, keys, gone, scale):
+    """A row's first key tiles (of all keys, or of a part) have scores of -inf, the others far below 0: the result is that
+    of the others alone."""
+    rng = np.random.default_rng(keys)
+    H = 2
+    q, k = ac.rows16(rng, (rows, H, D), dtype, 0.1), ac.rows16(rng, (keys, 1, D), dtype, 0.1)
+    v = ac.rows16(rng, (keys, 1, D), dtype)
+    q[:, :, 0], k[:, :, 0] = 64.0, -64.0
+    if scale == 1e9:
+        q[:, :, 1:] = 0.0  # one score for all: differences would be past any weight
+    x = k.copy()
+    x[gone[0]:gone[1], :, 0] = -np.inf
+    out, lse = attention.attend_prompt(ac.dev(q, dtype), ac.dev(x, dtype), ac.dev(v, dtype), ac.i32([0, rows]),
+                                       ac.i32([0, keys]), scale=scale, return_lse=True)
+    left = np.r_[0:gone[0], gone[1]:keys]
+    for i in range(0, rows, 7):
+        see = left[left <= keys - rows + i]
+        if len(see):
+            ac.check_attention(out[i:i + 1], lse[i:i + 1], q[i:i + 1], k[see], v[see], scale, dtype, dtype)
+        else:
+            assert torch.isneginf(lse[i]).all() and not out[i].any()
