@@ -67,7 +67,7 @@ constexpr int kStageKeys = 32;
 // 1; 64 steps of six rows 82 against 91. 10 and 24 are no better than 16.
 constexpr int kOver = 16;
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
-constexpr float kNone = 1e30f;           // minus the reference of a row that has seen no key
+constexpr float kNone = 3e38f;           // minus the reference of a row that has seen no key: below any score
 constexpr int kCombineThreads = 256;
 constexpr int kMaxBlocks = 1024;         // blocks of the main kernel, at most
 

@@ -687,7 +687,7 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
       if (real) real = index_ok(a.status, int64_t(w.slot) * 2 + x, a.part_cap);
       float *const part = a.parts + (int64_t(w.slot) * 2 + x) * kRows * (D + 2);
       if (real) {
-        part[kRows * D + row] = total != 0.0f ? ref * a.scale2 : -1e30f;
+        part[kRows * D + row] = total != 0.0f ? ref * a.scale2 : -INFINITY;
         part[kRows * D + kRows + row] = total;
       }
       if (tiles > 0) {
@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const PromptA
         !index_ok(a.status, int64_t(w.slot + w.parts - 1) * 2 + x, a.part_cap))
       continue;
     const float *const from = a.parts + w.slot * kPart + int64_t(x) * kRows * (D + 2);
-    float ref = -1e30f, sum = 0.0f;
+    float ref = -INFINITY, sum = 0.0f;  // a part without a weight for the row has no say in the reference
     if (lane < w.parts) {
       ref = from[lane * kPart + kRows * D + row];
       sum = from[lane * kPart + kRows * D + kRows + row];

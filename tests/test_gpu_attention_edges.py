@@ -363,3 +363,36 @@ def test_prompt_key_tiles_without_a_weight(D, dtype, rows, keys, gone, scale):
             ac.check_attention(out[i:i + 1], lse[i:i + 1], q[i:i + 1], k[see], v[see], scale, dtype, dtype)
         else:
             assert torch.isneginf(lse[i]).all() and not out[i].any()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("rows,keys", [(3, 40), (3, 3000)])
+def test_scores_near_the_ends_of_binary32(rows, keys, sign):
+    """All scores +-2^110 or so, a factor of 2^17 inside binary32: one weight for all keys that a row sees. In parts, some
+    see none of them."""
+    rng = np.random.default_rng(keys)
+    H, D, page = 2, 64, 16
+    q, k, v = np.zeros((rows, H, D)), np.zeros((keys, 1, D)), ac.rows16(rng, (keys, 1, D), "bf16")
+    q[:, :, 0], k[:, :, 0] = 2.0 ** 60, sign * 2.0 ** 50
+    cu, ck = ac.i32([0, rows]), ac.i32([0, keys])
+    pages = -(-keys // page)
+    c = attention.KVCacheMXFP4.empty(pages, page, 1, D)
+    kept = attention.qkv_append(ac.dev(k.repeat(H, 1), "bf16"), ac.dev(k, "bf16"), ac.dev(v, "bf16"), cache=c,
+                                slots=torch.arange(keys, device="cuda"), cached_values=True)
+    assert np.array_equal(ac.f64(kept["k_cached"]), k)
+    for what in ("prompt", "paged"):
+        if what == "prompt":
+            vv = v
+            out, lse = attention.attend_prompt(ac.dev(q, "bf16"), ac.dev(k, "bf16"), ac.dev(v, "bf16"), cu, ck, scale=1.0,
+                                               return_lse=True)
+        else:
+            vv = ac.f64(kept["v_cached"])
+            out, lse = attention.attend_paged(ac.dev(q, "bf16"), c, ac.i32([list(range(pages))]), ac.i32([keys]), cu,
+                                              max_rows=rows, scale=1.0, return_lse=True)
+        for i in range(rows):
+            see = vv[:keys - rows + i + 1, 0]
+            want = see.mean(0)
+            # weights are all 1: the output's rounding, and binary32 sums
+            bound = ac.HALF_STEP["bf16"] * np.abs(want) + 2 * len(see) * 2.0 ** -24 * np.abs(see).mean(0)
+            assert (np.abs(ac.f64(out[i]) - want) <= bound).all(), what
+            assert (np.abs(ac.f64(lse[i]) / (sign * 2.0 ** 110) - 1) <= 2.0 ** -21).all(), what
