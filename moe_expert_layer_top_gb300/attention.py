@@ -106,6 +106,8 @@ def rope_table(positions: int, rotary_dim: int, theta: float = 10000.0, device="
 
 def _on(stream, device: torch.device):
     """The stream of a call: its outputs and workspace belong to it."""
+    if not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
 
 

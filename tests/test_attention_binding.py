@@ -88,3 +88,10 @@ def test_inputs_that_require_gradients_are_refused():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # these are host tensors
             call()
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The call would run on the tensors' device, and not on that stream."""
+    stream = types.SimpleNamespace(device=torch.device("cuda:1"))
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        attention._on(stream, torch.device("cuda:0"))
