@@ -141,7 +141,9 @@ at::Tensor output(const at::Tensor *out, const at::Tensor &q, const Kind &kind, 
 moe_kv_cache_t kv_cache(PyObject *cache, at::Device &device, bool append) {
   PyObject *parts = PyObject_GetAttrString(cache, "_parts");
   if (!parts) throw Raised();
-  if (!PyTuple_Check(parts) || PyTuple_GET_SIZE(parts) != 4) {
+  bool good = PyTuple_Check(parts) && PyTuple_GET_SIZE(parts) == 4;
+  for (int i = 0; good && i < 4; ++i) good = THPVariable_Check(PyTuple_GET_ITEM(parts, i));
+  if (!good) {
     Py_DECREF(parts);
     refuse("cache must be a KVCacheMXFP4");
   }

@@ -396,3 +396,11 @@ def test_scores_near_the_ends_of_binary32(rows, keys, sign):
             bound = ac.HALF_STEP["bf16"] * np.abs(want) + 2 * len(see) * 2.0 ** -24 * np.abs(see).mean(0)
             assert (np.abs(ac.f64(out[i]) - want) <= bound).all(), what
             assert (np.abs(ac.f64(lse[i]) / (sign * 2.0 ** 110) - 1) <= 2.0 ** -21).all(), what
+
+
+@pytest.mark.parametrize("parts", [(1, 2, 3, 4), [1, 2, 3, 4], (1, 2), None])
+def test_what_only_looks_like_a_cache_is_refused(parts):
+    import types
+    q, cu = seeded(60, 4, 8, 64).bfloat16(), ac.i32([0, 4])
+    with pytest.raises(ValueError, match="KVCacheMXFP4"):
+        attention.attend_paged(q, types.SimpleNamespace(_parts=parts), ac.i32([[0]]), ac.i32([4]), cu)
