@@ -455,7 +455,8 @@ typedef struct moe_qkv_append_io {
  *   q_out = the rotated q, rounded once to 16 bits; the keys likewise, and the
  *   cache gets MXFP4 of those 16-bit keys and of v.
  * The keys are computed in two-float arithmetic (about 2^-45 relative), so their
- * 16-bit values, and with them the 4-bit codes, are those of the formula.
+ * 16-bit values, and with them the 4-bit codes, are those of the formula. The
+ * squares and their sum have binary32's range: elements of 2^60 and more overflow it.
  * q_out may be q itself (the same pointer with q_stride == num_heads * D);
  * otherwise outputs must not overlap inputs. The slots of one call must be
  * distinct: two tokens with the same slot leave a mixture of both there.
@@ -476,8 +477,8 @@ typedef struct moe_attend_paged_io {
   int32_t num_seqs;           /* 0..4096 */
   int32_t num_rows;           /* rows of q and out; num_rows * num_heads < 2^31 */
   int32_t max_pages;          /* columns of page_table; max_pages * page_size <= 2^30 */
-  int32_t max_rows;           /* query rows that a sequence usually has at most: picks the kernel variant; any
-                               * value >= 1 gives right results */
+  int32_t max_rows;           /* query rows that a sequence usually has at most: picks the kernel variant, and with
+                               * it the order of the sums; any value >= 1 gives right results */
   int32_t num_heads;          /* a multiple of the cache's num_kv_heads */
   uint32_t dtype;             /* MOE_DTYPE_*: of q and out */
   float scale;                /* of the scores, finite */
@@ -498,15 +499,17 @@ moe_status_t moe_attend_paged_workspace(const moe_attend_paged_io_t *io, const m
  * +inf among a row's scores (or a score past binary32) makes its out and lse
  * NaN. Rows of q past cu_rows[num_seqs] are not touched. Sums and statistics are
  * binary32, probabilities f16. A scale code of 0 counts as zero; of the values
- * (and of a query row) parts below 2^-23 of the largest may lose bits. A NaN
- * among the values of a key can reach earlier rows of its own sequence (their
- * weight of it is 0, and 0 * NaN is NaN). A sequence with a page, length or
- * offset out of range, or whose rows overlap another one's (possible only where
- * cu_rows decreases), has unspecified results; the others have theirs. out must
- * not overlap q. workspace: 16-byte aligned device memory of at least the size
- * above; its content before the call does not matter, and calls that may overlap
- * on the GPU need one each. Results do not depend on timing: the same call gives
- * the same bits. */
+ * (and of a query row) parts below 2^-23 of the largest may lose bits. A query
+ * row is scaled to 2^14 and more before its products, so keys beyond 2^100 may
+ * overflow them. A NaN among the values of a key can reach earlier rows of its
+ * own sequence (their weight of it is 0, and 0 * NaN is NaN). A sequence with a
+ * page, length or offset out of range, or whose rows overlap another one's
+ * (possible only where cu_rows decreases), has unspecified results; the others
+ * have theirs. out must not overlap q. workspace: 16-byte aligned device memory
+ * of at least the size above; its content before the call does not matter, and
+ * calls that may overlap on the GPU need one each. Results do not depend on
+ * timing: the same call gives the same bits (max_rows and the other sequences of
+ * a batch change the order of the sums). */
 moe_status_t moe_attend_paged(const moe_attend_paged_io_t *io, const moe_kv_cache_t *cache, void *workspace,
                               int64_t workspace_bytes, int32_t *d_status, void *cuda_stream);
 

@@ -133,7 +133,7 @@ def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: 
     rope fp32 [positions][R] as from ``rope_table``, R <= D, with positions int32 [T]; None: no rotation.
     q_norm, k_norm [D]: RMSNorm weights; None: that part is not normalised.
     cache with slots int64 [T] (page * page size + offset; negative: the token is not cached).
-    q_out: a contiguous output for q, which may be q itself.
+    q_out: a contiguous output for q, which may be q itself; otherwise outputs must not overlap inputs.
 
     Returns {"q"}, plus "k" (rotated keys in 16 bits) with rotated_keys, plus "k_cached" and "v_cached" (the
     values that the 4-bit cache keeps) with cached_values.
@@ -151,8 +151,10 @@ def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor,
     q [rows][heads][D]; page_table int32 [sequences][pages]; lengths int32 [sequences], the tokens in the
     cache with the query rows among them; cu_rows int32 [sequences + 1]: sequence b has rows
     cu_rows[b] .. cu_rows[b + 1] - 1, its last tokens, each seeing the keys up to itself. max_rows: the rows a
-    sequence usually has at most (it picks the kernel variant; the result does not depend on it).
-    scale: of the scores, 1/sqrt(D) by default. Rows that see no key give 0 and lse -inf.
+    sequence usually has at most: it picks the kernel variant. Any value gives right results, but the order of the
+    sums, and so their last bits, follow it and the other sequences of the batch.
+    scale: of the scores, 1/sqrt(D) by default. Rows that see no key give 0 and lse -inf; rows with a NaN or +inf
+    among their scores give NaN in both. out must not overlap q.
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
@@ -166,7 +168,8 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
     """Attention over packed prompts, or over chunks of prompts with the keys before them.
 
     q [rows][heads][D], k and v [keys][kv heads][D]; cu_rows, cu_keys int32 [sequences + 1]. Row i of a sequence
-    with n rows and m keys sees keys 0 .. m - n + i (causal), or all m. Rows that see no key give 0 and lse -inf.
+    with n rows and m keys sees keys 0 .. m - n + i (causal), or all m. Rows that see no key give 0 and lse -inf; rows
+    with a NaN or +inf among their scores give NaN in both. out must not overlap the inputs.
     Few rows over many keys are computed in parts (the sizes of the tensors decide, not their contents).
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
