@@ -94,7 +94,7 @@ struct PromptArgs {
   float up;        // T::kWeightUp in score units: the reference stands that far below (added to the exponent instead, the
                    // same number of operations, chunks with D = 64 took 149 us in place of 141.6)
   float scale2;    // |scale| log2 e, at least 2^-100: scores times this are exponents of two
-  float lowest;    // reference of a row without a weight yet: any finite score is far above it
+  float lowest;    // reference of a row without a weight yet: below any score
   bool negative;   // the scale is: scores change sign
   int32_t *status;
   bool skip_tail;  // test hook: the mark of a zeroed last V tile is never set
@@ -645,7 +645,7 @@ __device__ __forceinline__ bool softmax_work(const PromptArgs &a, Smem<D> &sm, c
       for (int i = 0; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
       top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       if (j == 0) {
-        ref = top == -INFINITY ? a.lowest : T::kWeightUp != 0.0f ? top - a.up : top;
+        ref = fmaxf(T::kWeightUp != 0.0f ? top - a.up : top, a.lowest);
       } else {
         // O has to hold every tile before this one: then V of key tile j - 1 has been released. (Its slot is not
         // released again before this step is done, and was not in an older phase when S of this step was issued.)
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const PromptA
       const float4 v = *reinterpret_cast<const float4 *>(from + p * kPart + row * D + 4 * lane);
       o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
     }
-    const float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a NaN stays one, also of a part whose O has no weight
+    const float inv = total > 0.0f ? 1.0f / total : total;  // 0, or a NaN: also of a part whose O has no weight
     if (lane < D / 4)
       *reinterpret_cast<uint2 *>(a.out + int64_t(w.row0 + t) * a.out_stride + int64_t(h) * D + 4 * lane) =
           total != 0.0f ? make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)) : make_uint2(0, 0);
@@ -1013,7 +1013,7 @@ cudaError_t launch_attend_prompt(const moe_attend_prompt_io_t &io, int32_t *stat
   a.skip_tail = io.flags & MOE_FLAG_TEST_SKIP_READY;
   a.scale2 = fmaxf(fabsf(io.scale) * 1.4426950408889634f, 0x1p-100f);
   a.up = io.dtype == MOE_DTYPE_F16 ? F16::kWeightUp / a.scale2 : 0.0f;
-  a.lowest = -1e30f / fmaxf(a.scale2, 1.0f);  // times scale2 it is finite
+  a.lowest = -3e38f / fmaxf(a.scale2, 1.0f);  // times scale2 it is finite
   a.negative = io.scale < 0.0f;
   a.status = status;
   const int D = io.head_dim;
