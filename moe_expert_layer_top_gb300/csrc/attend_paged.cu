@@ -25,9 +25,10 @@
 // fixed latencies; tensor pipe 36 %, issue 44 %, HBM 30 %. One token over 4,096:
 // 10.7 us, launches and the chain lookup - load - join.
 // The codes go from shared memory straight into the registers that the MMA
-// reads: tcgen05 would need K and V in 16 bits in shared memory first, and
-// writing and reading those (for D = 128: 48 KB per 128 tokens beside 17 KB of
-// codes in and out) would make shared memory the bound.
+// reads. tcgen05 would need V in 16 bits in shared memory first, since V's scale
+// groups do not lie along the product's inner dimension (the keys). K's do: its
+// codes and scales could be the operands of a block-scaled MMA as they are, with the
+// queries split into 8-bit terms. That has not been built.
 //
 // Layout. Keys are the MMA's M (scores transposed: 16 keys x 8 rows), so a step
 // of 8 rows wastes nothing on padding. The order of a product's inner dimension

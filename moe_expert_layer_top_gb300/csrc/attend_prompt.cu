@@ -13,12 +13,13 @@
 //
 // Bound. 4 D flops per (row, head, key) against 16-bit inputs read once: the
 // tensor pipe, for all but the shortest prompts. 16,384 tokens (32 + 8 heads of
-// 128) take 1.40 ms, 1.57 PFLOP/s or 83 % of the measured bf16 rate, at the power
-// limit. A pair of row tiles costs 1.5 us for a key tile (1.06 of MMAs) and 4.4 us
-// beside them (first loads, the first and last softmax, output), so 16 packed
-// prompts with few key tiles each take 78 us where their MMAs need 35. D = 64: an MMA
-// with N = 64 takes as long as one with 128, so the value product has half the rate:
-// three chunks behind 4,000 tokens 139 us, of which 88 for the MMAs. 257 tokens: 11.4.
+// 128) take 1.40 ms alone and 1.47 to 1.52 call after call (1.57 and 1.45 to 1.50
+// PFLOP/s, 83 and 76 to 79 % of the measured bf16 rate; the clock falls then). A
+// pair of row tiles costs 1.5 us for a key tile (1.06 of MMAs) and 4.4 us beside
+// them (first loads, the first and last softmax, output), so 16 packed prompts with
+// few key tiles each take 79 us where their MMAs need 35. D = 64: an MMA with N = 64
+// takes as long as one with 128, so the value product has half the rate: three
+// chunks behind 4,000 tokens 139 us, of which 88 for the MMAs. 257 tokens: 11.3.
 //
 // Layout. A row of the tile is a (token, head) pair: the G heads of a kv head's
 // group are packed, r = token * G + head, so one key tile serves all of them and
@@ -48,7 +49,7 @@
 // A block goes from work to work without stopping: its barriers and TMEM stay, and
 // the next Q, K and V are loaded while the last softmax and the output of this work
 // run. With a block for each work these cost 6.5 us in place of 4.4 (16 packed
-// prompts 90 us, 4,096 prompts of 30 tokens 11.4 ms against 1.09, 257 tokens 10.3).
+// prompts 90 us, 4,096 prompts of 30 tokens 11.4 ms against 1.12, 257 tokens 10.3).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -947,7 +948,7 @@ void set_groups(const moe_attend_prompt_io_t &io, PromptArgs &a) {
 
 // The keys are split where the works alone leave half of the GPU idle and the keys suffice for three parts (the join is
 // a kernel of its own: 64 rows over 1,024 keys take 25 us in two parts, 21 in one). 32 + 8 heads of 128, 32,768 keys:
-// one row 41 us (364 in one part), 64 rows 74 (395), 512 rows 236 (399).
+// one row 40 us (364 in one part), 64 rows 71 (395), 512 rows 231 (399).
 int splits_of(const PromptArgs &a, int num_keys, int num_sms) {
   const int64_t works = works_bound(a);
   if (works < 1 || num_keys < 3 * kSplitTiles * kKeys) return 1;

@@ -99,7 +99,7 @@ struct TileAt {
 };
 
 // Where a search may begin: `base` tiles lie before sequence b0. A search that goes on where the last one ended makes
-// all searches of a block one pass over the sequences (4,096 prompts of 30 tokens: 1.09 ms; 11.4 with searches from the
+// all searches of a block one pass over the sequences (4,096 prompts of 30 tokens: 1.12 ms; 11.4 with searches from the
 // start and without taking over the blocks past the last tile).
 struct TileCursor {
   int b0 = 0;
