@@ -37,7 +37,7 @@ import torch
 from . import abi, build
 
 _module = None
-_bound = None  # the library (abi.load()) whose entry points the module calls
+_bound = object()  # the library (abi.load()) whose entry points the module calls; none yet
 
 
 def _native():
@@ -74,7 +74,8 @@ class KVCacheMXFP4:
     __slots__ = ("_parts",)
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor):
-        _native().check_cache(k_codes, k_scales, v_codes, v_scales)
+        module = _module if abi._lib is _bound else _native()
+        module.check_cache(k_codes, k_scales, v_codes, v_scales)
         self._parts = (k_codes, k_scales, v_codes, v_scales)
 
     k_codes = property(lambda self: self._parts[0])
@@ -138,8 +139,9 @@ def qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, positions: 
     Returns {"q"}, plus "k" (rotated keys in 16 bits) with rotated_keys, plus "k_cached" and "v_cached" (the
     values that the 4-bit cache keeps) with cached_values.
     """
-    return _call("moe_qkv_append", _native().append, stream, q, k, v, positions, rope, interleaved, q_norm,
-                 k_norm, eps, cache, slots, q_out, rotated_keys, cached_values, d_status)
+    module = _module if abi._lib is _bound else _native()
+    return _call("moe_qkv_append", module.append, stream, q, k, v, positions, rope, interleaved, q_norm, k_norm, eps,
+                 cache, slots, q_out, rotated_keys, cached_values, d_status)
 
 
 def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -158,8 +160,9 @@ def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor,
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
-    return _call("moe_attend_paged", _native().paged, stream, q, cache, page_table, lengths, cu_rows,
-                 max_rows, scale, out, return_lse, d_status)
+    module = _module if abi._lib is _bound else _native()
+    return _call("moe_attend_paged", module.paged, stream, q, cache, page_table, lengths, cu_rows, max_rows, scale, out,
+                 return_lse, d_status)
 
 
 def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, cu_keys: torch.Tensor, *,
@@ -174,5 +177,6 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """
-    return _call("moe_attend_prompt", _native().prompt, stream, q, k, v, cu_rows, cu_keys, causal, scale,
-                 out, return_lse, d_status)
+    module = _module if abi._lib is _bound else _native()
+    return _call("moe_attend_prompt", module.prompt, stream, q, k, v, cu_rows, cu_keys, causal, scale, out, return_lse,
+                 d_status)
