@@ -404,3 +404,34 @@ def test_what_only_looks_like_a_cache_is_refused(parts):
     q, cu = seeded(60, 4, 8, 64).bfloat16(), ac.i32([0, 4])
     with pytest.raises(ValueError, match="KVCacheMXFP4"):
         attention.attend_paged(q, types.SimpleNamespace(_parts=parts), ac.i32([[0]]), ac.i32([4]), cu)
+
+
+# ------------------------------------------------------------------ nothing to attend to
+
+def test_calls_without_keys_rows_or_sequences():
+    """Tensors of no rows: no keys at all, a cache of no pages, tables of no columns, no sequences, no rows."""
+    H, K, D = 4, 2, 64
+    q, none, cu = seeded(70, 3, H, D).bfloat16(), torch.empty(0, K, D, device="cuda").bfloat16(), ac.i32([0, 3])
+    st = status()
+    out, lse = attention.attend_prompt(q, none, none, cu, ac.i32([0, 0]), return_lse=True, d_status=st)
+    assert not out.any() and torch.isneginf(lse).all()
+    k = seeded(71, 5, K, D).bfloat16()
+    assert attention.attend_prompt(q[:0], k, k, ac.i32([0, 0]), ac.i32([0, 5]), d_status=st).shape == (0, H, D)
+    given = torch.full_like(q, 3.0)
+    for rows in ([0], [0, 0, 0]):  # no sequences; sequences without rows
+        keys = ac.i32([0] * len(rows))
+        attention.attend_prompt(q, k, k, ac.i32(rows), keys, out=given, d_status=st)
+    empty, c = attention.KVCacheMXFP4.empty(0, 16, K, D), attention.KVCacheMXFP4.empty(1, 16, K, D)
+    for cache in (empty, c):
+        for columns in (0, 1):
+            table = torch.zeros(1, columns, dtype=torch.int32, device="cuda")
+            out, lse = attention.attend_paged(q, cache, table, ac.i32([0]), cu, max_rows=3, return_lse=True, d_status=st)
+            assert not out.any() and torch.isneginf(lse).all()
+    attention.attend_paged(q, c, torch.zeros(0, 1, dtype=torch.int32, device="cuda"), ac.i32([]), ac.i32([0]), out=given,
+                           d_status=st)
+    attention.attend_paged(q, c, ac.i32([[0]]), ac.i32([0]), ac.i32([0, 0]), out=given, d_status=st)
+    assert attention.attend_paged(q[:0], c, ac.i32([[0]]), ac.i32([0]), ac.i32([0, 0]), d_status=st).shape == (0, H, D)
+    o = attention.qkv_append(q, q[:, :K], q[:, :K], cache=empty, slots=torch.full((3,), -1, device="cuda"), d_status=st,
+                             cached_values=True)
+    assert torch.equal(o["q"], q) and o["k_cached"].shape == (3, K, D)
+    assert st.item() == abi.MOE_OK and (given == 3).all()
