@@ -10,7 +10,9 @@
  *   -> weighted combine (+ an optional always-active shared expert).
  * In front of it, the attention of the layer: per-head RMSNorm, rotary
  * positions and the append to a paged MXFP4 key/value cache, attention over
- * that cache, and causal attention over prompts.
+ * that cache (of the newest tokens, or of a tree of drafted ones), and causal
+ * attention over prompts. Behind the layers, the end of a speculative step:
+ * verification of the drafted tokens, and the commit of the accepted ones.
  *
  * Passages that define the operation (page title, section):
  *  - "SGLang's Low-Latency Mode Boosts DeepSeek-V4.1-Flash Speed by 1.56x on
@@ -67,7 +69,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 5
+#define MOE_ABI_VERSION 6
 
 typedef enum {
   MOE_OK = 0,
@@ -555,6 +557,117 @@ moe_status_t moe_attend_prompt_workspace(const moe_attend_prompt_io_t *io, int64
  * overlap the inputs. A workspace smaller than moe_attend_prompt_workspace says
  * is MOE_ERR_INVALID_ARG; calls that may overlap on the GPU need one each. */
 moe_status_t moe_attend_prompt(const moe_attend_prompt_io_t *io, int32_t *d_status, void *cuda_stream);
+
+/* ---------------------------------------------------------------- trees of drafted tokens
+ * A speculative step whose drafted tokens form a tree. The step's rows of a
+ * sequence are its last n tokens in the cache (appended by moe_qkv_append at
+ * consecutive places, in any order that puts a row behind its parent); parents
+ * says which of them each one follows. Three calls, without a plan, under the
+ * rules of the attention calls above (streams, captures, d_status):
+ *   moe_attend_tree    attention of the tree's rows in every layer;
+ *   moe_verify_drafts  the drafted tokens against the target's probabilities;
+ *   moe_commit_drafts  the accepted tokens' keys and values moved together. */
+
+#define MOE_MAX_TREE_ROWS 256 /* rows of one sequence's tree */
+
+typedef struct moe_attend_tree_io {
+  moe_attend_paged_io_t rows;  /* as for moe_attend_paged */
+  const int32_t *parents;      /* [num_rows] place of each row's parent among its sequence's rows, less than its own; negative:
+                                * a root, which sees no other row of the tree */
+} moe_attend_tree_io_t;
+
+/* Bytes of device workspace that moe_attend_tree needs for these sizes (see moe_attend_paged_workspace). */
+moe_status_t moe_attend_tree_workspace(const moe_attend_tree_io_t *io, const moe_kv_cache_t *cache, int64_t *bytes_out);
+
+/* Attention of a tree's rows over the paged MXFP4 cache. Row i of the n rows of
+ * a sequence of length L sees the keys 0 .. L - n - 1, and key L - n + j for j = i
+ * and every row j on its way to the root. Everything else is as for
+ * moe_attend_paged, whose result this is when each row's parent is the row in
+ * front of it (to the last bits: the sums have another order). A parent that does not lie in front of its row
+ * is reported and counts as none. A sequence with more than MOE_MAX_TREE_ROWS rows is reported and gets no
+ * result: its rows are not touched. */
+moe_status_t moe_attend_tree(const moe_attend_tree_io_t *io, const moe_kv_cache_t *cache, void *workspace,
+                             int64_t workspace_bytes, int32_t *d_status, void *cuda_stream);
+
+#define MOE_DTYPE_F32 2u /* logits only */
+
+typedef struct moe_verify_drafts_io {
+  const void *logits;        /* [num_rows][vocab] the target's logits behind each row; element-aligned */
+  int64_t logits_stride;     /* elements from one row to the next, >= vocab */
+  const float *draft_probs;  /* [num_rows][vocab] the probabilities that the children of each row were drawn from,
+                              * independently; or NULL: the children were chosen without chance */
+  int64_t draft_stride;
+  const int32_t *tokens;     /* [num_rows] token of each row (that of a sequence's first row is not looked at) */
+  const int32_t *parents;    /* [num_rows] as for moe_attend_tree; or NULL: each row follows the one in front of it */
+  const int32_t *cu_rows;    /* [num_seqs + 1] first row of each sequence, then the end */
+  const float *temperature;  /* [num_seqs] of the target, 0: greedy; or NULL: 1 */
+  const float *accept_u;     /* [num_rows] a random number in [0, 1) for each row */
+  const float *sample_u;     /* [num_seqs] one for the new token */
+  int32_t *out_tokens;       /* [num_seqs][max_rows] the accepted rows' tokens, the new token, then -1 */
+  int32_t *path;             /* [num_seqs][max_rows] the accepted rows from the root (0) on, then -1 */
+  int32_t *accepted;         /* [num_seqs] how many rows were accepted, the root not counted */
+  int32_t num_seqs;          /* 0..65535 */
+  int32_t num_rows;
+  int32_t max_rows;          /* rows of a sequence at most, 1..MOE_MAX_TREE_ROWS */
+  int32_t vocab;             /* 1..2^24 */
+  uint32_t dtype;            /* MOE_DTYPE_*: of the logits */
+  uint32_t flags;            /* 0 */
+} moe_verify_drafts_io_t;
+
+/* Which drafted tokens the target accepts, and the token behind them, so that
+ * they are distributed as the target's own. The first row of each sequence is
+ * the root: a token that is settled. From there, with p = softmax(logits of the
+ * row / temperature) (at temperature 0: 1 for the first largest logit), the row's
+ * children are asked in their order:
+ *   with draft_probs q (of the row): child y is accepted if
+ *     u_y N q(y) < max(p(y) - c q(y), 0),    c = 0 and N = 1 at first;
+ *     a rejection adds N to c, and N becomes sum_t max(p(t) - c q(t), 0)
+ *     (p_k = max(p_(k-1) - q, 0) / sum is max(p - c_k q, 0) / N_k);
+ *   without: child y is accepted if u_y N < p(y), N = 1 at first; a rejection
+ *     sets p(y) to 0 and N to the sum of what is left;
+ *   at temperature 0: child y is accepted if it is the first largest logit's.
+ * The walk goes on from the accepted child. Where none is accepted, the new
+ * token is the first t at which the sum of what is left up to t exceeds
+ * sample_u times the whole (p itself, if nothing is left).
+ * Only the rows on the way are read. Decisions are made in binary32 from sums
+ * of relative error 2^-20; the sums that choose the new token have an error
+ * below 2^-34 of the whole, so it is the formula's but for numbers that close to a border.
+ * The same call gives the same result. A row on the way whose logits hold a NaN
+ * or +inf, or nothing but -inf, has no distribution: its children are rejected
+ * and the new token is -1. A sequence without rows gets accepted 0, and -1
+ * everywhere else; so does one whose offsets are out of range or that has more than max_rows rows (reported). A
+ * parent that does not lie in front of its row is reported, and the row has no
+ * parent; a token outside the vocabulary is reported and never accepted; a
+ * temperature that is negative or not finite is reported and counts as 1, one
+ * below 2^-100 as 2^-100. Rows other than the first without a parent are never
+ * asked. draft_probs must be finite and not negative. */
+moe_status_t moe_verify_drafts(const moe_verify_drafts_io_t *io, int32_t *d_status, void *cuda_stream);
+
+typedef struct moe_commit_drafts_io {
+  const int32_t *page_table;  /* [num_seqs][max_pages] as for moe_attend_paged */
+  const int32_t *lengths;     /* [num_seqs] tokens in the cache, the tree's rows included */
+  const int32_t *cu_rows;     /* [num_seqs + 1] */
+  const int32_t *path;        /* [num_seqs][path_stride] as moe_verify_drafts leaves it */
+  const int32_t *accepted;    /* [num_seqs] */
+  int32_t *new_lengths;       /* [num_seqs]; must not overlap the other arrays */
+  int32_t num_seqs;           /* 0..65535 */
+  int32_t max_pages;          /* max_pages * page_size <= 2^30 */
+  int32_t path_stride;        /* columns of path, >= 1 */
+  int32_t num_caches;         /* layers, 1..4096 */
+  uint32_t flags;             /* 0, or MOE_FLAG_TEST_BOUNDS */
+} moe_commit_drafts_io_t;
+
+/* Moves the accepted rows' keys and values to follow the context, in the caches
+ * of all layers: with base = lengths - n, token base + path[j] goes to base + j
+ * for j = 1 .. accepted, and new_lengths = base + 1 + accepted (lengths itself for
+ * a sequence without rows). What lies behind is left as it is. caches: a host
+ * array of num_caches descriptors, read during the call, alike in page_size,
+ * num_kv_heads and head_dim; the layers share page_table. A path must begin with
+ * 0 and rise; a sequence with a path, an accepted number, offsets or a length out of range
+ * is reported and left as it is, its length too (a negative one becomes 0). A token whose page is out of range is reported and
+ * not moved. Sequences must not share the pages that hold their rows. */
+moe_status_t moe_commit_drafts(const moe_commit_drafts_io_t *io, const moe_kv_cache_t *caches, int32_t *d_status,
+                               void *cuda_stream);
 
 /* Teardown: frees the plan's device memory and events, after a device-wide
  * synchronise. NULL is a no-op. */

@@ -12,7 +12,7 @@ import os
 
 from . import build as _build
 
-MOE_ABI_VERSION = 5
+MOE_ABI_VERSION = 6
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = 1
@@ -27,6 +27,9 @@ MOE_WEIGHTS_MXFP4 = 1
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2  # logits only
+
+MOE_MAX_TREE_ROWS = 256
 
 MOE_FLAG_TIMING = 1 << 0
 MOE_FLAG_PATH_GEMV = 1 << 1
@@ -54,6 +57,10 @@ EXPORTED = (
     "moe_attend_paged",
     "moe_attend_prompt_workspace",
     "moe_attend_prompt",
+    "moe_attend_tree_workspace",
+    "moe_attend_tree",
+    "moe_verify_drafts",
+    "moe_commit_drafts",
     "moe_destroy",
 )
 
@@ -182,6 +189,40 @@ class MoeAttendPromptIO(ctypes.Structure):
     ]
 
 
+class MoeAttendTreeIO(ctypes.Structure):
+    _fields_ = [("rows", MoeAttendPagedIO), ("parents", _P)]
+
+
+class MoeVerifyDraftsIO(ctypes.Structure):
+    _fields_ = [
+        ("logits", _P),
+        ("logits_stride", ctypes.c_int64),
+        ("draft_probs", _P),
+        ("draft_stride", ctypes.c_int64),
+        ("tokens", _P), ("parents", _P), ("cu_rows", _P),
+        ("temperature", _P), ("accept_u", _P), ("sample_u", _P),
+        ("out_tokens", _P), ("path", _P), ("accepted", _P),
+        ("num_seqs", ctypes.c_int32),
+        ("num_rows", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("dtype", ctypes.c_uint32),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
+class MoeCommitDraftsIO(ctypes.Structure):
+    _fields_ = [
+        ("page_table", _P), ("lengths", _P), ("cu_rows", _P), ("path", _P), ("accepted", _P),
+        ("new_lengths", _P),
+        ("num_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("path_stride", ctypes.c_int32),
+        ("num_caches", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
 _lib = None
 
 
@@ -239,6 +280,16 @@ def load(path: str | None = None):
     lib.moe_attend_prompt_workspace.argtypes = [ctypes.POINTER(MoeAttendPromptIO), ctypes.POINTER(ctypes.c_int64)]
     lib.moe_attend_prompt.restype = ctypes.c_int
     lib.moe_attend_prompt.argtypes = [ctypes.POINTER(MoeAttendPromptIO), _P, _P]
+    lib.moe_attend_tree_workspace.restype = ctypes.c_int
+    lib.moe_attend_tree_workspace.argtypes = [ctypes.POINTER(MoeAttendTreeIO), ctypes.POINTER(MoeKvCache),
+                                              ctypes.POINTER(ctypes.c_int64)]
+    lib.moe_attend_tree.restype = ctypes.c_int
+    lib.moe_attend_tree.argtypes = [ctypes.POINTER(MoeAttendTreeIO), ctypes.POINTER(MoeKvCache), _P, ctypes.c_int64, _P,
+                                    _P]
+    lib.moe_verify_drafts.restype = ctypes.c_int
+    lib.moe_verify_drafts.argtypes = [ctypes.POINTER(MoeVerifyDraftsIO), _P, _P]
+    lib.moe_commit_drafts.restype = ctypes.c_int
+    lib.moe_commit_drafts.argtypes = [ctypes.POINTER(MoeCommitDraftsIO), ctypes.POINTER(MoeKvCache), _P, _P]
     lib.moe_destroy.restype = ctypes.c_int
     lib.moe_destroy.argtypes = [_P]
     if lib.moe_abi_version() != MOE_ABI_VERSION:
@@ -407,6 +458,36 @@ def moe_attend_prompt(io: MoeAttendPromptIO, d_status=None, stream=None) -> int:
     """Causal attention over packed prompts."""
     lib = load()
     return lib.moe_attend_prompt(ctypes.byref(io), ptr(d_status), stream_ptr(stream))
+
+
+def moe_attend_tree_workspace(io: MoeAttendTreeIO, cache: MoeKvCache) -> int:
+    """Bytes of workspace that moe_attend_tree needs; raises MoeError on a non-OK status."""
+    lib = load()
+    n = ctypes.c_int64()
+    check("moe_attend_tree_workspace",
+          lib.moe_attend_tree_workspace(ctypes.byref(io), ctypes.byref(cache), ctypes.byref(n)))
+    return n.value
+
+
+def moe_attend_tree(io: MoeAttendTreeIO, cache: MoeKvCache, workspace, workspace_bytes: int, d_status=None,
+                    stream=None) -> int:
+    """Attention of trees of drafted tokens over the paged MXFP4 cache."""
+    lib = load()
+    return lib.moe_attend_tree(ctypes.byref(io), ctypes.byref(cache), ptr(workspace), workspace_bytes, ptr(d_status),
+                               stream_ptr(stream))
+
+
+def moe_verify_drafts(io: MoeVerifyDraftsIO, d_status=None, stream=None) -> int:
+    """Drafted tokens against the target's probabilities."""
+    lib = load()
+    return lib.moe_verify_drafts(ctypes.byref(io), ptr(d_status), stream_ptr(stream))
+
+
+def moe_commit_drafts(io: MoeCommitDraftsIO, caches, d_status=None, stream=None) -> int:
+    """The accepted rows moved together in the caches (a list of MoeKvCache)."""
+    lib = load()
+    return lib.moe_commit_drafts(ctypes.byref(io), (MoeKvCache * max(1, len(caches)))(*caches), ptr(d_status),
+                                 stream_ptr(stream))
 
 
 def moe_destroy(plan: int | None) -> int:

@@ -1,11 +1,13 @@
 """The attention in front of the MoE step, for PyTorch device memory and streams.
 
-Three calls over the C ABI, in the order a decoder layer makes them:
+Calls over the C ABI, in the order a decoder layer makes them:
 
 * ``qkv_append``: RMSNorm of each query and key head, rotary positions, and
   the MXFP4 append of keys and values to a paged cache;
 * ``attend_paged``: attention of the newest rows of each sequence (single
   tokens, or the rows of a verify step) over that cache;
+* ``attend_tree``: the same for rows that form a tree of drafted tokens (the end
+  of such a step is in ``speculative``);
 * ``attend_prompt``: causal attention over packed prompts in 16 bits. Given
   ``k_cached`` and ``v_cached`` of ``qkv_append`` it attends over the very
   values that later steps read from the cache.
@@ -38,6 +40,7 @@ from . import abi, build
 
 _module = None
 _bound = object()  # the library (abi.load()) whose entry points the module calls; none yet
+_bound_trees = object()  # the same for the calls of a step with drafted trees
 
 
 def _native():
@@ -52,6 +55,18 @@ def _native():
             "moe_attend_prompt")))
         _bound = lib
     return _module
+
+
+def _native_trees():
+    """The module, bound for the calls of a step with drafted trees too."""
+    global _bound_trees
+    module = _module if abi._lib is _bound else _native()
+    if _bound is not _bound_trees:
+        import ctypes
+        module.bind_trees(*(ctypes.cast(getattr(_bound, name), ctypes.c_void_p).value for name in (
+            "moe_attend_tree_workspace", "moe_attend_tree", "moe_verify_drafts", "moe_commit_drafts")))
+        _bound_trees = _bound
+    return module
 
 
 def _load():
@@ -163,6 +178,24 @@ def attend_paged(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor,
     module = _module if abi._lib is _bound else _native()
     return _call("moe_attend_paged", module.paged, stream, q, cache, page_table, lengths, cu_rows, max_rows, scale, out,
                  return_lse, d_status)
+
+
+def attend_tree(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor, lengths: torch.Tensor,
+                cu_rows: torch.Tensor, parents: torch.Tensor, *, max_rows: int = 1, scale: float | None = None,
+                out: torch.Tensor | None = None, return_lse: bool = False, d_status: torch.Tensor | None = None,
+                stream=None):
+    """Attention of trees of drafted tokens over the MXFP4 cache.
+
+    As ``attend_paged``, where the n rows of a sequence, its last n tokens in the cache, form a tree: parents int32
+    [rows] holds the place of each row's parent among its sequence's rows (less than its own; negative: a root). A row
+    sees the keys in front of the tree, the rows on its way to the root, and itself. At most 256 rows a sequence;
+    one with more is reported in d_status and its rows of out are left as they are.
+
+    Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
+    """
+    module = _module if abi._lib is _bound is _bound_trees else _native_trees()
+    return _call("moe_attend_tree", module.tree, stream, q, cache, page_table, lengths, cu_rows, parents, max_rows,
+                 scale, out, return_lse, d_status)
 
 
 def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, cu_keys: torch.Tensor, *,

@@ -1,5 +1,6 @@
-// attention_torch.cpp — the PyTorch side of the attention calls: checks of the
-// tensors, outputs and workspace from PyTorch's allocator, the C entry point.
+// attention_torch.cpp — the PyTorch side of the attention calls and of those of a
+// step with drafted trees: checks of the tensors, outputs and workspace from
+// PyTorch's allocator, the C entry point.
 //
 // What the calls of a decode step do on the GPU takes 4 to 12 us with few rows; a
 // binding written in Python needs 20 to 30 us a call to check and pass on some
@@ -20,6 +21,7 @@
 #include <cmath>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "moe.h"
 
@@ -30,6 +32,10 @@ decltype(&moe_attend_paged_workspace) attend_paged_workspace = nullptr;
 decltype(&moe_attend_paged) attend_paged = nullptr;
 decltype(&moe_attend_prompt_workspace) attend_prompt_workspace = nullptr;
 decltype(&moe_attend_prompt) attend_prompt = nullptr;
+decltype(&moe_attend_tree_workspace) attend_tree_workspace = nullptr;
+decltype(&moe_attend_tree) attend_tree = nullptr;
+decltype(&moe_verify_drafts) verify_drafts = nullptr;
+decltype(&moe_commit_drafts) commit_drafts = nullptr;
 
 struct Refused : std::runtime_error {  // becomes a ValueError
   using std::runtime_error::runtime_error;
@@ -83,10 +89,12 @@ void written(const at::Tensor &t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
-// Device and type of q, which the other tensors share.
+// Device and type of q (or of the tensor that a call is named after), which the other tensors share.
 struct Kind {
   at::Device device = at::Device(at::kCPU);
   at::ScalarType type = at::kBFloat16;
+
+  Kind(at::Device d, at::ScalarType t) : device(d), type(t) {}
 
   explicit Kind(const at::Tensor &q) : device(q.device()), type(q.scalar_type()) {
     if (q.dim() != 3) refuse("q must have 3 dimensions");
@@ -218,6 +226,22 @@ PyObject *py_bind(PyObject *, PyObject *const *arg, Py_ssize_t n) {
   });
 }
 
+// bind_trees(addresses of the four entry points of a step with drafted trees)
+PyObject *py_bind_trees(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject * {
+    void *p[4];
+    for (int i = 0; i < 4; ++i) {
+      p[i] = PyLong_AsVoidPtr(arg[i]);
+      if (!p[i]) throw std::runtime_error("no address");
+    }
+    attend_tree_workspace = reinterpret_cast<decltype(attend_tree_workspace)>(p[0]);
+    attend_tree = reinterpret_cast<decltype(attend_tree)>(p[1]);
+    verify_drafts = reinterpret_cast<decltype(verify_drafts)>(p[2]);
+    commit_drafts = reinterpret_cast<decltype(commit_drafts)>(p[3]);
+    Py_RETURN_NONE;
+  });
+}
+
 // check_cache(k_codes, k_scales, v_codes, v_scales)
 PyObject *py_check_cache(PyObject *, PyObject *const *arg, Py_ssize_t n) {
   return guarded(n, 4, [&]() -> PyObject * {
@@ -321,59 +345,193 @@ PyObject *py_append(PyObject *, PyObject *const *arg, Py_ssize_t n) {
   });
 }
 
+// The arguments of attention over the paged cache: q, cache, page_table, lengths, cu_rows, and from arg[at] on max_rows,
+// scale or None, out, return_lse, d_status. parents: of the rows of trees, or null.
+PyObject *paged_call(PyObject *const *arg, int at, const at::Tensor *parents) {
+  const at::Tensor &q = tensor(arg[0], "q"), &table = tensor(arg[2], "page_table");
+  const at::Tensor &lengths = tensor(arg[3], "lengths"), &cu_rows = tensor(arg[4], "cu_rows");
+  no_gradients({&q, optional_tensor(arg[at + 2], "out")});
+  const Kind kind(q);
+  moe_attend_tree_io_t tree = {};
+  moe_attend_paged_io_t &io = tree.rows;
+  io.q_stride = rows(q, "q", kind);
+  const int64_t T = q.size(0), H = q.size(1), D = q.size(2), B = lengths.dim() == 1 ? lengths.size(0) : -1;
+  io.lengths = vector<int32_t>(lengths, "lengths", at::kInt, B, kind);
+  io.cu_rows = vector<int32_t>(cu_rows, "cu_rows", at::kInt, B + 1, kind);
+  if (parents) tree.parents = vector<int32_t>(*parents, "parents", at::kInt, T, kind);
+  if (table.dim() != 2 || table.scalar_type() != at::kInt || table.device() != kind.device || table.size(0) != B ||
+      !table.is_contiguous())
+    refuse("page_table must be a contiguous int32 [sequences][pages] tensor on q's device");
+  at::Device device(at::kCPU);
+  const moe_kv_cache_t cache = kv_cache(arg[1], device, false);
+  if (device != kind.device || cache.head_dim != D) refuse("the cache must be on q's device, with q's head size");
+  const int64_t max_rows = PyLong_AsLongLong(arg[at]);
+  if (max_rows == -1 && PyErr_Occurred()) return nullptr;
+  int32_t *const word = status_word(optional_tensor(arg[at + 4], "d_status"), kind);
+  io.num_seqs = size32(B, "lengths");
+  io.num_rows = size32(T, "q");
+  io.max_pages = size32(table.size(1), "page_table");
+  io.max_rows = size32(max_rows, "max_rows");
+  io.num_heads = size32(H, "q");
+  io.dtype = kind.code();
+  io.scale = arg[at + 1] == Py_None ? float(1.0 / std::sqrt(double(D))) : float(number(arg[at + 1]));
+  const at::Tensor *given = optional_tensor(arg[at + 2], "out");
+  const bool return_lse = flag(arg[at + 3]);
+  at::Tensor out, lse, workspace;
+  moe_status_t s;
+  {
+    const WithoutGil free;
+    const c10::cuda::CUDAGuard guard(kind.device);
+    int64_t bytes = 0;
+    s = parents ? attend_tree_workspace(&tree, &cache, &bytes) : attend_paged_workspace(&io, &cache, &bytes);
+    if (s == MOE_OK) {
+      out = output(given, q, kind, io.out_stride);
+      if (return_lse) {
+        lse = make({T, H}, at::kFloat, kind);
+        io.lse = static_cast<float *>(lse.data_ptr());
+      }
+      workspace = make({bytes}, at::kByte, kind);
+      io.q = q.data_ptr();
+      io.out = out.data_ptr();
+      io.page_table = static_cast<const int32_t *>(table.data_ptr());
+      s = parents ? attend_tree(&tree, &cache, workspace.data_ptr(), bytes, word, stream_of(kind))
+                  : attend_paged(&io, &cache, workspace.data_ptr(), bytes, word, stream_of(kind));
+    }
+  }
+  if (s != MOE_OK) return PyLong_FromLong(s);
+  if (given) written(*given);
+  return outputs(out, lse);
+}
+
 // paged(q, cache, page_table, lengths, cu_rows, max_rows, scale or None, out, return_lse, d_status)
 PyObject *py_paged(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject * { return paged_call(arg, 5, nullptr); });
+}
+
+// tree(q, cache, page_table, lengths, cu_rows, parents, max_rows, scale or None, out, return_lse, d_status)
+PyObject *py_tree(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject * { return paged_call(arg, 6, &tensor(arg[5], "parents")); });
+}
+
+// Row stride of a [rows][vocab] tensor whose rows are contiguous.
+int64_t vocab_rows(const at::Tensor &t, const char *name) {
+  if (t.numel() && t.size(1) > 1 && t.stride(1) != 1) refuse(std::string("the rows of ") + name + " must be contiguous");
+  return t.size(0) > 1 && t.numel() ? t.stride(0) : t.size(1);
+}
+
+// verify(logits, tokens, cu_rows, accept_u, sample_u, parents, draft_probs, temperature, max_rows, d_status)
+PyObject *py_verify(PyObject *, PyObject *const *arg, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject * {
-    const at::Tensor &q = tensor(arg[0], "q"), &table = tensor(arg[2], "page_table");
-    const at::Tensor &lengths = tensor(arg[3], "lengths"), &cu_rows = tensor(arg[4], "cu_rows");
-    no_gradients({&q, optional_tensor(arg[7], "out")});
-    const Kind kind(q);
-    moe_attend_paged_io_t io = {};
-    io.q_stride = rows(q, "q", kind);
-    const int64_t T = q.size(0), H = q.size(1), D = q.size(2), B = lengths.dim() == 1 ? lengths.size(0) : -1;
-    io.lengths = vector<int32_t>(lengths, "lengths", at::kInt, B, kind);
+    const at::Tensor &logits = tensor(arg[0], "logits"), &tokens = tensor(arg[1], "tokens");
+    const at::Tensor &cu_rows = tensor(arg[2], "cu_rows");
+    const at::Tensor &accept_u = tensor(arg[3], "accept_u"), &sample_u = tensor(arg[4], "sample_u");
+    const at::Tensor *parents = optional_tensor(arg[5], "parents"), *draft = optional_tensor(arg[6], "draft_probs");
+    const at::Tensor *temperature = optional_tensor(arg[7], "temperature");
+    no_gradients({&logits, draft, temperature, &accept_u, &sample_u});
+    const Kind kind(logits.device(), logits.scalar_type());
+    if (logits.dim() != 2) refuse("logits must have 2 dimensions");
+    if (!kind.device.is_cuda() || (kind.type != at::kBFloat16 && kind.type != at::kHalf && kind.type != at::kFloat))
+      refuse("logits must be a CUDA tensor in bf16, fp16 or fp32");
+    const int64_t T = logits.size(0), V = logits.size(1), B = sample_u.dim() == 1 ? sample_u.size(0) : -1;
+    moe_verify_drafts_io_t io = {};
+    io.logits_stride = vocab_rows(logits, "logits");
+    if (draft) {
+      if (draft->sizes() != logits.sizes() || draft->scalar_type() != at::kFloat || draft->device() != kind.device)
+        refuse("draft_probs must be fp32, with the shape and device of logits");
+      io.draft_stride = vocab_rows(*draft, "draft_probs");
+      io.draft_probs = static_cast<const float *>(draft->data_ptr());
+    }
+    io.sample_u = vector<float>(sample_u, "sample_u", at::kFloat, B, kind);
     io.cu_rows = vector<int32_t>(cu_rows, "cu_rows", at::kInt, B + 1, kind);
-    if (table.dim() != 2 || table.scalar_type() != at::kInt || table.device() != kind.device || table.size(0) != B ||
-        !table.is_contiguous())
-      refuse("page_table must be a contiguous int32 [sequences][pages] tensor on q's device");
-    at::Device device(at::kCPU);
-    const moe_kv_cache_t cache = kv_cache(arg[1], device, false);
-    if (device != kind.device || cache.head_dim != D) refuse("the cache must be on q's device, with q's head size");
-    const int64_t max_rows = PyLong_AsLongLong(arg[5]);
+    io.tokens = vector<int32_t>(tokens, "tokens", at::kInt, T, kind);
+    io.accept_u = vector<float>(accept_u, "accept_u", at::kFloat, T, kind);
+    if (parents) io.parents = vector<int32_t>(*parents, "parents", at::kInt, T, kind);
+    if (temperature) io.temperature = vector<float>(*temperature, "temperature", at::kFloat, B, kind);
+    const int64_t max_rows = PyLong_AsLongLong(arg[8]);
     if (max_rows == -1 && PyErr_Occurred()) return nullptr;
+    if (max_rows < 1 || max_rows > MOE_MAX_TREE_ROWS)
+      refuse("max_rows must lie between 1 and " + std::to_string(MOE_MAX_TREE_ROWS));
     int32_t *const word = status_word(optional_tensor(arg[9], "d_status"), kind);
-    io.num_seqs = size32(B, "lengths");
-    io.num_rows = size32(T, "q");
-    io.max_pages = size32(table.size(1), "page_table");
-    io.max_rows = size32(max_rows, "max_rows");
-    io.num_heads = size32(H, "q");
-    io.dtype = kind.code();
-    io.scale = arg[6] == Py_None ? float(1.0 / std::sqrt(double(D))) : float(number(arg[6]));
-    const at::Tensor *given = optional_tensor(arg[7], "out");
-    const bool return_lse = flag(arg[8]);
-    at::Tensor out, lse, workspace;
+    io.num_seqs = size32(B, "sample_u");
+    io.num_rows = size32(T, "logits");
+    io.max_rows = int32_t(max_rows);
+    io.vocab = size32(V, "logits");
+    io.dtype = kind.type == at::kFloat ? MOE_DTYPE_F32 : kind.code();
+    at::Tensor out, path, accepted;
     moe_status_t s;
     {
       const WithoutGil free;
       const c10::cuda::CUDAGuard guard(kind.device);
-      int64_t bytes = 0;
-      s = attend_paged_workspace(&io, &cache, &bytes);
-      if (s == MOE_OK) {
-        out = output(given, q, kind, io.out_stride);
-        if (return_lse) {
-          lse = make({T, H}, at::kFloat, kind);
-          io.lse = static_cast<float *>(lse.data_ptr());
-        }
-        workspace = make({bytes}, at::kByte, kind);
-        io.q = q.data_ptr();
-        io.out = out.data_ptr();
-        io.page_table = static_cast<const int32_t *>(table.data_ptr());
-        s = attend_paged(&io, &cache, workspace.data_ptr(), bytes, word, stream_of(kind));
-      }
+      out = make({B, max_rows}, at::kInt, kind);
+      path = make({B, max_rows}, at::kInt, kind);
+      accepted = make({B}, at::kInt, kind);
+      io.logits = logits.data_ptr();
+      io.out_tokens = static_cast<int32_t *>(out.data_ptr());
+      io.path = static_cast<int32_t *>(path.data_ptr());
+      io.accepted = static_cast<int32_t *>(accepted.data_ptr());
+      s = verify_drafts(&io, word, stream_of(kind));
     }
     if (s != MOE_OK) return PyLong_FromLong(s);
-    if (given) written(*given);
-    return outputs(out, lse);
+    PyObject *dict = PyDict_New();
+    if (!dict) return nullptr;
+    put(dict, "tokens", out);
+    put(dict, "accepted", accepted);
+    put(dict, "path", path);
+    return dict;
+  });
+}
+
+// commit(caches, page_table, lengths, cu_rows, path, accepted, d_status); caches: a list or tuple
+PyObject *py_commit(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject * {
+    if (!PyList_Check(arg[0]) && !PyTuple_Check(arg[0])) throw std::invalid_argument("caches must be a list or a tuple");
+    const at::Tensor &table = tensor(arg[1], "page_table"), &lengths = tensor(arg[2], "lengths");
+    const at::Tensor &cu_rows = tensor(arg[3], "cu_rows"), &path = tensor(arg[4], "path");
+    const at::Tensor &accepted = tensor(arg[5], "accepted");
+    const Kind kind(lengths.device(), at::kInt);
+    if (!kind.device.is_cuda()) refuse("lengths must be a CUDA tensor");
+    moe_commit_drafts_io_t io = {};
+    const int64_t B = lengths.dim() == 1 ? lengths.size(0) : -1;
+    io.lengths = vector<int32_t>(lengths, "lengths", at::kInt, B, kind);
+    io.cu_rows = vector<int32_t>(cu_rows, "cu_rows", at::kInt, B + 1, kind);
+    io.accepted = vector<int32_t>(accepted, "accepted", at::kInt, B, kind);
+    for (const at::Tensor *t : {&table, &path})
+      if (t->dim() != 2 || t->scalar_type() != at::kInt || t->device() != kind.device || t->size(0) != B ||
+          !t->is_contiguous())
+        refuse(std::string(t == &table ? "page_table" : "path") +
+               " must be a contiguous int32 tensor with a row for each sequence, on the device of lengths");
+    int32_t *const word = status_word(optional_tensor(arg[6], "d_status"), kind);
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(arg[0]);
+    if (count < 1) refuse("there must be a cache");
+    std::vector<moe_kv_cache_t> caches(count);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      at::Device device(at::kCPU);
+      caches[i] = kv_cache(PySequence_Fast_GET_ITEM(arg[0], i), device, false);
+      if (device != kind.device) refuse("the caches must be on the device of lengths");
+      for (Py_ssize_t j = 0; j < i; ++j)
+        if (caches[j].k_codes == caches[i].k_codes && caches[i].num_pages) refuse("a cache must not be given twice");
+    }
+    io.num_seqs = size32(B, "lengths");
+    io.max_pages = size32(table.size(1), "page_table");
+    io.path_stride = size32(path.size(1), "path");
+    io.num_caches = size32(count, "caches");
+    at::Tensor out;
+    moe_status_t s;
+    {
+      const WithoutGil free;
+      const c10::cuda::CUDAGuard guard(kind.device);
+      out = make({B}, at::kInt, kind);
+      io.page_table = static_cast<const int32_t *>(table.data_ptr());
+      io.path = static_cast<const int32_t *>(path.data_ptr());
+      io.new_lengths = static_cast<int32_t *>(out.data_ptr());
+      s = commit_drafts(&io, caches.data(), word, stream_of(kind));
+    }
+    if (s != MOE_OK) return PyLong_FromLong(s);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      at::Device device(at::kCPU);
+      kv_cache(PySequence_Fast_GET_ITEM(arg[0], i), device, true);  // they count as written
+    }
+    return THPVariable_Wrap(out);
   });
 }
 
@@ -440,7 +598,9 @@ PyCFunction fast(F *f) {
 PyMethodDef methods[] = {
     {"bind", fast(py_bind), METH_FASTCALL, nullptr},         {"check_cache", fast(py_check_cache), METH_FASTCALL, nullptr},
     {"append", fast(py_append), METH_FASTCALL, nullptr},     {"paged", fast(py_paged), METH_FASTCALL, nullptr},
-    {"prompt", fast(py_prompt), METH_FASTCALL, nullptr},     {nullptr, nullptr, 0, nullptr}};
+    {"prompt", fast(py_prompt), METH_FASTCALL, nullptr},     {"bind_trees", fast(py_bind_trees), METH_FASTCALL, nullptr},
+    {"tree", fast(py_tree), METH_FASTCALL, nullptr},         {"verify", fast(py_verify), METH_FASTCALL, nullptr},
+    {"commit", fast(py_commit), METH_FASTCALL, nullptr},     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "attention_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
