@@ -1,0 +1,1176 @@
+// tree_tiles.cu — attention of large trees over the paged MXFP4 cache, on the 5th-generation tensor cores.
+//
+// Mathematics. As in attend_paged.cu: s_j = scale q . K_j, o = sum_j softmax(s)_j V_j
+// in one pass over the keys with a lazy reference, K_j = 2^(a - 127) k with
+// codes k and one scale code a per 32 dimensions, V likewise. Rows are (token,
+// head) pairs of one kv head's group; a row sees the keys in front of the tree,
+// its ancestors' and its own.
+//   Keys and values become f16 in shared memory: code times 2^(a - a_ref + 13), a_ref the largest scale code of
+//   32 keys. That is exact down to 2^-36 of the largest; what 2^a_ref takes off goes into the softmax: of keys into the
+//   factor of their scores, of values into the exponent of their weights (the sum of the weights is taken
+//   without it). Neither costs an operation per score. The accumulators are relative to one scale
+//   code of their own, which moves up when values beyond it appear.
+//   Queries become f16 times a power of two per row, probabilities f16 as in attend_paged.cu. All sums are binary32.
+//
+// Bound. 4 D flops per (row, head, key) on the tensor cores; a decoded key tile serves 128 or 256 rows, so
+// decoding (2 D conversions a key) is a small part of it, unlike with the 8 to 32 rows of a verify step.
+//
+// Layout. A block has two streams of 128 rows (MMA M, TMEM lanes), whose softmax runs in turn with the other's MMAs:
+//   wide items (more than 128 rows of a kv head): two row tiles over the same key tiles;
+//   narrow ones: the same rows over alternate key tiles, joined at the item's end through shared memory.
+//   warps 0-3   softmax of stream 0, a row a thread; warps 4-7 of stream 1; they also make the queries' tiles
+//   warps 8-11  codes and scales of 128 keys at a time: cp.async two tiles ahead into places of each thread's own,
+//               conversion into K and V tiles (K-major and N-major, 128-byte swizzle) of a ring
+//   warp 12     MMA issuer: S = Q K^T, then O += P V with P from TMEM, where the softmax wrote it over S
+// Step q is stream q mod 2; S of step q + 2 is issued behind P V of step q, so the S of a step that is complete also
+// says that the stream's accumulators are.
+//
+// Schedule. As in attend_paged.cu: the items' key tiles in units, equal contiguous shares for one block on each SM, parts of
+// items that several blocks share in a workspace, joined in a fixed order by a second kernel. Every warp finds
+// its block's share by itself, and goes from item to item without a queue.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "attention.cuh"
+#include "speculative.h"
+#include "tcgen05.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRows = 128;     // rows of a stream
+constexpr int kKeys = 128;     // keys of a tile
+constexpr int kThreads = 512;  // four warpgroups
+// Registers: 128 a thread at launch. 2 x 176 + 96 + 64 = 4 x 128.
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 176, kRegsDecode = 96, kRegsMma = 64;
+static_assert(2 * kRegsSoftmax + kRegsDecode + kRegsMma <= 4 * kRegsLaunch, "register split");
+constexpr int kWarpDecode = 8, kWarpMma = 12;
+constexpr uint32_t kTmemCols = 512;
+constexpr int64_t kWaitNs = 1000000000;
+constexpr float kLazy = 8.0f;       // the reference moves when the maximum is 2^kLazy beyond it
+constexpr float kUp = 7.0f;         // weights are held times 2^kUp (F16::kWeightUp)
+constexpr float kLowest = -3e38f;   // reference of a row without a weight
+constexpr int kTop = 13;            // the largest scale of 32 keys becomes 2^kTop
+constexpr int kBias = 127 + kTop;   // a value is its f16 times 2^(a_ref - kBias)
+constexpr int kHeadroom = 3;        // the accumulators' scale code lies that far above the largest seen
+constexpr int kLeast = -60;         // a value's exponent relative to it, at least (2^-60 of the largest)
+// What an item costs beside its tiles, in units of a narrow tile.
+constexpr int kOver = 8;
+constexpr int kMinShare = 2;  // units of a share, at least: each block between an item's first and last has a tile of it
+constexpr int kRaw = 2;             // tiles on their way
+constexpr int kJoinThreads = 256;
+constexpr int kMaxBlocks = 1024;
+
+struct TileArgs {
+  const uint16_t *q;
+  int64_t q_stride;
+  uint16_t *out;
+  int64_t out_stride;
+  float *lse;
+  const int32_t *page_table, *lengths, *cu_rows, *parents;
+  int num_seqs, num_rows, max_pages, num_heads, num_kv_heads, group;
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int num_pages, page_size;
+  float scale2;   // |scale| log2 e, at least 2^-100
+  uint32_t flip;  // 0x80008000 with a negative scale
+  float *parts;
+  int64_t part_cap, cached_rows;
+  int32_t *status;
+};
+
+// ------------------------------------------------------------------ the list of work
+// An item is a (sequence, kv head, block of 256 rows): kOver units, then one (sequences of up to 128 rows) or two for
+// each of its key tiles. A tile belongs to the block that has its first unit.
+
+struct Seq {
+  int b, row0, n, len;
+  int items, blocks, tiles, weight;
+
+  __device__ __forceinline__ int item_units() const { return tiles * weight + kOver; }
+  __device__ __forceinline__ int64_t units() const { return int64_t(items) * item_units(); }
+};
+
+__device__ __forceinline__ Seq load_seq(const TileArgs &a, int b, int32_t *status) {
+  Seq s = {b, 0, 0, 0, 0, 1, 0, 1};
+  if (b >= a.num_seqs) return s;
+  const Span r = seq_span(a.cu_rows, b, a.num_rows, status);
+  if (r.n <= 0) return s;
+  if (r.n > kMaxTree) {
+    out_of_range(status);
+    return s;
+  }
+  s.row0 = r.first;
+  s.n = r.n;
+  const int cap = a.max_pages * a.page_size;
+  int len = __ldg(a.lengths + b);
+  if (len < 0 || len > cap) {
+    out_of_range(status);
+    len = len < 0 ? 0 : cap;
+  }
+  s.len = len;
+  const int rows = s.n * a.group;
+  s.blocks = (rows + 2 * kRows - 1) / (2 * kRows);
+  s.items = a.num_kv_heads * s.blocks;
+  s.weight = rows > kRows ? 2 : 1;
+  s.tiles = max(1, (len + kKeys - 1) / kKeys);  // a sequence without keys still writes its rows
+  return s;
+}
+
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return uint64_t(a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
+
+__device__ __forceinline__ int64_t warp_sums(int64_t v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+struct Place {
+  Seq s;
+  int item, unit;
+};
+
+// Units in front of each 32 sequences, summed by the whole block; then every warp looks places up by itself.
+struct List {
+  const TileArgs &a;
+  const int64_t *before;
+  int64_t all;
+
+  __device__ List(const TileArgs &args, int64_t *shared, int64_t *total) : a(args), before(shared) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int chunks = (a.num_seqs + 31) / 32;
+    for (int c = warp; c < chunks; c += blockDim.x / 32) {
+      const int64_t v = warp_sums(load_seq(a, c * 32 + lane, nullptr).units());
+      if (lane == 31 && index_ok(a.status, c, kMaxSeqs / 32 + 1)) shared[c] = v;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int64_t base = 0;
+      for (int c0 = 0; c0 < chunks; c0 += 32) {
+        const int64_t v = c0 + lane < chunks ? shared[c0 + lane] : 0, s = warp_sums(v);
+        if (c0 + lane < chunks) shared[c0 + lane] = base + s - v;
+        base += __shfl_sync(0xFFFFFFFFu, s, 31);
+      }
+      if (lane == 0) *total = base;
+    }
+    __syncthreads();
+    all = *total;
+  }
+
+  // The place of unit p (0 <= p < all). Whole warp.
+  __device__ Place find(int64_t p) const {
+    const int lane = threadIdx.x & 31;
+    int c = 0;
+    for (int lo = 0, hi = (a.num_seqs + 31) / 32; lo < hi;) {  // the last chunk with before <= p
+      const int mid = (lo + hi) / 2;
+      if (before[mid] <= p) {
+        c = mid;
+        lo = mid + 1;
+      } else {
+        hi = mid;
+      }
+    }
+    const Seq s = load_seq(a, c * 32 + lane, nullptr);
+    const int64_t stop = warp_sums(s.units()), rest = p - before[c];
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, rest < stop);
+    const int w = hit ? __ffs(hit) - 1 : 31;
+    const int64_t in = rest - (__shfl_sync(0xFFFFFFFFu, stop, w) - __shfl_sync(0xFFFFFFFFu, s.units(), w));
+    Place pl;
+    pl.s = load_seq(a, c * 32 + w, nullptr);
+    pl.item = int(divide(in, pl.s.item_units()));
+    pl.unit = int(in - int64_t(pl.item) * pl.s.item_units());
+    return pl;
+  }
+};
+
+// A run of tiles of one item that a block computes (count may be 0).
+struct Segment {
+  Seq s;
+  int kv, r0;        // kv head, first (token, head) pair
+  int first, count;  // tiles
+  bool wide;         // two row tiles
+
+  __device__ __forceinline__ int steps() const { return wide ? 2 * count : count; }
+};
+
+// Cuts the next segment off a block's share; `left` units remain after it.
+__device__ __forceinline__ Segment next_segment(const TileArgs &a, Place &p, int64_t &left) {
+  Segment g;
+  g.s = p.s;
+  g.kv = p.item / p.s.blocks;
+  g.r0 = (p.item - g.kv * p.s.blocks) * 2 * kRows;
+  g.wide = p.s.n * a.group - g.r0 > kRows;
+  const int64_t room = p.s.item_units() - p.unit;
+  const int take = int(room < left ? room : left), w = p.s.weight;
+  g.first = (max(0, p.unit - kOver) + w - 1) / w;
+  g.count = (max(0, p.unit + take - kOver) + w - 1) / w - g.first;
+  left -= take;
+  p.unit = 0;
+  ++p.item;
+  if (left > 0) {
+    while (p.item >= p.s.items) {  // the next sequence with rows
+      p.s = load_seq(a, p.s.b + 1, nullptr);
+      p.item = 0;
+      if (p.s.b >= a.num_seqs) {
+        left = 0;
+        break;
+      }
+    }
+  }
+  return g;
+}
+
+struct Shares {
+  int64_t blocks, each, more;  // the first `more` blocks have each + 1 units
+
+  __device__ __forceinline__ int64_t begin(int64_t b) const { return b * each + (b < more ? b : more); }
+};
+
+__device__ __forceinline__ Shares make_shares(int64_t units, int64_t grid) {
+  Shares s;
+  s.blocks = units < grid * kMinShare ? units / kMinShare : grid;  // an item alone has more units than that
+  s.each = s.blocks ? divide(units, s.blocks) : 0;
+  s.more = units - s.each * s.blocks;
+  return s;
+}
+
+// ------------------------------------------------------------------ shared memory
+
+template <int D>
+struct Smem {
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of Q, K or V in f16: D/64 parts of 128 rows x 128 bytes
+  // Largest scales are kept for as many tiles. Those of tile j + kStages are written behind V of tile j + kStages - 1, whose
+  // slot was free when P V of tile j + kStages / 2 - 1 was done, so the softmax has read those of tile j.
+  static constexpr int kExps = kStages;
+  static constexpr int kRawBytes = kKeys * D / 2;
+  static constexpr uint32_t kColO = 2 * kKeys;
+  static_assert(kColO + 2 * D <= kTmemCols, "TMEM budget");
+  uint8_t q[2][kTileBytes];
+  uint8_t kv[kStages][kTileBytes];
+  uint8_t raw[kRaw][2][kRawBytes];             // codes of K and V as each thread copied them
+  uint8_t join[D == 128 ? 16 : kRows * 64 * 4];  // D = 128: the second stream's query tile serves
+  int2 exps[kExps][4];                         // by tile mod kExps and 32 keys: the largest scale codes of K and V
+  uint8_t parent[kMaxTree];                    // place of the parent plus one
+  int64_t total;
+  uint64_t q_full[2];      // the stream's queries are there (4 warps)
+  uint64_t full[kStages];  // a K or V tile is there (4 warps)
+  uint64_t empty[kStages]; // the MMAs that read it are done
+  uint64_t exps_full[kExps];  // a tile's largest scales are there (4 warps)
+  uint64_t s_full[2];      // S of a step complete, and everything issued before it
+  uint64_t p_full[2];      // P of a step written (4 warps)
+  uint64_t o_full[2];      // the stream's last P V is in O
+  uint64_t met;            // the softmax warps among themselves (8 warps)
+  uint64_t mma_done;
+  uint32_t tmem_base;
+
+  __device__ __forceinline__ uint8_t *exchange() { return D == 128 ? q[1] : join; }
+  static constexpr size_t bytes() { return sizeof(Smem) + 1024; }
+};
+
+// ------------------------------------------------------------------ PTX wrappers
+
+// D (+)= A B^T for K = 16 values of 16 bits, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with A in TMEM (two values per 32-bit column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// One lane of the (whole) warp, known to the compiler as such.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Descriptor of V as the N-major B operand (see attend_prompt.cu).
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  return (sw128_desc(saddr) & ~(uint64_t(0x3FFFu) << 16)) | (uint64_t(kKeys * 128 >> 4) << 16);
+}
+
+// 32 consecutive columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Every load of this thread has its values; the registers pass through, so that no use moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (test(bar, parity) || mbar_wait(bar, parity, kWaitNs)) return true;
+  if (status) report_error(status, MOE_ERR_TIMEOUT);
+  return false;
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Codes of byte B of w (low nibble first) as two f16.
+template <int B>
+__device__ __forceinline__ uint32_t decode2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b%2;\n\t}"
+      : "=r"(r)
+      : "r"(w), "n"(B));
+  return r;
+}
+
+// 2^e as binary32, e from -126 on (up to 127).
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((max(e, -126) + 127) << 23); }
+// The same down to the smallest of all, 2^-149.
+__device__ __forceinline__ float pow2_small(int e) { return e >= -126 ? pow2(e) : __int_as_float(1 << max(149 + e, 0)); }
+
+__device__ __forceinline__ bool row_ok(const TileArgs &a, int row, int head) {
+  return index_ok(a.status, row, a.num_rows) && index_ok(a.status, head, a.num_heads);
+}
+
+// ------------------------------------------------------------------ keys and values (warps 8-11)
+// A warp takes 32 keys of each tile, a lane one group of 32 dimensions of every 8th (D = 128) or 16th key: 16 bytes of codes.
+// Its lanes then store the 16-byte pieces of eight keys at a time, which the swizzle puts into different banks.
+
+template <int D>
+struct Decoder {
+  using S = Smem<D>;
+  static constexpr int kGroups = D / 32, kSpan = 32 / kGroups, kPer = 32 / kSpan;  // keys a pass, passes
+  static constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+  const TileArgs &a;
+  S &sm;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpDecode;
+  const int group = lane / kSpan, in = lane % kSpan;
+  const int32_t *table;
+  uint32_t at;  // lane 2 j + u: cached row of granule u (16 keys) of the warp's keys in the j-th tile of the batch
+  int looked;   // tiles of the segment that were looked up
+  uint32_t ks[kRaw][kPer], vs[kRaw][kPer];  // scale codes of the tiles on their way
+
+  __device__ __forceinline__ Decoder(const TileArgs &args, S &smem) : a(args), sm(smem) {}
+
+  __device__ __forceinline__ void start(const Segment &seg) {
+    table = a.page_table + int64_t(seg.s.b) * a.max_pages;
+    looked = 0;
+  }
+
+  __device__ __forceinline__ static void copy16(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
+                 : "memory");
+  }
+
+  // Codes and scales of tile i of the segment on their way; R = i mod kRaw.
+  template <int R>
+  __device__ __forceinline__ void fetch(const Segment &seg, int i) {
+    if (i < seg.count) {
+      const int j = i - looked;
+      if (i == looked || j == 16) {
+        looked = i;
+        const int step = i + (lane >> 1), key = (seg.first + step) * kKeys + warp * 32 + (lane & 1) * 16;
+        at = kNoRow;
+        if (step < seg.count && key < seg.s.len) {
+          const int pi = key / a.page_size;
+          const int page = index_ok(a.status, pi, a.max_pages) ? __ldg(table + pi) : 0;
+          if (page < 0 || page >= a.num_pages)
+            out_of_range(a.status);
+          else
+            at = (uint32_t(page) * a.num_kv_heads + seg.kv) * a.page_size + (key - pi * a.page_size);
+          if (at != kNoRow && !index_ok(a.status, int64_t(at) + 15, a.cached_rows)) at = kNoRow;
+        }
+      }
+      const int from = 2 * (i - looked);
+      const uint32_t r0 = __shfl_sync(0xFFFFFFFFu, at, from), r1 = __shfl_sync(0xFFFFFFFFu, at, from + 1);
+      uint8_t *const to = sm.raw[R][0] + (threadIdx.x & 127) * 16;
+#pragma unroll
+      for (int p = 0; p < kPer; ++p) {
+        const int key = p * kSpan + in;  // of the warp's 32
+        const uint32_t r = p * kSpan < 16 ? r0 : r1;
+        const bool some = r != kNoRow && (seg.first + i) * kKeys + warp * 32 + key < seg.s.len;
+        const uint64_t row = some ? uint64_t(r) + (key & 15) : 0;
+        copy16(to + p * 2048, a.k_codes + row * (D / 2) + group * 16, some ? 16 : 0);
+        copy16(to + p * 2048 + S::kRawBytes, a.v_codes + row * (D / 2) + group * 16, some ? 16 : 0);
+        ks[R][p] = some ? __ldg(a.k_scales + row * kGroups + group) : 0;
+        vs[R][p] = some ? __ldg(a.v_scales + row * kGroups + group) : 0;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  static __device__ __forceinline__ int largest(const uint32_t (&s)[kPer]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) m = max(m, s[p] == 255 ? 0u : s[p]);
+    return int(__reduce_max_sync(0xFFFFFFFFu, m));
+  }
+
+  // This thread's codes of a tile as f16 into their places.
+  __device__ __forceinline__ void convert(uint8_t *tile, const uint8_t *raw, const uint32_t (&s)[kPer], int top) const {
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+      const uint4 c = *reinterpret_cast<const uint4 *>(raw + (threadIdx.x & 127) * 16 + p * 2048);
+      const float f = s[p] == 255 ? INFINITY : __int_as_float(max(int(s[p]) - top + kBias, 0) << 23);
+      const uint32_t f2 = F16::pack(f, f);
+      const int key = warp * 32 + p * kSpan + in;
+      uint8_t *const row = tile + (group / 2) * (kKeys * 128) + key * 128;
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = make_uint4(mul2(decode2<0>(w[i]), f2), mul2(decode2<1>(w[i]), f2), mul2(decode2<2>(w[i]), f2),
+                                   mul2(decode2<3>(w[i]), f2));
+        *reinterpret_cast<uint4 *>(row + ((((group & 1) * 4 + i) ^ (key & 7)) << 4)) = v;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void filled(uint64_t *bar) const {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+
+  __device__ __forceinline__ bool ready(uint32_t e) const {  // the ring's entry e may be filled
+    return e < S::kStages || __all_sync(0xFFFFFFFFu, wait(&sm.empty[e % S::kStages], (e / S::kStages & 1) ^ 1, a.status));
+  }
+
+  // Tile i of the segment, tile number t of the block.
+  template <int R>
+  __device__ __forceinline__ bool tile(const Segment &seg, int i, uint32_t t) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
+    const int ktop = largest(ks[R]), vtop = largest(vs[R]);
+    if (lane == 0) {
+      sm.exps[t % S::kExps][warp] = make_int2(ktop, vtop);
+      mbar_arrive(&sm.exps_full[t % S::kExps]);
+    }
+    const uint32_t e = 2 * t, k = e % S::kStages, v = (e + 1) % S::kStages;
+    if (!ready(e)) return false;
+    convert(sm.kv[k], sm.raw[R][0], ks[R], ktop);
+    filled(&sm.full[k]);
+    if (!ready(e + 1)) return false;
+    convert(sm.kv[v], sm.raw[R][1], vs[R], vtop);
+    filled(&sm.full[v]);
+    fetch<R>(seg, i + kRaw);
+    return true;
+  }
+
+  __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t) {
+    start(seg);
+    static_assert(kRaw == 2, "two places in turn");
+    fetch<0>(seg, 0);
+    fetch<1>(seg, 1);
+    bool ok = true;
+    for (int i = 0; ok && i < seg.count; i += 2) {
+      ok = tile<0>(seg, i, t + i);
+      if (ok && i + 1 < seg.count) ok = tile<1>(seg, i + 1, t + i + 1);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    return ok;
+  }
+};
+
+// ------------------------------------------------------------------ MMA issuer (one lane of warp 12)
+
+template <int D>
+struct Issuer {
+  using S = Smem<D>;
+  static constexpr uint32_t kBase = (1u << 4) | (uint32_t(kRows >> 4) << 24);  // f16 operands, binary32 sums
+  static constexpr uint32_t kDescS = kBase | (uint32_t(kKeys >> 3) << 17);
+  static constexpr uint32_t kDescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);  // B is N-major
+  const TileArgs &a;
+  S &sm;
+  const uint32_t tmem;
+  uint32_t queries[2] = {0, 0}, written[2] = {0, 0};  // phases of q_full and p_full
+
+  __device__ __forceinline__ Issuer(const TileArgs &args, S &smem, uint32_t t) : a(args), sm(smem), tmem(t) {}
+
+  __device__ __forceinline__ bool full(uint32_t e) const {
+    return wait(&sm.full[e % S::kStages], e / S::kStages & 1, a.status);
+  }
+
+  __device__ __forceinline__ bool scores(const Segment &seg, int q, uint32_t t) {
+    const int x = q & 1, tile = seg.wide ? q >> 1 : q;
+    const uint32_t e = 2 * (t + tile);
+    if ((q == 0 || (q == 1 && seg.wide))) {
+      if (!wait(&sm.q_full[x], queries[x] & 1, a.status)) return false;
+      ++queries[x];
+    }
+    if ((!seg.wide || x == 0) && !full(e)) return false;
+    tmem_fence_after();
+    const uint64_t qd = sw128_desc(smem_u32(sm.q[seg.wide ? x : 0])), kd = sw128_desc(smem_u32(sm.kv[e % S::kStages]));
+    const uint32_t d = tmem + x * kKeys;
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)  // 16 values are 32 bytes: 2 in the address field
+        mma_ss(d, qd + p * (kRows * 128 >> 4) + 2 * c, kd + p * (kKeys * 128 >> 4) + 2 * c, kDescS, (p | c) != 0);
+    mma_commit(&sm.s_full[x]);
+    if (!seg.wide || x == 1) mma_commit(&sm.empty[e % S::kStages]);
+    return true;
+  }
+
+  __device__ __forceinline__ bool values(const Segment &seg, int q, uint32_t t) {
+    const int x = q & 1, tile = seg.wide ? q >> 1 : q;
+    const uint32_t e = 2 * (t + tile) + 1;
+    if ((!seg.wide || x == 0) && !full(e)) return false;
+    if (!wait(&sm.p_full[x], written[x] & 1, a.status)) return false;
+    ++written[x];
+    tmem_fence_after();
+    const uint64_t vd = v_desc(smem_u32(sm.kv[e % S::kStages]));
+    const uint32_t pa = tmem + x * kKeys, d = tmem + S::kColO + x * D;
+#pragma unroll
+    for (int c = 0; c < kKeys / 16; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
+      mma_ts(d, pa + 8 * c, vd + c * (2048 >> 4), kDescO, ((q >> 1) | c) != 0);
+    if (!seg.wide || x == 1) mma_commit(&sm.empty[e % S::kStages]);
+    return true;
+  }
+
+  __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t) {
+    const int steps = seg.steps();
+    for (int q = 0; q < 2 && q < steps; ++q)
+      if (!scores(seg, q, t)) return false;
+    for (int q = 0; q < steps; ++q) {
+      if (!values(seg, q, t)) return false;
+      if (q + 2 < steps) {
+        if (!scores(seg, q + 2, t)) return false;
+      } else {
+        mma_commit(&sm.o_full[q & 1]);
+      }
+    }
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ softmax (warps 0-7)
+
+template <class T, int D>
+struct Softmax {
+  using S = Smem<D>;
+  const TileArgs &a;
+  S &sm;
+  const int x = threadIdx.x >> 7, row = threadIdx.x & 127;
+  const uint32_t lanes, ts, to;  // TMEM addresses of the warp's S and O
+  uint32_t scored = 0, ended = 0, meetings = 0;  // phases of s_full, o_full and met
+
+  __device__ __forceinline__ Softmax(const TileArgs &args, S &smem, uint32_t tmem)
+      : a(args), sm(smem), lanes(uint32_t((threadIdx.x >> 5 & 3) * 32) << 16), ts(tmem + lanes + x * kKeys),
+        to(tmem + lanes + S::kColO + x * D) {}
+
+  // All softmax warps have come here. A barrier with a limit: a warp that gave up elsewhere does not come.
+  __device__ __forceinline__ bool meet() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.met);
+    return __all_sync(0xFFFFFFFFu, wait(&sm.met, meetings++ & 1, a.status));
+  }
+
+  // The thread's query as f16 into the stream's tile; the factor from products with f16 keys to exponents of two.
+  __device__ __forceinline__ float load_query(const Segment &seg, int token, int head, bool real, bool store) {
+    uint4 raw[D / 8];
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + int64_t(seg.s.row0 + token) * a.q_stride + int64_t(head) * D);
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) raw[i] = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      uint4 &v = raw[i];
+      v.x ^= a.flip, v.y ^= a.flip, v.z ^= a.flip, v.w ^= a.flip;
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) amax = fmaxf(amax, fmaxf(fabsf(T::lo(w[c])), fabsf(T::hi(w[c]))));
+    }
+    // times 2^(14 - e): the largest lies in [2^14, 2^15), parts down to 2^-28 of it keep all their bits
+    const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -100), 126);
+    const float up = __uint_as_float(uint32_t(127 + 14 - e) << 23);
+    if (store) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] = F16::pack(T::lo(w[c]) * up, T::hi(w[c]) * up);
+        *reinterpret_cast<uint4 *>(sm.q[seg.wide ? x : 0] + (i / 8) * (kRows * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+            make_uint4(f[0], f[1], f[2], f[3]);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.q_full[seg.wide ? x : 0]);
+    }
+    return a.scale2 / up;
+  }
+
+  // Which of 128 keys, the first `ahead` places behind the tree's first, the row of a token sees.
+  __device__ __forceinline__ void visible(int token, int ahead, bool real, uint32_t (&see)[4]) const {
+    uint32_t m[kMaxTree / 32];
+#pragma unroll
+    for (int w = 0; w < kMaxTree / 32; ++w) m[w] = 0;
+    if (real) {
+      for (int j = token; j >= 0; j = int(sm.parent[j]) - 1) {
+#pragma unroll
+        for (int w = 0; w < kMaxTree / 32; ++w)
+          if (j >> 5 == w) m[w] |= 1u << (j & 31);
+      }
+    }
+    const auto word = [&](int i) {  // bits 32 i .. of the tree, all set in front of it
+      uint32_t r = i < 0 ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+      for (int w = 0; w < kMaxTree / 32; ++w)
+        if (i == w) r = m[w];
+      return r;
+    };
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int first = ahead + 32 * c;
+      see[c] = __funnelshift_r(word(first >> 5), word((first >> 5) + 1), first & 31);
+    }
+  }
+
+  // The row's scores of a key tile, as far as it sees the keys.
+  __device__ __forceinline__ void load_scores(bool masked, const uint32_t (&see)[4], uint32_t (&s)[kKeys]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_wait_ld(s + 32 * i);
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (!(see[i / 32] >> (i & 31) & 1)) s[i] = 0xFF800000u;  // -inf
+    }
+  }
+
+  // The row's largest score, an exponent of two.
+  static __device__ __forceinline__ float largest(const uint32_t (&s)[kKeys], const float (&mul)[4]) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        m[0] = fmaxf(m[0], fmaxf(__uint_as_float(s[32 * c + i]), __uint_as_float(s[32 * c + i + 1])));
+        m[1] = fmaxf(m[1], fmaxf(__uint_as_float(s[32 * c + i + 2]), __uint_as_float(s[32 * c + i + 3])));
+      }
+      top = fmaxf(top, fmaxf(m[0], m[1]) * mul[c]);
+    }
+    return top;
+  }
+
+  // P = 2^(s mul + base) in f16, over the first half of s, and the sum of 2^(s mul + base - shift).
+  static __device__ __forceinline__ float exponentials(uint32_t (&s)[kKeys], const float (&mul)[4], float base,
+                                                       const int (&shift)[4]) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float b = base + float(shift[c]);
+      float add[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float u = exp2_approx(fmaf(__uint_as_float(s[32 * c + i]), mul[c], b));
+        const float v = exp2_approx(fmaf(__uint_as_float(s[32 * c + i + 1]), mul[c], b));
+        add[(i >> 1) & 1] += u + v;
+        s[16 * c + i / 2] = F16::pack(u, v);
+      }
+      sum = fmaf(add[0] + add[1], pow2(-shift[c]), sum);
+    }
+    return sum;
+  }
+
+  __device__ __forceinline__ void scale_accumulators(float f) const {
+#pragma unroll 1
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t o[32];
+      tmem_ld32(to + 32 * i, o);
+      tmem_wait_ld(o);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+      tmem_st32(to + 32 * i, o);
+    }
+  }
+
+  // 32 dimensions of the row's accumulators.
+  __device__ __forceinline__ void load_out(int first, float f, float (&v)[32]) const {
+    uint32_t o[32];
+    tmem_ld32(to + first, o);
+    tmem_wait_ld(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f;
+  }
+
+  // The row's result: 32 dimensions from `first` on, whole or as a part.
+  __device__ __forceinline__ void store_out(const Segment &seg, float *part, int part_row, int token, int head, int first, float inv,
+                                            const float (&v)[32]) const {
+    if (part) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<float4 *>(part + part_row * D + first + 4 * c) =
+            make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    } else {
+      uint16_t *out = a.out + int64_t(seg.s.row0 + token) * a.out_stride + int64_t(head) * D + first;
+      const bool some = inv != 0.0f;  // a NaN counts
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = some ? T::pack(v[8 * c + 2 * i] * inv, v[8 * c + 2 * i + 1] * inv) : 0u;
+        *reinterpret_cast<uint4 *>(out + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t, int slot) {
+    const int r = seg.r0 + (seg.wide ? x * kRows : 0) + row;
+    const int token = r / a.group, head = seg.kv * a.group + r - token * a.group;
+    bool real = r < seg.s.n * a.group;
+    if (real) real = row_ok(a, seg.s.row0 + token, head);
+    const float unit = load_query(seg, token, head, real, seg.wide || x == 0);
+    const int before = seg.s.len - seg.s.n;  // keys in front of the tree
+    if ((seg.first + seg.count) * kKeys > before) {
+      const int i = threadIdx.x;
+      if (i < seg.s.n) {
+        int p = index_ok(a.status, seg.s.row0 + i, a.num_rows) ? __ldg(a.parents + seg.s.row0 + i) : -1;
+        if (p >= i) {
+          out_of_range(a.status);
+          p = -1;
+        }
+        sm.parent[i] = uint8_t(p < 0 ? 0 : p + 1);
+      }
+      if (!meet()) return false;
+    }
+    float ref = kLowest, total = 0.0f;
+    int scale = 0;  // of the accumulators
+    const int steps = seg.steps();
+    for (int q = x; q < steps; q += 2) {
+      const int i = seg.wide ? q >> 1 : q, key0 = (seg.first + i) * kKeys;
+      const uint32_t n = t + i;
+      if (!__all_sync(0xFFFFFFFFu, wait(&sm.exps_full[n % S::kExps], n / S::kExps & 1, a.status))) return false;
+      int shift[4], vtop = 0;
+      float mul[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int2 e = sm.exps[n % S::kExps][c];
+        mul[c] = fmaxf(unit * pow2(e.x - kBias), 0x1p-126f);  // not 0: -inf must stay -inf
+        shift[c] = e.y;
+        vtop = max(vtop, e.y);
+      }
+      const bool masked = key0 + kKeys > before;  // some key of the tile may be hidden
+      uint32_t see[4] = {0, 0, 0, 0};
+      if (masked) visible(token, key0 - before, real, see);
+      if (!__all_sync(0xFFFFFFFFu, wait(&sm.s_full[x], scored & 1, a.status))) return false;
+      ++scored;
+      tmem_fence_after();
+      uint32_t s[kKeys];
+      load_scores(masked, see, s);
+      const float top = largest(s, mul);
+      if (q < 2) {
+        scale = vtop + kHeadroom;
+        ref = fmaxf(top, kLowest);
+      } else if (__any_sync(0xFFFFFFFFu, top - ref > kLazy) || vtop > scale) {
+        // the accumulators hold every tile before this one (see the order of issue)
+        float f = 1.0f;
+        if (top - ref > kLazy) {
+          f = exp2_approx(ref - top);
+          ref = top;
+        }
+        total *= f;
+        if (vtop > scale) {
+          f *= pow2(scale - (vtop + kHeadroom));
+          scale = vtop + kHeadroom;
+        }
+        scale_accumulators(f);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) shift[c] = max(shift[c] - scale, kLeast);
+      total += exponentials(s, mul, kUp - ref, shift);
+      tmem_st32(ts, s);
+      tmem_st32(ts + 32, s + 32);
+      tmem_wait_st();
+      tmem_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.p_full[x]);
+    }
+    if (x < steps) {
+      if (!__all_sync(0xFFFFFFFFu, wait(&sm.o_full[x], ended & 1, a.status))) return false;
+      ++ended;
+      tmem_fence_after();
+    }
+    // ---- results
+    const bool whole = seg.count == seg.s.tiles;
+    float *part = nullptr;
+    if (!whole) {
+      if (!index_ok(a.status, slot, a.part_cap)) real = false;
+      part = a.parts + int64_t(slot) * 2 * kRows * (D + 2);
+    }
+    const bool both = !seg.wide && steps > 1;  // two streams of the same rows
+    float f = pow2_small(scale - kBias);
+    if (both) {
+      float2 *const rows = reinterpret_cast<float2 *>(sm.exchange());  // reference and sum, by stream
+      rows[x * kRows + row] = make_float2(ref, total);
+      if (!meet()) return false;
+      const float2 u = rows[row], v = rows[kRows + row];
+      if (!meet()) return false;
+      const float m = fmaxf(u.x, v.x);
+      total = u.y * exp2_approx(u.x - m) + v.y * exp2_approx(v.x - m);
+      f *= exp2_approx(ref - m);
+      ref = m;
+    }
+    const float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a NaN stays one
+    const int part_row = (seg.wide ? x * kRows : 0) + row;
+    const bool writes = seg.wide || x == 0;
+    if (real && writes) {
+      if (part) {
+        part[2 * kRows * D + part_row] = ref;
+        part[2 * kRows * D + 2 * kRows + part_row] = total;
+      } else if (a.lse) {
+        a.lse[int64_t(seg.s.row0 + token) * a.num_heads + head] =
+            total != 0.0f ? (log2f(total) + (ref - kUp)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+#pragma unroll 1
+    for (int half = 0; half < D / 64; ++half) {
+      uint8_t *const place = sm.exchange() + row * 256;  // 64 floats of the row, 16-byte pieces exchanged by row
+      if (both && x == 1) {
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          float v[32];
+          load_out(64 * half + 32 * i, f, v);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4 *>(place + (((8 * i + c) ^ (row & 15)) << 4)) =
+                make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        }
+      }
+      if (both && !meet()) return false;
+      if (writes) {
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          float v[32];
+          load_out(64 * half + 32 * i, f, v);
+          if (both) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float4 o = *reinterpret_cast<const float4 *>(place + (((8 * i + c) ^ (row & 15)) << 4));
+              v[4 * c] += o.x, v[4 * c + 1] += o.y, v[4 * c + 2] += o.z, v[4 * c + 3] += o.w;
+            }
+          }
+          if (real) store_out(seg, part, part_row, token, head, 64 * half + 32 * i, inv, v);
+        }
+      }
+      if (both && !meet()) return false;
+    }
+    tmem_fence_before();
+    return meet();  // parents and sums of this segment have been read
+  }
+};
+
+// ------------------------------------------------------------------ kernel
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs a) {
+  extern __shared__ unsigned char tiles_smem_raw[];
+  using S = Smem<D>;
+  static_assert(S::bytes() <= 227 * 1024, "shared memory budget");
+  S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(tiles_smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == kWarpMma + 1 && elect_one()) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&sm.full[i], 4);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < S::kExps; ++i) mbar_init(&sm.exps_full[i], 4);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.q_full[x], 4);
+      mbar_init(&sm.s_full[x], 1);
+      mbar_init(&sm.p_full[x], 4);
+      mbar_init(&sm.o_full[x], 1);
+    }
+    mbar_init(&sm.met, 8);
+    mbar_init(&sm.mma_done, 1);
+    fence_mbar_init();
+  }
+  if (blockIdx.x == 0)  // what is out of range is reported once
+    for (int b = threadIdx.x; b < a.num_seqs; b += kThreads) load_seq(a, b, a.status);
+  // the sums lie where the first keys come later
+  const List list(a, reinterpret_cast<int64_t *>(sm.kv[0]), &sm.total);
+  const Shares shares = make_shares(list.all, gridDim.x);
+  const bool any = int64_t(blockIdx.x) < shares.blocks;
+  const int64_t begin = any ? shares.begin(blockIdx.x) : 0, end = any ? shares.begin(int64_t(blockIdx.x) + 1) : 0;
+  Place place;
+  if (any) place = list.find(begin);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  int64_t left = end - begin;
+  uint32_t t = 0;  // tiles of the block so far
+  if (warp < kWarpDecode) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    Softmax<T, D> role(a, sm, tmem);
+    for (int i = 0; left > 0; ++i) {
+      const Segment seg = next_segment(a, place, left);
+      if (seg.count == 0) continue;
+      if (!role.segment(seg, t, int(blockIdx.x) * 2 + (i ? 1 : 0))) break;
+      t += seg.count;
+    }
+  } else if (warp < kWarpMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
+    Decoder<D> role(a, sm);
+    while (left > 0) {
+      const Segment seg = next_segment(a, place, left);
+      if (seg.count == 0) continue;
+      if (!role.segment(seg, t)) break;
+      t += seg.count;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (warp == kWarpMma && elect_one()) {
+      Issuer<D> role(a, sm, tmem);
+      while (left > 0) {
+        const Segment seg = next_segment(a, place, left);
+        if (seg.count == 0) continue;
+        if (!role.segment(seg, t)) break;
+        t += seg.count;
+      }
+      if (end > begin) {
+        mma_commit(&sm.mma_done);  // every MMA is done before TMEM is freed
+        mbar_wait(&sm.mma_done, 0, kWaitNs);
+      }
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == kWarpMma)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// ------------------------------------------------------------------ joining the blocks
+// Block c joins the item whose first tile is the main kernel's block c's, if later blocks have tiles of it too.
+
+constexpr int kJoinRows = 8, kJoinY = 8;  // rows at a time, blocks of an item
+
+template <class T, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const TileArgs a) {
+  __shared__ int64_t before[kMaxSeqs / 32 + 1], total;
+  __shared__ float weight[kJoinRows][kMaxBlocks], sums[kJoinRows], tops[kJoinRows];
+  static_assert(kJoinThreads == kJoinRows * 32 && kJoinRows * (D / 4) <= kJoinThreads, "a warp for each row's weights");
+  const List list(a, before, &total);
+  const Shares shares = make_shares(list.all, gridDim.x);
+  const int64_t c = blockIdx.x;
+  Place p;
+  bool none = true;
+  int64_t last = c + 1, item0 = 0, begin = 0;
+  if (c + 1 < shares.blocks) {
+    begin = shares.begin(c);
+    const int64_t end = shares.begin(c + 1);
+    p = list.find(end - 1);
+    item0 = end - 1 - p.unit;
+    const int64_t tile0 = item0 + kOver, tile1 = tile0 + int64_t(p.s.tiles - 1) * p.s.weight;  // the first and last tile's units
+    none = tile0 < begin || tile0 >= end || tile1 < end;
+    while (!none && shares.begin(last + 1) <= tile1) ++last;
+  }
+  pdl_wait_primary();  // every block: this kernel must not end before the main one
+  if (none) return;
+  const int parts = int(last - c) + 1;
+  if (!index_ok(a.status, parts - 1, kMaxBlocks) || !index_ok(a.status, 2 * last, a.part_cap)) return;
+  constexpr int64_t kPart = 2 * kRows * (D + 2);
+  const float *const part0 = a.parts + (c * 2 + (item0 <= begin ? 0 : 1)) * kPart, *const part1 = a.parts + c * 2 * kPart;
+  const auto part = [&](int b) { return b ? part1 + int64_t(b) * 2 * kPart : part0; };
+  const int kv = p.item / p.s.blocks, r0 = (p.item - kv * p.s.blocks) * 2 * kRows;
+  const int rows = min(2 * kRows, p.s.n * a.group - r0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int first = int(blockIdx.y) * kJoinRows; first < rows; first += kJoinY * kJoinRows) {
+    {
+      const int head = 2 * kRows * D + first + warp;
+      float m = kLowest, l = 0.0f;
+      for (int b = lane; b < parts; b += 32) m = fmaxf(m, part(b)[head]);
+#pragma unroll
+      for (int k = 16; k; k /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
+      for (int b = lane; b < parts; b += 32) {
+        const float f = exp2_approx(part(b)[head] - m);
+        weight[warp][b] = f;
+        l = fmaf(part(b)[head + 2 * kRows], f, l);
+      }
+#pragma unroll
+      for (int k = 16; k; k /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, k);
+      if (lane == 0) {
+        tops[warp] = m;
+        sums[warp] = l;
+      }
+    }
+    __syncthreads();
+    const int row = threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4)), r = r0 + first + row;
+    if (row < kJoinRows && first + row < rows) {
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+      for (int b = 0; b < parts; ++b) {
+        const float4 v = *reinterpret_cast<const float4 *>(part(b) + (first + row) * D + d);
+        const float w = weight[row][b];
+        o.x = fmaf(v.x, w, o.x), o.y = fmaf(v.y, w, o.y), o.z = fmaf(v.z, w, o.z), o.w = fmaf(v.w, w, o.w);
+      }
+      const float l = sums[row], inv = l != 0.0f ? 1.0f / l : 0.0f;
+      const int token = r / a.group, h = kv * a.group + r - token * a.group;
+      if (row_ok(a, p.s.row0 + token, h)) {
+        *reinterpret_cast<uint2 *>(a.out + int64_t(p.s.row0 + token) * a.out_stride + int64_t(h) * D + d) =
+            l != 0.0f ? make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+        if (d == 0 && a.lse)
+          a.lse[int64_t(p.s.row0 + token) * a.num_heads + h] =
+              l != 0.0f ? (log2f(l) + (tops[row] - kUp)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+int blocks_of(int num_sms) { return num_sms < kMaxBlocks ? num_sms : kMaxBlocks; }
+
+template <class T, int D>
+cudaError_t launch(const TileArgs &a, int num_sms, cudaStream_t st) {
+  // The register split assumes the launch's share: a build that gave the kernel less must not run. Only the answer is
+  // remembered, not a query that failed.
+  static std::atomic<int> regs{0};
+  if (!regs.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes at;
+    const cudaError_t asked = cudaFuncGetAttributes(&at, tree_tiles_kernel<T, D>);
+    if (asked != cudaSuccess) return asked;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kRegsLaunch) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(tree_tiles_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(Smem<D>::bytes()));
+  if (e != cudaSuccess) return e;
+  const unsigned grid = unsigned(blocks_of(num_sms));
+  tree_tiles_kernel<T, D><<<grid, kThreads, Smem<D>::bytes(), st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, kJoinY);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_tiles_kernel<T, D>, a);
+}
+
+}  // namespace
+
+int64_t tree_tiles_workspace(const moe_kv_cache_t &c, int num_sms) {
+  return int64_t(blocks_of(num_sms)) * 2 * 2 * kRows * (c.head_dim + 2) * 4;
+}
+
+cudaError_t launch_tree_tiles(const moe_attend_tree_io_t &io, const moe_kv_cache_t &c, void *workspace,
+                              int64_t workspace_bytes, int32_t *status, int num_sms, cudaStream_t st) {
+  const moe_attend_paged_io_t &r = io.rows;
+  TileArgs a = {};
+  a.q = static_cast<const uint16_t *>(r.q);
+  a.q_stride = r.q_stride;
+  a.out = static_cast<uint16_t *>(r.out);
+  a.out_stride = r.out_stride;
+  a.lse = r.lse;
+  a.page_table = r.page_table;
+  a.lengths = r.lengths;
+  a.cu_rows = r.cu_rows;
+  a.parents = io.parents;
+  a.num_seqs = r.num_seqs;
+  a.num_rows = r.num_rows;
+  a.max_pages = r.max_pages;
+  a.num_heads = r.num_heads;
+  a.num_kv_heads = c.num_kv_heads;
+  a.group = r.num_heads / c.num_kv_heads;
+  a.k_codes = c.k_codes;
+  a.k_scales = c.k_scales;
+  a.v_codes = c.v_codes;
+  a.v_scales = c.v_scales;
+  a.num_pages = c.num_pages;
+  a.page_size = c.page_size;
+  a.cached_rows = int64_t(c.num_pages) * c.page_size * c.num_kv_heads;
+  a.scale2 = fmaxf(fabsf(r.scale) * 1.4426950408889634f, 0x1p-100f);
+  a.flip = r.scale < 0.0f ? 0x80008000u : 0u;
+  a.parts = static_cast<float *>(workspace);
+  a.part_cap = checked_capacity(workspace_bytes / (int64_t(2) * kRows * (c.head_dim + 2) * 4), r.flags);
+  a.status = status;
+  const bool h = r.dtype == MOE_DTYPE_F16;
+  if (c.head_dim == 64) return h ? launch<F16, 64>(a, num_sms, st) : launch<Bf16, 64>(a, num_sms, st);
+  return h ? launch<F16, 128>(a, num_sms, st) : launch<Bf16, 128>(a, num_sms, st);
+}
+
+}  // namespace moe

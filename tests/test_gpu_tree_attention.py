@@ -39,6 +39,8 @@ TREES = [
     ([(256, 400), (3, 90)], 5, 1, 128, 32, "bf16", 256),                      # 1280 rows of a kv head
     ([(100, 2100)], 1, 1, 128, 1024, "bf16", 100),
     ([(48, 257), (5, 640)], 24, 8, 128, 64, "bf16", 48),
+    ([(61, 6000), (5, 7000), (40, 2500), (13, 5001)], 16, 2, 64, 16, "fp16", 61),  # long runs of key tiles
+    ([(61, 6000), (5, 7000), (40, 2500), (13, 5001)], 8, 2, 128, 16, "bf16", 61),
 ]
 
 
