@@ -18,12 +18,13 @@
 // Layout. A block has two streams of 128 rows (MMA M, TMEM lanes), whose softmax runs in turn with the other's MMAs:
 //   wide items (more than 128 rows of a kv head): two row tiles over the same key tiles;
 //   narrow ones: the same rows over alternate key tiles, joined at the item's end through shared memory.
-//   warps 0-3   softmax of stream 0, a row a thread; warps 4-7 of stream 1; they also make the queries' tiles
+//   warps 0-3   softmax of stream 0, a row a thread; warps 4-7 of stream 1; they also make the queries' tiles, and
+//               one lane of each four issues the stream's MMAs: S = Q K^T, then O += P V with P from TMEM, where the softmax wrote
+//               it over S (the stream has to wait for them anyway; a warp for them alone cost everyone 40 registers)
 //   warps 8-11  codes and scales of 128 keys at a time: cp.async two tiles ahead into places of each thread's own,
 //               conversion into K and V tiles (K-major and N-major, 128-byte swizzle) of a ring
-//   warp 12     MMA issuer: S = Q K^T, then O += P V with P from TMEM, where the softmax wrote it over S
-// Step q is stream q mod 2; S of step q + 2 is issued behind P V of step q, so the S of a step that is complete also
-// says that the stream's accumulators are.
+// A stream's next S is issued behind P V of its step, by the same lane, so the S of a step that is complete also says that
+// the stream's accumulators are.
 //
 // Schedule. As in attend_paged.cu: the items' key tiles in units, equal contiguous shares for one block on each SM, parts of
 // items that several blocks share in a workspace, joined in a fixed order by a second kernel. Every warp finds
@@ -43,11 +44,11 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a stream
 constexpr int kKeys = 128;     // keys of a tile
-constexpr int kThreads = 512;  // four warpgroups
-// Registers: 128 a thread at launch. 2 x 176 + 96 + 64 = 4 x 128.
-constexpr int kRegsLaunch = 128, kRegsSoftmax = 176, kRegsDecode = 96, kRegsMma = 64;
-static_assert(2 * kRegsSoftmax + kRegsDecode + kRegsMma <= 4 * kRegsLaunch, "register split");
-constexpr int kWarpDecode = 8, kWarpMma = 12;
+constexpr int kThreads = 384;  // three warpgroups
+// Registers: 168 a thread at launch. 2 x 208 + 88 = 3 x 168.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsDecode = 88;
+static_assert(2 * kRegsSoftmax + kRegsDecode <= 3 * kRegsLaunch, "register split");
+constexpr int kWarpDecode = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int64_t kWaitNs = 1000000000;
 constexpr float kLazy = 8.0f;       // the reference moves when the maximum is 2^kLazy beyond it
@@ -198,7 +199,6 @@ struct Segment {
   int first, count;  // tiles
   bool wide;         // two row tiles
 
-  __device__ __forceinline__ int steps() const { return wide ? 2 * count : count; }
 };
 
 // Cuts the next segment off a block's share; `left` units remain after it.
@@ -261,15 +261,15 @@ struct Smem {
   int2 exps[kExps][4];                         // by tile mod kExps and 32 keys: the largest scale codes of K and V
   uint8_t parent[kMaxTree];                    // place of the parent plus one
   int64_t total;
-  uint64_t q_full[2];      // the stream's queries are there (4 warps)
+  uint64_t q_full[2];      // the query tile is there (4 warps)
   uint64_t full[kStages];  // a K or V tile is there (4 warps)
-  uint64_t empty[kStages]; // the MMAs that read it are done
+  uint64_t empty[kStages]; // the MMAs that read it are done (2 commits: one of each stream, or two of one)
   uint64_t exps_full[kExps];  // a tile's largest scales are there (4 warps)
   uint64_t s_full[2];      // S of a step complete, and everything issued before it
   uint64_t p_full[2];      // P of a step written (4 warps)
-  uint64_t o_full[2];      // the stream's last P V is in O
+  uint64_t o_full[2];      // the stream's last P V is in O, and every MMA of the stream is done
   uint64_t met;            // the softmax warps among themselves (8 warps)
-  uint64_t mma_done;
+  uint64_t mma_done[2];    // the stream's MMAs are done, where it gave up
   uint32_t tmem_base;
 
   __device__ __forceinline__ uint8_t *exchange() { return D == 128 ? q[1] : join; }
@@ -335,6 +335,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
@@ -417,7 +425,7 @@ struct Decoder {
   const int32_t *table;
   uint32_t at;  // lane 2 j + u: cached row of granule u (16 keys) of the warp's keys in the j-th tile of the batch
   int looked;   // tiles of the segment that were looked up
-  uint32_t ks[kRaw][kPer], vs[kRaw][kPer];  // scale codes of the tiles on their way
+  uint32_t scales[kRaw][2][kPer] = {};  // scale codes of K and V of the tiles on their way, the next one first
 
   __device__ __forceinline__ Decoder(const TileArgs &args, S &smem) : a(args), sm(smem) {}
 
@@ -426,13 +434,24 @@ struct Decoder {
     looked = 0;
   }
 
-  __device__ __forceinline__ static void copy16(void *dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
-                 : "memory");
+  __device__ __forceinline__ static void copy16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
   }
 
-  // Codes and scales of tile i of the segment on their way; R = i mod kRaw.
-  template <int R>
+  // A scale code, or 0. In assembly, so that no selection behind the load waits for it here.
+  __device__ __forceinline__ static uint32_t load_scale(const uint8_t *p, bool some) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %2, 0;\n\t"
+        "mov.u32 %0, 0;\n\t"
+        "@p ld.global.nc.u8 %0, [%1];\n\t}"
+        : "=r"(r)
+        : "l"(p), "r"(uint32_t(some)));
+    return r;
+  }
+
+  // Codes and scales of tile i of the segment on their way, as the last of kRaw.
   __device__ __forceinline__ void fetch(const Segment &seg, int i) {
     if (i < seg.count) {
       const int j = i - looked;
@@ -450,19 +469,30 @@ struct Decoder {
           if (at != kNoRow && !index_ok(a.status, int64_t(at) + 15, a.cached_rows)) at = kNoRow;
         }
       }
-      const int from = 2 * (i - looked);
-      const uint32_t r0 = __shfl_sync(0xFFFFFFFFu, at, from), r1 = __shfl_sync(0xFFFFFFFFu, at, from + 1);
-      uint8_t *const to = sm.raw[R][0] + (threadIdx.x & 127) * 16;
+      const int from = 2 * (i - looked), rest = seg.s.len - (seg.first + i) * kKeys - warp * 32;  // of the warp's 32 keys
+      uint32_t r[2] = {__shfl_sync(0xFFFFFFFFu, at, from), __shfl_sync(0xFFFFFFFFu, at, from + 1)};
+      int end[2];  // keys that are there
 #pragma unroll
-      for (int p = 0; p < kPer; ++p) {
-        const int key = p * kSpan + in;  // of the warp's 32
-        const uint32_t r = p * kSpan < 16 ? r0 : r1;
-        const bool some = r != kNoRow && (seg.first + i) * kKeys + warp * 32 + key < seg.s.len;
-        const uint64_t row = some ? uint64_t(r) + (key & 15) : 0;
-        copy16(to + p * 2048, a.k_codes + row * (D / 2) + group * 16, some ? 16 : 0);
-        copy16(to + p * 2048 + S::kRawBytes, a.v_codes + row * (D / 2) + group * 16, some ? 16 : 0);
-        ks[R][p] = some ? __ldg(a.k_scales + row * kGroups + group) : 0;
-        vs[R][p] = some ? __ldg(a.v_scales + row * kGroups + group) : 0;
+      for (int u = 0; u < 2; ++u) {
+        end[u] = r[u] == kNoRow ? 0 : rest;
+        if (r[u] == kNoRow) r[u] = 0;
+      }
+      const uint32_t to = smem_u32(sm.raw[i % kRaw][0]) + (threadIdx.x & 127) * 16;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint64_t codes = uint64_t(r[u]) * (D / 2) + (in * (D / 2) + group * 16);
+        const uint64_t codes_of = uint64_t(r[u]) * kGroups + (in * kGroups + group);
+        const uint8_t *const kc = a.k_codes + codes, *const vc = a.v_codes + codes;
+        const uint8_t *const kq = a.k_scales + codes_of, *const vq = a.v_scales + codes_of;
+#pragma unroll
+        for (int h = 0; h < kPer / 2; ++h) {
+          const int p = u * (kPer / 2) + h;
+          const bool some = p * kSpan + in < end[u];
+          copy16(to + p * 2048, kc + h * (kSpan * D / 2), some ? 16 : 0);
+          copy16(to + p * 2048 + S::kRawBytes, vc + h * (kSpan * D / 2), some ? 16 : 0);
+          scales[kRaw - 1][0][p] = load_scale(kq + h * (kSpan * kGroups), some);
+          scales[kRaw - 1][1][p] = load_scale(vq + h * (kSpan * kGroups), some);
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -477,9 +507,12 @@ struct Decoder {
 
   // This thread's codes of a tile as f16 into their places.
   __device__ __forceinline__ void convert(uint8_t *tile, const uint8_t *raw, const uint32_t (&s)[kPer], int top) const {
+    uint4 codes[kPer];
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) codes[p] = *reinterpret_cast<const uint4 *>(raw + (threadIdx.x & 127) * 16 + p * 2048);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const uint4 c = *reinterpret_cast<const uint4 *>(raw + (threadIdx.x & 127) * 16 + p * 2048);
+      const uint4 c = codes[p];
       const float f = s[p] == 255 ? INFINITY : __int_as_float(max(int(s[p]) - top + kBias, 0) << 23);
       const uint32_t f2 = F16::pack(f, f);
       const int key = warp * 32 + p * kSpan + in;
@@ -504,42 +537,51 @@ struct Decoder {
     return e < S::kStages || __all_sync(0xFFFFFFFFu, wait(&sm.empty[e % S::kStages], (e / S::kStages & 1) ^ 1, a.status));
   }
 
-  // Tile i of the segment, tile number t of the block.
-  template <int R>
-  __device__ __forceinline__ bool tile(const Segment &seg, int i, uint32_t t) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-    const int ktop = largest(ks[R]), vtop = largest(vs[R]);
-    if (lane == 0) {
-      sm.exps[t % S::kExps][warp] = make_int2(ktop, vtop);
-      mbar_arrive(&sm.exps_full[t % S::kExps]);
-    }
-    const uint32_t e = 2 * t, k = e % S::kStages, v = (e + 1) % S::kStages;
-    if (!ready(e)) return false;
-    convert(sm.kv[k], sm.raw[R][0], ks[R], ktop);
-    filled(&sm.full[k]);
-    if (!ready(e + 1)) return false;
-    convert(sm.kv[v], sm.raw[R][1], vs[R], vtop);
-    filled(&sm.full[v]);
-    fetch<R>(seg, i + kRaw);
-    return true;
+  __device__ __forceinline__ void next_scales() {
+#pragma unroll
+    for (int j = 0; j + 1 < kRaw; ++j)
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) scales[j][v][p] = scales[j + 1][v][p];
   }
 
+  // t: tiles of the block in front of the segment's. One copy of the code for K and V and for every tile: see the softmax.
   __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t) {
     start(seg);
-    static_assert(kRaw == 2, "two places in turn");
-    fetch<0>(seg, 0);
-    fetch<1>(seg, 1);
-    bool ok = true;
-    for (int i = 0; ok && i < seg.count; i += 2) {
-      ok = tile<0>(seg, i, t + i);
-      if (ok && i + 1 < seg.count) ok = tile<1>(seg, i + 1, t + i + 1);
+#pragma unroll 1
+    for (int i = -kRaw; i < seg.count; ++i) {
+      if (i >= 0) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
+        const int tops[2] = {largest(scales[0][0]), largest(scales[0][1])};
+        const uint32_t n = t + i;
+        if (lane == 0) {
+          sm.exps[n % S::kExps][warp] = make_int2(tops[0], tops[1]);
+          mbar_arrive(&sm.exps_full[n % S::kExps]);
+        }
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t e = 2 * n + v, slot = e % S::kStages;
+          if (!ready(e)) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            return false;
+          }
+          uint32_t mine[kPer];
+#pragma unroll
+          for (int p = 0; p < kPer; ++p) mine[p] = v ? scales[0][1][p] : scales[0][0][p];
+          convert(sm.kv[slot], sm.raw[i % kRaw][v], mine, v ? tops[1] : tops[0]);
+          filled(&sm.full[slot]);
+        }
+      }
+      next_scales();
+      fetch(seg, i + kRaw);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    return ok;
+    return true;
   }
 };
 
-// ------------------------------------------------------------------ MMA issuer (one lane of warp 12)
+// ------------------------------------------------------------------ MMAs (one lane of a stream's first softmax warp)
 
 template <int D>
 struct Issuer {
@@ -549,25 +591,28 @@ struct Issuer {
   static constexpr uint32_t kDescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);  // B is N-major
   const TileArgs &a;
   S &sm;
+  const int x;
   const uint32_t tmem;
-  uint32_t queries[2] = {0, 0}, written[2] = {0, 0};  // phases of q_full and p_full
 
-  __device__ __forceinline__ Issuer(const TileArgs &args, S &smem, uint32_t t) : a(args), sm(smem), tmem(t) {}
+  __device__ __forceinline__ Issuer(const TileArgs &args, S &smem, int stream, uint32_t t)
+      : a(args), sm(smem), x(stream), tmem(t) {}
 
   __device__ __forceinline__ bool full(uint32_t e) const {
     return wait(&sm.full[e % S::kStages], e / S::kStages & 1, a.status);
   }
 
-  __device__ __forceinline__ bool scores(const Segment &seg, int q, uint32_t t) {
-    const int x = q & 1, tile = seg.wide ? q >> 1 : q;
-    const uint32_t e = 2 * (t + tile);
-    if ((q == 0 || (q == 1 && seg.wide))) {
-      if (!wait(&sm.q_full[x], queries[x] & 1, a.status)) return false;
-      ++queries[x];
-    }
-    if ((!seg.wide || x == 0) && !full(e)) return false;
+  // The ring's entry e is no longer needed by this stream when what was issued is done.
+  __device__ __forceinline__ void release(uint32_t e, bool wide) const {
+    mma_commit(&sm.empty[e % S::kStages]);
+    if (!wide) mma_commit(&sm.empty[e % S::kStages]);
+  }
+
+  // S of the block's tile t with query tile y.
+  __device__ __forceinline__ bool scores(int y, uint32_t t, bool wide) const {
+    const uint32_t e = 2 * t;
+    if (!full(e)) return false;
     tmem_fence_after();
-    const uint64_t qd = sw128_desc(smem_u32(sm.q[seg.wide ? x : 0])), kd = sw128_desc(smem_u32(sm.kv[e % S::kStages]));
+    const uint64_t qd = sw128_desc(smem_u32(sm.q[y])), kd = sw128_desc(smem_u32(sm.kv[e % S::kStages]));
     const uint32_t d = tmem + x * kKeys;
 #pragma unroll
     for (int p = 0; p < D / 64; ++p)
@@ -575,38 +620,21 @@ struct Issuer {
       for (int c = 0; c < 4; ++c)  // 16 values are 32 bytes: 2 in the address field
         mma_ss(d, qd + p * (kRows * 128 >> 4) + 2 * c, kd + p * (kKeys * 128 >> 4) + 2 * c, kDescS, (p | c) != 0);
     mma_commit(&sm.s_full[x]);
-    if (!seg.wide || x == 1) mma_commit(&sm.empty[e % S::kStages]);
+    release(e, wide);
     return true;
   }
 
-  __device__ __forceinline__ bool values(const Segment &seg, int q, uint32_t t) {
-    const int x = q & 1, tile = seg.wide ? q >> 1 : q;
-    const uint32_t e = 2 * (t + tile) + 1;
-    if ((!seg.wide || x == 0) && !full(e)) return false;
-    if (!wait(&sm.p_full[x], written[x] & 1, a.status)) return false;
-    ++written[x];
+  // O of the stream with P and V of tile t.
+  __device__ __forceinline__ bool values(uint32_t t, bool first, uint32_t parity, bool wide) const {
+    const uint32_t e = 2 * t + 1;
+    if (!full(e) || !wait(&sm.p_full[x], parity, a.status)) return false;
     tmem_fence_after();
     const uint64_t vd = v_desc(smem_u32(sm.kv[e % S::kStages]));
     const uint32_t pa = tmem + x * kKeys, d = tmem + S::kColO + x * D;
 #pragma unroll
     for (int c = 0; c < kKeys / 16; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
-      mma_ts(d, pa + 8 * c, vd + c * (2048 >> 4), kDescO, ((q >> 1) | c) != 0);
-    if (!seg.wide || x == 1) mma_commit(&sm.empty[e % S::kStages]);
-    return true;
-  }
-
-  __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t) {
-    const int steps = seg.steps();
-    for (int q = 0; q < 2 && q < steps; ++q)
-      if (!scores(seg, q, t)) return false;
-    for (int q = 0; q < steps; ++q) {
-      if (!values(seg, q, t)) return false;
-      if (q + 2 < steps) {
-        if (!scores(seg, q + 2, t)) return false;
-      } else {
-        mma_commit(&sm.o_full[q & 1]);
-      }
-    }
+      mma_ts(d, pa + 8 * c, vd + c * (2048 >> 4), kDescO, !first || c != 0);
+    release(e, wide);
     return true;
   }
 };
@@ -620,11 +648,22 @@ struct Softmax {
   S &sm;
   const int x = threadIdx.x >> 7, row = threadIdx.x & 127;
   const uint32_t lanes, ts, to;  // TMEM addresses of the warp's S and O
-  uint32_t scored = 0, ended = 0, meetings = 0;  // phases of s_full, o_full and met
+  const Issuer<D> issue;
+  const bool issues = (threadIdx.x & 127) < 32;
+  uint32_t scored = 0, ended = 0, meetings = 0, asked = 0;  // phases of s_full (and p_full), o_full, met; bit y: of q_full[y]
 
   __device__ __forceinline__ Softmax(const TileArgs &args, S &smem, uint32_t tmem)
       : a(args), sm(smem), lanes(uint32_t((threadIdx.x >> 5 & 3) * 32) << 16), ts(tmem + lanes + x * kKeys),
-        to(tmem + lanes + S::kColO + x * D) {}
+        to(tmem + lanes + S::kColO + x * D),
+        issue(args, smem, threadIdx.x >> 7, tmem) {}
+
+  // No MMA may be in flight when TMEM is freed.
+  __device__ __forceinline__ void give_up() const {
+    if (issues && elect_one()) {
+      mma_commit(&sm.mma_done[x]);
+      mbar_wait(&sm.mma_done[x], 0, kWaitNs);
+    }
+  }
 
   // All softmax warps have come here. A barrier with a limit: a warp that gave up elsewhere does not come.
   __device__ __forceinline__ bool meet() {
@@ -694,54 +733,19 @@ struct Softmax {
     }
   }
 
-  // The row's scores of a key tile, as far as it sees the keys.
-  __device__ __forceinline__ void load_scores(bool masked, const uint32_t (&see)[4], uint32_t (&s)[kKeys]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_wait_ld(s + 32 * i);
+  // 32 of the row's scores of a key tile, as far as it sees the keys.
+  __device__ __forceinline__ void load_scores(int c, bool masked, uint32_t see, uint32_t (&s)[32]) const {
+    tmem_ld32(ts + 32 * c, s);
+    tmem_wait_ld(s);
     if (masked) {
 #pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (!(see[i / 32] >> (i & 31) & 1)) s[i] = 0xFF800000u;  // -inf
+      for (int i = 0; i < 32; ++i)
+        if (!(see >> i & 1)) s[i] = 0xFF800000u;  // -inf
     }
   }
 
-  // The row's largest score, an exponent of two.
-  static __device__ __forceinline__ float largest(const uint32_t (&s)[kKeys], const float (&mul)[4]) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float m[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        m[0] = fmaxf(m[0], fmaxf(__uint_as_float(s[32 * c + i]), __uint_as_float(s[32 * c + i + 1])));
-        m[1] = fmaxf(m[1], fmaxf(__uint_as_float(s[32 * c + i + 2]), __uint_as_float(s[32 * c + i + 3])));
-      }
-      top = fmaxf(top, fmaxf(m[0], m[1]) * mul[c]);
-    }
-    return top;
-  }
-
-  // P = 2^(s mul + base) in f16, over the first half of s, and the sum of 2^(s mul + base - shift).
-  static __device__ __forceinline__ float exponentials(uint32_t (&s)[kKeys], const float (&mul)[4], float base,
-                                                       const int (&shift)[4]) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float b = base + float(shift[c]);
-      float add[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float u = exp2_approx(fmaf(__uint_as_float(s[32 * c + i]), mul[c], b));
-        const float v = exp2_approx(fmaf(__uint_as_float(s[32 * c + i + 1]), mul[c], b));
-        add[(i >> 1) & 1] += u + v;
-        s[16 * c + i / 2] = F16::pack(u, v);
-      }
-      sum = fmaf(add[0] + add[1], pow2(-shift[c]), sum);
-    }
-    return sum;
-  }
+  // Factor from the products with 32 keys to exponents of two; not 0: -inf must stay -inf.
+  __device__ __forceinline__ float factor(float unit, int code) const { return fmaxf(unit * pow2(code - kBias), 0x1p-126f); }
 
   __device__ __forceinline__ void scale_accumulators(float f) const {
 #pragma unroll 1
@@ -806,32 +810,47 @@ struct Softmax {
     }
     float ref = kLowest, total = 0.0f;
     int scale = 0;  // of the accumulators
-    const int steps = seg.steps();
-    for (int q = x; q < steps; q += 2) {
-      const int i = seg.wide ? q >> 1 : q, key0 = (seg.first + i) * kKeys;
+    // the stream's tiles of the segment: every one, or every second
+    const int start = seg.wide ? 0 : x, stride = seg.wide ? 1 : 2;
+    const int y = seg.wide ? x : 0;  // its query tile
+    if (start < seg.count && issues) {
+      bool ok = true;
+      if (elect_one()) ok = wait(&sm.q_full[y], asked >> y & 1, a.status) && issue.scores(y, t + start, seg.wide);
+      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+    }
+    asked ^= seg.wide ? 3 : 1;
+    for (int i = start; i < seg.count; i += stride) {
+      const int key0 = (seg.first + i) * kKeys;
+      const bool opening = i == start;
       const uint32_t n = t + i;
       if (!__all_sync(0xFFFFFFFFu, wait(&sm.exps_full[n % S::kExps], n / S::kExps & 1, a.status))) return false;
-      int shift[4], vtop = 0;
-      float mul[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int2 e = sm.exps[n % S::kExps][c];
-        mul[c] = fmaxf(unit * pow2(e.x - kBias), 0x1p-126f);  // not 0: -inf must stay -inf
-        shift[c] = e.y;
-        vtop = max(vtop, e.y);
-      }
+      const int2 *const exps = sm.exps[n % S::kExps];
+      const int vtop = max(max(exps[0].y, exps[1].y), max(exps[2].y, exps[3].y));
       const bool masked = key0 + kKeys > before;  // some key of the tile may be hidden
       uint32_t see[4] = {0, 0, 0, 0};
       if (masked) visible(token, key0 - before, real, see);
+      const auto seen = [&](int c) { return c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3]; };
       if (!__all_sync(0xFFFFFFFFu, wait(&sm.s_full[x], scored & 1, a.status))) return false;
-      ++scored;
       tmem_fence_after();
-      uint32_t s[kKeys];
-      load_scores(masked, see, s);
-      const float top = largest(s, mul);
-      if (q < 2) {
-        scale = vtop + kHeadroom;
+      // The loops over 32 keys stay loops: their code has to share the instruction cache with the decoders' (unrolled, and with
+      // the exponentials of most tiles in the pass that finds the maximum, the warps waited for instructions a third of the
+      // time: 16 trees of 64 rows 520 us).
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t s[32];
+        load_scores(c, masked, seen(c), s);
+        float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          m[0] = fmaxf(m[0], fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+          m[1] = fmaxf(m[1], fmaxf(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])));
+        }
+        top = fmaxf(top, fmaxf(m[0], m[1]) * factor(unit, exps[c].x));
+      }
+      if (opening) {
         ref = fmaxf(top, kLowest);
+        scale = vtop + kHeadroom;
       } else if (__any_sync(0xFFFFFFFFu, top - ref > kLazy) || vtop > scale) {
         // the accumulators hold every tile before this one (see the order of issue)
         float f = 1.0f;
@@ -846,17 +865,42 @@ struct Softmax {
         }
         scale_accumulators(f);
       }
+      // P = 2^(s - ref) in f16, with what the values' scales lie below the accumulators', and the sum without that
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t s[32], p[16];
+        load_scores(c, masked, seen(c), s);
+        const int shift = max(exps[c].y - scale, kLeast);
+        const float mul = factor(unit, exps[c].x), base = kUp - ref + float(shift);
+        float add[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) shift[c] = max(shift[c] - scale, kLeast);
-      total += exponentials(s, mul, kUp - ref, shift);
-      tmem_st32(ts, s);
-      tmem_st32(ts + 32, s + 32);
+        for (int j = 0; j < 32; j += 2) {
+          const float u = exp2_approx(fmaf(__uint_as_float(s[j]), mul, base));
+          const float v = exp2_approx(fmaf(__uint_as_float(s[j + 1]), mul, base));
+          add[(j >> 1) & 1] += u + v;
+          p[j / 2] = F16::pack(u, v);
+        }
+        total = fmaf(add[0] + add[1], pow2(-shift), total);
+        tmem_st16(ts + 16 * c, p);
+      }
       tmem_wait_st();
       tmem_fence_before();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.p_full[x]);
+      if (issues) {
+        bool ok = true;
+        if (elect_one()) {
+          ok = issue.values(t + i, opening, scored & 1, seg.wide);
+          if (i + stride < seg.count)
+            ok = ok && issue.scores(y, t + i + stride, seg.wide);
+          else
+            mma_commit(&sm.o_full[x]);
+        }
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+      }
+      ++scored;
     }
-    if (x < steps) {
+    if (start < seg.count) {
       if (!__all_sync(0xFFFFFFFFu, wait(&sm.o_full[x], ended & 1, a.status))) return false;
       ++ended;
       tmem_fence_after();
@@ -868,7 +912,7 @@ struct Softmax {
       if (!index_ok(a.status, slot, a.part_cap)) real = false;
       part = a.parts + int64_t(slot) * 2 * kRows * (D + 2);
     }
-    const bool both = !seg.wide && steps > 1;  // two streams of the same rows
+    const bool both = !seg.wide && seg.count > 1;  // two streams of the same rows
     float f = pow2_small(scale - kBias);
     if (both) {
       float2 *const rows = reinterpret_cast<float2 *>(sm.exchange());  // reference and sum, by stream
@@ -940,15 +984,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
   S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(tiles_smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   pdl_launch_dependents();
-  if (warp == kWarpMma) {
+  if (warp == kWarpDecode) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else if (warp == kWarpMma + 1 && elect_one()) {
+  } else if (warp == kWarpDecode + 1 && elect_one()) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sm.full[i], 4);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.empty[i], 2);
     }
     for (int i = 0; i < S::kExps; ++i) mbar_init(&sm.exps_full[i], 4);
     for (int x = 0; x < 2; ++x) {
@@ -956,9 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
       mbar_init(&sm.s_full[x], 1);
       mbar_init(&sm.p_full[x], 4);
       mbar_init(&sm.o_full[x], 1);
+      mbar_init(&sm.mma_done[x], 1);
     }
     mbar_init(&sm.met, 8);
-    mbar_init(&sm.mma_done, 1);
     fence_mbar_init();
   }
   if (blockIdx.x == 0)  // what is out of range is reported once
@@ -982,10 +1026,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
     for (int i = 0; left > 0; ++i) {
       const Segment seg = next_segment(a, place, left);
       if (seg.count == 0) continue;
-      if (!role.segment(seg, t, int(blockIdx.x) * 2 + (i ? 1 : 0))) break;
+      if (!role.segment(seg, t, int(blockIdx.x) * 2 + (i ? 1 : 0))) {
+        role.give_up();
+        break;
+      }
       t += seg.count;
     }
-  } else if (warp < kWarpMma) {
+  } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     Decoder<D> role(a, sm);
     while (left > 0) {
@@ -994,27 +1041,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
       if (!role.segment(seg, t)) break;
       t += seg.count;
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
-    if (warp == kWarpMma && elect_one()) {
-      Issuer<D> role(a, sm, tmem);
-      while (left > 0) {
-        const Segment seg = next_segment(a, place, left);
-        if (seg.count == 0) continue;
-        if (!role.segment(seg, t)) break;
-        t += seg.count;
-      }
-      if (end > begin) {
-        mma_commit(&sm.mma_done);  // every MMA is done before TMEM is freed
-        mbar_wait(&sm.mma_done, 0, kWaitNs);
-      }
-    }
   }
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == kWarpMma)
+  if (warp == kWarpDecode)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
