@@ -21,8 +21,8 @@
 //   warps 0-3   softmax of stream 0, a row a thread; warps 4-7 of stream 1; they also make the queries' tiles, and
 //               one lane of each four issues the stream's MMAs: S = Q K^T, then O += P V with P from TMEM, where the softmax wrote
 //               it over S (the stream has to wait for them anyway; a warp for them alone cost everyone 40 registers)
-//   warps 8-11  codes and scales of 128 keys at a time: cp.async two tiles ahead into places of each thread's own,
-//               conversion into K and V tiles (K-major and N-major, 128-byte swizzle) of a ring
+//   warps 8-11  keys, warps 12-15 values: codes and scales of 128 at a time, cp.async two tiles ahead into places of each thread's own,
+//               conversion into tiles (K-major and N-major, 128-byte swizzle) of a ring
 // A stream's next S is issued behind P V of its step, by the same lane, so the S of a step that is complete also says that
 // the stream's accumulators are.
 //
@@ -31,8 +31,6 @@
 // its block's share by itself, and goes from item to item without a queue.
 #include <cuda_runtime.h>
 #include <stdint.h>
-
-#include <atomic>
 
 #include "attention.cuh"
 #include "speculative.h"
@@ -44,10 +42,7 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a stream
 constexpr int kKeys = 128;     // keys of a tile
-constexpr int kThreads = 384;  // three warpgroups
-// Registers: 168 a thread at launch. 2 x 208 + 88 = 3 x 168.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsDecode = 88;
-static_assert(2 * kRegsSoftmax + kRegsDecode <= 3 * kRegsLaunch, "register split");
+constexpr int kThreads = 512;  // four warpgroups
 constexpr int kWarpDecode = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int64_t kWaitNs = 1000000000;
@@ -248,9 +243,11 @@ template <int D>
 struct Smem {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of Q, K or V in f16: D/64 parts of 128 rows x 128 bytes
-  // Largest scales are kept for as many tiles. Those of tile j + kStages are written behind V of tile j + kStages - 1, whose
-  // slot was free when P V of tile j + kStages / 2 - 1 was done, so the softmax has read those of tile j.
-  static constexpr int kExps = kStages;
+  // Largest scales are kept for 8 tiles. Those of K tile j + 8 are written when K of tile j + 7 is there, for which S of
+  // tile j + 7 - kStages / 2 >= j + 3 was done; that was issued behind P V of the tile before (or two before) in its stream, and so were
+  // those before it: the softmax has read those of tile j.
+  static constexpr int kExps = 8;
+  static_assert(kExps >= kStages / 2 + 4, "largest scales");
   static constexpr int kRawBytes = kKeys * D / 2;
   static constexpr uint32_t kColO = 2 * kKeys;
   static_assert(kColO + 2 * D <= kTmemCols, "TMEM budget");
@@ -258,13 +255,13 @@ struct Smem {
   uint8_t kv[kStages][kTileBytes];
   uint8_t raw[kRaw][2][kRawBytes];             // codes of K and V as each thread copied them
   uint8_t join[D == 128 ? 16 : kRows * 64 * 4];  // D = 128: the second stream's query tile serves
-  int2 exps[kExps][4];                         // by tile mod kExps and 32 keys: the largest scale codes of K and V
+  int exps[kExps][2][4];                       // by tile mod kExps: the largest scale codes of 32 keys each, and of their values
   uint8_t parent[kMaxTree];                    // place of the parent plus one
   int64_t total;
   uint64_t q_full[2];      // the query tile is there (4 warps)
   uint64_t full[kStages];  // a K or V tile is there (4 warps)
   uint64_t empty[kStages]; // the MMAs that read it are done (2 commits: one of each stream, or two of one)
-  uint64_t exps_full[kExps];  // a tile's largest scales are there (4 warps)
+  uint64_t exps_full[kExps];  // a tile's largest scales are there (8 warps)
   uint64_t s_full[2];      // S of a step complete, and everything issued before it
   uint64_t p_full[2];      // P of a step written (4 warps)
   uint64_t o_full[2];      // the stream's last P V is in O, and every MMA of the stream is done
@@ -409,7 +406,7 @@ __device__ __forceinline__ bool row_ok(const TileArgs &a, int row, int head) {
   return index_ok(a.status, row, a.num_rows) && index_ok(a.status, head, a.num_heads);
 }
 
-// ------------------------------------------------------------------ keys and values (warps 8-11)
+// ------------------------------------------------------------------ keys (warps 8-11) and values (warps 12-15)
 // A warp takes 32 keys of each tile, a lane one group of 32 dimensions of every 8th (D = 128) or 16th key: 16 bytes of codes.
 // Its lanes then store the 16-byte pieces of eight keys at a time, which the swizzle puts into different banks.
 
@@ -420,14 +417,16 @@ struct Decoder {
   static constexpr uint32_t kNoRow = 0xFFFFFFFFu;
   const TileArgs &a;
   S &sm;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpDecode;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, v = (threadIdx.x >> 7) & 1;  // v: values
+  const uint8_t *const codes, *const scales;
   const int group = lane / kSpan, in = lane % kSpan;
   const int32_t *table;
   uint32_t at;  // lane 2 j + u: cached row of granule u (16 keys) of the warp's keys in the j-th tile of the batch
   int looked;   // tiles of the segment that were looked up
-  uint32_t scales[kRaw][2][kPer] = {};  // scale codes of K and V of the tiles on their way, the next one first
+  uint32_t scale[kRaw][kPer] = {};  // scale codes of the tiles on their way, the next one first
 
-  __device__ __forceinline__ Decoder(const TileArgs &args, S &smem) : a(args), sm(smem) {}
+  __device__ __forceinline__ Decoder(const TileArgs &args, S &smem)
+      : a(args), sm(smem), codes(v ? a.v_codes : a.k_codes), scales(v ? a.v_scales : a.k_scales) {}
 
   __device__ __forceinline__ void start(const Segment &seg) {
     table = a.page_table + int64_t(seg.s.b) * a.max_pages;
@@ -477,21 +476,17 @@ struct Decoder {
         end[u] = r[u] == kNoRow ? 0 : rest;
         if (r[u] == kNoRow) r[u] = 0;
       }
-      const uint32_t to = smem_u32(sm.raw[i % kRaw][0]) + (threadIdx.x & 127) * 16;
+      const uint32_t to = smem_u32(sm.raw[i % kRaw][v]) + (threadIdx.x & 127) * 16;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint64_t codes = uint64_t(r[u]) * (D / 2) + (in * (D / 2) + group * 16);
-        const uint64_t codes_of = uint64_t(r[u]) * kGroups + (in * kGroups + group);
-        const uint8_t *const kc = a.k_codes + codes, *const vc = a.v_codes + codes;
-        const uint8_t *const kq = a.k_scales + codes_of, *const vq = a.v_scales + codes_of;
+        const uint8_t *const c = codes + (uint64_t(r[u]) * (D / 2) + (in * (D / 2) + group * 16));
+        const uint8_t *const q = scales + (uint64_t(r[u]) * kGroups + (in * kGroups + group));
 #pragma unroll
         for (int h = 0; h < kPer / 2; ++h) {
           const int p = u * (kPer / 2) + h;
           const bool some = p * kSpan + in < end[u];
-          copy16(to + p * 2048, kc + h * (kSpan * D / 2), some ? 16 : 0);
-          copy16(to + p * 2048 + S::kRawBytes, vc + h * (kSpan * D / 2), some ? 16 : 0);
-          scales[kRaw - 1][0][p] = load_scale(kq + h * (kSpan * kGroups), some);
-          scales[kRaw - 1][1][p] = load_scale(vq + h * (kSpan * kGroups), some);
+          copy16(to + p * 2048, c + h * (kSpan * D / 2), some ? 16 : 0);
+          scale[kRaw - 1][p] = load_scale(q + h * (kSpan * kGroups), some);
         }
       }
     }
@@ -527,53 +522,36 @@ struct Decoder {
     }
   }
 
-  __device__ __forceinline__ void filled(uint64_t *bar) const {
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-  }
-
   __device__ __forceinline__ bool ready(uint32_t e) const {  // the ring's entry e may be filled
     return e < S::kStages || __all_sync(0xFFFFFFFFu, wait(&sm.empty[e % S::kStages], (e / S::kStages & 1) ^ 1, a.status));
   }
 
-  __device__ __forceinline__ void next_scales() {
-#pragma unroll
-    for (int j = 0; j + 1 < kRaw; ++j)
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int p = 0; p < kPer; ++p) scales[j][v][p] = scales[j + 1][v][p];
-  }
-
-  // t: tiles of the block in front of the segment's. One copy of the code for K and V and for every tile: see the softmax.
+  // t: tiles of the block in front of the segment's. One copy of the code for K, V and every tile: see the softmax.
   __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t) {
     start(seg);
 #pragma unroll 1
     for (int i = -kRaw; i < seg.count; ++i) {
       if (i >= 0) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-        const int tops[2] = {largest(scales[0][0]), largest(scales[0][1])};
-        const uint32_t n = t + i;
+        const int top = largest(scale[0]);
+        const uint32_t n = t + i, e = 2 * n + v, slot = e % S::kStages;
         if (lane == 0) {
-          sm.exps[n % S::kExps][warp] = make_int2(tops[0], tops[1]);
+          sm.exps[n % S::kExps][v][warp] = top;
           mbar_arrive(&sm.exps_full[n % S::kExps]);
         }
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t e = 2 * n + v, slot = e % S::kStages;
-          if (!ready(e)) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            return false;
-          }
-          uint32_t mine[kPer];
-#pragma unroll
-          for (int p = 0; p < kPer; ++p) mine[p] = v ? scales[0][1][p] : scales[0][0][p];
-          convert(sm.kv[slot], sm.raw[i % kRaw][v], mine, v ? tops[1] : tops[0]);
-          filled(&sm.full[slot]);
+        if (!ready(e)) {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          return false;
         }
+        convert(sm.kv[slot], sm.raw[i % kRaw][v], scale[0], top);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.full[slot]);
       }
-      next_scales();
+#pragma unroll
+      for (int j = 0; j + 1 < kRaw; ++j)
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) scale[j][p] = scale[j + 1][p];
       fetch(seg, i + kRaw);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -674,31 +652,38 @@ struct Softmax {
 
   // The thread's query as f16 into the stream's tile; the factor from products with f16 keys to exponents of two.
   __device__ __forceinline__ float load_query(const Segment &seg, int token, int head, bool real, bool store) {
-    uint4 raw[D / 8];
     const uint4 *src = reinterpret_cast<const uint4 *>(a.q + int64_t(seg.s.row0 + token) * a.q_stride + int64_t(head) * D);
     float amax = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < D / 8; i += 8) {
+      uint4 raw[8];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) raw[i] = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 8; ++j) raw[j] = real ? __ldg(src + i + j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      uint4 &v = raw[i];
-      v.x ^= a.flip, v.y ^= a.flip, v.z ^= a.flip, v.w ^= a.flip;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) amax = fmaxf(amax, fmaxf(fabsf(T::lo(w[c])), fabsf(T::hi(w[c]))));
+        for (int c = 0; c < 4; ++c) amax = fmaxf(amax, fmaxf(fabsf(T::lo(w[c])), fabsf(T::hi(w[c]))));
+      }
     }
     // times 2^(14 - e): the largest lies in [2^14, 2^15), parts down to 2^-28 of it keep all their bits
     const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -100), 126);
     const float up = __uint_as_float(uint32_t(127 + 14 - e) << 23);
     if (store) {
+#pragma unroll 1
+      for (int i = 0; i < D / 8; i += 8) {  // once more, now near
+        uint4 raw[8];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t f[4];
+        for (int j = 0; j < 8; ++j) raw[j] = real ? __ldg(src + i + j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] = F16::pack(T::lo(w[c]) * up, T::hi(w[c]) * up);
-        *reinterpret_cast<uint4 *>(sm.q[seg.wide ? x : 0] + (i / 8) * (kRows * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
-            make_uint4(f[0], f[1], f[2], f[3]);
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t w[4] = {raw[j].x ^ a.flip, raw[j].y ^ a.flip, raw[j].z ^ a.flip, raw[j].w ^ a.flip};
+          uint32_t f[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) f[c] = F16::pack(T::lo(w[c]) * up, T::hi(w[c]) * up);
+          *reinterpret_cast<uint4 *>(sm.q[seg.wide ? x : 0] + (i / 8) * (kRows * 128) + row * 128 + ((j ^ (row & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+        }
       }
       fence_proxy_async();
       __syncwarp();
@@ -824,8 +809,8 @@ struct Softmax {
       const bool opening = i == start;
       const uint32_t n = t + i;
       if (!__all_sync(0xFFFFFFFFu, wait(&sm.exps_full[n % S::kExps], n / S::kExps & 1, a.status))) return false;
-      const int2 *const exps = sm.exps[n % S::kExps];
-      const int vtop = max(max(exps[0].y, exps[1].y), max(exps[2].y, exps[3].y));
+      const int(&exps)[2][4] = sm.exps[n % S::kExps];
+      const int vtop = max(max(exps[1][0], exps[1][1]), max(exps[1][2], exps[1][3]));
       const bool masked = key0 + kKeys > before;  // some key of the tile may be hidden
       uint32_t see[4] = {0, 0, 0, 0};
       if (masked) visible(token, key0 - before, real, see);
@@ -846,7 +831,7 @@ struct Softmax {
           m[0] = fmaxf(m[0], fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
           m[1] = fmaxf(m[1], fmaxf(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])));
         }
-        top = fmaxf(top, fmaxf(m[0], m[1]) * factor(unit, exps[c].x));
+        top = fmaxf(top, fmaxf(m[0], m[1]) * factor(unit, exps[0][c]));
       }
       if (opening) {
         ref = fmaxf(top, kLowest);
@@ -870,8 +855,8 @@ struct Softmax {
       for (int c = 0; c < 4; ++c) {
         uint32_t s[32], p[16];
         load_scores(c, masked, seen(c), s);
-        const int shift = max(exps[c].y - scale, kLeast);
-        const float mul = factor(unit, exps[c].x), base = kUp - ref + float(shift);
+        const int shift = max(exps[1][c] - scale, kLeast);
+        const float mul = factor(unit, exps[0][c]), base = kUp - ref + float(shift);
         float add[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
@@ -994,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
       mbar_init(&sm.full[i], 4);
       mbar_init(&sm.empty[i], 2);
     }
-    for (int i = 0; i < S::kExps; ++i) mbar_init(&sm.exps_full[i], 4);
+    for (int i = 0; i < S::kExps; ++i) mbar_init(&sm.exps_full[i], 8);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.q_full[x], 4);
       mbar_init(&sm.s_full[x], 1);
@@ -1021,7 +1006,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
   int64_t left = end - begin;
   uint32_t t = 0;  // tiles of the block so far
   if (warp < kWarpDecode) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     Softmax<T, D> role(a, sm, tmem);
     for (int i = 0; left > 0; ++i) {
       const Segment seg = next_segment(a, place, left);
@@ -1033,7 +1017,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
       t += seg.count;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     Decoder<D> role(a, sm);
     while (left > 0) {
       const Segment seg = next_segment(a, place, left);
@@ -1134,16 +1117,6 @@ int blocks_of(int num_sms) { return num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
 
 template <class T, int D>
 cudaError_t launch(const TileArgs &a, int num_sms, cudaStream_t st) {
-  // The register split assumes the launch's share: a build that gave the kernel less must not run. Only the answer is
-  // remembered, not a query that failed.
-  static std::atomic<int> regs{0};
-  if (!regs.load(std::memory_order_relaxed)) {
-    cudaFuncAttributes at;
-    const cudaError_t asked = cudaFuncGetAttributes(&at, tree_tiles_kernel<T, D>);
-    if (asked != cudaSuccess) return asked;
-    regs.store(at.numRegs, std::memory_order_relaxed);
-  }
-  if (regs.load(std::memory_order_relaxed) != kRegsLaunch) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(tree_tiles_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(Smem<D>::bytes()));
   if (e != cudaSuccess) return e;
