@@ -32,6 +32,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "attention.cuh"
 #include "speculative.h"
 #include "tcgen05.cuh"
@@ -43,6 +45,9 @@ namespace {
 constexpr int kRows = 128;     // rows of a stream
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kThreads = 512;  // four warpgroups
+// Registers: 128 a thread at launch; the softmax takes 24 more from the decoders.
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 152, kRegsDecode = 104;
+static_assert(2 * kRegsSoftmax + 2 * kRegsDecode <= 4 * kRegsLaunch, "register split");
 constexpr int kWarpDecode = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int64_t kWaitNs = 1000000000;
@@ -324,6 +329,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
       : "memory");
 }
 
+// The same, and the largest of the row's values (NaN aside).
+__device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t *r, float &top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(top)
+      : "r"(taddr)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -353,12 +371,39 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *r, float &top) {
+  tmem_wait_ld(r);
+  asm volatile("" : "+f"(top)::"memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two binary32 operations at a time.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity) {
@@ -651,14 +696,14 @@ struct Softmax {
   }
 
   // The thread's query as f16 into the stream's tile; the factor from products with f16 keys to exponents of two.
-  __device__ __forceinline__ float load_query(const Segment &seg, int token, int head, bool real, bool store) {
+  __device__ __forceinline__ float load_query(const Segment &seg, int token, int head, bool store) {
     const uint4 *src = reinterpret_cast<const uint4 *>(a.q + int64_t(seg.s.row0 + token) * a.q_stride + int64_t(head) * D);
     float amax = 0.0f;
 #pragma unroll 1
     for (int i = 0; i < D / 8; i += 8) {
       uint4 raw[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) raw[j] = real ? __ldg(src + i + j) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 8; ++j) raw[j] = __ldg(src + i + j);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
@@ -674,7 +719,7 @@ struct Softmax {
       for (int i = 0; i < D / 8; i += 8) {  // once more, now near
         uint4 raw[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) raw[j] = real ? __ldg(src + i + j) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 8; ++j) raw[j] = __ldg(src + i + j);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint32_t w[4] = {raw[j].x ^ a.flip, raw[j].y ^ a.flip, raw[j].z ^ a.flip, raw[j].w ^ a.flip};
@@ -693,16 +738,14 @@ struct Softmax {
   }
 
   // Which of 128 keys, the first `ahead` places behind the tree's first, the row of a token sees.
-  __device__ __forceinline__ void visible(int token, int ahead, bool real, uint32_t (&see)[4]) const {
+  __device__ __forceinline__ void visible(int token, int ahead, uint32_t (&see)[4]) const {
     uint32_t m[kMaxTree / 32];
 #pragma unroll
     for (int w = 0; w < kMaxTree / 32; ++w) m[w] = 0;
-    if (real) {
-      for (int j = token; j >= 0; j = int(sm.parent[j]) - 1) {
+    for (int j = token; j >= 0; j = int(sm.parent[j]) - 1) {
 #pragma unroll
-        for (int w = 0; w < kMaxTree / 32; ++w)
-          if (j >> 5 == w) m[w] |= 1u << (j & 31);
-      }
+      for (int w = 0; w < kMaxTree / 32; ++w)
+        if (j >> 5 == w) m[w] |= 1u << (j & 31);
     }
     const auto word = [&](int i) {  // bits 32 i .. of the tree, all set in front of it
       uint32_t r = i < 0 ? 0xFFFFFFFFu : 0u;
@@ -718,15 +761,32 @@ struct Softmax {
     }
   }
 
-  // 32 of the row's scores of a key tile, as far as it sees the keys.
-  __device__ __forceinline__ void load_scores(int c, bool masked, uint32_t see, uint32_t (&s)[32]) const {
-    tmem_ld32(ts + 32 * c, s);
-    tmem_wait_ld(s);
-    if (masked) {
+  // 32 of the row's scores as far as it sees the keys, and the largest of them.
+  static __device__ __forceinline__ float hide(uint32_t see, uint32_t (&s)[32]) {
+    float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (!(see >> i & 1)) s[i] = 0xFF800000u;  // -inf
+    for (int i = 0; i < 32; ++i) {
+      if (!(see >> i & 1)) s[i] = 0xFF800000u;  // -inf
+      top = fmaxf(top, __uint_as_float(s[i]));
     }
+    return top;
+  }
+
+  // P = 2^(s mul + base) of 32 scores in f16 into its place, and the sum.
+  __device__ __forceinline__ float exponentials(int c, const uint32_t (&s)[32], float mul, float base) const {
+    uint32_t p[16];
+    uint64_t add[2] = {0, 0};
+    const uint64_t m = pair(mul, mul), b = pair(base, base);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float2 e = unpair(fma_pair(pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), m, b));
+      const float u = exp2_approx(e.x), v = exp2_approx(e.y);
+      add[(j >> 1) & 1] = add_pair(add[(j >> 1) & 1], pair(u, v));
+      p[j / 2] = F16::pack(u, v);
+    }
+    tmem_st16(ts + 16 * c, p);
+    const float2 sum = unpair(add_pair(add[0], add[1]));
+    return sum.x + sum.y;
   }
 
   // Factor from the products with 32 keys to exponents of two; not 0: -inf must stay -inf.
@@ -753,13 +813,13 @@ struct Softmax {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f;
   }
 
-  // The row's result: 32 dimensions from `first` on, whole or as a part.
+  // The row's result: 32 dimensions from `first` on, whole or as a part (four dimensions of all rows, then the next four).
   __device__ __forceinline__ void store_out(const Segment &seg, float *part, int part_row, int token, int head, int first, float inv,
                                             const float (&v)[32]) const {
     if (part) {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        *reinterpret_cast<float4 *>(part + part_row * D + first + 4 * c) =
+        *reinterpret_cast<float4 *>(part + ((first / 4 + c) * (2 * kRows) + part_row) * 4) =
             make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
     } else {
       uint16_t *out = a.out + int64_t(seg.s.row0 + token) * a.out_stride + int64_t(head) * D + first;
@@ -775,11 +835,12 @@ struct Softmax {
   }
 
   __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t, int slot) {
-    const int r = seg.r0 + (seg.wide ? x * kRows : 0) + row;
+    // The thread's row; those behind the last compute what it does, and write nothing.
+    const int wanted = seg.r0 + (seg.wide ? x * kRows : 0) + row, r = min(wanted, seg.s.n * a.group - 1);
     const int token = r / a.group, head = seg.kv * a.group + r - token * a.group;
-    bool real = r < seg.s.n * a.group;
-    if (real) real = row_ok(a, seg.s.row0 + token, head);
-    const float unit = load_query(seg, token, head, real, seg.wide || x == 0);
+    bool real = r == wanted;
+    if (!row_ok(a, seg.s.row0 + token, head)) return false;
+    const float unit = load_query(seg, token, head, seg.wide || x == 0);
     const int before = seg.s.len - seg.s.n;  // keys in front of the tree
     if ((seg.first + seg.count) * kKeys > before) {
       const int i = threadIdx.x;
@@ -813,26 +874,24 @@ struct Softmax {
       const int vtop = max(max(exps[1][0], exps[1][1]), max(exps[1][2], exps[1][3]));
       const bool masked = key0 + kKeys > before;  // some key of the tile may be hidden
       uint32_t see[4] = {0, 0, 0, 0};
-      if (masked) visible(token, key0 - before, real, see);
-      const auto seen = [&](int c) { return c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3]; };
+      if (masked) visible(token, key0 - before, see);
       if (!__all_sync(0xFFFFFFFFu, wait(&sm.s_full[x], scored & 1, a.status))) return false;
       tmem_fence_after();
-      // The loops over 32 keys stay loops: their code has to share the instruction cache with the decoders' (unrolled, and with
-      // the exponentials of most tiles in the pass that finds the maximum, the warps waited for instructions a third of the
-      // time: 16 trees of 64 rows 520 us).
-      float top = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t s[32];
-        load_scores(c, masked, seen(c), s);
-        float m[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          m[0] = fmaxf(m[0], fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
-          m[1] = fmaxf(m[1], fmaxf(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])));
-        }
-        top = fmaxf(top, fmaxf(m[0], m[1]) * factor(unit, exps[0][c]));
-      }
+      // The row's largest score. Of the four times 32 the first two stay, in s1 and s0.
+      uint32_t s0[32], s1[32];
+      float t0, t1, top;
+      tmem_ld32_max(ts + 96, s1, t1);
+      tmem_ld32_max(ts + 64, s0, t0);
+      tmem_wait_ld(s1, t1);
+      tmem_wait_ld(s0, t0);
+      if (masked) t1 = hide(see[3], s1), t0 = hide(see[2], s0);
+      top = fmaxf(t1 * factor(unit, exps[0][3]), t0 * factor(unit, exps[0][2]));
+      tmem_ld32_max(ts + 32, s1, t1);
+      tmem_ld32_max(ts, s0, t0);
+      tmem_wait_ld(s1, t1);
+      tmem_wait_ld(s0, t0);
+      if (masked) t1 = hide(see[1], s1), t0 = hide(see[0], s0);
+      top = fmaxf(top, fmaxf(t1 * factor(unit, exps[0][1]), t0 * factor(unit, exps[0][0])));
       if (opening) {
         ref = fmaxf(top, kLowest);
         scale = vtop + kHeadroom;
@@ -850,23 +909,21 @@ struct Softmax {
         }
         scale_accumulators(f);
       }
-      // P = 2^(s - ref) in f16, with what the values' scales lie below the accumulators', and the sum without that
+      // P = 2^(s - ref) in f16, with what the values' scales lie below the accumulators', and the sum without that. A loop: its
+      // code has to share the instruction cache with the decoders' (with four times 32 exponentials one after another, twice, and four
+      // copies of the decoding the warps waited for instructions a third of the time: 16 trees of 64 rows 520 us).
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t s[32], p[16];
-        load_scores(c, masked, seen(c), s);
-        const int shift = max(exps[1][c] - scale, kLeast);
-        const float mul = factor(unit, exps[0][c]), base = kUp - ref + float(shift);
-        float add[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float u = exp2_approx(fmaf(__uint_as_float(s[j]), mul, base));
-          const float v = exp2_approx(fmaf(__uint_as_float(s[j + 1]), mul, base));
-          add[(j >> 1) & 1] += u + v;
-          p[j / 2] = F16::pack(u, v);
+      for (int c = 0; c < 4; c += 2) {
+        if (c) {
+          tmem_wait_ld(s0);
+          tmem_wait_ld(s1);
+          if (masked) hide(see[2], s0), hide(see[3], s1);
         }
-        total = fmaf(add[0] + add[1], pow2(-shift), total);
-        tmem_st16(ts + 16 * c, p);
+        const int d0 = max(exps[1][c] - scale, kLeast), d1 = max(exps[1][c + 1] - scale, kLeast);
+        total = fmaf(exponentials(c, s0, factor(unit, exps[0][c]), kUp - ref + float(d0)), pow2(-d0), total);
+        if (c == 0) tmem_ld32(ts + 64, s0);
+        total = fmaf(exponentials(c + 1, s1, factor(unit, exps[0][c + 1]), kUp - ref + float(d1)), pow2(-d1), total);
+        if (c == 0) tmem_ld32(ts + 96, s1);
       }
       tmem_wait_st();
       tmem_fence_before();
@@ -1006,6 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
   int64_t left = end - begin;
   uint32_t t = 0;  // tiles of the block so far
   if (warp < kWarpDecode) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     Softmax<T, D> role(a, sm, tmem);
     for (int i = 0; left > 0; ++i) {
       const Segment seg = next_segment(a, place, left);
@@ -1017,6 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
       t += seg.count;
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     Decoder<D> role(a, sm);
     while (left > 0) {
       const Segment seg = next_segment(a, place, left);
@@ -1036,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
 // ------------------------------------------------------------------ joining the blocks
 // Block c joins the item whose first tile is the main kernel's block c's, if later blocks have tiles of it too.
 
-constexpr int kJoinRows = 8, kJoinY = 8;  // rows at a time, blocks of an item
+constexpr int kJoinRows = 8;  // rows at a time
 
 template <class T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const TileArgs a) {
@@ -1068,7 +1127,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const TileArgs
   const int kv = p.item / p.s.blocks, r0 = (p.item - kv * p.s.blocks) * 2 * kRows;
   const int rows = min(2 * kRows, p.s.n * a.group - r0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int first = int(blockIdx.y) * kJoinRows; first < rows; first += kJoinY * kJoinRows) {
+  for (int first = int(blockIdx.y) * kJoinRows; first < rows; first += int(gridDim.y) * kJoinRows) {
     {
       const int head = 2 * kRows * D + first + warp;
       float m = kLowest, l = 0.0f;
@@ -1088,12 +1147,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const TileArgs
       }
     }
     __syncthreads();
-    const int row = threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4)), r = r0 + first + row;
-    if (row < kJoinRows && first + row < rows) {
+    const int row = threadIdx.x % kJoinRows, d = 4 * (threadIdx.x / kJoinRows), r = r0 + first + row;
+    if (d < D && first + row < rows) {
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
       for (int b = 0; b < parts; ++b) {
-        const float4 v = *reinterpret_cast<const float4 *>(part(b) + (first + row) * D + d);
+        const float4 v = *reinterpret_cast<const float4 *>(part(b) + d * (2 * kRows) + (first + row) * 4);
         const float w = weight[row][b];
         o.x = fmaf(v.x, w, o.x), o.y = fmaf(v.y, w, o.y), o.z = fmaf(v.z, w, o.z), o.w = fmaf(v.w, w, o.w);
       }
@@ -1116,7 +1175,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const TileArgs
 int blocks_of(int num_sms) { return num_sms < kMaxBlocks ? num_sms : kMaxBlocks; }
 
 template <class T, int D>
-cudaError_t launch(const TileArgs &a, int num_sms, cudaStream_t st) {
+cudaError_t launch(const TileArgs &a, int usual_rows, int num_sms, cudaStream_t st) {
+  // The register split assumes the launch's share: a build that gave the kernel less must not run. Only the answer is
+  // remembered, not a query that failed.
+  static std::atomic<int> regs{0};
+  if (!regs.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes at;
+    const cudaError_t asked = cudaFuncGetAttributes(&at, tree_tiles_kernel<T, D>);
+    if (asked != cudaSuccess) return asked;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kRegsLaunch) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(tree_tiles_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(Smem<D>::bytes()));
   if (e != cudaSuccess) return e;
@@ -1125,7 +1194,13 @@ cudaError_t launch(const TileArgs &a, int num_sms, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, kJoinY);
+  // Blocks of an item that is joined: about eight for each SM in all, of 8 rows at least. (Those without anything to join cost
+  // a little too: one tree of 16 rows 24.9 us with 8 of an item, 30.7 with 32; one of 64 rows 175 and 162; 24 ragged trees
+  // 83 with 4, 75 with 8, 82 with 32.)
+  const int64_t items = int64_t(a.num_seqs) * a.num_kv_heads * ((usual_rows + 2 * kRows - 1) / (2 * kRows));
+  const int64_t joined = items < grid ? items : grid, most = ((usual_rows < 2 * kRows ? usual_rows : 2 * kRows) + kJoinRows - 1) / kJoinRows;
+  const int64_t wanted = (8 * int64_t(grid) + joined - 1) / joined;
+  cfg.gridDim = dim3(grid, unsigned(wanted < most ? wanted : most));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1142,7 +1217,7 @@ int64_t tree_tiles_workspace(const moe_kv_cache_t &c, int num_sms) {
   return int64_t(blocks_of(num_sms)) * 2 * 2 * kRows * (c.head_dim + 2) * 4;
 }
 
-cudaError_t launch_tree_tiles(const moe_attend_tree_io_t &io, const moe_kv_cache_t &c, void *workspace,
+cudaError_t launch_tree_tiles(const moe_attend_tree_io_t &io, const moe_kv_cache_t &c, int usual_rows, void *workspace,
                               int64_t workspace_bytes, int32_t *status, int num_sms, cudaStream_t st) {
   const moe_attend_paged_io_t &r = io.rows;
   TileArgs a = {};
@@ -1174,8 +1249,8 @@ cudaError_t launch_tree_tiles(const moe_attend_tree_io_t &io, const moe_kv_cache
   a.part_cap = checked_capacity(workspace_bytes / (int64_t(2) * kRows * (c.head_dim + 2) * 4), r.flags);
   a.status = status;
   const bool h = r.dtype == MOE_DTYPE_F16;
-  if (c.head_dim == 64) return h ? launch<F16, 64>(a, num_sms, st) : launch<Bf16, 64>(a, num_sms, st);
-  return h ? launch<F16, 128>(a, num_sms, st) : launch<Bf16, 128>(a, num_sms, st);
+  if (c.head_dim == 64) return h ? launch<F16, 64>(a, usual_rows, num_sms, st) : launch<Bf16, 64>(a, usual_rows, num_sms, st);
+  return h ? launch<F16, 128>(a, usual_rows, num_sms, st) : launch<Bf16, 128>(a, usual_rows, num_sms, st);
 }
 
 }  // namespace moe
