@@ -37,8 +37,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kBatch = 4;  // units of a lane on their way at once
 constexpr int kUnit = 8;  // tokens that a lane takes at a time
 
 struct VerifyArgs {
@@ -113,6 +114,24 @@ __device__ __forceinline__ Two power(float d, Two c, const float2 *powers) {
   return {none ? 0.0f : hi * scale, none ? 0.0f : lo * scale};
 }
 
+// The same in one binary32: 2^-23 relative, from roundings without a common sign. (With y = d c.hi alone all weights
+// would be too large or too small together, by 2^-22; the series leaves 2^-28 off at its ends, 2^-31 on the whole.) Without the table: its
+// look-ups meet in the same banks.
+__device__ __forceinline__ float power_short(float d, Two c) {
+  constexpr float k1 = 0.693147182f, k2 = 0.240226507f, k3 = 0.0555041087f, k4 = 0.00961812911f, k5 = 0.00133335581f,
+                  k6 = 0.000154035304f, k7 = 1.52527338e-05f;  // ln 2^i / i!
+  const float y = __fmul_rn(d, c.hi), at = fmaxf(y, -150.0f) + 12582912.0f;
+  const float f = (y - (at - 12582912.0f)) + fmaf(d, c.lo, fmaf(d, c.hi, -y));
+  const float q = fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, k7, k6), k5), k4), k3), k2), k1);
+  const float w = fmaf(f, q, 1.0f);
+  const int n = __float_as_int(at) - 0x4B400000;
+  return n < -126 ? 0.0f : w * __int_as_float((n + 127) << 23);
+}
+
+// Weights of this part of the largest and more are computed in two binary32, the others in one. With 2^16 tokens, a fifth of
+// the whole below it, the running sums are then off by 2^-34 of the whole; with 2^-12 by 2^-33, with 2^-16 by 2^-35.
+constexpr float kShort = 0x1p-13f;
+
 // ------------------------------------------------------------------ rows of the vocabulary
 
 __device__ __forceinline__ float value(const float *p) { return __ldg(p); }
@@ -146,14 +165,27 @@ struct Row {
   __device__ __forceinline__ int units() const { return (vocab + shift + kUnit - 1) / kUnit; }
   __device__ __forceinline__ int first(int u) const { return u * kUnit - shift; }
 
+  // Units [a, b) lie in the row as a whole.
+  __device__ __forceinline__ bool whole(int a, int b) const { return first(a) >= 0 && first(b) <= vocab; }
+
+  // The logits of a unit that does.
+  static constexpr int kPer = 16 / sizeof(E), kPieces = kUnit / kPer;  // of a 16-byte piece; pieces
+  __device__ __forceinline__ void ask(int u, uint4 (&v)[kPieces]) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(p + first(u)) + i);
+  }
+  static __device__ __forceinline__ void take(const uint4 (&v)[kPieces], float (&x)[kUnit]) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) unpack(v[i], x + i * kPer, static_cast<const E *>(nullptr));
+  }
+
   // The unit's logits; -inf past the row's ends.
   __device__ __forceinline__ void load(int u, float (&x)[kUnit]) const {
     const int e = first(u);
-    if (e >= 0 && e + kUnit <= vocab) {
-      constexpr int kPer = 16 / sizeof(E);
-#pragma unroll
-      for (int i = 0; i < kUnit / kPer; ++i)
-        unpack(__ldg(reinterpret_cast<const uint4 *>(p + e) + i), x + i * kPer, static_cast<const E *>(nullptr));
+    if (whole(u, u + 1)) {
+      uint4 v[kPieces];
+      ask(u, v);
+      take(v, x);
     } else {
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) x[i] = e + i >= 0 && e + i < vocab ? value(p + e + i) : -INFINITY;
@@ -206,6 +238,8 @@ struct Smem {
   int parent[kMaxTree];    // kNever: not asked
   int rejected[kMaxTree];  // tokens of the rejected children of the row
   int way[kMaxTree];       // accepted rows, the root first
+  Two part[kWarps];        // sums of the warps where the new token is looked for, and what they found
+  int found[kWarps];
 };
 constexpr int kNever = -2;
 
@@ -255,10 +289,7 @@ struct Walker {
     part(row, begin, end);
     Peak k = {-INFINITY, 0.0f, INT32_MAX};
     const float c = unit.hi;
-#pragma unroll 4
-    for (int u = begin + lane; u < end; u += 32) {
-      float x[kUnit];
-      row.load(u, x);
+    const auto look = [&](int u, const float (&x)[kUnit]) {
       float t = x[0];
 #pragma unroll
       for (int i = 1; i < kUnit; ++i) t = fmaxf(t, x[i]);
@@ -272,6 +303,27 @@ struct Walker {
       const float ref = k.top == -INFINITY ? 0.0f : k.top;
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) k.sum += exp2_approx((x[i] - ref) * c);
+    };
+#pragma unroll 1
+    for (int u0 = begin; u0 < end; u0 += 32 * kBatch) {
+      if (u0 + 32 * kBatch <= end && row.whole(u0, u0 + 32 * kBatch)) {
+        uint4 v[kBatch][Row<E>::kPieces];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) row.ask(u0 + 32 * j + lane, v[j]);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          float x[kUnit];
+          row.take(v[j], x);
+          look(u0 + 32 * j + lane, x);
+        }
+      } else {
+#pragma unroll 1
+        for (int u = u0 + lane; u < min(end, u0 + 32 * kBatch); u += 32) {
+          float x[kUnit];
+          row.load(u, x);
+          look(u, x);
+        }
+      }
     }
 #pragma unroll
     for (int d = 16; d; d /= 2)
@@ -289,29 +341,61 @@ struct Walker {
     return k;
   }
 
-  // What is left of the unit's tokens: 2^((x - top) c) less taken q, or without the rejected tokens.
-  __device__ __forceinline__ void left(const Row<E> &row, const float *draft, int u, float top, Two taken, Two (&w)[kUnit]) const {
-    float x[kUnit], q[kUnit];
-    row.load(u, x);
-    const int e = row.first(u);
-    if (DRAFT && taken.hi != 0.0f) load_draft(draft, e, row.vocab, q);
+  // What is left of a weight 2^((x - top) c): less taken q, and nothing below 0.
+  __device__ __forceinline__ Two left_long(float x, float q, float top, Two taken) const {
+    Two w = power(x - top, unit, sm.powers);
+    if (DRAFT && taken.hi != 0.0f) {
+      const float g = __fmul_rn(taken.hi, q), gl = fmaf(taken.lo, q, fmaf(taken.hi, q, -g));
+      const float s = w.hi - g, b = s - w.hi;
+      const float lo = ((w.hi - (s - b)) - (g + b)) + (w.lo - gl), hi = s + lo;
+      w = hi > 0.0f ? Two{hi, lo - (hi - s)} : Two{0.0f, 0.0f};
+    }
+    return w;
+  }
+
+  // What is left of the 8 tokens of a unit, in one binary32 and 0 for those whose weight is large; these as a mask.
+  // e: the first of them.
+  __device__ __forceinline__ uint32_t left_short(int e, float top, Two taken, float (&x)[kUnit], const float (&q)[kUnit],
+                                                 float (&w)[kUnit]) const {
+    const bool drafted = DRAFT && taken.hi != 0.0f;
     if (!DRAFT) {
       for (int j = 0; j < count; ++j) {
         const int at = sm.rejected[j] - e;
+        if (uint32_t(at) >= kUnit) continue;
 #pragma unroll
         for (int i = 0; i < kUnit; ++i)
           if (at == i) x[i] = -INFINITY;
       }
     }
+    uint32_t large = 0;
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
-      w[i] = power(x[i] - top, unit, sm.powers);
-      if (DRAFT && taken.hi != 0.0f) {
-        const float g = __fmul_rn(taken.hi, q[i]), gl = fmaf(taken.lo, q[i], fmaf(taken.hi, q[i], -g));
-        const float s = w[i].hi - g, b = s - w[i].hi;
-        const float lo = ((w[i].hi - (s - b)) - (g + b)) + (w[i].lo - gl), hi = s + lo;
-        w[i] = hi > 0.0f ? Two{hi, lo - (hi - s)} : Two{0.0f, 0.0f};
+      w[i] = power_short(x[i] - top, unit);
+      const bool big = w[i] > kShort;
+      if (drafted) w[i] = fmaxf(fmaf(-taken.lo, q[i], fmaf(-taken.hi, q[i], w[i])), 0.0f);
+      if (big) {
+        w[i] = 0.0f;
+        large |= 1u << i;
       }
+    }
+    return large;
+  }
+
+  // f(i, what is left of token i) for the large ones of a unit. Whole warp; a lane's one after another.
+  template <class F>
+  __device__ __forceinline__ void each_large(uint32_t large, const float (&x)[kUnit], const float (&q)[kUnit], float top, Two taken,
+                                             F f) const {
+    while (__any_sync(0xFFFFFFFFu, large != 0)) {
+      const int i = large ? __ffs(large) - 1 : 0;
+      float xi = x[0], qi = q[0];
+#pragma unroll
+      for (int j = 1; j < kUnit; ++j) {
+        if (i == j) xi = x[j];
+        if (i == j) qi = q[j];
+      }
+      const Two w = left_long(xi, qi, top, taken);
+      if (large) f(i, w);
+      large &= large - 1;
     }
   }
 
@@ -320,11 +404,27 @@ struct Walker {
     int begin, end;
     part(row, begin, end);
     Two s = {0.0f, 0.0f};
-    for (int u = begin + lane; u < end; u += 32) {
-      Two w[kUnit];
-      left(row, draft, u, top, taken, w);
+    const bool drafted = DRAFT && taken.hi != 0.0f;
+    float x[kUnit], q[kUnit] = {}, nx[kUnit], nq[kUnit] = {};  // of this unit and the next
+    if (begin + lane < end) {
+      row.load(begin + lane, nx);
+      if (drafted) load_draft(draft, row.first(begin + lane), row.vocab, nq);
+    }
+#pragma unroll 1
+    for (int u0 = begin; u0 < end; u0 += 32) {
+      const int u = u0 + lane;
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) s = add(s, w[i].hi, w[i].lo);
+      for (int i = 0; i < kUnit; ++i) x[i] = nx[i], q[i] = nq[i];
+      if (u + 32 < end) {
+        row.load(u + 32, nx);
+        if (drafted) load_draft(draft, row.first(u + 32), row.vocab, nq);
+      }
+      float w[kUnit] = {};
+      uint32_t large = 0;
+      if (u < end) large = left_short(row.first(u), top, taken, x, q, w);
+      s = add(s, (w[0] + w[1]) + (w[2] + w[3]), 0.0f);
+      s = add(s, (w[4] + w[5]) + (w[6] + w[7]), 0.0f);
+      each_large(large, x, q, top, taken, [&](int, Two v) { s = add(s, v.hi, v.lo); });
     }
     s = add(s, Two{0.0f, 0.0f});
 #pragma unroll
@@ -356,7 +456,7 @@ struct Walker {
     return {__shfl_sync(0xFFFFFFFFu, s.hi, l), __shfl_sync(0xFFFFFFFFu, s.lo, l)};
   }
 
-  // The new token, on one lane of the warp whose part holds it; -1 elsewhere. `total`: whether there was anything to choose from.
+  // The new token, on one thread of the block that has it; -1 elsewhere. any: whether there was anything to choose from.
   __device__ int choose(const Row<E> &row, const float *draft, float top, Two taken, float u, bool &any) {
     const float4 *slots = sums(row, draft, top, taken);
     // running sums over the slots, consecutive ones a lane
@@ -381,55 +481,76 @@ struct Walker {
         run = next;
       }
     }
-    const int first = __reduce_min_sync(0xFFFFFFFFu, hit);
-    int owner = first;
-    if (first == INT32_MAX) {
+    int owner = __reduce_min_sync(0xFFFFFFFFu, hit);
+    if (owner == INT32_MAX) {
       owner = __reduce_max_sync(0xFFFFFFFFu, last);
       before = before_last;
     }
     before = from_lane(before, owner / per);
-    if (owner != int(rank) * kWarps + warp) return -1;
-    // this warp's part once more, 32 units at a time
-    int begin, end;
-    part(row, begin, end);
-    int found = -1, positive = -1;
-    for (int u0 = begin; u0 < end && found < 0; u0 += 32) {
-      Two w[kUnit], s = {0.0f, 0.0f};
-      const int unit_at = u0 + lane;
-      if (unit_at < end) {
-        left(row, draft, unit_at, top, taken, w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) w[i] = {0.0f, 0.0f};
+    if (owner / kWarps != int(rank)) return -1;  // the whole block
+    // the owner's part once more, by all warps: 32 units each, one a lane
+    const int units = row.units(), each = (units + n - 1) / n, begin = min(units, owner * each), end = min(units, begin + each);
+    int positive = -1;  // the last token with a weight
+    for (int u0 = begin; u0 < end; u0 += 32 * kWarps) {
+      const int at = u0 + 32 * warp + lane;
+      float x[kUnit], q[kUnit] = {}, v[kUnit] = {};
+      uint32_t large = 0;
+      if (at < end) {
+        row.load(at, x);
+        if (DRAFT && taken.hi != 0.0f) load_draft(draft, row.first(at), row.vocab, q);
+        large = left_short(row.first(at), top, taken, x, q, v);
       }
+      Two w[kUnit], s = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) w[i] = {v[i], 0.0f};
+      each_large(large, x, q, top, taken, [&](int k, Two l) {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i)
+          if (i == k) w[i] = l;
+      });
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) s = add(s, w[i].hi, w[i].lo);
       s = add(s, Two{0.0f, 0.0f});
       const Two to = scan(s, lane);
-      const unsigned over = __ballot_sync(0xFFFFFFFFu, s.hi > 0.0f && less(border, add(before, to)));
-      Two from = {__shfl_up_sync(0xFFFFFFFFu, to.hi, 1), __shfl_up_sync(0xFFFFFFFFu, to.lo, 1)};
-      from = lane ? add(before, from) : before;
-      int mine_found = -1;
+      __syncthreads();  // the last round's sums have been read
+      if (lane == 31) sm.part[warp] = to;
+      __syncthreads();
+      Two from = before;
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) from = add(from, sm.part[i]);
+        before = add(before, sm.part[i]);
+      }
+      const Two above = {__shfl_up_sync(0xFFFFFFFFu, to.hi, 1), __shfl_up_sync(0xFFFFFFFFu, to.lo, 1)};
+      if (lane) from = add(from, above);
+      // the first token of the lane's whose running sum exceeds the border, if the one in front of the lane does not
+      int found = INT32_MAX;
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
         if (w[i].hi > 0.0f) {
-          positive = row.first(unit_at) + i;
-          from = add(from, Two{w[i].hi, w[i].lo});
-          if (mine_found < 0 && less(border, from)) mine_found = positive;
+          positive = row.first(at) + i;
+          from = add(from, w[i]);
+          if (found == INT32_MAX && less(border, from)) found = positive;
         }
       }
-      if (mine_found < 0) mine_found = positive;
-      if (over) found = __shfl_sync(0xFFFFFFFFu, mine_found, __ffs(over) - 1);
-      before = add(before, from_lane(to, 31));
+      found = __reduce_min_sync(0xFFFFFFFFu, found);
+      if (lane == 0) sm.found[warp] = found;
+      __syncthreads();
+      found = INT32_MAX;
+      for (int i = 0; i < kWarps; ++i) found = min(found, sm.found[i]);
+      if (found != INT32_MAX) return threadIdx.x == 0 ? found : -1;
     }
-    if (found < 0) found = __reduce_max_sync(0xFFFFFFFFu, positive);
-    return lane == 0 ? found : -1;
+    positive = __reduce_max_sync(0xFFFFFFFFu, positive);
+    __syncthreads();
+    if (lane == 0) sm.found[warp] = positive;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) positive = max(positive, sm.found[i]);
+    return threadIdx.x == 0 ? positive : -1;
   }
 };
 
 // A block of a cluster of one sequence.
 template <class E, bool DRAFT>
-__global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ Smem sm;
   Walker<E, DRAFT> w(a, sm);
   const int tid = threadIdx.x, lane = w.lane, b = int(blockIdx.x / w.size);
@@ -576,6 +697,10 @@ cudaError_t launch(const VerifyArgs &a, int num_seqs, int cluster, cudaStream_t 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cluster > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(verify_drafts_kernel<E, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<E, DRAFT>, a);
 }
 
@@ -613,9 +738,9 @@ cudaError_t launch_verify_drafts(const moe_verify_drafts_io_t &io, int32_t *stat
   a.vocab = io.vocab;
   a.status = status;
   for (int i = 0; i < 32; ++i) a.powers[i] = powers.v[i];
-  // blocks of a sequence: as many as fill the GPU twice, of 4096 tokens at least
+  // blocks of a sequence: as many as are resident at once (four an SM), of 2048 tokens at least
   int cluster = 1;
-  while (cluster < kMaxCluster && int64_t(io.num_seqs) * cluster < 2 * num_sms && io.vocab / (2 * cluster) >= 4096) cluster *= 2;
+  while (cluster < kMaxCluster && int64_t(io.num_seqs) * 2 * cluster <= 4 * num_sms && io.vocab / (2 * cluster) >= 2048) cluster *= 2;
   const bool draft = io.draft_probs != nullptr;
   if (io.dtype == MOE_DTYPE_F32)
     return draft ? launch<float, true>(a, io.num_seqs, cluster, st) : launch<float, false>(a, io.num_seqs, cluster, st);
