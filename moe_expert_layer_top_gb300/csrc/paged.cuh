@@ -65,7 +65,7 @@ struct Cfg {
     uint2 q[NT][KS][32];       // query operand registers
     float mul[ROWS];           // score units to exponents of two
     int limit[ROWS];           // keys that a row sees; of a tree: the keys in front of it
-    uint32_t seen[TREE ? ROWS : 1][TREE ? kMaxTree / 32 : 1];  // by row: which rows of the tree are on its way to the root
+    uint32_t seen[TREE ? W : 1][TREE ? ROWS : 1][TREE ? kMaxTree / 32 : 1];  // by warp and row: the rows on its way to the root
     int16_t parent[TREE ? kMaxTree : 1];
     float ref[W][ROWS], sum[W][ROWS];
     int64_t before[kMaxSeqs / 32 + 1];  // units of each 32 sequences, then summed
@@ -503,7 +503,7 @@ __device__ __forceinline__ void granules(const typename C::Smem &sm, const uint8
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int key = key0 + 16 * u + 8 * v + g, j = key - before;
-            if (j >= 0 && (key >= len || !(sm.seen[row][j >> 5] >> (j & 31) & 1))) s[u][n][2 * v + e] = -INFINITY;
+            if (j >= 0 && (key >= len || !(sm.seen[threadIdx.x >> 5][row][j >> 5] >> (j & 31) & 1))) s[u][n][2 * v + e] = -INFINITY;
           }
       }
   } else if (masked) {  // hidden keys to -inf
@@ -643,28 +643,48 @@ __device__ __forceinline__ void store_lse(const PagedArgs &a, const Seq &s, int 
 
 // ------------------------------------------------------------------ trees
 // Which rows of the tree each row of the block sees: itself and those on its way
-// to the root. Whole block. A parent lies in front of its row; one that does not
-// is reported and counts as none, so every way ends.
+// to the root. A parent lies in front of its row; one that does not is reported
+// and counts as none, so every way ends. The parents come with the queries; each
+// warp traces the ways when it comes to keys of the tree (with a barrier for the
+// parents and another for the ways 64 trees of 6 rows took 96 us).
 template <class C>
-__device__ __forceinline__ void load_parents(const PagedArgs &a, typename C::Smem &sm, const Segment &seg) {
-  for (int i = threadIdx.x; i < seg.s.n; i += C::THREADS) {
-    int p = index_ok(a.status, seg.s.row0 + i, a.num_rows) ? __ldg(a.parents + seg.s.row0 + i) : -1;
-    if (p >= i) {
-      out_of_range(a.status);
-      p = -1;
-    }
-    sm.parent[i] = int16_t(p < 0 ? -1 : p);
-  }
-}
+struct Parents {
+  static constexpr int PER = C::TREE ? (kMaxTree + C::THREADS - 1) / C::THREADS : 1;
+  int p[PER];
 
+  __device__ __forceinline__ void load(const PagedArgs &a, const Segment &seg) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = threadIdx.x + k * C::THREADS;
+      p[k] = -1;
+      if (i < seg.s.n && index_ok(a.status, seg.s.row0 + i, a.num_rows)) p[k] = __ldg(a.parents + seg.s.row0 + i);
+    }
+  }
+
+  __device__ __forceinline__ void store(const PagedArgs &a, typename C::Smem &sm, const Segment &seg) const {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = threadIdx.x + k * C::THREADS;
+      if (i >= seg.s.n) continue;
+      if (p[k] >= i) out_of_range(a.status);
+      sm.parent[i] = int16_t(p[k] < 0 || p[k] >= i ? -1 : p[k]);
+    }
+  }
+};
+
+// The warp's copy.
 template <class C>
 __device__ __forceinline__ void trace_rows(const PagedArgs &a, typename C::Smem &sm, const Segment &seg) {
-  const int r = threadIdx.x, t = (seg.r0 + r) / a.group;
-  if (r >= C::ROWS) return;
+  const int r = threadIdx.x & 31, t = (seg.r0 + r) / a.group;
+  static_assert(!C::TREE || C::ROWS <= 32, "a lane for each row");
+  if (r < C::ROWS) {
+    uint32_t *const seen = sm.seen[threadIdx.x >> 5][r];
 #pragma unroll
-  for (int w = 0; w < kMaxTree / 32; ++w) sm.seen[r][w] = 0;
-  if (t < seg.s.n)
-    for (int j = t; j >= 0; j = sm.parent[j]) sm.seen[r][j >> 5] |= 1u << (j & 31);
+    for (int w = 0; w < kMaxTree / 32; ++w) seen[w] = 0;
+    if (t < seg.s.n)
+      for (int j = t; j >= 0; j = sm.parent[j]) seen[j >> 5] |= 1u << (j & 31);
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ main kernel
@@ -754,19 +774,16 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
     const Segment seg = next_segment<C>(a, place, left);
     if (seg.count == 0) continue;
     Queries<T, C> queries;
+    Parents<C> parents;
+    const bool tree = C::TREE && (seg.first + seg.count) * kStageKeys > seg.s.len - seg.s.n;  // it has keys of the tree
     queries.load(a, seg, warp);
+    if (tree) parents.load(a, seg);
     Copier<C> copier;
     copier.start(a, seg);
 #pragma unroll
     for (int c = 0; c < C::DEPTH - 1; ++c) copier.copy(a, seg, warp + c * C::W, sm.ring[warp][c]);
     queries.store(a, sm, seg, warp);
-    if constexpr (C::TREE) {
-      if ((seg.first + seg.count) * kStageKeys > seg.s.len - seg.s.n) {  // the same for the whole block
-        load_parents<C>(a, sm, seg);
-        __syncthreads();
-        trace_rows<C>(a, sm, seg);
-      }
-    }
+    if (tree) parents.store(a, sm, seg);
     __syncthreads();
     State<C> st;
 #pragma unroll
@@ -793,12 +810,17 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
     const int clear = C::TREE ? max(0, seg.s.len - seg.s.n)
                               : min(seg.s.len, max(0, seg.s.len - seg.s.n + 1 + seg.r0 / a.group));
     int slot = 0;
+    bool traced = false;
     for (int i = warp; i < seg.count; i += C::W) {
       copy_wait<C::DEPTH - 2>();
       __syncwarp();  // every lane's copies of this stage are there, and nobody reads the slot that is filled next
       copier.copy(a, seg, i + (C::DEPTH - 1) * C::W, sm.ring[warp][slot == 0 ? C::DEPTH - 1 : slot - 1]);
       const int key0 = (seg.first + i) * kStageKeys;
       const bool masked = key0 + kStageKeys > clear;
+      if (C::TREE && masked && !traced) {
+        trace_rows<C>(a, sm, seg);
+        traced = true;
+      }
 #pragma unroll 1
       for (int u = 0; u < 2; u += C::U)
         granules<C>(sm, sm.ring[warp][slot], st, qreg, u, key0, seg.s.len, masked);

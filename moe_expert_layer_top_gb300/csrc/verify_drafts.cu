@@ -114,23 +114,23 @@ __device__ __forceinline__ Two power(float d, Two c, const float2 *powers) {
   return {none ? 0.0f : hi * scale, none ? 0.0f : lo * scale};
 }
 
-// The same in one binary32: 2^-23 relative, from roundings without a common sign. (With y = d c.hi alone all weights
-// would be too large or too small together, by 2^-22; the series leaves 2^-28 off at its ends, 2^-31 on the whole.) Without the table: its
-// look-ups meet in the same banks.
+// The same in one binary32: 2^-23 relative, from roundings without a common sign (the series leaves 2^-28 off at its ends, 2^-31
+// on the whole). d >= -126 / c. With y = n - g: n from y's rounding, g exact but for one rounding. (Two at a time with the packed
+// instructions took more, for the constants, which those cannot take from the instruction.)
 __device__ __forceinline__ float power_short(float d, Two c) {
   constexpr float k1 = 0.693147182f, k2 = 0.240226507f, k3 = 0.0555041087f, k4 = 0.00961812911f, k5 = 0.00133335581f,
                   k6 = 0.000154035304f, k7 = 1.52527338e-05f;  // ln 2^i / i!
-  const float y = __fmul_rn(d, c.hi), at = fmaxf(y, -150.0f) + 12582912.0f;
-  const float f = (y - (at - 12582912.0f)) + fmaf(d, c.lo, fmaf(d, c.hi, -y));
+  const float at = fmaf(d, c.hi, 12582912.0f);  // 1.5 2^23 + n
+  const float f = fmaf(d, c.lo, fmaf(d, c.hi, 12582912.0f - at));
   const float q = fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, k7, k6), k5), k4), k3), k2), k1);
-  const float w = fmaf(f, q, 1.0f);
-  const int n = __float_as_int(at) - 0x4B400000;
-  return n < -126 ? 0.0f : w * __int_as_float((n + 127) << 23);
+  return fmaf(f, q, 1.0f) * __int_as_float((__float_as_int(at) << 23) + 0x3F800000);  // the low bits of `at` into the exponent
 }
 
 // Weights of this part of the largest and more are computed in two binary32, the others in one. With 2^16 tokens, a fifth of
 // the whole below it, the running sums are then off by 2^-34 of the whole; with 2^-12 by 2^-33, with 2^-16 by 2^-35.
 constexpr float kShort = 0x1p-13f;
+// Weights below 2^-126 of the largest are computed as that: what is less than kNothing is no weight, and no sum of them either.
+constexpr float kNothing = 0x1p-100f;
 
 // ------------------------------------------------------------------ rows of the vocabulary
 
@@ -150,6 +150,15 @@ __device__ __forceinline__ void unpack(uint4 v, float *x, const __half *) {
 }
 __device__ __forceinline__ void unpack(uint4 v, float *x, const float *) {
   x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+}
+
+// Values from p[e] on, `none` in front of the row and behind it. Out of line, as all that is rare or called in several places: a
+// call runs most of this code once, from a cold instruction cache (with everything inline the kernels had 125 and 180 KB;
+// one chain took 12.7 us).
+template <class E>
+__device__ __noinline__ void load_cut(const E *p, int e, int vocab, float none, float *x) {
+#pragma unroll 1
+  for (int i = 0; i < kUnit; ++i) x[i] = e + i >= 0 && e + i < vocab ? value(p + e + i) : none;
 }
 
 // A row in units of 8 tokens that begin on 16-byte boundaries: the first and the last may be cut by the row's ends.
@@ -187,8 +196,10 @@ struct Row {
       ask(u, v);
       take(v, x);
     } else {
+      float c[kUnit];
+      load_cut(p, e, vocab, -INFINITY, c);
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) x[i] = e + i >= 0 && e + i < vocab ? value(p + e + i) : -INFINITY;
+      for (int i = 0; i < kUnit; ++i) x[i] = c[i];
     }
   }
 };
@@ -199,8 +210,10 @@ __device__ __forceinline__ void load_draft(const float *p, int e, int vocab, flo
     const float4 a = __ldg(reinterpret_cast<const float4 *>(p + e)), b = __ldg(reinterpret_cast<const float4 *>(p + e) + 1);
     q[0] = a.x, q[1] = a.y, q[2] = a.z, q[3] = a.w, q[4] = b.x, q[5] = b.y, q[6] = b.z, q[7] = b.w;
   } else {
+    float c[kUnit];
+    load_cut(p, e, vocab, 0.0f, c);
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) q[i] = e + i >= 0 && e + i < vocab ? __ldg(p + e + i) : 0.0f;
+    for (int i = 0; i < kUnit; ++i) q[i] = c[i];
   }
 }
 
@@ -238,6 +251,7 @@ struct Smem {
   int parent[kMaxTree];    // kNever: not asked
   int rejected[kMaxTree];  // tokens of the rejected children of the row
   int way[kMaxTree];       // accepted rows, the root first
+  float2 large[kWarps][32 * kUnit + 32];  // logits (and draft probabilities) of large weights, until there are 32
   Two part[kWarps];        // sums of the warps where the new token is looked for, and what they found
   int found[kWarps];
 };
@@ -264,6 +278,7 @@ struct Walker {
   const uint32_t rank = cluster_rank(), size = cluster_size();
   int set = 0;
   Two unit = {0.0f, 0.0f};  // log2(e) / temperature
+  float least = 0.0f;       // -126 of it
   int count = 0;            // rejected tokens
 
   __device__ Walker(const VerifyArgs &args, Smem &smem) : a(args), sm(smem) {}
@@ -284,7 +299,9 @@ struct Walker {
     return slots;
   }
 
-  __device__ __forceinline__ Peak peak(const Row<E> &row) {
+  // behind: what else is to be done before all warps meet.
+  template <class F>
+  __device__ __forceinline__ Peak peak(const Row<E> &row, F behind) {
     int begin, end;
     part(row, begin, end);
     Peak k = {-INFINITY, 0.0f, INT32_MAX};
@@ -330,6 +347,7 @@ struct Walker {
       k.join({__shfl_xor_sync(0xFFFFFFFFu, k.top, d), __shfl_xor_sync(0xFFFFFFFFu, k.sum, d),
               __shfl_xor_sync(0xFFFFFFFFu, k.token, d)},
              c);
+    behind();
     const float4 *slots = exchange(make_float4(k.top, k.sum, __int_as_float(k.token), 0.0f));
     k = {-INFINITY, 0.0f, INT32_MAX};
     for (int i = lane; i < int(size) * kWarps; i += 32) k.join({slots[i].x, slots[i].y, __float_as_int(slots[i].z)}, c);
@@ -341,9 +359,8 @@ struct Walker {
     return k;
   }
 
-  // What is left of a weight 2^((x - top) c): less taken q, and nothing below 0.
-  __device__ __forceinline__ Two left_long(float x, float q, float top, Two taken) const {
-    Two w = power(x - top, unit, sm.powers);
+  // What is left of a weight less taken q: nothing below 0.
+  static __device__ __forceinline__ Two left_long(Two w, float q, Two taken) {
     if (DRAFT && taken.hi != 0.0f) {
       const float g = __fmul_rn(taken.hi, q), gl = fmaf(taken.lo, q, fmaf(taken.hi, q, -g));
       const float s = w.hi - g, b = s - w.hi;
@@ -353,32 +370,39 @@ struct Walker {
     return w;
   }
 
-  // What is left of the 8 tokens of a unit, in one binary32 and 0 for those whose weight is large; these as a mask.
-  // e: the first of them.
-  __device__ __forceinline__ uint32_t left_short(int e, float top, Two taken, float (&x)[kUnit], const float (&q)[kUnit],
-                                                 float (&w)[kUnit]) const {
-    const bool drafted = DRAFT && taken.hi != 0.0f;
-    if (!DRAFT) {
-      for (int j = 0; j < count; ++j) {
-        const int at = sm.rejected[j] - e;
-        if (uint32_t(at) >= kUnit) continue;
+  // The rejected tokens among the 8 from e on have no weight.
+  __device__ __forceinline__ void reject(int e, float (&x)[kUnit]) const {
+#pragma unroll 1
+    for (int j = 0; j < count; ++j) {
+      const int at = sm.rejected[j] - e;
+      if (uint32_t(at) >= kUnit) continue;
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i)
-          if (at == i) x[i] = -INFINITY;
-      }
+      for (int i = 0; i < kUnit; ++i)
+        if (at == i) x[i] = -INFINITY;
     }
-    uint32_t large = 0;
+  }
+
+  // The weights of 8 tokens in one binary32; the large ones as a mask, and 0 in their place. Whole warp.
+  __device__ __forceinline__ uint32_t weights_short(const float (&x)[kUnit], float top, float (&w)[kUnit]) const {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) {
-      w[i] = power_short(x[i] - top, unit);
-      const bool big = w[i] > kShort;
-      if (drafted) w[i] = fmaxf(fmaf(-taken.lo, q[i], fmaf(-taken.hi, q[i], w[i])), 0.0f);
-      if (big) {
-        w[i] = 0.0f;
-        large |= 1u << i;
-      }
+    for (int i = 0; i < kUnit; ++i) w[i] = power_short(fmaxf(x[i] - top, least), unit);
+    uint32_t large = 0;
+    const float most = fmaxf(fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])), fmaxf(fmaxf(w[4], w[5]), fmaxf(w[6], w[7])));
+    if (__any_sync(0xFFFFFFFFu, most > kShort)) {
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i)
+        if (w[i] > kShort) {
+          w[i] = 0.0f;
+          large |= 1u << i;
+        }
     }
     return large;
+  }
+
+  // What is left of them less taken q.
+  static __device__ __forceinline__ void less_draft(Two taken, const float (&q)[kUnit], float (&w)[kUnit]) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) w[i] = fmaxf(fmaf(-taken.lo, q[i], fmaf(-taken.hi, q[i], w[i])), 0.0f);
   }
 
   // f(i, what is left of token i) for the large ones of a unit. Whole warp; a lane's one after another.
@@ -393,44 +417,107 @@ struct Walker {
         if (i == j) xi = x[j];
         if (i == j) qi = q[j];
       }
-      const Two w = left_long(xi, qi, top, taken);
+      const Two w = left_long(power(xi - top, unit, sm.powers), qi, taken);
       if (large) f(i, w);
       large &= large - 1;
     }
   }
 
-  // The warps' sums of what is left, in their slots.
-  __device__ __forceinline__ const float4 *sums(const Row<E> &row, const float *draft, float top, Two taken) {
+  struct Sums {
+    const float4 *slots;  // of the warps, of what is left
+    Two all;              // of all weights
+  };
+
+  // Sums of what is left with c = taken / (sum of all weights), or, without a draft, of all tokens but the rejected ones.
+  // fresh (with a draft): c = 1, with a guess at the sum of all weights, which is computed in the same pass. The sums are
+  // corrected for what the guess was off by, d: what is left of w - guess q becomes less by d q, where it is positive (where it
+  // changes its sign, by d^2).
+  __device__ __forceinline__ Sums sums(const Row<E> &row, const float *draft, float top, Two taken, bool fresh) {
     int begin, end;
     part(row, begin, end);
-    Two s = {0.0f, 0.0f};
+    Two s = {0.0f, 0.0f}, all = {0.0f, 0.0f};
+    float share = 0.0f;  // the draft's probabilities where something is left
     const bool drafted = DRAFT && taken.hi != 0.0f;
-    float x[kUnit], q[kUnit] = {}, nx[kUnit], nq[kUnit] = {};  // of this unit and the next
-    if (begin + lane < end) {
-      row.load(begin + lane, nx);
-      if (drafted) load_draft(draft, row.first(begin + lane), row.vocab, nq);
-    }
+    int kept = 0;        // large weights that wait
+    const auto long_sum = [&](float2 l) {
+      const Two w = power(l.x - top, unit, sm.powers), r = left_long(w, l.y, taken);
+      s = add(s, r.hi, r.lo);
+      if (DRAFT && fresh) {
+        all = add(all, w.hi, w.lo);
+        if (r.hi > 0.0f) share += l.y;
+      }
+    };
+    float x[kUnit], q[kUnit] = {}, nq[kUnit] = {};  // of this unit, and the next
+    uint4 nx[Row<E>::kPieces];                      // logits of the next, as they come
+    const auto ask = [&](int u) {
+      if (u >= end) return;
+      if (row.whole(u, u + 1)) row.ask(u, nx);
+      if (drafted) load_draft(draft, row.first(u), row.vocab, nq);
+    };
+    const auto take = [&](int u) {
+      if (u >= end) {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) x[i] = -INFINITY;
+      } else if (row.whole(u, u + 1)) {
+        row.take(nx, x);
+      } else {
+        load_cut(row.p, row.first(u), row.vocab, -INFINITY, x);
+      }
+    };
+    ask(begin + lane);
 #pragma unroll 1
     for (int u0 = begin; u0 < end; u0 += 32) {
       const int u = u0 + lane;
+      take(u);
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) x[i] = nx[i], q[i] = nq[i];
-      if (u + 32 < end) {
-        row.load(u + 32, nx);
-        if (drafted) load_draft(draft, row.first(u + 32), row.vocab, nq);
+      for (int i = 0; i < kUnit; ++i) q[i] = nq[i];
+      ask(u + 32);
+      if (!DRAFT) reject(row.first(u), x);
+      float w[kUnit];
+      const uint32_t large = weights_short(x, top, w);
+      if (DRAFT && fresh) {
+        all = add(all, (w[0] + w[1]) + (w[2] + w[3]), 0.0f);
+        all = add(all, (w[4] + w[5]) + (w[6] + w[7]), 0.0f);
       }
-      float w[kUnit] = {};
-      uint32_t large = 0;
-      if (u < end) large = left_short(row.first(u), top, taken, x, q, w);
+      if (drafted) {
+        less_draft(taken, q, w);
+        if (fresh) {
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) share += w[i] > 0.0f ? q[i] : 0.0f;
+        }
+      }
       s = add(s, (w[0] + w[1]) + (w[2] + w[3]), 0.0f);
       s = add(s, (w[4] + w[5]) + (w[6] + w[7]), 0.0f);
-      each_large(large, x, q, top, taken, [&](int, Two v) { s = add(s, v.hi, v.lo); });
-    }
-    s = add(s, Two{0.0f, 0.0f});
+      if (__any_sync(0xFFFFFFFFu, large != 0)) {  // 32 of them at a time
+        const int mine = __popc(large);
+        int at = kept + warp_inclusive_sum(mine) - mine;
+        kept = __shfl_sync(0xFFFFFFFFu, at + mine, 31);
 #pragma unroll
-    for (int d = 16; d; d /= 2)
+        for (int i = 0; i < kUnit; ++i)
+          if (large >> i & 1) sm.large[warp][at++] = make_float2(x[i], q[i]);
+        __syncwarp();
+#pragma unroll 1
+        for (; kept >= 32; kept -= 32) long_sum(sm.large[warp][kept - 32 + lane]);
+        __syncwarp();
+      }
+    }
+    if (lane < kept) long_sum(sm.large[warp][lane]);
+    s = add(s, Two{0.0f, 0.0f});
+    all = add(all, Two{0.0f, 0.0f});
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
       s = add(s, Two{__shfl_xor_sync(0xFFFFFFFFu, s.hi, d), __shfl_xor_sync(0xFFFFFFFFu, s.lo, d)});
-    return exchange(make_float4(s.hi, s.lo, 0.0f, 0.0f));
+      if (DRAFT && fresh) {
+        all = add(all, Two{__shfl_xor_sync(0xFFFFFFFFu, all.hi, d), __shfl_xor_sync(0xFFFFFFFFu, all.lo, d)});
+        share += __shfl_xor_sync(0xFFFFFFFFu, share, d);
+      }
+    }
+    if (!DRAFT || !fresh) return {exchange(make_float4(s.hi, s.lo, 0.0f, 0.0f)), all};
+    all = whole(exchange(make_float4(all.hi, all.lo, 0.0f, 0.0f)));
+    const float off = (all.hi - taken.hi) + all.lo;
+    s = add(s, Two{-off * share, 0.0f});
+    if (s.hi < 0.0f) s = {0.0f, 0.0f};
+    return {exchange(make_float4(s.hi, s.lo, 0.0f, 0.0f)), all};
   }
 
   // Sum of all of them.
@@ -457,28 +544,38 @@ struct Walker {
   }
 
   // The new token, on one thread of the block that has it; -1 elsewhere. any: whether there was anything to choose from.
-  __device__ int choose(const Row<E> &row, const float *draft, float top, Two taken, float u, bool &any) {
-    const float4 *slots = sums(row, draft, top, taken);
+  // fresh: see sums().
+  __device__ int choose(const Row<E> &row, const float *draft, float top, Two taken, bool fresh, float u, bool &any) {
+    const Sums found_sums = sums(row, draft, top, taken, fresh);
+    const float4 *slots = found_sums.slots;
+    if (DRAFT && fresh) taken = found_sums.all;
     // running sums over the slots, consecutive ones a lane
+    constexpr int kPerLane = (kMaxCluster * kWarps + 31) / 32;
     const int n = int(size) * kWarps, per = (n + 31) / 32;
-    Two mine = {0.0f, 0.0f};
-    for (int i = lane * per; i < min(n, lane * per + per); ++i) mine = add(mine, Two{slots[i].x, slots[i].y});
-    const Two upto = scan(mine, lane), all = from_lane(upto, 31);
-    any = all.hi > 0.0f;
+    Two slot[kPerLane], upto[kPerLane];
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      const int i = lane * per + j;
+      const bool some = j < per && i < n;
+      slot[j] = {some ? slots[i].x : 0.0f, some ? slots[i].y : 0.0f};
+      upto[j] = j ? add(upto[j - 1], slot[j]) : slot[j];
+    }
+    const Two to_lane = scan(upto[kPerLane - 1], lane), all = from_lane(to_lane, 31);
+    any = all.hi > kNothing;
     if (!any) return -1;
     const Two border = times(all, fminf(fmaxf(u, 0.0f), 1.0f));
     // the first slot whose running sum exceeds the border; by a rounding, or with u = 1, there may be none: the last that has
     // a weight
-    Two run = {__shfl_up_sync(0xFFFFFFFFu, upto.hi, 1), __shfl_up_sync(0xFFFFFFFFu, upto.lo, 1)};
+    Two run = {__shfl_up_sync(0xFFFFFFFFu, to_lane.hi, 1), __shfl_up_sync(0xFFFFFFFFu, to_lane.lo, 1)};
     if (lane == 0) run = {0.0f, 0.0f};
     int hit = INT32_MAX, last = -1;
     Two before = run, before_last = run;
-    for (int i = lane * per; i < min(n, lane * per + per); ++i) {
-      if (slots[i].x > 0.0f) {
-        const Two next = add(run, Two{slots[i].x, slots[i].y});
-        if (hit == INT32_MAX && less(border, next)) hit = i, before = run;
-        last = i, before_last = run;
-        run = next;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      if (slot[j].hi > kNothing) {
+        const Two in_front = j ? add(run, upto[j - 1]) : run;
+        if (hit == INT32_MAX && less(border, add(run, upto[j]))) hit = lane * per + j, before = in_front;
+        last = lane * per + j, before_last = in_front;
       }
     }
     int owner = __reduce_min_sync(0xFFFFFFFFu, hit);
@@ -493,13 +590,17 @@ struct Walker {
     int positive = -1;  // the last token with a weight
     for (int u0 = begin; u0 < end; u0 += 32 * kWarps) {
       const int at = u0 + 32 * warp + lane;
-      float x[kUnit], q[kUnit] = {}, v[kUnit] = {};
-      uint32_t large = 0;
+      float x[kUnit], q[kUnit] = {}, v[kUnit];
       if (at < end) {
         row.load(at, x);
         if (DRAFT && taken.hi != 0.0f) load_draft(draft, row.first(at), row.vocab, q);
-        large = left_short(row.first(at), top, taken, x, q, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) x[i] = -INFINITY;
       }
+      if (!DRAFT) reject(row.first(at), x);
+      const uint32_t large = weights_short(x, top, v);
+      if (DRAFT && taken.hi != 0.0f) less_draft(taken, q, v);
       Two w[kUnit], s = {0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) w[i] = {v[i], 0.0f};
@@ -515,18 +616,17 @@ struct Walker {
       __syncthreads();  // the last round's sums have been read
       if (lane == 31) sm.part[warp] = to;
       __syncthreads();
-      Two from = before;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) from = add(from, sm.part[i]);
-        before = add(before, sm.part[i]);
-      }
+      Two parts = scan(lane < kWarps ? sm.part[lane] : Two{0.0f, 0.0f}, lane);
+      Two from = from_lane(parts, max(warp - 1, 0));
+      from = warp ? add(before, from) : before;
+      before = add(before, from_lane(parts, kWarps - 1));
       const Two above = {__shfl_up_sync(0xFFFFFFFFu, to.hi, 1), __shfl_up_sync(0xFFFFFFFFu, to.lo, 1)};
       if (lane) from = add(from, above);
       // the first token of the lane's whose running sum exceeds the border, if the one in front of the lane does not
       int found = INT32_MAX;
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
-        if (w[i].hi > 0.0f) {
+        if (w[i].hi > kNothing) {
           positive = row.first(at) + i;
           from = add(from, w[i]);
           if (found == INT32_MAX && less(border, from)) found = positive;
@@ -535,8 +635,7 @@ struct Walker {
       found = __reduce_min_sync(0xFFFFFFFFu, found);
       if (lane == 0) sm.found[warp] = found;
       __syncthreads();
-      found = INT32_MAX;
-      for (int i = 0; i < kWarps; ++i) found = min(found, sm.found[i]);
+      found = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? sm.found[lane] : INT32_MAX);
       if (found != INT32_MAX) return threadIdx.x == 0 ? found : -1;
     }
     positive = __reduce_max_sync(0xFFFFFFFFu, positive);
@@ -550,7 +649,7 @@ struct Walker {
 
 // A block of a cluster of one sequence.
 template <class E, bool DRAFT>
-__global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ Smem sm;
   Walker<E, DRAFT> w(a, sm);
   const int tid = threadIdx.x, lane = w.lane, b = int(blockIdx.x / w.size);
@@ -569,20 +668,23 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
     return;
   }
   const int n = rows.n;
-  for (int i = tid; i < n; i += kThreads) {
-    const int at = rows.first + i, token = __ldg(a.tokens + at);
-    int parent = a.parents ? __ldg(a.parents + at) : i - 1;
-    if (parent >= i) out_of_range(status);
+  // A row's logit and draft probability lie in its parent's row: they come while the root's row is read.
+  static_assert(kThreads >= kMaxTree, "a thread for each row");
+  float row_x = 0.0f, row_q = 1.0f;
+  if (tid < n) {
+    const int at = rows.first + tid, token = __ldg(a.tokens + at);
+    int parent = a.parents ? __ldg(a.parents + at) : tid - 1;
+    if (parent >= tid) out_of_range(status);
     const bool good = token >= 0 && token < a.vocab;
-    if (i > 0 && !good) out_of_range(status);
-    if (i == 0 || parent < 0 || parent >= i || !good) parent = kNever;
-    sm.parent[i] = parent;
-    sm.token[i] = token;
-    sm.u[i] = __ldg(a.accept_u + at);
+    if (tid > 0 && !good) out_of_range(status);
+    if (tid == 0 || parent < 0 || parent >= tid || !good) parent = kNever;
+    sm.parent[tid] = parent;
+    sm.token[tid] = token;
+    sm.u[tid] = __ldg(a.accept_u + at);
     if (parent >= 0) {
       const int64_t row = rows.first + parent;
-      sm.x[i] = value(static_cast<const E *>(a.logits) + row * a.logits_stride + token);
-      sm.q[i] = DRAFT ? __ldg(a.draft + row * a.draft_stride + token) : 1.0f;
+      row_x = value(static_cast<const E *>(a.logits) + row * a.logits_stride + token);
+      if (DRAFT) row_q = __ldg(a.draft + row * a.draft_stride + token);
     }
   }
   if (tid < 32) sm.powers[tid] = a.powers[tid];
@@ -594,22 +696,27 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
   }
   const bool greedy = t == 0.0f;
   w.unit = exponent_unit(greedy ? 1.0f : fmaxf(t, 0x1p-100f));
+  w.least = -126.0f / w.unit.hi;
   __syncthreads();
 
   int node = 0, accepted = 0;
   Peak k;
   Two taken;   // c times the sum of all weights
+  Two all;     // that sum, if it is known
   bool valid;  // there is a distribution
   while (true) {
     const Row<E> row(a.logits, a.logits_stride, rows.first + node, a.vocab);
     const float *draft = DRAFT ? a.draft + int64_t(rows.first + node) * a.draft_stride : nullptr;
-    k = w.peak(row);
+    k = w.peak(row, [&] {
+      if (node == 0 && tid < n) sm.x[tid] = row_x, sm.q[tid] = row_q;
+    });
     valid = k.sum > 0.0f && k.sum < INFINITY && k.top > -INFINITY;
     if (!valid) break;
     taken = {0.0f, 0.0f};
     w.count = 0;
     float mass = 1.0f;  // N
-    Two all = {0.0f, 0.0f}, rest = {0.0f, 0.0f};  // the sum of all weights, and N times it
+    all = {0.0f, 0.0f};
+    Two rest = {0.0f, 0.0f};  // N times the sum of all weights
     bool stale = false;  // N is to be computed
     int next = -1;
     for (int base = 0; base < n && next < 0; base += 32) {
@@ -625,7 +732,9 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
           yes = y == k.token;
         } else if constexpr (DRAFT) {
           if (stale) {
-            rest = w.whole(w.sums(row, draft, k.top, taken));
+            const auto sums = w.sums(row, draft, k.top, taken, all.hi == 0.0f);
+            rest = w.whole(sums.slots);
+            if (all.hi == 0.0f) all = taken = sums.all;
             mass = rest.hi / all.hi;
             stale = false;
           }
@@ -641,8 +750,8 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
         }
         if (greedy) continue;
         if constexpr (DRAFT) {
-          if (all.hi == 0.0f) all = rest = w.whole(w.sums(row, draft, k.top, taken));
-          taken = add(taken, rest);
+          // c becomes 1, for now with the sum that the walk has; then it grows by N
+          taken = taken.hi == 0.0f ? Two{k.sum, 0.0f} : add(taken, rest);
           stale = true;
         } else {
           mass = fmaxf(mass - p, 0.0f);
@@ -674,11 +783,13 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
   const Row<E> row(a.logits, a.logits_stride, rows.first + node, a.vocab);
   const float *draft = DRAFT ? a.draft + int64_t(rows.first + node) * a.draft_stride : nullptr;
   const float u = __ldg(a.sample_u + b);
-  bool any;
-  int token = w.choose(row, draft, k.top, taken, u, any);
-  if (!any) {  // nothing is left: the target's own probabilities
-    w.count = 0;
-    token = w.choose(row, draft, k.top, {0.0f, 0.0f}, u, any);
+  bool any = false;
+  int token = -1;
+#pragma unroll 1
+  for (int again = 0; again < 2 && !any; ++again) {
+    token = w.choose(row, draft, k.top, taken, DRAFT && taken.hi != 0.0f && all.hi == 0.0f, u, any);
+    w.count = 0;  // if nothing is left: the target's own probabilities
+    taken = {0.0f, 0.0f};
   }
   if (token >= 0) out[accepted] = token;
 }
@@ -738,9 +849,10 @@ cudaError_t launch_verify_drafts(const moe_verify_drafts_io_t &io, int32_t *stat
   a.vocab = io.vocab;
   a.status = status;
   for (int i = 0; i < 32; ++i) a.powers[i] = powers.v[i];
-  // blocks of a sequence: as many as are resident at once (four an SM), of 2048 tokens at least
+  // blocks of a sequence: of 2048 tokens at least, and no more in all than 2.6 an SM (64 sequences: 4 each; with 8, for which registers would
+  // have to be fewer, 71 us in place of 65; 24 sequences of 50,021 tokens: 16 each, 35 us, 40 with 8)
   int cluster = 1;
-  while (cluster < kMaxCluster && int64_t(io.num_seqs) * 2 * cluster <= 4 * num_sms && io.vocab / (2 * cluster) >= 2048) cluster *= 2;
+  while (cluster < kMaxCluster && int64_t(io.num_seqs) * 2 * cluster * 10 <= 26 * num_sms && io.vocab / (2 * cluster) >= 2048) cluster *= 2;
   const bool draft = io.draft_probs != nullptr;
   if (io.dtype == MOE_DTYPE_F32)
     return draft ? launch<float, true>(a, io.num_seqs, cluster, st) : launch<float, false>(a, io.num_seqs, cluster, st);
