@@ -506,7 +506,7 @@ PyObject *py_commit(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     std::vector<moe_kv_cache_t> caches(count);
     for (Py_ssize_t i = 0; i < count; ++i) {
       at::Device device(at::kCPU);
-      caches[i] = kv_cache(PySequence_Fast_GET_ITEM(arg[0], i), device, false);
+      caches[i] = kv_cache(PySequence_Fast_GET_ITEM(arg[0], i), device, true);
       if (device != kind.device) refuse("the caches must be on the device of lengths");
       for (Py_ssize_t j = 0; j < i; ++j)
         if (caches[j].k_codes == caches[i].k_codes && caches[i].num_pages) refuse("a cache must not be given twice");
@@ -527,10 +527,6 @@ PyObject *py_commit(PyObject *, PyObject *const *arg, Py_ssize_t n) {
       s = commit_drafts(&io, caches.data(), word, stream_of(kind));
     }
     if (s != MOE_OK) return PyLong_FromLong(s);
-    for (Py_ssize_t i = 0; i < count; ++i) {
-      at::Device device(at::kCPU);
-      kv_cache(PySequence_Fast_GET_ITEM(arg[0], i), device, true);  // they count as written
-    }
     return THPVariable_Wrap(out);
   });
 }

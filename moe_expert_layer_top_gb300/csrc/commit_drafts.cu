@@ -8,6 +8,11 @@
 // A path rises, so path[j] >= j: rows moved in turn never overwrite one that is
 // still to move. Rows are moved in batches in the order of the path, and within a batch every
 // byte is read before any is written.
+//
+// Two caches a block and four pieces a thread: one cache a block starts too many blocks (64 sequences x 32 caches, five
+// rows: 9.3 us against 7.4), four leave too few of them (the same 7.7; 32 sequences x 2 caches, D = 64: 4.2 against
+// 3.6), eight pieces a thread cost registers (10.3). One sequence with two caches takes 3.2 us, a launch and four loads
+// that wait for one another. Measured device times, calls in a graph.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -77,50 +82,51 @@ __global__ void __launch_bounds__(kThreads) commit_drafts_kernel(const __grid_co
     return;
   }
   if (blockIdx.y == 0 && tid == 0) a.new_lengths[b] = n ? base + 1 + accepted : length;
-  // every piece of the block: by row, then cache, kv head and piece
-  const int caches = (a.num_caches - int(blockIdx.y) + int(gridDim.y) - 1) / int(gridDim.y);
-  const int per_row = caches * a.num_kv_heads * kPieces;
-  const int all = accepted * per_row;  // at most 255 rows of 4 caches and 1024 heads
-  for (int batch = 0; batch < all; batch += kThreads * kHold) {
-    uint4 held[kHold];
-    uint8_t *dst[kHold];
+  // A move is a row in one cache; groups of threads take moves in turn, a thread one piece of one kv head of each.
+  const int caches = (a.num_caches - int(blockIdx.y) + int(gridDim.y) - 1) / int(gridDim.y), moves = accepted * caches;
+  const int pieces = a.num_kv_heads * kPieces, groups = max(1, kThreads / pieces);
+  const int group = pieces < kThreads ? tid / pieces : 0;
+  for (int part = 0; part < pieces; part += kThreads) {
+    const int mine = pieces < kThreads ? tid - group * pieces : part + tid;
+    const int kv = mine / kPieces, piece = mine - kv * kPieces;
+    const bool works = group < groups && mine < pieces;
+    for (int batch = 0; batch < moves; batch += groups * kHold) {
+      uint4 held[kHold];
+      uint8_t *dst[kHold];
 #pragma unroll
-    for (int h = 0; h < kHold; ++h) {
-      const int i = batch + h * kThreads + tid;
-      dst[h] = nullptr;
-      if (i >= all) continue;
-      const int j = 1 + i / per_row, r = i - (j - 1) * per_row;
-      const int c = r / (a.num_kv_heads * kPieces), rest = r - c * (a.num_kv_heads * kPieces);
-      const int kv = rest / kPieces, piece = rest - kv * kPieces;
-      if (to[j] == kNowhere) continue;
-      const int64_t at = int64_t(from[j]) + kv * a.page_size, into = int64_t(to[j]) + kv * a.page_size;
-      if (!index_ok(a.status, at, a.cached_rows) || !index_ok(a.status, into, a.cached_rows)) continue;
-      const Cache &cache = a.caches[blockIdx.y + c * gridDim.y];
-      if (piece < 2 * kCodes) {
-        uint8_t *const codes = cache.part[piece / kCodes] + (piece % kCodes) * 16;
-        held[h] = *reinterpret_cast<const uint4 *>(codes + at * (D / 2));
-        dst[h] = codes + into * (D / 2);
-      } else {
-        uint8_t *const scales = cache.part[piece - 2 * kCodes + 2];
-        held[h].x = D == 128 ? *reinterpret_cast<const uint32_t *>(scales + at * 4)
-                             : *reinterpret_cast<const uint16_t *>(scales + at * 2);
-        held[h].y = 0;
-        dst[h] = scales + into * (D / 32);
+      for (int h = 0; h < kHold; ++h) {
+        const int m = batch + h * groups + group;
+        dst[h] = nullptr;
+        if (!works || m >= moves) continue;
+        const int j = m / caches, c = m - j * caches;
+        if (to[j + 1] == kNowhere) continue;
+        const int64_t at = int64_t(from[j + 1]) + kv * a.page_size, into = int64_t(to[j + 1]) + kv * a.page_size;
+        if (!index_ok(a.status, at, a.cached_rows) || !index_ok(a.status, into, a.cached_rows)) continue;
+        const Cache &cache = a.caches[blockIdx.y + c * gridDim.y];
+        if (piece < 2 * kCodes) {
+          uint8_t *const codes = cache.part[piece / kCodes] + (piece % kCodes) * 16;
+          held[h] = *reinterpret_cast<const uint4 *>(codes + at * (D / 2));
+          dst[h] = codes + into * (D / 2);
+        } else {
+          uint8_t *const scales = cache.part[piece - 2 * kCodes + 2];
+          held[h].x = D == 128 ? *reinterpret_cast<const uint32_t *>(scales + at * 4)
+                               : *reinterpret_cast<const uint16_t *>(scales + at * 2);
+          dst[h] = scales + into * (D / 32);
+        }
       }
-    }
-    __syncthreads();
+      __syncthreads();
 #pragma unroll
-    for (int h = 0; h < kHold; ++h) {
-      if (!dst[h]) continue;
-      const int piece = (batch + h * kThreads + tid) % kPieces;
-      if (piece < 2 * kCodes)
-        *reinterpret_cast<uint4 *>(dst[h]) = held[h];
-      else if (D == 128)
-        *reinterpret_cast<uint32_t *>(dst[h]) = held[h].x;
-      else
-        *reinterpret_cast<uint16_t *>(dst[h]) = uint16_t(held[h].x);
+      for (int h = 0; h < kHold; ++h) {
+        if (!dst[h]) continue;
+        if (piece < 2 * kCodes)
+          *reinterpret_cast<uint4 *>(dst[h]) = held[h];
+        else if (D == 128)
+          *reinterpret_cast<uint32_t *>(dst[h]) = held[h].x;
+        else
+          *reinterpret_cast<uint16_t *>(dst[h]) = uint16_t(held[h].x);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -150,8 +156,8 @@ cudaError_t launch_commit_drafts(const moe_commit_drafts_io_t &io, const moe_kv_
       const moe_kv_cache_t &c = caches[first + i];
       a.caches[i] = {{c.k_codes, c.v_codes, c.k_scales, c.v_scales}};
     }
-    // four caches a block
-    const dim3 grid(unsigned(io.num_seqs), unsigned(a.num_caches + 3) / 4);
+    // two caches a block
+    const dim3 grid(unsigned(io.num_seqs), unsigned(a.num_caches + 1) / 2);
     if (c0.head_dim == 64)
       commit_drafts_kernel<64><<<grid, kThreads, 0, st>>>(a);
     else
