@@ -44,6 +44,17 @@ TREES = [
 ]
 
 
+# Rows of a kv head and (sequence, kv head) pairs on both sides of where the kernels change.
+BORDERS = [(tokens, group, seqs) for tokens, group in ((32, 1), (33, 1), (12, 4), (49, 1)) for seqs in (1, 16, 17)]
+
+
+@pytest.mark.parametrize("tokens, group, seqs", BORDERS, ids=[f"{t * g}rows_{n}seqs" for t, g, n in BORDERS])
+@pytest.mark.parametrize("D", [64, 128])
+def test_either_kind_of_kernel(tokens, group, seqs, D):
+    K = 2
+    run_tree([(tokens, 200 + 7 * b) for b in range(seqs)], K * group, K, D, 16, "bf16", tokens, seed=tokens + seqs)
+
+
 @pytest.mark.parametrize("case", TREES, ids=[f"{c[0][0][0]}x{c[0][0][1]}_H{c[1]}_D{c[3]}_p{c[4]}_{c[5]}" for c in TREES])
 @pytest.mark.parametrize("kind", ["tree", "chain", "forest"])
 def test_tree_matches_the_oracle(case, kind):
