@@ -108,7 +108,9 @@ typedef enum {
  * moe_forward on a plan without this flag is unaffected.
  * In moe_attend_prompt: the mark that a sequence's last, partial tile of values
  * is ready is never set. The products that wait for it give up, with the same
- * consequences. */
+ * consequences.
+ * In moe_attend_tree, where a kv head has many rows: a quarter of each key tile
+ * never comes, and what waits for it gives up likewise. */
 
 #define MOE_FLAG_TEST_BOUNDS (1u << 9)
 /* Test hook of the bounds-checked build (libmoe_debug.so, compiled with
@@ -583,9 +585,16 @@ moe_status_t moe_attend_tree_workspace(const moe_attend_tree_io_t *io, const moe
  * a sequence of length L sees the keys 0 .. L - n - 1, and key L - n + j for j = i
  * and every row j on its way to the root. Everything else is as for
  * moe_attend_paged, whose result this is when each row's parent is the row in
- * front of it (to the last bits: the sums have another order). A parent that does not lie in front of its row
- * is reported and counts as none. A sequence with more than MOE_MAX_TREE_ROWS rows is reported and gets no
- * result: its rows are not touched. */
+ * front of it (to the last bits: the sums have another order). A parent that
+ * does not lie in front of its row is reported and counts as none. A sequence
+ * with more than MOE_MAX_TREE_ROWS rows is reported and gets no result: its rows
+ * are not touched. A scale code of 255 counts as 2^128, as it does there. Where
+ * a kv head usually has many rows (max_rows, num_rows, num_seqs and the heads
+ * say so) the kernel's parts wait for one another, as those of
+ * moe_attend_prompt do: if such a wait does not end within a second,
+ * MOE_ERR_TIMEOUT is stored in *d_status, the kernel ends by itself, and the
+ * call's results are unspecified (the next call is not affected). rows.flags may
+ * also be MOE_FLAG_TEST_SKIP_READY. */
 moe_status_t moe_attend_tree(const moe_attend_tree_io_t *io, const moe_kv_cache_t *cache, void *workspace,
                              int64_t workspace_bytes, int32_t *d_status, void *cuda_stream);
 
@@ -631,12 +640,14 @@ typedef struct moe_verify_drafts_io {
  * sample_u times the whole (p itself, if nothing is left).
  * Only the rows on the way are read. Decisions are made in binary32 from sums
  * of relative error 2^-20; the sums that choose the new token have an error
- * below 2^-34 of the whole, so it is the formula's but for numbers that close to a border.
+ * of about 2^-34 of the whole, and below 2^-30 even where nearly all of it lies
+ * in tokens below 2^-13 of the largest, so it is the formula's but for numbers
+ * that close to a border. Weights below 2^-100 of the largest count as none.
  * The same call gives the same result. A row on the way whose logits hold a NaN
  * or +inf, or nothing but -inf, has no distribution: its children are rejected
  * and the new token is -1. A sequence without rows gets accepted 0, and -1
- * everywhere else; so does one whose offsets are out of range or that has more than max_rows rows (reported). A
- * parent that does not lie in front of its row is reported, and the row has no
+ * everywhere else; so does one whose offsets are out of range or that has more
+ * than max_rows rows (reported). A parent that does not lie in front of its row is reported, and the row has no
  * parent; a token outside the vocabulary is reported and never accepted; a
  * temperature that is negative or not finite is reported and counts as 1, one
  * below 2^-100 as 2^-100. Rows other than the first without a parent are never
@@ -662,10 +673,12 @@ typedef struct moe_commit_drafts_io {
  * for j = 1 .. accepted, and new_lengths = base + 1 + accepted (lengths itself for
  * a sequence without rows). What lies behind is left as it is. caches: a host
  * array of num_caches descriptors, read during the call, alike in page_size,
- * num_kv_heads and head_dim; the layers share page_table. A path must begin with
- * 0 and rise; a sequence with a path, an accepted number, offsets or a length out of range
- * is reported and left as it is, its length too (a negative one becomes 0). A token whose page is out of range is reported and
- * not moved. Sequences must not share the pages that hold their rows. */
+ * num_kv_heads and head_dim, which must not overlap; the layers share
+ * page_table. A path must begin with 0 and rise; a sequence with a path, an
+ * accepted number, offsets or a length out of range is reported and left as it
+ * is, its length too (a negative one becomes 0). A token whose page is out of
+ * range is reported and not moved. Sequences must not share the pages that hold
+ * their rows. */
 moe_status_t moe_commit_drafts(const moe_commit_drafts_io_t *io, const moe_kv_cache_t *caches, int32_t *d_status,
                                void *cuda_stream);
 

@@ -16,8 +16,9 @@ PyTorch only supplies device memory and streams here; every step runs in
 libmoe.so, and a failed call raises. Sizes that live on the device (lengths,
 pages, slots, positions) are checked there: pass ``d_status``, an int32 tensor
 set to MOE_OK, and look at it when convenient (MOE_ERR_DEVICE_BOUNDS: something
-was out of range and was not accessed; MOE_ERR_TIMEOUT: a wait inside the prompt
-kernel did not end within a second, and the results are unspecified).
+was out of range and was not accessed; MOE_ERR_TIMEOUT: a wait inside the
+kernels of prompts or large trees did not end within a second, and the results
+are unspecified).
 
 The calls serve only: they have no backward pass, and refuse inputs that require
 a gradient unless gradients are off (``torch.no_grad()``).

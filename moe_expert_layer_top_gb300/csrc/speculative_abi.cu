@@ -32,7 +32,7 @@ moe_status_t moe_attend_tree(const moe_attend_tree_io_t *io, const moe_kv_cache_
   if (s == MOE_OK) s = cache_ok(*cache);
   if (s != MOE_OK) return s;
   if (!finite(r.scale) || !aligned(d_status, 4) || !aligned(r.lse, 4)) return MOE_ERR_INVALID_ARG;
-  if (r.flags & ~MOE_FLAG_TEST_BOUNDS) return MOE_ERR_INVALID_ARG;
+  if (r.flags & ~(MOE_FLAG_TEST_SKIP_READY | MOE_FLAG_TEST_BOUNDS)) return MOE_ERR_INVALID_ARG;
   if (r.num_rows == 0 || r.num_seqs == 0) return MOE_OK;
   const int64_t width = int64_t(r.num_heads) * cache->head_dim;
   if (!good(r.q, 16) || !good(r.out, 16) || !stride_ok(r.q_stride, width) || !stride_ok(r.out_stride, width))

@@ -79,6 +79,7 @@ struct TileArgs {
   uint32_t flip;  // 0x80008000 with a negative scale
   float *parts;
   int64_t part_cap, cached_rows;
+  bool skip;  // the first decoding warp does nothing: every wait runs out
   int32_t *status;
 };
 
@@ -1047,6 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     Decoder<D> role(a, sm);
+    if (a.skip && warp == kWarpDecode) left = 0;
     while (left > 0) {
       const Segment seg = next_segment(a, place, left);
       if (seg.count == 0) continue;
@@ -1217,6 +1219,7 @@ cudaError_t launch_tree_tiles(const moe_attend_tree_io_t &io, const moe_kv_cache
   a.flip = r.scale < 0.0f ? 0x80008000u : 0u;
   a.parts = static_cast<float *>(workspace);
   a.part_cap = checked_capacity(workspace_bytes / (int64_t(2) * kRows * (c.head_dim + 2) * 4), r.flags);
+  a.skip = r.flags & MOE_FLAG_TEST_SKIP_READY;
   a.status = status;
   const bool h = r.dtype == MOE_DTYPE_F16;
   if (c.head_dim == 64) return h ? launch<F16, 64>(a, usual_rows, num_sms, st) : launch<Bf16, 64>(a, usual_rows, num_sms, st);

@@ -44,6 +44,32 @@ TREES = [
 ]
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seqs", [1, 40])  # one item and several a block, shared and whole
+def test_wait_that_runs_out_is_reported(D, seqs):
+    """Keys that never come: the waits end at their bound (a second), the status says so, the next call is right."""
+    H, K, rows, n = 8, 2, 40, 700
+    rng = np.random.default_rng(30)
+    c = ac.Cache(rng, [n] * seqs, K, D, 64)
+    q = ac.dev(ac.rows16(rng, (rows * seqs, H, D), "bf16", 1.0), "bf16")
+    parents, lens = ac.i32(list(range(-1, rows - 1)) * seqs), ac.i32([n] * seqs)
+    cu = ac.i32(ac.offsets([rows] * seqs))
+    want, z = attention.attend_tree(q, c.cache, c.table, lens, cu, parents, max_rows=rows, return_lse=True)
+    out, lse = torch.zeros_like(q), torch.zeros(rows * seqs, H, device="cuda")
+    for flags, code in ((abi.MOE_FLAG_TEST_SKIP_READY, abi.MOE_ERR_TIMEOUT), (0, abi.MOE_OK)):
+        io = abi.MoeAttendTreeIO(
+            abi.MoeAttendPagedIO(q.data_ptr(), H * D, out.data_ptr(), H * D, lse.data_ptr(), c.table.data_ptr(),
+                                 lens.data_ptr(), cu.data_ptr(), seqs, rows * seqs, c.max_pages, rows, H,
+                                 abi.MOE_DTYPE_BF16, D ** -0.5, flags), parents.data_ptr())
+        kv, st = c.cache.as_abi(), status()
+        size = abi.moe_attend_tree_workspace(io, kv)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        assert abi.moe_attend_tree(io, kv, ws, size, st, torch.cuda.current_stream()) == abi.MOE_OK
+        torch.cuda.synchronize()
+        assert st.item() == code
+    assert torch.equal(out, want) and torch.equal(lse, z)
+
+
 # Rows of a kv head and (sequence, kv head) pairs on both sides of where the kernels change.
 BORDERS = [(tokens, group, seqs) for tokens, group in ((32, 1), (33, 1), (12, 4), (49, 1)) for seqs in (1, 16, 17)]
 
