@@ -40,7 +40,7 @@ int64_t attend_tree_workspace(const moe_attend_tree_io_t &io, const moe_kv_cache
 cudaError_t launch_attend_tree(const moe_attend_tree_io_t &io, const moe_kv_cache_t &c, void *workspace,
                                int64_t workspace_bytes, int32_t *status, int num_sms, cudaStream_t st) {
   if (tiles(io, c))
-    return launch_tree_tiles(io, c, usual_rows(io.rows, c), workspace, workspace_bytes, status, num_sms, st);
+    return launch_tree_tiles(io, c, usual_rows(io.rows, c), workspace, status, num_sms, st);
   return launch_paged<true>(io.rows, io.parents, c, workspace, workspace_bytes, status, num_sms, st);
 }
 

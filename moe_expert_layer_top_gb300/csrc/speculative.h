@@ -16,7 +16,7 @@ cudaError_t launch_attend_tree(const moe_attend_tree_io_t &io, const moe_kv_cach
                                int64_t workspace_bytes, int32_t *status, int num_sms, cudaStream_t st);
 int64_t tree_tiles_workspace(const moe_kv_cache_t &c, int num_sms);
 cudaError_t launch_tree_tiles(const moe_attend_tree_io_t &io, const moe_kv_cache_t &c, int usual_rows, void *workspace,
-                              int64_t workspace_bytes, int32_t *status, int num_sms, cudaStream_t st);
+                              int32_t *status, int num_sms, cudaStream_t st);
 cudaError_t launch_verify_drafts(const moe_verify_drafts_io_t &io, int32_t *status, int num_sms, cudaStream_t st);
 cudaError_t launch_commit_drafts(const moe_commit_drafts_io_t &io, const moe_kv_cache_t *caches, int32_t *status,
                                  cudaStream_t st);

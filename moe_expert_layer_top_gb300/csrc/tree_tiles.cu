@@ -65,6 +65,12 @@ constexpr int kMinShare = 2;  // units of a share, at least: each block between 
 constexpr int kJoinThreads = 256;
 constexpr int kMaxBlocks = 1024;
 
+// An item that several blocks share, told by the first of them; parts 0: there is none.
+struct Joint {
+  int32_t parts, slot;          // of the first block's two parts; the later ones' is their first
+  int32_t row0, kv, r0, rows;  // first row of the sequence, kv head, first (token, head) pair, pairs
+};
+
 struct TileArgs {
   const uint16_t *q;
   int64_t q_stride;
@@ -78,7 +84,8 @@ struct TileArgs {
   float scale2;   // |scale| log2 e, at least 2^-100
   uint32_t flip;  // 0x80008000 with a negative scale
   float *parts;
-  int64_t part_cap, cached_rows;
+  Joint *joints;  // of each block
+  int64_t part_cap, joint_cap, cached_rows;
   bool skip;  // the first decoding warp does nothing: every wait runs out
   int32_t *status;
 };
@@ -167,6 +174,9 @@ struct List {
     all = *total;
   }
 
+  // The sums are there.
+  __device__ __forceinline__ List(const TileArgs &args, const int64_t *shared, int64_t total) : a(args), before(shared), all(total) {}
+
   // The place of unit p (0 <= p < all). Whole warp.
   __device__ Place find(int64_t p) const {
     const int lane = threadIdx.x & 31;
@@ -243,6 +253,30 @@ __device__ __forceinline__ Shares make_shares(int64_t units, int64_t grid) {
   return s;
 }
 
+// What the block leaves to be joined: its last item, if it has the item's first tile and later blocks have others. Whole warp.
+__device__ __forceinline__ void tell_joint(const TileArgs &a, const List &list) {
+  const Shares shares = make_shares(list.all, gridDim.x);
+  const int64_t c = blockIdx.x;
+  Joint j = {};
+  if (c + 1 < shares.blocks) {
+    const int64_t begin = shares.begin(c), end = shares.begin(c + 1);
+    const Place p = list.find(end - 1);
+    const int64_t item0 = end - 1 - p.unit, tile0 = item0 + kOver;
+    const int64_t tile1 = tile0 + int64_t(p.s.tiles - 1) * p.s.weight;  // the first and last tile's units
+    if (tile0 >= begin && tile0 < end && tile1 >= end) {
+      int64_t last = c + 1;
+      while (shares.begin(last + 1) <= tile1) ++last;
+      j.parts = int(last - c) + 1;
+      j.slot = item0 <= begin ? 0 : 1;
+      j.row0 = p.s.row0;
+      j.kv = p.item / p.s.blocks;
+      j.r0 = (p.item - j.kv * p.s.blocks) * 2 * kRows;
+      j.rows = min(2 * kRows, p.s.n * a.group - j.r0);
+    }
+  }
+  if ((threadIdx.x & 31) == 0 && index_ok(a.status, c, a.joint_cap)) a.joints[c] = j;
+}
+
 // ------------------------------------------------------------------ shared memory
 
 template <int D>
@@ -263,7 +297,7 @@ struct Smem {
   uint8_t join[D == 128 ? 16 : kRows * 64 * 4];  // D = 128: the second stream's query tile serves
   int exps[kExps][2][4];                       // by tile mod kExps: the largest scale codes of 32 keys each, and of their values
   uint8_t parent[kMaxTree];                    // place of the parent plus one
-  int64_t total;
+  int64_t before[kMaxSeqs / 32 + 1], total;    // of the list of work
   uint64_t q_full[2];      // the query tile is there (4 warps)
   uint64_t full[kStages];  // a K or V tile is there (4 warps)
   uint64_t empty[kStages]; // the MMAs that read it are done (2 commits: one of each stream, or two of one)
@@ -1020,8 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
   }
   if (blockIdx.x == 0)  // what is out of range is reported once
     for (int b = threadIdx.x; b < a.num_seqs; b += kThreads) load_seq(a, b, a.status);
-  // the sums lie where the first keys come later
-  const List list(a, reinterpret_cast<int64_t *>(sm.kv[0]), &sm.total);
+  const List list(a, sm.before, &sm.total);
   const Shares shares = make_shares(list.all, gridDim.x);
   const bool any = int64_t(blockIdx.x) < shares.blocks;
   const int64_t begin = any ? shares.begin(blockIdx.x) : 0, end = any ? shares.begin(int64_t(blockIdx.x) + 1) : 0;
@@ -1056,6 +1089,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
       t += seg.count;
     }
   }
+  if (warp == kThreads / 32 - 1) tell_joint(a, List(a, sm.before, sm.total));  // in the shadow of the last softmax
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
@@ -1065,86 +1099,69 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
 }
 
 // ------------------------------------------------------------------ joining the blocks
-// Block c joins the item whose first tile is the main kernel's block c's, if later blocks have tiles of it too.
+// Block c joins the item whose first tile is the main kernel's block c's, if later blocks have tiles of it too. What there is
+// to join the main kernel has left: the blocks without work, most of them, end at once (with the list of work looked through
+// again by each block the joins took 10 to 23 us).
 
-constexpr int kJoinRows = 8;  // rows at a time
+template <int D>
+constexpr int kJoinRows = kJoinThreads / (D / 4);  // rows at a time: a thread has four dimensions of one
 
 template <class T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const TileArgs a) {
-  __shared__ int64_t before[kMaxSeqs / 32 + 1], total;
-  __shared__ float weight[kJoinRows][kMaxBlocks], sums[kJoinRows], tops[kJoinRows];
-  static_assert(kJoinThreads == kJoinRows * 32 && kJoinRows * (D / 4) <= kJoinThreads, "a warp for each row's weights");
-  const List list(a, before, &total);
-  const Shares shares = make_shares(list.all, gridDim.x);
-  const int64_t c = blockIdx.x;
-  Place p;
-  bool none = true;
-  int64_t last = c + 1, item0 = 0, begin = 0;
-  if (c + 1 < shares.blocks) {
-    begin = shares.begin(c);
-    const int64_t end = shares.begin(c + 1);
-    p = list.find(end - 1);
-    item0 = end - 1 - p.unit;
-    const int64_t tile0 = item0 + kOver, tile1 = tile0 + int64_t(p.s.tiles - 1) * p.s.weight;  // the first and last tile's units
-    none = tile0 < begin || tile0 >= end || tile1 < end;
-    while (!none && shares.begin(last + 1) <= tile1) ++last;
-  }
+  const int c = int(blockIdx.x);
   pdl_wait_primary();  // every block: this kernel must not end before the main one
-  if (none) return;
-  const int parts = int(last - c) + 1;
-  if (!index_ok(a.status, parts - 1, kMaxBlocks) || !index_ok(a.status, 2 * last, a.part_cap)) return;
+  const Joint p = a.joints[c];
+  const int parts = p.parts;
+  if (parts == 0) return;
+  if (!index_ok(a.status, parts - 1, kMaxBlocks) || !index_ok(a.status, 2 * (c + parts - 1), a.part_cap)) return;
   constexpr int64_t kPart = 2 * kRows * (D + 2);
-  const float *const part0 = a.parts + (c * 2 + (item0 <= begin ? 0 : 1)) * kPart, *const part1 = a.parts + c * 2 * kPart;
+  const float *const part0 = a.parts + int64_t(c * 2 + p.slot) * kPart, *const part1 = a.parts + int64_t(c) * 2 * kPart;
   const auto part = [&](int b) { return b ? part1 + int64_t(b) * 2 * kPart : part0; };
-  const int kv = p.item / p.s.blocks, r0 = (p.item - kv * p.s.blocks) * 2 * kRows;
-  const int rows = min(2 * kRows, p.s.n * a.group - r0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int first = int(blockIdx.y) * kJoinRows; first < rows; first += int(gridDim.y) * kJoinRows) {
-    {
-      const int head = 2 * kRows * D + first + warp;
-      float m = kLowest, l = 0.0f;
-      for (int b = lane; b < parts; b += 32) m = fmaxf(m, part(b)[head]);
+  const int kv = p.kv, r0 = p.r0, rows = p.rows;
+  const int row = threadIdx.x % kJoinRows<D>, d = 4 * (threadIdx.x / kJoinRows<D>);
+  constexpr int kAtOnce = 2;  // parts (with 8 of them 16 trees of 64 rows take 326 us in place of 315)
+  for (int i = int(blockIdx.y) * kJoinRows<D> + row; i < rows; i += int(gridDim.y) * kJoinRows<D>) {
+    float m = kLowest, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int b0 = 0; b0 < parts; b0 += kAtOnce) {
+      float mb[kAtOnce], lb[kAtOnce];
+      float4 v[kAtOnce];
 #pragma unroll
-      for (int k = 16; k; k /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
-      for (int b = lane; b < parts; b += 32) {
-        const float f = exp2_approx(part(b)[head] - m);
-        weight[warp][b] = f;
-        l = fmaf(part(b)[head + 2 * kRows], f, l);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const bool some = b0 + k < parts;
+        const float *const from = part(some ? b0 + k : b0);
+        mb[k] = some ? from[2 * kRows * D + i] : kLowest;
+        lb[k] = some ? from[2 * kRows * (D + 1) + i] : 0.0f;
+        v[k] = *reinterpret_cast<const float4 *>(from + d * (2 * kRows) + i * 4);
+        if (!some) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
+      float top = m;
 #pragma unroll
-      for (int k = 16; k; k /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, k);
-      if (lane == 0) {
-        tops[warp] = m;
-        sums[warp] = l;
+      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, mb[k]);
+      const float f = exp2_approx(m - top);
+      m = top;
+      l *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float w = exp2_approx(mb[k] - top);
+        l = fmaf(lb[k], w, l);
+        o.x = fmaf(v[k].x, w, o.x), o.y = fmaf(v[k].y, w, o.y), o.z = fmaf(v[k].z, w, o.z), o.w = fmaf(v[k].w, w, o.w);
       }
     }
-    __syncthreads();
-    const int row = threadIdx.x % kJoinRows, d = 4 * (threadIdx.x / kJoinRows), r = r0 + first + row;
-    if (d < D && first + row < rows) {
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int b = 0; b < parts; ++b) {
-        const float4 v = *reinterpret_cast<const float4 *>(part(b) + d * (2 * kRows) + (first + row) * 4);
-        const float w = weight[row][b];
-        o.x = fmaf(v.x, w, o.x), o.y = fmaf(v.y, w, o.y), o.z = fmaf(v.z, w, o.z), o.w = fmaf(v.w, w, o.w);
-      }
-      const float l = sums[row], inv = l != 0.0f ? 1.0f / l : 0.0f;
-      const int token = r / a.group, h = kv * a.group + r - token * a.group;
-      if (row_ok(a, p.s.row0 + token, h)) {
-        *reinterpret_cast<uint2 *>(a.out + int64_t(p.s.row0 + token) * a.out_stride + int64_t(h) * D + d) =
-            l != 0.0f ? make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)) : make_uint2(0, 0);
-        if (d == 0 && a.lse)
-          a.lse[int64_t(p.s.row0 + token) * a.num_heads + h] =
-              l != 0.0f ? (log2f(l) + (tops[row] - kUp)) * 0.6931471805599453f : -INFINITY;
-      }
-    }
-    __syncthreads();
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    const int r = r0 + i, token = r / a.group, h = kv * a.group + r - token * a.group;
+    if (!row_ok(a, p.row0 + token, h)) continue;
+    *reinterpret_cast<uint2 *>(a.out + int64_t(p.row0 + token) * a.out_stride + int64_t(h) * D + d) =
+        l != 0.0f ? make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+    if (d == 0 && a.lse)
+      a.lse[int64_t(p.row0 + token) * a.num_heads + h] = l != 0.0f ? (log2f(l) + (m - kUp)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
 // ------------------------------------------------------------------ host
 
 int blocks_of(int num_sms) { return num_sms < kMaxBlocks ? num_sms : kMaxBlocks; }
+int64_t part_bytes(const moe_kv_cache_t &c) { return int64_t(2) * kRows * (c.head_dim + 2) * 4; }
 
 template <class T, int D>
 cudaError_t launch(const TileArgs &a, int usual_rows, int num_sms, cudaStream_t st) {
@@ -1166,13 +1183,10 @@ cudaError_t launch(const TileArgs &a, int usual_rows, int num_sms, cudaStream_t 
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  // Blocks of an item that is joined: about eight for each SM in all, of 8 rows at least. (Those without anything to join cost
-  // a little too: one tree of 16 rows 24.9 us with 8 of an item, 30.7 with 32; one of 64 rows 175 and 162; 24 ragged trees
-  // 83 with 4, 75 with 8, 82 with 32.)
-  const int64_t items = int64_t(a.num_seqs) * a.num_kv_heads * ((usual_rows + 2 * kRows - 1) / (2 * kRows));
-  const int64_t joined = items < grid ? items : grid, most = ((usual_rows < 2 * kRows ? usual_rows : 2 * kRows) + kJoinRows - 1) / kJoinRows;
-  const int64_t wanted = (8 * int64_t(grid) + joined - 1) / joined;
-  cfg.gridDim = dim3(grid, unsigned(wanted < most ? wanted : most));
+  // As many blocks of an item as the usual rows need. (With fewer, each with several runs of rows, 16 trees of 64 rows took 324
+  // and 327 us in place of 321, 24 ragged ones 72 and 81 in place of 70.)
+  const int most = usual_rows < 2 * kRows ? usual_rows : 2 * kRows;
+  cfg.gridDim = dim3(grid, unsigned((most + kJoinRows<D> - 1) / kJoinRows<D>));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1186,11 +1200,11 @@ cudaError_t launch(const TileArgs &a, int usual_rows, int num_sms, cudaStream_t 
 }  // namespace
 
 int64_t tree_tiles_workspace(const moe_kv_cache_t &c, int num_sms) {
-  return int64_t(blocks_of(num_sms)) * 2 * 2 * kRows * (c.head_dim + 2) * 4;
+  return int64_t(blocks_of(num_sms)) * (2 * part_bytes(c) + int64_t(sizeof(Joint)));
 }
 
 cudaError_t launch_tree_tiles(const moe_attend_tree_io_t &io, const moe_kv_cache_t &c, int usual_rows, void *workspace,
-                              int64_t workspace_bytes, int32_t *status, int num_sms, cudaStream_t st) {
+                              int32_t *status, int num_sms, cudaStream_t st) {
   const moe_attend_paged_io_t &r = io.rows;
   TileArgs a = {};
   a.q = static_cast<const uint16_t *>(r.q);
@@ -1218,7 +1232,10 @@ cudaError_t launch_tree_tiles(const moe_attend_tree_io_t &io, const moe_kv_cache
   a.scale2 = fmaxf(fabsf(r.scale) * 1.4426950408889634f, 0x1p-100f);
   a.flip = r.scale < 0.0f ? 0x80008000u : 0u;
   a.parts = static_cast<float *>(workspace);
-  a.part_cap = checked_capacity(workspace_bytes / (int64_t(2) * kRows * (c.head_dim + 2) * 4), r.flags);
+  const int blocks = blocks_of(num_sms);
+  a.joints = reinterpret_cast<Joint *>(static_cast<char *>(workspace) + 2 * blocks * part_bytes(c));
+  a.part_cap = checked_capacity(int64_t(2) * blocks, r.flags);
+  a.joint_cap = blocks;
   a.skip = r.flags & MOE_FLAG_TEST_SKIP_READY;
   a.status = status;
   const bool h = r.dtype == MOE_DTYPE_F16;
