@@ -29,6 +29,13 @@ __device__ __forceinline__ bool index_ok(int32_t *status, int64_t i, int64_t n) 
   return true;
 }
 
+// An item that several blocks share, as the first of them leaves it to the kernel that joins them; no parts: there is none.
+struct alignas(16) Joint {
+  int32_t parts, slot;         // which of the first block's two parts; of the later blocks it is the first
+  int32_t row0, kv, r0, rows;  // first row of the sequence, kv head, first (token, head) pair, pairs
+  int32_t unused[2];
+};
+
 // ------------------------------------------------------------------ 16-bit types
 
 struct Bf16 {

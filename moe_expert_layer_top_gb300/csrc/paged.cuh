@@ -37,7 +37,8 @@ struct PagedArgs {
   int num_pages, page_size;
   float scale2;    // |scale| log2 e, at least 2^-100
   uint32_t flip;   // 0x80008000 with a negative scale
-  float *parts;    // workspace: two partial results a block
+  float *parts;    // workspace: two partial results a block,
+  Joint *joints;   // and what they leave to be joined
   int64_t part_cap, cached_rows;  // partial results that it holds, rows of the cache: for the checks
   int32_t *status;
 };
@@ -243,6 +244,10 @@ struct Shares {
   int64_t blocks, each, more;  // the first `more` blocks have each + 1 units
 
   __device__ __forceinline__ int64_t begin(int64_t b) const { return b * each + (b < more ? b : more); }
+  __device__ __forceinline__ int64_t block_of(int64_t unit) const {
+    const int64_t longer = more * (each + 1);
+    return unit < longer ? divide(unit, each + 1) : more + divide(unit - longer, each);
+  }
 };
 
 template <class C>
@@ -627,18 +632,18 @@ __device__ __forceinline__ bool row_ok(const PagedArgs &a, int row, int head) {
 
 // Writes row (token, head) pair r of an item: 4 dimensions from d on, or (d < 0) its log sum exp.
 template <class T>
-__device__ __forceinline__ void store4(const PagedArgs &a, const Seq &s, int kv, int r, int dims, int d, float4 v) {
+__device__ __forceinline__ void store4(const PagedArgs &a, int row0, int kv, int r, int dims, int d, float4 v) {
   const int tok = r / a.group, h = kv * a.group + r - tok * a.group;
-  if (!row_ok(a, s.row0 + tok, h)) return;
-  uint16_t *dst = a.out + int64_t(s.row0 + tok) * a.out_stride + int64_t(h) * dims + d;
+  if (!row_ok(a, row0 + tok, h)) return;
+  uint16_t *dst = a.out + int64_t(row0 + tok) * a.out_stride + int64_t(h) * dims + d;
   *reinterpret_cast<uint2 *>(dst) = make_uint2(T::pack(v.x, v.y), T::pack(v.z, v.w));
 }
 
-__device__ __forceinline__ void store_lse(const PagedArgs &a, const Seq &s, int kv, int r, float ref, float sum) {
+__device__ __forceinline__ void store_lse(const PagedArgs &a, int row0, int kv, int r, float ref, float sum) {
   if (!a.lse) return;
   const int tok = r / a.group, h = kv * a.group + r - tok * a.group;
-  if (!row_ok(a, s.row0 + tok, h)) return;
-  a.lse[int64_t(s.row0 + tok) * a.num_heads + h] = sum != 0.0f ? (log2f(sum) + ref) * 0.6931471805599453f : -INFINITY;
+  if (!row_ok(a, row0 + tok, h)) return;
+  a.lse[int64_t(row0 + tok) * a.num_heads + h] = sum != 0.0f ? (log2f(sum) + ref) * 0.6931471805599453f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ trees
@@ -759,12 +764,17 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
   typename C::Smem &sm =
       *reinterpret_cast<typename C::Smem *>((reinterpret_cast<uintptr_t>(paged_smem_raw) + 127) & ~uintptr_t(127));
   __shared__ int64_t total;
+  __shared__ Shares divided;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   if (blockIdx.x == 0)  // what is out of range is reported once
     for (int b = tid; b < a.num_seqs; b += C::THREADS) load_seq<C>(a, b, a.status);
   const List<C> list(a, sm.before, &total);
   const Shares shares = make_shares<C>(list.all, gridDim.x);
+  if (tid == 0) {
+    a.joints[blockIdx.x].parts = 0;
+    divided = shares;
+  }
   if (int64_t(blockIdx.x) >= shares.blocks) return;
   const int64_t begin = shares.begin(blockIdx.x), end = shares.begin(int64_t(blockIdx.x) + 1);
   Place place = list.find(begin);
@@ -846,6 +856,11 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
     const int rows = seg.s.n * a.group - seg.r0;  // real rows of the block
     const int64_t slot_of = int64_t(blockIdx.x) * 2 + (first ? 0 : 1);
     float *part = a.parts + slot_of * C::PART;
+    if (tid == 0 && !whole && seg.first == 0) {  // the block's last item, which goes on in later ones
+      const int64_t end = divided.begin(int64_t(blockIdx.x) + 1), rest = seg.s.steps - seg.count;  // units of it behind `end`
+      const int64_t last = divided.block_of(end + rest - 1);
+      a.joints[blockIdx.x] = {int(last - blockIdx.x) + 1, first ? 0 : 1, seg.s.row0, seg.kv, seg.r0, min(C::ROWS, rows), {}};
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float f[2];
@@ -877,9 +892,9 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
         if (whole) {
           if (rr < rows) {
             const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-            store4<T>(a, seg.s, seg.kv, seg.r0 + rr, D, d,
+            store4<T>(a, seg.s.row0, seg.kv, seg.r0 + rr, D, d,
                       l != 0.0f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0, 0, 0, 0));
-            if (d == 0) store_lse(a, seg.s, seg.kv, seg.r0 + rr, m, l);
+            if (d == 0) store_lse(a, seg.s.row0, seg.kv, seg.r0 + rr, m, l);
           }
         } else if (index_ok(a.status, slot_of, a.part_cap)) {
           *reinterpret_cast<float4 *>(part + rr * D + d) = v;
@@ -897,38 +912,23 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
 
 // ------------------------------------------------------------------ joining the blocks
 // Block c joins the item that block c of the main kernel began last, if that
-// item went on into later blocks.
+// item went on into later blocks; the main kernel says so, and blocks without work end at once.
 
 template <class T, class C>
 __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const PagedArgs a) {
-  __shared__ int64_t before[kMaxSeqs / 32 + 1], total;
   __shared__ float weight[8][kMaxBlocks], top[8], sum[8];  // by row
   static_assert(kCombineThreads == 8 * 32, "a warp for each row's weights");
-  const List<C> list(a, before, &total);
-  const Shares shares = make_shares<C>(list.all, gridDim.x);
-  const int64_t c = blockIdx.x;
-  Place p;
-  int64_t begin = 0, end = 0, item0 = 0, item1 = 0, last = c + 1;  // the block's units, the item's, its last block
-  if (c + 1 < shares.blocks) {
-    begin = shares.begin(c);
-    end = shares.begin(c + 1);
-    p = list.find(end - 1);
-    item0 = end - 1 - p.unit;
-    item1 = item0 + kOver + p.s.steps;
-    while (shares.begin(last + 1) < item1) ++last;
-  }
-  // the item's first stage is in a later block, or in an earlier one, or all of them are in this block: nothing to join
-  const bool none = end <= item0 + kOver || begin > item0 + kOver || item1 <= end;
-  pdl_wait_primary();  // every block: this kernel must not end before the main one
-  if (none) return;
-  // the blocks that hold parts of it: c, whose part is its last segment, and those after it, whose first it is
-  constexpr int D = C::D, kAhead = 16;
+  constexpr int D = C::D, kAhead = 8;  // 16: 98 us in place of 94 with 64 trees of six rows, 83 and 80 with 64 chains; 4: one token 11.6 and 10.3
   static_assert(8 * (D / 4) <= kCombineThreads, "one thread for four dimensions of a row");
-  const int parts = int(last - c) + 1;
-  if (!index_ok(a.status, parts - 1, kMaxBlocks) || !index_ok(a.status, 2 * last + 1, a.part_cap)) return;
+  const int c = int(blockIdx.x);
+  pdl_wait_primary();  // every block: this kernel must not end before the main one
+  const Joint p = a.joints[c];
+  const int parts = p.parts;
+  if (parts == 0) return;
+  if (!index_ok(a.status, parts - 1, kMaxBlocks) || !index_ok(a.status, 2 * (c + parts) - 1, a.part_cap)) return;
   const int row0 = 8 * int(blockIdx.y);  // this block's 8 rows of the item
-  const float *part0 = a.parts + (c * 2 + (item0 <= begin ? 0 : 1)) * C::PART;
-  const float *part1 = a.parts + c * 2 * C::PART;  // the others: part b is 2 b slots on
+  const float *part0 = a.parts + int64_t(c * 2 + p.slot) * C::PART;
+  const float *part1 = a.parts + int64_t(c) * 2 * C::PART;  // the others: part b is 2 b slots on
   const auto part = [&](int b) { return b ? part1 + int64_t(b) * 2 * C::PART : part0; };
   const int row = threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4)), at = (row0 + row) * D + d;
   const bool mine = row < 8;
@@ -965,8 +965,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const Pa
     }
   }
   __syncthreads();
-  const int per = p.s.items / a.num_kv_heads, kv = p.item / per, r0 = (p.item - kv * per) * C::ROWS;
-  if (!mine || r0 + row0 + row >= p.s.n * a.group) return;
+  if (!mine || row0 + row >= p.rows) return;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const auto add = [&](const float4 &x, float w) {
     o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
@@ -977,9 +976,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const Pa
 #pragma unroll 8
   for (int b = kAhead; b < parts; ++b) add(*reinterpret_cast<const float4 *>(part(b) + at), weight[row][b]);
   const float l = sum[row], inv = l != 0.0f ? 1.0f / l : 0.0f;
-  store4<T>(a, p.s, kv, r0 + row0 + row, D, d,
+  store4<T>(a, p.row0, p.kv, p.r0 + row0 + row, D, d,
             l != 0.0f ? make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv) : make_float4(0, 0, 0, 0));
-  if (d == 0) store_lse(a, p.s, kv, r0 + row0 + row, top[row], l);
+  if (d == 0) store_lse(a, p.row0, p.kv, p.r0 + row0 + row, top[row], l);
 }
 
 // ------------------------------------------------------------------ host
@@ -1046,7 +1045,7 @@ template <bool TREE>
 int64_t workspace_of(const moe_attend_paged_io_t &io, const moe_kv_cache_t &c, int num_sms) {
   const auto bytes = [&](auto cfg) {
     using C = decltype(cfg);
-    return int64_t(blocks_of<C>(num_sms)) * 2 * C::PART * 4;
+    return int64_t(blocks_of<C>(num_sms)) * (2 * C::PART * 4 + int64_t(sizeof(Joint)));
   };
   const int rows = usual_rows(io, c);
   return c.head_dim == 64 ? pick<64, TREE>(rows, bytes) : pick<128, TREE>(rows, bytes);
@@ -1085,7 +1084,9 @@ cudaError_t launch_paged(const moe_attend_paged_io_t &io, const int32_t *parents
   const bool h = io.dtype == MOE_DTYPE_F16;
   const auto go = [&](auto cfg) {
     using C = decltype(cfg);
-    a.part_cap = checked_capacity(workspace_bytes / (C::PART * 4), io.flags);
+    const int64_t all = int64_t(2) * blocks_of<C>(num_sms);
+    a.joints = reinterpret_cast<Joint *>(a.parts + all * C::PART);
+    a.part_cap = checked_capacity(all, io.flags);
     return h ? launch<F16, C>(a, num_sms, st) : launch<Bf16, C>(a, num_sms, st);
   };
   const int rows = usual_rows(io, c);

@@ -65,12 +65,6 @@ constexpr int kMinShare = 2;  // units of a share, at least: each block between 
 constexpr int kJoinThreads = 256;
 constexpr int kMaxBlocks = 1024;
 
-// An item that several blocks share, told by the first of them; parts 0: there is none.
-struct Joint {
-  int32_t parts, slot;          // of the first block's two parts; the later ones' is their first
-  int32_t row0, kv, r0, rows;  // first row of the sequence, kv head, first (token, head) pair, pairs
-};
-
 struct TileArgs {
   const uint16_t *q;
   int64_t q_stride;
