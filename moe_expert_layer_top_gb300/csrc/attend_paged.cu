@@ -20,10 +20,10 @@
 // whatever multiplies them (2 D conversions a token, at half rate). 128 single
 // tokens of 4,000 to 16,000 (D = 128, 32 + 8 heads) take 243 us, 4.83 TB/s or 71 %
 // of the copy bandwidth: issue slots are 63 % busy, the ALU pipe 56 %. With 24
-// rows of a kv head (steps of six rows, 64 sequences of 1,024 to 5,120, 82 us) it
+// rows of a kv head (steps of six rows, 64 sequences of 1,024 to 5,120, 77 us) it
 // is neither: two warps a scheduler (the accumulators take the registers) wait on
 // fixed latencies; tensor pipe 36 %, issue 44 %, HBM 30 %. One token over 4,096:
-// 10.7 us, launches and the chain lookup - load - join.
+// 10.3 us, launches and the chain lookup - load - join.
 // The codes go from shared memory straight into the registers that the MMA
 // reads. tcgen05 would need V in 16 bits in shared memory first, since V's scale
 // groups do not lie along the product's inner dimension (the keys). K's do: its
@@ -50,7 +50,9 @@
 // there the accumulators of all warps are joined through shared memory, which the
 // drained rings leave free. What a block holds of an item that it shares with
 // other blocks goes to the workspace; a second kernel, launched with programmatic
-// dependent launch, joins these in a fixed order. Results do not depend on timing.
+// dependent launch, joins these in a fixed order. Which ones, the main kernel leaves
+// in the workspace too (looked up again in the join: 82 us with 64 steps of six rows,
+// 25.5 with 24 ragged sequences, now 77 and 20). Results do not depend on timing.
 // Tried and slower: one copying warp with bulk copies (128 tokens 479 us against
 // 244), the next granule's scores between this one's exponentials and products
 // (six rows 94 us against 82), whose registers cost more than the wait.

@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kStageKeys = 32;
 // What an item costs beside its stages, in units of one stage. 24 ragged sequences with D = 64: 25.5 us with 16, 41 with
-// 1; 64 steps of six rows 82 against 91. 10 and 24 are no better than 16.
+// 1; 64 steps of six rows 82 against 91 (with a join 5 us slower). 10 and 24 are no better than 16.
 constexpr int kOver = 16;
 constexpr float kLazy = 8.0f;            // the reference moves when the maximum is 2^kLazy beyond it
 constexpr float kNone = 3e38f;           // minus the reference of a row that has seen no key: below any score
@@ -859,7 +859,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) attend_paged_kernel(con
     if (tid == 0 && !whole && seg.first == 0) {  // the block's last item, which goes on in later ones
       const int64_t end = divided.begin(int64_t(blockIdx.x) + 1), rest = seg.s.steps - seg.count;  // units of it behind `end`
       const int64_t last = divided.block_of(end + rest - 1);
-      a.joints[blockIdx.x] = {int(last - blockIdx.x) + 1, first ? 0 : 1, seg.s.row0, seg.kv, seg.r0, min(C::ROWS, rows), {}};
+      a.joints[blockIdx.x] = {int(last - blockIdx.x) + 1, first ? 0 : 1, seg.s.row0, seg.kv, seg.r0, min(C::ROWS, rows),
+                              {}};
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -918,7 +919,9 @@ template <class T, class C>
 __global__ void __launch_bounds__(kCombineThreads) combine_paged_kernel(const PagedArgs a) {
   __shared__ float weight[8][kMaxBlocks], top[8], sum[8];  // by row
   static_assert(kCombineThreads == 8 * 32, "a warp for each row's weights");
-  constexpr int D = C::D, kAhead = 8;  // 16: 98 us in place of 94 with 64 trees of six rows, 83 and 80 with 64 chains; 4: one token 11.6 and 10.3
+  // parts ahead: with 16 blocks are fewer an SM, 93.5 us in place of 91.4 with 64 trees of six rows; with 4 one token
+  // over 4,096 takes 11.5 in place of 10.5
+  constexpr int D = C::D, kAhead = 8;
   static_assert(8 * (D / 4) <= kCombineThreads, "one thread for four dimensions of a row");
   const int c = int(blockIdx.x);
   pdl_wait_primary();  // every block: this kernel must not end before the main one
@@ -1019,12 +1022,13 @@ cudaError_t launch(const PagedArgs &a, int num_sms, cudaStream_t st) {
 // The variants: as few row blocks of at most 32 rows as the usual rows of a
 // sequence need, and as few n-tiles a block as those leave. 64 sequences of 1,024
 // to 5,120 (D = 128, groups of 4): 1 to 2 rows of a sequence take 49 us, 4 rows
-// 67 (109 in the variant of 32), 6 rows 82 (110 there), 8 rows 112.
+// 62, 6 rows 77, 8 rows, the variant of 32, 103.
 // Warps and blocks follow the registers: 16, 12 and 8 warps an SM with 128, 168
 // and 255 (D = 64: 12). 8 rows: blocks of 4 warps instead of 8 gain 3 % with 128
 // sequences (236 us against 243) and lose 7 % with one (11.4 against 10.7), whose
 // parts to join are then twice as many. 24 rows: 12 or 10 warps an SM spill or halve
-// the granules computed at once, 88 to 114 us against 65 (one long sequence) and 82.
+// the granules computed at once, 88 to 114 us against 65 (one long sequence) and 82
+// (with a slower join, 5 us of these).
 template <int D, bool TREE, class F>
 auto pick(int rows, F f) {
   const int blocks = (rows + 31) / 32, tiles = ((rows + blocks - 1) / blocks + 7) / 8;

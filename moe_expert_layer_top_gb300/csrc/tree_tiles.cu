@@ -12,23 +12,34 @@
 //   code of their own, which moves up when values beyond it appear.
 //   Queries become f16 times a power of two per row, probabilities f16 as in attend_paged.cu. All sums are binary32.
 //
-// Bound. 4 D flops per (row, head, key) on the tensor cores; a decoded key tile serves 128 or 256 rows, so
-// decoding (2 D conversions a key) is a small part of it, unlike with the 8 to 32 rows of a verify step.
+// Bound. 4 D flops per (row, head, key) on the tensor cores; a decoded key tile serves 128 or 256 rows, so decoding
+// (2 D conversions a key) is a small part of it, unlike with the 8 to 32 rows of a verify step.
+//   Measured (32 + 8 heads of 128, 152 SMs, device time in a graph): 16 trees of 64 rows over 8,000 to 32,000 tokens
+// 315 us, 990 TFLOP/s or half of a library product's rate; one of 64 rows over 131,071 tokens 148 us (930); one of 16
+// rows over 4,096 20.6; 24 ragged ones (64 + 8 heads of 64, f16) 64. A step of a stream, 128 keys, takes 4,700
+// clocks: 2,250 for the softmax (1,500 of them exponentials), 1,850 until its MMAs are issued and done, which at 128
+// x 128 take all of the shared memory's bandwidth, the rest waits and mask. The streams overlap to 44 % of the tensor
+// pipe's time and 42 % of the issue slots. Leaving out single parts (exponentials, decoding, its stores) gains 5 % at
+// most each: what is left is the chain of latencies.
+//   Tried and slower (16 trees of 64 rows): steps of 64 keys, so that one half's MMAs run under the other's softmax,
+// 382 us; the same with two warps that only issue, 352 (96 registers a thread at launch, and their code falls out of
+// the instruction cache); a thread for half a row 341 to 349; loads of S in front of the wait for the scales 339;
+// waits that spin 396.
 //
 // Layout. A block has two streams of 128 rows (MMA M, TMEM lanes), whose softmax runs in turn with the other's MMAs:
 //   wide items (more than 128 rows of a kv head): two row tiles over the same key tiles;
 //   narrow ones: the same rows over alternate key tiles, joined at the item's end through shared memory.
 //   warps 0-3   softmax of stream 0, a row a thread; warps 4-7 of stream 1; they also make the queries' tiles, and
-//               one lane of each four issues the stream's MMAs: S = Q K^T, then O += P V with P from TMEM, where the softmax wrote
-//               it over S (the stream has to wait for them anyway; a warp for them alone cost everyone 40 registers)
-//   warps 8-11  keys, warps 12-15 values: codes and scales of 128 at a time, the next tile's by cp.async into places of each thread's own,
-//               conversion into tiles (K-major and N-major, 128-byte swizzle) of a ring
-// A stream's next S is issued behind P V of its step, by the same lane, so the S of a step that is complete also says that
-// the stream's accumulators are.
+//               one lane of each four issues the stream's MMAs: S = Q K^T, then O += P V with P from TMEM, where the
+//               softmax wrote it over S (the stream has to wait for them anyway)
+//   warps 8-11  keys, warps 12-15 values: codes and scales of 128 at a time, the next tile's by cp.async into places
+//               of each thread's own, conversion into tiles (K-major and N-major, 128-byte swizzle) of a ring
+// A stream's next S is issued behind P V of its step, by the same lane, so the S of a step that is complete also says
+// that the stream's accumulators are.
 //
-// Schedule. As in attend_paged.cu: the items' key tiles in units, equal contiguous shares for one block on each SM, parts of
-// items that several blocks share in a workspace, joined in a fixed order by a second kernel. Every warp finds
-// its block's share by itself, and goes from item to item without a queue.
+// Schedule. As in attend_paged.cu: the items' key tiles in units, equal contiguous shares for one block on each SM, parts
+// of items that several blocks share in a workspace, joined in a fixed order by a second kernel. Every warp finds its
+// block's share by itself, and goes from item to item without a queue.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -169,7 +180,8 @@ struct List {
   }
 
   // The sums are there.
-  __device__ __forceinline__ List(const TileArgs &args, const int64_t *shared, int64_t total) : a(args), before(shared), all(total) {}
+  __device__ __forceinline__ List(const TileArgs &args, const int64_t *shared, int64_t total)
+      : a(args), before(shared), all(total) {}
 
   // The place of unit p (0 <= p < all). Whole warp.
   __device__ Place find(int64_t p) const {
@@ -247,7 +259,8 @@ __device__ __forceinline__ Shares make_shares(int64_t units, int64_t grid) {
   return s;
 }
 
-// What the block leaves to be joined: its last item, if it has the item's first tile and later blocks have others. Whole warp.
+// What the block leaves to be joined: its last item, if it has the item's first tile and later blocks have others.
+// Whole warp.
 __device__ __forceinline__ void tell_joint(const TileArgs &a, const List &list) {
   const Shares shares = make_shares(list.all, gridDim.x);
   const int64_t c = blockIdx.x;
@@ -278,8 +291,8 @@ struct Smem {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of Q, K or V in f16: D/64 parts of 128 rows x 128 bytes
   // Largest scales are kept for 8 tiles. Those of K tile j + 8 are written when K of tile j + 7 is there, for which S of
-  // tile j + 7 - kStages / 2 >= j + 3 was done; that was issued behind P V of the tile before (or two before) in its stream, and so were
-  // those before it: the softmax has read those of tile j.
+  // tile j + 7 - kStages / 2 >= j + 3 was done; that was issued behind P V of the tile before (or two before) in its
+  // stream, and so were those before it: the softmax has read those of tile j.
   static constexpr int kExps = 8;
   static_assert(kExps >= kStages / 2 + 4, "largest scales");
   static constexpr int kRawBytes = kKeys * D / 2;
@@ -289,7 +302,7 @@ struct Smem {
   uint8_t kv[kStages][kTileBytes];
   uint8_t raw[2][kRawBytes];                   // codes of K and V of the next tile as each thread copied them
   uint8_t join[D == 128 ? 16 : kRows * 64 * 4];  // D = 128: the second stream's query tile serves
-  int exps[kExps][2][4];                       // by tile mod kExps: the largest scale codes of 32 keys each, and of their values
+  int exps[kExps][2][4];                       // by tile mod kExps: largest scale codes of 32 keys, of their values
   uint8_t parent[kMaxTree];                    // place of the parent plus one
   int64_t before[kMaxSeqs / 32 + 1], total;    // of the list of work
   uint64_t q_full[2];      // the query tile is there (4 warps)
@@ -459,8 +472,8 @@ __device__ __forceinline__ bool row_ok(const TileArgs &a, int row, int head) {
 }
 
 // ------------------------------------------------------------------ keys (warps 8-11) and values (warps 12-15)
-// A warp takes 32 keys of each tile, a lane one group of 32 dimensions of every 8th (D = 128) or 16th key: 16 bytes of codes.
-// Its lanes then store the 16-byte pieces of eight keys at a time, which the swizzle puts into different banks.
+// A warp takes 32 keys of each tile, a lane one group of 32 dimensions of every 8th (D = 128) or 16th key: 16 bytes of
+// codes. Its lanes then store the 16-byte pieces of eight keys at a time, which the swizzle puts into different banks.
 
 template <int D>
 struct Decoder {
@@ -502,8 +515,8 @@ struct Decoder {
     return r;
   }
 
-  // Codes and scales of tile i of the segment on their way. (Two tiles ahead measured the same, 331 and 75.7 us against 329
-  // and 74.5 with 16 trees of 64 rows and ragged ones of D = 64.)
+  // Codes and scales of tile i of the segment on their way. (Two tiles ahead measured the same, 331 and 75.7 us against
+  // 329 and 74.5 with 16 trees of 64 rows and ragged ones of D = 64.)
   __device__ __forceinline__ void fetch(const Segment &seg, int i) {
     if (i < seg.count) {
       const int j = i - looked;
@@ -672,7 +685,7 @@ struct Softmax {
   const uint32_t lanes, ts, to;  // TMEM addresses of the warp's S and O
   const Issuer<D> issue;
   const bool issues = (threadIdx.x & 127) < 32;
-  uint32_t scored = 0, ended = 0, meetings = 0, asked = 0;  // phases of s_full (and p_full), o_full, met; bit y: of q_full[y]
+  uint32_t scored = 0, ended = 0, meetings = 0, asked = 0;  // phases of s_full and p_full, o_full, met; bit y: of q_full[y]
 
   __device__ __forceinline__ Softmax(const TileArgs &args, S &smem, uint32_t tmem)
       : a(args), sm(smem), lanes(uint32_t((threadIdx.x >> 5 & 3) * 32) << 16), ts(tmem + lanes + x * kKeys),
@@ -813,8 +826,8 @@ struct Softmax {
   }
 
   // The row's result: 32 dimensions from `first` on, whole or as a part (four dimensions of all rows, then the next four).
-  __device__ __forceinline__ void store_out(const Segment &seg, float *part, int part_row, int token, int head, int first, float inv,
-                                            const float (&v)[32]) const {
+  __device__ __forceinline__ void store_out(const Segment &seg, float *part, int part_row, int token, int head, int first,
+                                            float inv, const float (&v)[32]) const {
     if (part) {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -908,9 +921,10 @@ struct Softmax {
         }
         scale_accumulators(f);
       }
-      // P = 2^(s - ref) in f16, with what the values' scales lie below the accumulators', and the sum without that. A loop: its
-      // code has to share the instruction cache with the decoders' (with four times 32 exponentials one after another, twice, and four
-      // copies of the decoding the warps waited for instructions a third of the time: 16 trees of 64 rows 520 us).
+      // P = 2^(s - ref) in f16, with what the values' scales lie below the accumulators', and the sum without that. A
+      // loop: its code has to share the instruction cache with the decoders' (with four times 32 exponentials one after
+      // another, twice, and four copies of the decoding the warps waited for instructions a third of the time: 16 trees
+      // of 64 rows 520 us).
 #pragma unroll 1
       for (int c = 0; c < 4; c += 2) {
         if (c) {
@@ -1093,9 +1107,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
 }
 
 // ------------------------------------------------------------------ joining the blocks
-// Block c joins the item whose first tile is the main kernel's block c's, if later blocks have tiles of it too. What there is
-// to join the main kernel has left: the blocks without work, most of them, end at once (with the list of work looked through
-// again by each block the joins took 10 to 23 us).
+// Block c joins the item whose first tile is the main kernel's block c's, if later blocks have tiles of it too. What
+// there is to join the main kernel has left: the blocks without work, most of them, end at once (with the list of work
+// looked through again by each block the joins took 10 to 23 us).
 
 template <int D>
 constexpr int kJoinRows = kJoinThreads / (D / 4);  // rows at a time: a thread has four dimensions of one
@@ -1177,8 +1191,8 @@ cudaError_t launch(const TileArgs &a, int usual_rows, int num_sms, cudaStream_t 
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  // As many blocks of an item as the usual rows need. (With fewer, each with several runs of rows, 16 trees of 64 rows took 324
-  // and 327 us in place of 321, 24 ragged ones 72 and 81 in place of 70.)
+  // As many blocks of an item as the usual rows need. (With fewer, each with several runs of rows, 16 trees of 64 rows
+  // took 324 and 327 us in place of 321, 24 ragged ones 72 and 81 in place of 70.)
   const int most = usual_rows < 2 * kRows ? usual_rows : 2 * kRows;
   cfg.gridDim = dim3(grid, unsigned((most + kJoinRows<D> - 1) / kJoinRows<D>));
   cfg.blockDim = dim3(kJoinThreads);
