@@ -18,7 +18,7 @@
 // pass over the vocabulary that ends in a barrier. A cluster of blocks takes a sequence, and each block a part of the
 // vocabulary.
 //   Measured (131,072 tokens, device time in a graph): one chain of six in bf16 12.5 us, of a single row 6; 64 chains of
-// six with a draft, fp32, 65 us, of single rows 11 to 15; 16 trees of 64 rows 21.6; 24 of up to 16 rows with a draft over
+// six with a draft, fp32, 68 us (65 without the differences' low parts), of single rows 11 to 15; 16 trees of 64 rows 21.6; 24 of up to 16 rows with a draft over
 // 50,021 tokens 35. Issue slots are 20 to 30 % busy, HBM 4 to 23 %: rows one after another, each a chain of latencies.
 //
 // Layout. A block's warps have consecutive parts of its part, in units of 8 tokens, a unit a lane. What every warp finds
@@ -76,6 +76,12 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 
 __device__ __forceinline__ bool less(Two a, Two b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
 
+// a - b in two, without an error.
+__device__ __forceinline__ Two minus(float a, float b) {
+  const float s = a - b, c = s - a;
+  return {s, (a - (s - c)) - (b + c)};
+}
+
 __device__ __forceinline__ Two times(Two a, float f) {
   const float p = a.hi * f, e = fmaf(a.hi, f, -p) + a.lo * f, hi = p + e;
   return {hi, e - (hi - p)};
@@ -96,11 +102,11 @@ __device__ __forceinline__ Two exponent_unit(float t) {
 
 // 2^(d c) for d <= 0. With y = d c = n + k/32 + r, |r| <= 1/64: 2^y = 2^n 2^(k/32) (1 + z), z = 2^r - 1 by its series, the
 // first term in two. Below 2^-126: 0.
-__device__ __forceinline__ Two power(float d, Two c, const float2 *powers) {
+__device__ __forceinline__ Two power(Two d, Two c, const float2 *powers) {
   constexpr float kHi = 0.693147182f, kLo = float(0.69314718055994530942 - double(0.693147182f));  // ln 2
   constexpr float k2 = 0.240226507f, k3 = 0.0555041087f, k4 = 0.00961812911f;                      // ln 2^i / i!
   constexpr float kRound = 12582912.0f;                                                           // 1.5 2^23
-  const float yh = d * c.hi, yl = fmaf(d, c.lo, fmaf(d, c.hi, -yh));
+  const float yh = d.hi * c.hi, yl = fmaf(d.lo, c.hi, fmaf(d.hi, c.lo, fmaf(d.hi, c.hi, -yh)));
   const float at = fmaf(yh, 32.0f, kRound), r = fmaf(at - kRound, -0x1p-5f, yh);
   const int i = __float_as_int(at) - 0x4B400000;
   const float2 p = powers[i & 31];
@@ -117,11 +123,11 @@ __device__ __forceinline__ Two power(float d, Two c, const float2 *powers) {
 // The same in one binary32: 2^-23 relative, from roundings without a common sign (the series leaves 2^-28 off at its
 // ends, 2^-31 on the whole). d >= -126 / c. With y = n - g: n from y's rounding, g exact but for one rounding. (Two at a
 // time with the packed instructions took more, for the constants, which those cannot take from the instruction.)
-__device__ __forceinline__ float power_short(float d, Two c) {
+__device__ __forceinline__ float power_short(float d, float lo, Two c) {
   constexpr float k1 = 0.693147182f, k2 = 0.240226507f, k3 = 0.0555041087f, k4 = 0.00961812911f, k5 = 0.00133335581f,
                   k6 = 0.000154035304f, k7 = 1.52527338e-05f;  // ln 2^i / i!
   const float at = fmaf(d, c.hi, 12582912.0f);  // 1.5 2^23 + n
-  const float f = fmaf(d, c.lo, fmaf(d, c.hi, 12582912.0f - at));
+  const float f = fmaf(lo, c.hi, fmaf(d, c.lo, fmaf(d, c.hi, 12582912.0f - at)));
   const float q = fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, k7, k6), k5), k4), k3), k2), k1);
   return fmaf(f, q, 1.0f) * __int_as_float((__float_as_int(at) << 23) + 0x3F800000);  // the low bits of `at` into the exponent
 }
@@ -386,7 +392,11 @@ struct Walker {
   // The weights of 8 tokens in one binary32; the large ones as a mask, and 0 in their place. Whole warp.
   __device__ __forceinline__ uint32_t weights_short(const float (&x)[kUnit], float top, float (&w)[kUnit]) const {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) w[i] = power_short(fmaxf(x[i] - top, least), unit);
+    for (int i = 0; i < kUnit; ++i) {
+      // 32-bit logits: the difference's rounding would be 2^-20 of a small weight
+      const Two d = sizeof(E) == 4 ? minus(x[i], top) : Two{x[i] - top, 0.0f};
+      w[i] = power_short(fmaxf(d.hi, least), d.hi > least ? d.lo : 0.0f, unit);
+    }
     uint32_t large = 0;
     const float most = fmaxf(fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])), fmaxf(fmaxf(w[4], w[5]), fmaxf(w[6], w[7])));
     if (__any_sync(0xFFFFFFFFu, most > kShort)) {
@@ -418,7 +428,7 @@ struct Walker {
         if (i == j) xi = x[j];
         if (i == j) qi = q[j];
       }
-      const Two w = left_long(power(xi - top, unit, sm.powers), qi, taken);
+      const Two w = left_long(power(minus(xi, top), unit, sm.powers), qi, taken);
       if (large) f(i, w);
       large &= large - 1;
     }
@@ -441,7 +451,7 @@ struct Walker {
     const bool drafted = DRAFT && taken.hi != 0.0f;
     int kept = 0;        // large weights that wait
     const auto long_sum = [&](float2 l) {
-      const Two w = power(l.x - top, unit, sm.powers), r = left_long(w, l.y, taken);
+      const Two w = power(minus(l.x, top), unit, sm.powers), r = left_long(w, l.y, taken);
       s = add(s, r.hi, r.lo);
       if (DRAFT && fresh) {
         all = add(all, w.hi, w.lo);

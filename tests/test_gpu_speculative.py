@@ -91,6 +91,40 @@ def check_verify(s, out):
     return close
 
 
+@pytest.mark.parametrize("drafted", [False, True], ids=["alone", "behind_a_rejection"])
+@pytest.mark.parametrize("V", [300, 20000])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_new_token_next_to_borders(dtype, V, drafted):
+    """The random numbers lie next to borders between tokens, as close as their 24 bits allow, mostly 2^-26 to 2^-30 of the
+    whole. What the sums are off by is about 2^-34: those closer than 2^-31 are moved on by a step."""
+    B, rng = 96, np.random.default_rng(V + len(dtype))
+    n = 2 if drafted else 1
+    logits = torch.from_numpy(3.0 * rng.standard_normal((B * n, V))).to(TYPES[dtype])
+    if drafted:
+        logits[0::2, 0] = -40.0  # the child's token: sure to be rejected
+    exact = logits.double().numpy()[::n]
+    draft = rng.random((B * n, V)).astype(np.float32) ** 4
+    draft[:, 0] = draft.sum(1)
+    draft /= draft.sum(1, keepdims=True)
+    temperature = rng.uniform(0.7, 1.3, B).astype(np.float32)
+    u, want = np.zeros(B, dtype=np.float32), np.zeros(B, dtype=np.int32)
+    for b in range(B):
+        p = osp.softmax(exact[b], float(temperature[b]))
+        left = np.maximum(p - draft[2 * b].astype(np.float64), 0) if drafted else p
+        sums = np.cumsum(left) / left.sum()
+        u[b] = np.float32(sums[np.argmin(np.abs(sums - rng.uniform(0.1, 0.9)))])
+        while np.abs(sums - float(u[b])).min() < 2.0 ** -31:
+            u[b] = np.nextafter(u[b], np.float32(1))
+        want[b] = np.flatnonzero((sums > float(u[b])) & (left > 0))[0]
+    st, dev = status(), lambda a: torch.from_numpy(a).cuda()
+    got = speculative.verify_drafts(logits.cuda(), torch.zeros(B * n, dtype=torch.int32, device="cuda"),
+                                    ac.i32([n * b for b in range(B + 1)]), torch.full((B * n,), 0.9, device="cuda"), dev(u),
+                                    draft_probs=dev(draft) if drafted else None, temperature=dev(temperature), max_rows=n,
+                                    d_status=st)
+    assert st.item() == abi.MOE_OK and not got["accepted"].any()
+    assert np.array_equal(got["tokens"][:, 0].cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("drafted", [False, True])
 @pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 1000, 4099, 33333])
