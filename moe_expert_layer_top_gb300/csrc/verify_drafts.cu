@@ -23,14 +23,15 @@
 //
 // Layout. A block's warps have consecutive parts of its part, in units of 8 tokens, a unit a lane. What every warp finds
 // goes to a slot of its own in every block of the cluster (distributed shared memory), and every warp of every block
-// joins all slots in the same order: all hold the same numbers, and walk the tree alike without telling one another. The
-// slots lie in the order of the vocabulary, so they also say which warp's part holds the new token.
+// joins all slots in the same order (peak.h): all hold the same numbers, and walk the tree alike without telling one
+// another. The slots lie in the order of the vocabulary, so they also say which warp's part holds the new token.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <cmath>
 
 #include "attention.cuh"
+#include "peak.h"
 #include "speculative.h"
 
 namespace moe {
@@ -264,19 +265,6 @@ struct Smem {
 };
 constexpr int kNever = -2;
 
-// Largest logit (and the first token that has it), and the sum of 2^((x - max) c).
-struct Peak {
-  float top, sum;
-  int token;
-
-  __device__ __forceinline__ void join(const Peak &o, float c) {
-    const float t = fmaxf(top, o.top), ref = t == -INFINITY ? 0.0f : t;
-    sum = sum * exp2_approx((top - ref) * c) + o.sum * exp2_approx((o.top - ref) * c);
-    if (o.top > top || (o.top == top && o.token < token)) token = o.token;
-    top = t;
-  }
-};
-
 template <class E, bool DRAFT>
 struct Walker {
   const VerifyArgs &a;
@@ -297,8 +285,10 @@ struct Walker {
     end = min(units, begin + each);
   }
 
-  // This warp's value into its slot everywhere; then all slots are there.
+  // This warp's value (its first lane's: every block gets the same) into its slot everywhere; then all slots are there.
   __device__ __forceinline__ const float4 *exchange(float4 v) {
+    v = make_float4(__shfl_sync(0xFFFFFFFFu, v.x, 0), __shfl_sync(0xFFFFFFFFu, v.y, 0), __shfl_sync(0xFFFFFFFFu, v.z, 0),
+                    __shfl_sync(0xFFFFFFFFu, v.w, 0));
     float4 *slots = sm.slots[set];
     set ^= 1;
     if (lane < int(size)) store_remote(&slots[rank * kWarps + warp], lane, v);
@@ -306,6 +296,17 @@ struct Walker {
     return slots;
   }
 
+  // Joined over the warp's lanes; the first lane's result everywhere.
+  __device__ __forceinline__ Peak join_lanes(Peak k) const {
+#pragma unroll
+    for (int d = 16; d; d /= 2)
+      k.join({__shfl_xor_sync(0xFFFFFFFFu, k.top, d), __shfl_xor_sync(0xFFFFFFFFu, k.sum, d),
+              __shfl_xor_sync(0xFFFFFFFFu, k.token, d)},
+             unit.hi, exp2_approx);
+    return {__shfl_sync(0xFFFFFFFFu, k.top, 0), __shfl_sync(0xFFFFFFFFu, k.sum, 0), __shfl_sync(0xFFFFFFFFu, k.token, 0)};
+  }
+
+  // The same numbers on every thread of the cluster: the walk goes by them, and no thread may take another way.
   // behind: what else is to be done before all warps meet.
   template <class F>
   __device__ __forceinline__ Peak peak(const Row<E> &row, F behind) {
@@ -349,21 +350,13 @@ struct Walker {
         }
       }
     }
-#pragma unroll
-    for (int d = 16; d; d /= 2)
-      k.join({__shfl_xor_sync(0xFFFFFFFFu, k.top, d), __shfl_xor_sync(0xFFFFFFFFu, k.sum, d),
-              __shfl_xor_sync(0xFFFFFFFFu, k.token, d)},
-             c);
+    k = join_lanes(k);
     behind();
     const float4 *slots = exchange(make_float4(k.top, k.sum, __int_as_float(k.token), 0.0f));
     k = {-INFINITY, 0.0f, INT32_MAX};
-    for (int i = lane; i < int(size) * kWarps; i += 32) k.join({slots[i].x, slots[i].y, __float_as_int(slots[i].z)}, c);
-#pragma unroll
-    for (int d = 16; d; d /= 2)
-      k.join({__shfl_xor_sync(0xFFFFFFFFu, k.top, d), __shfl_xor_sync(0xFFFFFFFFu, k.sum, d),
-              __shfl_xor_sync(0xFFFFFFFFu, k.token, d)},
-             c);
-    return k;
+    for (int i = lane; i < int(size) * kWarps; i += 32)
+      k.join({slots[i].x, slots[i].y, __float_as_int(slots[i].z)}, c, exp2_approx);
+    return join_lanes(k);
   }
 
   // What is left of a weight less taken q: nothing below 0.
@@ -538,7 +531,7 @@ struct Walker {
 #pragma unroll
     for (int d = 16; d; d /= 2)
       s = add(s, Two{__shfl_xor_sync(0xFFFFFFFFu, s.hi, d), __shfl_xor_sync(0xFFFFFFFFu, s.lo, d)});
-    return s;
+    return from_lane(s, 0);
   }
 
   static __device__ __forceinline__ Two scan(Two s, int lane) {  // inclusive

@@ -1,0 +1,98 @@
+"""Verification of drafted tokens where a step could go wrong in a few calls of a million: random numbers on the borders
+of the decisions, and residuals that lie in a few places of the vocabulary.
+
+On the border of a decision either answer is right, but all threads of the cluster have to give the same: what they write
+then fits one walk."""
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_layer_top_gb300 import abi, speculative
+from oracle import speculative as osp
+
+import attention_cases as ac
+from tree_cases import status
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+CHOICE = 2.0 ** -34
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import moe_expert_layer_top_gb300.build as b
+    b.build()
+    abi.load()
+    assert torch.cuda.is_available()
+
+
+def chains(rng, B, n, V, dtype, drafted):
+    """B chains of n rows; the children are likely tokens. Logits on the device, in 64 bits, the draft, the tokens."""
+    logits = torch.from_numpy(2.0 * rng.standard_normal((B * n, V))).to(TYPES[dtype])
+    for r in range(B * n):  # a few tokens hold much of the row
+        logits[r, torch.from_numpy(rng.choice(V, 5, replace=False))] += 9.0
+    exact = logits.double().numpy()
+    draft = None
+    if drafted:
+        d = exact + 0.5 * rng.standard_normal(exact.shape)
+        d = np.exp(d - d.max(1, keepdims=True))
+        draft = (d / d.sum(1, keepdims=True)).astype(np.float32)
+    tokens = np.zeros(B * n, np.int32)
+    for r in range(B * n):
+        if r % n:
+            tokens[r] = np.argsort(-exact[r - 1])[rng.integers(0, 4)]
+    return logits, exact, draft, tokens
+
+
+# sequences: clusters of 16, 8, 4 and 1 blocks
+@pytest.mark.parametrize("B", [3, 24, 96, 400])
+@pytest.mark.parametrize("drafted", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_one_walk_whatever_the_border_decides(dtype, drafted, B):
+    rng = np.random.default_rng(B + drafted)
+    n, V = (6, 33001) if B < 300 else (4, 5000)
+    logits, exact, draft, tokens = chains(rng, B, n, V, dtype, drafted)
+    device = [logits.cuda(), ac.dev(tokens), ac.i32([n * b for b in range(B + 1)])]
+    chance = np.zeros(B * n)
+    for r in range(B * n):
+        if r % n:
+            chance[r] = osp.accept_chance(osp.softmax(exact[r - 1], 1.0), None if draft is None else draft[r - 1].astype(np.float64),
+                                          [], tokens[r])
+    sample = rng.random(B).astype(np.float32)
+    kw = {"draft_probs": ac.dev(draft)} if drafted else {}
+    ways = np.zeros(n, int)
+    wants = {}  # the new token of (sequence, accepted), and how near it is to a border
+    for trial in range(12):
+        u = chance.astype(np.float32)
+        for _ in range(trial // 2):  # 0 to 5 steps above and below
+            u = np.nextafter(u, np.float32(0 if trial % 2 else 1))
+        sure = rng.random(B * n) < 0.5  # half of them are surely accepted, so that the walk gets further
+        u = np.where(sure & (chance > 1e-3), np.float32(0.0), u).astype(np.float32)
+        st = status()
+        args = (*device, ac.dev(u), ac.dev(sample))
+        out = speculative.verify_drafts(*args, **kw, max_rows=n, d_status=st)
+        again = speculative.verify_drafts(*args, **kw, max_rows=n)
+        assert st.item() == abi.MOE_OK and all(torch.equal(out[k], again[k]) for k in out)
+        said, accepted, path = (out[k].cpu().numpy() for k in ("tokens", "accepted", "path"))
+        for b in range(B):
+            a = int(accepted[b])
+            ways[a] += 1
+            r0 = n * b
+            for i in range(1, n):  # what is far from its border is decided
+                if abs(float(u[r0 + i]) - chance[r0 + i]) > 2.0 ** -20 and i <= a + 1:
+                    assert (u[r0 + i] < chance[r0 + i]) == (i <= a)
+            assert path[b].tolist() == list(range(a + 1)) + [-1] * (n - 1 - a)
+            assert said[b, :a].tolist() == tokens[r0 + 1:r0 + 1 + a].tolist() and (said[b, a + 1:] == -1).all()
+            if (b, a) not in wants:
+                row = r0 + a
+                rejected = [tokens[row + 1]] if a < n - 1 else []
+                p = osp.softmax(exact[row], 1.0)
+                left = osp.residual(p, None if draft is None else draft[row].astype(np.float64), rejected)
+                whole = left.sum()
+                sums = np.cumsum(left) / whole
+                edge = np.abs(sums - float(sample[b])).min() * whole  # as a part of p's whole
+                wants[b, a] = int(np.flatnonzero((sums > sample[b]) & (left > 0))[0]), edge
+            token, edge = wants[b, a]
+            assert edge < CHOICE or said[b, a] == token
+    assert B < 24 or (ways > 0).all()
