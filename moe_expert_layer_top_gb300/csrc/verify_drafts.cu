@@ -227,8 +227,11 @@ __device__ __forceinline__ void load_draft(const float *p, int e, int vocab, flo
 
 // ------------------------------------------------------------------ the cluster
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -671,6 +674,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
     }
     return;
   }
+  // No block may store into another one's shared memory before that one has begun: each says so here, and waits for the
+  // others in front of its first exchange, when the root's row has been read.
+  cluster_arrive();
   const int n = rows.n;
   // A row's logit and draft probability lie in its parent's row: they come while the root's row is read.
   static_assert(kThreads >= kMaxTree, "a thread for each row");
@@ -712,7 +718,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
     const Row<E> row(a.logits, a.logits_stride, rows.first + node, a.vocab);
     const float *draft = DRAFT ? a.draft + int64_t(rows.first + node) * a.draft_stride : nullptr;
     k = w.peak(row, [&] {
-      if (node == 0 && tid < n) sm.x[tid] = row_x, sm.q[tid] = row_q;
+      if (node != 0) return;  // once
+      if (tid < n) sm.x[tid] = row_x, sm.q[tid] = row_q;
+      cluster_wait();
     });
     valid = k.sum > 0.0f && k.sum < INFINITY && k.top > -INFINITY;
     if (!valid) break;

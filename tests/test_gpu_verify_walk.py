@@ -96,3 +96,22 @@ def test_one_walk_whatever_the_border_decides(dtype, drafted, B):
             token, edge = wants[b, a]
             assert edge < CHOICE or said[b, a] == token
     assert B < 24 or (ways > 0).all()
+
+
+@pytest.mark.parametrize("B, V", [(190, 4096), (97, 8200), (40, 16400), (14, 32800)])
+def test_short_rows_of_more_clusters_than_fit(B, V):
+    """Blocks whose part of a row is done at once, and clusters that begin behind others: the first values that blocks give
+    one another must not come before their receiver has begun. Calls one behind another, all with the same result."""
+    rng = np.random.default_rng(V)
+    logits, exact, _, tokens = chains(rng, B, 2, V, "bf16", False)
+    u, sample = rng.random(2 * B).astype(np.float32), rng.random(B).astype(np.float32)
+    args = (logits.cuda(), ac.dev(tokens), ac.i32([2 * b for b in range(B + 1)]), ac.dev(u), ac.dev(sample))
+    outs = [speculative.verify_drafts(*args, max_rows=2) for _ in range(60)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[k], outs[0][k]) for o in outs for k in o)
+    said, accepted = outs[0]["tokens"].cpu().numpy(), outs[0]["accepted"].cpu().numpy()
+    for b in range(B):
+        r = slice(2 * b, 2 * b + 2)
+        path, token, near, edge = osp.verify(exact[r], tokens[r], [-1, 0], u[r], sample[b])
+        assert near < 2.0 ** -20 or accepted[b] == len(path) - 1
+        assert near < 2.0 ** -20 or edge < CHOICE or said[b, accepted[b]] == token
