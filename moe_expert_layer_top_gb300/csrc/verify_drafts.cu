@@ -140,6 +140,11 @@ constexpr float kShort = 0x1p-13f;
 // either.
 constexpr float kNothing = 0x1p-100f;
 
+// With a draft: tokens of which less than this part of c q is left or missing are computed in two binary32 as well. In one
+// they would have the rounding of the weight, 2^-23 of it, cut off below 0: where the draft is nearly the target, all that
+// is left would be that (a part of 2^-26 of the weights, next to a true residual of any size).
+constexpr float kNear = 0x1p-18f;
+
 // ------------------------------------------------------------------ rows of the vocabulary
 
 __device__ __forceinline__ float value(const float *p) { return __ldg(p); }
@@ -262,7 +267,7 @@ struct Smem {
   int parent[kMaxTree];    // kNever: not asked
   int rejected[kMaxTree];  // tokens of the rejected children of the row
   int way[kMaxTree];       // accepted rows, the root first
-  float2 large[kWarps][32 * kUnit + 32];  // logits (and draft probabilities) of large weights, until there are 32
+  float2 large[kWarps][32 * kUnit + 32];  // logits (and draft probabilities) of weights to compute in two, until there are 32
   Two part[kWarps];        // sums of the warps where the new token is looked for, and what they found
   int found[kWarps];
 };
@@ -406,10 +411,28 @@ struct Walker {
     return large;
   }
 
-  // What is left of them less taken q.
-  static __device__ __forceinline__ void less_draft(Two taken, const float (&q)[kUnit], float (&w)[kUnit]) {
+  // What is left of them less taken q; those next to it as a mask, and 0 in their place, in w too. Whole warp.
+  static __device__ __forceinline__ uint32_t less_draft(Two taken, const float (&q)[kUnit], float (&w)[kUnit],
+                                                        float (&left)[kUnit]) {
+    const float near = taken.hi * kNear;
+    bool some = false;
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) w[i] = fmaxf(fmaf(-taken.lo, q[i], fmaf(-taken.hi, q[i], w[i])), 0.0f);
+    for (int i = 0; i < kUnit; ++i) {
+      left[i] = fmaf(-taken.lo, q[i], fmaf(-taken.hi, q[i], w[i]));
+      some |= fabsf(left[i]) < near * q[i];
+    }
+    uint32_t mask = 0;
+    if (__any_sync(0xFFFFFFFFu, some)) {
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i)
+        if (fabsf(left[i]) < near * q[i]) {
+          left[i] = w[i] = 0.0f;
+          mask |= 1u << i;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) left[i] = fmaxf(left[i], 0.0f);
+    return mask;
   }
 
   // f(i, what is left of token i) for the large ones of a unit. Whole warp; a lane's one after another.
@@ -437,93 +460,113 @@ struct Walker {
 
   // Sums of what is left with c = taken / (sum of all weights), or, without a draft, of all tokens but the rejected ones.
   // fresh (with a draft): c = 1, with a guess at the sum of all weights, which is computed in the same pass. The sums are
-  // corrected for what the guess was off by, d: what is left of w - guess q becomes less by d q, where it is positive (where it
-  // changes its sign, by d^2).
+  // corrected for what the guess was off by, d: what is left of w - guess q becomes less by d q, where it is positive.
+  // Where it changes its sign that is not so: these tokens are among those next to c q as long as d is within kNear, and
+  // if they are of any weight, the sums are computed again with the sum of all weights.
   __device__ __forceinline__ Sums sums(const Row<E> &row, const float *draft, float top, Two taken, bool fresh) {
     int begin, end;
     part(row, begin, end);
-    Two s = {0.0f, 0.0f}, all = {0.0f, 0.0f};
-    float share = 0.0f;  // the draft's probabilities where something is left
-    const bool drafted = DRAFT && taken.hi != 0.0f;
-    int kept = 0;        // large weights that wait
-    const auto long_sum = [&](float2 l) {
-      const Two w = power(minus(l.x, top), unit, sm.powers), r = left_long(w, l.y, taken);
-      s = add(s, r.hi, r.lo);
-      if (DRAFT && fresh) {
-        all = add(all, w.hi, w.lo);
-        if (r.hi > 0.0f) share += l.y;
-      }
-    };
-    float x[kUnit], q[kUnit] = {}, nq[kUnit] = {};  // of this unit, and the next
-    uint4 nx[Row<E>::kPieces];                      // logits of the next, as they come
-    const auto ask = [&](int u) {
-      if (u >= end) return;
-      if (row.whole(u, u + 1)) row.ask(u, nx);
-      if (drafted) load_draft(draft, row.first(u), row.vocab, nq);
-    };
-    const auto take = [&](int u) {
-      if (u >= end) {
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) x[i] = -INFINITY;
-      } else if (row.whole(u, u + 1)) {
-        row.take(nx, x);
-      } else {
-        load_cut(row.p, row.first(u), row.vocab, -INFINITY, x);
-      }
-    };
-    ask(begin + lane);
+    Two s, all = {0.0f, 0.0f};
 #pragma unroll 1
-    for (int u0 = begin; u0 < end; u0 += 32) {
-      const int u = u0 + lane;
-      take(u);
+    while (true) {
+      s = {0.0f, 0.0f};
+      float share = 0.0f;  // the draft's probabilities where something is left
+      float close = 0.0f;  // and next to c q
+      const bool drafted = DRAFT && taken.hi != 0.0f;
+      int kept = 0;        // weights that wait to be computed in two
+      const auto long_sum = [&](float2 l) {
+        const Two w = power(minus(l.x, top), unit, sm.powers), r = left_long(w, l.y, taken);
+        s = add(s, r.hi, r.lo);
+        if (DRAFT && fresh) {
+          all = add(all, w.hi, w.lo);
+          if (r.hi > 0.0f) share += l.y;
+          if (fabsf(fmaf(-taken.hi, l.y, w.hi)) < taken.hi * kNear * l.y) close += l.y;
+        }
+      };
+      float x[kUnit], q[kUnit] = {}, nq[kUnit] = {};  // of this unit, and the next
+      uint4 nx[Row<E>::kPieces];                      // logits of the next, as they come
+      const auto ask = [&](int u) {
+        if (u >= end) return;
+        if (row.whole(u, u + 1)) row.ask(u, nx);
+        if (drafted) load_draft(draft, row.first(u), row.vocab, nq);
+      };
+      const auto take = [&](int u) {
+        if (u >= end) {
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) q[i] = nq[i];
-      ask(u + 32);
-      if (!DRAFT) reject(row.first(u), x);
-      float w[kUnit];
-      const uint32_t large = weights_short(x, top, w);
-      if (DRAFT && fresh) {
-        all = add(all, (w[0] + w[1]) + (w[2] + w[3]), 0.0f);
-        all = add(all, (w[4] + w[5]) + (w[6] + w[7]), 0.0f);
-      }
-      if (drafted) {
-        less_draft(taken, q, w);
-        if (fresh) {
+          for (int i = 0; i < kUnit; ++i) x[i] = -INFINITY;
+        } else if (row.whole(u, u + 1)) {
+          row.take(nx, x);
+        } else {
+          load_cut(row.p, row.first(u), row.vocab, -INFINITY, x);
+        }
+      };
+      ask(begin + lane);
+#pragma unroll 1
+      for (int u0 = begin; u0 < end; u0 += 32) {
+        const int u = u0 + lane;
+        take(u);
 #pragma unroll
-          for (int i = 0; i < kUnit; ++i) share += w[i] > 0.0f ? q[i] : 0.0f;
+        for (int i = 0; i < kUnit; ++i) q[i] = nq[i];
+        ask(u + 32);
+        if (!DRAFT) reject(row.first(u), x);
+        float w[kUnit], left[kUnit];
+        uint32_t longer = weights_short(x, top, w);
+        if (drafted) {
+          longer |= less_draft(taken, q, w, left);
+          if (fresh) {
+            all = add(all, (w[0] + w[1]) + (w[2] + w[3]), 0.0f);
+            all = add(all, (w[4] + w[5]) + (w[6] + w[7]), 0.0f);
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) share += left[i] > 0.0f ? q[i] : 0.0f;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) left[i] = w[i];
+        }
+        s = add(s, (left[0] + left[1]) + (left[2] + left[3]), 0.0f);
+        s = add(s, (left[4] + left[5]) + (left[6] + left[7]), 0.0f);
+        if (__any_sync(0xFFFFFFFFu, longer != 0)) {  // 32 of them at a time
+          const int mine = __popc(longer);
+          int at = kept + warp_inclusive_sum(mine) - mine;
+          kept = __shfl_sync(0xFFFFFFFFu, at + mine, 31);
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i)
+            if (longer >> i & 1) sm.large[warp][at++] = make_float2(x[i], q[i]);
+          __syncwarp();
+#pragma unroll 1
+          for (; kept >= 32; kept -= 32) long_sum(sm.large[warp][kept - 32 + lane]);
+          __syncwarp();
         }
       }
-      s = add(s, (w[0] + w[1]) + (w[2] + w[3]), 0.0f);
-      s = add(s, (w[4] + w[5]) + (w[6] + w[7]), 0.0f);
-      if (__any_sync(0xFFFFFFFFu, large != 0)) {  // 32 of them at a time
-        const int mine = __popc(large);
-        int at = kept + warp_inclusive_sum(mine) - mine;
-        kept = __shfl_sync(0xFFFFFFFFu, at + mine, 31);
+      if (lane < kept) long_sum(sm.large[warp][lane]);
+      s = add(s, Two{0.0f, 0.0f});
+      all = add(all, Two{0.0f, 0.0f});
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i)
-          if (large >> i & 1) sm.large[warp][at++] = make_float2(x[i], q[i]);
-        __syncwarp();
-#pragma unroll 1
-        for (; kept >= 32; kept -= 32) long_sum(sm.large[warp][kept - 32 + lane]);
-        __syncwarp();
+      for (int d = 16; d; d /= 2) {
+        s = add(s, Two{__shfl_xor_sync(0xFFFFFFFFu, s.hi, d), __shfl_xor_sync(0xFFFFFFFFu, s.lo, d)});
+        if (DRAFT && fresh) {
+          all = add(all, Two{__shfl_xor_sync(0xFFFFFFFFu, all.hi, d), __shfl_xor_sync(0xFFFFFFFFu, all.lo, d)});
+          share += __shfl_xor_sync(0xFFFFFFFFu, share, d);
+          close += __shfl_xor_sync(0xFFFFFFFFu, close, d);
+        }
       }
-    }
-    if (lane < kept) long_sum(sm.large[warp][lane]);
-    s = add(s, Two{0.0f, 0.0f});
-    all = add(all, Two{0.0f, 0.0f});
+      if (!DRAFT || !fresh) break;
+      const float4 *const slots = exchange(make_float4(all.hi, all.lo, close, 0.0f));
+      all = whole(slots);
+      close = 0.0f;
+      for (int i = lane; i < int(size) * kWarps; i += 32) close += slots[i].z;
 #pragma unroll
-    for (int d = 16; d; d /= 2) {
-      s = add(s, Two{__shfl_xor_sync(0xFFFFFFFFu, s.hi, d), __shfl_xor_sync(0xFFFFFFFFu, s.lo, d)});
-      if (DRAFT && fresh) {
-        all = add(all, Two{__shfl_xor_sync(0xFFFFFFFFu, all.hi, d), __shfl_xor_sync(0xFFFFFFFFu, all.lo, d)});
-        share += __shfl_xor_sync(0xFFFFFFFFu, share, d);
+      for (int d = 16; d; d /= 2) close += __shfl_xor_sync(0xFFFFFFFFu, close, d);
+      close = __shfl_sync(0xFFFFFFFFu, close, 0);
+      const float off = (all.hi - taken.hi) + all.lo;
+      if (close <= 0x1p-14f && fabsf(off) <= taken.hi * (kNear / 2)) {
+        s = add(s, Two{-off * share, 0.0f});
+        if (s.hi < 0.0f) s = {0.0f, 0.0f};
+        break;
       }
+      taken = all;
+      fresh = false;
     }
-    if (!DRAFT || !fresh) return {exchange(make_float4(s.hi, s.lo, 0.0f, 0.0f)), all};
-    all = whole(exchange(make_float4(all.hi, all.lo, 0.0f, 0.0f)));
-    const float off = (all.hi - taken.hi) + all.lo;
-    s = add(s, Two{-off * share, 0.0f});
-    if (s.hi < 0.0f) s = {0.0f, 0.0f};
     return {exchange(make_float4(s.hi, s.lo, 0.0f, 0.0f)), all};
   }
 
@@ -606,8 +649,13 @@ struct Walker {
         for (int i = 0; i < kUnit; ++i) x[i] = -INFINITY;
       }
       if (!DRAFT) reject(row.first(at), x);
-      const uint32_t large = weights_short(x, top, v);
-      if (DRAFT && taken.hi != 0.0f) less_draft(taken, q, v);
+      uint32_t large = weights_short(x, top, v);
+      if (DRAFT && taken.hi != 0.0f) {
+        float left[kUnit];
+        large |= less_draft(taken, q, v, left);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) v[i] = left[i];
+      }
       Two w[kUnit], s = {0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) w[i] = {v[i], 0.0f};

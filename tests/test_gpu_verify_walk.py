@@ -115,3 +115,44 @@ def test_short_rows_of_more_clusters_than_fit(B, V):
         path, token, near, edge = osp.verify(exact[r], tokens[r], [-1, 0], u[r], sample[b])
         assert near < 2.0 ** -20 or accepted[b] == len(path) - 1
         assert near < 2.0 ** -20 or edge < CHOICE or said[b, accepted[b]] == token
+
+
+# sequences: clusters of 16 and of 4 blocks
+@pytest.mark.parametrize("B", [3, 96])
+@pytest.mark.parametrize("moved", [0.05, 2.0 ** -10])
+@pytest.mark.parametrize("end", ["front", "back"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_residual_in_one_end_of_the_vocabulary(dtype, end, moved, B):
+    """The draft is the target's own distribution but for a part of it that lies in the other end: what is left of nearly
+    all tokens is next to nothing, and an error in c or a rounding of their weights, added up, would move every border.
+
+    The sums have an error of about 2^-34 of p's whole: random numbers closer than 2^-32 of it to a border do not count."""
+    V, rng = 33001, np.random.default_rng(B)
+    logits = torch.from_numpy(2.0 * rng.standard_normal((2 * B, V))).to(TYPES[dtype])
+    exact = logits.double().numpy()
+    draft = np.zeros((2 * B, V), np.float32)
+    sample, want = np.zeros(B, np.float32), np.zeros(B, np.int32)
+    tokens = np.zeros(2 * B, np.int32)
+    few = V // 16
+    for b in range(B):
+        p = osp.softmax(exact[2 * b], 1.0)
+        less, more = (slice(0, few), slice(V - few, V)) if end == "front" else (slice(V - few, V), slice(0, few))
+        q = p.copy()
+        part = min(moved, 0.9 * p[less].sum())
+        q[less] *= 1 - part / p[less].sum()
+        q[more] *= 1 + part / p[more].sum()
+        draft[2 * b] = q.astype(np.float32)
+        tokens[2 * b + 1] = more.start + int(np.argmax(p[more]))  # rejected by a number of 1
+        left = np.maximum(p - draft[2 * b].astype(np.float64), 0.0)
+        N = left.sum()
+        sums = np.cumsum(left) / N
+        sample[b] = np.float32(sums[np.argmin(np.abs(sums - rng.uniform(0.05, 0.95)))])
+        while np.abs(sums - float(sample[b])).min() * N < 2.0 ** -32:
+            sample[b] = np.nextafter(sample[b], np.float32(1))
+        want[b] = np.flatnonzero((sums > float(sample[b])) & (left > 0))[0]
+    st = status()
+    out = speculative.verify_drafts(logits.cuda(), ac.dev(tokens), ac.i32([2 * b for b in range(B + 1)]),
+                                    torch.ones(2 * B, device="cuda"), ac.dev(sample), draft_probs=ac.dev(draft), max_rows=2,
+                                    d_status=st)
+    assert st.item() == abi.MOE_OK and not out["accepted"].any()
+    assert np.array_equal(out["tokens"][:, 0].cpu().numpy(), want)
