@@ -637,7 +637,8 @@ typedef struct moe_verify_drafts_io {
  *   at temperature 0: child y is accepted if it is the first largest logit's.
  * The walk goes on from the accepted child. Where none is accepted, the new
  * token is the first t at which the sum of what is left up to t exceeds
- * sample_u times the whole (p itself, if nothing is left).
+ * sample_u times the whole (p itself, if nothing is left, or of p less a draft
+ * not 2^-30).
  * Only the rows on the way are read. Decisions are made in binary32 from sums
  * of relative error 2^-20; the sums that choose the new token have an error
  * of about 2^-34 of the whole, and below 2^-30 even where nearly all of it lies

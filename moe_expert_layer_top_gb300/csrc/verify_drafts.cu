@@ -144,6 +144,8 @@ constexpr float kNothing = 0x1p-100f;
 // they would have the rounding of the weight, 2^-23 of it, cut off below 0: where the draft is nearly the target, all that
 // is left would be that (a part of 2^-26 of the weights, next to a true residual of any size).
 constexpr float kNear = 0x1p-18f;
+// What is left behind rejections of less than this part of all weights is nothing: it is of the size of the sums' errors.
+constexpr float kRest = 0x1p-30f;
 
 // ------------------------------------------------------------------ rows of the vocabulary
 
@@ -594,11 +596,12 @@ struct Walker {
   }
 
   // The new token, on one thread of the block that has it; -1 elsewhere. any: whether there was anything to choose from.
-  // fresh: see sums().
-  __device__ int choose(const Row<E> &row, const float *draft, float top, Two taken, bool fresh, float u, bool &any) {
+  // weights: their sum, where something is taken; fresh (it is not known yet): see sums().
+  __device__ int choose(const Row<E> &row, const float *draft, float top, Two taken, Two weights, bool fresh, float u,
+                        bool &any) {
     const Sums found_sums = sums(row, draft, top, taken, fresh);
     const float4 *slots = found_sums.slots;
-    if (DRAFT && fresh) taken = found_sums.all;
+    if (DRAFT && fresh) taken = weights = found_sums.all;
     // running sums over the slots, consecutive ones a lane
     constexpr int kPerLane = (kMaxCluster * kWarps + 31) / 32;
     const int n = int(size) * kWarps, per = (n + 31) / 32;
@@ -611,7 +614,7 @@ struct Walker {
       upto[j] = j ? add(upto[j - 1], slot[j]) : slot[j];
     }
     const Two to_lane = scan(upto[kPerLane - 1], lane), all = from_lane(to_lane, 31);
-    any = all.hi > kNothing;
+    any = all.hi > (DRAFT && taken.hi != 0.0f ? fmaxf(kNothing, kRest * weights.hi) : kNothing);
     if (!any) return -1;
     const Two border = times(all, fminf(fmaxf(u, 0.0f), 1.0f));
     // the first slot whose running sum exceeds the border; by a rounding, or with u = 1, there may be none: the last that has
@@ -835,8 +838,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
     }
     if (tid == 0) {
       a.accepted[b] = accepted;
-      if (!valid) out[accepted] = -1;
-      if (valid && greedy) out[accepted] = k.token;
+      // Also where one is to be chosen: should the sums find a place and the tokens there, by their rounding, none, it
+      // stays. The block that finds one writes it behind the cluster's barriers, and so after this.
+      out[accepted] = valid ? k.token : -1;
     }
   }
   if (!valid || greedy) return;
@@ -847,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
   int token = -1;
 #pragma unroll 1
   for (int again = 0; again < 2 && !any; ++again) {
-    token = w.choose(row, draft, k.top, taken, DRAFT && taken.hi != 0.0f && all.hi == 0.0f, u, any);
+    token = w.choose(row, draft, k.top, taken, all, DRAFT && taken.hi != 0.0f && all.hi == 0.0f, u, any);
     w.count = 0;  // if nothing is left: the target's own probabilities
     taken = {0.0f, 0.0f};
   }

@@ -156,3 +156,61 @@ def test_residual_in_one_end_of_the_vocabulary(dtype, end, moved, B):
                                     d_status=st)
     assert st.item() == abi.MOE_OK and not out["accepted"].any()
     assert np.array_equal(out["tokens"][:, 0].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("B", [3, 96])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["rounded", "softmax", "exact"])
+def test_draft_equal_to_the_target(kind, dtype, B):
+    """What is left behind a rejection is the draft's rounding, or nothing: 2^-26 of the whole where each probability is
+    rounded, about 2^-22 where they come of a softmax in binary32, 0 where they are p to the last bit. Every sequence gets a
+    token, the formula's where the random number is not next to a border."""
+    V, rng = 33001, np.random.default_rng(B)
+    if kind == "exact":  # powers of two, so that p is exact in binary32
+        x = np.full((2 * B, V), -np.inf)
+        for r in range(2 * B):
+            x[r, rng.choice(V, 5, replace=False)] = np.log(np.array([8, 4, 2, 1, 1.0]))
+        logits = torch.from_numpy(np.where(np.isneginf(x), -np.inf, np.round(x / np.log(2)))).to(TYPES[dtype])
+        t = float(np.float32(1 / np.log(2)))
+    else:
+        logits, t = torch.from_numpy(2.0 * rng.standard_normal((2 * B, V))).to(TYPES[dtype]), 1.0
+    exact = logits.double().numpy()
+    if kind == "softmax":
+        draft = torch.softmax(logits.float(), -1).numpy()
+    else:
+        draft = np.stack([osp.softmax(e, t) for e in exact]).astype(np.float32)
+    sample = rng.random(B).astype(np.float32)
+    tokens = np.zeros(2 * B, np.int32)
+    tokens[1::2] = exact[::2].argmax(1)
+    lo, u, temp = logits.cuda(), torch.ones(2 * B, device="cuda"), torch.full((B,), t, device="cuda")
+    out = [torch.full((B, 2), -77, dtype=torch.int32, device="cuda") for _ in range(2)]
+    accepted, st = torch.full((B,), -77, dtype=torch.int32, device="cuda"), status()
+    held = (lo, ac.dev(draft), ac.dev(tokens), ac.i32([2 * b for b in range(B + 1)]), temp, u, ac.dev(sample))
+    io = abi.MoeVerifyDraftsIO(held[0].data_ptr(), V, held[1].data_ptr(), V, held[2].data_ptr(), None, held[3].data_ptr(),
+                               held[4].data_ptr(), held[5].data_ptr(), held[6].data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
+                               accepted.data_ptr(), B, 2 * B, 2, V, {"bf16": abi.MOE_DTYPE_BF16, "fp32": abi.MOE_DTYPE_F32}[dtype], 0)
+    assert abi.moe_verify_drafts(io, st, torch.cuda.current_stream()) == abi.MOE_OK
+    torch.cuda.synchronize()
+    assert st.item() == abi.MOE_OK
+    said = out[0].cpu().numpy()
+    assert ((said[:, 0] >= 0) & (said[:, 0] < V)).all() and not (said == -77).any() and not (out[1] == -77).any()
+    away = 0
+    for b in range(B):
+        p = osp.softmax(exact[2 * b], t)
+        assert p[said[b, 0]] > 0
+        path, token, near, edge = osp.verify(exact[2 * b:2 * b + 2], tokens[2 * b:2 * b + 2], [-1, 0], [1.0, 1.0], sample[b], t,
+                                             draft[2 * b:2 * b + 2])
+        if accepted[b]:  # the child's own rounding is above its p: accepted as surely as the number is 1
+            assert near < 2.0 ** -20
+            continue
+        N = np.maximum(p - draft[2 * b].astype(np.float64), 0).sum()
+        nothing = N < 2.0 ** -31
+        if nothing:  # by the formula a residue of the 64-bit softmax; for the call nothing: p's own choice
+            sums = np.cumsum(p)
+            token, edge = int(np.flatnonzero(sums > sample[b])[0]), np.abs(sums - float(sample[b])).min()
+        elif N < 2.0 ** -29:
+            continue
+        if edge * (1.0 if nothing else N) > 2.0 ** -32:
+            away += 1
+            assert said[b, 0] == token
+    assert away > 0 or kind == "rounded"
