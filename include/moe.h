@@ -639,10 +639,11 @@ typedef struct moe_verify_drafts_io {
  * token is the first t at which the sum of what is left up to t exceeds
  * sample_u times the whole (p itself, if nothing is left, or of p less a draft
  * not 2^-30).
- * Only the rows on the way are read. Decisions are made in binary32 from sums
- * of relative error 2^-20; the sums that choose the new token have an error
- * of about 2^-34 of the whole, and below 2^-30 even where nearly all of it lies
- * in tokens below 2^-13 of the largest, so it is the formula's but for numbers
+ * Only the rows on the way are read. Decisions compare numbers of relative error
+ * 2^-20 (what is left of p less a draft: and 2^-34 of p's whole). The sums that
+ * choose the new token have an error of about 2^-34 of p's whole; where much of it
+ * lies in tokens below 2^-13 of the largest 2^-30, and up to 2^-25 where these
+ * have one logit in common. So they are the formula's but for numbers
  * that close to a border. Weights below 2^-100 of the largest count as none.
  * The same call gives the same result. A row on the way whose logits hold a NaN
  * or +inf, or nothing but -inf, has no distribution: its children are rejected

@@ -9,7 +9,8 @@
 // minus what was taken off. The new token is the first whose running sum exceeds u times the whole.
 //
 // Accuracy. A decision compares numbers of relative error 2^-20: it is the formula's unless u lies that close to the
-// border. The new token has a border for each token: with 2^17 tokens sums off by 2^-24 of the whole (one rounding of a
+// border. To keep that behind rejections, where both sides are what is left of larger numbers, the child's weight and the
+// sums are held in two binary32. The new token has a border for each token: with 2^17 tokens sums off by 2^-24 of the whole (one rounding of a
 // large weight) would give another token once in some hundred draws. So the weights that a token is chosen from are
 // computed in two binary32 each where they are large (a table of 2^(k/32) and a polynomial, about 2^-36 relative), in one
 // without a bias where they are not, and their sums are kept in two; binary64 runs at a hundredth of the rate here.
@@ -102,7 +103,7 @@ __device__ __forceinline__ Two exponent_unit(float t) {
 }
 
 // 2^(d c) for d <= 0. With y = d c = n + k/32 + r, |r| <= 1/64: 2^y = 2^n 2^(k/32) (1 + z), z = 2^r - 1 by its series, the
-// first term in two. Below 2^-126: 0.
+// first term in two. Below 2^-126: 0. The low part reaches 2^-14 of the high one.
 __device__ __forceinline__ Two power(Two d, Two c, const float2 *powers) {
   constexpr float kHi = 0.693147182f, kLo = float(0.69314718055994530942 - double(0.693147182f));  // ln 2
   constexpr float k2 = 0.240226507f, k3 = 0.0555041087f, k4 = 0.00961812911f;                      // ln 2^i / i!
@@ -121,7 +122,13 @@ __device__ __forceinline__ Two power(Two d, Two c, const float2 *powers) {
   return {none ? 0.0f : hi * scale, none ? 0.0f : lo * scale};
 }
 
-// The same in one binary32: 2^-23 relative, from roundings without a common sign (the series leaves 2^-28 off at its
+// The same with 2^-22 relative, by the exponential instruction.
+__device__ __forceinline__ float power_approx(Two d, Two c) {
+  const float y = d.hi * c.hi, yl = fmaf(d.lo, c.hi, fmaf(d.hi, c.lo, fmaf(d.hi, c.hi, -y))), p = exp2_approx(y);
+  return y < -126.0f ? 0.0f : fmaf(p * 0.693147182f, yl, p);
+}
+
+// In one binary32: 2^-23 relative, from roundings without a common sign (the series leaves 2^-28 off at its
 // ends, 2^-31 on the whole). d >= -126 / c. With y = n - g: n from y's rounding, g exact but for one rounding. (Two at a
 // time with the packed instructions took more, for the constants, which those cannot take from the instruction.)
 __device__ __forceinline__ float power_short(float d, float lo, Two c) {
@@ -323,21 +330,25 @@ struct Walker {
     int begin, end;
     part(row, begin, end);
     Peak k = {-INFINITY, 0.0f, INT32_MAX};
+    float low = 0.0f, batch = 0.0f;  // of k.sum (a lane may add up thousands of units); what it is to grow by
     const float c = unit.hi;
     const auto look = [&](int u, const float (&x)[kUnit]) {
       float t = x[0];
 #pragma unroll
       for (int i = 1; i < kUnit; ++i) t = fmaxf(t, x[i]);
       if (t > k.top) {
-        k.sum *= exp2_approx((k.top - t) * c);
+        const float f = exp2_approx((k.top - t) * c);
+        k.sum *= f, low *= f, batch *= f;
         k.top = t;
 #pragma unroll
         for (int i = kUnit - 1; i >= 0; --i)
           if (x[i] == t) k.token = row.first(u) + i;
       }
       const float ref = k.top == -INFINITY ? 0.0f : k.top;
+      float e[kUnit];
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) k.sum += exp2_approx((x[i] - ref) * c);
+      for (int i = 0; i < kUnit; ++i) e[i] = exp2_approx((x[i] - ref) * c);
+      batch += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
     };
 #pragma unroll 1
     for (int u0 = begin; u0 < end; u0 += 32 * kBatch) {
@@ -359,7 +370,10 @@ struct Walker {
           look(u, x);
         }
       }
+      const Two s = add(Two{k.sum, low}, batch, 0.0f);
+      k.sum = s.hi, low = s.lo, batch = 0.0f;
     }
+    k.sum += low;
     k = join_lanes(k);
     behind();
     const float4 *slots = exchange(make_float4(k.top, k.sum, __int_as_float(k.token), 0.0f));
@@ -482,7 +496,7 @@ struct Walker {
         if (DRAFT && fresh) {
           all = add(all, w.hi, w.lo);
           if (r.hi > 0.0f) share += l.y;
-          if (fabsf(fmaf(-taken.hi, l.y, w.hi)) < taken.hi * kNear * l.y) close += l.y;
+          if (fabsf(fmaf(-taken.hi, l.y, w.hi + w.lo)) < taken.hi * kNear * l.y) close += l.y;
         }
       };
       float x[kUnit], q[kUnit] = {}, nq[kUnit] = {};  // of this unit, and the next
@@ -777,10 +791,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
     if (!valid) break;
     taken = {0.0f, 0.0f};
     w.count = 0;
-    float mass = 1.0f;  // N
     all = {0.0f, 0.0f};
-    Two rest = {0.0f, 0.0f};  // N times the sum of all weights
-    bool stale = false;  // N is to be computed
+    Two rest = {0.0f, 0.0f};  // N times the sum of all weights, where it was summed
+    float mass = 1.0f;        // without a draft, before that: N
+    float summed = 0.0f;      // and what the sum was
+    bool stale = false;       // with a draft: N is to be computed
+    bool nothing = false;     // and nothing is left
     int next = -1;
     for (int base = 0; base < n && next < 0; base += 32) {
       const int i0 = base + lane;
@@ -790,22 +806,39 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
         asked &= asked - 1;
         const int y = sm.token[i];
         bool yes;
-        float p = exp2_approx((sm.x[i] - k.top) * w.unit.hi) / k.sum;
+        const Two d = minus(sm.x[i], k.top);
+        const auto exactly = [&] {
+          const Two e = power(d, w.unit, sm.powers);
+          return e.hi > kNothing ? add(e, Two{0.0f, 0.0f}) : Two{0.0f, 0.0f};
+        };
+        Two p = {power_approx(d, w.unit), 0.0f};  // the child's weight
+        if (p.hi <= kNothing) p.hi = 0.0f;
         if (greedy) {
           yes = y == k.token;
         } else if constexpr (DRAFT) {
-          if (stale) {
+          if (stale && !nothing) {
             const auto sums = w.sums(row, draft, k.top, taken, all.hi == 0.0f);
             rest = w.whole(sums.slots);
             if (all.hi == 0.0f) all = taken = sums.all;
-            mass = rest.hi / all.hi;
+            nothing = rest.hi <= kRest * all.hi;
             stale = false;
           }
-          yes = sm.u[i] * mass * sm.q[i] < p - taken.hi / k.sum * sm.q[i];
+          if (taken.hi != 0.0f) p = w.left_long(exactly(), sm.q[i], taken);
+          yes = !nothing && sm.u[i] * (taken.hi == 0.0f ? k.sum : rest.hi) * sm.q[i] < p.hi;
         } else {
+          // Taken off 1, N would lose as many bits as the rejected tokens took of it: once less than half is left, the
+          // others are summed, and again where less than 2^-10 of that sum is left. (What this second place for sums costs
+          // calls that never come here, in registers and instructions to fetch: one chain 12.8 -> 13.1 us, 16 trees 22.3 ->
+          // 23.4; out of line, with a walker of its own or this one, it was no better.)
+          if (summed == 0.0f ? mass < 0.5f : rest.hi < 0x1p-10f * summed) {
+            rest = w.whole(w.sums(row, draft, k.top, taken, false).slots);
+            summed = rest.hi;
+            if (rest.hi <= kNothing) rest = {0.0f, 0.0f}, summed = -1.0f;  // and so it stays
+          }
+          if (summed != 0.0f) p = exactly();
           for (int j = 0; j < w.count; ++j)
-            if (sm.rejected[j] == y) p = 0.0f;
-          yes = sm.u[i] * mass < p;
+            if (sm.rejected[j] == y) p = {0.0f, 0.0f};
+          yes = sm.u[i] * (summed == 0.0f ? mass * k.sum : rest.hi) < p.hi;
         }
         if (yes) {
           next = i;
@@ -814,10 +847,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
         if (greedy) continue;
         if constexpr (DRAFT) {
           // c becomes 1, for now with the sum that the walk has; then it grows by N
-          taken = taken.hi == 0.0f ? Two{k.sum, 0.0f} : add(taken, rest);
+          if (!nothing) taken = taken.hi == 0.0f ? Two{k.sum, 0.0f} : add(taken, rest);
           stale = true;
         } else {
-          mass = fmaxf(mass - p, 0.0f);
+          mass = fmaxf(mass - p.hi / k.sum, 0.0f);
+          if (summed != 0.0f) {
+            rest = add(rest, Two{-p.hi, -p.lo});
+            if (rest.hi < 0.0f) rest = {0.0f, 0.0f};
+          }
           __syncthreads();  // nobody reads the list
           if (tid == 0) sm.rejected[w.count] = y;
           ++w.count;
@@ -825,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
         }
       }
     }
+    if (nothing) taken = {0.0f, 0.0f};  // the new token is p's own
     if (next < 0) break;
     node = next;
     ++accepted;

@@ -214,3 +214,97 @@ def test_draft_equal_to_the_target(kind, dtype, B):
             away += 1
             assert said[b, 0] == token
     assert away > 0 or kind == "rounded"
+
+
+def nodes(parents_of, B):
+    """cu_rows and parents of B equal trees."""
+    n = len(parents_of)
+    return ac.i32([n * b for b in range(B + 1)]), ac.i32(list(parents_of) * B)
+
+
+@pytest.mark.parametrize("heavy", [[0.999], [1 - 2.0 ** -16], [0.4, 0.5, 0.09], [0.6, 0.3999, 0.0000999]])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+def test_chances_behind_rejected_likely_children(dtype, heavy):
+    """Children that hold nearly all of the row are rejected; the others' chances are p over the little that is left. Their
+    random numbers lie 2^-18 of the chance beside it, four times the error that the decisions may have."""
+    B, V, rng = 32, 9001, np.random.default_rng(len(heavy))
+    h, n = len(heavy), len(heavy) + 4
+    logits = rng.standard_normal((B * n, V))
+    tokens, u, want = np.zeros(B * n, np.int32), np.ones(B * n, np.float32), np.zeros(B, int)
+    exact = np.zeros((B, V))
+    for b in range(B):
+        own = rng.choice(V, h + 3, replace=False)
+        w = np.exp(logits[n * b])
+        w[own[:h]] = 0
+        w[own[h:]] *= 50  # so that their chances are some percent
+        w *= (1 - sum(heavy)) / w.sum()
+        w[own[:h]] = heavy
+        logits[n * b] = np.log(w)
+        tokens[n * b + 1:n * b + 4 + h] = own
+        if b % 3 == 0:
+            tokens[n * b + h] = own[0] if h > 1 else own[h - 1]  # one of the heavy twice, another one left
+    held = torch.from_numpy(logits).to(TYPES[dtype])
+    for b in range(B):
+        p = osp.softmax(held[n * b].double().numpy(), 1.0)
+        gone = list(tokens[n * b + 1:n * b + 1 + h])
+        good = int(rng.integers(0, 4))  # which of the others is accepted; 3: none
+        for j in range(3):
+            child = n * b + 1 + h + j
+            chance = osp.accept_chance(p, None, gone, tokens[child])
+            u[child] = np.float32(chance * (1 - 2.0 ** -18 if j == good else 1 + 2.0 ** -18))
+            gone.append(tokens[child])
+        want[b] = good
+    cu, parents = nodes([-1] + [0] * (n - 1), B)
+    out = speculative.verify_drafts(held.cuda(), ac.dev(tokens), cu, ac.dev(u), torch.full((B,), 0.5, device="cuda"),
+                                    parents=parents, max_rows=n)
+    for b in range(B):
+        assert out["path"][b, :2].tolist() == ([0, -1] if want[b] == 3 else [0, 1 + h + want[b]]), b
+
+
+@pytest.mark.parametrize("noise", [0.01, 0.001])
+@pytest.mark.parametrize("B", [3, 40])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_chances_behind_a_draft_close_to_the_target(dtype, B, noise):
+    """N is 2^-8 and 2^-11 of p, and a child's chance what is left of its p over what is left in all."""
+    V, rng = 33001, np.random.default_rng(B)
+    n = 4
+    logits = torch.from_numpy(2.0 * rng.standard_normal((B * n, V))).to(TYPES[dtype])
+    exact = logits.double().numpy()
+    draft = np.zeros((B * n, V), np.float32)
+    tokens, u, want = np.zeros(B * n, np.int32), np.ones(B * n, np.float32), np.zeros(B, int)
+    for b in range(B):
+        p = osp.softmax(exact[n * b], 1.0)
+        q = p * np.exp(noise * rng.standard_normal(V))
+        draft[n * b] = (q / q.sum()).astype(np.float32)
+        q = draft[n * b].astype(np.float64)
+        gone = [int(np.argmax(np.where(q > p, p, 0)))]  # surely rejected by a number of 1
+        tokens[n * b + 1] = gone[0]
+        good = int(rng.integers(0, 3))
+        for j in range(2):
+            left = osp.residual(p, q, gone)
+            ratio = left / left.sum() / q
+            some = np.flatnonzero((ratio > 0.2) & (ratio < 0.8))
+            y = int(some[rng.integers(0, len(some))])
+            child = n * b + 2 + j
+            tokens[child] = y
+            u[child] = np.float32(ratio[y] * (1 - 2.0 ** -18 if j == good else 1 + 2.0 ** -18))
+            gone.append(y)
+        want[b] = good
+    cu, parents = nodes([-1, 0, 0, 0], B)
+    out = speculative.verify_drafts(logits.cuda(), ac.dev(tokens), cu, ac.dev(u), torch.full((B,), 0.5, device="cuda"),
+                                    parents=parents, draft_probs=ac.dev(draft), max_rows=n)
+    for b in range(B):
+        assert out["path"][b, :2].tolist() == ([0, -1] if want[b] == 2 else [0, 2 + want[b]]), b
+
+
+def test_rejected_tokens_that_were_all_there_was():
+    """Three tokens allowed, all of them rejected, then children without a chance: the new token is one of the three."""
+    V, n = 5000, 200
+    logits = torch.full((n, V), -float("inf"), device="cuda")
+    logits[:, [10, 20, 4999]] = torch.tensor([1.0, 2.0, 3.0], device="cuda")
+    tokens = ac.i32([0, 10, 20, 4999] + list(range(100, 100 + n - 4)))
+    u = torch.zeros(n, device="cuda")
+    u[:4] = 1.0
+    out = speculative.verify_drafts(logits, tokens, ac.i32([0, n]), u, torch.tensor([0.2], device="cuda"),
+                                    parents=ac.i32([-1] + [0] * (n - 1)), max_rows=n)
+    assert out["accepted"].item() == 0 and out["tokens"][0, :2].tolist() == [20, -1]
