@@ -649,11 +649,12 @@ typedef struct moe_verify_drafts_io {
  * or +inf, or nothing but -inf, has no distribution: its children are rejected
  * and the new token is -1. A sequence without rows gets accepted 0, and -1
  * everywhere else; so does one whose offsets are out of range or that has more
- * than max_rows rows (reported). A parent that does not lie in front of its row is reported, and the row has no
- * parent; a token outside the vocabulary is reported and never accepted; a
- * temperature that is negative or not finite is reported and counts as 1, one
- * below 2^-100 as 2^-100. Rows other than the first without a parent are never
- * asked. draft_probs must be finite and not negative. */
+ * than max_rows rows (reported). A parent that does not lie in front of its row
+ * is reported, and the row has no parent; a token outside the vocabulary is
+ * reported and never accepted; a temperature that is negative or not finite is
+ * reported and counts as 1, one below 2^-100 or above 2^100 as that. Rows other
+ * than the first without a parent are never asked. draft_probs must be finite
+ * and not negative. */
 moe_status_t moe_verify_drafts(const moe_verify_drafts_io_t *io, int32_t *d_status, void *cuda_stream);
 
 typedef struct moe_commit_drafts_io {

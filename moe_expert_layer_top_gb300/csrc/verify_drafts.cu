@@ -770,7 +770,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
     t = 1.0f;
   }
   const bool greedy = t == 0.0f;
-  w.unit = exponent_unit(greedy ? 1.0f : fmaxf(t, 0x1p-100f));
+  // Beyond these ends all that is computed from it would not stay in range: `least` of a temperature of 2^122 is -inf, and
+  // then a logit of -inf gets a NaN as its weight.
+  w.unit = exponent_unit(greedy ? 1.0f : fminf(fmaxf(t, 0x1p-100f), 0x1p100f));
   w.least = -126.0f / w.unit.hi;
   __syncthreads();
 

@@ -308,3 +308,34 @@ def test_rejected_tokens_that_were_all_there_was():
     out = speculative.verify_drafts(logits, tokens, ac.i32([0, n]), u, torch.tensor([0.2], device="cuda"),
                                     parents=ac.i32([-1] + [0] * (n - 1)), max_rows=n)
     assert out["accepted"].item() == 0 and out["tokens"][0, :2].tolist() == [20, -1]
+
+
+@pytest.mark.parametrize("t", [2.0 ** 100, 1e37, 3e38])
+@pytest.mark.parametrize("drafted", [False, True])
+@pytest.mark.parametrize("V", [129, 5000])
+def test_large_temperatures_make_all_allowed_tokens_alike(V, drafted, t):
+    """Also beside logits of -inf, and in a row whose last unit is cut."""
+    rng = np.random.default_rng(V)
+    B = 40
+    logits = torch.from_numpy(rng.standard_normal((2 * B, V))).float()
+    out_of = torch.from_numpy(rng.random((2 * B, V)) < 0.3)
+    out_of[:, 0] = False
+    logits[out_of] = -float("inf")
+    exact = logits.double().numpy()
+    draft = np.zeros((2 * B, V), np.float32)
+    draft[:, 0] = 0.75
+    draft[:, 1:] = 0.25 / (V - 1)
+    u, sample, tokens = rng.random(2 * B).astype(np.float32), rng.random(B).astype(np.float32), np.zeros(2 * B, np.int32)
+    u[1::4] = 1.0  # every second child is surely rejected
+    out = speculative.verify_drafts(logits.cuda(), ac.dev(tokens), ac.i32([2 * b for b in range(B + 1)]), ac.dev(u),
+                                    ac.dev(sample), draft_probs=ac.dev(draft) if drafted else None,
+                                    temperature=torch.full((B,), t, device="cuda"), max_rows=2)
+    checked = 0
+    for b in range(B):
+        r = slice(2 * b, 2 * b + 2)
+        path, token, near, edge = osp.verify(exact[r], tokens[r], [-1, 0], u[r], sample[b], float(np.float32(t)),
+                                             draft[r] if drafted else None)
+        if near > 2.0 ** -20 and edge > 2.0 ** -24:  # equal weights: the borders are multiples of one
+            checked += 1
+            assert out["tokens"][b].tolist() == ([0, token] if len(path) == 2 else [token, -1])
+    assert checked > B // 2
