@@ -5,11 +5,11 @@
 // codes k and one scale code a per 32 dimensions, V likewise. Rows are (token,
 // head) pairs of one kv head's group; a row sees the keys in front of the tree,
 // its ancestors' and its own.
-//   Keys and values become f16 in shared memory: code times 2^(a - a_ref + 13), a_ref the largest scale code of
-//   32 keys. That is exact down to 2^-36 of the largest; what 2^a_ref takes off goes into the softmax: of keys into the
-//   factor of their scores, of values into the exponent of their weights (the sum of the weights is taken
-//   without it). Neither costs an operation per score. The accumulators are relative to one scale
-//   code of their own, which moves up when values beyond it appear.
+//   Keys and values become f16 in shared memory: code times 2^(a - a_ref + 13). Of keys a_ref is the largest scale code of
+//   32; what it takes off goes into the factor of their scores, without an operation per score. Of values it is the scale
+//   code that the accumulators are relative to: 3 above the largest so far where it moves, and it moves up when values
+//   beyond it appear. Exact down to 2^-33 of the largest seen. (With values relative to those of 32 keys, and the rest in
+//   the exponents of their weights, the weights next to a far larger value lost their bits in f16.)
 //   Queries become f16 times a power of two per row, probabilities f16 as in attend_paged.cu. All sums are binary32.
 //
 // Bound. 4 D flops per (row, head, key) on the tensor cores; a decoded key tile serves 128 or 256 rows, so decoding
@@ -69,7 +69,6 @@ constexpr float kLowest = -3e38f;   // reference of a row without a weight
 constexpr int kTop = 13;            // the largest scale of 32 keys becomes 2^kTop
 constexpr int kBias = 127 + kTop;   // a value is its f16 times 2^(a_ref - kBias)
 constexpr int kHeadroom = 3;        // the accumulators' scale code lies that far above the largest seen
-constexpr int kLeast = -60;         // a value's exponent relative to it, at least (2^-60 of the largest)
 // What an item costs beside its tiles, in units of a narrow tile.
 constexpr int kOver = 8;
 constexpr int kMinShare = 2;  // units of a share, at least: each block between an item's first and last has a tile of it
@@ -292,7 +291,8 @@ struct Smem {
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of Q, K or V in f16: D/64 parts of 128 rows x 128 bytes
   // Largest scales are kept for 8 tiles. Those of K tile j + 8 are written when K of tile j + 7 is there, for which S of
   // tile j + 7 - kStages / 2 >= j + 3 was done; that was issued behind P V of the tile before (or two before) in its
-  // stream, and so were those before it: the softmax has read those of tile j.
+  // stream, and so were those before it: the softmax has read those of tile j. V's likewise, by the P V that its entry of
+  // the ring was waited for; and no warp of theirs is a tile ahead of one that has yet to read the four.
   static constexpr int kExps = 8;
   static_assert(kExps >= kStages / 2 + 4, "largest scales");
   static constexpr int kRawBytes = kKeys * D / 2;
@@ -303,12 +303,14 @@ struct Smem {
   uint8_t raw[2][kRawBytes];                   // codes of K and V of the next tile as each thread copied them
   uint8_t join[D == 128 ? 16 : kRows * 64 * 4];  // D = 128: the second stream's query tile serves
   int exps[kExps][2][4];                       // by tile mod kExps: largest scale codes of 32 keys, of their values
+  int values[kExps];                           // and the scale code that the tile's values are relative to
   uint8_t parent[kMaxTree];                    // place of the parent plus one
   int64_t before[kMaxSeqs / 32 + 1], total;    // of the list of work
   uint64_t q_full[2];      // the query tile is there (4 warps)
   uint64_t full[kStages];  // a K or V tile is there (4 warps)
   uint64_t empty[kStages]; // the MMAs that read it are done (2 commits: one of each stream, or two of one)
-  uint64_t exps_full[kExps];  // a tile's largest scales are there (8 warps)
+  uint64_t tops_full[kExps];  // a tile's largest scales of the values are there (4 warps)
+  uint64_t exps_full[kExps];  // and those of the keys, and what the values are relative to (8 warps)
   uint64_t s_full[2];      // S of a step complete, and everything issued before it
   uint64_t p_full[2];      // P of a step written (4 warps)
   uint64_t o_full[2];      // the stream's last P V is in O, and every MMA of the stream is done
@@ -594,16 +596,26 @@ struct Decoder {
   // t: tiles of the block in front of the segment's. One copy of the code for K, V and every tile: see the softmax.
   __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t) {
     start(seg);
+    int relative = 0;  // what values are relative to
 #pragma unroll 1
     for (int i = -1; i < seg.count; ++i) {
       if (i >= 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");
-        const int top = largest(scale);
+        int top = largest(scale);
         const uint32_t n = t + i, e = 2 * n + v, slot = e % S::kStages;
-        if (lane == 0) {
-          sm.exps[n % S::kExps][v][warp] = top;
-          mbar_arrive(&sm.exps_full[n % S::kExps]);
+        int(&exps)[2][4] = sm.exps[n % S::kExps];
+        if (lane == 0) exps[v][warp] = top;
+        // The four warps of the values agree on it, and say it to the softmax. (With the softmax following it by itself 24
+        // ragged trees of D = 64 took 74 us, with scales looked up a tile ahead, so that none waits here, 68; so 65.)
+        if (v) {
+          if (lane == 0) mbar_arrive(&sm.tops_full[n % S::kExps]);
+          if (!__all_sync(0xFFFFFFFFu, wait(&sm.tops_full[n % S::kExps], n / S::kExps & 1, a.status))) return false;
+          top = max(max(exps[1][0], exps[1][1]), max(exps[1][2], exps[1][3]));
+          if (i == 0 || top > relative) relative = top + kHeadroom;
+          top = relative;
+          if (warp == 0 && lane == 0) sm.values[n % S::kExps] = relative;
         }
+        if (lane == 0) mbar_arrive(&sm.exps_full[n % S::kExps]);
         if (!ready(e)) return false;
         convert(sm.kv[slot], sm.raw[v], scale, top);
         fence_proxy_async();
@@ -883,7 +895,7 @@ struct Softmax {
       const uint32_t n = t + i;
       if (!__all_sync(0xFFFFFFFFu, wait(&sm.exps_full[n % S::kExps], n / S::kExps & 1, a.status))) return false;
       const int(&exps)[2][4] = sm.exps[n % S::kExps];
-      const int vtop = max(max(exps[1][0], exps[1][1]), max(exps[1][2], exps[1][3]));
+      const int values = sm.values[n % S::kExps];
       const bool masked = key0 + kKeys > before;  // some key of the tile may be hidden
       uint32_t see[4] = {0, 0, 0, 0};
       if (masked) visible(token, key0 - before, see);
@@ -906,8 +918,8 @@ struct Softmax {
       top = fmaxf(top, fmaxf(t1 * factor(unit, exps[0][1]), t0 * factor(unit, exps[0][0])));
       if (opening) {
         ref = fmaxf(top, kLowest);
-        scale = vtop + kHeadroom;
-      } else if (__any_sync(0xFFFFFFFFu, top - ref > kLazy) || vtop > scale) {
+        scale = values;
+      } else if (__any_sync(0xFFFFFFFFu, top - ref > kLazy) || values > scale) {
         // the accumulators hold every tile before this one (see the order of issue)
         float f = 1.0f;
         if (top - ref > kLazy) {
@@ -915,16 +927,15 @@ struct Softmax {
           ref = top;
         }
         total *= f;
-        if (vtop > scale) {
-          f *= pow2(scale - (vtop + kHeadroom));
-          scale = vtop + kHeadroom;
+        if (values > scale) {
+          f *= pow2(scale - values);
+          scale = values;
         }
         scale_accumulators(f);
       }
-      // P = 2^(s - ref) in f16, with what the values' scales lie below the accumulators', and the sum without that. A
-      // loop: its code has to share the instruction cache with the decoders' (with four times 32 exponentials one after
-      // another, twice, and four copies of the decoding the warps waited for instructions a third of the time: 16 trees
-      // of 64 rows 520 us).
+      // P = 2^(s - ref) in f16, and the sum. A loop: its code has to share the instruction cache with the decoders' (with
+      // four times 32 exponentials one after another, twice, and four copies of the decoding the warps waited for
+      // instructions a third of the time: 16 trees of 64 rows 520 us).
 #pragma unroll 1
       for (int c = 0; c < 4; c += 2) {
         if (c) {
@@ -932,10 +943,9 @@ struct Softmax {
           tmem_wait_ld(s1);
           if (masked) hide(see[2], s0), hide(see[3], s1);
         }
-        const int d0 = max(exps[1][c] - scale, kLeast), d1 = max(exps[1][c + 1] - scale, kLeast);
-        total = fmaf(exponentials(c, s0, factor(unit, exps[0][c]), kUp - ref + float(d0)), pow2(-d0), total);
+        total += exponentials(c, s0, factor(unit, exps[0][c]), kUp - ref);
         if (c == 0) tmem_ld32(ts + 64, s0);
-        total = fmaf(exponentials(c + 1, s1, factor(unit, exps[0][c + 1]), kUp - ref + float(d1)), pow2(-d1), total);
+        total += exponentials(c + 1, s1, factor(unit, exps[0][c + 1]), kUp - ref);
         if (c == 0) tmem_ld32(ts + 96, s1);
       }
       tmem_wait_st();
@@ -1049,7 +1059,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
       mbar_init(&sm.full[i], 4);
       mbar_init(&sm.empty[i], 2);
     }
-    for (int i = 0; i < S::kExps; ++i) mbar_init(&sm.exps_full[i], 8);
+    for (int i = 0; i < S::kExps; ++i) {
+      mbar_init(&sm.tops_full[i], 4);
+      mbar_init(&sm.exps_full[i], 8);
+    }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.q_full[x], 4);
       mbar_init(&sm.s_full[x], 1);
