@@ -18,9 +18,9 @@
 // Bound. Only the rows on the way are read: with one accepted child after another the rows come one after another, each a
 // pass over the vocabulary that ends in a barrier. A cluster of blocks takes a sequence, and each block a part of the
 // vocabulary.
-//   Measured (131,072 tokens, device time in a graph): one chain of six in bf16 12.5 us, of a single row 6; 64 chains of
-// six with a draft, fp32, 68 us (65 without the differences' low parts), of single rows 11 to 15; 16 trees of 64 rows 21.6; 24 of up to 16 rows with a draft over
-// 50,021 tokens 35. Issue slots are 20 to 30 % busy, HBM 4 to 23 %: rows one after another, each a chain of latencies.
+//   Measured (131,072 tokens, device time in a graph): one chain of six in bf16 13.1 us, of a single row 6; 64 chains of
+// six with a draft, fp32, 70 us, of single rows 11 to 15; 16 trees of 64 rows 24; 24 of up to 16 rows with a draft over
+// 50,021 tokens 37 to 39. Issue slots are 20 to 30 % busy, HBM 4 to 23 %: rows one after another, each a chain of latencies.
 //
 // Layout. A block's warps have consecutive parts of its part, in units of 8 tokens, a unit a lane. What every warp finds
 // goes to a slot of its own in every block of the cluster (distributed shared memory), and every warp of every block
@@ -953,9 +953,30 @@ cudaError_t launch_verify_drafts(const moe_verify_drafts_io_t &io, int32_t *stat
   a.vocab = io.vocab;
   a.status = status;
   for (int i = 0; i < 32; ++i) a.powers[i] = powers.v[i];
-  // Blocks of a sequence: of 2,048 tokens at least, and no more in all than 2.6 an SM (64 sequences: 4 each; with 8, for
-  // which registers would have to be fewer, 71 us in place of 65; 24 sequences of 50,021 tokens: 16 each, 35 us, 40 with 8).
-  const auto fits = [&](int n) { return int64_t(io.num_seqs) * n * 10 <= 26 * num_sms && io.vocab / n >= 2048; };
+  // Blocks of a sequence: of 2,048 tokens at least, and in all at most 1.7 an SM in clusters of 16, 2.6 in smaller ones (the
+  // kernel holds two an SM: what is more waits for the sequences that end first). Measured, device us by blocks of a cluster:
+  //                                        sequences     1     2     4     8    16
+  //   chains of 6, 131,072 tokens, drafted       14   149    88    52    34    30
+  //                                              16   161    91    54    37    40
+  //                                              20   141    79    48    37    39
+  //                                              24   155    82    52    39    48
+  //                                              48   167    95    67    64    83
+  //                                              56   175    97    71    72    98
+  //                                              96   184   116   105   110   159
+  //                                             128   182   122   118   133   200
+  //   trees of 16, 131,072 tokens                14   120    69    41    27    23
+  //                                              16   130    73    42    29    31
+  //                                              20   114    63    37    27    31
+  //   trees of 64, a quarter greedy              16     -     -    43    30    27
+  //   chains of 6, 50,021 tokens                 14    51    35    27    21    20
+  //                                              24    45    30    23    20    25
+  //                                              96    54    40    40    48    79
+  //                                             160    60    51    56    76   130
+  //                                             256    79    74    91   126   215
+  //                                             512   120   122   159   238   422
+  const auto fits = [&](int n) {
+    return int64_t(io.num_seqs) * n * 10 <= (n == kMaxCluster ? 17 : 26) * num_sms && io.vocab / n >= 2048;
+  };
   int cluster = 1;
   while (cluster < kMaxCluster && fits(2 * cluster)) cluster *= 2;
   const bool draft = io.draft_probs != nullptr;
