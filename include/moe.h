@@ -640,7 +640,7 @@ typedef struct moe_verify_drafts_io {
  * sample_u times the whole (p itself, if nothing is left, or of p less a draft
  * not 2^-30).
  * Only the rows on the way are read. Decisions compare numbers of relative error
- * 2^-20 (what is left of p less a draft: and 2^-34 of p's whole). The sums that
+ * about 2^-20 (what is left of p less a draft: and 2^-34 of p's whole). The sums that
  * choose the new token have an error of about 2^-34 of p's whole; where much of it
  * lies in tokens below 2^-13 of the largest 2^-30, and up to 2^-25 where these
  * have one logit in common. So they are the formula's but for numbers

@@ -828,11 +828,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(const __grid
           if (taken.hi != 0.0f) p = w.left_long(exactly(), sm.q[i], taken);
           yes = !nothing && sm.u[i] * (taken.hi == 0.0f ? k.sum : rest.hi) * sm.q[i] < p.hi;
         } else {
-          // Taken off 1, N would lose as many bits as the rejected tokens took of it: once less than half is left, the
-          // others are summed, and again where less than 2^-10 of that sum is left. (What this second place for sums costs
-          // calls that never come here, in registers and instructions to fetch: one chain 12.8 -> 13.1 us, 16 trees 22.3 ->
-          // 23.4; out of line, with a walker of its own or this one, it was no better.)
-          if (summed == 0.0f ? mass < 0.5f : rest.hi < 0x1p-10f * summed) {
+          // Taken off 1, N loses as many bits as the rejected tokens took of it (its terms are good to 2^-22): once less than
+          // a quarter is left, the others are summed, and again where less than 2^-10 of that sum is left. (Already with a
+          // half left: 16 trees of 64, the mean of 24 draws, 31.0 us, with an eighth 29.4. What this second place for sums
+          // costs calls that never come here, in registers and instructions to fetch: one chain 12.5 -> 12.9 us; out of line,
+          // with a walker of its own or this one, it was no better.)
+          if (summed == 0.0f ? mass < 0.25f : rest.hi < 0x1p-10f * summed) {
             rest = w.whole(w.sums(row, draft, k.top, taken, false).slots);
             summed = rest.hi;
             if (rest.hi <= kNothing) rest = {0.0f, 0.0f}, summed = -1.0f;  // and so it stays
