@@ -588,13 +588,17 @@ moe_status_t moe_attend_tree_workspace(const moe_attend_tree_io_t *io, const moe
  * front of it (to the last bits: the sums have another order). A parent that
  * does not lie in front of its row is reported and counts as none. A sequence
  * with more than MOE_MAX_TREE_ROWS rows is reported and gets no result: its rows
- * are not touched. A scale code of 255 counts as 2^128, as it does there. Where
- * a kv head usually has many rows (max_rows, num_rows, num_seqs and the heads
- * say so) the kernel's parts wait for one another, as those of
- * moe_attend_prompt do: if such a wait does not end within a second,
- * MOE_ERR_TIMEOUT is stored in *d_status, the kernel ends by itself, and the
- * call's results are unspecified (the next call is not affected). rows.flags may
- * also be MOE_FLAG_TEST_SKIP_READY. */
+ * are not touched. A scale code of 255, which moe_qkv_append never writes, counts
+ * as infinite: a row that sees such a key gets a NaN, or a result without the key
+ * where its score is -inf; one among the values is a NaN, which can reach other
+ * rows of its own sequence. Where a kv head usually has many rows (max_rows,
+ * num_rows, num_seqs and the heads say so; with max_rows far too small the
+ * kernels for few rows run, in about twice the time from 96 rows of a kv head on)
+ * the kernel's parts wait for one another, as those of moe_attend_prompt do: if
+ * such a wait does not end within a second, MOE_ERR_TIMEOUT is stored in
+ * *d_status, the kernel ends by itself, and the call's results are unspecified
+ * (the next call is not affected). rows.flags may also be
+ * MOE_FLAG_TEST_SKIP_READY. */
 moe_status_t moe_attend_tree(const moe_attend_tree_io_t *io, const moe_kv_cache_t *cache, void *workspace,
                              int64_t workspace_bytes, int32_t *d_status, void *cuda_stream);
 
@@ -654,7 +658,7 @@ typedef struct moe_verify_drafts_io {
  * reported and never accepted; a temperature that is negative or not finite is
  * reported and counts as 1, one below 2^-100 or above 2^100 as that. Rows other
  * than the first without a parent are never asked. draft_probs must be finite
- * and not negative. */
+ * and not negative; outputs must not overlap inputs. */
 moe_status_t moe_verify_drafts(const moe_verify_drafts_io_t *io, int32_t *d_status, void *cuda_stream);
 
 typedef struct moe_commit_drafts_io {

@@ -190,7 +190,9 @@ def attend_tree(q: torch.Tensor, cache: KVCacheMXFP4, page_table: torch.Tensor, 
     As ``attend_paged``, where the n rows of a sequence, its last n tokens in the cache, form a tree: parents int32
     [rows] holds the place of each row's parent among its sequence's rows (less than its own; negative: a root). A row
     sees the keys in front of the tree, the rows on its way to the root, and itself. At most 256 rows a sequence;
-    one with more is reported in d_status and its rows of out are left as they are.
+    one with more is reported in d_status and its rows of out are left as they are. max_rows picks the kernels: give the
+    rows that the largest trees have, since with the default those of single rows run, which take about twice as long from
+    96 rows of a kv head (rows times query heads to a kv head) on.
 
     Returns out [rows][heads][D], and with return_lse also lse fp32 [rows][heads].
     """

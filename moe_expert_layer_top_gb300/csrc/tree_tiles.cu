@@ -16,7 +16,7 @@
 // (2 D conversions a key) is a small part of it, unlike with the 8 to 32 rows of a verify step.
 //   Measured (32 + 8 heads of 128, 152 SMs, device time in a graph): 16 trees of 64 rows over 8,000 to 32,000 tokens
 // 315 us, 990 TFLOP/s or half of a library product's rate; one of 64 rows over 131,071 tokens 148 us (930); one of 16
-// rows over 4,096 20.6; 24 ragged ones (64 + 8 heads of 64, f16) 64. A step of a stream, 128 keys, takes 4,700
+// rows over 4,096 20.6; 24 ragged ones (64 + 8 heads of 64, f16) 65 to 68. A step of a stream, 128 keys, takes 4,700
 // clocks: 2,250 for the softmax (1,500 of them exponentials), 1,850 until its MMAs are issued and done, which at 128
 // x 128 take all of the shared memory's bandwidth, the rest waits and mask. The streams overlap to 44 % of the tensor
 // pipe's time and 42 % of the issue slots. Leaving out single parts (exponentials, decoding, its stores) gains 5 % at
@@ -606,7 +606,9 @@ struct Decoder {
         int(&exps)[2][4] = sm.exps[n % S::kExps];
         if (lane == 0) exps[v][warp] = top;
         // The four warps of the values agree on it, and say it to the softmax. (With the softmax following it by itself 24
-        // ragged trees of D = 64 took 74 us, with scales looked up a tile ahead, so that none waits here, 68; so 65.)
+        // ragged trees of D = 64 took 74 us, with scales looked up a tile ahead, so that none waits here, 68, and D = 128 8 %
+        // more; so 65. With tiles converted first and once more where the scale has moved ragged ones are as fast and D = 128
+        // takes 4 to 13 % more.)
         if (v) {
           if (lane == 0) mbar_arrive(&sm.tops_full[n % S::kExps]);
           if (!__all_sync(0xFFFFFFFFu, wait(&sm.tops_full[n % S::kExps], n / S::kExps & 1, a.status))) return false;
