@@ -7,8 +7,8 @@
 // its ancestors' and its own.
 //   Keys and values become f16 in shared memory: code times 2^(a - a_ref + 13). Of keys a_ref is the largest scale code of
 //   32; what it takes off goes into the factor of their scores, without an operation per score. Of values it is the scale
-//   code that the accumulators are relative to: 3 above the largest so far where it moves, and it moves up when values
-//   beyond it appear. Exact down to 2^-33 of the largest seen. (With values relative to those of 32 keys, and the rest in
+//   code that the accumulators are relative to: 3 above the largest of 16 tiles where it moves, and it moves up when values
+//   beyond it are among the next 16. Exact down to 2^-33 of the largest seen. (With values relative to those of 32 keys, and the rest in
 //   the exponents of their weights, the weights next to a far larger value lost their bits in f16.)
 //   Queries become f16 times a power of two per row, probabilities f16 as in attend_paged.cu. All sums are binary32.
 //
@@ -16,7 +16,7 @@
 // (2 D conversions a key) is a small part of it, unlike with the 8 to 32 rows of a verify step.
 //   Measured (32 + 8 heads of 128, 152 SMs, device time in a graph): 16 trees of 64 rows over 8,000 to 32,000 tokens
 // 315 us, 990 TFLOP/s or half of a library product's rate; one of 64 rows over 131,071 tokens 148 us (930); one of 16
-// rows over 4,096 20.6; 24 ragged ones (64 + 8 heads of 64, f16) 65 to 68. A step of a stream, 128 keys, takes 4,700
+// rows over 4,096 20.6; 24 ragged ones (64 + 8 heads of 64, f16) 64. A step of a stream, 128 keys, takes 4,700
 // clocks: 2,250 for the softmax (1,500 of them exponentials), 1,850 until its MMAs are issued and done, which at 128
 // x 128 take all of the shared memory's bandwidth, the rest waits and mask. The streams overlap to 44 % of the tensor
 // pipe's time and 42 % of the issue slots. Leaving out single parts (exponentials, decoding, its stores) gains 5 % at
@@ -291,8 +291,8 @@ struct Smem {
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of Q, K or V in f16: D/64 parts of 128 rows x 128 bytes
   // Largest scales are kept for 8 tiles. Those of K tile j + 8 are written when K of tile j + 7 is there, for which S of
   // tile j + 7 - kStages / 2 >= j + 3 was done; that was issued behind P V of the tile before (or two before) in its
-  // stream, and so were those before it: the softmax has read those of tile j. V's likewise, by the P V that its entry of
-  // the ring was waited for; and no warp of theirs is a tile ahead of one that has yet to read the four.
+  // stream, and so were those before it: the softmax has read those of tile j. What V's are relative to likewise, by the P V
+  // that V's entry of the ring was waited for.
   static constexpr int kExps = 8;
   static_assert(kExps >= kStages / 2 + 4, "largest scales");
   static constexpr int kRawBytes = kKeys * D / 2;
@@ -302,15 +302,16 @@ struct Smem {
   uint8_t kv[kStages][kTileBytes];
   uint8_t raw[2][kRawBytes];                   // codes of K and V of the next tile as each thread copied them
   uint8_t join[D == 128 ? 16 : kRows * 64 * 4];  // D = 128: the second stream's query tile serves
-  int exps[kExps][2][4];                       // by tile mod kExps: largest scale codes of 32 keys, of their values
+  int exps[kExps][4];                          // by tile mod kExps: largest scale codes of 32 keys,
   int values[kExps];                           // and the scale code that the tile's values are relative to
+  int tops[2][4];                              // of 16 tiles, by turns: the values' largest scale code, by warp
   uint8_t parent[kMaxTree];                    // place of the parent plus one
   int64_t before[kMaxSeqs / 32 + 1], total;    // of the list of work
   uint64_t q_full[2];      // the query tile is there (4 warps)
   uint64_t full[kStages];  // a K or V tile is there (4 warps)
   uint64_t empty[kStages]; // the MMAs that read it are done (2 commits: one of each stream, or two of one)
-  uint64_t tops_full[kExps];  // a tile's largest scales of the values are there (4 warps)
-  uint64_t exps_full[kExps];  // and those of the keys, and what the values are relative to (8 warps)
+  uint64_t exps_full[kExps];  // a tile's exps and what its values are relative to are there (8 warps)
+  uint64_t tops_full[2];   // 16 tiles' tops are there (4 warps)
   uint64_t s_full[2];      // S of a step complete, and everything issued before it
   uint64_t p_full[2];      // P of a step written (4 warps)
   uint64_t o_full[2];      // the stream's last P V is in O, and every MMA of the stream is done
@@ -489,7 +490,8 @@ struct Decoder {
   const int group = lane / kSpan, in = lane % kSpan;
   const int32_t *table;
   uint32_t at;  // lane 2 j + u: cached row of granule u (16 keys) of the warp's keys in the j-th tile of the batch
-  int looked;   // tiles of the segment that were looked up
+  int looked;   // the batch's first tile: 16 of the segment are looked up at a time
+  uint32_t batches = 0;  // of values, that the warps have agreed on
   uint32_t scale[kPer] = {};  // scale codes of the tile on its way
 
   __device__ __forceinline__ Decoder(const TileArgs &args, S &smem)
@@ -521,8 +523,9 @@ struct Decoder {
   // 329 and 74.5 with 16 trees of 64 rows and ragged ones of D = 64.)
   __device__ __forceinline__ void fetch(const Segment &seg, int i) {
     if (i < seg.count) {
-      const int j = i - looked;
-      if (i == looked || j == 16) {
+      uint4 of[kGroups] = {};  // values: the scale codes of the lane's granule, and how many bytes of them are there
+      int bytes = -1;
+      if (i == looked || i - looked == 16) {
         looked = i;
         const int step = i + (lane >> 1), key = (seg.first + step) * kKeys + warp * 32 + (lane & 1) * 16;
         at = kNoRow;
@@ -534,6 +537,13 @@ struct Decoder {
           else
             at = (uint32_t(page) * a.num_kv_heads + seg.kv) * a.page_size + (key - pi * a.page_size);
           if (at != kNoRow && !index_ok(a.status, int64_t(at) + 15, a.cached_rows)) at = kNoRow;
+        }
+        if (v) {
+          bytes = at == kNoRow ? 0 : min(16, seg.s.len - key) * kGroups;
+          if (bytes) {
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) of[k] = __ldg(reinterpret_cast<const uint4 *>(scales + uint64_t(at) * kGroups) + k);
+          }
         }
       }
       const int from = 2 * (i - looked), rest = seg.s.len - (seg.first + i) * kKeys - warp * 32;  // of the warp's 32 keys
@@ -557,6 +567,30 @@ struct Decoder {
           scale[p] = load_scale(q + h * (kSpan * kGroups), some);
         }
       }
+      if (bytes >= 0) tell(of, bytes);  // the whole warp
+    }
+  }
+
+  // The largest of the warp's scale codes of the batch, for the other warps of the values. Short, since most items come here
+  // once and its code has to be fetched (byte by byte 24 ragged trees of D = 128 took 69 us in place of 62).
+  __device__ __forceinline__ void tell(const uint4 (&of)[kGroups], int bytes) {
+    uint32_t even = 0, odd = 0;  // of the bytes plus one, 255 (no scale) being 0
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const uint32_t w[4] = {of[k].x, of[k].y, of[k].z, of[k].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        // the word's bytes that are there: a shift by 32 and more leaves none
+        const uint32_t x = w[c] & __funnelshift_rc(0xFFFFFFFFu, 0u, max(8 * (16 * k + 4 * c + 4 - bytes), 0));
+        even = __vmaxu2(even, ((x & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu);
+        odd = __vmaxu2(odd, ((x >> 8 & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu);
+      }
+    }
+    even = __vmaxu2(even, odd);
+    const int most = max(int(__reduce_max_sync(0xFFFFFFFFu, max(even & 0xFFFFu, even >> 16))) - 1, 0);
+    if (lane == 0) {
+      sm.tops[batches & 1][warp] = most;
+      mbar_arrive(&sm.tops_full[batches & 1]);
     }
   }
 
@@ -596,26 +630,29 @@ struct Decoder {
   // t: tiles of the block in front of the segment's. One copy of the code for K, V and every tile: see the softmax.
   __device__ __forceinline__ bool segment(const Segment &seg, uint32_t t) {
     start(seg);
-    int relative = 0;  // what values are relative to
+    // What values are relative to. Their four warps agree on it, for 16 tiles at a time. (For each tile, so that all waited
+    // for the slowest load, 24 ragged trees of D = 64 took 66 us in place of 64, with a cold L2 81 in place of 75; with tiles
+    // converted first and once more where the scale moves D = 128 took 4 to 13 % more.)
+    int relative = 0;
 #pragma unroll 1
     for (int i = -1; i < seg.count; ++i) {
       if (i >= 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");
-        int top = largest(scale);
         const uint32_t n = t + i, e = 2 * n + v, slot = e % S::kStages;
-        int(&exps)[2][4] = sm.exps[n % S::kExps];
-        if (lane == 0) exps[v][warp] = top;
-        // The four warps of the values agree on it, and say it to the softmax. (With the softmax following it by itself 24
-        // ragged trees of D = 64 took 74 us, with scales looked up a tile ahead, so that none waits here, 68, and D = 128 8 %
-        // more; so 65. With tiles converted first and once more where the scale has moved ragged ones are as fast and D = 128
-        // takes 4 to 13 % more.)
+        int top;
         if (v) {
-          if (lane == 0) mbar_arrive(&sm.tops_full[n % S::kExps]);
-          if (!__all_sync(0xFFFFFFFFu, wait(&sm.tops_full[n % S::kExps], n / S::kExps & 1, a.status))) return false;
-          top = max(max(exps[1][0], exps[1][1]), max(exps[1][2], exps[1][3]));
-          if (i == 0 || top > relative) relative = top + kHeadroom;
+          if (i == looked) {  // with a batch
+            const int(&tops)[4] = sm.tops[batches & 1];
+            if (!__all_sync(0xFFFFFFFFu, wait(&sm.tops_full[batches & 1], batches >> 1 & 1, a.status))) return false;
+            ++batches;
+            top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+            if (i == 0 || top > relative) relative = top + kHeadroom;
+          }
           top = relative;
-          if (warp == 0 && lane == 0) sm.values[n % S::kExps] = relative;
+          if (warp == 0 && lane == 0) sm.values[n % S::kExps] = top;
+        } else {
+          top = largest(scale);
+          if (lane == 0) sm.exps[n % S::kExps][warp] = top;
         }
         if (lane == 0) mbar_arrive(&sm.exps_full[n % S::kExps]);
         if (!ready(e)) return false;
@@ -896,7 +933,7 @@ struct Softmax {
       const bool opening = i == start;
       const uint32_t n = t + i;
       if (!__all_sync(0xFFFFFFFFu, wait(&sm.exps_full[n % S::kExps], n / S::kExps & 1, a.status))) return false;
-      const int(&exps)[2][4] = sm.exps[n % S::kExps];
+      const int(&exps)[4] = sm.exps[n % S::kExps];
       const int values = sm.values[n % S::kExps];
       const bool masked = key0 + kKeys > before;  // some key of the tile may be hidden
       uint32_t see[4] = {0, 0, 0, 0};
@@ -911,13 +948,13 @@ struct Softmax {
       tmem_wait_ld(s1, t1);
       tmem_wait_ld(s0, t0);
       if (masked) t1 = hide(see[3], s1), t0 = hide(see[2], s0);
-      top = fmaxf(t1 * factor(unit, exps[0][3]), t0 * factor(unit, exps[0][2]));
+      top = fmaxf(t1 * factor(unit, exps[3]), t0 * factor(unit, exps[2]));
       tmem_ld32_max(ts + 32, s1, t1);
       tmem_ld32_max(ts, s0, t0);
       tmem_wait_ld(s1, t1);
       tmem_wait_ld(s0, t0);
       if (masked) t1 = hide(see[1], s1), t0 = hide(see[0], s0);
-      top = fmaxf(top, fmaxf(t1 * factor(unit, exps[0][1]), t0 * factor(unit, exps[0][0])));
+      top = fmaxf(top, fmaxf(t1 * factor(unit, exps[1]), t0 * factor(unit, exps[0])));
       if (opening) {
         ref = fmaxf(top, kLowest);
         scale = values;
@@ -945,9 +982,9 @@ struct Softmax {
           tmem_wait_ld(s1);
           if (masked) hide(see[2], s0), hide(see[3], s1);
         }
-        total += exponentials(c, s0, factor(unit, exps[0][c]), kUp - ref);
+        total += exponentials(c, s0, factor(unit, exps[c]), kUp - ref);
         if (c == 0) tmem_ld32(ts + 64, s0);
-        total += exponentials(c + 1, s1, factor(unit, exps[0][c + 1]), kUp - ref);
+        total += exponentials(c + 1, s1, factor(unit, exps[c + 1]), kUp - ref);
         if (c == 0) tmem_ld32(ts + 96, s1);
       }
       tmem_wait_st();
@@ -1061,11 +1098,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const TileArgs 
       mbar_init(&sm.full[i], 4);
       mbar_init(&sm.empty[i], 2);
     }
-    for (int i = 0; i < S::kExps; ++i) {
-      mbar_init(&sm.tops_full[i], 4);
-      mbar_init(&sm.exps_full[i], 8);
-    }
+    for (int i = 0; i < S::kExps; ++i) mbar_init(&sm.exps_full[i], 8);
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.tops_full[x], 4);
       mbar_init(&sm.q_full[x], 4);
       mbar_init(&sm.s_full[x], 1);
       mbar_init(&sm.p_full[x], 4);

@@ -68,3 +68,51 @@ def test_a_large_value_without_weight(rows, D, dtype, at, shift):
     zz = lambda a: np.asarray(a)[keep]
     lim = delta + m * 2.0 ** -24 + 4 * 2.0 ** -24 * (np.abs(z) + reach)
     assert (np.abs(zz(ac.f64(lse)) - zz(z)) <= zz(lim)).all()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "fp16"), (128, "bf16")])
+def test_large_values_along_long_contexts(D, dtype):
+    """As above, with runs of more than 16 tiles of 128 keys, which agree on a scale together, several items a block, and
+    large values without weight on both sides of where a run may end. Also scale codes of 255 behind the last
+    token, and large ones: neither counts."""
+    B, K, group, rows, m = 8, 8, 2, 40, 6000
+    H = K * group
+    rng = np.random.default_rng(D)
+    lengths = [m - 37 * b for b in range(B)]
+    c = ac.Cache(rng, lengths, K, D, 64)
+    parents = [tc.random_tree(rng, rows) for _ in range(B)]
+    q = np.zeros((B * rows, H, D))
+    heavy = [(300, 3), (700, 12), (2047, 12), (2048, 13), (2303, 9), (4100, 13)]
+    for b in range(B):
+        table = c.table[b].long()
+        place = lambda j: (int(table[j // 64]), slice(None), j % 64)
+        c.cache.v_scales[place(0)] = 0
+        c.v[b][0] = 0.0
+        for j, shift in heavy:
+            c.cache.v_scales[place(j)] += shift
+            c.v[b][j] *= 2.0 ** shift
+            c.cache.k_codes[place(j)] = c.cache.k_codes[place(0)] ^ 0x88
+            c.cache.k_scales[place(j)] = c.cache.k_scales[place(0)] + 1
+            c.k[b][j] = -2.0 * c.k[b][0]
+        for j in range(lengths[b], -(-lengths[b] // 64) * 64):
+            c.cache.v_scales[place(j)] = 255 if j % 2 else 250
+        for h in range(H):
+            k0 = c.k[b][0, h // group]
+            q[b * rows:(b + 1) * rows, h] = (11.0 * D ** 0.5 / (k0 @ k0)) * k0
+    q += 0.2 * rng.standard_normal(q.shape)
+    x = torch.from_numpy(q).to(ac.TORCH[dtype])
+    q = x.double().numpy()
+    st = tc.status()
+    out = attention.attend_tree(x.cuda(), c.cache, c.table, ac.i32(lengths), ac.i32([rows * b for b in range(B + 1)]),
+                                ac.i32(sum(parents, [])), max_rows=rows, d_status=st)
+    assert st.item() == abi.MOE_OK
+    for b in range(B):
+        r = slice(b * rows, (b + 1) * rows)
+        o, z, spread, reach, seen = osp.attend_tree(q[r], c.k[b], c.v[b], parents[b], D ** -0.5)
+        seen[:, [j for j, _ in heavy]] = False
+        delta = (D + 8) * 2.0 ** -24 * reach + 2.0 ** -21
+        bound = ac.HALF_STEP[dtype] * np.abs(o) + 1.05 * (ac.HALF_STEP["fp16"] + 2 * delta + 2 * m * 2.0 ** -24)[..., None] * spread
+        tiny = np.einsum("nm,mkd->nkd", seen.astype(float), np.abs(c.v[b]))
+        bound += ac.HALF_TINY[dtype] + 2.0 ** -32 * np.repeat(tiny, group, axis=1)
+        err = np.abs(ac.f64(out[r]) - o)
+        assert (err <= bound).all(), f"{np.max(err / bound):.2f} of its bound"
