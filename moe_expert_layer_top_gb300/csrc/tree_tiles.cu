@@ -15,7 +15,7 @@
 // Bound. 4 D flops per (row, head, key) on the tensor cores; a decoded key tile serves 128 or 256 rows, so decoding
 // (2 D conversions a key) is a small part of it, unlike with the 8 to 32 rows of a verify step.
 //   Measured (32 + 8 heads of 128, 152 SMs, device time in a graph): 16 trees of 64 rows over 8,000 to 32,000 tokens
-// 315 us, 990 TFLOP/s or half of a library product's rate; one of 64 rows over 131,071 tokens 148 us (930); one of 16
+// 316 us, 985 TFLOP/s or half of a library product's rate; one of 64 rows over 131,071 tokens 149 us (925); one of 16
 // rows over 4,096 20.6; 24 ragged ones (64 + 8 heads of 64, f16) 64. A step of a stream, 128 keys, takes 4,700
 // clocks: 2,250 for the softmax (1,500 of them exponentials), 1,850 until its MMAs are issued and done, which at 128
 // x 128 take all of the shared memory's bandwidth, the rest waits and mask. The streams overlap to 44 % of the tensor

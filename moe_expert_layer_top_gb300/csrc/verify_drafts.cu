@@ -19,7 +19,7 @@
 // pass over the vocabulary that ends in a barrier. A cluster of blocks takes a sequence, and each block a part of the
 // vocabulary.
 //   Measured (131,072 tokens, device time in a graph): one chain of six in bf16 13 us, of a single row 6; 64 chains of
-// six with a draft, fp32, 71 us, of single rows 11 to 15; 16 trees of 64 rows 24 to 30; 24 of up to 16 rows with a draft over
+// six with a draft, fp32, 71 us, of single rows 11 to 15; 16 trees of 64 rows 23 to 30; 24 of up to 16 rows with a draft over
 // 50,021 tokens 37 to 42. Issue slots are 20 to 30 % busy, HBM 4 to 23 %: rows one after another, each a chain of latencies.
 //
 // Layout. A block's warps have consecutive parts of its part, in units of 8 tokens, a unit a lane. What every warp finds
