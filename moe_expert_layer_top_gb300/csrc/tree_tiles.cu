@@ -5,11 +5,12 @@
 // codes k and one scale code a per 32 dimensions, V likewise. Rows are (token,
 // head) pairs of one kv head's group; a row sees the keys in front of the tree,
 // its ancestors' and its own.
-//   Keys and values become f16 in shared memory: code times 2^(a - a_ref + 13). Of keys a_ref is the largest scale code of
-//   32; what it takes off goes into the factor of their scores, without an operation per score. Of values it is the scale
-//   code that the accumulators are relative to: 3 above the largest of 16 tiles where it moves, and it moves up when values
-//   beyond it are among the next 16. Exact down to 2^-33 of the largest seen. (With values relative to those of 32 keys, and the rest in
-//   the exponents of their weights, the weights next to a far larger value lost their bits in f16.)
+//   Keys and values become f16 in shared memory: code times 2^(a - a_ref + 13). Of keys a_ref is the largest scale
+//   code of 32; what it takes off goes into the factor of their scores, without an operation per score. Of values it
+//   is the scale code that the accumulators are relative to: 3 above the largest of 16 tiles where it moves, and it
+//   moves up when values beyond it are among the next 16. Exact down to 2^-33 of the largest seen. (With values
+//   relative to those of 32 keys, and the rest in the exponents of their weights, the weights next to a far larger
+//   value lost their bits in f16.)
 //   Queries become f16 times a power of two per row, probabilities f16 as in attend_paged.cu. All sums are binary32.
 //
 // Bound. 4 D flops per (row, head, key) on the tensor cores; a decoded key tile serves 128 or 256 rows, so decoding
@@ -542,7 +543,8 @@ struct Decoder {
           bytes = at == kNoRow ? 0 : min(16, seg.s.len - key) * kGroups;
           if (bytes) {
 #pragma unroll
-            for (int k = 0; k < kGroups; ++k) of[k] = __ldg(reinterpret_cast<const uint4 *>(scales + uint64_t(at) * kGroups) + k);
+            for (int k = 0; k < kGroups; ++k)
+              of[k] = __ldg(reinterpret_cast<const uint4 *>(scales + uint64_t(at) * kGroups) + k);
           }
         }
       }

@@ -5,15 +5,16 @@
 // were drawn from, what is left after k rejections is p_k = max(p_(k-1) - q, 0) /
 // sum; by induction max(p - c_k q, 0) / N_k with c_0 = 0, N_0 = 1, c_(k+1) = c_k + N_k
 // and N_k the sum, so a rejection costs one pass over the vocabulary and one
-// number. Without q a rejected token's p becomes 0 and no pass is needed: N is 1
-// minus what was taken off. The new token is the first whose running sum exceeds u times the whole.
+// number. Without q a rejected token's p becomes 0 and N is 1 minus what was taken off,
+// without a pass until little is left. The new token is the first whose running sum exceeds u times the whole.
 //
 // Accuracy. A decision compares numbers of relative error 2^-20: it is the formula's unless u lies that close to the
 // border. To keep that behind rejections, where both sides are what is left of larger numbers, the child's weight and the
-// sums are held in two binary32. The new token has a border for each token: with 2^17 tokens sums off by 2^-24 of the whole (one rounding of a
-// large weight) would give another token once in some hundred draws. So the weights that a token is chosen from are
-// computed in two binary32 each where they are large (a table of 2^(k/32) and a polynomial, about 2^-36 relative), in one
-// without a bias where they are not, and their sums are kept in two; binary64 runs at a hundredth of the rate here.
+// sums are held in two binary32. The new token has a border for each token: with 2^17 tokens sums off by 2^-24 of the
+// whole (one rounding of a large weight) would give another token once in some hundred draws. So the weights that a token
+// is chosen from are computed in two binary32 each where they are large (a table of 2^(k/32) and a polynomial, about 2^-36
+// relative) or next to what the draft takes of them, in one without a bias where they are not, and their sums are kept in
+// two; binary64 runs at a hundredth of the rate here.
 //
 // Bound. Only the rows on the way are read: with one accepted child after another the rows come one after another, each a
 // pass over the vocabulary that ends in a barrier. A cluster of blocks takes a sequence, and each block a part of the
@@ -276,7 +277,7 @@ struct Smem {
   int parent[kMaxTree];    // kNever: not asked
   int rejected[kMaxTree];  // tokens of the rejected children of the row
   int way[kMaxTree];       // accepted rows, the root first
-  float2 large[kWarps][32 * kUnit + 32];  // logits (and draft probabilities) of weights to compute in two, until there are 32
+  float2 large[kWarps][32 * kUnit + 32];  // logits (and draft probabilities) of weights to be in two, until there are 32
   Two part[kWarps];        // sums of the warps where the new token is looked for, and what they found
   int found[kWarps];
 };
